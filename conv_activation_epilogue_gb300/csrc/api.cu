@@ -15,6 +15,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "api_internal.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "mmact.h"
@@ -886,6 +887,23 @@ mmact_status residual_check(const void *R, const void *out, int64_t bytes)
 }
 
 }  // namespace
+
+mmact_status device_context(DeviceContext *out)
+{
+    DeviceInfo *dev = nullptr;
+    const mmact_status s = device_info(&dev);
+    if (s != MMACT_OK) return s;
+    out->sm_count = dev->sm_count;
+    out->status = dev->status;
+    out->wait_ns = g_wait_ns.load();
+    return MMACT_OK;
+}
+
+bool encode_tensor_map(CUtensorMap *m, mmact_dtype dt, int rank, const void *ptr, const uint64_t *dims,
+                       const uint64_t *strides_bytes, const uint32_t *box, bool swizzle)
+{
+    return encode(m, dt, rank, ptr, dims, strides_bytes, box, swizzle);
+}
 
 // Host validation shared by every mmact_gemm-family entry point (also used by
 // the no-allocation entry point in noalloc.cu, before its own size limit).

@@ -1,0 +1,323 @@
+// api_mx.cu -- the C ABI of the MXFP4 and mixture-of-experts operators
+// (include/mmact.h): argument validation and launch planning.  As in api.cu,
+// every check happens on the host before anything is enqueued.
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "api_internal.h"
+#include "common.cuh"
+#include "kernels_mx.h"
+#include "mmact.h"
+#include "mxfp4.cuh"
+
+#define MMACT_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace mmact {
+namespace {
+
+constexpr int MAX_DEVICES = 64;
+constexpr int64_t MAX_DIM = (int64_t(1) << 31) - 1;
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+int out_kind(mmact_dtype d) { return d == MMACT_BF16 ? OUT_BF16 : (d == MMACT_F16 ? OUT_F16 : OUT_F32); }
+int elem_bytes(mmact_dtype d) { return d == MMACT_F32 ? 4 : 2; }
+bool valid_16(mmact_dtype d) { return d == MMACT_F16 || d == MMACT_BF16; }
+bool valid_float(mmact_dtype d) { return valid_16(d) || d == MMACT_F32; }
+bool valid_act(mmact_act a) { return a >= MMACT_ACT_NONE && a <= MMACT_ACT_SILU; }
+
+// The current device, with this file's kernels set up on it (once per device).
+mmact_status mx_context(DeviceContext *out)
+{
+    static std::mutex mutex;
+    static bool ready[MAX_DEVICES];
+    const mmact_status s = device_context(out);
+    if (s != MMACT_OK) return s;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!ready[dev]) {
+        if (setup_mxfp4_kernels() != cudaSuccess) return MMACT_ERR_CUDA;
+        ready[dev] = true;
+    }
+    return MMACT_OK;
+}
+
+int64_t mx_codes_bytes(int64_t rows, int64_t K) { return rows * (mx_blocks(K) * 16); }
+int64_t mx_scales_bytes(int64_t rows, int64_t K) { return (rows + 127) / 128 * mx_tiles(K) * 512; }
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+bool mx_dims(int64_t rows, int64_t K) { return rows >= 0 && K >= 0 && rows <= MAX_DIM && K <= MAX_DIM; }
+
+mmact_status mx_gemm_check(const void *ac, const void *as, const void *bc, const void *bs, const float *bias,
+                           const void *C, int64_t M, int64_t N, int64_t K, mmact_dtype cd, mmact_act act)
+{
+    if (!mx_dims(M, K) || !mx_dims(N, K)) return MMACT_ERR_INVALID_ARG;
+    if (((ac == nullptr || as == nullptr) && M * K != 0) || ((bc == nullptr || bs == nullptr) && N * K != 0) ||
+        (C == nullptr && M * N != 0))
+        return MMACT_ERR_INVALID_ARG;
+    if (!valid_float(cd) || !valid_act(act)) return MMACT_ERR_INVALID_ARG;
+    if (bias != nullptr && !aligned4(bias)) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(ac) || !aligned16(as) || !aligned16(bc) || !aligned16(bs) || !aligned16(C))
+        return MMACT_ERR_UNSUPPORTED;
+    if (((M + 127) / 128) * ((N + 127) / 128) > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
+    return MMACT_OK;
+}
+
+// Tensor maps of an MXFP4 matrix: its codes as 16-bit words (box 64 words = 256
+// codes x `box_rows` rows, 128-byte swizzle) and its scale tiles as 32-bit words
+// (box 256 words = two tiles = 256 K, of `box_tiles` rows of tiles).  Rows, codes and tiles past the
+// end arrive as zeros.
+bool mx_encode(CUtensorMap *mc, CUtensorMap *ms, const void *codes, const void *scales, int64_t rows, int64_t K,
+               uint32_t box_rows, uint32_t box_tiles)
+{
+    const uint64_t dc[2] = {(uint64_t)mx_blocks(K) * 8, (uint64_t)rows}, sc[1] = {(uint64_t)mx_blocks(K) * 16};
+    const uint32_t bc[2] = {64, box_rows};
+    const uint64_t ds[2] = {(uint64_t)mx_tiles(K) * 128, (uint64_t)(rows + 127) / 128};
+    const uint64_t ss[1] = {(uint64_t)mx_tiles(K) * 512};
+    const uint32_t bs[2] = {256, box_tiles};
+    return encode_tensor_map(mc, MMACT_BF16, 2, codes, dc, sc, bc, true) &&
+           encode_tensor_map(ms, MMACT_F32, 2, scales, ds, ss, bs, false);
+}
+
+// Plan of one product (M, N > 0, K > 0).
+mmact_status mx_gemm_plan(MxGemmLaunch &L, const void *ac, const void *as, const void *bc, const void *bs,
+                          const float *bias, void *C, int64_t M, int64_t N, int64_t K, mmact_dtype cd, mmact_act act,
+                          float alpha)
+{
+    DeviceContext dev;
+    const mmact_status st = mx_context(&dev);
+    if (st != MMACT_OK) return st;
+    std::memset(&L, 0, sizeof(L));
+    MxGemmArgs &a = L.args;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.nk64 = (int)((mx_blocks(K) + 1) / 2);
+    a.tiles_m = (int)((M + 127) / 128);
+    a.tiles_n = (int)((N + 127) / 128);
+    a.num_tiles = a.tiles_m * a.tiles_n;
+    a.num_kb = (int)((K + 255) / 256);
+    a.group_m = 16;
+    a.act = (int)act;
+    a.alpha = alpha;
+    a.bias = bias;
+    a.C = C;
+    a.status = dev.status;
+    a.wait_ns = dev.wait_ns;
+    const int ce = elem_bytes(cd);
+    a.c_tma = N * ce % 16 == 0 ? 1 : 0;
+    L.out = out_kind(cd);
+    L.grid = (int)std::min<int64_t>(a.num_tiles, dev.sm_count);
+    if (!mx_encode(&L.tmA, &L.tmSA, ac, as, M, K, 128, 1) || !mx_encode(&L.tmB, &L.tmSB, bc, bs, N, K, 128, 1))
+        return MMACT_ERR_CUDA;
+    if (a.c_tma) {
+        const uint64_t dC[2] = {(uint64_t)N, (uint64_t)M}, sC[1] = {(uint64_t)N * ce};
+        const uint32_t bC[2] = {(uint32_t)(128 / ce), 32};
+        if (!encode_tensor_map(&L.tmC, cd, 2, C, dC, sC, bC, true)) return MMACT_ERR_CUDA;
+    }
+    return MMACT_OK;
+}
+
+mmact_status enqueued(cudaError_t e) { return e == cudaSuccess ? MMACT_OK : MMACT_ERR_CUDA; }
+
+cudaError_t quantize_launch(const void *x, void *codes, void *scales, int64_t rows, int64_t K, mmact_dtype xd,
+                            int transposed, cudaStream_t stream)
+{
+    return launch_quantize_mxfp4(x, out_kind(xd), static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), rows, K,
+                                 transposed != 0, stream);
+}
+
+// Where the parts of mmact_moe's workspace begin.
+struct MoeWorkspace {
+    int64_t x_hi, x_lo, h_hi, h_lo, part, bytes;
+    int num_counters;
+};
+
+MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t top)
+{
+    MoeWorkspace w;
+    const int64_t Hp = round_up(H, 32), Ip = round_up(I, 32);
+    w.num_counters = (int)(1 + (H + 15) / 16);
+    int64_t at = round_up(w.num_counters * 4, 256);
+    auto take = [&at](int64_t bytes) {
+        const int64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    w.x_hi = take(T * Hp * 2);
+    w.x_lo = take(T * Hp * 2);
+    w.h_hi = take(T * top * Ip * 2);
+    w.h_lo = take(T * top * Ip * 2);
+    w.part = take(T * top * H * 4);
+    w.bytes = at;
+    return w;
+}
+
+constexpr int64_t MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 16, MOE_MAX_EXPERTS = 512;
+
+mmact_status moe_sizes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
+{
+    if (T < 0 || H < 0 || I < 0 || E < 0 || top < 0 || H > MAX_DIM || I > MAX_DIM) return MMACT_ERR_INVALID_ARG;
+    if (T > MOE_MAX_TOKENS || E > MOE_MAX_EXPERTS || top < 1 || top > MOE_MAX_TOP || top > E || H < 8 || I < 8 ||
+        H % 8 != 0 || I % 8 != 0)
+        return MMACT_ERR_UNSUPPORTED;
+    // rows of the experts' matrices and the items of a product are counted in 32 bits
+    if (E * 2 * I > MAX_DIM || E * H > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
+    return MMACT_OK;
+}
+
+}  // namespace
+}  // namespace mmact
+
+using namespace mmact;
+
+MMACT_EXPORT mmact_status mmact_mxfp4_size(int64_t rows, int64_t K, int64_t *codes_bytes, int64_t *scales_bytes)
+{
+    if (!mx_dims(rows, K) || codes_bytes == nullptr || scales_bytes == nullptr) return MMACT_ERR_INVALID_ARG;
+    *codes_bytes = mx_codes_bytes(rows, K);
+    *scales_bytes = mx_scales_bytes(rows, K);
+    return MMACT_OK;
+}
+
+MMACT_EXPORT mmact_status mmact_quantize_mxfp4(const void *x, void *codes, void *scales, int64_t rows, int64_t K,
+                                               mmact_dtype x_dtype, int transposed, void *stream)
+{
+    if (!mx_dims(rows, K) || !valid_float(x_dtype)) return MMACT_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return MMACT_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MMACT_ERR_UNSUPPORTED;
+    return enqueued(quantize_launch(x, codes, scales, rows, K, x_dtype, transposed, static_cast<cudaStream_t>(stream)));
+}
+
+MMACT_EXPORT mmact_status mmact_dequantize_mxfp4(const void *codes, const void *scales, void *y, int64_t rows, int64_t K,
+                                                 mmact_dtype y_dtype, void *stream)
+{
+    if (!mx_dims(rows, K) || !valid_float(y_dtype)) return MMACT_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return MMACT_OK;
+    if (codes == nullptr || scales == nullptr || y == nullptr) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return MMACT_ERR_UNSUPPORTED;
+    return enqueued(launch_dequantize_mxfp4(static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), y,
+                                            out_kind(y_dtype), rows, K, static_cast<cudaStream_t>(stream)));
+}
+
+MMACT_EXPORT mmact_status mmact_gemm_mxfp4(const void *a_codes, const void *a_scales, const void *b_codes,
+                                           const void *b_scales, const float *bias, void *C, int64_t M, int64_t N,
+                                           int64_t K, mmact_dtype c_dtype, mmact_act act, float alpha, void *stream)
+{
+    mmact_status s = mx_gemm_check(a_codes, a_scales, b_codes, b_scales, bias, C, M, N, K, c_dtype, act);
+    if (s != MMACT_OK) return s;
+    if (M == 0 || N == 0) return MMACT_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
+    MxGemmLaunch L;
+    s = mx_gemm_plan(L, a_codes, a_scales, b_codes, b_scales, bias, C, M, N, K, c_dtype, act, alpha);
+    return s == MMACT_OK ? enqueued(launch_gemm_mxfp4(L, st)) : s;
+}
+
+MMACT_EXPORT mmact_status mmact_linear_mxfp4_workspace_bytes(int64_t M, int64_t K, int64_t *bytes)
+{
+    if (!mx_dims(M, K) || bytes == nullptr) return MMACT_ERR_INVALID_ARG;
+    *bytes = round_up(mx_codes_bytes(M, K), 512) + mx_scales_bytes(M, K);
+    return MMACT_OK;
+}
+
+MMACT_EXPORT mmact_status mmact_linear_mxfp4(const void *x, const void *w_codes, const void *w_scales, const float *bias,
+                                             void *C, int64_t M, int64_t N, int64_t K, mmact_dtype x_dtype,
+                                             mmact_dtype c_dtype, mmact_act act, float alpha, void *workspace,
+                                             void *stream)
+{
+    if (!mx_dims(M, K) || !valid_float(x_dtype)) return MMACT_ERR_INVALID_ARG;
+    if ((x == nullptr || workspace == nullptr) && M * K != 0) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(workspace)) return MMACT_ERR_UNSUPPORTED;
+    uint8_t *codes = static_cast<uint8_t *>(workspace);
+    uint8_t *scales = M * K != 0 ? codes + round_up(mx_codes_bytes(M, K), 512) : codes;
+    mmact_status s = mx_gemm_check(codes, scales, w_codes, w_scales, bias, C, M, N, K, c_dtype, act);
+    if (s != MMACT_OK) return s;
+    if (M == 0 || N == 0) return MMACT_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
+    MxGemmLaunch L;
+    if ((s = mx_gemm_plan(L, codes, scales, w_codes, w_scales, bias, C, M, N, K, c_dtype, act, alpha)) != MMACT_OK)
+        return s;
+    if ((s = enqueued(quantize_launch(x, codes, scales, M, K, x_dtype, 0, st))) != MMACT_OK) return s;
+    return enqueued(launch_gemm_mxfp4(L, st));
+}
+
+MMACT_EXPORT mmact_status mmact_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top,
+                                                    int64_t *bytes)
+{
+    if (bytes == nullptr) return MMACT_ERR_INVALID_ARG;
+    const mmact_status s = moe_sizes(T, H, I, E, top);
+    if (s != MMACT_OK) return s;
+    *bytes = moe_workspace(T, H, I, top).bytes;
+    return MMACT_OK;
+}
+
+MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const float *router_bias, const void *w1,
+                                    const void *w1_scales, const float *b1, const void *w2, const void *w2_scales,
+                                    const float *b2, void *y, int32_t *experts, float *probs, int64_t T, int64_t H,
+                                    int64_t I, int64_t E, int64_t top, mmact_dtype x_dtype, mmact_dtype w_dtype,
+                                    mmact_act act, float alpha, int gated, int normalize, void *workspace, void *stream)
+{
+    if (!valid_16(x_dtype) || !valid_act(act)) return MMACT_ERR_INVALID_ARG;
+    if (w_dtype < MMACT_F16 || w_dtype > MMACT_MXFP4) return MMACT_ERR_INVALID_ARG;
+    mmact_status s = moe_sizes(T, H, I, E, top);
+    if (s != MMACT_OK) return s;
+    const bool mx = w_dtype == MMACT_MXFP4;
+    if (!mx && w_dtype != x_dtype) return MMACT_ERR_UNSUPPORTED;
+    if (T == 0) return MMACT_OK;
+    if (x == nullptr || router == nullptr || w1 == nullptr || w2 == nullptr || y == nullptr || experts == nullptr ||
+        probs == nullptr || workspace == nullptr || (mx && (w1_scales == nullptr || w2_scales == nullptr)))
+        return MMACT_ERR_INVALID_ARG;
+    if ((router_bias != nullptr && !aligned4(router_bias)) || (b1 != nullptr && !aligned4(b1)) ||
+        (b2 != nullptr && !aligned4(b2)) || !aligned4(experts) || !aligned4(probs))
+        return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(router) || !aligned16(w1) || !aligned16(w2) || !aligned16(y) ||
+        !aligned16(workspace) || (mx && (!aligned16(w1_scales) || !aligned16(w2_scales))))
+        return MMACT_ERR_UNSUPPORTED;
+    DeviceContext dev;
+    if ((s = mx_context(&dev)) != MMACT_OK) return s;
+    MoeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.T = (int)T;
+    a.H = (int)H;
+    a.I = (int)I;
+    a.E = (int)E;
+    a.top = (int)top;
+    a.gated = gated != 0;
+    a.normalize = normalize != 0;
+    a.R1 = (int)(a.gated ? 2 * I : I);
+    a.Hp = (int)round_up(H, 32);
+    a.Ip = (int)round_up(I, 32);
+    a.act = (int)act;
+    a.alpha = alpha;
+    a.w_type = mx ? 2 : (w_dtype == MMACT_BF16 ? 1 : 0);
+    a.x = x;
+    a.router = router;
+    a.w1 = w1;
+    a.w2 = w2;
+    a.s1 = w1_scales;
+    a.s2 = w2_scales;
+    a.router_bias = router_bias;
+    a.b1 = b1;
+    a.b2 = b2;
+    a.y = y;
+    a.experts = experts;
+    a.probs = probs;
+    const MoeWorkspace w = moe_workspace(T, H, I, top);
+    char *ws = static_cast<char *>(workspace);
+    a.counters = reinterpret_cast<unsigned int *>(ws);
+    a.num_counters = w.num_counters;
+    a.x_hi = reinterpret_cast<__nv_bfloat16 *>(ws + w.x_hi);
+    a.x_lo = reinterpret_cast<__nv_bfloat16 *>(ws + w.x_lo);
+    a.h_hi = reinterpret_cast<__nv_bfloat16 *>(ws + w.h_hi);
+    a.h_lo = reinterpret_cast<__nv_bfloat16 *>(ws + w.h_lo);
+    a.part = reinterpret_cast<float *>(ws + w.part);
+    a.status = dev.status;
+    a.wait_ns = dev.wait_ns;
+    return enqueued(launch_moe(a, out_kind(x_dtype), dev.sm_count, static_cast<cudaStream_t>(stream)));
+}

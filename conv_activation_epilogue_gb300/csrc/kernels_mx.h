@@ -1,0 +1,74 @@
+// kernels_mx.h -- host-side view of the MXFP4 and mixture-of-experts kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "mmact.h"
+
+namespace mmact {
+
+cudaError_t launch_quantize_mxfp4(const void *x, int type, uint8_t *codes, uint8_t *scales, int64_t rows, int64_t K,
+                                  bool trans, cudaStream_t s);
+cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, void *y, int type, int64_t rows,
+                                    int64_t K, cudaStream_t s);
+
+// Product of two MXFP4 matrices with the fused epilogue.
+struct MxGemmArgs {
+    int M, N;
+    int nk64;            // K steps of 64 (one instruction each) that hold values
+    int tiles_m, tiles_n, num_tiles, num_kb;   // num_kb: K blocks of 256 (one ring stage each)
+    int group_m;
+    int act;
+    float alpha;
+    const float *bias;   // [N] or null
+    void *C;
+    int c_tma;           // 1: output tiles by TMA store, 0: element stores (row pitch not a multiple of 16 bytes)
+    unsigned int *status;
+    unsigned long long wait_ns;
+};
+
+struct MxGemmLaunch {
+    CUtensorMap tmA, tmB, tmSA, tmSB, tmC;   // codes as 16-bit words, scale tiles as 32-bit words
+    MxGemmArgs args;
+    int out;
+    int grid;
+};
+
+cudaError_t setup_mxfp4_kernels();
+cudaError_t launch_gemm_mxfp4(const MxGemmLaunch &L, cudaStream_t stream);
+
+// A mixture-of-experts layer for a few tokens.
+struct MoeArgs {
+    int T, H, I, E, top;         // tokens, model width, experts' width, experts, experts per token
+    int R1;                      // rows of one expert's w1: 2 I when gated, else I
+    int Hp, Ip;                  // H and I rounded up to 32 (row pitches of the workspace's arrays)
+    int gated, normalize, act;
+    int w_type;                  // 0 fp16, 1 bf16, 2 MXFP4
+    float alpha;
+    const void *x, *router;      // [T, H], [E, H]
+    const void *w1, *w2;         // [E, R1, H], [E, H, I] (MXFP4: codes of [E * R1, H], [E * H, I])
+    const void *s1, *s2;         // MXFP4: scale tiles of the same
+    const float *router_bias, *b1, *b2;   // [E], [E, R1], [E, H], or null
+    void *y;                     // [T, H]
+    int *experts;                // [T, top]
+    float *probs;                // [T, top]
+    // workspace
+    unsigned int *counters;      // [0] grid barrier, [1 + i] experts done with rows 16 i .. of y
+    int num_counters;
+    __nv_bfloat16 *x_hi, *x_lo;  // MXFP4: x in the codes' order [T, Hp]
+    __nv_bfloat16 *h_hi, *h_lo;  // [T * top, Ip]
+    float *part;                 // [T * top, H]
+    unsigned int *status;
+    unsigned long long wait_ns;
+};
+
+cudaError_t launch_moe(const MoeArgs &a, int x_out, int sms, cudaStream_t stream);
+
+// out [rows, cols] = act(bias): a product over an empty K.
+cudaError_t launch_mx_bias_act(const float *bias, void *out, int64_t rows, int64_t cols, int out_kind, int act,
+                               float alpha, cudaStream_t stream);
+
+}  // namespace mmact

@@ -1,0 +1,166 @@
+// mxfp4.cuh -- the 4-bit microscaled format: layout, conversions, tensor-core
+// instructions; and the activations of the operators that use it.
+//
+// MXFP4 (OCP Microscaling Formats specification 1.0): 32 consecutive values
+// along K share the scale X = 2^(b - 127) with b one byte (255 = NaN); a value
+// is X times an E2M1 number, one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign.
+// Quantisation: b = max(floor(log2(amax)) - 2 + 127, 0), values rounded to
+// nearest even on the E2M1 grid, those past 6 set to 6.
+//
+// A quantised matrix [rows, K] is two arrays:
+//   codes   [rows][KB * 16] bytes, KB = ceil(K / 32): two codes to a byte, the
+//           even k in the low half; codes past K are 0
+//   scales  tiles of 512 bytes, [ceil(rows / 128)][ceil(KB / 4)]: the scale of
+//           row r, block b is byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of
+//           its tile; bytes of rows or blocks that do not exist are 0.
+// A tile is what one tcgen05.cp.32x128b.warpx4 moves into tensor memory: 32
+// lanes x 16 bytes, column c holding the four scales of row lane + 32 c.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace mmact {
+
+constexpr int MX_BLOCK = 32;
+
+__host__ __device__ constexpr int64_t mx_blocks(int64_t k) { return (k + 31) / 32; }
+__host__ __device__ constexpr int64_t mx_tiles(int64_t k) { return (k + 127) / 128; }
+
+// Byte offset of the scale of row r, block b (tiles = mx_tiles(K)).
+__device__ __forceinline__ int64_t mx_scale_at(int64_t r, int64_t b, int64_t tiles)
+{
+    return ((r >> 7) * tiles + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
+}
+
+// Scale byte of a block from the bits of its largest |x| (as fp32): the
+// exponent field minus 2, at least 0; 255 when the block holds an infinity or
+// a NaN.  A block of zeros gets 0.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits)
+{
+    const uint32_t e = amax_bits >> 23;
+    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+
+// 1 / X for a finite block (b <= 252): exact.
+__device__ __forceinline__ float mx_inv_scale(uint32_t b)
+{
+    return __uint_as_float((254u - b) << 23);
+}
+
+// X of a scale byte: 2^-127 is subnormal, 255 is NaN.
+__device__ __forceinline__ float mx_scale(uint32_t b)
+{
+    return __uint_as_float(b == 0u ? 0x00400000u : (b == 255u ? 0x7fc00000u : b << 23));
+}
+
+// Eight values, already divided by X, to eight codes (v[0] in the low bits):
+// round to nearest even, saturating at +-6.
+__device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8])
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n\t"
+        "mov.b32 %0, {c0, c1, c2, c3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Eight codes to eight E2M1 values.
+__device__ __forceinline__ void mx_decode8(uint32_t c, float (&v)[8])
+{
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+        "mov.b32 {c0, c1, c2, c3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, c0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, c1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, c3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// -------------------------------------------------------------- activations --
+enum : int { ACT_SILU = ACT_GELU + 1 };
+
+// z * sigma(z) = z / (1 + e^-z): one hardware exponential and one fast divide, a
+// few ulp each.  Below z = -87 the divisor passes 2^126, where __fdividef gives 0
+// (the value is above -1e-36 there), and e^-z = inf would give NaN from
+// -inf / inf: both are cut off at -87.
+__device__ __forceinline__ float silu_f32(float z)
+{
+    return z < -87.0f ? z * 0.0f : __fdividef(z, 1.0f + __expf(-z));
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_mx(float z, float alpha)
+{
+    if constexpr (ACT == ACT_SILU) return silu_f32(z);
+    else return act_f32<ACT>(z, alpha);
+}
+
+__device__ __forceinline__ float act_mx(int act, float z, float alpha)
+{
+    switch (act) {
+    case ACT_RELU: return act_mx<ACT_RELU>(z, alpha);
+    case ACT_LEAKY: return act_mx<ACT_LEAKY>(z, alpha);
+    case ACT_TANH: return act_mx<ACT_TANH>(z, alpha);
+    case ACT_SIGMOID: return act_mx<ACT_SIGMOID>(z, alpha);
+    case ACT_GELU: return act_mx<ACT_GELU>(z, alpha);
+    case ACT_SILU: return act_mx<ACT_SILU>(z, alpha);
+    default: return z;
+    }
+}
+
+// -------------------------------------------------- tensor-core instructions --
+namespace ptx {
+
+// D[tmem] (+)= (A x scale_A)(B x scale_B), kind::mxf4: E2M1 operands packed two
+// to a byte, K-major, K = 64 per instruction, one UE8M0 scale per row and 32 K
+// (two per row and instruction), scales in tensor memory.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// Copy 32 rows x 16 bytes of shared memory (an unswizzled descriptor, 8-row
+// groups of 128 bytes) to four 32-bit columns of all four lane quarters of
+// tensor memory: one scale tile.  Ordered before the MMAs that the same thread
+// issues after it.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Instruction descriptor for kind::mxf4: A and B E2M1 (format 1), scales UE8M0,
+// M and N extents; sa and sb (0 or 2) say which two bytes of the 32-bit scale
+// columns hold this instruction's scales.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t sa, uint32_t sb)
+{
+    return (sb << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(M >> 7) << 27) | (sa << 29);
+}
+
+}  // namespace ptx
+
+}  // namespace mmact

@@ -18,8 +18,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(_HERE, "libmmact.so")
 
 MMACT_OK, MMACT_ERR_INVALID_ARG, MMACT_ERR_UNSUPPORTED, MMACT_ERR_CUDA, MMACT_ERR_TIMEOUT = range(5)
-ACT = {"none": 0, "relu": 1, "leaky_relu": 2, "tanh": 3, "sigmoid": 4, "gelu": 5}
+ACT = {"none": 0, "relu": 1, "leaky_relu": 2, "tanh": 3, "sigmoid": 4, "gelu": 5,
+       "silu": 6}   # silu: MXFP4 products and mmact_moe only
 DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+MMACT_MXFP4 = 4  # mmact_moe's weights in the 4-bit microscaled format
 MMACT_TF32 = 3   # fp32 inputs computed as tf32 (one pass); float32 tensors default to split precision
 
 _lib = None
@@ -35,6 +37,8 @@ SYMBOLS = [
     "mmact_gemm_split_k_choice", "mmact_set_gemm_pair", "mmact_gemm_kernel_choice", "mmact_set_conv_tmem",
     "mmact_gemm_auto", "mmact_gemm_auto_choice", "mmact_conv2d_auto", "mmact_conv2d_auto_choice",
     "mmact_set_gemm_l2_policy", "mmact_tensor_map_cache_stats", "mmact_status_string", "mmact_version",
+    "mmact_mxfp4_size", "mmact_quantize_mxfp4", "mmact_dequantize_mxfp4", "mmact_gemm_mxfp4",
+    "mmact_linear_mxfp4", "mmact_linear_mxfp4_workspace_bytes", "mmact_moe", "mmact_moe_workspace_bytes",
 ]
 
 
@@ -102,6 +106,19 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     L.mmact_status_string.argtypes = [ci]
     L.mmact_status_string.restype = ctypes.c_char_p
     L.mmact_version.argtypes = []
+    p_i64 = ctypes.POINTER(i64)
+    L.mmact_mxfp4_size.argtypes = [i64, i64, p_i64, p_i64]
+    L.mmact_quantize_mxfp4.argtypes = [vp, vp, vp, i64, i64, ci, ci, vp]
+    L.mmact_dequantize_mxfp4.argtypes = [vp, vp, vp, i64, i64, ci, vp]
+    L.mmact_gemm_mxfp4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, f32, vp]
+    L.mmact_linear_mxfp4.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, f32, vp, vp]
+    L.mmact_linear_mxfp4_workspace_bytes.argtypes = [i64, i64, p_i64]
+    L.mmact_moe.argtypes = [vp] * 12 + [i64] * 5 + [ci, ci, ci, f32, ci, ci, vp, vp]
+    L.mmact_moe_workspace_bytes.argtypes = [i64] * 5 + [p_i64]
+    for name in ("mmact_mxfp4_size", "mmact_quantize_mxfp4", "mmact_dequantize_mxfp4", "mmact_gemm_mxfp4",
+                 "mmact_linear_mxfp4", "mmact_linear_mxfp4_workspace_bytes", "mmact_moe",
+                 "mmact_moe_workspace_bytes"):
+        getattr(L, name).restype = ci
     for name in ("mmact_gemm", "mmact_gemm_split", "mmact_conv2d", "mmact_conv2d_split",
                  "mmact_conv2d_out_shape", "mmact_get_last_error", "mmact_selftest_wait_timeout",
                  "mmact_set_gemm_tile_n", "mmact_set_gemm_split_k", "mmact_gemm_split_k_choice",
@@ -416,6 +433,165 @@ def mmact_conv2d_nhwc_residual(x, w, bias, R, y, stride=(1, 1), pads=(0, 0, 0, 0
     _check(L.mmact_conv2d_nhwc_residual(px, pw, pb, pr, py, *rest, _in_code(x, tf32), DTYPE[y.dtype],
                                         ACT[act], float(alpha), _stream_handle(stream)),
            "mmact_conv2d_nhwc_residual")
+
+
+_BYTES = (torch.uint8,)
+
+
+def mmact_mxfp4_size(rows: int, K: int) -> tuple[int, int]:
+    """(bytes of codes, bytes of scales) of an MXFP4 matrix [rows, K] (see include/mmact.h)."""
+    c, s = ctypes.c_int64(0), ctypes.c_int64(0)
+    _check(load().mmact_mxfp4_size(int(rows), int(K), ctypes.byref(c), ctypes.byref(s)), "mmact_mxfp4_size")
+    return c.value, s.value
+
+
+def _mxfp4_ptrs(codes, scales, rows: int, K: int, name: str):
+    pc, ps = _dev(codes, name + " codes", _BYTES), _dev(scales, name + " scales", _BYTES)
+    # the sizes of mmact_mxfp4_size
+    if codes.numel() != rows * ((K + 31) // 32 * 16):
+        raise ValueError(f"{name} codes must hold {rows} x {(K + 31) // 32 * 16} bytes")
+    if scales.numel() != (rows + 127) // 128 * ((K + 127) // 128) * 512:
+        raise ValueError(f"{name} scales must hold {(rows + 127) // 128} x {(K + 127) // 128} tiles of 512 bytes")
+    return pc, ps
+
+
+def mmact_quantize_mxfp4(x, codes, scales, transposed: bool = False, stream=None) -> None:
+    """Quantise x [rows, K] (or, transposed, [K, rows]) to MXFP4 with blocks along K; codes and
+    scales are uint8 tensors of mmact_mxfp4_size(rows, K) bytes."""
+    L = load()
+    px = _dev(x, "x", _IN)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, K = (x.shape[1], x.shape[0]) if transposed else x.shape
+    pc, ps = _mxfp4_ptrs(codes, scales, rows, K, "x")
+    _check(L.mmact_quantize_mxfp4(px, pc, ps, rows, K, DTYPE[x.dtype], 1 if transposed else 0,
+                                  _stream_handle(stream)), "mmact_quantize_mxfp4")
+
+
+def mmact_dequantize_mxfp4(codes, scales, y, stream=None) -> None:
+    """y [rows, K] = the values of an MXFP4 matrix."""
+    L = load()
+    py = _dev(y, "y", _OUT)
+    if y.dim() != 2:
+        raise ValueError("y must be 2-D")
+    rows, K = y.shape
+    pc, ps = _mxfp4_ptrs(codes, scales, rows, K, "y")
+    _check(L.mmact_dequantize_mxfp4(pc, ps, py, rows, K, DTYPE[y.dtype], _stream_handle(stream)),
+           "mmact_dequantize_mxfp4")
+
+
+def mmact_gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, bias, C, K: int, act: str = "none",
+                     alpha: float = 0.0, stream=None) -> None:
+    """C = act(A @ B.T + bias) of MXFP4 matrices A [M, K] and B [N, K]; C [M, N]."""
+    L = load()
+    pc = _dev(C, "C", _OUT)
+    if C.dim() != 2:
+        raise ValueError("C must be 2-D")
+    M, N = C.shape
+    pa, psa = _mxfp4_ptrs(a_codes, a_scales, M, K, "A")
+    pb, psb = _mxfp4_ptrs(b_codes, b_scales, N, K, "B")
+    _check(L.mmact_gemm_mxfp4(pa, psa, pb, psb, _bias_ptr(bias, N), pc, M, N, K, DTYPE[C.dtype], ACT[act],
+                              float(alpha), _stream_handle(stream)), "mmact_gemm_mxfp4")
+
+
+def mmact_linear_mxfp4_workspace_bytes(M: int, K: int) -> int:
+    """Bytes of the workspace that mmact_linear_mxfp4 needs for x [M, K]."""
+    out = ctypes.c_int64(0)
+    _check(load().mmact_linear_mxfp4_workspace_bytes(int(M), int(K), ctypes.byref(out)),
+           "mmact_linear_mxfp4_workspace_bytes")
+    return out.value
+
+
+def mmact_linear_mxfp4(x, w_codes, w_scales, bias, C, workspace, act: str = "none", alpha: float = 0.0,
+                       stream=None) -> None:
+    """C = act(q(x) @ W.T + bias): x [M, K] is quantised to MXFP4 on the way in, W [N, K] is MXFP4."""
+    L = load()
+    px, pc = _dev(x, "x", _IN), _dev(C, "C", _OUT)
+    if x.dim() != 2 or C.dim() != 2 or C.shape[0] != x.shape[0]:
+        raise ValueError("x must be [M, K] and C [M, N]")
+    M, K = x.shape
+    N = C.shape[1]
+    pw, ps = _mxfp4_ptrs(w_codes, w_scales, N, K, "W")
+    pws = _dev(workspace, "workspace", _BYTES)
+    if workspace.numel() < -(-M * ((K + 31) // 32 * 16) // 512) * 512 + (M + 127) // 128 * ((K + 127) // 128) * 512:
+        raise ValueError("workspace must hold mmact_linear_mxfp4_workspace_bytes(M, K) bytes")
+    _check(L.mmact_linear_mxfp4(px, pw, ps, _bias_ptr(bias, N), pc, M, N, K, DTYPE[x.dtype], DTYPE[C.dtype],
+                                ACT[act], float(alpha), pws, _stream_handle(stream)), "mmact_linear_mxfp4")
+
+
+def mmact_moe_workspace_bytes(T: int, H: int, I: int, E: int, top: int) -> int:
+    """Bytes of the workspace that mmact_moe needs."""
+    out = ctypes.c_int64(0)
+    _check(load().mmact_moe_workspace_bytes(int(T), int(H), int(I), int(E), int(top), ctypes.byref(out)),
+           "mmact_moe_workspace_bytes")
+    return out.value
+
+
+_MOE_WORKSPACE: dict = {}
+
+
+def _f32_ptr(t, shape, name: str):
+    if t is None:
+        return None
+    p = _dev(t, name, (torch.float32,))
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return p
+
+
+def mmact_moe(x, router, w1, w2, y, experts, probs, workspace, act: str = "silu", alpha: float = 0.0,
+              gated: bool = True, normalize: bool = True, router_bias=None, b1=None, b2=None, w1_scales=None,
+              w2_scales=None, stream=None) -> None:
+    """A whole mixture-of-experts layer for a few tokens (see include/mmact.h): x [T, H], router [E, H],
+    y [T, H]; w1 [E, 2 I or I, H] and w2 [E, H, I] in x's dtype, or, with w1_scales and w2_scales, the
+    codes of MXFP4 matrices [E * (2 I or I), H] and [E * H, I]; experts [T, top] int32 and probs
+    [T, top] float32 are outputs."""
+    L = load()
+    io = (torch.float16, torch.bfloat16)
+    px, pr, py = _dev(x, "x", io), _dev(router, "router", io), _dev(y, "y", io)
+    pe, pp = _dev(experts, "experts", (torch.int32,)), _dev(probs, "probs", (torch.float32,))
+    if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1] or y.shape != x.shape:
+        raise ValueError("x must be [T, H], router [E, H] and y [T, H]")
+    if router.dtype != x.dtype or y.dtype != x.dtype:
+        raise ValueError("x, router and y must have the same dtype")
+    T, H = x.shape
+    E = router.shape[0]
+    if experts.dim() != 2 or experts.shape[0] != T or probs.shape != experts.shape:
+        raise ValueError("experts and probs must be [T, top]")
+    top = experts.shape[1]
+    halves = 2 if gated else 1
+    mx = w1_scales is not None or w2_scales is not None
+    if mx:
+        if w1_scales is None or w2_scales is None:
+            raise ValueError("w1_scales and w2_scales go together")
+        row = (H + 31) // 32 * 16                   # bytes of one row of w1's codes
+        if E == 0 or H == 0 or w1.numel() % (E * halves * row):
+            raise ValueError("w1 must be the codes of an MXFP4 matrix [E * rows, H]")
+        I = w1.numel() // (E * halves * row)
+        p1, ps1 = _mxfp4_ptrs(w1, w1_scales, E * halves * I, H, "w1")
+        p2, ps2 = _mxfp4_ptrs(w2, w2_scales, E * H, I, "w2")
+        wd = MMACT_MXFP4
+    else:
+        p1, p2, ps1, ps2 = _dev(w1, "w1", (x.dtype,)), _dev(w2, "w2", (x.dtype,)), None, None
+        if w1.dim() != 3 or w2.dim() != 3 or w1.shape[0] != E or w1.shape[2] != H or tuple(w2.shape[:2]) != (E, H):
+            raise ValueError("w1 must be [E, rows, H] and w2 [E, H, I]")
+        I = w2.shape[2]
+        if w1.shape[1] != halves * I:
+            raise ValueError("w1 must have 2 * I rows for each expert (gated), or I")
+        wd = DTYPE[x.dtype]
+    pws = _dev(workspace, "workspace", _BYTES)
+    key = (T, H, I, E, top)
+    need = _MOE_WORKSPACE.get(key)
+    if need is None:
+        if len(_MOE_WORKSPACE) > 1024:
+            _MOE_WORKSPACE.clear()
+        need = _MOE_WORKSPACE[key] = mmact_moe_workspace_bytes(*key)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    _check(L.mmact_moe(px, pr, _f32_ptr(router_bias, (E,), "router_bias"), p1, ps1,
+                       _f32_ptr(b1, (E, halves * I), "b1"), p2, ps2, _f32_ptr(b2, (E, H), "b2"), py, pe, pp, T, H, I, E,
+                       top, DTYPE[x.dtype], wd, ACT[act], float(alpha), 1 if gated else 0, 1 if normalize else 0, pws,
+                       _stream_handle(stream)), "mmact_moe")
 
 
 def mmact_get_last_error(stream=None) -> int:

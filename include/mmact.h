@@ -22,6 +22,15 @@
  *     work".  The *_split variants are that article's two-kernel "half fusion"
  *     (fp32 workspace in device memory, then a separate activation pass), kept
  *     as a measured ablation.
+ *   codes, scales = mxfp4(x); x = values(codes, scales)   mmact_quantize_mxfp4, mmact_dequantize_mxfp4
+ *   C = act(A x B^T + bias), A and B in MXFP4             mmact_gemm_mxfp4, mmact_linear_mxfp4
+ *     Products of 4-bit operands with the same epilogue (OCP Microscaling
+ *     Formats specification 1.0: E2M1 elements, a power-of-two scale for 32).
+ *   y = mixture of experts(x)                             mmact_moe
+ *     Router, choice of experts, both products, activation and weighted sum
+ *     for a few tokens; experts' weights in 16 bits or in MXFP4.
+ *     (The pages have no counterpart of either: these are the operators that
+ *     a model's feed-forward path needs beside the products above.)
  *
  * Activations (all evaluated in fp32 on the fp32 accumulator plus the fp32
  * bias, then rounded to the output dtype with round-to-nearest-even):
@@ -34,6 +43,8 @@
  *   MMACT_ACT_GELU        z/2 * (1 + erf(z / sqrt(2)))   (the fused_matmul_relu
  *                         article's matmul + GELU / Sigmoid / Tanh family; exact
  *                         erf form, the pages print no formula)
+ *   MMACT_ACT_SILU        z / (1 + e^-z)       (mmact_gemm_mxfp4, mmact_linear_mxfp4
+ *                         and mmact_moe only)
  *
  * Conventions for every entry point
  *   - Tensor pointers are DEVICE pointers (cudaMalloc / torch CUDA memory) on
@@ -76,14 +87,16 @@ typedef enum {
     MMACT_ACT_LEAKY_RELU = 2,
     MMACT_ACT_TANH = 3,
     MMACT_ACT_SIGMOID = 4,
-    MMACT_ACT_GELU = 5
+    MMACT_ACT_GELU = 5,
+    MMACT_ACT_SILU = 6   /* MXFP4 products and mmact_moe only */
 } mmact_act;
 
 typedef enum {
     MMACT_F16 = 0,
     MMACT_BF16 = 1,
     MMACT_F32 = 2,   /* as an input: fp32 values used to fp32 accuracy (split precision, below) */
-    MMACT_TF32 = 3   /* input only: fp32 values rounded to tf32 (10 fraction bits) by the tensor core */
+    MMACT_TF32 = 3,  /* input only: fp32 values rounded to tf32 (10 fraction bits) by the tensor core */
+    MMACT_MXFP4 = 4  /* mmact_moe's weights only: 4-bit microscaled (below) */
 } mmact_dtype;
 
 /*
@@ -483,6 +496,101 @@ mmact_status mmact_gemm_kernel_choice(int64_t M, int64_t N, int64_t K, int has_r
  * MMACT_ERR_CUDA when the device cannot be queried.
  */
 mmact_status mmact_gemm_split_k_choice(int64_t M, int64_t N, int64_t K, int *split_k);
+
+/*
+ * The 4-bit microscaled format MXFP4 (OCP Microscaling Formats specification
+ * 1.0).  32 consecutive values along K share a scale X = 2^(b - 127), b one byte
+ * (255: NaN); a value is X times one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign
+ * (codes 0..7, bit 3 the sign).  A matrix [rows, K] is two arrays:
+ *   codes   [rows][KB * 16] bytes, KB = ceil(K / 32); two codes to a byte, the
+ *           even k in the low half; codes past K are 0
+ *   scales  tiles of 512 bytes, [ceil(rows / 128)][ceil(KB / 4)]; the scale of
+ *           row r and block b is byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of
+ *           its tile, the order in which the tensor core reads them; bytes of
+ *           rows and blocks that do not exist are 0
+ * Both arrays are 16-byte aligned.  mmact_mxfp4_size gives their sizes in bytes
+ * (host only; MMACT_ERR_INVALID_ARG for a null pointer or a negative extent).
+ */
+mmact_status mmact_mxfp4_size(int64_t rows, int64_t K, int64_t *codes_bytes, int64_t *scales_bytes);
+
+/*
+ * Quantise x to MXFP4 with blocks along K.
+ *   x  transposed == 0: [rows, K] row-major; transposed != 0: [K, rows]
+ *      row-major (mmact_gemm's B, quantised along its K into the form
+ *      mmact_gemm_mxfp4 takes); x_dtype F16, BF16 or F32
+ *   b = max(floor(log2(largest |x| of the block)) - 2 + 127, 0), values x / X
+ *   rounded to nearest even, saturating at 6 (so up to one eighth of the
+ *   largest value's binade is cut off, as the specification has it).  A block
+ *   with an infinity or a NaN gets b = 255 and codes 0: it reads back as NaN.
+ * Every byte of codes and scales is written.  Results do not depend on the
+ * order of anything: they are exact.
+ */
+mmact_status mmact_quantize_mxfp4(const void *x, void *codes, void *scales, int64_t rows, int64_t K,
+                                  mmact_dtype x_dtype, int transposed, void *stream);
+
+/* y [rows, K] row-major (F16, BF16 or F32) = the values of an MXFP4 matrix, rounded to y_dtype. */
+mmact_status mmact_dequantize_mxfp4(const void *codes, const void *scales, void *y, int64_t rows, int64_t K,
+                                    mmact_dtype y_dtype, void *stream);
+
+/*
+ * C = act(A x B^T + bias) of MXFP4 matrices A [M, K] and B [N, K] (both with
+ * their blocks along K), bias [N] fp32 or NULL, C [M, N] row-major in c_dtype,
+ * accumulated in fp32 on the tensor cores and rounded once.  Any M, N and K:
+ * an N whose rows of C are not a multiple of 16 bytes is stored element by
+ * element (slower).  M == 0 or N == 0 enqueues nothing; K == 0 gives
+ * C = act(bias).  A NaN scale makes the rows or columns of C it reaches NaN.
+ */
+mmact_status mmact_gemm_mxfp4(const void *a_codes, const void *a_scales, const void *b_codes,
+                              const void *b_scales, const float *bias, void *C, int64_t M, int64_t N,
+                              int64_t K, mmact_dtype c_dtype, mmact_act act, float alpha, void *stream);
+
+/*
+ * C = act(q(x) x W^T + bias): x [M, K] row-major in x_dtype (F16, BF16 or F32)
+ * is quantised to MXFP4 on the way in, W [N, K] is held in MXFP4.  The same
+ * result as mmact_quantize_mxfp4 into `workspace` and mmact_gemm_mxfp4.
+ *   workspace  at least mmact_linear_mxfp4_workspace_bytes, 16-byte aligned; calls that may overlap
+ *              on the GPU need one each.
+ */
+mmact_status mmact_linear_mxfp4(const void *x, const void *w_codes, const void *w_scales, const float *bias,
+                                void *C, int64_t M, int64_t N, int64_t K, mmact_dtype x_dtype,
+                                mmact_dtype c_dtype, mmact_act act, float alpha, void *workspace,
+                                void *stream);
+
+/* Bytes of mmact_linear_mxfp4's workspace (host only): x's codes, rounded up to 512, and its scales. */
+mmact_status mmact_linear_mxfp4_workspace_bytes(int64_t M, int64_t K, int64_t *bytes);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (T <= 64), in two kernels:
+ *   logits[t][e] = x[t] . router[e] + router_bias[e]
+ *   experts[t]   = the `top` experts of the largest logits, largest first (equal
+ *                  logits: the lower index first; NaN counts as the largest)
+ *   probs[t][j]  = softmax of the chosen logits (normalize != 0), or of all
+ *                  logits at the chosen experts (normalize == 0)
+ *   h            = act(w1[e, 0:I] x + b1[e, 0:I]) * (w1[e, I:2I] x + b1[e, I:2I])   (gated != 0)
+ *                = act(w1[e] x + b1[e])                                             (gated == 0)
+ *   y[t]         = sum_j probs[t][j] * (w2[e] h + b2[e]), e = experts[t][j]
+ *   x [T, H], router [E, H], y [T, H] in x_dtype (F16 or BF16)
+ *   w1 [E, R1, H], R1 = 2 I (gated) or I; w2 [E, H, I]; w_dtype = x_dtype, or
+ *      MXFP4: w1 the codes of a matrix [E * R1, H] and w1_scales its scale
+ *      tiles, w2 those of [E * H, I]
+ *   router_bias [E], b1 [E, R1], b2 [E, H] fp32, each may be NULL
+ *   experts [T, top] int32 and probs [T, top] fp32 are outputs
+ *   workspace  at least mmact_moe_workspace_bytes, 16-byte aligned, contents
+ *      ignored; calls that may overlap on the GPU need one each
+ * Sums, the softmax and h are held in fp32 (h as two bf16 halves, 16 bits of
+ * it, between the products); y is rounded once.  The sum over j is taken in
+ * order: results repeat bit for bit.  Limits: H and I multiples of 8 and at
+ * least 8, 1 <= top <= min(E, 16), E <= 512, T <= 64, else
+ * MMACT_ERR_UNSUPPORTED.  T == 0 enqueues nothing.
+ */
+mmact_status mmact_moe(const void *x, const void *router, const float *router_bias, const void *w1,
+                       const void *w1_scales, const float *b1, const void *w2, const void *w2_scales,
+                       const float *b2, void *y, int32_t *experts, float *probs, int64_t T, int64_t H,
+                       int64_t I, int64_t E, int64_t top, mmact_dtype x_dtype, mmact_dtype w_dtype,
+                       mmact_act act, float alpha, int gated, int normalize, void *workspace, void *stream);
+
+/* Bytes of mmact_moe's workspace (host only). */
+mmact_status mmact_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, int64_t *bytes);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *mmact_status_string(mmact_status status);
