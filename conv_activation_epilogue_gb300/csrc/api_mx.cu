@@ -2,6 +2,7 @@
 // (include/mmact.h): argument validation and launch planning.  As in api.cu,
 // every check happens on the host before anything is enqueued.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -31,20 +32,30 @@ bool valid_16(mmact_dtype d) { return d == MMACT_F16 || d == MMACT_BF16; }
 bool valid_float(mmact_dtype d) { return valid_16(d) || d == MMACT_F32; }
 bool valid_act(mmact_act a) { return a >= MMACT_ACT_NONE && a <= MMACT_ACT_SILU; }
 
+std::atomic<int> g_mx_kernel{0};   // 0: chosen per shape; 1: rows kernel; 2: pair kernel
+
 // The current device, with this file's kernels set up on it (once per device).
-mmact_status mx_context(DeviceContext *out)
+struct MxContext {
+    DeviceContext dev;
+    int max_pairs;
+};
+
+mmact_status mx_context(MxContext *out)
 {
     static std::mutex mutex;
     static bool ready[MAX_DEVICES];
-    const mmact_status s = device_context(out);
+    static int pairs[MAX_DEVICES];
+    const mmact_status s = device_context(&out->dev);
     if (s != MMACT_OK) return s;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
     std::lock_guard<std::mutex> lock(mutex);
     if (!ready[dev]) {
-        if (setup_mxfp4_kernels() != cudaSuccess) return MMACT_ERR_CUDA;
+        if (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels() != cudaSuccess)
+            return MMACT_ERR_CUDA;
         ready[dev] = true;
     }
+    out->max_pairs = pairs[dev];
     return MMACT_OK;
 }
 
@@ -84,42 +95,98 @@ bool mx_encode(CUtensorMap *mc, CUtensorMap *ms, const void *codes, const void *
            encode_tensor_map(ms, MMACT_F32, 2, scales, ds, ss, bs, false);
 }
 
-// Plan of one product (M, N > 0, K > 0).
-mmact_status mx_gemm_plan(MxGemmLaunch &L, const void *ac, const void *as, const void *bc, const void *bs,
+// Plan of one product: either kernel's launch.
+struct MxPlan {
+    bool pair;
+    MxGemmLaunch P;
+    MxRowsLaunch R;
+};
+
+// Whether a product runs on the pair kernel.
+bool mx_choose_pair(const MxContext &c, int64_t M, int64_t N)
+{
+    const int mode = g_mx_kernel.load();
+    if (c.max_pairs < 1 || mode == 1) return false;
+    if (mode == 2) return true;
+    return M > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= c.max_pairs / 2;
+}
+
+mmact_status mx_gemm_plan(MxPlan &plan, const void *ac, const void *as, const void *bc, const void *bs,
                           const float *bias, void *C, int64_t M, int64_t N, int64_t K, mmact_dtype cd, mmact_act act,
                           float alpha)
 {
-    DeviceContext dev;
-    const mmact_status st = mx_context(&dev);
+    MxContext c;
+    const mmact_status st = mx_context(&c);
     if (st != MMACT_OK) return st;
+    const int nk64 = (int)((mx_blocks(K) + 1) / 2), num_kb = (int)((K + 255) / 256);
+    plan.pair = mx_choose_pair(c, M, N);
+    if (plan.pair) {
+        MxGemmLaunch &L = plan.P;
+        std::memset(&L, 0, sizeof(L));
+        MxGemmArgs &a = L.args;
+        a.M = (int)M;
+        a.N = (int)N;
+        a.nk64 = nk64;
+        a.num_kb = num_kb;
+        a.tiles_m = (int)((M + 255) / 256);
+        a.tiles_n = (int)((N + 255) / 256);
+        a.num_tiles = a.tiles_m * a.tiles_n;
+        a.group_m = 8;
+        a.act = (int)act;
+        a.alpha = alpha;
+        a.bias = bias;
+        a.C = C;
+        a.status = c.dev.status;
+        a.wait_ns = c.dev.wait_ns;
+        const int ce = elem_bytes(cd);
+        a.c_tma = N * ce % 16 == 0 ? 1 : 0;
+        L.out = out_kind(cd);
+        L.grid = 2 * (int)std::min<int64_t>(a.num_tiles, c.max_pairs);
+        if (!mx_encode(&L.tmA, &L.tmSA, ac, as, M, K, 128, 1) || !mx_encode(&L.tmB, &L.tmSB, bc, bs, N, K, 128, 2))
+            return MMACT_ERR_CUDA;
+        if (a.c_tma) {
+            const uint64_t dC[2] = {(uint64_t)N, (uint64_t)M}, sC[1] = {(uint64_t)N * ce};
+            const uint32_t bC[2] = {(uint32_t)(128 / ce), 32};
+            if (!encode_tensor_map(&L.tmC, cd, 2, C, dC, sC, bC, true)) return MMACT_ERR_CUDA;
+        }
+        return MMACT_OK;
+    }
+    MxRowsLaunch &L = plan.R;
     std::memset(&L, 0, sizeof(L));
-    MxGemmArgs &a = L.args;
+    MxRowsArgs &a = L.args;
     a.M = (int)M;
     a.N = (int)N;
-    a.nk64 = (int)((mx_blocks(K) + 1) / 2);
-    a.tiles_m = (int)((M + 127) / 128);
+    a.nk64 = nk64;
+    a.num_kb = num_kb;
     a.tiles_n = (int)((N + 127) / 128);
-    a.num_tiles = a.tiles_m * a.tiles_n;
-    a.num_kb = (int)((K + 255) / 256);
-    a.group_m = 16;
+    const int sms = c.dev.sm_count;
+    // the narrowest tile that takes every row (a narrower one than 128 has to be the only one)
+    int bt = 16;
+    while (bt < 128 && bt < M) bt *= 2;
+    const int64_t tiles = a.tiles_n * ((M + bt - 1) / bt);
+    if (tiles * 8 > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= sms && num_kb >= split * 2) split *= 2;
+    a.kb_per = (num_kb + split - 1) / split;
+    while (split > 1 && (split - 1) * a.kb_per >= num_kb) split /= 2, a.kb_per = (num_kb + split - 1) / split;
+    a.split = split;
     a.act = (int)act;
     a.alpha = alpha;
     a.bias = bias;
     a.C = C;
-    a.status = dev.status;
-    a.wait_ns = dev.wait_ns;
-    const int ce = elem_bytes(cd);
-    a.c_tma = N * ce % 16 == 0 ? 1 : 0;
+    a.status = c.dev.status;
+    a.wait_ns = c.dev.wait_ns;
     L.out = out_kind(cd);
-    L.grid = (int)std::min<int64_t>(a.num_tiles, dev.sm_count);
-    if (!mx_encode(&L.tmA, &L.tmSA, ac, as, M, K, 128, 1) || !mx_encode(&L.tmB, &L.tmSB, bc, bs, N, K, 128, 1))
+    L.bt = bt;
+    L.grid = (int)(tiles * split);
+    if (!mx_encode(&L.tmW, &L.tmSW, bc, bs, N, K, 128, 1) || !mx_encode(&L.tmT, &L.tmST, ac, as, M, K, (uint32_t)bt, 1))
         return MMACT_ERR_CUDA;
-    if (a.c_tma) {
-        const uint64_t dC[2] = {(uint64_t)N, (uint64_t)M}, sC[1] = {(uint64_t)N * ce};
-        const uint32_t bC[2] = {(uint32_t)(128 / ce), 32};
-        if (!encode_tensor_map(&L.tmC, cd, 2, C, dC, sC, bC, true)) return MMACT_ERR_CUDA;
-    }
     return MMACT_OK;
+}
+
+cudaError_t mx_gemm_launch(const MxPlan &plan, cudaStream_t stream)
+{
+    return plan.pair ? launch_gemm_mxfp4_pair(plan.P, stream) : launch_gemm_mxfp4_rows(plan.R, stream);
 }
 
 mmact_status enqueued(cudaError_t e) { return e == cudaSuccess ? MMACT_OK : MMACT_ERR_CUDA; }
@@ -213,9 +280,16 @@ MMACT_EXPORT mmact_status mmact_gemm_mxfp4(const void *a_codes, const void *a_sc
     if (M == 0 || N == 0) return MMACT_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
-    MxGemmLaunch L;
+    MxPlan L;
     s = mx_gemm_plan(L, a_codes, a_scales, b_codes, b_scales, bias, C, M, N, K, c_dtype, act, alpha);
-    return s == MMACT_OK ? enqueued(launch_gemm_mxfp4(L, st)) : s;
+    return s == MMACT_OK ? enqueued(mx_gemm_launch(L, st)) : s;
+}
+
+MMACT_EXPORT mmact_status mmact_set_gemm_mxfp4_kernel(int mode)
+{
+    if (mode < 0 || mode > 2) return MMACT_ERR_INVALID_ARG;
+    g_mx_kernel.store(mode);
+    return MMACT_OK;
 }
 
 MMACT_EXPORT mmact_status mmact_linear_mxfp4_workspace_bytes(int64_t M, int64_t K, int64_t *bytes)
@@ -240,11 +314,11 @@ MMACT_EXPORT mmact_status mmact_linear_mxfp4(const void *x, const void *w_codes,
     if (M == 0 || N == 0) return MMACT_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
-    MxGemmLaunch L;
+    MxPlan L;
     if ((s = mx_gemm_plan(L, codes, scales, w_codes, w_scales, bias, C, M, N, K, c_dtype, act, alpha)) != MMACT_OK)
         return s;
     if ((s = enqueued(quantize_launch(x, codes, scales, M, K, x_dtype, 0, st))) != MMACT_OK) return s;
-    return enqueued(launch_gemm_mxfp4(L, st));
+    return enqueued(mx_gemm_launch(L, st));
 }
 
 MMACT_EXPORT mmact_status mmact_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top,
@@ -280,7 +354,7 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
         !aligned16(workspace) || (mx && (!aligned16(w1_scales) || !aligned16(w2_scales))))
         return MMACT_ERR_UNSUPPORTED;
     DeviceContext dev;
-    if ((s = mx_context(&dev)) != MMACT_OK) return s;
+    if ((s = device_context(&dev)) != MMACT_OK) return s;
     MoeArgs a;
     std::memset(&a, 0, sizeof(a));
     a.T = (int)T;

@@ -1,43 +1,54 @@
 // gemm_mxfp4.cu -- C = act(A x B^T + bias) of two matrices in the 4-bit
-// microscaled format (mxfp4.cuh): A [M, K], B [N, K], tcgen05.mma.kind::mxf4.
+// microscaled format (mxfp4.cuh), A [M, K] and B [N, K], for large outputs:
+// 256 x 256 tiles on CTA pairs, tcgen05.mma.cta_group::2.kind::mxf4.
 //
-// Persistent kernel, one CTA per SM, 128 x 128 output tiles.  A ring stage is
-// 256 K: the codes of 128 rows of A and of B (128-byte rows, TMA with the
-// 128-byte swizzle) and their scale tiles (two tiles of 512 bytes each, TMA).
-// The MMA issuer copies the scale tiles to tensor memory (tcgen05.cp) into
-// columns that belong to the ring stage, so that a copy never overtakes an
-// MMA that still reads the columns: the stage itself is only refilled when
-// that MMA has finished.
+// The arithmetic runs four times as fast as in 16 bits and the operands are a
+// quarter of the size, so the balance of a tile is that of the 16-bit pair
+// kernel: a ring stage is 256 K (128-byte rows of codes) of the CTA's 128 rows of
+// A and 128 rows of B, 16 KB each, by TMA with the 128-byte swizzle, plus 3 KB of
+// scale tiles (its own A rows', all 256 B rows').  The MMA issuer copies the
+// scale tiles into tensor memory (tcgen05.cp) ahead of the stage's MMAs.
 //
-//   warp 0      TMA producer
-//   warp 1      TMEM allocation, scale copies and MMAs
-//   warps 2..5  epilogue
+// Tensor memory: the two 256-column accumulators overlap by 64 columns (0..255
+// and 192..447) to leave 64 columns for scales.  The epilogue of a tile drains
+// the shared columns first and then lets the next tile's MMAs start, so they
+// wait for a quarter of an epilogue at most instead of all of it.  Scales of
+// two stages fit (2 x 24 columns): before the issuer copies a stage's scales it
+// waits until the MMAs that read those columns, two stages earlier, are done,
+// while the stage between them keeps the tensor core busy.
+//
+//   warp 0      (both CTAs) TMA producer; copies complete on the even CTA's barriers
+//   warp 1      TMEM allocation; in the even CTA the scale copies and the MMAs
+//   warps 2..9  (both CTAs) epilogue of the CTA's 128 rows, two warps for each 32
+//
+// Every wait is bounded, and both CTAs pass a final cluster barrier before TMEM
+// is released.
 #include "common.cuh"
 #include "kernels_mx.h"
 #include "mxfp4.cuh"
 
 namespace mmact {
 
-struct MxCfg {
-    static constexpr int BM = 128, BN = 128, BK = 256;
-    static constexpr int A_BYTES = BM * BK / 2, B_BYTES = BN * BK / 2;      // 16 KB each
-    static constexpr int S_BYTES = 1024;                                    // scales of one operand and stage
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * S_BYTES;
-    static constexpr int EPI_BYTES = 4 * 2 * 4096;
+struct MxPairCfg {
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;       // 256 K of 128 rows
+    static constexpr int S_BYTES = 3 * 1024;                             // A: 1 KB, B: 2 KB
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + S_BYTES;
+    static constexpr int EPI_WARPS = 8, EPI_BYTES = EPI_WARPS * 4096;
     static constexpr int STAGES = 5;
-    static constexpr uint32_t ACC_STRIDE = BN, SCALE_COL = 2 * BN, TMEM_COLS = 512;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr uint32_t ACC_STRIDE = 192, SCALE_COL = 448, SLOT_COLS = 24, TMEM_COLS = 512;
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_EPI = OFF_B + STAGES * B_BYTES;
     static constexpr int OFF_S = OFF_EPI + EPI_BYTES;
-    static constexpr int OFF_BAR = OFF_S + STAGES * 2 * S_BYTES;
-    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 5) * 8;
+    static constexpr int OFF_BAR = OFF_S + STAGES * S_BYTES;
+    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-    static_assert(SCALE_COL + STAGES * 16 <= TMEM_COLS, "tensor memory budget");
+    static_assert(SCALE_COL + 2 * SLOT_COLS <= TMEM_COLS, "tensor memory budget");
 };
 
-// Tile t -> (M block, N block), grouped M-first.
+// Pair tile t -> (M block, N block) of 256 x 256, grouped M-first.
 __device__ __forceinline__ void mx_tile(int t, const MxGemmArgs &p, int &mb, int &nb)
 {
     const int per_group = p.group_m * p.tiles_n;
@@ -138,17 +149,20 @@ __device__ __forceinline__ void mx_store_elements(void *C, uint32_t buf, int row
 }
 
 template <int OUT>
-__global__ void __launch_bounds__(192, 1)
-    gemm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                      const __grid_constant__ CUtensorMap tmC, const MxGemmArgs p)
+__global__ void __launch_bounds__(MxPairCfg::THREADS, 1)
+    gemm_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                           const __grid_constant__ CUtensorMap tmC, const MxGemmArgs p)
 {
-    using Cfg = MxCfg;
+    using Cfg = MxPairCfg;
     constexpr int STAGES = Cfg::STAGES;
     constexpr int COLS = OUT == OUT_F32 ? 32 : 64;
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = ptx::smem_addr(smem);
+    const uint32_t rank = ptx::cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
 
     ptx::griddep_launch_dependents();
     const bool aligned = (base & 1023u) == 0;
@@ -158,9 +172,9 @@ __global__ void __launch_bounds__(192, 1)
     Pipe pp;
     pp.full0 = base + Cfg::OFF_BAR;
     pp.empty0 = pp.full0 + 8 * STAGES;
-    pp.tfull0 = pp.empty0 + 8 * STAGES;
-    pp.tempty0 = pp.tfull0 + 16;
-    pp.drain = pp.tempty0 + 16;
+    pp.tfull0 = pp.empty0 + 8 * STAGES;       // two, one for each accumulator
+    pp.tempty0 = pp.tfull0 + 16;              // one: the shared columns of the last tile are drained
+    pp.drain = pp.tempty0 + 8;
     pp.abort = misc + 1;
     pp.status = p.status;
     pp.wait_ns = p.wait_ns;
@@ -172,116 +186,134 @@ __global__ void __launch_bounds__(192, 1)
                 ptx::mbar_init(pp.full0 + 8 * s, 1);
                 ptx::mbar_init(pp.empty0 + 8 * s, 1);
             }
-            for (int a = 0; a < 2; ++a) {
-                ptx::mbar_init(pp.tfull0 + 8 * a, 1);
-                ptx::mbar_init(pp.tempty0 + 8 * a, 4);
-            }
+            ptx::mbar_init(pp.tfull0, 1);
+            ptx::mbar_init(pp.tfull0 + 8, 1);
+            ptx::mbar_init(pp.tempty0, 2 * Cfg::EPI_WARPS);
             ptx::mbar_init(pp.drain, 1);
             misc[1] = 0;
             ptx::fence_mbar_init();
         }
         if (warp == 1) {
-            ptx::tmem_alloc(base + Cfg::OFF_MISC, Cfg::TMEM_COLS);
-            ptx::tmem_relinquish();
+            ptx::tmem_alloc_pair(base + Cfg::OFF_MISC, Cfg::TMEM_COLS);
+            ptx::tmem_relinquish_pair();
         }
     }
     ptx::tc_fence_before();
     ptx::cta_sync();
     ptx::tc_fence_after();
+    ptx::cluster_sync();
     pp.tmem = misc[0];
+    // the pair's MMAs address both CTAs' tensor memory by the even CTA's columns
+    const bool usable = aligned && ptx::ld_cluster_u32(ptx::mapa(base + Cfg::OFF_MISC, rank ^ 1u)) == pp.tmem;
+    if (aligned && !usable && threadIdx.x == 0) atomicOr(p.status, ST_PAIR_TMEM);
     ptx::griddep_wait();
-
     const uint32_t sA = base + Cfg::OFF_A, sB = base + Cfg::OFF_B, sS = base + Cfg::OFF_S;
-    if (aligned && warp == 0) {
+    ptx::cluster_sync();
+
+    if (usable && warp == 0) {
         if (lane == 0) {
-            uint32_t stage = 0, phase = 0, issued = 0;
+            uint32_t stage = 0, phase = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < p.num_tiles && ok; t += gridDim.x) {
+            for (int t = pair; t < p.num_tiles && ok; t += npairs) {
                 int mb, nb;
                 mx_tile(t, p, mb, nb);
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!pipe_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) { ok = false; break; }
                     const uint32_t fb = pp.full0 + 8 * stage;
-                    ptx::mbar_arrive_expect_tx(fb, (uint32_t)Cfg::STAGE_BYTES);
-                    ptx::tma_load_2d(sA + stage * Cfg::A_BYTES, &tmA, fb, kb * 64, mb * 128);
-                    ptx::tma_load_2d(sB + stage * Cfg::B_BYTES, &tmB, fb, kb * 64, nb * 128);
-                    ptx::tma_load_2d(sS + stage * 2048u, &tmSA, fb, kb * 256, mb);
-                    ptx::tma_load_2d(sS + stage * 2048u + 1024u, &tmSB, fb, kb * 256, nb);
-                    ++issued;
+                    if (leader) ptx::mbar_arrive_expect_tx(fb, 2u * Cfg::STAGE_BYTES);
+                    const uint32_t to = ptx::mapa(fb, 0);
+                    ptx::tma_load_2d_pair(sA + stage * Cfg::A_BYTES, &tmA, to, kb * 64, mb * 256 + (int)rank * 128);
+                    ptx::tma_load_2d_pair(sB + stage * Cfg::B_BYTES, &tmB, to, kb * 64, nb * 256 + (int)rank * 128);
+                    ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES, &tmSA, to, kb * 256, mb * 2 + (int)rank);
+                    ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES + 1024u, &tmSB, to, kb * 256, nb * 2);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
             if (!ok) pipe_fail(pp);
-            // Every copy has landed before the CTA exits (the MMA issuer may have given up
-            // before it consumed them): the last STAGES uses, oldest first.
-            const uint32_t n = issued < (uint32_t)STAGES ? issued : (uint32_t)STAGES;
-            for (uint32_t u = issued - n; u < issued; ++u)
-                ptx::mbar_wait_bounded(pp.full0 + 8 * (u % STAGES), (u / STAGES) & 1u, DRAIN_NS, nullptr);
         }
-    } else if (aligned && warp == 1) {
-        if (lane == 0) {
-            const uint32_t id0 = ptx::idesc_mxf4(128, Cfg::BN, 0, 0), id2 = ptx::idesc_mxf4(128, Cfg::BN, 2, 2);
-            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+    } else if (usable && warp == 1) {
+        if (leader) {                                         // the whole warp: see mma_mxf4
+            const uint32_t id0 = ptx::idesc_mxf4(256, 256, 0, 0), id2 = ptx::idesc_mxf4(256, 256, 2, 2);
+            uint32_t stage = 0, phase = 0, use = 0, tile = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < p.num_tiles && ok; t += gridDim.x) {
-                if (!pipe_wait(pp, pp.tempty0 + 8 * acc, acc_phase ^ 1u)) { ok = false; break; }
+            for (int t = pair; t < p.num_tiles && ok; t += npairs, ++tile) {
+                // the shared columns of the previous tile's accumulator, and all of the one before it
+                if (tile != 0 && !mx_warp_wait(pp, pp.tempty0, (tile - 1) & 1u)) { ok = false; break; }
                 ptx::tc_fence_after();
-                const uint32_t d = pp.tmem + acc * Cfg::ACC_STRIDE;
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!pipe_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
+                const uint32_t d = pp.tmem + (tile & 1u) * Cfg::ACC_STRIDE;
+                for (int kb = 0; kb < p.num_kb; ++kb, ++use) {
+                    if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
+                    // the MMAs that read this stage's scale columns, two stages ago
+                    if (use >= 2) {
+                        const uint32_t u = use - 2;
+                        if (!mx_warp_wait(pp, pp.empty0 + 8 * (u % STAGES), (u / STAGES) & 1u)) { ok = false; break; }
+                    }
                     ptx::tc_fence_after();
                     const uint32_t a0 = sA + stage * Cfg::A_BYTES, b0 = sB + stage * Cfg::B_BYTES;
-                    const uint32_t s0 = sS + stage * 2048u, ts = pp.tmem + Cfg::SCALE_COL + stage * 16u;
+                    const uint32_t s0 = sS + stage * Cfg::S_BYTES;
+                    const uint32_t ts = pp.tmem + Cfg::SCALE_COL + (use & 1u) * Cfg::SLOT_COLS;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        ptx::tmem_cp_scales(ts + 4 * j, ptx::smem_desc(s0 + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
-                        ptx::tmem_cp_scales(ts + 8 + 4 * j,
-                                            ptx::smem_desc(s0 + 1024u + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
+                    for (int j = 0; j < 2; ++j) {                 // B: two times eight columns, then A: two times four
+                        ptx::tmem_cp_scales_pair(ts + 8 * j, ptx::smem_desc(s0 + 1024u + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
+                        ptx::tmem_cp_scales_pair(ts + 8 * j + 4,
+                                                 ptx::smem_desc(s0 + 2048u + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
+                        ptx::tmem_cp_scales_pair(ts + 16 + 4 * j, ptx::smem_desc(s0 + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
                     }
                     const int n = min(4, p.nk64 - 4 * kb);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (k < n)
-                            ptx::mma_mxf4(d, ptx::smem_desc(a0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B),
-                                          ptx::smem_desc(b0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B),
-                                          k & 1 ? id2 : id0, ts + 4 * (k >> 1), ts + 8 + 4 * (k >> 1),
-                                          (kb | k) != 0 ? 1u : 0u);
-                    ptx::mma_commit(pp.empty0 + 8 * stage);
+                            ptx::mma_mxf4_pair(d, ptx::smem_desc(a0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B),
+                                               ptx::smem_desc(b0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B),
+                                               k & 1 ? id2 : id0, ts + 16 + 4 * (k >> 1), ts + 8 * (k >> 1),
+                                               (kb | k) != 0 ? 1u : 0u);
+                    ptx::commit_elected_pair(pp.empty0 + 8 * stage, 3);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
                 if (!ok) break;
-                ptx::mma_commit(pp.tfull0 + 8 * acc);
-                acc ^= 1u;
-                if (acc == 0) acc_phase ^= 1u;
+                ptx::commit_elected_pair(pp.tfull0 + 8 * (tile & 1u), 3);
             }
-            if (!ok) pipe_fail(pp);
-            ptx::mma_commit(pp.drain);
+            if (!ok && lane == 0) pipe_fail(pp);
+            ptx::commit_elected_pair(pp.drain, 1);
             ptx::mbar_wait_bounded(pp.drain, 0, DRAIN_NS, nullptr);
         }
-    } else if (aligned) {
-        const int q = warp & 3;
-        const uint32_t my_buf = base + Cfg::OFF_EPI + (uint32_t)q * 8192u;
-        uint32_t acc = 0, acc_phase = 0, units = 0;
-        for (int t = blockIdx.x; t < p.num_tiles; t += gridDim.x) {
+    } else if (usable) {
+        const int q = warp & 3, part = (warp - 2) >> 2;
+        const uint32_t buf = base + Cfg::OFF_EPI + (uint32_t)(warp - 2) * 4096u;
+        const uint32_t tempty_leader = ptx::mapa(pp.tempty0, 0);
+        const uint64_t pol_c = ptx::createpolicy_evict_first();   // C is not read back here
+        constexpr int NU = 256 / COLS, SHARED = 64 / COLS;        // units of a tile; of its shared columns
+        uint32_t tile = 0;
+        for (int t = pair; t < p.num_tiles; t += npairs, ++tile) {
             int mb, nb;
             mx_tile(t, p, mb, nb);
-            if (!warp_epi_wait(pp, pp.tfull0 + 8 * acc, acc_phase)) { pipe_fail(pp); break; }
+            if (!warp_epi_wait(pp, pp.tfull0 + 8 * (tile & 1u), (tile >> 1) & 1u)) { pipe_fail(pp); break; }
             ptx::tc_fence_after();
-            const uint32_t tbase = pp.tmem + ((uint32_t)(q * 32) << 16) + acc * Cfg::ACC_STRIDE;
-            const int row0 = mb * 128 + q * 32;
+            const uint32_t tbase = pp.tmem + ((uint32_t)(q * 32) << 16) + (tile & 1u) * Cfg::ACC_STRIDE;
+            const int row0 = mb * 256 + (int)rank * 128 + q * 32;
+            // the shared columns are the last of the lower accumulator and the first of the upper one
+            const int first = (tile & 1u) == 0 ? NU - SHARED : 0;
 #pragma unroll 1
-            for (int u = 0; u < Cfg::BN / COLS; ++u) {
-                const uint32_t buf = my_buf + (units++ & 1u) * 4096u;
-                const int col0 = nb * Cfg::BN + u * COLS;
-                if (lane == 0) ptx::bulk_wait_read<1>();
+            for (int i = part; i < NU; i += 2) {
+                const int u = (first + i) & (NU - 1);
+                const int col0 = nb * 256 + u * COLS;
+                if (lane == 0) ptx::bulk_wait_read<0>();
                 __syncwarp();
                 mx_epi_unit<OUT>(p.act, tbase + u * COLS, p.bias != nullptr ? p.bias + col0 : nullptr, p.N - col0,
                                  p.alpha, buf, lane);
+                if (i < 2) {                                      // after the first unit of each warp
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) ptx::mbar_arrive(pp.tempty0);
+                        else ptx::mbar_arrive_cluster(tempty_leader);
+                    }
+                }
                 if (p.c_tma) {
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && row0 < p.M && col0 < p.N) {
-                        ptx::tma_store_2d(&tmC, buf, col0, row0);
+                        ptx::tma_store_2d_hint(&tmC, buf, col0, row0, pol_c);
                         ptx::bulk_commit();
                     }
                 } else {
@@ -290,49 +322,66 @@ __global__ void __launch_bounds__(192, 1)
                     __syncwarp();
                 }
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(pp.tempty0 + 8 * acc);
-            acc ^= 1u;
-            if (acc == 0) acc_phase ^= 1u;
         }
         if (lane == 0) ptx::bulk_wait<0>();
         __syncwarp();
     }
+
+    // No commit, copy or arrival is still addressed to either CTA after this.
     ptx::tc_fence_before();
+    ptx::cluster_sync();
     ptx::cta_sync();
     __syncwarp();
     if (aligned && warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(pp.tmem, Cfg::TMEM_COLS);
+        ptx::tmem_dealloc_pair(pp.tmem, Cfg::TMEM_COLS);
     }
 }
 
+static void pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int grid, cudaStream_t stream)
+{
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(MxPairCfg::THREADS);
+    cfg.dynamicSmemBytes = MxPairCfg::SMEM_BYTES;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+}
+
 template <int OUT>
-static cudaError_t launch_mx_t(const MxGemmLaunch &L, cudaStream_t stream)
+static cudaError_t launch_mx_pair_t(const MxGemmLaunch &L, cudaStream_t stream)
 {
-    return launch_k(gemm_mxfp4_kernel<OUT>, dim3((unsigned)L.grid), dim3(192), MxCfg::SMEM_BYTES, stream, L.tmA, L.tmB,
-                    L.tmSA, L.tmSB, L.tmC, L.args);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    pair_config(cfg, attr, L.grid, stream);
+    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_pair_kernel<OUT>, L.tmA, L.tmB, L.tmSA, L.tmSB, L.tmC, L.args);
 }
 
-cudaError_t setup_mxfp4_kernels()
+cudaError_t setup_mxfp4_pair_kernels(int *max_pairs)
 {
-    cudaError_t e = cudaFuncSetAttribute(gemm_mxfp4_kernel<OUT_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         MxCfg::SMEM_BYTES);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(gemm_mxfp4_kernel<OUT_F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 MxCfg::SMEM_BYTES);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(gemm_mxfp4_kernel<OUT_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 MxCfg::SMEM_BYTES);
-    return e;
+    const auto attr_of = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(gemm_mxfp4_pair_kernel<OUT_BF16>, attr_of, MxPairCfg::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_mxfp4_pair_kernel<OUT_F16>, attr_of, MxPairCfg::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_mxfp4_pair_kernel<OUT_F32>, attr_of, MxPairCfg::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    pair_config(cfg, attr, 2 * 128, nullptr);
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(max_pairs, gemm_mxfp4_pair_kernel<OUT_BF16>, &cfg);
 }
 
-cudaError_t launch_gemm_mxfp4(const MxGemmLaunch &L, cudaStream_t stream)
+cudaError_t launch_gemm_mxfp4_pair(const MxGemmLaunch &L, cudaStream_t stream)
 {
-    if (L.out == OUT_BF16) return launch_mx_t<OUT_BF16>(L, stream);
-    if (L.out == OUT_F16) return launch_mx_t<OUT_F16>(L, stream);
-    return launch_mx_t<OUT_F32>(L, stream);
+    if (L.out == OUT_BF16) return launch_mx_pair_t<OUT_BF16>(L, stream);
+    if (L.out == OUT_F16) return launch_mx_pair_t<OUT_F16>(L, stream);
+    return launch_mx_pair_t<OUT_F32>(L, stream);
 }
 
 }  // namespace mmact

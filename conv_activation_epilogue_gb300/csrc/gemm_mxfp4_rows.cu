@@ -1,0 +1,322 @@
+// gemm_mxfp4_rows.cu -- C = act(A x B^T + bias) of MXFP4 matrices when the output
+// has few rows or few tiles: the weights B are the work, and every SM has to be
+// reading them.
+//
+// The operands change sides: an output tile is 128 rows of B (the MMA's 128
+// accumulator lanes) by BT rows of A (16 to 128, its columns), so that a product
+// with one row of A loads 128-row boxes of weights and 2 KB of everything else.
+// The K loop of a tile is shared by a cluster of S CTAs, each over a consecutive
+// range of K; their fp32 partial tiles meet in shared memory, each CTA adding up
+// a slice of BT / S columns over the cluster in rank order (so results repeat),
+// then bias, activation and the stores: consecutive lanes hold consecutive
+// columns of C.
+//
+// The scales of A's rows are read from the first column of a scale tile on: a
+// tile narrower than 128 rows is always the only one, because the MMA takes no
+// scale address that is not a multiple of four columns.
+//
+//   warp 0      TMA producer: a ring of stages of 256 K (codes with the 128-byte
+//               swizzle, scale tiles).  While the kernel before this one in the
+//               stream still runs (it may be writing A's codes) the producer
+//               already brings the CTA's first weight boxes to L2.
+//   warp 1      TMEM allocation, scale copies into columns of the ring stage, MMAs
+//   warps 2..5  partial tile, reduction, epilogue
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels_mx.h"
+#include "mxfp4.cuh"
+
+namespace mmact {
+
+template <int BT>
+struct MxRowsCfg {
+    static constexpr int W_BYTES = 128 * 128, T_BYTES = BT * 128, S_BYTES = 2 * 1024;
+    static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + S_BYTES;
+    static constexpr int STAGES = BT <= 64 ? 8 : 6;
+    static constexpr uint32_t SCALE_COL = BT;                            // 16 columns for each stage
+    static constexpr uint32_t TMEM_COLS = BT + 16 * STAGES <= 256 ? 256 : 512;
+    static constexpr int OFF_W = 0;
+    static constexpr int OFF_T = OFF_W + STAGES * W_BYTES;
+    static constexpr int OFF_S = OFF_T + STAGES * T_BYTES;
+    static constexpr int OFF_BAR = OFF_S + STAGES * S_BYTES;
+    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2) * 8;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16;
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(BT + 16 * STAGES <= TMEM_COLS, "tensor memory budget");
+    static_assert(BT * 512 <= STAGES * W_BYTES, "the partial tile takes the ring's place");
+};
+
+// C[m0 + j][n] = act(z[j] + bias) for this lane's n and the rows that exist:
+// element stores, a warp covering 32 consecutive n.
+template <int OUT, int CH>
+__device__ __forceinline__ void rows_store(const MxRowsArgs &p, int m0, int n, float (&z)[CH], float bias)
+{
+#pragma unroll
+    for (int j = 0; j < CH; ++j) z[j] += bias;
+    act_mx_all(p.act, z, p.alpha);
+    if (n >= p.N) return;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        if (m0 + j >= p.M) break;
+        const int64_t at = (int64_t)(m0 + j) * p.N + n;
+        if constexpr (OUT == OUT_F32) static_cast<float *>(p.C)[at] = z[j];
+        else if constexpr (OUT == OUT_BF16) static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(z[j]);
+        else static_cast<__half *>(p.C)[at] = __float2half_rn(z[j]);
+    }
+}
+
+// Sum of CH columns of the cluster's partial tiles at this thread's lane, in rank
+// order: all loads of a rank in flight together.
+template <int CH>
+__device__ __forceinline__ void cluster_columns(uint32_t at, int split, float (&z)[CH])
+{
+#pragma unroll
+    for (int j = 0; j < CH; ++j) z[j] = 0.0f;
+#pragma unroll 2
+    for (int s = 0; s < split; ++s) {
+        const uint32_t from = ptx::mapa(at, (uint32_t)s);
+        float v[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) v[j] = ptx::ld_cluster_f32(from + j * 512u);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) z[j] += v[j];
+    }
+}
+
+template <int OUT, int BT>
+__global__ void __launch_bounds__(192, 1)
+    gemm_mxfp4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
+                           const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmST,
+                           const MxRowsArgs p)
+{
+    using Cfg = MxRowsCfg<BT>;
+    constexpr int STAGES = Cfg::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t base = ptx::smem_addr(smem);
+    const int rank = p.split > 1 ? (int)ptx::cluster_ctarank() : 0;
+    const int tile = blockIdx.x / p.split;
+    const int nb = tile % p.tiles_n, tb = tile / p.tiles_n;
+    const int kb0 = rank * p.kb_per, kb1 = min(p.num_kb, kb0 + p.kb_per);
+
+    ptx::griddep_launch_dependents();
+    const bool aligned = (base & 1023u) == 0;
+    if (!aligned && threadIdx.x == 0) atomicOr(p.status, ST_SMEM_ALIGN);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
+    Pipe pp;
+    pp.full0 = base + Cfg::OFF_BAR;
+    pp.empty0 = pp.full0 + 8 * STAGES;
+    pp.tfull0 = pp.empty0 + 8 * STAGES;
+    pp.drain = pp.tfull0 + 8;
+    pp.tempty0 = 0;
+    pp.abort = misc + 1;
+    pp.status = p.status;
+    pp.wait_ns = p.wait_ns;
+    if (aligned) {
+        if (threadIdx.x == 0) {
+            ptx::prefetch_tensormap(&tmW);
+            ptx::prefetch_tensormap(&tmT);
+            for (int s = 0; s < STAGES; ++s) {
+                ptx::mbar_init(pp.full0 + 8 * s, 1);
+                ptx::mbar_init(pp.empty0 + 8 * s, 1);
+            }
+            ptx::mbar_init(pp.tfull0, 1);
+            ptx::mbar_init(pp.drain, 1);
+            misc[1] = 0;
+            ptx::fence_mbar_init();
+            for (int kb = kb0; kb < min(kb1, kb0 + STAGES); ++kb) {
+                ptx::tma_prefetch_2d(&tmW, kb * 64, nb * 128);
+                ptx::tma_prefetch_2d(&tmSW, kb * 256, nb);
+            }
+        }
+        if (warp == 1) {
+            ptx::tmem_alloc(base + Cfg::OFF_MISC, Cfg::TMEM_COLS);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    ptx::cta_sync();
+    ptx::tc_fence_after();
+    pp.tmem = misc[0];
+    ptx::griddep_wait();
+
+    const uint32_t sW = base + Cfg::OFF_W, sT = base + Cfg::OFF_T, sS = base + Cfg::OFF_S;
+    if (aligned && warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int issued = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+                const uint32_t stage = (uint32_t)issued % STAGES, phase = ((uint32_t)issued / STAGES) & 1u;
+                if (!pipe_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) { ok = false; break; }
+                const uint32_t fb = pp.full0 + 8 * stage;
+                ptx::mbar_arrive_expect_tx(fb, (uint32_t)Cfg::STAGE_BYTES);
+                ptx::tma_load_2d(sW + stage * Cfg::W_BYTES, &tmW, fb, kb * 64, nb * 128);
+                ptx::tma_load_2d(sS + stage * Cfg::S_BYTES, &tmSW, fb, kb * 256, nb);
+                ptx::tma_load_2d(sT + stage * Cfg::T_BYTES, &tmT, fb, kb * 64, tb * BT);
+                ptx::tma_load_2d(sS + stage * Cfg::S_BYTES + 1024u, &tmST, fb, kb * 256, tb);
+            }
+            if (!ok) pipe_fail(pp);
+            // every copy has landed before the ring's memory is used again or the CTA exits
+            for (int u = max(0, issued - STAGES); u < issued; ++u)
+                ptx::mbar_wait_bounded(pp.full0 + 8 * (u % STAGES), (u / STAGES) & 1, DRAIN_NS, nullptr);
+        }
+    } else if (aligned && warp == 1) {
+        {                                                     // the whole warp: see mma_mxf4
+            const uint32_t id0 = ptx::idesc_mxf4(128, BT, 0, 0), id2 = ptx::idesc_mxf4(128, BT, 2, 2);
+            bool ok = true;
+            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+                const uint32_t stage = (uint32_t)i % STAGES, phase = ((uint32_t)i / STAGES) & 1u;
+                if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
+                ptx::tc_fence_after();
+                const uint32_t w0 = sW + stage * Cfg::W_BYTES, t0 = sT + stage * Cfg::T_BYTES;
+                const uint32_t s0 = sS + stage * Cfg::S_BYTES, ts = pp.tmem + Cfg::SCALE_COL + stage * 16u;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    ptx::tmem_cp_scales(ts + 4 * j, ptx::smem_desc(s0 + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
+                    ptx::tmem_cp_scales(ts + 8 + 4 * j,
+                                        ptx::smem_desc(s0 + 1024u + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
+                }
+                const int n = min(4, p.nk64 - 4 * kb);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < n)
+                        ptx::mma_mxf4(pp.tmem, ptx::smem_desc(w0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B),
+                                      ptx::smem_desc(t0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B), k & 1 ? id2 : id0,
+                                      ts + 4 * (k >> 1), ts + 8 + 4 * (k >> 1), (i | k) != 0 ? 1u : 0u);
+                ptx::commit_elected(pp.empty0 + 8 * stage);
+            }
+            if (ok) ptx::commit_elected(pp.tfull0);
+            else if (lane == 0) pipe_fail(pp);
+            ptx::commit_elected(pp.drain);
+            ptx::mbar_wait_bounded(pp.drain, 0, DRAIN_NS, nullptr);
+        }
+    }
+    __syncwarp();
+    // The epilogue warps take part in cluster barriers with the others below, so
+    // the partial tile is read out in one place for every warp's control flow.
+    const int q = warp & 3, n = nb * 128 + q * 32 + lane;
+    const bool epi = warp >= 2;
+    const float bias = epi && p.bias != nullptr && n < p.N ? p.bias[n] : 0.0f;
+    bool good = aligned;
+    if (epi && aligned) {
+        if (!warp_epi_wait(pp, pp.tfull0, 0)) {
+            pipe_fail(pp);
+            good = false;
+        }
+        ptx::tc_fence_after();
+    }
+    const uint32_t taddr = pp.tmem + ((uint32_t)(q * 32) << 16);
+    if (p.split == 1) {
+        if (epi && good) {
+#pragma unroll 1
+            for (int c = 0; c < BT; c += 16) {
+                if (tb * BT + c >= p.M) break;
+                uint32_t r[16];
+                float z[16];
+                ptx::tmem_ld16(taddr + c, r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(r[j]);
+                rows_store<OUT>(p, tb * BT + c, n, z, bias);
+                __syncwarp();
+            }
+        }
+    } else {
+        // partial tile [column][lane] over the ring, whose copies and MMAs are done
+        float *part = reinterpret_cast<float *>(smem);
+        if (epi && good) {
+#pragma unroll 1
+            for (int c = 0; c < BT; c += 16) {
+                uint32_t r[16];
+                ptx::tmem_ld16(taddr + c, r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) part[(c + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
+            }
+        }
+        ptx::cluster_sync();
+        if (epi && good) {
+            // this CTA's slice of the columns: 16 at a time, or the 2 to 8 it has
+            const int cols = BT / p.split, c0 = rank * cols;
+            const uint32_t at = base + (uint32_t)(c0 * 128 + q * 32 + lane) * 4u;
+            auto slice = [&](auto ch) {
+                constexpr int CH = decltype(ch)::value;
+                for (int c = 0; c < cols && tb * BT + c0 + c < p.M; c += CH) {
+                    float z[CH];
+                    cluster_columns<CH>(at + c * 512u, p.split, z);
+                    rows_store<OUT>(p, tb * BT + c0 + c, n, z, bias);
+                }
+            };
+            if (cols >= 16) slice(std::integral_constant<int, 16>());
+            else if (cols == 8) slice(std::integral_constant<int, 8>());
+            else if (cols == 4) slice(std::integral_constant<int, 4>());
+            else slice(std::integral_constant<int, 2>());
+        }
+        ptx::cluster_sync();                                  // no CTA exits while its partial tile is read
+    }
+    ptx::tc_fence_before();
+    ptx::cta_sync();
+    __syncwarp();
+    if (aligned && warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(pp.tmem, Cfg::TMEM_COLS);
+    }
+}
+
+template <int OUT, int BT>
+static cudaError_t launch_rows_t(const MxRowsLaunch &L, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)L.grid);
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = MxRowsCfg<BT>::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)L.args.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.args.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_rows_kernel<OUT, BT>, L.tmW, L.tmT, L.tmSW, L.tmST, L.args);
+}
+
+template <int OUT>
+static cudaError_t launch_rows_o(const MxRowsLaunch &L, cudaStream_t stream)
+{
+    switch (L.bt) {
+    case 16: return launch_rows_t<OUT, 16>(L, stream);
+    case 32: return launch_rows_t<OUT, 32>(L, stream);
+    case 64: return launch_rows_t<OUT, 64>(L, stream);
+    default: return launch_rows_t<OUT, 128>(L, stream);
+    }
+}
+
+template <int OUT>
+static cudaError_t setup_rows_o()
+{
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, 16>, attr, MxRowsCfg<16>::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, 32>, attr, MxRowsCfg<32>::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, 64>, attr, MxRowsCfg<64>::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, 128>, attr, MxRowsCfg<128>::SMEM_BYTES);
+    return e;
+}
+
+cudaError_t setup_mxfp4_rows_kernels()
+{
+    cudaError_t e = setup_rows_o<OUT_BF16>();
+    if (e == cudaSuccess) e = setup_rows_o<OUT_F16>();
+    if (e == cudaSuccess) e = setup_rows_o<OUT_F32>();
+    return e;
+}
+
+cudaError_t launch_gemm_mxfp4_rows(const MxRowsLaunch &L, cudaStream_t stream)
+{
+    if (L.out == OUT_BF16) return launch_rows_o<OUT_BF16>(L, stream);
+    if (L.out == OUT_F16) return launch_rows_o<OUT_F16>(L, stream);
+    return launch_rows_o<OUT_F32>(L, stream);
+}
+
+}  // namespace mmact

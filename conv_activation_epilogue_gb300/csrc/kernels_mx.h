@@ -37,8 +37,34 @@ struct MxGemmLaunch {
     int grid;
 };
 
-cudaError_t setup_mxfp4_kernels();
-cudaError_t launch_gemm_mxfp4(const MxGemmLaunch &L, cudaStream_t stream);
+cudaError_t setup_mxfp4_pair_kernels(int *max_pairs);   // max_pairs: CTA pairs resident at once
+cudaError_t launch_gemm_mxfp4_pair(const MxGemmLaunch &L, cudaStream_t stream);
+
+// The same product with few rows or tiles: W = B's rows on the MMA's 128 lanes,
+// T = A's rows on its columns, the K blocks of a tile shared by a cluster.
+struct MxRowsArgs {
+    int M, N;
+    int nk64, num_kb;    // as above
+    int tiles_n;         // tiles of 128 rows of B
+    int split, kb_per;   // CTAs of a tile's cluster, K blocks of each
+    int act;
+    float alpha;
+    const float *bias;
+    void *C;
+    unsigned int *status;
+    unsigned long long wait_ns;
+};
+
+struct MxRowsLaunch {
+    CUtensorMap tmW, tmT, tmSW, tmST;
+    MxRowsArgs args;
+    int out;
+    int bt;              // rows of A in a tile: 16, 32, 64 or 128
+    int grid;
+};
+
+cudaError_t setup_mxfp4_rows_kernels();
+cudaError_t launch_gemm_mxfp4_rows(const MxRowsLaunch &L, cudaStream_t stream);
 
 // A mixture-of-experts layer for a few tokens.
 struct MoeArgs {

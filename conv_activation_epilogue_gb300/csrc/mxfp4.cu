@@ -10,14 +10,6 @@ namespace mmact {
 enum : int { IN_F32 = OUT_F32, IN_F16 = OUT_F16, IN_BF16 = OUT_BF16 };
 
 template <int T>
-__device__ __forceinline__ float load1(const void *p, int64_t i)
-{
-    if constexpr (T == IN_F32) return static_cast<const float *>(p)[i];
-    else if constexpr (T == IN_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    else return __half2float(static_cast<const __half *>(p)[i]);
-}
-
-template <int T>
 __device__ __forceinline__ void store1(void *p, int64_t i, float v)
 {
     if constexpr (T == IN_F32) static_cast<float *>(p)[i] = v;
@@ -25,38 +17,79 @@ __device__ __forceinline__ void store1(void *p, int64_t i, float v)
     else static_cast<__half *>(p)[i] = __float2half_rn(v);
 }
 
-// Eight consecutive values x[i..i+8) (those at or past `n` are 0).
+// Eight consecutive values x[i..i+8) as raw 32-bit words, two 16-bit values or
+// one fp32 to a word (values at or past `n` are 0).
+template <int T>
+struct Raw8 {
+    static constexpr int WORDS = T == IN_F32 ? 8 : 4;
+    uint32_t w[WORDS];
+};
+
 template <int T, bool VEC>
-__device__ __forceinline__ void load8(const void *x, int64_t i, int n, float (&v)[8])
+__device__ __forceinline__ void load8(const void *x, int64_t i, int n, Raw8<T> &r)
 {
     if (VEC && n >= 8) {
-        if constexpr (T == IN_F32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
-            const float4 a = __ldcs(p), b = __ldcs(p + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i));
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack2<T>(w[j]);
-                v[2 * j] = f.x;
-                v[2 * j + 1] = f.y;
-            }
+        for (int j = 0; j < Raw8<T>::WORDS / 4; ++j) {
+            const char *p = static_cast<const char *>(x) + i * (T == IN_F32 ? 4 : 2) + 16 * j;
+            const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
+            r.w[4 * j] = u.x, r.w[4 * j + 1] = u.y, r.w[4 * j + 2] = u.z, r.w[4 * j + 3] = u.w;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? load1<T>(x, i + j) : 0.0f;
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (T == IN_F32) {
+                r.w[j] = j < n ? static_cast<const uint32_t *>(x)[i + j] : 0u;
+            } else {
+                const uint32_t v = j < n ? static_cast<const uint16_t *>(x)[i + j] : 0u;
+                r.w[j / 2] = j % 2 == 0 ? v : r.w[j / 2] | (v << 16);
+            }
+        }
     }
+}
+
+// The largest |value| of raw words so far: of 16-bit types in each half of `m`
+// (their magnitudes order as unsigned integers, infinities and NaN on top).
+template <int T>
+__device__ __forceinline__ uint32_t raw_max(uint32_t m, uint32_t w)
+{
+    if constexpr (T == IN_F32) return max(m, w & 0x7fffffffu);
+    else return __vmaxu2(m, w & 0x7fff7fffu);
+}
+
+// The fp32 bits of a 16-bit magnitude.
+template <int T>
+__device__ __forceinline__ uint32_t bits_of(uint32_t h)
+{
+    if constexpr (T == IN_BF16) return h << 16;
+    else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
+}
+
+// Codes of eight values held as raw words, times `inv`.
+template <int T>
+__device__ __forceinline__ uint32_t raw_encode(const uint32_t (&w)[Raw8<T>::WORDS], float inv)
+{
+    float v[8];
+    if constexpr (T == IN_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]) * inv;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack2<T>(w[j]);
+            v[2 * j] = f.x * inv;
+            v[2 * j + 1] = f.y * inv;
+        }
+    }
+    return mx_encode8(v);
 }
 
 // x [rows, K] row-major.  Sixteen lanes take one row's 128 values (one scale
 // word): each lane 8 values, four lanes a block, whose largest |x| they find by
 // two shuffles.  A block of 256 threads covers `tpr` tiles (a power of two, at
-// most 16) of 16 / tpr rows; rows past the last one, up to a multiple of 128,
-// only get their zero scales.
-template <int T, bool VEC>
+// most 16) of 16 / tpr rows, U times (U sets of loads in flight); rows past the
+// last one, up to a multiple of 128, only get their zero scales.
+template <int T, bool VEC, int U>
 __global__ void __launch_bounds__(256) quantize_kernel(const void *__restrict__ x, uint8_t *__restrict__ codes,
                                                        uint8_t *__restrict__ scales, int64_t rows, int64_t K,
                                                        int tpr_log2, int segs)
@@ -66,43 +99,52 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void *__restrict__ 
     const int unit = threadIdx.x >> 4, l = threadIdx.x & 15;
     const int64_t rb = blockIdx.x / segs;
     const int seg = (int)(blockIdx.x - rb * segs);
-    const int64_t tiles = mx_tiles(K), kb = mx_blocks(K);
-    const int64_t row = (rb << (4 - tpr_log2)) + (unit >> tpr_log2);
+    const int64_t tiles = mx_tiles(K), kb = mx_blocks(K), padded = (rows + 127) & ~(int64_t)127;
+    const int per = 16 >> tpr_log2;                            // rows of one set
+    const int64_t row0 = rb * (per * U) + (unit >> tpr_log2);
     const int64_t tile = ((int64_t)seg << tpr_log2) + (unit & ((1 << tpr_log2) - 1));
     const int64_t k0 = tile * 128 + l * 8;
-    float v[8] = {};
-    uint32_t amax = 0;
-    if (row < rows && k0 < K) {
-        load8<T, VEC>(x, row * K + k0, (int)min((int64_t)8, K - k0), v);
+    Raw8<T> r[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int j = 0; j < Raw8<T>::WORDS; ++j) r[u].w[j] = 0;
+        const int64_t row = row0 + u * per;
+        if (row < rows && k0 < K) load8<T, VEC>(x, row * K + k0, (int)min((int64_t)8, K - k0), r[u]);
     }
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const uint32_t b = mx_scale_byte(amax);
-    const float inv = mx_inv_scale(b == 255u ? 0u : b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= inv;
-    const uint32_t c = b == 255u ? 0u : mx_encode8(v);
-    if (row < rows && k0 < kb * 32)
-        *reinterpret_cast<uint32_t *>(codes + row * (kb * 16) + tile * 64 + l * 4) = c;
-    uint32_t word = b << (8 * (l >> 2));
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if (l == 0 && tile < tiles && row < ((rows + 127) & ~(int64_t)127))
-        *reinterpret_cast<uint32_t *>(scales + mx_scale_at(row, tile * 4, tiles)) = word;
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = row0 + u * per;
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < Raw8<T>::WORDS; ++j) amax = raw_max<T>(amax, r[u].w[j]);
+        if constexpr (T != IN_F32) amax = max(amax & 0xffffu, amax >> 16);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        if constexpr (T != IN_F32) amax = bits_of<T>(amax);
+        const uint32_t b = mx_scale_byte(amax);
+        const uint32_t c = b == 255u ? 0u : raw_encode<T>(r[u].w, mx_inv_scale(b));
+        if (row < rows && k0 < kb * 32)
+            *reinterpret_cast<uint32_t *>(codes + row * (kb * 16) + tile * 64 + l * 4) = c;
+        uint32_t word = b << (8 * (l >> 2));
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        if (l == 0 && tile < tiles && row < padded)
+            *reinterpret_cast<uint32_t *>(scales + mx_scale_at(row, tile * 4, tiles)) = word;
+    }
 }
 
 // x [K, rows] row-major, blocks along K (the right operand of a row-major
 // product).  A warp takes one block of 32 k and 64 columns, two to a lane: 32
-// coalesced loads, each column's largest |x| and codes in the lane.  The eight
-// warps of a CTA take eight consecutive blocks, and the codes go through shared
-// memory so that each row's 128 bytes are written together.
+// coalesced loads in flight, each column's largest |x| and codes in the lane.
+// The eight warps of a CTA take eight consecutive blocks, and the codes go
+// through shared memory so that each row's 128 bytes are written together.
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) quantize_trans_kernel(const void *__restrict__ x, uint8_t *__restrict__ codes,
                                                              uint8_t *__restrict__ scales, int64_t rows, int64_t K,
                                                              int col_tiles)
 {
+    constexpr int WPP = T == IN_F32 ? 2 : 1;                   // words of a pair of columns
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     __shared__ uint32_t sc[64][33];       // [row][8 blocks x 4 words] (+1: the lanes' rows on other banks)
@@ -112,43 +154,64 @@ __global__ void __launch_bounds__(256) quantize_trans_kernel(const void *__restr
     const int64_t c0 = (int64_t)(blockIdx.x - kt * col_tiles) * 64;
     const int64_t k0 = kt * 256 + warp * 32, col = c0 + 2 * lane;
     const int64_t tiles = mx_tiles(K), kb = mx_blocks(K);
-    float a[32], d[32];
+    uint32_t a[32 * WPP];
+    if (VEC && c0 + 64 <= rows && k0 + 32 <= K) {              // a whole tile: the same for the warp
+        const char *p = static_cast<const char *>(x) + (k0 * rows + col) * (T == IN_F32 ? 4 : 2);
+        const int64_t pitch = rows * (T == IN_F32 ? 4 : 2);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        a[j] = d[j] = 0.0f;
-        if (k0 + j < K) {
-            const int64_t i = (k0 + j) * rows + col;
-            if (VEC && col + 1 < rows) {
-                if constexpr (T == IN_F32) {
-                    const float2 f = __ldcs(reinterpret_cast<const float2 *>(static_cast<const float *>(x) + i));
-                    a[j] = f.x, d[j] = f.y;
-                } else {
-                    const float2 f = unpack2<T>(
-                        __ldcs(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(x) + i)));
-                    a[j] = f.x, d[j] = f.y;
-                }
+        for (int j = 0; j < 32; ++j) {
+            if constexpr (T == IN_F32) {
+                const uint2 f = __ldcs(reinterpret_cast<const uint2 *>(p + j * pitch));
+                a[2 * j] = f.x, a[2 * j + 1] = f.y;
             } else {
-                if (col < rows) a[j] = load1<T>(x, i);
-                if (col + 1 < rows) d[j] = load1<T>(x, i + 1);
+                a[j] = __ldcs(reinterpret_cast<const uint32_t *>(p + j * pitch));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const int64_t i = (k0 + j) * rows + col;
+            const bool in0 = k0 + j < K && col < rows, in1 = k0 + j < K && col + 1 < rows;
+            if constexpr (T == IN_F32) {
+                a[2 * j] = in0 ? static_cast<const uint32_t *>(x)[i] : 0u;
+                a[2 * j + 1] = in1 ? static_cast<const uint32_t *>(x)[i + 1] : 0u;
+            } else {
+                a[j] = in0 ? static_cast<const uint16_t *>(x)[i] : 0u;
+                if (in1) a[j] |= (uint32_t) static_cast<const uint16_t *>(x)[i + 1] << 16;
             }
         }
     }
+    uint32_t m[2] = {0, 0};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t amax = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) amax = max(amax, __float_as_uint(h ? d[j] : a[j]) & 0x7fffffffu);
-        const uint32_t b = mx_scale_byte(amax);
-        const float inv = mx_inv_scale(b == 255u ? 0u : b);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = (h ? d[8 * q + j] : a[8 * q + j]) * inv;
-            sc[2 * lane + h][warp * 4 + q] = b == 255u ? 0u : mx_encode8(v);
-        }
-        ss[2 * lane + h][warp] = (uint8_t)b;
+    for (int j = 0; j < 32; ++j) {
+        m[0] = raw_max<T>(m[0], a[WPP * j]);
+        if constexpr (T == IN_F32) m[1] = raw_max<T>(m[1], a[2 * j + 1]);
     }
+    if constexpr (T != IN_F32) {
+        m[1] = bits_of<T>(m[0] >> 16);
+        m[0] = bits_of<T>(m[0] & 0xffffu);
+    }
+    const uint32_t b0 = mx_scale_byte(m[0]), b1 = mx_scale_byte(m[1]);
+    const float inv0 = mx_inv_scale(b0 == 255u ? 0u : b0), inv1 = mx_inv_scale(b1 == 255u ? 0u : b1);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float v[8], w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (T == IN_F32) {
+                v[j] = __uint_as_float(a[2 * (8 * q + j)]) * inv0;
+                w[j] = __uint_as_float(a[2 * (8 * q + j) + 1]) * inv1;
+            } else {
+                const float2 f = unpack2<T>(a[8 * q + j]);
+                v[j] = f.x * inv0;
+                w[j] = f.y * inv1;
+            }
+        }
+        sc[2 * lane][warp * 4 + q] = b0 == 255u ? 0u : mx_encode8(v);
+        sc[2 * lane + 1][warp * 4 + q] = b1 == 255u ? 0u : mx_encode8(w);
+    }
+    ss[2 * lane][warp] = (uint8_t)b0;
+    ss[2 * lane + 1][warp] = (uint8_t)b1;
     __syncthreads();
     // codes: 4 bytes to a thread, a warp writes 128 bytes of one row at a time
     const int64_t word0 = kt * 32;                           // first 4-byte word of the row's segment
@@ -167,7 +230,7 @@ __global__ void __launch_bounds__(256) quantize_trans_kernel(const void *__restr
 }
 
 // codes and scales -> y [rows, K]; the same lanes as quantize_kernel.
-template <int T, bool VEC>
+template <int T, bool VEC, int U>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restrict__ codes,
                                                          const uint8_t *__restrict__ scales, void *__restrict__ y,
                                                          int64_t rows, int64_t K, int tpr_log2, int segs)
@@ -178,40 +241,57 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restri
     const int64_t rb = blockIdx.x / segs;
     const int seg = (int)(blockIdx.x - rb * segs);
     const int64_t tiles = mx_tiles(K), kb = mx_blocks(K);
-    const int64_t row = (rb << (4 - tpr_log2)) + (unit >> tpr_log2);
+    const int per = 16 >> tpr_log2;
+    const int64_t row0 = rb * (per * U) + (unit >> tpr_log2);
     const int64_t tile = ((int64_t)seg << tpr_log2) + (unit & ((1 << tpr_log2) - 1));
     const int64_t k0 = tile * 128 + l * 8;
-    if (row >= rows || k0 >= K) return;
-    const uint32_t c = *reinterpret_cast<const uint32_t *>(codes + row * (kb * 16) + tile * 64 + l * 4);
-    const float s = mx_scale(scales[mx_scale_at(row, tile * 4 + (l >> 2), tiles)]);
-    float v[8];
-    mx_decode8(c, v);
+    if (k0 >= K) return;
+    uint32_t c[U], b[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= s;
-    const int64_t i = row * K + k0;
-    if (VEC && k0 + 8 <= K) {
-        if constexpr (T == IN_F32) {
-            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(y) + i);
-            __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
-            __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = row0 + u * per;
+        c[u] = b[u] = 0;
+        if (row >= rows) continue;
+        c[u] = __ldcs(reinterpret_cast<const uint32_t *>(codes + row * (kb * 16) + tile * 64 + l * 4));
+        b[u] = scales[mx_scale_at(row, tile * 4 + (l >> 2), tiles)];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = row0 + u * per;
+        if (row >= rows) break;
+        const float s = mx_scale(b[u]);
+        float v[8];
+        mx_decode8(c[u], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= s;
+        const int64_t i = row * K + k0;
+        if (VEC && k0 + 8 <= K) {
+            if constexpr (T == IN_F32) {
+                float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(y) + i);
+                __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
+                __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+            } else {
+                uint4 w;
+                w.x = pack2<T>(v[0], v[1]);
+                w.y = pack2<T>(v[2], v[3]);
+                w.z = pack2<T>(v[4], v[5]);
+                w.w = pack2<T>(v[6], v[7]);
+                __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(y) + i), w);
+            }
         } else {
-            uint4 u;
-            u.x = pack2<T>(v[0], v[1]);
-            u.y = pack2<T>(v[2], v[3]);
-            u.z = pack2<T>(v[4], v[5]);
-            u.w = pack2<T>(v[6], v[7]);
-            __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(y) + i), u);
-        }
-    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (k0 + j < K) store1<T>(y, i + j, v[j]);
+            for (int j = 0; j < 8; ++j)
+                if (k0 + j < K) store1<T>(y, i + j, v[j]);
+        }
     }
 }
 
-// Rows and tiles of one CTA of the row kernels: as many of a row's tiles as it has, up to 16.
+// The row kernels' grid: a CTA takes as many of a row's tiles as it has, up to
+// 16, and U sets of rows; U = 4 once that still leaves four CTAs for each of the
+// 152 SMs, so that small calls spread over more SMs and large ones keep more
+// loads in flight.
 struct RowGrid {
-    int tpr_log2, segs;
+    int tpr_log2, segs, u;
     int64_t grid;
 };
 
@@ -223,7 +303,8 @@ static RowGrid row_grid(int64_t rows, int64_t K)
     while (g.tpr_log2 < 4 && (1 << g.tpr_log2) < tiles) ++g.tpr_log2;
     g.segs = (int)((tiles + (1 << g.tpr_log2) - 1) >> g.tpr_log2);
     const int64_t per = 16 >> g.tpr_log2;
-    g.grid = (rows + per - 1) / per * g.segs;
+    g.u = (rows + per * 4 - 1) / (per * 4) * g.segs >= 4 * 152 ? 4 : 1;
+    g.grid = (rows + per * g.u - 1) / (per * g.u) * g.segs;
     return g;
 }
 
@@ -241,7 +322,9 @@ static cudaError_t quantize_t(const void *x, uint8_t *codes, uint8_t *scales, in
     }
     const RowGrid g = row_grid(padded, K);
     if (g.grid > INT32_MAX) return cudaErrorInvalidValue;
-    auto k = K * e % 16 == 0 ? quantize_kernel<T, true> : quantize_kernel<T, false>;
+    const bool vec = K * e % 16 == 0;
+    auto k = g.u == 4 ? (vec ? quantize_kernel<T, true, 4> : quantize_kernel<T, false, 4>)
+                      : (vec ? quantize_kernel<T, true, 1> : quantize_kernel<T, false, 1>);
     return launch_k(k, dim3((unsigned)g.grid), dim3(256), 0, s, x, codes, scales, rows, K, g.tpr_log2, g.segs);
 }
 
@@ -252,7 +335,9 @@ static cudaError_t dequantize_t(const uint8_t *codes, const uint8_t *scales, voi
     const int e = T == IN_F32 ? 4 : 2;
     const RowGrid g = row_grid(rows, K);
     if (g.grid > INT32_MAX) return cudaErrorInvalidValue;
-    auto k = K * e % 16 == 0 ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
+    const bool vec = K * e % 16 == 0;
+    auto k = g.u == 4 ? (vec ? dequantize_kernel<T, true, 4> : dequantize_kernel<T, false, 4>)
+                      : (vec ? dequantize_kernel<T, true, 1> : dequantize_kernel<T, false, 1>);
     return launch_k(k, dim3((unsigned)g.grid), dim3(256), 0, s, codes, scales, y, rows, K, g.tpr_log2, g.segs);
 }
 

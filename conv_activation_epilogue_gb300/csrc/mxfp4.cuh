@@ -125,19 +125,65 @@ __device__ __forceinline__ float act_mx(int act, float z, float alpha)
     }
 }
 
+// The same over an array, the activation looked up once.
+template <int ACT, int N>
+__device__ __forceinline__ void act_mx_all(float (&v)[N], float alpha)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = act_mx<ACT>(v[i], alpha);
+}
+
+template <int N>
+__device__ __forceinline__ void act_mx_all(int act, float (&v)[N], float alpha)
+{
+    switch (act) {
+    case ACT_RELU: act_mx_all<ACT_RELU>(v, alpha); break;
+    case ACT_LEAKY: act_mx_all<ACT_LEAKY>(v, alpha); break;
+    case ACT_TANH: act_mx_all<ACT_TANH>(v, alpha); break;
+    case ACT_SIGMOID: act_mx_all<ACT_SIGMOID>(v, alpha); break;
+    case ACT_GELU: act_mx_all<ACT_GELU>(v, alpha); break;
+    case ACT_SILU: act_mx_all<ACT_SILU>(v, alpha); break;
+    default: break;
+    }
+}
+
 // -------------------------------------------------- tensor-core instructions --
 namespace ptx {
 
+// The tcgen05 instructions below are executed by a whole converged warp and
+// issued by one elected lane of it (always the same one, so that a commit covers
+// the MMAs before it).  A warp-uniform loop keeps descriptors and addresses in
+// uniform registers; the same loop run by a single lane moves them there before
+// every instruction, and was measured at 108 cycles an instruction where a
+// 256 x 256 x 64 MMA of a CTA pair takes 128 (133 with this form, the scale
+// copies of its stage included).
+#define MMACT_ELECTED "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\t"
+
 // D[tmem] (+)= (A x scale_A)(B x scale_B), kind::mxf4: E2M1 operands packed two
 // to a byte, K-major, K = 64 per instruction, one UE8M0 scale per row and 32 K
-// (two per row and instruction), scales in tensor memory.
+// (two per row and instruction), scales in tensor memory at columns that are a
+// multiple of four.
 __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        MMACT_ELECTED
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// The same over a CTA pair (issued in the even CTA): M = 256, each CTA holds its
+// 128 rows of A, half of B's rows, its own A rows' scales and all of B's scales.
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        MMACT_ELECTED
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
@@ -145,12 +191,40 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64
 
 // Copy 32 rows x 16 bytes of shared memory (an unswizzled descriptor, 8-row
 // groups of 128 bytes) to four 32-bit columns of all four lane quarters of
-// tensor memory: one scale tile.  Ordered before the MMAs that the same thread
-// issues after it.
+// tensor memory: one scale tile.  Ordered before the MMAs issued after it.
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc)
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    asm volatile(MMACT_ELECTED "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
 }
+
+// The same in both CTAs of a pair, each from its own shared memory to its own
+// tensor memory (issued in the even CTA).
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile(MMACT_ELECTED "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
+}
+
+// Arrive once on `bar` when every MMA and copy issued so far is done; on a pair,
+// on the barrier of every CTA in `mask`.
+__device__ __forceinline__ void commit_elected(uint32_t bar)
+{
+    asm volatile(MMACT_ELECTED
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void commit_elected_pair(uint32_t bar, uint16_t mask)
+{
+    asm volatile(MMACT_ELECTED
+                 "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+                 "%1;\n\t}" ::"r"(bar),
+                 "h"(mask)
+                 : "memory");
+}
+
+#undef MMACT_ELECTED
 
 // Instruction descriptor for kind::mxf4: A and B E2M1 (format 1), scales UE8M0,
 // M and N extents; sa and sb (0 or 2) say which two bytes of the 32-bit scale
@@ -161,6 +235,51 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t sa, uin
            ((uint32_t)(M >> 7) << 27) | (sa << 29);
 }
 
+// Non-binding copy of a tensor box to L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *m, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
+// 32-bit float load from another CTA's shared memory (address from mapa).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns: thread i gets lane (base + i).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 }  // namespace ptx
+
+// A pipeline wait of a whole warp with one verdict for it.
+__device__ __forceinline__ bool mx_warp_wait(const Pipe &pp, uint32_t bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, pipe_wait(pp, bar, parity)) != 0;
+}
 
 }  // namespace mmact

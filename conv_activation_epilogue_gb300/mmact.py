@@ -39,6 +39,7 @@ SYMBOLS = [
     "mmact_set_gemm_l2_policy", "mmact_tensor_map_cache_stats", "mmact_status_string", "mmact_version",
     "mmact_mxfp4_size", "mmact_quantize_mxfp4", "mmact_dequantize_mxfp4", "mmact_gemm_mxfp4",
     "mmact_linear_mxfp4", "mmact_linear_mxfp4_workspace_bytes", "mmact_moe", "mmact_moe_workspace_bytes",
+    "mmact_set_gemm_mxfp4_kernel",
 ]
 
 
@@ -115,9 +116,10 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     L.mmact_linear_mxfp4_workspace_bytes.argtypes = [i64, i64, p_i64]
     L.mmact_moe.argtypes = [vp] * 12 + [i64] * 5 + [ci, ci, ci, f32, ci, ci, vp, vp]
     L.mmact_moe_workspace_bytes.argtypes = [i64] * 5 + [p_i64]
+    L.mmact_set_gemm_mxfp4_kernel.argtypes = [ci]
     for name in ("mmact_mxfp4_size", "mmact_quantize_mxfp4", "mmact_dequantize_mxfp4", "mmact_gemm_mxfp4",
                  "mmact_linear_mxfp4", "mmact_linear_mxfp4_workspace_bytes", "mmact_moe",
-                 "mmact_moe_workspace_bytes"):
+                 "mmact_moe_workspace_bytes", "mmact_set_gemm_mxfp4_kernel"):
         getattr(L, name).restype = ci
     for name in ("mmact_gemm", "mmact_gemm_split", "mmact_conv2d", "mmact_conv2d_split",
                  "mmact_conv2d_out_shape", "mmact_get_last_error", "mmact_selftest_wait_timeout",
@@ -517,6 +519,11 @@ def mmact_linear_mxfp4(x, w_codes, w_scales, bias, C, workspace, act: str = "non
         raise ValueError("workspace must hold mmact_linear_mxfp4_workspace_bytes(M, K) bytes")
     _check(L.mmact_linear_mxfp4(px, pw, ps, _bias_ptr(bias, N), pc, M, N, K, DTYPE[x.dtype], DTYPE[C.dtype],
                                 ACT[act], float(alpha), pws, _stream_handle(stream)), "mmact_linear_mxfp4")
+
+
+def mmact_set_gemm_mxfp4_kernel(mode: int) -> None:
+    """MXFP4 products: 0 kernel chosen per shape; 1 few rows or tiles; 2 CTA pairs."""
+    _check(load().mmact_set_gemm_mxfp4_kernel(int(mode)), "mmact_set_gemm_mxfp4_kernel")
 
 
 def mmact_moe_workspace_bytes(T: int, H: int, I: int, E: int, top: int) -> int:

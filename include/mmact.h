@@ -560,6 +560,15 @@ mmact_status mmact_linear_mxfp4(const void *x, const void *w_codes, const void *
 mmact_status mmact_linear_mxfp4_workspace_bytes(int64_t M, int64_t K, int64_t *bytes);
 
 /*
+ * Tuning and testing aid: the kernel of mmact_gemm_mxfp4 and mmact_linear_mxfp4.
+ * mode: 0 = chosen per shape (the default), 1 = the kernel for few rows or tiles
+ * (128 rows of B by 16 to 128 rows of A, K shared by clusters), 2 = the kernel
+ * for large outputs (256 x 256 tiles on CTA pairs).  Applies to later calls in
+ * the process.  Returns MMACT_ERR_INVALID_ARG for other values.
+ */
+mmact_status mmact_set_gemm_mxfp4_kernel(int mode);
+
+/*
  * A whole mixture-of-experts layer for a few tokens (T <= 64), in two kernels:
  *   logits[t][e] = x[t] . router[e] + router_bias[e]
  *   experts[t]   = the `top` experts of the largest logits, largest first (equal

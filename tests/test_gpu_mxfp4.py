@@ -119,9 +119,17 @@ GEMMS = [(1, 1, 1), (1, 128, 32), (1, 136, 64), (2, 8, 96), (7, 129, 100), (16, 
          (513, 520, 544), (640, 384, 4096)]
 
 
+@pytest.fixture(params=[0, 1, 2], ids=["chosen", "rows", "pair"])
+def kernel(request):
+    """Each kernel for every shape: the shape's own choice is only about speed."""
+    mmact.mmact_set_gemm_mxfp4_kernel(request.param)
+    yield request.param
+    mmact.mmact_set_gemm_mxfp4_kernel(0)
+
+
 @pytest.mark.parametrize("M,N,K", GEMMS)
 @pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
-def test_gemm(M, N, K, out):
+def test_gemm(M, N, K, out, kernel):
     rng = np.random.default_rng(M * 7919 + N * 31 + K)
     (ac, as_, av), (bc, bs, bv) = random_mx(rng, M, K), random_mx(rng, N, K, K ** -0.5)
     bias = rng.normal(0, 1, N).astype(np.float32)
@@ -134,7 +142,7 @@ def test_gemm(M, N, K, out):
 
 @pytest.mark.parametrize("name", ["none", "relu", "leaky_relu", "tanh", "sigmoid", "gelu", "silu"])
 @pytest.mark.parametrize("M,N,K", [(3, 200, 160), (130, 192, 300), (260, 300, 256)])
-def test_gemm_activations(name, M, N, K):
+def test_gemm_activations(name, M, N, K, kernel):
     rng = np.random.default_rng(M + N + K)
     (ac, as_, av), (bc, bs, bv) = random_mx(rng, M, K), random_mx(rng, N, K, K ** -0.5)
     for out, bias in (("f32", None), ("bf16", rng.normal(0, 1, N).astype(np.float32))):
@@ -144,7 +152,7 @@ def test_gemm_activations(name, M, N, K):
         check(C, want, bound, out)
 
 
-def test_gemm_against_its_own_scales():
+def test_gemm_against_its_own_scales(kernel):
     """A one-hot A picks single values of B through every block and row: each scale byte and code
     has to be the one of its own row, block and place (exact)."""
     rng = np.random.default_rng(5)
@@ -159,7 +167,7 @@ def test_gemm_against_its_own_scales():
 
 
 @pytest.mark.parametrize("M", [2, 140, 300])
-def test_gemm_nan_scales_reach_their_row_or_column_only(M):
+def test_gemm_nan_scales_reach_their_row_or_column_only(M, kernel):
     rng = np.random.default_rng(6)
     N, K = 200, 192
     (ac, as_, av), (bc, bs, bv) = random_mx(rng, M, K), random_mx(rng, N, K)
@@ -227,6 +235,23 @@ def test_calls_on_a_side_stream_and_in_a_graph():
     want, bound = ref.gemm(ref.quantize(host64(x))[2], wv, None, "none", 0.0)
     check(C, want, bound, "f32")
     assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 520, 8192), (16, 136, 4100), (100, 400, 2500), (1536, 1280, 640), (2816, 2560, 96)])
+def test_gemm_many_k_blocks_and_many_tiles(M, N, K, kernel):
+    """K shared by clusters, rings that go round, several tiles for each CTA pair."""
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    a, b = (torch.empty((r, K), device="cuda").normal_(0, 1, generator=g) for r in (M, N))
+    (ac, as_), (bc, bs) = quantized(a), quantized(b)
+    C = torch.full((M, N), float("nan"), dtype=torch.float32, device="cuda")
+    mmact.mmact_gemm_mxfp4(ac, as_, bc, bs, None, C, K)
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+    va, vb = torch.empty_like(a), torch.empty_like(b)          # exact (tested above)
+    mmact.mmact_dequantize_mxfp4(ac, as_, va)
+    mmact.mmact_dequantize_mxfp4(bc, bs, vb)
+    va, vb = va.double(), vb.double()
+    err, bound = (C.double() - va @ vb.t()).abs(), ref.sum_error(K) * (va.abs() @ vb.abs().t())
+    assert bool((err <= bound).all())
 
 
 def test_long_rows_pass_32_bit_offsets():

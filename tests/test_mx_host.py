@@ -114,6 +114,13 @@ def test_moe_host_validation(lib):
     assert moe(lib, T=0, x=None, y=None) == OK
 
 
+def test_kernel_mode_validation(lib):
+    for bad in (-1, 3):
+        assert lib.mmact_set_gemm_mxfp4_kernel(bad) == E
+    for good in (1, 2, 0):
+        assert lib.mmact_set_gemm_mxfp4_kernel(good) == OK
+
+
 def test_silu_belongs_to_the_new_operators_only(lib):
     assert lib.mmact_gemm(P, P, None, P, 64, 64, 64, 1, 1, mmact.ACT["silu"], ctypes.c_float(0), None) == E
 
