@@ -51,7 +51,8 @@ mmact_status mx_context(MxContext *out)
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
     std::lock_guard<std::mutex> lock(mutex);
     if (!ready[dev]) {
-        if (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels() != cudaSuccess)
+        if (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels() != cudaSuccess ||
+            setup_moe_kernels() != cudaSuccess)
             return MMACT_ERR_CUDA;
         ready[dev] = true;
     }
@@ -200,21 +201,20 @@ cudaError_t quantize_launch(const void *x, void *codes, void *scales, int64_t ro
 
 // Where the parts of mmact_moe's workspace begin.
 struct MoeWorkspace {
-    int64_t x_hi, x_lo, h_hi, h_lo, part, bytes;
-    int num_counters;
+    int64_t logits, x_hi, x_lo, h_hi, h_lo, part, bytes;
 };
 
-MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t top)
+MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
 {
     MoeWorkspace w;
     const int64_t Hp = round_up(H, 32), Ip = round_up(I, 32);
-    w.num_counters = (int)(1 + (H + 15) / 16);
-    int64_t at = round_up(w.num_counters * 4, 256);
+    int64_t at = 256;                                          // two counters
     auto take = [&at](int64_t bytes) {
         const int64_t here = at;
         at += round_up(bytes, 256);
         return here;
     };
+    w.logits = take(T * E * 4);
     w.x_hi = take(T * Hp * 2);
     w.x_lo = take(T * Hp * 2);
     w.h_hi = take(T * top * Ip * 2);
@@ -222,6 +222,22 @@ MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t top)
     w.part = take(T * top * H * 4);
     w.bytes = at;
     return w;
+}
+
+// Boxes of eight rows of the experts' weights (rows of all experts in one matrix)
+// and, for MXFP4, of the scale words that go with them: 32 words = 8 rows x 16
+// bytes of each of four tiles.
+bool moe_encode(CUtensorMap *mw, CUtensorMap *ms, const void *w, const void *scales, int64_t rows, int64_t K, bool mx)
+{
+    const uint64_t row_bytes = (uint64_t)(mx ? mx_blocks(K) * 16 : K * 2);
+    const uint64_t d[2] = {row_bytes / 2, (uint64_t)rows}, st[1] = {row_bytes};
+    const uint32_t box[2] = {(uint32_t)(mx ? MOE_ROW_BYTES_MX : MOE_ROW_BYTES) / 2, MOE_BOX_ROWS};
+    if (!encode_tensor_map(mw, MMACT_BF16, 2, w, d, st, box, false)) return false;
+    if (!mx) return true;
+    const uint64_t tiles = (uint64_t)mx_tiles(K);
+    const uint64_t ds[3] = {128, tiles, (uint64_t)(rows + 127) / 128}, ss[2] = {512, tiles * 512};
+    const uint32_t bs[3] = {MOE_BOX_ROWS * 4, 4, 1};
+    return encode_tensor_map(ms, MMACT_F32, 3, scales, ds, ss, bs, false);
 }
 
 constexpr int64_t MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 16, MOE_MAX_EXPERTS = 512;
@@ -327,7 +343,7 @@ MMACT_EXPORT mmact_status mmact_moe_workspace_bytes(int64_t T, int64_t H, int64_
     if (bytes == nullptr) return MMACT_ERR_INVALID_ARG;
     const mmact_status s = moe_sizes(T, H, I, E, top);
     if (s != MMACT_OK) return s;
-    *bytes = moe_workspace(T, H, I, top).bytes;
+    *bytes = moe_workspace(T, H, I, E, top).bytes;
     return MMACT_OK;
 }
 
@@ -353,10 +369,11 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
     if (!aligned16(x) || !aligned16(router) || !aligned16(w1) || !aligned16(w2) || !aligned16(y) ||
         !aligned16(workspace) || (mx && (!aligned16(w1_scales) || !aligned16(w2_scales))))
         return MMACT_ERR_UNSUPPORTED;
-    DeviceContext dev;
-    if ((s = device_context(&dev)) != MMACT_OK) return s;
-    MoeArgs a;
-    std::memset(&a, 0, sizeof(a));
+    MxContext c;
+    if ((s = mx_context(&c)) != MMACT_OK) return s;
+    MoeLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    MoeArgs &a = L.args;
     a.T = (int)T;
     a.H = (int)H;
     a.I = (int)I;
@@ -382,16 +399,21 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
     a.y = y;
     a.experts = experts;
     a.probs = probs;
-    const MoeWorkspace w = moe_workspace(T, H, I, top);
+    const MoeWorkspace w = moe_workspace(T, H, I, E, top);
     char *ws = static_cast<char *>(workspace);
     a.counters = reinterpret_cast<unsigned int *>(ws);
-    a.num_counters = w.num_counters;
+    a.logits = reinterpret_cast<float *>(ws + w.logits);
     a.x_hi = reinterpret_cast<__nv_bfloat16 *>(ws + w.x_hi);
     a.x_lo = reinterpret_cast<__nv_bfloat16 *>(ws + w.x_lo);
     a.h_hi = reinterpret_cast<__nv_bfloat16 *>(ws + w.h_hi);
     a.h_lo = reinterpret_cast<__nv_bfloat16 *>(ws + w.h_lo);
     a.part = reinterpret_cast<float *>(ws + w.part);
-    a.status = dev.status;
-    a.wait_ns = dev.wait_ns;
-    return enqueued(launch_moe(a, out_kind(x_dtype), dev.sm_count, static_cast<cudaStream_t>(stream)));
+    a.status = c.dev.status;
+    a.wait_ns = c.dev.wait_ns;
+    L.x_out = out_kind(x_dtype);
+    // no more CTAs than the down product of the fewest experts has items for
+    L.grid = (int)std::min<int64_t>(c.dev.sm_count, std::max<int64_t>((H + 15) / 16, (I + 7) / 8) * std::min(T * top, E));
+    if (!moe_encode(&L.tm1, &L.ts1, w1, w1_scales, E * a.R1, H, mx) || !moe_encode(&L.tm2, &L.ts2, w2, w2_scales, E * H, I, mx))
+        return MMACT_ERR_CUDA;
+    return enqueued(launch_moe(L, static_cast<cudaStream_t>(stream)));
 }

@@ -82,8 +82,8 @@ struct MoeArgs {
     int *experts;                // [T, top]
     float *probs;                // [T, top]
     // workspace
-    unsigned int *counters;      // [0] grid barrier, [1 + i] experts done with rows 16 i .. of y
-    int num_counters;
+    unsigned int *counters;      // two grid barriers
+    float *logits;               // [T, E]
     __nv_bfloat16 *x_hi, *x_lo;  // MXFP4: x in the codes' order [T, Hp]
     __nv_bfloat16 *h_hi, *h_lo;  // [T * top, Ip]
     float *part;                 // [T * top, H]
@@ -91,7 +91,18 @@ struct MoeArgs {
     unsigned long long wait_ns;
 };
 
-cudaError_t launch_moe(const MoeArgs &a, int x_out, int sms, cudaStream_t stream);
+struct MoeLaunch {
+    CUtensorMap tm1, ts1, tm2, ts2;   // w1, its scales, w2, its scales
+    MoeArgs args;
+    int x_out;           // OUT_* of x, the router and y
+    int grid;            // CTAs of the experts kernel: one for each SM at most
+};
+
+// Bytes of a row in one box of weights, and its words of scale tiles.
+constexpr int MOE_BOX_ROWS = 8, MOE_ROW_BYTES = 512, MOE_ROW_BYTES_MX = 256;
+
+cudaError_t setup_moe_kernels();
+cudaError_t launch_moe(const MoeLaunch &L, cudaStream_t stream);
 
 // out [rows, cols] = act(bias): a product over an empty K.
 cudaError_t launch_mx_bias_act(const float *bias, void *out, int64_t rows, int64_t cols, int out_kind, int act,

@@ -14,7 +14,7 @@ def tiles_of(rows: int, K: int) -> tuple[int, int]:
     return -(-rows // 128), -(-K // 128)
 
 
-def scale_place(r: int, b: int, ktiles: int) -> int:
+def scale_place(r, b, ktiles):
     return ((r // 128) * ktiles + b // 4) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + b % 4
 
 
@@ -52,9 +52,7 @@ def quantize(x: np.ndarray) -> tuple[np.ndarray, np.ndarray, np.ndarray]:
     packed = (flat[:, 0::2] | (flat[:, 1::2] << 4)).astype(np.uint8)
     rt, kt = tiles_of(rows, K)
     tiled = np.zeros(rt * kt * 512, dtype=np.uint8)
-    for r in range(rows):
-        for k in range(kb):
-            tiled[scale_place(r, k, kt)] = b[r, k]
+    tiled[scale_place(np.arange(rows)[:, None], np.arange(kb)[None, :], kt)] = b
     return packed, tiled, vals.reshape(rows, -1)[:, :K]
 
 
@@ -65,11 +63,8 @@ def values(codes: np.ndarray, tiled: np.ndarray, rows: int, K: int) -> np.ndarra
     out[:, 0::2], out[:, 1::2] = codes & 15, codes >> 4
     c = out.astype(np.int64)
     v = GRID[c & 7] * np.where(c & 8, -1.0, 1.0)
-    for r in range(rows):
-        for k in range(kb):
-            b = int(tiled[scale_place(r, k, kt)])
-            v[r, 32 * k: 32 * k + 32] *= math.nan if b == 255 else 2.0 ** (b - 127)
-    return v[:, :K]
+    b = tiled[scale_place(np.arange(rows)[:, None], np.arange(kb)[None, :], kt)].astype(np.float64)
+    return (v * np.where(b == 255, np.nan, np.exp2(b - 127)).repeat(32, axis=1))[:, :K]
 
 
 def act(z: np.ndarray, name: str, alpha: float) -> np.ndarray:
