@@ -224,20 +224,14 @@ MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t t
     return w;
 }
 
-// Boxes of eight rows of the experts' weights (rows of all experts in one matrix)
-// and, for MXFP4, of the scale words that go with them: 32 words = 8 rows x 16
-// bytes of each of four tiles.
-bool moe_encode(CUtensorMap *mw, CUtensorMap *ms, const void *w, const void *scales, int64_t rows, int64_t K, bool mx)
+// Boxes of `box_rows` rows x 128 bytes of the experts' weights (the rows of all
+// experts as one matrix; MXFP4 codes as 16-bit words).
+bool moe_encode(CUtensorMap *map, const void *w, int64_t rows, int64_t K, bool mx, int box_rows)
 {
     const uint64_t row_bytes = (uint64_t)(mx ? mx_blocks(K) * 16 : K * 2);
     const uint64_t d[2] = {row_bytes / 2, (uint64_t)rows}, st[1] = {row_bytes};
-    const uint32_t box[2] = {(uint32_t)(mx ? MOE_ROW_BYTES_MX : MOE_ROW_BYTES) / 2, MOE_BOX_ROWS};
-    if (!encode_tensor_map(mw, MMACT_BF16, 2, w, d, st, box, false)) return false;
-    if (!mx) return true;
-    const uint64_t tiles = (uint64_t)mx_tiles(K);
-    const uint64_t ds[3] = {128, tiles, (uint64_t)(rows + 127) / 128}, ss[2] = {512, tiles * 512};
-    const uint32_t bs[3] = {MOE_BOX_ROWS * 4, 4, 1};
-    return encode_tensor_map(ms, MMACT_F32, 3, scales, ds, ss, bs, false);
+    const uint32_t box[2] = {64, (uint32_t)box_rows};
+    return encode_tensor_map(map, MMACT_BF16, 2, w, d, st, box, true);
 }
 
 constexpr int64_t MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 16, MOE_MAX_EXPERTS = 512;
@@ -411,9 +405,15 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
     a.status = c.dev.status;
     a.wait_ns = c.dev.wait_ns;
     L.x_out = out_kind(x_dtype);
-    // no more CTAs than the down product of the fewest experts has items for
-    L.grid = (int)std::min<int64_t>(c.dev.sm_count, std::max<int64_t>((H + 15) / 16, (I + 7) / 8) * std::min(T * top, E));
-    if (!moe_encode(&L.tm1, &L.ts1, w1, w1_scales, E * a.R1, H, mx) || !moe_encode(&L.tm2, &L.ts2, w2, w2_scales, E * H, I, mx))
+    // Rows of a tile: the most (128, all eight product warps) that still give three
+    // quarters of the SMs an item of the up product, were every choice another
+    // expert; half and a quarter of that for layers with fewer.
+    a.half_rows = 64;
+    const int64_t groups = std::min(T * top, E);
+    while (a.half_rows > 16 && groups * ((a.R1 + 2 * a.half_rows - 1) / (2 * a.half_rows)) < c.dev.sm_count * 3 / 4)
+        a.half_rows /= 2;
+    L.grid = c.dev.sm_count;
+    if (!moe_encode(&L.tm1, w1, E * a.R1, H, mx, a.half_rows) || !moe_encode(&L.tm2, w2, E * H, I, mx, a.half_rows))
         return MMACT_ERR_CUDA;
     return enqueued(launch_moe(L, static_cast<cudaStream_t>(stream)));
 }

@@ -70,6 +70,7 @@ cudaError_t launch_gemm_mxfp4_rows(const MxRowsLaunch &L, cudaStream_t stream);
 struct MoeArgs {
     int T, H, I, E, top;         // tokens, model width, experts' width, experts, experts per token
     int R1;                      // rows of one expert's w1: 2 I when gated, else I
+    int half_rows;               // rows of half a tile of weights: 64, 32 or 16
     int Hp, Ip;                  // H and I rounded up to 32 (row pitches of the workspace's arrays)
     int gated, normalize, act;
     int w_type;                  // 0 fp16, 1 bf16, 2 MXFP4
@@ -92,14 +93,11 @@ struct MoeArgs {
 };
 
 struct MoeLaunch {
-    CUtensorMap tm1, ts1, tm2, ts2;   // w1, its scales, w2, its scales
+    CUtensorMap tm1, tm2;   // w1, w2: boxes of half_rows rows x 128 bytes
     MoeArgs args;
     int x_out;           // OUT_* of x, the router and y
     int grid;            // CTAs of the experts kernel: one for each SM at most
 };
-
-// Bytes of a row in one box of weights, and its words of scale tiles.
-constexpr int MOE_BOX_ROWS = 8, MOE_ROW_BYTES = 512, MOE_ROW_BYTES_MX = 256;
 
 cudaError_t setup_moe_kernels();
 cudaError_t launch_moe(const MoeLaunch &L, cudaStream_t stream);

@@ -12,19 +12,22 @@
 // With few tokens every weight is used a handful of times: the time is that of
 // reading the chosen experts' weights once, and everything is arranged so that
 // the copies never stop.  The experts kernel is persistent, one CTA on each SM,
-// with a contiguous share of the items (16 weight rows x all of K of one expert;
-// for a gated layer 8 gate rows and the 8 up rows that go with them):
+// with a contiguous share of the items (a tile of weight rows x all of K of one
+// expert; for a gated layer half of the rows are gate rows and half the up rows
+// that go with them):
 //
-//   warp 0       producer: TMA boxes of 8 rows x 512 bytes (MXFP4: 256 bytes and
-//                the scales that belong to them) into a ring of stages.  It runs
-//                ahead over items and over the grid barrier: weights of the down
-//                product are on their way while the last h is being finished.
-//   warps 1..8   products: the stages go round the eight warps; on
-//                mma.sync.m16n8k16 with the weights as the 16-row operand and
-//                eight tokens to its columns; which K a lane holds does not
-//                matter to a sum over K as long as both operands agree, so the
-//                fragments are 16-byte loads in memory order
-//   warps 9..11  sums over the eight warps, bias, activation, stores
+//   warp 0       producer: two TMA boxes (the tile's halves) of 128 bytes of K to a
+//                ring stage.  It runs ahead over items and over the grid barrier:
+//                weights of the down product are on their way while the last h is
+//                being finished.
+//   warps 1..8   products: each has 8 + 8 rows of the tile on mma.sync.m16n8k16
+//                as the 16-row operand (a gate row and its up row meet in one
+//                thread) and eight tokens to its columns, over all of K, so no sums
+//                cross warps; bias, activation and stores follow in registers.
+//                Which K a lane holds does not matter to a sum over K as long as
+//                both operands agree, so fragments are 16-byte loads in memory
+//                order.  A stage's tokens are loaded (from L2 once, from L1 by the
+//                other warps) while the stage before it is computed.
 //
 // The intermediate h is held as two bf16 halves hi = bf16(h), lo = bf16(h - hi),
 // 16 bits of it, and multiplied as both, so no rounding to 16 bits stands between
@@ -40,10 +43,18 @@ namespace mmact {
 enum : int { W_F16 = 0, W_BF16 = 1, W_MX = 2 };
 
 constexpr int MOE_MAX_T = 64, MOE_MAX_K = 16, MOE_MAX_E = 512;
-constexpr int MOE_MMA_WARPS = 8, MOE_EPI_WARPS = 3;
-constexpr int MOE_THREADS = 32 * (1 + MOE_MMA_WARPS + MOE_EPI_WARPS);
-constexpr int MOE_EPI_THREADS = 32 * MOE_EPI_WARPS;
-constexpr int MOE_GROUP = 32;                                  // tokens of one expert that share a read of its weights
+constexpr int MOE_MMA_WARPS = 8;
+constexpr int MOE_THREADS = 32 * (1 + MOE_MMA_WARPS);
+
+// Tokens of one expert that share a read of its weights.  MXFP4 rows cover four
+// times the K of a 16-byte load, so their tokens take four times the registers.
+template <int W>
+constexpr int MOE_GROUP = W == W_MX ? 16 : 32;
+constexpr int MOE_MIN_GROUP = 16;
+
+// The ring: 8 stages of at most 128 rows x 128 bytes, twice what has to be in
+// flight on an SM; the rest of its memory caches the tokens.
+constexpr int MOE_STAGES = 8, MOE_STAGE_BYTES = 16384;
 
 // ------------------------------------------------------------------ helpers --
 // A logit as a key whose unsigned order is the float order, NaN above all, and
@@ -129,15 +140,6 @@ __device__ __forceinline__ void elected_load_2d(uint32_t dst, const CUtensorMap 
                  : "memory");
 }
 
-__device__ __forceinline__ void elected_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z)
-{
-    asm volatile(MMACT_ELECTED
-                 "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
-
 #undef MMACT_ELECTED
 
 // ------------------------------------------------------------------- router --
@@ -217,23 +219,24 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
 // ------------------------------------------------------------ choice of experts --
 // Shared memory of the experts kernel beside the ring.
 struct MoeShared {
-    float red[2][MOE_MMA_WARPS][16][MOE_GROUP];    // partial sums of two items
+    float logits[MOE_THREADS / 32][MOE_MAX_E];     // one token's to a warp, while experts are chosen
     float probs[MOE_MAX_T * MOE_MAX_K];
     short choice[MOE_MAX_T * MOE_MAX_K];           // slot t * k + j -> expert
     short slot[MOE_MAX_T * MOE_MAX_K];             // slots by expert
     short count[MOE_MAX_E];
-    short act[MOE_MAX_E + 32];                     // groups of at most 32 tokens of one expert, by expert:
-    short first[MOE_MAX_E + 33];                   // the expert and the first entry of slot[]
+    short act[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP];       // groups of tokens of one expert, by expert:
+    short first[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP + 1];                   // the expert and the first entry of slot[]
     int nact;
     int abort_flag, go;
-    uint64_t bar[2 * 24 + 4];
+    uint64_t bar[2 * MOE_STAGES];
 };
 
 // Top k of one token by one warp: each round the largest (key, lowest index) of
-// those left; then the softmax weights.  The token's logits are kept in shared
-// memory where the partial sums will be (`row`: MOE_MAX_E floats of this warp).
-__device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, float *row, int t, int lane, bool write)
+// those left; then the softmax weights.
+__device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, int t, int lane, bool write)
 {
+    static_assert(MOE_MAX_E <= 32 * 32, "one bit for each of a lane's logits");
+    float *row = S.logits[threadIdx.x >> 5];
     __syncwarp();
     for (int e = lane; e < p.E; e += 32) row[e] = __ldcg(p.logits + (int64_t)t * p.E + e);
     __syncwarp();
@@ -278,7 +281,8 @@ __device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, f
     }
 }
 
-// The slots of each expert, in groups of at most 32, built by every CTA.
+// The slots of each expert, in groups, built by every CTA.
+template <int GROUP>
 __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S)
 {
     const int tid = threadIdx.x, n_slots = p.T * p.top;
@@ -291,7 +295,7 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S)
     if (tid < 32) {                                            // 32 experts at a time: running sums over the warp
         int n = 0, at = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + tid, c = e < p.E ? S.count[e] : 0, groups = (c + MOE_GROUP - 1) / MOE_GROUP;
+            const int e = e0 + tid, c = e < p.E ? S.count[e] : 0, groups = (c + GROUP - 1) / GROUP;
             int sum = c, gsum = groups;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -300,7 +304,7 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S)
             }
             for (int g = 0; g < groups; ++g) {
                 S.act[n + gsum - groups + g] = (short)e;
-                S.first[n + gsum - groups + g] = (short)(at + sum - c + g * MOE_GROUP);
+                S.first[n + gsum - groups + g] = (short)(at + sum - c + g * GROUP);
             }
             n += __shfl_sync(0xffffffffu, gsum, 31);
             at += __shfl_sync(0xffffffffu, sum, 31);
@@ -322,31 +326,23 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S)
 }
 
 // ----------------------------------------------------------------- products --
-// A ring stage: 2 boxes of 8 rows, ROW_BYTES of each row; MXFP4: and 2 boxes of
-// scales, 4 tiles x 8 rows x 16 bytes.
-template <int W>
-struct MoeStage {
-    static constexpr int KS = W == W_MX ? 512 : 256;           // K of a stage
-    static constexpr int ROW_BYTES = W == W_MX ? MOE_ROW_BYTES_MX : MOE_ROW_BYTES;
-    static constexpr int BOX = 8 * ROW_BYTES;
-    static constexpr int BYTES = 2 * BOX + (W == W_MX ? 1024 : 0);
-    // About 128 KB: twice what has to be in flight; the rest of the SM's memory caches the tokens.  A
-    // multiple of the product warps: slot i always belongs to warp i % 8.  (A wait for a phase only tells
-    // the phase from the one before it, so the warp that waits has to have seen that one end itself.)
-    static constexpr int SLOTS = W == W_MX ? 24 : 16;
-    static constexpr int SMEM = SLOTS * BYTES + 1024 + (int)sizeof(MoeShared);
-    static_assert(2 * SLOTS <= 48 && SLOTS % MOE_MMA_WARPS == 0, "barriers");
-};
-
-// One product of the layer as the roles see it.
+// One product of the layer as the roles see it.  A tile is 2 * half_rows weight
+// rows: r0 .. r0 + half_rows and the same number from `half` rows further on.
 struct MoeProduct {
-    int K, stages;                   // stages of one item
+    int K, stages;                   // ring stages of one item
     int tiles;                       // items of one group of tokens
     int rows;                        // rows of one expert's matrix
-    int half;                        // row distance between an item's two boxes
-    int step;                        // rows from one item to the next
-    int limit;                       // rows that the items count over: I or H
+    int half;                        // row distance between a tile's halves: I (gate, up), or half_rows
+    int step;                        // rows from one tile to the next
+    int limit;                       // rows the tiles count over: I or H
+    const uint8_t *scales;           // MXFP4
+    int64_t all_rows;                // rows of all experts
+    int scale_tiles;                 // tiles of 128 K
+    bool pairs;                      // the halves go together (gate, up)
 };
+
+template <int W>
+constexpr int STAGE_K = W == W_MX ? 256 : 64;                  // 128 bytes of a row
 
 __device__ __forceinline__ uint32_t word_of(const uint4 &u, int i)
 {
@@ -364,177 +360,165 @@ __device__ __forceinline__ uint32_t mx_factor(uint32_t b, uint32_t &rest)
 }
 
 
-__device__ __forceinline__ uint4 ld_token(const uint16_t *p, int64_t k, bool have)
+// A warp's view of an item.
+struct MoeItem {
+    uint32_t row;                    // shared address of this lane's row in the lower half, from a stage's start
+    uint32_t upper;                  // from there to its row in the upper half
+    int64_t ra, rb;                  // the two rows in the matrix of all experts
+};
+
+// Tokens of one piece of K (16 bytes of each row): this lane's 8 values of one
+// token of each eight, hi and lo.
+template <int NT, bool LO>
+struct MoeTokens {
+    uint4 h[NT], l[LO ? NT : 1];
+};
+
+// xh / xl: this lane's token rows (hi, lo), null where there is no token.
+template <int NT, bool LO>
+__device__ __forceinline__ void load_tokens(MoeTokens<NT, LO> &x, const uint16_t *const (&xh)[NT],
+                                            const uint16_t *const (&xl)[NT], int k, int K)
 {
-    return have && p != nullptr ? *reinterpret_cast<const uint4 *>(p + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        x.h[n] = make_uint4(0, 0, 0, 0);
+        if constexpr (LO) x.l[n] = make_uint4(0, 0, 0, 0);
+        if (k < K && xh[n] != nullptr) {
+            x.h[n] = *reinterpret_cast<const uint4 *>(xh[n] + k);
+            if constexpr (LO) x.l[n] = *reinterpret_cast<const uint4 *>(xl[n] + k);
+        }
+    }
 }
 
-// acc += one stage's 16 rows x this lane's token columns, K from k0.  xh / xl:
-// this lane's token rows (hi, lo) for each group of eight tokens, null where there
-// is no token.  LO: multiply the lo half too.  SPLITW: fp16 weights as two bf16
-// halves.  `wait` is called once, after the first tokens are on their way.
-template <int W, int NT, bool LO, bool SPLITW, typename Wait>
-__device__ __forceinline__ bool stage_mma(float (&acc)[NT][4], uint32_t slot, const uint16_t *const (&xh)[NT],
-                                          const uint16_t *const (&xl)[NT], int k0, int K, uint32_t sa_off,
-                                          uint32_t sb_off, Wait wait)
+// acc += 16 rows x tokens over one piece: a, b the two rows' four pairs of values.
+template <bool BF, int NT, bool LO>
+__device__ __forceinline__ void piece_mma(float (&acc)[NT][4], const uint32_t (&a)[4], const uint32_t (&b)[4],
+                                          const MoeTokens<NT, LO> &x)
 {
-    const int lane = threadIdx.x & 31, t4 = lane & 3, g = lane >> 2;
-    using St = MoeStage<W>;
-    const uint32_t row = slot + (uint32_t)g * St::ROW_BYTES + (uint32_t)t4 * 16u;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        mma_16816<BF>(acc[n], a[0], b[0], a[1], b[1], x.h[n].x, x.h[n].y);
+        mma_16816<BF>(acc[n], a[2], b[2], a[3], b[3], x.h[n].z, x.h[n].w);
+        if constexpr (LO) {
+            mma_16816<BF>(acc[n], a[0], b[0], a[1], b[1], x.l[n].x, x.l[n].y);
+            mma_16816<BF>(acc[n], a[2], b[2], a[3], b[3], x.l[n].z, x.l[n].w);
+        }
+    }
+}
+
+// The ring of one CTA.
+struct MoePipe {
+    Pipe pp;
+    uint32_t ring;                   // shared address of the stages
+};
+
+// One warp's rows of an item over all of K: the two units of 64 bytes of each
+// stage.  Every piece of tokens is loaded again, for the unit or stage after the
+// next, as soon as its products are issued.
+template <int W, int NT, bool LO, bool SPLITW>
+__device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
+                                         uint32_t use, const uint16_t *const (&xh)[NT], const uint16_t *const (&xl)[NT])
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t sw = (uint32_t)(lane >> 2), t4 = (uint32_t)(lane & 3);   // the 128-byte swizzle: chunk ^ (row & 7)
+    const uint32_t c0 = (t4 ^ sw) << 4, c1 = ((4u + t4) ^ sw) << 4;
     if constexpr (W == W_MX) {
-        // units of 128 K: 16 bytes = one block of 32 codes to a lane
-        constexpr int WB = NT == 1 ? 4 : (NT == 2 ? 2 : 1);    // words of codes whose tokens are loaded together
+        // a unit is 128 K: a block of 32 codes to a lane, four words of eight
+        MoeTokens<NT, LO> x[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) load_tokens<NT, LO>(x[w], xh, xl, (int)t4 * 32 + w * 8, pr.K);
+        const int64_t sa_at = mx_scale_at(it.ra, 0, pr.scale_tiles), sb_at = mx_scale_at(it.rb, 0, pr.scale_tiles);
+        const bool has_a = it.ra < pr.all_rows, has_b = it.rb < pr.all_rows;
+        auto scales = [&](int u, uint32_t &a, uint32_t &b) {   // the rows' scale words of unit u
+            a = has_a && u < pr.scale_tiles ? __ldg(reinterpret_cast<const uint32_t *>(pr.scales + sa_at + (int64_t)u * 512)) : 0u;
+            b = has_b && u < pr.scale_tiles ? __ldg(reinterpret_cast<const uint32_t *>(pr.scales + sb_at + (int64_t)u * 512)) : 0u;
+        };
+        uint32_t wa[2], wb[2];
+        scales(0, wa[0], wb[0]);
+        scales(1, wa[1], wb[1]);
 #pragma unroll 1
-        for (int u = 0; u < 4; ++u) {
-            const int k = k0 + u * 128 + t4 * 32;
-            if (k0 + u * 128 >= K) break;
-            const bool have = k < K;                           // token rows are zero up to a multiple of 32
-            uint4 h[WB][NT], l[WB][NT];
+        for (int s = 0; s < pr.stages; ++s, ++use) {
+            const uint32_t slot = use % MOE_STAGES, row = m.ring + slot * MOE_STAGE_BYTES + it.row;
+            if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * slot, (use / MOE_STAGES) & 1u)) return false;
 #pragma unroll
-            for (int w = 0; w < WB; ++w)
+            for (int u = 0; u < 2; ++u) {
+                const uint4 fa = ptx::ld_shared_v4(row + (u ? c1 : c0)), fb = ptx::ld_shared_v4(row + it.upper + (u ? c1 : c0));
+                const uint32_t sa = (wa[u] >> (8 * t4)) & 255u, sb = (wb[u] >> (8 * t4)) & 255u;
+                scales(2 * s + 2 + u, wa[u], wb[u]);
+                uint32_t ra, rb;
+                const uint32_t ma = mx_factor(sa, ra), mb = mx_factor(sb, rb);
+                const bool big = __any_sync(0xffffffffu, sa > 128u || sb > 128u);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    h[w][n] = ld_token(xh[n], k + w * 8, have);
-                    if constexpr (LO) l[w][n] = ld_token(xl[n], k + w * 8, have);
-                }
-            if (u == 0 && !wait()) return false;
-            const uint4 a = ptx::ld_shared_v4(row + u * 64u), b = ptx::ld_shared_v4(row + St::BOX + u * 64u);
-            const uint32_t so = slot + 2 * St::BOX + u * 128u + (uint32_t)g * 16u + (uint32_t)t4;
-            uint32_t sa, sb;
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sa) : "r"(so + sa_off));
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb) : "r"(so + 512u + sb_off));
-            uint32_t ra, rb;
-            const uint32_t ma = mx_factor(sa, ra), mb = mx_factor(sb, rb);
-            const bool big = __any_sync(0xffffffffu, sa > 128u || sb > 128u);
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t va[4], vb[4];
+                    mx_word_bf16(word_of(fa, w), ma, va);
+                    mx_word_bf16(word_of(fb, w), mb, vb);
+                    if (big) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if (w > 0 && w % WB == 0) {
-#pragma unroll
-                    for (int i = 0; i < WB; ++i)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            h[i][n] = ld_token(xh[n], k + (w + i) * 8, have);
-                            if constexpr (LO) l[i][n] = ld_token(xl[n], k + (w + i) * 8, have);
+                        for (int i = 0; i < 4; ++i) {
+                            va[i] = mul_bf16x2(va[i], ra);
+                            vb[i] = mul_bf16x2(vb[i], rb);
                         }
-                }
-                uint32_t va[4], vb[4];
-                mx_word_bf16(word_of(a, w), ma, va);
-                mx_word_bf16(word_of(b, w), mb, vb);
-                if (big) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        va[i] = mul_bf16x2(va[i], ra);
-                        vb[i] = mul_bf16x2(vb[i], rb);
                     }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 x = h[w % WB][n];
-                    mma_16816<true>(acc[n], va[0], vb[0], va[1], vb[1], x.x, x.y);
-                    mma_16816<true>(acc[n], va[2], vb[2], va[3], vb[3], x.z, x.w);
-                    if constexpr (LO) {
-                        const uint4 y = l[w % WB][n];
-                        mma_16816<true>(acc[n], va[0], vb[0], va[1], vb[1], y.x, y.y);
-                        mma_16816<true>(acc[n], va[2], vb[2], va[3], vb[3], y.z, y.w);
-                    }
+                    piece_mma<true, NT, LO>(acc, va, vb, x[w]);
+                    load_tokens<NT, LO>(x[w], xh, xl, (2 * s + u + 1) * 128 + (int)t4 * 32 + w * 8, pr.K);
                 }
             }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(m.pp.empty0 + 8 * slot);
         }
     } else {
-        // units of 32 K: 16 bytes to a lane, two instructions
+        // a unit is 32 K: 8 values to a lane
         constexpr bool BF = W == W_BF16 || SPLITW;
-        constexpr int UB = NT == 1 ? 4 : (NT == 2 ? 2 : 1);
+        MoeTokens<NT, LO> x[2];
+        load_tokens<NT, LO>(x[0], xh, xl, (int)t4 * 8, pr.K);
+        load_tokens<NT, LO>(x[1], xh, xl, 32 + (int)t4 * 8, pr.K);
 #pragma unroll 1
-        for (int u0 = 0; u0 < 8; u0 += UB) {
-            if (k0 + u0 * 32 >= K) break;
-            uint4 h[UB][NT], l[UB][NT];
+        for (int s = 0; s < pr.stages; ++s, ++use) {
+            const uint32_t slot = use % MOE_STAGES, row = m.ring + slot * MOE_STAGE_BYTES + it.row;
+            if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * slot, (use / MOE_STAGES) & 1u)) return false;
 #pragma unroll
-            for (int u = 0; u < UB; ++u)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int k = k0 + (u0 + u) * 32 + t4 * 8;
-                    h[u][n] = ld_token(xh[n], k, k < K);
-                    if constexpr (LO) l[u][n] = ld_token(xl[n], k, k < K);
-                }
-            if (u0 == 0 && !wait()) return false;
-#pragma unroll
-            for (int u = 0; u < UB; ++u) {
-                const uint4 fa = ptx::ld_shared_v4(row + (u0 + u) * 64u);
-                const uint4 fb = ptx::ld_shared_v4(row + St::BOX + (u0 + u) * 64u);
+            for (int u = 0; u < 2; ++u) {
+                const uint4 fa = ptx::ld_shared_v4(row + (u ? c1 : c0)), fb = ptx::ld_shared_v4(row + it.upper + (u ? c1 : c0));
                 uint32_t a[4] = {fa.x, fa.y, fa.z, fa.w}, b[4] = {fb.x, fb.y, fb.z, fb.w};
-                uint32_t al[4], bl[4];
                 if constexpr (SPLITW) {
+                    // fp16 weights as two bf16 halves; the lo halves meet the tokens' hi halves only
+                    uint32_t al[4], bl[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 va = unpack2<OUT_F16>(a[i]), vb = unpack2<OUT_F16>(b[i]);
                         split_pair(va.x, va.y, a[i], al[i]);
                         split_pair(vb.x, vb.y, b[i], bl[i]);
                     }
-                }
+                    MoeTokens<NT, false> hi;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 x = h[u][n];
-                    mma_16816<BF>(acc[n], a[0], b[0], a[1], b[1], x.x, x.y);
-                    mma_16816<BF>(acc[n], a[2], b[2], a[3], b[3], x.z, x.w);
-                    if constexpr (LO) {
-                        const uint4 y = l[u][n];
-                        mma_16816<BF>(acc[n], a[0], b[0], a[1], b[1], y.x, y.y);
-                        mma_16816<BF>(acc[n], a[2], b[2], a[3], b[3], y.z, y.w);
-                    }
-                    if constexpr (SPLITW) {
-                        mma_16816<BF>(acc[n], al[0], bl[0], al[1], bl[1], x.x, x.y);
-                        mma_16816<BF>(acc[n], al[2], bl[2], al[3], bl[3], x.z, x.w);
-                    }
+                    for (int n = 0; n < NT; ++n) hi.h[n] = x[u].h[n];
+                    piece_mma<true, NT, false>(acc, al, bl, hi);
                 }
+                piece_mma<BF, NT, LO>(acc, a, b, x[u]);
+                load_tokens<NT, LO>(x[u], xh, xl, (2 * s + 2 + u) * 32 + (int)t4 * 8, pr.K);
             }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(m.pp.empty0 + 8 * slot);
         }
     }
     return true;
 }
 
-// The ring and the item buffers of one CTA.
-struct MoePipe {
-    Pipe pp;
-    uint32_t ring;                   // shared address of the stages
-    uint32_t rfull, rempty;          // partial sums: written / read, two buffers each
-};
-
-// One warp's part of an item: its stages, then its partial sums to red[buf].
-template <int W, int NT, bool LO, bool SPLITW>
-__device__ __forceinline__ bool item_mma(MoeShared &S, const MoePipe &m, const MoeProduct &pr, uint32_t base, uint32_t item,
-                                         const uint16_t *const (&xh)[NT], const uint16_t *const (&xl)[NT],
-                                         uint32_t sa_off, uint32_t sb_off)
-{
-    using St = MoeStage<W>;
-    const int w = (int)(threadIdx.x >> 5) - 1, lane = threadIdx.x & 31, t4 = lane & 3, g = lane >> 2;
-    float acc[NT][4] = {};
-    for (int s = (int)(((uint32_t)w - base) % MOE_MMA_WARPS); s < pr.stages; s += MOE_MMA_WARPS) {
-        const uint32_t use = base + (uint32_t)s, slot = use % St::SLOTS, phase = (use / St::SLOTS) & 1u;
-        const bool ok = stage_mma<W, NT, LO, SPLITW>(
-            acc, m.ring + slot * St::BYTES, xh, xl, s * St::KS, pr.K, sa_off, sb_off,
-            [&] { return mx_warp_wait(m.pp, m.pp.full0 + 8 * slot, phase); });
-        if (!ok) return false;
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(m.pp.empty0 + 8 * slot);
-    }
-    const uint32_t buf = item & 1u;
-    if (!mx_warp_wait(m.pp, m.rempty + 8 * buf, ((item >> 1) & 1u) ^ 1u)) return false;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        *reinterpret_cast<float2 *>(&S.red[buf][w][g][n * 8 + 2 * t4]) = make_float2(acc[n][0], acc[n][1]);
-        *reinterpret_cast<float2 *>(&S.red[buf][w][g + 8][n * 8 + 2 * t4]) = make_float2(acc[n][2], acc[n][3]);
-    }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(m.rfull + 8 * buf);
-    return true;
-}
-
-// This lane's token rows: x by token, h by slot.
+// One item of the up (DOWN = false) or down product by one warp, stores included.
 template <int XT, int W, bool DOWN, int NT>
-__device__ __forceinline__ bool item_product(const MoeArgs &p, MoeShared &S, const MoePipe &m, const MoeProduct &pr,
-                                             uint32_t base, uint32_t item, int ai, int row0)
+__device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, const MoePipe &m, const MoeProduct &pr,
+                                         uint32_t use, int ai, int tile)
 {
-    const int g = (threadIdx.x & 31) >> 2, first = S.first[ai], cnt = S.first[ai + 1] - first;
+    constexpr bool LO = DOWN || (W == W_MX && XT == OUT_F16);
+    const int w = (int)(threadIdx.x >> 5) - 1, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int e = S.act[ai], first = S.first[ai], cnt = S.first[ai + 1] - first;
+    const int r = tile * pr.step + 8 * w + g;                  // this lane's row in the lower half, within the expert
+    MoeItem it;
+    it.row = (uint32_t)(8 * w + g) * 128u;
+    it.upper = (uint32_t)p.half_rows * 128u;
+    it.ra = (int64_t)e * pr.rows + r;
+    it.rb = it.ra + pr.half;
     const uint16_t *xh[NT], *xl[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -552,81 +536,59 @@ __device__ __forceinline__ bool item_product(const MoeArgs &p, MoeShared &S, con
             xh[n] = static_cast<const uint16_t *>(p.x) + s / p.top * p.H;
         }
     }
-    // the byte of a row's scale word: its place among the four 32-row groups of a tile
-    const uint32_t sa = (uint32_t)(row0 >> 5 & 3) * 4u, sb = (uint32_t)((row0 + pr.half) >> 5 & 3) * 4u;
-    constexpr bool LO = DOWN || (W == W_MX && XT == OUT_F16);
-    return item_mma<W, NT, LO, DOWN && W == W_F16>(S, m, pr, base, item, xh, xl, sa, sb);
-}
+    float acc[NT][4] = {};
+    if (!item_mma<W, NT, LO, DOWN && W == W_F16>(acc, m, pr, it, use, xh, xl)) return false;
 
-template <int XT, int W, bool DOWN>
-__device__ __forceinline__ bool mma_phase(const MoeArgs &p, MoeShared &S, const MoePipe &m, const MoeProduct &pr,
-                                          uint32_t &base, uint32_t &item)
-{
-    const int n = S.nact * pr.tiles;
-    const int i0 = (int)((int64_t)n * blockIdx.x / gridDim.x), i1 = (int)((int64_t)n * (blockIdx.x + 1) / gridDim.x);
-    for (int it = i0; it < i1; ++it, ++item, base += (uint32_t)pr.stages) {
-        const int ai = it / pr.tiles, cnt = S.first[ai + 1] - S.first[ai];
-        const int row0 = S.act[ai] * pr.rows + (it - ai * pr.tiles) * pr.step;
-        const bool ok = cnt <= 8    ? item_product<XT, W, DOWN, 1>(p, S, m, pr, base, item, ai, row0)
-                        : cnt <= 16 ? item_product<XT, W, DOWN, 2>(p, S, m, pr, base, item, ai, row0)
-                                    : item_product<XT, W, DOWN, 4>(p, S, m, pr, base, item, ai, row0);
-        if (!ok) return false;
-    }
+    // acc[n][0..1]: the lower row, tokens n * 8 + 2 t4 and the next; acc[n][2..3]: the upper row
+    const bool gated = pr.pairs;
+    const int r2 = gated ? r : r + pr.half;
+    const bool in1 = r < pr.limit, in2 = !gated && r2 < pr.limit;
+    const float *bias = DOWN ? p.b2 : p.b1;
+    const float bias1 = bias != nullptr && in1 ? bias[it.ra] : 0.0f;
+    const float bias2 = bias != nullptr && (gated ? in1 : in2) ? bias[it.rb] : 0.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = n * 8 + 2 * t4 + j;
+            if (c >= cnt) continue;
+            const int64_t s = S.slot[first + c];
+            float v1 = acc[n][j] + bias1, v2 = acc[n][2 + j] + bias2;
+            if constexpr (DOWN) {
+                if (in1) p.part[s * p.H + r] = v1;
+                if (in2) p.part[s * p.H + r2] = v2;
+            } else {
+                auto put = [&](int row, float v) {
+                    const int64_t at = s * p.Ip + (W == W_MX ? mx_order(row) : row);
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                    p.h_hi[at] = hi;
+                    p.h_lo[at] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                };
+                v1 = act_mx(p.act, v1, p.alpha);
+                if (gated) {
+                    if (in1) put(r, v1 * v2);
+                } else {
+                    if (in1) put(r, v1);
+                    if (in2) put(r2, act_mx(p.act, v2, p.alpha));
+                }
+            }
+        }
     return true;
 }
 
-// ----------------------------------------------------------------- epilogue --
-// Barrier of the epilogue's threads, which may arrive one lane after another.
-__device__ __forceinline__ void epilogue_sync()
+template <int XT, int W, bool DOWN>
+__device__ __forceinline__ bool mma_phase(const MoeArgs &p, const MoeShared &S, const MoePipe &m, const MoeProduct &pr,
+                                          uint32_t &use)
 {
-    asm volatile("barrier.sync 1, %0;" ::"n"(MOE_EPI_THREADS) : "memory");
-}
-
-__device__ __forceinline__ float red_sum(const MoeShared &S, uint32_t buf, int row, int col)
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < MOE_MMA_WARPS; ++w) s += S.red[buf][w][row][col];
-    return s;
-}
-
-template <int W, bool DOWN>
-__device__ __forceinline__ bool epilogue_phase(const MoeArgs &p, MoeShared &S, const MoePipe &m, const MoeProduct &pr,
-                                               uint32_t &item)
-{
-    const int tid = (int)threadIdx.x - 32 * (1 + MOE_MMA_WARPS), lane = threadIdx.x & 31;
     const int n = S.nact * pr.tiles;
     const int i0 = (int)((int64_t)n * blockIdx.x / gridDim.x), i1 = (int)((int64_t)n * (blockIdx.x + 1) / gridDim.x);
-    const int step = pr.step, shift = step == 8 ? 3 : 4;
-    for (int it = i0; it < i1; ++it, ++item) {
-        const int ai = it / pr.tiles, first = S.first[ai], cnt = S.first[ai + 1] - first;
-        const int e = S.act[ai], r0 = (it - ai * pr.tiles) * step;
-        const uint32_t buf = item & 1u;
-        if (!mx_warp_wait(m.pp, m.rfull + 8 * buf, (item >> 1) & 1u)) return false;
-        for (int i = tid; i < cnt << shift; i += MOE_EPI_THREADS) {
-            const int row = i & (step - 1), c = i >> shift, r = r0 + row;
-            if (r >= pr.limit) continue;
-            const int64_t s = S.slot[first + c];
-            float v = red_sum(S, buf, row, c);
-            if constexpr (DOWN) {
-                if (p.b2 != nullptr) v += p.b2[(int64_t)e * p.H + r];
-                p.part[s * p.H + r] = v;
-            } else {
-                if (p.b1 != nullptr) v += p.b1[(int64_t)e * p.R1 + r];
-                v = act_mx(p.act, v, p.alpha);
-                if (p.gated) {
-                    float u = red_sum(S, buf, 8 + row, c);
-                    if (p.b1 != nullptr) u += p.b1[(int64_t)e * p.R1 + p.I + r];
-                    v *= u;
-                }
-                const int64_t at = s * p.Ip + (W == W_MX ? mx_order(r) : r);
-                const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                p.h_hi[at] = hi;
-                p.h_lo[at] = __float2bfloat16_rn(v - __bfloat162float(hi));
-            }
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(m.rempty + 8 * buf);
+    for (int i = i0; i < i1; ++i, use += (uint32_t)pr.stages) {
+        const int ai = i / pr.tiles, tile = i - ai * pr.tiles, cnt = S.first[ai + 1] - S.first[ai];
+        bool ok;
+        if (cnt <= 8) ok = run_item<XT, W, DOWN, 1>(p, S, m, pr, use, ai, tile);
+        else if (cnt <= 16 || MOE_GROUP<W> == 16) ok = run_item<XT, W, DOWN, 2>(p, S, m, pr, use, ai, tile);
+        else ok = run_item<XT, W, DOWN, MOE_GROUP<W> / 8>(p, S, m, pr, use, ai, tile);
+        if (!ok) return false;
     }
     return true;
 }
@@ -655,25 +617,22 @@ __device__ __forceinline__ bool grid_wait(const Pipe &pp, unsigned int *counter)
 
 // ------------------------------------------------------------------- kernel --
 template <int W>
-__device__ __forceinline__ bool produce(const CUtensorMap *w, const CUtensorMap *sc, MoeShared &S, const MoePipe &m,
+__device__ __forceinline__ bool produce(const CUtensorMap *map, const MoeArgs &p, const MoeShared &S, const MoePipe &m,
                                         const MoeProduct &pr, uint32_t &use, uint64_t pol)
 {
-    using St = MoeStage<W>;
     const int n = S.nact * pr.tiles;
     const int i0 = (int)((int64_t)n * blockIdx.x / gridDim.x), i1 = (int)((int64_t)n * (blockIdx.x + 1) / gridDim.x);
-    for (int it = i0; it < i1; ++it) {
-        const int ai = it / pr.tiles, row = S.act[ai] * pr.rows + (it - ai * pr.tiles) * pr.step;
+    const uint32_t box = (uint32_t)p.half_rows * 128u;
+    for (int i = i0; i < i1; ++i) {
+        const int ai = i / pr.tiles, tile = i - ai * pr.tiles, row = S.act[ai] * pr.rows + tile * pr.step;
+        // the upper half of the last tile may have no rows (its products are not stored either)
+        const bool both = pr.pairs || tile * pr.step + p.half_rows < pr.limit;
         for (int s = 0; s < pr.stages; ++s, ++use) {
-            const uint32_t slot = use % St::SLOTS, full = m.pp.full0 + 8 * slot, to = m.ring + slot * St::BYTES;
-            if (!mx_warp_wait(m.pp, m.pp.empty0 + 8 * slot, ((use / St::SLOTS) & 1u) ^ 1u)) return false;
-            elected_expect_tx(full, (uint32_t)St::BYTES);
-            elected_load_2d(to, w, full, s * (St::ROW_BYTES / 2), row, pol);
-            elected_load_2d(to + St::BOX, w, full, s * (St::ROW_BYTES / 2), row + pr.half, pol);
-            if constexpr (W == W_MX) {
-                const int other = row + pr.half;
-                elected_load_3d(to + 2 * St::BOX, sc, full, (row & 31) * 4, s * 4, row >> 7);
-                elected_load_3d(to + 2 * St::BOX + 512, sc, full, (other & 31) * 4, s * 4, other >> 7);
-            }
+            const uint32_t slot = use % MOE_STAGES, full = m.pp.full0 + 8 * slot, to = m.ring + slot * MOE_STAGE_BYTES;
+            if (!mx_warp_wait(m.pp, m.pp.empty0 + 8 * slot, ((use / MOE_STAGES) & 1u) ^ 1u)) return false;
+            elected_expect_tx(full, both ? 2u * box : box);
+            elected_load_2d(to, map, full, s * 64, row, pol);
+            if (both) elected_load_2d(to + box, map, full, s * 64, row + pr.half, pol);
         }
     }
     return true;
@@ -681,68 +640,65 @@ __device__ __forceinline__ bool produce(const CUtensorMap *w, const CUtensorMap 
 
 template <int XT, int W>
 __global__ void __launch_bounds__(MOE_THREADS, 1)
-    moe_experts_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap ts1,
-                       const __grid_constant__ CUtensorMap tm2, const __grid_constant__ CUtensorMap ts2, const MoeArgs p)
+    moe_experts_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, const MoeArgs p)
 {
-    using St = MoeStage<W>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    MoeShared &S = *reinterpret_cast<MoeShared *>(smem + St::SLOTS * St::BYTES);
+    MoeShared &S = *reinterpret_cast<MoeShared *>(smem + MOE_STAGES * MOE_STAGE_BYTES);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int active = p.half_rows / 8;                        // product warps that have rows
     MoePipe m;
     m.ring = ptx::smem_addr(smem);
     m.pp.full0 = ptx::smem_addr(S.bar);
-    m.pp.empty0 = m.pp.full0 + 8 * St::SLOTS;
-    m.rfull = m.pp.empty0 + 8 * St::SLOTS;
-    m.rempty = m.rfull + 16;
+    m.pp.empty0 = m.pp.full0 + 8 * MOE_STAGES;
     m.pp.abort = reinterpret_cast<volatile uint32_t *>(&S.abort_flag);
     m.pp.status = p.status;
     m.pp.wait_ns = p.wait_ns;
+    const bool aligned = (m.ring & 1023u) == 0;                // the swizzle counts rows from multiples of 1024 bytes
     if (threadIdx.x == 0) {
+        if (!aligned) atomicOr(p.status, ST_SMEM_ALIGN);
         ptx::prefetch_tensormap(&tm1);
         ptx::prefetch_tensormap(&tm2);
-        for (int s = 0; s < 2 * St::SLOTS; ++s) ptx::mbar_init(m.pp.full0 + 8 * s, 1);
-        for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(m.rfull + 8 * b, MOE_MMA_WARPS);
-            ptx::mbar_init(m.rempty + 8 * b, MOE_EPI_WARPS);
+        for (int s = 0; s < MOE_STAGES; ++s) {
+            ptx::mbar_init(m.pp.full0 + 8 * s, 1);
+            ptx::mbar_init(m.pp.empty0 + 8 * s, (uint32_t)active);
         }
-        S.abort_flag = 0;
+        S.abort_flag = aligned ? 0 : 1;
         ptx::fence_mbar_init();
     }
-    static_assert(MOE_THREADS / 32 * MOE_MAX_E * 4 <= sizeof(S.red) && MOE_MAX_E <= 32 * 32, "a row of logits to a warp");
-    for (int t = warp; t < p.T; t += MOE_THREADS / 32)
-        choose_experts(p, S, &S.red[0][0][0][0] + warp * MOE_MAX_E, t, lane, blockIdx.x == 0);
+    for (int t = warp; t < p.T; t += MOE_THREADS / 32) choose_experts(p, S, t, lane, blockIdx.x == 0);
     ptx::cta_sync();
-    build_lists(p, S);
+    build_lists<MOE_GROUP<W>>(p, S);
 
-    const int per = p.gated ? 8 : 16;
-    const MoeProduct up = {p.H, (p.H + St::KS - 1) / St::KS, (p.I + per - 1) / per, p.R1, p.gated ? p.I : 8, per, p.I};
-    const MoeProduct down = {p.I, (p.I + St::KS - 1) / St::KS, (p.H + 15) / 16, p.H, 8, 16, p.H};
-    bool ok = true;
+    const int hr = p.half_rows, ks = STAGE_K<W>;
+    const int step1 = p.gated ? hr : 2 * hr, step2 = 2 * hr;
+    const MoeProduct up = {p.H, (p.H + ks - 1) / ks, (p.I + step1 - 1) / step1, p.R1, p.gated ? p.I : hr, step1, p.I,
+                           static_cast<const uint8_t *>(p.s1), (int64_t)p.E * p.R1, (p.H + 127) / 128, p.gated != 0};
+    const MoeProduct down = {p.I, (p.I + ks - 1) / ks, (p.H + step2 - 1) / step2, p.H, hr, step2, p.H,
+                             static_cast<const uint8_t *>(p.s2), (int64_t)p.E * p.H, (p.I + 127) / 128, false};
+    bool ok = aligned;
     if (warp == 0) {
         uint32_t use = 0;
         const uint64_t pol = ptx::createpolicy_evict_first();  // weights are read once
-        ok = produce<W>(&tm1, &ts1, S, m, up, use, pol) && produce<W>(&tm2, &ts2, S, m, down, use, pol);
+        ok = ok && produce<W>(&tm1, p, S, m, up, use, pol) && produce<W>(&tm2, p, S, m, down, use, pol);
         if (!ok && lane == 0) pipe_fail(m.pp);
         // every copy has landed before the CTA exits
-        for (uint32_t u = use > (uint32_t)St::SLOTS ? use - St::SLOTS : 0; u < use; ++u)
-            ptx::mbar_wait_bounded(m.pp.full0 + 8 * (u % St::SLOTS), (u / St::SLOTS) & 1u, DRAIN_NS, nullptr);
-    } else if (warp <= MOE_MMA_WARPS) {
-        uint32_t base = 0, item = 0;
-        ok = mma_phase<XT, W, false>(p, S, m, up, base, item);
-        // every h is written before any is read
-        if (ok) ok = __all_sync(0xffffffffu, lane != 0 || grid_wait(m.pp, p.counters)) != 0;
-        if (ok) ok = mma_phase<XT, W, true>(p, S, m, down, base, item);
-        if (!ok && lane == 0) pipe_fail(m.pp);
+        for (uint32_t u = use > (uint32_t)MOE_STAGES ? use - MOE_STAGES : 0; u < use; ++u)
+            ptx::mbar_wait_bounded(m.pp.full0 + 8 * (u % MOE_STAGES), (u / MOE_STAGES) & 1u, DRAIN_NS, nullptr);
     } else {
-        uint32_t item = 0;
-        ok = epilogue_phase<W, false>(p, S, m, up, item);
+        uint32_t use = 0;
+        if (ok && warp <= active) ok = mma_phase<XT, W, false>(p, S, m, up, use);
+        // every h is written before any is read
+        __syncwarp();
+        asm volatile("barrier.sync 1, %0;" ::"n"(32 * MOE_MMA_WARPS) : "memory");
         if (ok) {
-            epilogue_sync();
-            if (threadIdx.x == 32 * (1 + MOE_MMA_WARPS)) grid_arrive(p.counters);
-            ok = epilogue_phase<W, true>(p, S, m, down, item);
+            if (threadIdx.x == 32) grid_arrive(p.counters);
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, lane != 0 || grid_wait(m.pp, p.counters)) != 0;
         }
+        if (ok && warp <= active) ok = mma_phase<XT, W, true>(p, S, m, down, use);
         if (!ok && lane == 0) pipe_fail(m.pp);
     }
+    __syncwarp();
     // every o is written before y is summed
     ptx::cta_sync();
     if (threadIdx.x == 0) {
@@ -766,27 +722,29 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     }
 }
 
+constexpr int MOE_SMEM = MOE_STAGES * MOE_STAGE_BYTES + (int)sizeof(MoeShared);
+
 template <int XT, int W>
 static cudaError_t launch_experts(const MoeLaunch &L, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)L.grid);
     cfg.blockDim = dim3(MOE_THREADS);
-    cfg.dynamicSmemBytes = MoeStage<W>::SMEM;
+    cfg.dynamicSmemBytes = MOE_SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;               // the CTAs wait for one another
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_experts_kernel<XT, W>, L.tm1, L.ts1, L.tm2, L.ts2, L.args);
+    return cudaLaunchKernelEx(&cfg, moe_experts_kernel<XT, W>, L.tm1, L.tm2, L.args);
 }
 
 template <int XT, int W>
 static cudaError_t setup_experts()
 {
     return cudaFuncSetAttribute(moe_experts_kernel<XT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                MoeStage<W>::SMEM);
+                                MOE_SMEM);
 }
 
 cudaError_t setup_moe_kernels()

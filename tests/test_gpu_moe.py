@@ -81,7 +81,8 @@ TYPES = [("bf16", "bf16"), ("f16", "f16"), ("bf16", "mxfp4"), ("f16", "mxfp4")]
 @pytest.mark.parametrize("T,H,I,E,top", [(1, 8, 8, 1, 1), (1, 256, 64, 8, 2), (2, 40, 24, 5, 5), (3, 520, 136, 16, 3),
                                          (13, 264, 200, 21, 2), (17, 128, 96, 4, 1), (33, 96, 160, 7, 4),
                                          (64, 72, 40, 3, 2), (64, 136, 64, 40, 16), (5, 1032, 16, 512, 8), (1, 4096, 520, 6, 2),
-                                         (9, 2304, 1048, 4, 2), (40, 520, 2600, 3, 1)])
+                                         (9, 2304, 1048, 4, 2), (40, 520, 2600, 3, 1), (2, 48, 16, 3, 1),
+                                         (5, 64, 32, 4, 2), (2, 96, 64, 60, 1), (30, 200, 64, 90, 8)])
 def test_layer(dtype, weights, T, H, I, E, top):
     gated, bias = (T + E) % 3 != 0, T % 2 == 1
     L = layer(T * 131 + H + I + E, T, H, I, E, dtype, weights, gated, bias)
