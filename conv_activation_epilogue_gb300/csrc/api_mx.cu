@@ -199,6 +199,8 @@ cudaError_t quantize_launch(const void *x, void *codes, void *scales, int64_t ro
                                  transposed != 0, stream);
 }
 
+constexpr int64_t MOE_K_PAD = 256;   // K of a stage of tokens
+
 // Where the parts of mmact_moe's workspace begin.
 struct MoeWorkspace {
     int64_t logits, x_hi, x_lo, h_hi, h_lo, part, bytes;
@@ -207,7 +209,7 @@ struct MoeWorkspace {
 MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
 {
     MoeWorkspace w;
-    const int64_t Hp = round_up(H, 32), Ip = round_up(I, 32);
+    const int64_t Hp = round_up(H, MOE_K_PAD), Ip = round_up(I, MOE_K_PAD);
     int64_t at = 256;                                          // two counters
     auto take = [&at](int64_t bytes) {
         const int64_t here = at;
@@ -376,8 +378,8 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
     a.gated = gated != 0;
     a.normalize = normalize != 0;
     a.R1 = (int)(a.gated ? 2 * I : I);
-    a.Hp = (int)round_up(H, 32);
-    a.Ip = (int)round_up(I, 32);
+    a.Hp = (int)round_up(H, MOE_K_PAD);
+    a.Ip = (int)round_up(I, MOE_K_PAD);
     a.act = (int)act;
     a.alpha = alpha;
     a.w_type = mx ? 2 : (w_dtype == MMACT_BF16 ? 1 : 0);
@@ -397,10 +399,10 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
     char *ws = static_cast<char *>(workspace);
     a.counters = reinterpret_cast<unsigned int *>(ws);
     a.logits = reinterpret_cast<float *>(ws + w.logits);
-    a.x_hi = reinterpret_cast<__nv_bfloat16 *>(ws + w.x_hi);
-    a.x_lo = reinterpret_cast<__nv_bfloat16 *>(ws + w.x_lo);
-    a.h_hi = reinterpret_cast<__nv_bfloat16 *>(ws + w.h_hi);
-    a.h_lo = reinterpret_cast<__nv_bfloat16 *>(ws + w.h_lo);
+    a.x_hi = reinterpret_cast<uint16_t *>(ws + w.x_hi);
+    a.x_lo = reinterpret_cast<uint16_t *>(ws + w.x_lo);
+    a.h_hi = reinterpret_cast<uint16_t *>(ws + w.h_hi);
+    a.h_lo = reinterpret_cast<uint16_t *>(ws + w.h_lo);
     a.part = reinterpret_cast<float *>(ws + w.part);
     a.status = c.dev.status;
     a.wait_ns = c.dev.wait_ns;

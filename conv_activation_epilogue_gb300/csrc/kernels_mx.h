@@ -71,7 +71,7 @@ struct MoeArgs {
     int T, H, I, E, top;         // tokens, model width, experts' width, experts, experts per token
     int R1;                      // rows of one expert's w1: 2 I when gated, else I
     int half_rows;               // rows of half a tile of weights: 64, 32 or 16
-    int Hp, Ip;                  // H and I rounded up to 32 (row pitches of the workspace's arrays)
+    int Hp, Ip;                  // H and I rounded up to whole ring stages (row pitches of the workspace's arrays)
     int gated, normalize, act;
     int w_type;                  // 0 fp16, 1 bf16, 2 MXFP4
     float alpha;
@@ -85,8 +85,8 @@ struct MoeArgs {
     // workspace
     unsigned int *counters;      // two grid barriers
     float *logits;               // [T, E]
-    __nv_bfloat16 *x_hi, *x_lo;  // MXFP4: x in the codes' order [T, Hp]
-    __nv_bfloat16 *h_hi, *h_lo;  // [T * top, Ip]
+    uint16_t *x_hi, *x_lo;       // x as the products read it [T, Hp] (lo: fp16 x with MXFP4 weights)
+    uint16_t *h_hi, *h_lo;       // h in bf16 halves [T * top, Ip]
     float *part;                 // [T * top, H]
     unsigned int *status;
     unsigned long long wait_ns;

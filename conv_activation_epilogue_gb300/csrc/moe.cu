@@ -20,14 +20,15 @@
 //                ring stage.  It runs ahead over items and over the grid barrier:
 //                weights of the down product are on their way while the last h is
 //                being finished.
+//   warp 9       tokens of the stage (x, or h once the grid barrier is passed), one
+//                bulk copy for each token
 //   warps 1..8   products: each has 8 + 8 rows of the tile on mma.sync.m16n8k16
 //                as the 16-row operand (a gate row and its up row meet in one
 //                thread) and eight tokens to its columns, over all of K, so no sums
 //                cross warps; bias, activation and stores follow in registers.
 //                Which K a lane holds does not matter to a sum over K as long as
 //                both operands agree, so fragments are 16-byte loads in memory
-//                order.  A stage's tokens are loaded (from L2 once, from L1 by the
-//                other warps) while the stage before it is computed.
+//                order.
 //
 // The intermediate h is held as two bf16 halves hi = bf16(h), lo = bf16(h - hi),
 // 16 bits of it, and multiplied as both, so no rounding to 16 bits stands between
@@ -44,17 +45,32 @@ enum : int { W_F16 = 0, W_BF16 = 1, W_MX = 2 };
 
 constexpr int MOE_MAX_T = 64, MOE_MAX_K = 16, MOE_MAX_E = 512;
 constexpr int MOE_MMA_WARPS = 8;
-constexpr int MOE_THREADS = 32 * (1 + MOE_MMA_WARPS);
+constexpr int MOE_THREADS = 32 * (2 + MOE_MMA_WARPS);
 
-// Tokens of one expert that share a read of its weights.  MXFP4 rows cover four
-// times the K of a 16-byte load, so their tokens take four times the registers.
+// Tokens of one expert that share a read of its weights.
 template <int W>
 constexpr int MOE_GROUP = W == W_MX ? 16 : 32;
 constexpr int MOE_MIN_GROUP = 16;
 
-// The ring: 8 stages of at most 128 rows x 128 bytes, twice what has to be in
-// flight on an SM; the rest of its memory caches the tokens.
-constexpr int MOE_STAGES = 8, MOE_STAGE_BYTES = 16384;
+// Two rings.  A stage of weights is at most 128 rows x 128 bytes: 8 stages, about
+// twice what has to be in flight on an SM.  A stage of tokens is the group's
+// tokens over 256 K (four stages of 16-bit weights, one of MXFP4), hi and lo, a
+// record for each: 512 bytes to a copy, because copies of 128 bytes were measured
+// to keep one warp busy for twice the time of the weights' stage.  A record is 64
+// bytes longer than a multiple of 128, so that two tokens' 64-byte pieces lie on
+// different banks.
+constexpr int MOE_STAGE_BYTES = 16384, MOE_STAGES = 8;
+constexpr int MOE_TOKEN_K = 256, MOE_TOKEN = MOE_TOKEN_K * 2, MOE_RECORD = 2 * MOE_TOKEN + 64;
+template <int W>
+struct MoeRing {
+    static constexpr int K = W == W_MX ? 256 : 64;             // K of a stage of weights
+    static constexpr int SPAN = MOE_TOKEN_K / K;               // stages of weights to one of tokens
+    static constexpr int TOKENS = MOE_GROUP<W> * MOE_RECORD;   // bytes of a stage of tokens
+    static constexpr int TSTAGES = W == W_MX ? 4 : 2;
+    static constexpr int OFF_TOKENS = MOE_STAGES * MOE_STAGE_BYTES;
+    static constexpr int BYTES = OFF_TOKENS + TSTAGES * TOKENS;
+};
+constexpr int MOE_MAX_TSTAGES = 4;
 
 // ------------------------------------------------------------------ helpers --
 // A logit as a key whose unsigned order is the float order, NaN above all, and
@@ -82,12 +98,16 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Where element k of a token's row stands in the bf16 arrays that MXFP4 weights
-// multiply: within each group of eight the order 0 4 1 5 2 6 3 7, because a
-// 32-bit word of eight codes yields its values as the pairs (i, i + 4).
-__device__ __forceinline__ int mx_order(int k)
+// Where element k of a token's row stands in the arrays that the products read.
+// 16-bit weights: in place.  MXFP4: a lane holds a block of 32 codes, four words
+// of eight, and a warp multiplies word w of the blocks t = 0..3 of 128 K at a
+// time: so [w][t][8], and within the eight the order 0 4 1 5 2 6 3 7, because a
+// word of eight codes yields its values as the pairs (i, i + 4).
+template <int W>
+__device__ __forceinline__ int token_at(int k)
 {
-    return (k & ~7) | ((k & 3) << 1) | ((k >> 2) & 1);
+    if constexpr (W != W_MX) return k;
+    return (k & ~127) | ((k >> 3 & 3) << 5) | ((k >> 5 & 3) << 3) | ((k & 3) << 1) | (k >> 2 & 1);
 }
 
 // Eight codes times X as four bf16 pairs (i, i + 4).  A code moved to the top of
@@ -142,13 +162,30 @@ __device__ __forceinline__ void elected_load_2d(uint32_t dst, const CUtensorMap 
 
 #undef MMACT_ELECTED
 
+// Copy of `bytes` (a multiple of 16) from global to shared memory, both 16-byte
+// aligned, counted on an mbarrier; by each lane that calls it.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Orders this thread's (and, through barriers, others') ordinary global accesses
+// with bulk copies.
+__device__ __forceinline__ void fence_proxy_async_all()
+{
+    asm volatile("fence.proxy.async;" ::: "memory");
+}
+
 // ------------------------------------------------------------------- router --
 // One CTA for an expert and eight tokens: four warps share K.  The CTAs past
-// those prepare what the experts kernel needs: its counters, and for MXFP4
-// weights x in bf16 in the codes' order and the zeros past I of h.
+// those prepare what the experts kernel reads, a token each: its counters, x in
+// the products' order (MXFP4: as bf16, hi and for fp16 x lo) with zeros up to a
+// whole stage, and the same zeros of h.
 constexpr int MOE_ROUTER_THREADS = 128;
 
-template <int XT>
+template <int XT, int W>
 __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const MoeArgs p, int token_groups)
 {
     ptx::griddep_launch_dependents();
@@ -195,31 +232,29 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
     }
     const int t = blockIdx.x - p.E * token_groups;
     if (t == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
-    if (p.w_type == W_MX) {
-        const uint16_t *x = xs + (int64_t)t * p.H;
-        for (int k = threadIdx.x; k < p.Hp; k += MOE_ROUTER_THREADS) {
-            float v = 0.0f;
-            if (k < p.H) {
-                if constexpr (XT == OUT_BF16) v = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(x)[k]);
-                else v = __half2float(reinterpret_cast<const __half *>(x)[k]);
-            }
+    const uint16_t *x = xs + (int64_t)t * p.H;
+    for (int k = threadIdx.x; k < p.Hp; k += MOE_ROUTER_THREADS) {
+        const int64_t at = (int64_t)t * p.Hp + token_at<W>(k);
+        const uint16_t raw = k < p.H ? x[k] : (uint16_t)0;
+        if constexpr (W != W_MX || XT == OUT_BF16) {
+            p.x_hi[at] = raw;
+        } else {
+            const float v = __half2float(__ushort_as_half(raw));
             const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-            const int64_t at = (int64_t)t * p.Hp + mx_order(k);
-            p.x_hi[at] = hi;
-            if constexpr (XT == OUT_F16) p.x_lo[at] = __float2bfloat16_rn(v - __bfloat162float(hi));
+            p.x_hi[at] = __bfloat16_as_ushort(hi);
+            p.x_lo[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v - __bfloat162float(hi)));
         }
-        const int pad = p.Ip - p.I;
-        for (int i = threadIdx.x; i < pad * p.top; i += MOE_ROUTER_THREADS) {
-            const int64_t at = ((int64_t)t * p.top + i / pad) * p.Ip + p.I + i % pad;
-            p.h_hi[at] = p.h_lo[at] = __float2bfloat16_rn(0.0f);
-        }
+    }
+    const int pad = p.Ip - p.I;
+    for (int i = threadIdx.x; i < pad * p.top; i += MOE_ROUTER_THREADS) {
+        const int64_t at = ((int64_t)t * p.top + i / pad) * p.Ip + token_at<W>(p.I + i % pad);
+        p.h_hi[at] = p.h_lo[at] = 0;
     }
 }
 
 // ------------------------------------------------------------ choice of experts --
 // Shared memory of the experts kernel beside the ring.
 struct MoeShared {
-    float logits[MOE_THREADS / 32][MOE_MAX_E];     // one token's to a warp, while experts are chosen
     float probs[MOE_MAX_T * MOE_MAX_K];
     short choice[MOE_MAX_T * MOE_MAX_K];           // slot t * k + j -> expert
     short slot[MOE_MAX_T * MOE_MAX_K];             // slots by expert
@@ -228,15 +263,14 @@ struct MoeShared {
     short first[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP + 1];                   // the expert and the first entry of slot[]
     int nact;
     int abort_flag, go;
-    uint64_t bar[2 * MOE_STAGES];
+    uint64_t bar[2 * MOE_STAGES + 2 * MOE_MAX_TSTAGES];
 };
 
 // Top k of one token by one warp: each round the largest (key, lowest index) of
-// those left; then the softmax weights.
-__device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, int t, int lane, bool write)
+// those left; then the softmax weights.  The token's logits are kept in `row`.
+__device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, float *row, int t, int lane, bool write)
 {
     static_assert(MOE_MAX_E <= 32 * 32, "one bit for each of a lane's logits");
-    float *row = S.logits[threadIdx.x >> 5];
     __syncwarp();
     for (int e = lane; e < p.E; e += 32) row[e] = __ldcg(p.logits + (int64_t)t * p.E + e);
     __syncwarp();
@@ -329,7 +363,7 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S)
 // One product of the layer as the roles see it.  A tile is 2 * half_rows weight
 // rows: r0 .. r0 + half_rows and the same number from `half` rows further on.
 struct MoeProduct {
-    int K, stages;                   // ring stages of one item
+    int K, stages, tstages;          // ring stages of one item: weights, tokens
     int tiles;                       // items of one group of tokens
     int rows;                        // rows of one expert's matrix
     int half;                        // row distance between a tile's halves: I (gate, up), or half_rows
@@ -340,9 +374,6 @@ struct MoeProduct {
     int scale_tiles;                 // tiles of 128 K
     bool pairs;                      // the halves go together (gate, up)
 };
-
-template <int W>
-constexpr int STAGE_K = W == W_MX ? 256 : 64;                  // 128 bytes of a row
 
 __device__ __forceinline__ uint32_t word_of(const uint4 &u, int i)
 {
@@ -374,75 +405,82 @@ struct MoeTokens {
     uint4 h[NT], l[LO ? NT : 1];
 };
 
-// xh / xl: this lane's token rows (hi, lo), null where there is no token.
 template <int NT, bool LO>
-__device__ __forceinline__ void load_tokens(MoeTokens<NT, LO> &x, const uint16_t *const (&xh)[NT],
-                                            const uint16_t *const (&xl)[NT], int k, int K)
+__device__ __forceinline__ void load_tokens(MoeTokens<NT, LO> &x, uint32_t at)
 {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        x.h[n] = make_uint4(0, 0, 0, 0);
-        if constexpr (LO) x.l[n] = make_uint4(0, 0, 0, 0);
-        if (k < K && xh[n] != nullptr) {
-            x.h[n] = *reinterpret_cast<const uint4 *>(xh[n] + k);
-            if constexpr (LO) x.l[n] = *reinterpret_cast<const uint4 *>(xl[n] + k);
-        }
+        x.h[n] = ptx::ld_shared_v4(at + n * 8 * MOE_RECORD);
+        if constexpr (LO) x.l[n] = ptx::ld_shared_v4(at + n * 8 * MOE_RECORD + MOE_TOKEN);
     }
 }
 
 // acc += 16 rows x tokens over one piece: a, b the two rows' four pairs of values.
+// The lo halves have sums of their own, so that half as many instructions wait
+// for one another.
 template <bool BF, int NT, bool LO>
-__device__ __forceinline__ void piece_mma(float (&acc)[NT][4], const uint32_t (&a)[4], const uint32_t (&b)[4],
-                                          const MoeTokens<NT, LO> &x)
+__device__ __forceinline__ void piece_mma(float (&acc)[NT][4], float (&low)[LO ? NT : 1][4], const uint32_t (&a)[4],
+                                          const uint32_t (&b)[4], const MoeTokens<NT, LO> &x)
 {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         mma_16816<BF>(acc[n], a[0], b[0], a[1], b[1], x.h[n].x, x.h[n].y);
+        if constexpr (LO) mma_16816<BF>(low[n], a[0], b[0], a[1], b[1], x.l[n].x, x.l[n].y);
         mma_16816<BF>(acc[n], a[2], b[2], a[3], b[3], x.h[n].z, x.h[n].w);
-        if constexpr (LO) {
-            mma_16816<BF>(acc[n], a[0], b[0], a[1], b[1], x.l[n].x, x.l[n].y);
-            mma_16816<BF>(acc[n], a[2], b[2], a[3], b[3], x.l[n].z, x.l[n].w);
-        }
+        if constexpr (LO) mma_16816<BF>(low[n], a[2], b[2], a[3], b[3], x.l[n].z, x.l[n].w);
     }
 }
 
-// The ring of one CTA.
+// The rings of one CTA.
 struct MoePipe {
-    Pipe pp;
-    uint32_t ring;                   // shared address of the stages
+    Pipe pp;                         // weights: full0, empty0
+    uint32_t tfull0, tempty0;        // tokens
+    uint32_t ring, tokens;           // shared addresses
 };
 
-// One warp's rows of an item over all of K: the two units of 64 bytes of each
-// stage.  Every piece of tokens is loaded again, for the unit or stage after the
-// next, as soon as its products are issued.
+// Stages used so far by a role.
+struct MoeUse {
+    uint32_t w, t;
+};
+
+// One warp's rows of an item over all of K: the two units of 64 bytes of each stage.
 template <int W, int NT, bool LO, bool SPLITW>
 __device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
-                                         uint32_t use, const uint16_t *const (&xh)[NT], const uint16_t *const (&xl)[NT])
+                                         MoeUse use)
 {
+    using R = MoeRing<W>;
     const int lane = threadIdx.x & 31;
     const uint32_t sw = (uint32_t)(lane >> 2), t4 = (uint32_t)(lane & 3);   // the 128-byte swizzle: chunk ^ (row & 7)
     const uint32_t c0 = (t4 ^ sw) << 4, c1 = ((4u + t4) ^ sw) << 4;
+    float low[LO || SPLITW ? NT : 1][4] = {};
+    // MXFP4: the scale words of the two rows, loaded a stage ahead
+    int64_t sa_at = 0, sb_at = 0;
+    bool has_a = false, has_b = false;
+    uint32_t wa[2] = {}, wb[2] = {};
+    auto scales = [&](int u, uint32_t &a, uint32_t &b) {
+        a = has_a && u < pr.scale_tiles ? __ldg(reinterpret_cast<const uint32_t *>(pr.scales + sa_at + (int64_t)u * 512)) : 0u;
+        b = has_b && u < pr.scale_tiles ? __ldg(reinterpret_cast<const uint32_t *>(pr.scales + sb_at + (int64_t)u * 512)) : 0u;
+    };
     if constexpr (W == W_MX) {
-        // a unit is 128 K: a block of 32 codes to a lane, four words of eight
-        MoeTokens<NT, LO> x[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) load_tokens<NT, LO>(x[w], xh, xl, (int)t4 * 32 + w * 8, pr.K);
-        const int64_t sa_at = mx_scale_at(it.ra, 0, pr.scale_tiles), sb_at = mx_scale_at(it.rb, 0, pr.scale_tiles);
-        const bool has_a = it.ra < pr.all_rows, has_b = it.rb < pr.all_rows;
-        auto scales = [&](int u, uint32_t &a, uint32_t &b) {   // the rows' scale words of unit u
-            a = has_a && u < pr.scale_tiles ? __ldg(reinterpret_cast<const uint32_t *>(pr.scales + sa_at + (int64_t)u * 512)) : 0u;
-            b = has_b && u < pr.scale_tiles ? __ldg(reinterpret_cast<const uint32_t *>(pr.scales + sb_at + (int64_t)u * 512)) : 0u;
-        };
-        uint32_t wa[2], wb[2];
+        sa_at = mx_scale_at(it.ra, 0, pr.scale_tiles);
+        sb_at = mx_scale_at(it.rb, 0, pr.scale_tiles);
+        has_a = it.ra < pr.all_rows;
+        has_b = it.rb < pr.all_rows;
         scales(0, wa[0], wb[0]);
         scales(1, wa[1], wb[1]);
+    }
 #pragma unroll 1
-        for (int s = 0; s < pr.stages; ++s, ++use) {
-            const uint32_t slot = use % MOE_STAGES, row = m.ring + slot * MOE_STAGE_BYTES + it.row;
-            if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * slot, (use / MOE_STAGES) & 1u)) return false;
+    for (int s = 0; s < pr.stages; ++s, ++use.w) {
+        const uint32_t slot = use.w % MOE_STAGES, row = m.ring + slot * MOE_STAGE_BYTES + it.row;
+        const uint32_t part = (uint32_t)s % R::SPAN, tslot = use.t % R::TSTAGES;
+        const uint32_t tok = m.tokens + tslot * R::TOKENS + sw * MOE_RECORD + part * (R::K * 2u) + t4 * 16u;
+        if (part == 0 && !mx_warp_wait(m.pp, m.tfull0 + 8 * tslot, (use.t / R::TSTAGES) & 1u)) return false;
+        if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * slot, (use.w / MOE_STAGES) & 1u)) return false;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint4 fa = ptx::ld_shared_v4(row + (u ? c1 : c0)), fb = ptx::ld_shared_v4(row + it.upper + (u ? c1 : c0));
+        for (int u = 0; u < 2; ++u) {
+            const uint4 fa = ptx::ld_shared_v4(row + (u ? c1 : c0)), fb = ptx::ld_shared_v4(row + it.upper + (u ? c1 : c0));
+            if constexpr (W == W_MX) {
+                // 128 K: a block of 32 codes to a lane, four words of eight
                 const uint32_t sa = (wa[u] >> (8 * t4)) & 255u, sb = (wb[u] >> (8 * t4)) & 255u;
                 scales(2 * s + 2 + u, wa[u], wb[u]);
                 uint32_t ra, rb;
@@ -450,6 +488,8 @@ __device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, 
                 const bool big = __any_sync(0xffffffffu, sa > 128u || sb > 128u);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
+                    MoeTokens<NT, LO> x;
+                    load_tokens<NT, LO>(x, tok + u * 256u + w * 64u);
                     uint32_t va[4], vb[4];
                     mx_word_bf16(word_of(fa, w), ma, va);
                     mx_word_bf16(word_of(fb, w), mb, vb);
@@ -460,26 +500,12 @@ __device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, 
                             vb[i] = mul_bf16x2(vb[i], rb);
                         }
                     }
-                    piece_mma<true, NT, LO>(acc, va, vb, x[w]);
-                    load_tokens<NT, LO>(x[w], xh, xl, (2 * s + u + 1) * 128 + (int)t4 * 32 + w * 8, pr.K);
+                    piece_mma<true, NT, LO>(acc, low, va, vb, x);
                 }
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(m.pp.empty0 + 8 * slot);
-        }
-    } else {
-        // a unit is 32 K: 8 values to a lane
-        constexpr bool BF = W == W_BF16 || SPLITW;
-        MoeTokens<NT, LO> x[2];
-        load_tokens<NT, LO>(x[0], xh, xl, (int)t4 * 8, pr.K);
-        load_tokens<NT, LO>(x[1], xh, xl, 32 + (int)t4 * 8, pr.K);
-#pragma unroll 1
-        for (int s = 0; s < pr.stages; ++s, ++use) {
-            const uint32_t slot = use % MOE_STAGES, row = m.ring + slot * MOE_STAGE_BYTES + it.row;
-            if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * slot, (use / MOE_STAGES) & 1u)) return false;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint4 fa = ptx::ld_shared_v4(row + (u ? c1 : c0)), fb = ptx::ld_shared_v4(row + it.upper + (u ? c1 : c0));
+            } else {
+                // 32 K: 8 values to a lane
+                MoeTokens<NT, LO> x;
+                load_tokens<NT, LO>(x, tok + u * 64u);
                 uint32_t a[4] = {fa.x, fa.y, fa.z, fa.w}, b[4] = {fb.x, fb.y, fb.z, fb.w};
                 if constexpr (SPLITW) {
                     // fp16 weights as two bf16 halves; the lo halves meet the tokens' hi halves only
@@ -490,25 +516,35 @@ __device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, 
                         split_pair(va.x, va.y, a[i], al[i]);
                         split_pair(vb.x, vb.y, b[i], bl[i]);
                     }
-                    MoeTokens<NT, false> hi;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) hi.h[n] = x[u].h[n];
-                    piece_mma<true, NT, false>(acc, al, bl, hi);
+                    for (int n = 0; n < NT; ++n) {
+                        mma_16816<true>(low[n], al[0], bl[0], al[1], bl[1], x.h[n].x, x.h[n].y);
+                        mma_16816<true>(low[n], al[2], bl[2], al[3], bl[3], x.h[n].z, x.h[n].w);
+                    }
                 }
-                piece_mma<BF, NT, LO>(acc, a, b, x[u]);
-                load_tokens<NT, LO>(x[u], xh, xl, (2 * s + 2 + u) * 32 + (int)t4 * 8, pr.K);
+                piece_mma<W == W_BF16 || SPLITW, NT, LO>(acc, low, a, b, x);
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(m.pp.empty0 + 8 * slot);
         }
+        const bool last = part == R::SPAN - 1 || s == pr.stages - 1;   // of its stage of tokens
+        __syncwarp();
+        if (lane == 0) {
+            ptx::mbar_arrive(m.pp.empty0 + 8 * slot);
+            if (last) ptx::mbar_arrive(m.tempty0 + 8 * tslot);
+        }
+        use.t += last ? 1u : 0u;
     }
+    if constexpr (LO || SPLITW)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[n][j] += low[n][j];
     return true;
 }
 
 // One item of the up (DOWN = false) or down product by one warp, stores included.
 template <int XT, int W, bool DOWN, int NT>
 __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, const MoePipe &m, const MoeProduct &pr,
-                                         uint32_t use, int ai, int tile)
+                                         const MoeUse &use, int ai, int tile)
 {
     constexpr bool LO = DOWN || (W == W_MX && XT == OUT_F16);
     const int w = (int)(threadIdx.x >> 5) - 1, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -519,25 +555,8 @@ __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, c
     it.upper = (uint32_t)p.half_rows * 128u;
     it.ra = (int64_t)e * pr.rows + r;
     it.rb = it.ra + pr.half;
-    const uint16_t *xh[NT], *xl[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        xh[n] = xl[n] = nullptr;
-        const int c = n * 8 + g;
-        if (c >= cnt) continue;
-        const int64_t s = S.slot[first + c];
-        if constexpr (DOWN) {
-            xh[n] = reinterpret_cast<const uint16_t *>(p.h_hi) + s * p.Ip;
-            xl[n] = reinterpret_cast<const uint16_t *>(p.h_lo) + s * p.Ip;
-        } else if constexpr (W == W_MX) {
-            xh[n] = reinterpret_cast<const uint16_t *>(p.x_hi) + s / p.top * p.Hp;
-            xl[n] = reinterpret_cast<const uint16_t *>(p.x_lo) + s / p.top * p.Hp;
-        } else {
-            xh[n] = static_cast<const uint16_t *>(p.x) + s / p.top * p.H;
-        }
-    }
     float acc[NT][4] = {};
-    if (!item_mma<W, NT, LO, DOWN && W == W_F16>(acc, m, pr, it, use, xh, xl)) return false;
+    if (!item_mma<W, NT, LO, DOWN && W == W_F16>(acc, m, pr, it, use)) return false;
 
     // acc[n][0..1]: the lower row, tokens n * 8 + 2 t4 and the next; acc[n][2..3]: the upper row
     const bool gated = pr.pairs;
@@ -559,10 +578,10 @@ __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, c
                 if (in2) p.part[s * p.H + r2] = v2;
             } else {
                 auto put = [&](int row, float v) {
-                    const int64_t at = s * p.Ip + (W == W_MX ? mx_order(row) : row);
+                    const int64_t at = s * p.Ip + token_at<W>(row);
                     const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                    p.h_hi[at] = hi;
-                    p.h_lo[at] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                    p.h_hi[at] = __bfloat16_as_ushort(hi);
+                    p.h_lo[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v - __bfloat162float(hi)));
                 };
                 v1 = act_mx(p.act, v1, p.alpha);
                 if (gated) {
@@ -578,11 +597,11 @@ __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, c
 
 template <int XT, int W, bool DOWN>
 __device__ __forceinline__ bool mma_phase(const MoeArgs &p, const MoeShared &S, const MoePipe &m, const MoeProduct &pr,
-                                          uint32_t &use)
+                                          MoeUse &use)
 {
     const int n = S.nact * pr.tiles;
     const int i0 = (int)((int64_t)n * blockIdx.x / gridDim.x), i1 = (int)((int64_t)n * (blockIdx.x + 1) / gridDim.x);
-    for (int i = i0; i < i1; ++i, use += (uint32_t)pr.stages) {
+    for (int i = i0; i < i1; ++i, use.w += (uint32_t)pr.stages, use.t += (uint32_t)pr.tstages) {
         const int ai = i / pr.tiles, tile = i - ai * pr.tiles, cnt = S.first[ai + 1] - S.first[ai];
         bool ok;
         if (cnt <= 8) ok = run_item<XT, W, DOWN, 1>(p, S, m, pr, use, ai, tile);
@@ -638,18 +657,52 @@ __device__ __forceinline__ bool produce(const CUtensorMap *map, const MoeArgs &p
     return true;
 }
 
+// The tokens of every item, in the weights' order: lane c copies token c's pieces.
+template <int XT, int W, bool DOWN>
+__device__ __forceinline__ bool produce_tokens(const MoeArgs &p, const MoeShared &S, const MoePipe &m, const MoeProduct &pr,
+                                               uint32_t &use)
+{
+    using R = MoeRing<W>;
+    constexpr bool LO = DOWN || (W == W_MX && XT == OUT_F16);
+    const int lane = threadIdx.x & 31, n = S.nact * pr.tiles;
+    const int i0 = (int)((int64_t)n * blockIdx.x / gridDim.x), i1 = (int)((int64_t)n * (blockIdx.x + 1) / gridDim.x);
+    for (int i = i0; i < i1; ++i) {
+        const int ai = i / pr.tiles, first = S.first[ai], cnt = S.first[ai + 1] - first;
+        const int64_t slot_of = lane < cnt ? S.slot[first + lane] : 0;
+        const int64_t from = DOWN ? slot_of * p.Ip : slot_of / p.top * p.Hp;
+        const uint16_t *hi = (DOWN ? p.h_hi : p.x_hi) + from, *lo = (DOWN ? p.h_lo : p.x_lo) + from;
+        for (int s = 0; s < pr.tstages; ++s, ++use) {
+            const uint32_t slot = use % R::TSTAGES, full = m.tfull0 + 8 * slot;
+            const uint32_t to = m.tokens + slot * R::TOKENS + (uint32_t)lane * MOE_RECORD;
+            if (!mx_warp_wait(m.pp, m.tempty0 + 8 * slot, ((use / R::TSTAGES) & 1u) ^ 1u)) return false;
+            elected_expect_tx(full, (uint32_t)cnt * MOE_TOKEN * (LO ? 2u : 1u));
+            __syncwarp();
+            if (lane < cnt) {
+                bulk_load(to, hi + s * MOE_TOKEN_K, MOE_TOKEN, full);
+                if constexpr (LO) bulk_load(to + MOE_TOKEN, lo + s * MOE_TOKEN_K, MOE_TOKEN, full);
+            }
+            __syncwarp();
+        }
+    }
+    return true;
+}
+
 template <int XT, int W>
 __global__ void __launch_bounds__(MOE_THREADS, 1)
     moe_experts_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, const MoeArgs p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    MoeShared &S = *reinterpret_cast<MoeShared *>(smem + MOE_STAGES * MOE_STAGE_BYTES);
+    using R = MoeRing<W>;
+    MoeShared &S = *reinterpret_cast<MoeShared *>(smem + R::BYTES);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int active = p.half_rows / 8;                        // product warps that have rows
     MoePipe m;
     m.ring = ptx::smem_addr(smem);
+    m.tokens = m.ring + R::OFF_TOKENS;
     m.pp.full0 = ptx::smem_addr(S.bar);
     m.pp.empty0 = m.pp.full0 + 8 * MOE_STAGES;
+    m.tfull0 = m.pp.empty0 + 8 * MOE_STAGES;
+    m.tempty0 = m.tfull0 + 8 * R::TSTAGES;
     m.pp.abort = reinterpret_cast<volatile uint32_t *>(&S.abort_flag);
     m.pp.status = p.status;
     m.pp.wait_ns = p.wait_ns;
@@ -662,18 +715,26 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
             ptx::mbar_init(m.pp.full0 + 8 * s, 1);
             ptx::mbar_init(m.pp.empty0 + 8 * s, (uint32_t)active);
         }
+        for (int s = 0; s < R::TSTAGES; ++s) {
+            ptx::mbar_init(m.tfull0 + 8 * s, 1);
+            ptx::mbar_init(m.tempty0 + 8 * s, (uint32_t)active);
+        }
         S.abort_flag = aligned ? 0 : 1;
         ptx::fence_mbar_init();
     }
-    for (int t = warp; t < p.T; t += MOE_THREADS / 32) choose_experts(p, S, t, lane, blockIdx.x == 0);
+    // the logits stand where the tokens will
+    static_assert(MOE_THREADS / 32 * MOE_MAX_E * 4 <= R::TSTAGES * R::TOKENS, "a row of logits to a warp");
+    float *row = reinterpret_cast<float *>(smem + R::OFF_TOKENS) + warp * MOE_MAX_E;
+    for (int t = warp; t < p.T; t += MOE_THREADS / 32) choose_experts(p, S, row, t, lane, blockIdx.x == 0);
+    ptx::fence_proxy_async_smem();                             // before the copies that overwrite them
     ptx::cta_sync();
     build_lists<MOE_GROUP<W>>(p, S);
 
-    const int hr = p.half_rows, ks = STAGE_K<W>;
+    const int hr = p.half_rows, ks = R::K, kt = MOE_TOKEN_K;
     const int step1 = p.gated ? hr : 2 * hr, step2 = 2 * hr;
-    const MoeProduct up = {p.H, (p.H + ks - 1) / ks, (p.I + step1 - 1) / step1, p.R1, p.gated ? p.I : hr, step1, p.I,
+    const MoeProduct up = {p.H, (p.H + ks - 1) / ks, (p.H + kt - 1) / kt, (p.I + step1 - 1) / step1, p.R1, p.gated ? p.I : hr, step1, p.I,
                            static_cast<const uint8_t *>(p.s1), (int64_t)p.E * p.R1, (p.H + 127) / 128, p.gated != 0};
-    const MoeProduct down = {p.I, (p.I + ks - 1) / ks, (p.H + step2 - 1) / step2, p.H, hr, step2, p.H,
+    const MoeProduct down = {p.I, (p.I + ks - 1) / ks, (p.I + kt - 1) / kt, (p.H + step2 - 1) / step2, p.H, hr, step2, p.H,
                              static_cast<const uint8_t *>(p.s2), (int64_t)p.E * p.H, (p.I + 127) / 128, false};
     bool ok = aligned;
     if (warp == 0) {
@@ -684,17 +745,25 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         // every copy has landed before the CTA exits
         for (uint32_t u = use > (uint32_t)MOE_STAGES ? use - MOE_STAGES : 0; u < use; ++u)
             ptx::mbar_wait_bounded(m.pp.full0 + 8 * (u % MOE_STAGES), (u / MOE_STAGES) & 1u, DRAIN_NS, nullptr);
-    } else {
+    } else if (warp == 1 + MOE_MMA_WARPS) {
         uint32_t use = 0;
-        if (ok && warp <= active) ok = mma_phase<XT, W, false>(p, S, m, up, use);
+        ok = ok && produce_tokens<XT, W, false>(p, S, m, up, use);
         // every h is written before any is read
+        if (ok) ok = __all_sync(0xffffffffu, lane != 0 || grid_wait(m.pp, p.counters)) != 0;
+        fence_proxy_async_all();
+        ok = ok && produce_tokens<XT, W, true>(p, S, m, down, use);
+        if (!ok && lane == 0) pipe_fail(m.pp);
+        for (uint32_t u = use > (uint32_t)R::TSTAGES ? use - R::TSTAGES : 0; u < use; ++u)
+            ptx::mbar_wait_bounded(m.tfull0 + 8 * (u % R::TSTAGES), (u / R::TSTAGES) & 1u, DRAIN_NS, nullptr);
+    } else {
+        MoeUse use = {0, 0};
+        if (ok && warp <= active) ok = mma_phase<XT, W, false>(p, S, m, up, use);
+        // this CTA's part of h is written
+        fence_proxy_async_all();
         __syncwarp();
         asm volatile("barrier.sync 1, %0;" ::"n"(32 * MOE_MMA_WARPS) : "memory");
-        if (ok) {
-            if (threadIdx.x == 32) grid_arrive(p.counters);
-            __syncwarp();
-            ok = __all_sync(0xffffffffu, lane != 0 || grid_wait(m.pp, p.counters)) != 0;
-        }
+        if (ok && threadIdx.x == 32) grid_arrive(p.counters);
+        __syncwarp();
         if (ok && warp <= active) ok = mma_phase<XT, W, true>(p, S, m, down, use);
         if (!ok && lane == 0) pipe_fail(m.pp);
     }
@@ -722,7 +791,9 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     }
 }
 
-constexpr int MOE_SMEM = MOE_STAGES * MOE_STAGE_BYTES + (int)sizeof(MoeShared);
+template <int W>
+constexpr int MOE_SMEM = MoeRing<W>::BYTES + (int)sizeof(MoeShared);
+static_assert(MOE_SMEM<W_BF16> <= 232448 && MOE_SMEM<W_MX> <= 232448, "shared memory budget");
 
 template <int XT, int W>
 static cudaError_t launch_experts(const MoeLaunch &L, cudaStream_t stream)
@@ -730,7 +801,7 @@ static cudaError_t launch_experts(const MoeLaunch &L, cudaStream_t stream)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)L.grid);
     cfg.blockDim = dim3(MOE_THREADS);
-    cfg.dynamicSmemBytes = MOE_SMEM;
+    cfg.dynamicSmemBytes = MOE_SMEM<W>;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;               // the CTAs wait for one another
@@ -744,7 +815,7 @@ template <int XT, int W>
 static cudaError_t setup_experts()
 {
     return cudaFuncSetAttribute(moe_experts_kernel<XT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                MOE_SMEM);
+                                MOE_SMEM<W>);
 }
 
 cudaError_t setup_moe_kernels()
@@ -759,10 +830,12 @@ cudaError_t setup_moe_kernels()
 cudaError_t launch_moe(const MoeLaunch &L, cudaStream_t stream)
 {
     const MoeArgs &a = L.args;
-    const int groups = (a.T + 7) / 8, extra = a.w_type == W_MX ? a.T : 1;
-    const dim3 grid((unsigned)(a.E * groups + extra)), block(MOE_ROUTER_THREADS);
-    cudaError_t e = L.x_out == OUT_BF16 ? launch_k(moe_router_kernel<OUT_BF16>, grid, block, 0, stream, a, groups)
-                                        : launch_k(moe_router_kernel<OUT_F16>, grid, block, 0, stream, a, groups);
+    const int groups = (a.T + 7) / 8;
+    const dim3 grid((unsigned)(a.E * groups + a.T)), block(MOE_ROUTER_THREADS);
+    auto router = a.w_type == W_MX ? (L.x_out == OUT_BF16 ? moe_router_kernel<OUT_BF16, W_MX> : moe_router_kernel<OUT_F16, W_MX>)
+                                   : (L.x_out == OUT_BF16 ? moe_router_kernel<OUT_BF16, W_BF16>
+                                                          : moe_router_kernel<OUT_F16, W_F16>);
+    const cudaError_t e = launch_k(router, grid, block, 0, stream, a, groups);
     if (e != cudaSuccess) return e;
     if (a.w_type == W_MX)
         return L.x_out == OUT_BF16 ? launch_experts<OUT_BF16, W_MX>(L, stream) : launch_experts<OUT_F16, W_MX>(L, stream);
