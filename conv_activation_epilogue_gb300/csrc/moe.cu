@@ -12,9 +12,9 @@
 // With few tokens every weight is used a handful of times: the time is that of
 // reading the chosen experts' weights once, and everything is arranged so that
 // the copies never stop.  The experts kernel is persistent, one CTA on each SM,
-// with a contiguous share of the items (a tile of weight rows x all of K of one
-// expert; for a gated layer half of the rows are gate rows and half the up rows
-// that go with them):
+// taking the items in turn (a tile of weight rows x all of K of one expert; for a
+// gated layer half of the rows are gate rows and half the up rows that go with
+// them):
 //
 //   warp 0       producer: two TMA boxes (the tile's halves) of 128 bytes of K to a
 //                ring stage.  It runs ahead over items and over the grid barrier:
@@ -180,7 +180,7 @@ __device__ __forceinline__ void fence_proxy_async_all()
 
 // ------------------------------------------------------------------- router --
 // One CTA for an expert and eight tokens: four warps share K.  The CTAs past
-// those prepare what the experts kernel reads, a token each: its counters, x in
+// those prepare what the experts kernel reads: its counters, x in
 // the products' order (MXFP4: as bf16, hi and for fp16 x lo) with zeros up to a
 // whole stage, and the same zeros of h.
 constexpr int MOE_ROUTER_THREADS = 128;
@@ -200,14 +200,15 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
         for (int k = threadIdx.x * 8; k < p.H; k += MOE_ROUTER_THREADS * 8) {
             const uint4 b = __ldg(reinterpret_cast<const uint4 *>(r + k));
             const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+            uint4 a[8];                                        // tokens past the last one: the last one again
+#pragma unroll
+            for (int t = 0; t < 8; ++t) a[t] = __ldg(reinterpret_cast<const uint4 *>(xs + (int64_t)(t0 + min(t, n - 1)) * p.H + k));
             float2 g[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) g[j] = unpack2<XT>(bw[j]);
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
-                if (t >= n) break;
-                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(xs + (int64_t)(t0 + t) * p.H + k));
-                const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+                const uint32_t aw[4] = {a[t].x, a[t].y, a[t].z, a[t].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 f = unpack2<XT>(aw[j]);
@@ -218,7 +219,6 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            if (t >= n) break;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
             if (lane == 0) red[warp][t] = s[t];
@@ -230,25 +230,38 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
                 (p.router_bias != nullptr ? p.router_bias[e] : 0.0f);
         return;
     }
-    const int t = blockIdx.x - p.E * token_groups;
-    if (t == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
-    const uint16_t *x = xs + (int64_t)t * p.H;
-    for (int k = threadIdx.x; k < p.Hp; k += MOE_ROUTER_THREADS) {
-        const int64_t at = (int64_t)t * p.Hp + token_at<W>(k);
-        const uint16_t raw = k < p.H ? x[k] : (uint16_t)0;
-        if constexpr (W != W_MX || XT == OUT_BF16) {
-            p.x_hi[at] = raw;
+    // 1024 K of one token: 8 consecutive values, which stay together, to a thread
+    const int chunks = (p.Hp + 1023) / 1024, at = (int)blockIdx.x - p.E * token_groups, t = at / chunks;
+    const int k = (at - t * chunks) * 1024 + (int)threadIdx.x * 8;
+    if (at == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
+    if (k < p.Hp) {
+        const uint4 raw = k < p.H ? __ldg(reinterpret_cast<const uint4 *>(xs + (int64_t)t * p.H + k)) : make_uint4(0, 0, 0, 0);
+        const int64_t to = (int64_t)t * p.Hp + token_at<W>(k);
+        if constexpr (W != W_MX) {
+            *reinterpret_cast<uint4 *>(p.x_hi + to) = raw;
         } else {
-            const float v = __half2float(__ushort_as_half(raw));
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-            p.x_hi[at] = __bfloat16_as_ushort(hi);
-            p.x_lo[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v - __bfloat162float(hi)));
+            // the pairs (i, i + 4) of the eight values
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+            uint32_t v[4], l[4] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __byte_perm(w[i >> 1], w[2 + (i >> 1)], i & 1 ? 0x7632 : 0x5410);
+            if constexpr (XT == OUT_F16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2<OUT_F16>(v[i]);
+                    split_pair(f.x, f.y, v[i], l[i]);
+                }
+                *reinterpret_cast<uint4 *>(p.x_lo + to) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+            *reinterpret_cast<uint4 *>(p.x_hi + to) = make_uint4(v[0], v[1], v[2], v[3]);
         }
     }
-    const int pad = p.Ip - p.I;
+    if (at != t * chunks) return;
+    const int pad = (p.Ip - p.I) / 8;                          // eights of zeros past h's rows
     for (int i = threadIdx.x; i < pad * p.top; i += MOE_ROUTER_THREADS) {
-        const int64_t at = ((int64_t)t * p.top + i / pad) * p.Ip + token_at<W>(p.I + i % pad);
-        p.h_hi[at] = p.h_lo[at] = 0;
+        const int64_t to = ((int64_t)t * p.top + i / pad) * p.Ip + token_at<W>(p.I + i % pad * 8);
+        *reinterpret_cast<uint4 *>(p.h_hi + to) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(p.h_lo + to) = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -258,7 +271,7 @@ struct MoeShared {
     float probs[MOE_MAX_T * MOE_MAX_K];
     short choice[MOE_MAX_T * MOE_MAX_K];           // slot t * k + j -> expert
     short slot[MOE_MAX_T * MOE_MAX_K];             // slots by expert
-    short count[MOE_MAX_E];
+    short count[MOE_MAX_E], start[MOE_MAX_E];      // slots of an expert, its first entry of slot[]
     short act[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP];       // groups of tokens of one expert, by expert:
     short first[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP + 1];                   // the expert and the first entry of slot[]
     int nact;
@@ -266,63 +279,76 @@ struct MoeShared {
     uint64_t bar[2 * MOE_STAGES + 2 * MOE_MAX_TSTAGES];
 };
 
-// Top k of one token by one warp: each round the largest (key, lowest index) of
-// those left; then the softmax weights.  The token's logits are kept in `row`.
-__device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, float *row, int t, int lane, bool write)
+// Top k of N tokens t, t + stride, ... by one warp: each round the largest key of
+// those left, then the lowest index that has it; then the softmax weights, one to
+// a lane.  A round is a chain of dependent steps: several tokens go through it
+// side by side.
+template <int N>
+__device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, const float *logits, int t, int stride, int lane,
+                                               bool write)
 {
     static_assert(MOE_MAX_E <= 32 * 32, "one bit for each of a lane's logits");
-    __syncwarp();
-    for (int e = lane; e < p.E; e += 32) row[e] = __ldcg(p.logits + (int64_t)t * p.E + e);
-    __syncwarp();
-    uint32_t taken = 0;                                        // bit i: this lane's logit i * 32 + lane is chosen
-    float peak = 0.0f, w = 0.0f, total = 0.0f;
+    uint32_t taken[N] = {};                                    // bit i: this lane's logit i * 32 + lane is chosen
+    int mine[N] = {}, first[N] = {};
     for (int j = 0; j < p.top; ++j) {
-        uint64_t best = 0;
-        for (int e = lane, i = 0; e < p.E; e += 32, ++i) {
-            if ((taken >> i) & 1u) continue;
-            const uint64_t key = ((uint64_t)logit_key(row[e]) << 32) | (0xffffffffu - (uint32_t)e);
-            best = key > best ? key : best;
-        }
-        __syncwarp();
+        uint32_t key[N] = {}, at[N] = {};
+        for (int e = lane, i = 0; e < p.E; e += 32, ++i)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
-            best = other > best ? other : best;
-        }
-        const int e = (int)(0xffffffffu - (uint32_t)best);
-        float v = row[e];
-        if ((e & 31) == lane) taken |= 1u << (e >> 5);
-        if (j == 0) peak = v;
-        v = expf(v - peak);
-        total += v;
-        if (j == lane) w = v;
-        if (lane == 0) {
-            S.choice[t * p.top + j] = (short)e;
-            if (write) p.experts[t * p.top + j] = e;
+            for (int n = 0; n < N; ++n) {
+                const uint32_t k = (taken[n] >> i) & 1u ? 0u : logit_key(logits[(t + n * stride) * p.E + e]);
+                if (k > key[n]) key[n] = k, at[n] = (uint32_t)e;
+            }
+        __syncwarp();
+        uint32_t best[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) best[n] = __reduce_max_sync(0xffffffffu, key[n]);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int e = (int)__reduce_min_sync(0xffffffffu, key[n] == best[n] ? at[n] : 0xffffu);
+            if ((e & 31) == lane) taken[n] |= 1u << (e >> 5);
+            if (j == 0) first[n] = e;
+            if (j == lane) mine[n] = e;
         }
     }
-    if (!p.normalize) {
-        total = 0.0f;
-        for (int e = lane; e < p.E; e += 32) total += expf(row[e] - peak);
-        __syncwarp();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const float *row = logits + (t + n * stride) * p.E;
+        const float peak = row[first[n]];
+        const float w = lane < p.top ? expf(row[mine[n]] - peak) : 0.0f;
+        float total = w;
+        if (!p.normalize) {
+            total = 0.0f;
+            for (int e = lane; e < p.E; e += 32) total += expf(row[e] - peak);
+            __syncwarp();
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
-    if (lane < p.top) {
-        w /= total;
-        S.probs[t * p.top + lane] = w;
-        if (write) p.probs[t * p.top + lane] = w;
+        if (lane < p.top) {
+            const int at = (t + n * stride) * p.top + lane;
+            S.choice[at] = (short)mine[n];
+            S.probs[at] = w / total;
+            if (write) {
+                p.experts[at] = mine[n];
+                p.probs[at] = w / total;
+            }
+        }
     }
 }
 
-// The slots of each expert, in groups, built by every CTA.
+// The slots of each expert, in groups, built by every CTA.  `mask`: for each
+// expert one bit for each slot (in shared memory that is free until the rings
+// start), from which counts and places follow by counting bits.
 template <int GROUP>
-__device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S)
+__device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S, uint32_t *mask)
 {
-    const int tid = threadIdx.x, n_slots = p.T * p.top;
+    const int tid = threadIdx.x, n_slots = p.T * p.top, words = (n_slots + 31) / 32;
+    for (int i = tid; i < p.E * words; i += MOE_THREADS) mask[i] = 0;
+    ptx::cta_sync();
+    for (int s = tid; s < n_slots; s += MOE_THREADS) atomicOr(&mask[S.choice[s] * words + (s >> 5)], 1u << (s & 31));
+    ptx::cta_sync();
     for (int e = tid; e < p.E; e += MOE_THREADS) {
         int c = 0;
-        for (int s = 0; s < n_slots; ++s) c += S.choice[s] == e;
+        for (int w = 0; w < words; ++w) c += __popc(mask[e * words + w]);
         S.count[e] = (short)c;
     }
     ptx::cta_sync();
@@ -336,6 +362,7 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S)
                 const int up = __shfl_up_sync(0xffffffffu, sum, o), gup = __shfl_up_sync(0xffffffffu, gsum, o);
                 if (tid >= o) sum += up, gsum += gup;
             }
+            if (e < p.E) S.start[e] = (short)(at + sum - c);
             for (int g = 0; g < groups; ++g) {
                 S.act[n + gsum - groups + g] = (short)e;
                 S.first[n + gsum - groups + g] = (short)(at + sum - c + g * GROUP);
@@ -349,12 +376,11 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S)
         }
     }
     ptx::cta_sync();
-    for (int a = tid; a < S.nact; a += MOE_THREADS) {
-        const int e = S.act[a];
-        if (a > 0 && S.act[a - 1] == e) continue;              // the first group fills the others' entries too
-        int at = S.first[a];
-        for (int s = 0; s < n_slots; ++s)
-            if (S.choice[s] == e) S.slot[at++] = (short)s;
+    for (int s = tid; s < n_slots; s += MOE_THREADS) {
+        const int e = S.choice[s];
+        int at = S.start[e] + __popc(mask[e * words + (s >> 5)] & ((1u << (s & 31)) - 1u));
+        for (int w = 0; w < s >> 5; ++w) at += __popc(mask[e * words + w]);
+        S.slot[at] = (short)s;
     }
     ptx::cta_sync();
 }
@@ -600,8 +626,7 @@ __device__ __forceinline__ bool mma_phase(const MoeArgs &p, const MoeShared &S, 
                                           MoeUse &use)
 {
     const int n = S.nact * pr.tiles;
-    const int i0 = (int)((int64_t)n * blockIdx.x / gridDim.x), i1 = (int)((int64_t)n * (blockIdx.x + 1) / gridDim.x);
-    for (int i = i0; i < i1; ++i, use.w += (uint32_t)pr.stages, use.t += (uint32_t)pr.tstages) {
+    for (int i = blockIdx.x; i < n; i += gridDim.x, use.w += (uint32_t)pr.stages, use.t += (uint32_t)pr.tstages) {
         const int ai = i / pr.tiles, tile = i - ai * pr.tiles, cnt = S.first[ai + 1] - S.first[ai];
         bool ok;
         if (cnt <= 8) ok = run_item<XT, W, DOWN, 1>(p, S, m, pr, use, ai, tile);
@@ -640,9 +665,8 @@ __device__ __forceinline__ bool produce(const CUtensorMap *map, const MoeArgs &p
                                         const MoeProduct &pr, uint32_t &use, uint64_t pol)
 {
     const int n = S.nact * pr.tiles;
-    const int i0 = (int)((int64_t)n * blockIdx.x / gridDim.x), i1 = (int)((int64_t)n * (blockIdx.x + 1) / gridDim.x);
     const uint32_t box = (uint32_t)p.half_rows * 128u;
-    for (int i = i0; i < i1; ++i) {
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int ai = i / pr.tiles, tile = i - ai * pr.tiles, row = S.act[ai] * pr.rows + tile * pr.step;
         // the upper half of the last tile may have no rows (its products are not stored either)
         const bool both = pr.pairs || tile * pr.step + p.half_rows < pr.limit;
@@ -665,8 +689,7 @@ __device__ __forceinline__ bool produce_tokens(const MoeArgs &p, const MoeShared
     using R = MoeRing<W>;
     constexpr bool LO = DOWN || (W == W_MX && XT == OUT_F16);
     const int lane = threadIdx.x & 31, n = S.nact * pr.tiles;
-    const int i0 = (int)((int64_t)n * blockIdx.x / gridDim.x), i1 = (int)((int64_t)n * (blockIdx.x + 1) / gridDim.x);
-    for (int i = i0; i < i1; ++i) {
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int ai = i / pr.tiles, first = S.first[ai], cnt = S.first[ai + 1] - first;
         const int64_t slot_of = lane < cnt ? S.slot[first + lane] : 0;
         const int64_t from = DOWN ? slot_of * p.Ip : slot_of / p.top * p.Hp;
@@ -695,6 +718,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     using R = MoeRing<W>;
     MoeShared &S = *reinterpret_cast<MoeShared *>(smem + R::BYTES);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    ptx::griddep_launch_dependents();
     const int active = p.half_rows / 8;                        // product warps that have rows
     MoePipe m;
     m.ring = ptx::smem_addr(smem);
@@ -722,13 +746,26 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         S.abort_flag = aligned ? 0 : 1;
         ptx::fence_mbar_init();
     }
-    // the logits stand where the tokens will
-    static_assert(MOE_THREADS / 32 * MOE_MAX_E * 4 <= R::TSTAGES * R::TOKENS, "a row of logits to a warp");
-    float *row = reinterpret_cast<float *>(smem + R::OFF_TOKENS) + warp * MOE_MAX_E;
-    for (int t = warp; t < p.T; t += MOE_THREADS / 32) choose_experts(p, S, row, t, lane, blockIdx.x == 0);
-    ptx::fence_proxy_async_smem();                             // before the copies that overwrite them
+    // All logits where the weights will stand, the lists' masks where the tokens will.
+    static_assert(MOE_MAX_T * MOE_MAX_E * 4 <= R::OFF_TOKENS, "all logits");
+    static_assert(MOE_MAX_E * MOE_MAX_T * MOE_MAX_K / 8 <= R::TSTAGES * R::TOKENS, "a bit for each expert and slot");
+    float *logits = reinterpret_cast<float *>(smem);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < p.T * p.E; i += MOE_THREADS) logits[i] = __ldcg(p.logits + i);
     ptx::cta_sync();
-    build_lists<MOE_GROUP<W>>(p, S);
+    constexpr int WARPS = MOE_THREADS / 32;
+    for (int t = warp; t < p.T; t += 4 * WARPS) {
+        const int left = (p.T - t + WARPS - 1) / WARPS;        // tokens of this warp from t on
+        const bool write = blockIdx.x == 0;
+        if (left == 1) choose_experts<1>(p, S, logits, t, WARPS, lane, write);
+        else if (left == 2) choose_experts<2>(p, S, logits, t, WARPS, lane, write);
+        else if (left == 3) choose_experts<3>(p, S, logits, t, WARPS, lane, write);
+        else choose_experts<4>(p, S, logits, t, WARPS, lane, write);
+    }
+    ptx::cta_sync();
+    build_lists<MOE_GROUP<W>>(p, S, reinterpret_cast<uint32_t *>(smem + R::OFF_TOKENS));
+    ptx::fence_proxy_async_smem();                             // before the copies that overwrite both
+    ptx::cta_sync();
 
     const int hr = p.half_rows, ks = R::K, kt = MOE_TOKEN_K;
     const int step1 = p.gated ? hr : 2 * hr, step2 = 2 * hr;
@@ -831,7 +868,7 @@ cudaError_t launch_moe(const MoeLaunch &L, cudaStream_t stream)
 {
     const MoeArgs &a = L.args;
     const int groups = (a.T + 7) / 8;
-    const dim3 grid((unsigned)(a.E * groups + a.T)), block(MOE_ROUTER_THREADS);
+    const dim3 grid((unsigned)(a.E * groups + a.T * ((a.Hp + 1023) / 1024))), block(MOE_ROUTER_THREADS);
     auto router = a.w_type == W_MX ? (L.x_out == OUT_BF16 ? moe_router_kernel<OUT_BF16, W_MX> : moe_router_kernel<OUT_F16, W_MX>)
                                    : (L.x_out == OUT_BF16 ? moe_router_kernel<OUT_BF16, W_BF16>
                                                           : moe_router_kernel<OUT_F16, W_F16>);
