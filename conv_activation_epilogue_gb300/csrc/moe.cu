@@ -746,6 +746,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         S.abort_flag = aligned ? 0 : 1;
         ptx::fence_mbar_init();
     }
+    ptx::griddep_wait();                                       // the router's logits
     // All logits where the weights will stand, the lists' masks where the tokens will.
     static_assert(MOE_MAX_T * MOE_MAX_E * 4 <= R::OFF_TOKENS, "all logits");
     static_assert(MOE_MAX_E * MOE_MAX_T * MOE_MAX_K / 8 <= R::TSTAGES * R::TOKENS, "a bit for each expert and slot");
@@ -840,11 +841,13 @@ static cudaError_t launch_experts(const MoeLaunch &L, cudaStream_t stream)
     cfg.blockDim = dim3(MOE_THREADS);
     cfg.dynamicSmemBytes = MOE_SMEM<W>;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;               // the CTAs wait for one another
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, moe_experts_kernel<XT, W>, L.tm1, L.tm2, L.args);
 }
 
