@@ -9,13 +9,13 @@
 // scale tiles (its own A rows', all 256 B rows').  The MMA issuer copies the
 // scale tiles into tensor memory (tcgen05.cp) ahead of the stage's MMAs.
 //
-// Tensor memory: the two 256-column accumulators overlap by 64 columns (0..255
-// and 192..447) to leave 64 columns for scales.  The epilogue of a tile drains
-// the shared columns first and then lets the next tile's MMAs start, so they
-// wait for a quarter of an epilogue at most instead of all of it.  Scales of
-// two stages fit (2 x 24 columns): before the issuer copies a stage's scales it
-// waits until the MMAs that read those columns, two stages earlier, are done,
-// while the stage between them keeps the tensor core busy.
+// Tensor memory: the two 256-column accumulators overlap by 128 columns (0..255
+// and 128..383), which leaves 24 columns of scales for each ring stage (a stage's
+// columns are free when the stage is, so the issuer never waits for them; with
+// two slots for five stages it did, 590 cycles a stage where the MMAs take 532).
+// The epilogue of a tile takes the shared columns first, one half of its warps
+// each half of them, and lets the next tile's MMAs start as soon as they are in
+// registers, before it works on them.
 //
 //   warp 0      (both CTAs) TMA producer; copies complete on the even CTA's barriers
 //   warp 1      TMEM allocation; in the even CTA the scale copies and the MMAs
@@ -36,7 +36,7 @@ struct MxPairCfg {
     static constexpr int EPI_WARPS = 8, EPI_BYTES = EPI_WARPS * 4096;
     static constexpr int STAGES = 5;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-    static constexpr uint32_t ACC_STRIDE = 192, SCALE_COL = 448, SLOT_COLS = 24, TMEM_COLS = 512;
+    static constexpr uint32_t ACC_STRIDE = 128, SCALE_COL = 384, SLOT_COLS = 24, TMEM_COLS = 512;
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_EPI = OFF_B + STAGES * B_BYTES;
@@ -45,7 +45,7 @@ struct MxPairCfg {
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-    static_assert(SCALE_COL + 2 * SLOT_COLS <= TMEM_COLS, "tensor memory budget");
+    static_assert(SCALE_COL + STAGES * SLOT_COLS <= TMEM_COLS, "tensor memory budget");
 };
 
 // Pair tile t -> (M block, N block) of 256 x 256, grouped M-first.
@@ -63,14 +63,18 @@ __device__ __forceinline__ void mx_tile(int t, const MxGemmArgs &p, int &mb, int
 // One epilogue unit: this warp's 32 rows x one 128-byte row segment (32 fp32 or
 // 64 16-bit columns): accumulators from TMEM, + bias, activation, conversion,
 // into a 32 x 128 B buffer in the 128-byte swizzled order of a TMA store.
-template <int OUT, int ACT>
+// `loaded` is called when the accumulators are in registers.
+template <int OUT, int ACT, typename Loaded>
 __device__ __forceinline__ void mx_epi_unit(uint32_t taddr, const float *bias, int nvalid, float alpha, uint32_t buf,
-                                            int lane)
+                                            int lane, Loaded loaded)
 {
     constexpr int HALVES = OUT == OUT_F32 ? 1 : 2;           // 32 columns at a time
     uint32_t r[HALVES][32];
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) ptx::tmem_ld32(taddr + 32 * h, r[h]);
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) ptx::tmem_ld_wait(r[h]);
+    loaded();
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
         float b[32];
@@ -85,8 +89,6 @@ __device__ __forceinline__ void mx_epi_unit(uint32_t taddr, const float *bias, i
 #pragma unroll
             for (int j = 0; j < 32; ++j) b[j] = bias != nullptr && 32 * h + j < nvalid ? __ldg(src + j) : 0.0f;
         }
-        __syncwarp();                                         // converged before the warp-collective wait
-        ptx::tmem_ld_wait(r[h]);
         const uint32_t row = buf + (uint32_t)lane * 128u, sw = (uint32_t)(lane & 7);
         constexpr int PER = OUT == OUT_F32 ? 4 : 8;           // values per 16 bytes
 #pragma unroll
@@ -108,18 +110,19 @@ __device__ __forceinline__ void mx_epi_unit(uint32_t taddr, const float *bias, i
     }
 }
 
-template <int OUT>
+template <int OUT, typename Loaded>
 __device__ __forceinline__ void mx_epi_unit(int act, uint32_t taddr, const float *bias, int nvalid, float alpha,
-                                            uint32_t buf, int lane)
+                                            uint32_t buf, int lane,
+                                            Loaded loaded)
 {
     switch (act) {
-    case ACT_RELU: mx_epi_unit<OUT, ACT_RELU>(taddr, bias, nvalid, alpha, buf, lane); break;
-    case ACT_LEAKY: mx_epi_unit<OUT, ACT_LEAKY>(taddr, bias, nvalid, alpha, buf, lane); break;
-    case ACT_TANH: mx_epi_unit<OUT, ACT_TANH>(taddr, bias, nvalid, alpha, buf, lane); break;
-    case ACT_SIGMOID: mx_epi_unit<OUT, ACT_SIGMOID>(taddr, bias, nvalid, alpha, buf, lane); break;
-    case ACT_GELU: mx_epi_unit<OUT, ACT_GELU>(taddr, bias, nvalid, alpha, buf, lane); break;
-    case ACT_SILU: mx_epi_unit<OUT, ACT_SILU>(taddr, bias, nvalid, alpha, buf, lane); break;
-    default: mx_epi_unit<OUT, ACT_NONE>(taddr, bias, nvalid, alpha, buf, lane); break;
+    case ACT_RELU: mx_epi_unit<OUT, ACT_RELU>(taddr, bias, nvalid, alpha, buf, lane, loaded); break;
+    case ACT_LEAKY: mx_epi_unit<OUT, ACT_LEAKY>(taddr, bias, nvalid, alpha, buf, lane, loaded); break;
+    case ACT_TANH: mx_epi_unit<OUT, ACT_TANH>(taddr, bias, nvalid, alpha, buf, lane, loaded); break;
+    case ACT_SIGMOID: mx_epi_unit<OUT, ACT_SIGMOID>(taddr, bias, nvalid, alpha, buf, lane, loaded); break;
+    case ACT_GELU: mx_epi_unit<OUT, ACT_GELU>(taddr, bias, nvalid, alpha, buf, lane, loaded); break;
+    case ACT_SILU: mx_epi_unit<OUT, ACT_SILU>(taddr, bias, nvalid, alpha, buf, lane, loaded); break;
+    default: mx_epi_unit<OUT, ACT_NONE>(taddr, bias, nvalid, alpha, buf, lane, loaded); break;
     }
 }
 
@@ -234,24 +237,19 @@ __global__ void __launch_bounds__(MxPairCfg::THREADS, 1)
     } else if (usable && warp == 1) {
         if (leader) {                                         // the whole warp: see mma_mxf4
             const uint32_t id0 = ptx::idesc_mxf4(256, 256, 0, 0), id2 = ptx::idesc_mxf4(256, 256, 2, 2);
-            uint32_t stage = 0, phase = 0, use = 0, tile = 0;
+            uint32_t stage = 0, phase = 0, tile = 0;
             bool ok = true;
             for (int t = pair; t < p.num_tiles && ok; t += npairs, ++tile) {
-                // the shared columns of the previous tile's accumulator, and all of the one before it
+                // the shared columns of the previous tile's accumulator are read, and all of the one before it
                 if (tile != 0 && !mx_warp_wait(pp, pp.tempty0, (tile - 1) & 1u)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t d = pp.tmem + (tile & 1u) * Cfg::ACC_STRIDE;
-                for (int kb = 0; kb < p.num_kb; ++kb, ++use) {
+                for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
-                    // the MMAs that read this stage's scale columns, two stages ago
-                    if (use >= 2) {
-                        const uint32_t u = use - 2;
-                        if (!mx_warp_wait(pp, pp.empty0 + 8 * (u % STAGES), (u / STAGES) & 1u)) { ok = false; break; }
-                    }
                     ptx::tc_fence_after();
                     const uint32_t a0 = sA + stage * Cfg::A_BYTES, b0 = sB + stage * Cfg::B_BYTES;
                     const uint32_t s0 = sS + stage * Cfg::S_BYTES;
-                    const uint32_t ts = pp.tmem + Cfg::SCALE_COL + (use & 1u) * Cfg::SLOT_COLS;
+                    const uint32_t ts = pp.tmem + Cfg::SCALE_COL + stage * Cfg::SLOT_COLS;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {                 // B: two times eight columns, then A: two times four
                         ptx::tmem_cp_scales_pair(ts + 8 * j, ptx::smem_desc(s0 + 1024u + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
@@ -282,7 +280,7 @@ __global__ void __launch_bounds__(MxPairCfg::THREADS, 1)
         const uint32_t buf = base + Cfg::OFF_EPI + (uint32_t)(warp - 2) * 4096u;
         const uint32_t tempty_leader = ptx::mapa(pp.tempty0, 0);
         const uint64_t pol_c = ptx::createpolicy_evict_first();   // C is not read back here
-        constexpr int NU = 256 / COLS, SHARED = 64 / COLS;        // units of a tile; of its shared columns
+        constexpr int NU = 256 / COLS, SHARED = 128 / COLS;       // units of a tile; of its shared columns
         uint32_t tile = 0;
         for (int t = pair; t < p.num_tiles; t += npairs, ++tile) {
             int mb, nb;
@@ -300,15 +298,16 @@ __global__ void __launch_bounds__(MxPairCfg::THREADS, 1)
                 if (lane == 0) ptx::bulk_wait_read<0>();
                 __syncwarp();
                 mx_epi_unit<OUT>(p.act, tbase + u * COLS, p.bias != nullptr ? p.bias + col0 : nullptr, p.N - col0,
-                                 p.alpha, buf, lane);
-                if (i < 2) {                                      // after the first unit of each warp
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader) ptx::mbar_arrive(pp.tempty0);
-                        else ptx::mbar_arrive_cluster(tempty_leader);
-                    }
-                }
+                                 p.alpha, buf, lane, [&] {
+                                     // this warp's last unit of the shared columns
+                                     if (i < SHARED - 2 || i >= SHARED) return;
+                                     ptx::tc_fence_before();
+                                     __syncwarp();
+                                     if (lane == 0) {
+                                         if (leader) ptx::mbar_arrive(pp.tempty0);
+                                         else ptx::mbar_arrive_cluster(tempty_leader);
+                                     }
+                                 });
                 if (p.c_tma) {
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
