@@ -32,7 +32,7 @@ __device__ __forceinline__ void load8(const void *x, int64_t i, int n, Raw8<T> &
 #pragma unroll
         for (int j = 0; j < Raw8<T>::WORDS / 4; ++j) {
             const char *p = static_cast<const char *>(x) + i * (T == IN_F32 ? 4 : 2) + 16 * j;
-            const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
             r.w[4 * j] = u.x, r.w[4 * j + 1] = u.y, r.w[4 * j + 2] = u.z, r.w[4 * j + 3] = u.w;
         }
     } else {
@@ -84,54 +84,50 @@ __device__ __forceinline__ uint32_t raw_encode(const uint32_t (&w)[Raw8<T>::WORD
     return mx_encode8(v);
 }
 
-// x [rows, K] row-major.  Sixteen lanes take one row's 128 values (one scale
-// word): each lane 8 values, four lanes a block, whose largest |x| they find by
-// two shuffles.  A block of 256 threads covers `tpr` tiles (a power of two, at
-// most 16) of 16 / tpr rows, U times (U sets of loads in flight); rows past the
-// last one, up to a multiple of 128, only get their zero scales.
-template <int T, bool VEC, int U>
+// x [rows, K] row-major.  A lane takes one block of 32 values: its loads (64 or
+// 128 consecutive bytes) are all in flight before the first is used, the largest
+// |x| needs no other lane, and 32 lanes write 512 consecutive bytes of codes.
+// 2^lanes_log2 consecutive lanes take the blocks of a row; rows past the last
+// one, up to a multiple of 128, only get their zero scales.
+template <int T, bool VEC>
 __global__ void __launch_bounds__(256) quantize_kernel(const void *__restrict__ x, uint8_t *__restrict__ codes,
                                                        uint8_t *__restrict__ scales, int64_t rows, int64_t K,
-                                                       int tpr_log2, int segs)
+                                                       int lanes_log2, int segs)
 {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int unit = threadIdx.x >> 4, l = threadIdx.x & 15;
+    const int64_t tiles = mx_tiles(K), kb = mx_blocks(K), padded = (rows + 127) & ~(int64_t)127;
     const int64_t rb = blockIdx.x / segs;
     const int seg = (int)(blockIdx.x - rb * segs);
-    const int64_t tiles = mx_tiles(K), kb = mx_blocks(K), padded = (rows + 127) & ~(int64_t)127;
-    const int per = 16 >> tpr_log2;                            // rows of one set
-    const int64_t row0 = rb * (per * U) + (unit >> tpr_log2);
-    const int64_t tile = ((int64_t)seg << tpr_log2) + (unit & ((1 << tpr_log2) - 1));
-    const int64_t k0 = tile * 128 + l * 8;
-    Raw8<T> r[U];
+    const int64_t row = (rb << (8 - lanes_log2)) + (threadIdx.x >> lanes_log2);
+    const int64_t blk = ((int64_t)seg << lanes_log2) + (threadIdx.x & ((1 << lanes_log2) - 1)), k0 = blk * 32;
+    Raw8<T> r[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int j = 0; j < Raw8<T>::WORDS; ++j) r[u].w[j] = 0;
-        const int64_t row = row0 + u * per;
-        if (row < rows && k0 < K) load8<T, VEC>(x, row * K + k0, (int)min((int64_t)8, K - k0), r[u]);
+        for (int j = 0; j < Raw8<T>::WORDS; ++j) r[q].w[j] = 0;
+    if (row < rows && blk < kb) {
+        const int n = (int)min((int64_t)32, K - k0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load8<T, VEC>(x, row * K + k0 + 8 * q, n - 8 * q, r[q]);
     }
+    uint32_t amax = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t row = row0 + u * per;
-        uint32_t amax = 0;
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int j = 0; j < Raw8<T>::WORDS; ++j) amax = raw_max<T>(amax, r[u].w[j]);
-        if constexpr (T != IN_F32) amax = max(amax & 0xffffu, amax >> 16);
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        if constexpr (T != IN_F32) amax = bits_of<T>(amax);
-        const uint32_t b = mx_scale_byte(amax);
-        const uint32_t c = b == 255u ? 0u : raw_encode<T>(r[u].w, mx_inv_scale(b));
-        if (row < rows && k0 < kb * 32)
-            *reinterpret_cast<uint32_t *>(codes + row * (kb * 16) + tile * 64 + l * 4) = c;
-        uint32_t word = b << (8 * (l >> 2));
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if (l == 0 && tile < tiles && row < padded)
-            *reinterpret_cast<uint32_t *>(scales + mx_scale_at(row, tile * 4, tiles)) = word;
-    }
+        for (int j = 0; j < Raw8<T>::WORDS; ++j) amax = raw_max<T>(amax, r[q].w[j]);
+    if constexpr (T != IN_F32) amax = bits_of<T>(max(amax & 0xffffu, amax >> 16));
+    const uint32_t b = mx_scale_byte(amax);
+    const float inv = mx_inv_scale(b == 255u ? 0u : b);
+    uint32_t c[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[q] = b == 255u ? 0u : raw_encode<T>(r[q].w, inv);
+    if (row < rows && blk < kb) *reinterpret_cast<uint4 *>(codes + (row * kb + blk) * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+    uint32_t word = b << (8 * (threadIdx.x & 3));              // blocks that do not exist hold zeros: byte 0
+    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+    if ((threadIdx.x & 3) == 0 && (blk >> 2) < tiles && row < padded)
+        *reinterpret_cast<uint32_t *>(scales + mx_scale_at(row, blk, tiles)) = word;
 }
 
 // x [K, rows] row-major, blocks along K (the right operand of a row-major
@@ -229,7 +225,9 @@ __global__ void __launch_bounds__(256) quantize_trans_kernel(const void *__restr
     }
 }
 
-// codes and scales -> y [rows, K]; the same lanes as quantize_kernel.
+// codes and scales -> y [rows, K].  Sixteen lanes take one row's 128 values, 8 to a
+// lane; a block of 256 threads covers `tpr` tiles (a power of two, at most 16) of
+// 16 / tpr rows, U times (U sets of loads in flight).
 template <int T, bool VEC, int U>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restrict__ codes,
                                                          const uint8_t *__restrict__ scales, void *__restrict__ y,
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restri
     }
 }
 
-// The row kernels' grid: a CTA takes as many of a row's tiles as it has, up to
+// The grid of dequantize_kernel: a CTA takes as many of a row's tiles as it has, up to
 // 16, and U sets of rows; U = 4 once that still leaves four CTAs for each of the
 // 152 SMs, so that small calls spread over more SMs and large ones keep more
 // loads in flight.
@@ -320,12 +318,15 @@ static cudaError_t quantize_t(const void *x, uint8_t *codes, uint8_t *scales, in
         auto k = rows % 2 == 0 ? quantize_trans_kernel<T, true> : quantize_trans_kernel<T, false>;
         return launch_k(k, dim3((unsigned)grid), dim3(256), 0, s, x, codes, scales, rows, K, (int)col_tiles);
     }
-    const RowGrid g = row_grid(padded, K);
-    if (g.grid > INT32_MAX) return cudaErrorInvalidValue;
-    const bool vec = K * e % 16 == 0;
-    auto k = g.u == 4 ? (vec ? quantize_kernel<T, true, 4> : quantize_kernel<T, false, 4>)
-                      : (vec ? quantize_kernel<T, true, 1> : quantize_kernel<T, false, 1>);
-    return launch_k(k, dim3((unsigned)g.grid), dim3(256), 0, s, x, codes, scales, rows, K, g.tpr_log2, g.segs);
+    // a CTA: the blocks of a row (whole tiles) on a power of two of its 256 lanes
+    const int64_t blocks = mx_tiles(K) * 4;
+    int lanes_log2 = 2;
+    while (lanes_log2 < 8 && (1 << lanes_log2) < blocks) ++lanes_log2;
+    const int64_t segs = (blocks + (1 << lanes_log2) - 1) >> lanes_log2, per = 256 >> lanes_log2;
+    const int64_t grid = (padded + per - 1) / per * segs;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    auto k = K * e % 16 == 0 ? quantize_kernel<T, true> : quantize_kernel<T, false>;
+    return launch_k(k, dim3((unsigned)grid), dim3(256), 0, s, x, codes, scales, rows, K, lanes_log2, (int)segs);
 }
 
 template <int T>
