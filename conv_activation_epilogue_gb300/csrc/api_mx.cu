@@ -43,18 +43,18 @@ struct MxContext {
 mmact_status mx_context(MxContext *out)
 {
     static std::mutex mutex;
-    static bool ready[MAX_DEVICES];
+    static std::atomic<bool> ready[MAX_DEVICES];
     static int pairs[MAX_DEVICES];
     const mmact_status s = device_context(&out->dev);
     if (s != MMACT_OK) return s;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(mutex);
-    if (!ready[dev]) {
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(mutex);               // setting up twice is harmless
         if (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels() != cudaSuccess ||
             setup_moe_kernels() != cudaSuccess)
             return MMACT_ERR_CUDA;
-        ready[dev] = true;
+        ready[dev].store(true, std::memory_order_release);
     }
     out->max_pairs = pairs[dev];
     return MMACT_OK;
@@ -98,7 +98,7 @@ bool mx_encode(CUtensorMap *mc, CUtensorMap *ms, const void *codes, const void *
 
 // Plan of one product: either kernel's launch.
 struct MxPlan {
-    bool pair;
+    bool pair, quantize;             // quantize: x first, by a kernel of its own
     MxGemmLaunch P;
     MxRowsLaunch R;
 };
@@ -112,15 +112,22 @@ bool mx_choose_pair(const MxContext &c, int64_t M, int64_t N)
     return M > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= c.max_pairs / 2;
 }
 
+// Rows of x up to which the rows kernel quantises them itself (gemm_mxfp4_rows.cu
+// has both sides' times).
+constexpr int64_t MX_FUSED_ROWS = 8;
+
+// `x` (or null): A [M, K] in x_type, to be quantised into ac, as by mx_gemm_launch,
+// or by the rows kernel on the way.
 mmact_status mx_gemm_plan(MxPlan &plan, const void *ac, const void *as, const void *bc, const void *bs,
                           const float *bias, void *C, int64_t M, int64_t N, int64_t K, mmact_dtype cd, mmact_act act,
-                          float alpha)
+                          float alpha, const void *x = nullptr, mmact_dtype x_type = MMACT_F32)
 {
     MxContext c;
     const mmact_status st = mx_context(&c);
     if (st != MMACT_OK) return st;
     const int nk64 = (int)((mx_blocks(K) + 1) / 2), num_kb = (int)((K + 255) / 256);
     plan.pair = mx_choose_pair(c, M, N);
+    plan.quantize = x != nullptr && plan.pair;
     if (plan.pair) {
         MxGemmLaunch &L = plan.P;
         std::memset(&L, 0, sizeof(L));
@@ -157,6 +164,7 @@ mmact_status mx_gemm_plan(MxPlan &plan, const void *ac, const void *as, const vo
     MxRowsArgs &a = L.args;
     a.M = (int)M;
     a.N = (int)N;
+    a.K = (int)K;
     a.nk64 = nk64;
     a.num_kb = num_kb;
     a.tiles_n = (int)((N + 127) / 128);
@@ -180,9 +188,15 @@ mmact_status mx_gemm_plan(MxPlan &plan, const void *ac, const void *as, const vo
     L.out = out_kind(cd);
     L.bt = bt;
     L.grid = (int)(tiles * split);
-    if (!mx_encode(&L.tmW, &L.tmSW, bc, bs, N, K, 128, 1) || !mx_encode(&L.tmT, &L.tmST, ac, as, M, K, (uint32_t)bt, 1))
-        return MMACT_ERR_CUDA;
-    return MMACT_OK;
+    L.x_type = -1;
+    plan.quantize = x != nullptr && M > MX_FUSED_ROWS;
+    if (!mx_encode(&L.tmW, &L.tmSW, bc, bs, N, K, 128, 1)) return MMACT_ERR_CUDA;
+    if (x != nullptr && !plan.quantize) {
+        a.x = x;
+        L.x_type = out_kind(x_type);
+        return MMACT_OK;
+    }
+    return mx_encode(&L.tmT, &L.tmST, ac, as, M, K, (uint32_t)bt, 1) ? MMACT_OK : MMACT_ERR_CUDA;
 }
 
 cudaError_t mx_gemm_launch(const MxPlan &plan, cudaStream_t stream)
@@ -327,9 +341,10 @@ MMACT_EXPORT mmact_status mmact_linear_mxfp4(const void *x, const void *w_codes,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
     MxPlan L;
-    if ((s = mx_gemm_plan(L, codes, scales, w_codes, w_scales, bias, C, M, N, K, c_dtype, act, alpha)) != MMACT_OK)
+    if ((s = mx_gemm_plan(L, codes, scales, w_codes, w_scales, bias, C, M, N, K, c_dtype, act, alpha, x, x_dtype)) !=
+        MMACT_OK)
         return s;
-    if ((s = enqueued(quantize_launch(x, codes, scales, M, K, x_dtype, 0, st))) != MMACT_OK) return s;
+    if (L.quantize && (s = enqueued(quantize_launch(x, codes, scales, M, K, x_dtype, 0, st))) != MMACT_OK) return s;
     return enqueued(mx_gemm_launch(L, st));
 }
 

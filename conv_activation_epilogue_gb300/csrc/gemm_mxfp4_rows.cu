@@ -17,10 +17,14 @@
 //
 //   warp 0      TMA producer: a ring of stages of 256 K (codes with the 128-byte
 //               swizzle, scale tiles).  While the kernel before this one in the
-//               stream still runs (it may be writing A's codes) the producer
-//               already brings the CTA's first weight boxes to L2.
+//               stream still runs (it may be writing A's codes) the CTA already
+//               asks for its first 16 weight boxes in L2.
 //   warp 1      TMEM allocation, scale copies into columns of the ring stage, MMAs
 //   warps 2..5  partial tile, reduction, epilogue
+//   warps 6..9  when A arrives as x in 16 or 32 bits, up to 8 rows: they quantise
+//               its stages into the ring, where the codes would have been copied,
+//               which saves a kernel of its own (1 row, 8192 x 8192 weights: 8.9
+//               against 10.9 us with one; 8 rows 10.1 and 11.3, 16 rows 14.5 and 11.3)
 #include <type_traits>
 
 #include "common.cuh"
@@ -33,9 +37,11 @@ template <int BT>
 struct MxRowsCfg {
     static constexpr int W_BYTES = 128 * 128, T_BYTES = BT * 128, S_BYTES = 2 * 1024;
     static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + S_BYTES;
-    static constexpr int STAGES = BT <= 64 ? 8 : 6;
+    // up to 32 rows: two CTAs fit on an SM, so that the next product's set-up and first copies to L2
+    // overlap this one's work; else as many as fit
+    static constexpr int STAGES = BT <= 32 ? 5 : (BT == 64 ? 8 : 6);
     static constexpr uint32_t SCALE_COL = BT;                            // 16 columns for each stage
-    static constexpr uint32_t TMEM_COLS = BT + 16 * STAGES <= 256 ? 256 : 512;
+    static constexpr uint32_t TMEM_COLS = BT + 16 * STAGES <= 128 ? 128 : 256;
     static constexpr int OFF_W = 0;
     static constexpr int OFF_T = OFF_W + STAGES * W_BYTES;
     static constexpr int OFF_S = OFF_T + STAGES * T_BYTES;
@@ -84,8 +90,76 @@ __device__ __forceinline__ void cluster_columns(uint32_t at, int split, float (&
     }
 }
 
-template <int OUT, int BT>
-__global__ void __launch_bounds__(192, 1)
+// The rows of x as codes and scales in every stage of the ring (what stands in
+// place of rows that do not exist only reaches columns that are not stored).  A
+// stage to a warp, so that four stages' loads are in flight; a block of 32 values
+// to a lane, two at a time.
+template <int XT, int BT>
+__device__ __forceinline__ void quantize_stages(const MxRowsArgs &p, const Pipe &pp, uint32_t sT, uint32_t sS, int kb0, int kb1)
+{
+    using Cfg = MxRowsCfg<BT>;
+    const int w = (int)(threadIdx.x >> 5) - 6, lane = threadIdx.x & 31, blk = lane & 7;
+    const bool vec = (int64_t)p.K * (XT == IN_F32 ? 4 : 2) % 16 == 0;
+    for (int kb = kb0 + w, i = w; kb < kb1; kb += 4, i += 4) {
+        const uint32_t stage = (uint32_t)i % Cfg::STAGES, phase = ((uint32_t)i / Cfg::STAGES) & 1u;
+        const int k0 = kb * 256 + blk * 32, n = min(32, p.K - k0);
+#pragma unroll 1
+        for (int r0 = 0; r0 < p.M; r0 += 8) {
+            Raw8<XT> r[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int row = r0 + 4 * u + (lane >> 3);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                    for (int j = 0; j < Raw8<XT>::WORDS; ++j) r[u][q].w[j] = 0;
+                    if (row < p.M && n > 8 * q) {
+                        const int64_t at = (int64_t)row * p.K + k0 + 8 * q;
+                        if (vec) load8<XT, true>(p.x, at, n - 8 * q, r[u][q]);
+                        else load8<XT, false>(p.x, at, n - 8 * q, r[u][q]);
+                    }
+                }
+            }
+            // the warp's last stage before this one was four earlier, so the slot's last reader is known to be the one before
+            if (r0 == 0 && !mx_warp_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) {
+                if (lane == 0) pipe_fail(pp);
+                return;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t row = (uint32_t)(r0 + 4 * u + (lane >> 3));
+                if (row >= (uint32_t)p.M) continue;
+                uint32_t amax = 0, c[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < Raw8<XT>::WORDS; ++j) amax = raw_max<XT>(amax, r[u][q].w[j]);
+                if constexpr (XT != IN_F32) amax = bits_of<XT>(max(amax & 0xffffu, amax >> 16));
+                const uint32_t b = mx_scale_byte(amax);
+                const float inv = mx_inv_scale(b == 255u ? 0u : b);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) c[q] = b == 255u ? 0u : raw_encode<XT>(r[u][q].w, inv);
+                ptx::st_shared_v4(sT + stage * Cfg::T_BYTES + row * 128u + (((uint32_t)blk ^ (row & 7u)) << 4), c[0], c[1], c[2],
+                                  c[3]);
+                // at most 32 rows: the first of a scale tile's four groups
+                const uint32_t at = sS + stage * Cfg::S_BYTES + 1024u + (uint32_t)(blk >> 2) * 512u + row * 16u + (uint32_t)(blk & 3);
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(b) : "memory");
+            }
+            __syncwarp();
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(pp.full0 + 8 * stage);
+    }
+}
+
+constexpr int XT_NONE = -1;          // A comes as codes and scales
+
+template <int XT>
+constexpr int ROWS_THREADS = XT == XT_NONE ? 192 : 320;
+
+template <int OUT, int BT, int XT>
+__global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
     gemm_mxfp4_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
                            const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmST,
                            const MxRowsArgs p)
@@ -116,16 +190,16 @@ __global__ void __launch_bounds__(192, 1)
     if (aligned) {
         if (threadIdx.x == 0) {
             ptx::prefetch_tensormap(&tmW);
-            ptx::prefetch_tensormap(&tmT);
+            if constexpr (XT == XT_NONE) ptx::prefetch_tensormap(&tmT);
             for (int s = 0; s < STAGES; ++s) {
-                ptx::mbar_init(pp.full0 + 8 * s, 1);
+                ptx::mbar_init(pp.full0 + 8 * s, XT == XT_NONE ? 1 : 2);   // + a quantising warp
                 ptx::mbar_init(pp.empty0 + 8 * s, 1);
             }
             ptx::mbar_init(pp.tfull0, 1);
             ptx::mbar_init(pp.drain, 1);
             misc[1] = 0;
             ptx::fence_mbar_init();
-            for (int kb = kb0; kb < min(kb1, kb0 + STAGES); ++kb) {
+            for (int kb = kb0; kb < min(kb1, kb0 + 16); ++kb) {
                 ptx::tma_prefetch_2d(&tmW, kb * 64, nb * 128);
                 ptx::tma_prefetch_2d(&tmSW, kb * 256, nb);
             }
@@ -150,11 +224,13 @@ __global__ void __launch_bounds__(192, 1)
                 const uint32_t stage = (uint32_t)issued % STAGES, phase = ((uint32_t)issued / STAGES) & 1u;
                 if (!pipe_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) { ok = false; break; }
                 const uint32_t fb = pp.full0 + 8 * stage;
-                ptx::mbar_arrive_expect_tx(fb, (uint32_t)Cfg::STAGE_BYTES);
+                ptx::mbar_arrive_expect_tx(fb, (uint32_t)(XT == XT_NONE ? Cfg::STAGE_BYTES : Cfg::W_BYTES + 1024));
                 ptx::tma_load_2d(sW + stage * Cfg::W_BYTES, &tmW, fb, kb * 64, nb * 128);
                 ptx::tma_load_2d(sS + stage * Cfg::S_BYTES, &tmSW, fb, kb * 256, nb);
-                ptx::tma_load_2d(sT + stage * Cfg::T_BYTES, &tmT, fb, kb * 64, tb * BT);
-                ptx::tma_load_2d(sS + stage * Cfg::S_BYTES + 1024u, &tmST, fb, kb * 256, tb);
+                if constexpr (XT == XT_NONE) {
+                    ptx::tma_load_2d(sT + stage * Cfg::T_BYTES, &tmT, fb, kb * 64, tb * BT);
+                    ptx::tma_load_2d(sS + stage * Cfg::S_BYTES + 1024u, &tmST, fb, kb * 256, tb);
+                }
             }
             if (!ok) pipe_fail(pp);
             // every copy has landed before the ring's memory is used again or the CTA exits
@@ -192,11 +268,14 @@ __global__ void __launch_bounds__(192, 1)
             ptx::mbar_wait_bounded(pp.drain, 0, DRAIN_NS, nullptr);
         }
     }
+    if constexpr (XT != XT_NONE) {
+        if (aligned && warp >= 6) quantize_stages<XT, BT>(p, pp, sT, sS, kb0, kb1);
+    }
     __syncwarp();
     // The epilogue warps take part in cluster barriers with the others below, so
     // the partial tile is read out in one place for every warp's control flow.
     const int q = warp & 3, n = nb * 128 + q * 32 + lane;
-    const bool epi = warp >= 2;
+    const bool epi = warp >= 2 && warp < 6;
     const float bias = epi && p.bias != nullptr && n < p.N ? p.bias[n] : 0.0f;
     bool good = aligned;
     if (epi && aligned) {
@@ -262,12 +341,12 @@ __global__ void __launch_bounds__(192, 1)
     }
 }
 
-template <int OUT, int BT>
+template <int OUT, int BT, int XT>
 static cudaError_t launch_rows_t(const MxRowsLaunch &L, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)L.grid);
-    cfg.blockDim = dim3(192);
+    cfg.blockDim = dim3(ROWS_THREADS<XT>);
     cfg.dynamicSmemBytes = MxRowsCfg<BT>::SMEM_BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -279,28 +358,53 @@ static cudaError_t launch_rows_t(const MxRowsLaunch &L, cudaStream_t stream)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.args.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_rows_kernel<OUT, BT>, L.tmW, L.tmT, L.tmSW, L.tmST, L.args);
+    return cudaLaunchKernelEx(&cfg, gemm_mxfp4_rows_kernel<OUT, BT, XT>, L.tmW, L.tmT, L.tmSW, L.tmST, L.args);
+}
+
+template <int OUT, int BT>
+static cudaError_t launch_rows_x(const MxRowsLaunch &L, cudaStream_t stream)
+{
+    if (L.x_type == IN_BF16) return launch_rows_t<OUT, BT, IN_BF16>(L, stream);
+    if (L.x_type == IN_F16) return launch_rows_t<OUT, BT, IN_F16>(L, stream);
+    if (L.x_type == IN_F32) return launch_rows_t<OUT, BT, IN_F32>(L, stream);
+    return launch_rows_t<OUT, BT, XT_NONE>(L, stream);
 }
 
 template <int OUT>
 static cudaError_t launch_rows_o(const MxRowsLaunch &L, cudaStream_t stream)
 {
     switch (L.bt) {
-    case 16: return launch_rows_t<OUT, 16>(L, stream);
-    case 32: return launch_rows_t<OUT, 32>(L, stream);
-    case 64: return launch_rows_t<OUT, 64>(L, stream);
-    default: return launch_rows_t<OUT, 128>(L, stream);
+    case 16: return launch_rows_x<OUT, 16>(L, stream);
+    case 32: return launch_rows_t<OUT, 32, XT_NONE>(L, stream);
+    case 64: return launch_rows_t<OUT, 64, XT_NONE>(L, stream);
+    default: return launch_rows_t<OUT, 128, XT_NONE>(L, stream);
     }
+}
+
+template <int OUT, int BT, int XT>
+static cudaError_t setup_rows_t()
+{
+    return cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, BT, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                MxRowsCfg<BT>::SMEM_BYTES);
+}
+
+template <int OUT, int BT>
+static cudaError_t setup_rows_x()
+{
+    cudaError_t e = setup_rows_t<OUT, BT, XT_NONE>();
+    if (e == cudaSuccess) e = setup_rows_t<OUT, BT, IN_BF16>();
+    if (e == cudaSuccess) e = setup_rows_t<OUT, BT, IN_F16>();
+    if (e == cudaSuccess) e = setup_rows_t<OUT, BT, IN_F32>();
+    return e;
 }
 
 template <int OUT>
 static cudaError_t setup_rows_o()
 {
-    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, 16>, attr, MxRowsCfg<16>::SMEM_BYTES);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, 32>, attr, MxRowsCfg<32>::SMEM_BYTES);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, 64>, attr, MxRowsCfg<64>::SMEM_BYTES);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, 128>, attr, MxRowsCfg<128>::SMEM_BYTES);
+    cudaError_t e = setup_rows_x<OUT, 16>();
+    if (e == cudaSuccess) e = setup_rows_t<OUT, 32, XT_NONE>();
+    if (e == cudaSuccess) e = setup_rows_t<OUT, 64, XT_NONE>();
+    if (e == cudaSuccess) e = setup_rows_t<OUT, 128, XT_NONE>();
     return e;
 }
 

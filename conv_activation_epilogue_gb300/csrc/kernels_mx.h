@@ -43,7 +43,8 @@ cudaError_t launch_gemm_mxfp4_pair(const MxGemmLaunch &L, cudaStream_t stream);
 // The same product with few rows or tiles: W = B's rows on the MMA's 128 lanes,
 // T = A's rows on its columns, the K blocks of a tile shared by a cluster.
 struct MxRowsArgs {
-    int M, N;
+    int M, N, K;
+    const void *x;       // A not yet quantised [M, K], or null
     int nk64, num_kb;    // as above
     int tiles_n;         // tiles of 128 rows of B
     int split, kb_per;   // CTAs of a tile's cluster, K blocks of each
@@ -60,6 +61,7 @@ struct MxRowsLaunch {
     MxRowsArgs args;
     int out;
     int bt;              // rows of A in a tile: 16, 32, 64 or 128
+    int x_type;          // OUT_* of args.x; < 0: A is tmT, tmST
     int grid;
 };
 

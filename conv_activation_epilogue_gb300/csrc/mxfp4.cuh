@@ -93,6 +93,76 @@ __device__ __forceinline__ void mx_decode8(uint32_t c, float (&v)[8])
     }
 }
 
+// ------------------------------------------------------------- quantisation --
+enum : int { IN_F32 = OUT_F32, IN_F16 = OUT_F16, IN_BF16 = OUT_BF16 };
+
+// Eight consecutive values x[i..i+8) as raw 32-bit words, two 16-bit values or
+// one fp32 to a word (values at or past `n` are 0).
+template <int T>
+struct Raw8 {
+    static constexpr int WORDS = T == IN_F32 ? 8 : 4;
+    uint32_t w[WORDS];
+};
+
+template <int T, bool VEC>
+__device__ __forceinline__ void load8(const void *x, int64_t i, int n, Raw8<T> &r)
+{
+    if (VEC && n >= 8) {
+#pragma unroll
+        for (int j = 0; j < Raw8<T>::WORDS / 4; ++j) {
+            const char *p = static_cast<const char *>(x) + i * (T == IN_F32 ? 4 : 2) + 16 * j;
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+            r.w[4 * j] = u.x, r.w[4 * j + 1] = u.y, r.w[4 * j + 2] = u.z, r.w[4 * j + 3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (T == IN_F32) {
+                r.w[j] = j < n ? static_cast<const uint32_t *>(x)[i + j] : 0u;
+            } else {
+                const uint32_t v = j < n ? static_cast<const uint16_t *>(x)[i + j] : 0u;
+                r.w[j / 2] = j % 2 == 0 ? v : r.w[j / 2] | (v << 16);
+            }
+        }
+    }
+}
+
+// The largest |value| of raw words so far: of 16-bit types in each half of `m`
+// (their magnitudes order as unsigned integers, infinities and NaN on top).
+template <int T>
+__device__ __forceinline__ uint32_t raw_max(uint32_t m, uint32_t w)
+{
+    if constexpr (T == IN_F32) return max(m, w & 0x7fffffffu);
+    else return __vmaxu2(m, w & 0x7fff7fffu);
+}
+
+// The fp32 bits of a 16-bit magnitude.
+template <int T>
+__device__ __forceinline__ uint32_t bits_of(uint32_t h)
+{
+    if constexpr (T == IN_BF16) return h << 16;
+    else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
+}
+
+// Codes of eight values held as raw words, times `inv`.
+template <int T>
+__device__ __forceinline__ uint32_t raw_encode(const uint32_t (&w)[Raw8<T>::WORDS], float inv)
+{
+    float v[8];
+    if constexpr (T == IN_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]) * inv;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack2<T>(w[j]);
+            v[2 * j] = f.x * inv;
+            v[2 * j + 1] = f.y * inv;
+        }
+    }
+    return mx_encode8(v);
+}
+
 // -------------------------------------------------------------- activations --
 enum : int { ACT_SILU = ACT_GELU + 1 };
 

@@ -448,52 +448,60 @@ def mmact_mxfp4_size(rows: int, K: int) -> tuple[int, int]:
 
 
 def _mxfp4_ptrs(codes, scales, rows: int, K: int, name: str):
-    pc, ps = _dev(codes, name + " codes", _BYTES), _dev(scales, name + " scales", _BYTES)
-    # the sizes of mmact_mxfp4_size
+    # the sizes of mmact_mxfp4_size; _dev says what else is wrong
+    if not (codes.dtype is torch.uint8 and scales.dtype is torch.uint8 and codes.is_cuda and scales.is_cuda
+            and codes.is_contiguous() and scales.is_contiguous()):
+        _dev(codes, name + " codes", _BYTES)
+        _dev(scales, name + " scales", _BYTES)
     if codes.numel() != rows * ((K + 31) // 32 * 16):
         raise ValueError(f"{name} codes must hold {rows} x {(K + 31) // 32 * 16} bytes")
     if scales.numel() != (rows + 127) // 128 * ((K + 127) // 128) * 512:
         raise ValueError(f"{name} scales must hold {(rows + 127) // 128} x {(K + 127) // 128} tiles of 512 bytes")
-    return pc, ps
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def _matrix(t, name: str):
+    """(pointer, dtype code, rows, columns) of a contiguous 2-D CUDA tensor of floats."""
+    code = DTYPE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name, _IN)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    return t.data_ptr(), code, rows, cols
 
 
 def mmact_quantize_mxfp4(x, codes, scales, transposed: bool = False, stream=None) -> None:
     """Quantise x [rows, K] (or, transposed, [K, rows]) to MXFP4 with blocks along K; codes and
     scales are uint8 tensors of mmact_mxfp4_size(rows, K) bytes."""
-    L = load()
-    px = _dev(x, "x", _IN)
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D")
-    rows, K = (x.shape[1], x.shape[0]) if transposed else x.shape
+    px, dt, rows, K = _matrix(x, "x")
+    if transposed:
+        rows, K = K, rows
     pc, ps = _mxfp4_ptrs(codes, scales, rows, K, "x")
-    _check(L.mmact_quantize_mxfp4(px, pc, ps, rows, K, DTYPE[x.dtype], 1 if transposed else 0,
-                                  _stream_handle(stream)), "mmact_quantize_mxfp4")
+    s = (_lib or load()).mmact_quantize_mxfp4(px, pc, ps, rows, K, dt, 1 if transposed else 0, _stream_handle(stream))
+    if s:
+        _check(s, "mmact_quantize_mxfp4")
 
 
 def mmact_dequantize_mxfp4(codes, scales, y, stream=None) -> None:
     """y [rows, K] = the values of an MXFP4 matrix."""
-    L = load()
-    py = _dev(y, "y", _OUT)
-    if y.dim() != 2:
-        raise ValueError("y must be 2-D")
-    rows, K = y.shape
+    py, dt, rows, K = _matrix(y, "y")
     pc, ps = _mxfp4_ptrs(codes, scales, rows, K, "y")
-    _check(L.mmact_dequantize_mxfp4(pc, ps, py, rows, K, DTYPE[y.dtype], _stream_handle(stream)),
-           "mmact_dequantize_mxfp4")
+    s = (_lib or load()).mmact_dequantize_mxfp4(pc, ps, py, rows, K, dt, _stream_handle(stream))
+    if s:
+        _check(s, "mmact_dequantize_mxfp4")
 
 
 def mmact_gemm_mxfp4(a_codes, a_scales, b_codes, b_scales, bias, C, K: int, act: str = "none",
                      alpha: float = 0.0, stream=None) -> None:
     """C = act(A @ B.T + bias) of MXFP4 matrices A [M, K] and B [N, K]; C [M, N]."""
-    L = load()
-    pc = _dev(C, "C", _OUT)
-    if C.dim() != 2:
-        raise ValueError("C must be 2-D")
-    M, N = C.shape
+    pc, dt, M, N = _matrix(C, "C")
     pa, psa = _mxfp4_ptrs(a_codes, a_scales, M, K, "A")
     pb, psb = _mxfp4_ptrs(b_codes, b_scales, N, K, "B")
-    _check(L.mmact_gemm_mxfp4(pa, psa, pb, psb, _bias_ptr(bias, N), pc, M, N, K, DTYPE[C.dtype], ACT[act],
-                              float(alpha), _stream_handle(stream)), "mmact_gemm_mxfp4")
+    s = (_lib or load()).mmact_gemm_mxfp4(pa, psa, pb, psb, _bias_ptr(bias, N), pc, M, N, K, dt, ACT[act], alpha,
+                                          _stream_handle(stream))
+    if s:
+        _check(s, "mmact_gemm_mxfp4")
 
 
 def mmact_linear_mxfp4_workspace_bytes(M: int, K: int) -> int:
@@ -507,18 +515,18 @@ def mmact_linear_mxfp4_workspace_bytes(M: int, K: int) -> int:
 def mmact_linear_mxfp4(x, w_codes, w_scales, bias, C, workspace, act: str = "none", alpha: float = 0.0,
                        stream=None) -> None:
     """C = act(q(x) @ W.T + bias): x [M, K] is quantised to MXFP4 on the way in, W [N, K] is MXFP4."""
-    L = load()
-    px, pc = _dev(x, "x", _IN), _dev(C, "C", _OUT)
-    if x.dim() != 2 or C.dim() != 2 or C.shape[0] != x.shape[0]:
+    px, xd, M, K = _matrix(x, "x")
+    pc, cd, rows, N = _matrix(C, "C")
+    if rows != M:
         raise ValueError("x must be [M, K] and C [M, N]")
-    M, K = x.shape
-    N = C.shape[1]
     pw, ps = _mxfp4_ptrs(w_codes, w_scales, N, K, "W")
     pws = _dev(workspace, "workspace", _BYTES)
     if workspace.numel() < -(-M * ((K + 31) // 32 * 16) // 512) * 512 + (M + 127) // 128 * ((K + 127) // 128) * 512:
         raise ValueError("workspace must hold mmact_linear_mxfp4_workspace_bytes(M, K) bytes")
-    _check(L.mmact_linear_mxfp4(px, pw, ps, _bias_ptr(bias, N), pc, M, N, K, DTYPE[x.dtype], DTYPE[C.dtype],
-                                ACT[act], float(alpha), pws, _stream_handle(stream)), "mmact_linear_mxfp4")
+    s = (_lib or load()).mmact_linear_mxfp4(px, pw, ps, _bias_ptr(bias, N), pc, M, N, K, xd, cd, ACT[act], alpha, pws,
+                                            _stream_handle(stream))
+    if s:
+        _check(s, "mmact_linear_mxfp4")
 
 
 def mmact_set_gemm_mxfp4_kernel(mode: int) -> None:

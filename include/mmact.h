@@ -547,9 +547,11 @@ mmact_status mmact_gemm_mxfp4(const void *a_codes, const void *a_scales, const v
 /*
  * C = act(q(x) x W^T + bias): x [M, K] row-major in x_dtype (F16, BF16 or F32)
  * is quantised to MXFP4 on the way in, W [N, K] is held in MXFP4.  The same
- * result as mmact_quantize_mxfp4 into `workspace` and mmact_gemm_mxfp4.
- *   workspace  at least mmact_linear_mxfp4_workspace_bytes, 16-byte aligned; calls that may overlap
- *              on the GPU need one each.
+ * result as mmact_quantize_mxfp4 into `workspace` and mmact_gemm_mxfp4 (up to
+ * 32 rows are quantised inside the product's kernel instead).
+ *   workspace  at least mmact_linear_mxfp4_workspace_bytes, 16-byte aligned,
+ *              contents ignored and undefined afterwards; calls that may
+ *              overlap on the GPU need one each.
  */
 mmact_status mmact_linear_mxfp4(const void *x, const void *w_codes, const void *w_scales, const float *bias,
                                 void *C, int64_t M, int64_t N, int64_t K, mmact_dtype x_dtype,

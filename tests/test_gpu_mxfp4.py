@@ -193,8 +193,9 @@ def test_gemm_empty_k_is_the_activation_of_the_bias(M, N):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (1, 333, 100), (9, 264, 520), (80, 1001, 2056), (150, 128, 64), (260, 640, 256)])
-def test_linear_is_quantise_and_gemm(dtype, M, N, K):
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (1, 333, 100), (9, 264, 520), (16, 130, 33), (17, 260, 4100), (32, 128, 777),
+                                   (33, 640, 512), (80, 1001, 2056), (150, 128, 64), (260, 640, 256)])
+def test_linear_is_quantise_and_gemm(dtype, M, N, K, kernel):
     rng = np.random.default_rng(M + K)
     x = tensor(rng.normal(0, 1, (M, K)), dtype)
     wc, ws, wv = random_mx(rng, N, K, K ** -0.5)
@@ -209,6 +210,21 @@ def test_linear_is_quantise_and_gemm(dtype, M, N, K):
     assert torch.equal(outs[0], outs[1])
     want, bound = ref.gemm(ref.quantize(host64(x))[2], wv, bias.astype(np.float64), "gelu", 0.0)
     check(outs[0], want, bound, "bf16")
+
+
+def test_linear_marks_infinities_and_nan_like_the_quantiser():
+    """Few rows, quantised inside the product: a block with an infinity or a NaN makes its row NaN."""
+    rng = np.random.default_rng(9)
+    M, N, K = 5, 130, 320
+    x = rng.normal(0, 1, (M, K))
+    clean = x.copy()
+    x[1, 7], x[3, 300] = np.inf, np.nan
+    wc, ws, wv = random_mx(rng, N, K, K ** -0.5)
+    work = torch.empty(mmact.mmact_linear_mxfp4_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    out = [torch.empty((M, N), dtype=torch.float32, device="cuda") for _ in range(2)]
+    mmact.mmact_linear_mxfp4(tensor(x, "bf16"), wc, ws, None, out[0], work)
+    mmact.mmact_linear_mxfp4(tensor(clean, "bf16"), wc, ws, None, out[1], work)
+    assert torch.isnan(out[0][[1, 3]]).all() and torch.equal(out[0][[0, 2, 4]], out[1][[0, 2, 4]])
 
 
 def test_calls_on_a_side_stream_and_in_a_graph():
