@@ -37,26 +37,28 @@ std::atomic<int> g_mx_kernel{0};   // 0: chosen per shape; 1: rows kernel; 2: pa
 // The current device, with this file's kernels set up on it (once per device).
 struct MxContext {
     DeviceContext dev;
-    int max_pairs;
+    int max_pairs;                   // CTA pairs of the pair kernel resident at once
+    const int *max_clusters;         // [i]: clusters of 2^i CTAs of the rows kernel
 };
 
 mmact_status mx_context(MxContext *out)
 {
     static std::mutex mutex;
     static std::atomic<bool> ready[MAX_DEVICES];
-    static int pairs[MAX_DEVICES];
+    static int pairs[MAX_DEVICES], clusters[MAX_DEVICES][4];
     const mmact_status s = device_context(&out->dev);
     if (s != MMACT_OK) return s;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
     if (!ready[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(mutex);               // setting up twice is harmless
-        if (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels() != cudaSuccess ||
+        if (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels(clusters[dev]) != cudaSuccess ||
             setup_moe_kernels() != cudaSuccess)
             return MMACT_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
     out->max_pairs = pairs[dev];
+    out->max_clusters = clusters[dev];
     return MMACT_OK;
 }
 
@@ -103,13 +105,18 @@ struct MxPlan {
     MxRowsLaunch R;
 };
 
-// Whether a product runs on the pair kernel.
+// Whether a product runs on the pair kernel: when the rows kernel would have more
+// tiles (128 x 128) than there are SMs.  Measured on GB300 for M from 160 to 4096,
+// N from 256 to 8192 and K of 256, 1024 and 4096: up to one tile an SM the rows
+// kernel is 15 % faster (K = 256: 5.4 against 6.2 us), equal (K = 1024) or up to
+// 25 % faster (K = 4096: 8.0 against 10.2); past that the pair kernel is up to
+// twice and more as fast (1024 x 4096 x 4096: 11.3 against 20.8 us).
 bool mx_choose_pair(const MxContext &c, int64_t M, int64_t N)
 {
     const int mode = g_mx_kernel.load();
     if (c.max_pairs < 1 || mode == 1) return false;
     if (mode == 2) return true;
-    return M > 128 && ((M + 255) / 256) * ((N + 255) / 256) >= c.max_pairs / 2;
+    return M > 128 && ((M + 127) / 128) * ((N + 127) / 128) > c.dev.sm_count;
 }
 
 // Rows of x up to which the rows kernel quantises them itself (gemm_mxfp4_rows.cu
@@ -174,10 +181,12 @@ mmact_status mx_gemm_plan(MxPlan &plan, const void *ac, const void *as, const vo
     while (bt < 128 && bt < M) bt *= 2;
     const int64_t tiles = a.tiles_n * ((M + bt - 1) / bt);
     if (tiles * 8 > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= sms && num_kb >= split * 2) split *= 2;
+    // CTAs to a tile: as long as that leaves no cluster waiting for SMs and each CTA two K blocks
+    int split = 1, log2 = 0;
+    while (split < 8 && tiles * split * 2 <= sms && tiles <= c.max_clusters[log2 + 1] && num_kb >= split * 2) split *= 2, ++log2;
     a.kb_per = (num_kb + split - 1) / split;
     while (split > 1 && (split - 1) * a.kb_per >= num_kb) split /= 2, a.kb_per = (num_kb + split - 1) / split;
+    a.stages = std::min(MX_ROWS_STAGES(bt), a.kb_per);
     a.split = split;
     a.act = (int)act;
     a.alpha = alpha;

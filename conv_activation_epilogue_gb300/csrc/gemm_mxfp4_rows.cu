@@ -33,24 +33,29 @@
 
 namespace mmact {
 
+// Shared memory: barriers, then the ring: p.stages of weights, of tokens, of scales
+// (as many as the K blocks of a CTA ask for, so that small products leave room for
+// the next kernel's CTAs, whose set-up then overlaps).
 template <int BT>
 struct MxRowsCfg {
     static constexpr int W_BYTES = 128 * 128, T_BYTES = BT * 128, S_BYTES = 2 * 1024;
     static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + S_BYTES;
-    // up to 32 rows: two CTAs fit on an SM, so that the next product's set-up and first copies to L2
-    // overlap this one's work; else as many as fit
-    static constexpr int STAGES = BT <= 32 ? 5 : (BT == 64 ? 8 : 6);
+    // Up to 32 rows: two CTAs fit on an SM, for the same overlap; else as many as fit.
+    static constexpr int MAX_STAGES = MX_ROWS_STAGES(BT);
     static constexpr uint32_t SCALE_COL = BT;                            // 16 columns for each stage
-    static constexpr uint32_t TMEM_COLS = BT + 16 * STAGES <= 128 ? 128 : 256;
-    static constexpr int OFF_W = 0;
-    static constexpr int OFF_T = OFF_W + STAGES * W_BYTES;
-    static constexpr int OFF_S = OFF_T + STAGES * T_BYTES;
-    static constexpr int OFF_BAR = OFF_S + STAGES * S_BYTES;
-    static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2) * 8;
-    static constexpr int SMEM_BYTES = OFF_MISC + 16;
-    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-    static_assert(BT + 16 * STAGES <= TMEM_COLS, "tensor memory budget");
-    static_assert(BT * 512 <= STAGES * W_BYTES, "the partial tile takes the ring's place");
+    static constexpr uint32_t TMEM_COLS = BT + 16 * MAX_STAGES <= 128 ? 128 : 256;
+    static constexpr int OFF_BAR = 0, OFF_MISC = (2 * MAX_STAGES + 2) * 8, OFF_RING = 1024;
+    static constexpr int PART_BYTES = BT * 512;                          // a partial tile, over the ring
+    // at least so much that no more CTAs share an SM's 227 KB than its 512 columns of tensor memory serve
+    static constexpr int MIN_SMEM = 232448 / (512 / (int)TMEM_COLS + 1) + 1024;
+    static int smem_bytes(const MxRowsArgs &a)
+    {
+        const int ring = OFF_RING + a.stages * STAGE_BYTES, part = a.split > 1 ? OFF_RING + PART_BYTES : 0;
+        const int need = ring > part ? ring : part;
+        return need > MIN_SMEM ? need : MIN_SMEM;
+    }
+    static_assert(OFF_MISC + 16 <= OFF_RING && OFF_RING + MAX_STAGES * STAGE_BYTES <= 232448, "shared memory budget");
+    static_assert(BT + 16 * MAX_STAGES <= TMEM_COLS, "tensor memory budget");
 };
 
 // C[m0 + j][n] = act(z[j] + bias) for this lane's n and the rows that exist:
@@ -101,7 +106,7 @@ __device__ __forceinline__ void quantize_stages(const MxRowsArgs &p, const Pipe 
     const int w = (int)(threadIdx.x >> 5) - 6, lane = threadIdx.x & 31, blk = lane & 7;
     const bool vec = (int64_t)p.K * (XT == IN_F32 ? 4 : 2) % 16 == 0;
     for (int kb = kb0 + w, i = w; kb < kb1; kb += 4, i += 4) {
-        const uint32_t stage = (uint32_t)i % Cfg::STAGES, phase = ((uint32_t)i / Cfg::STAGES) & 1u;
+        const uint32_t stage = (uint32_t)(i % p.stages), phase = (uint32_t)(i / p.stages) & 1u;
         const int k0 = kb * 256 + blk * 32, n = min(32, p.K - k0);
 #pragma unroll 1
         for (int r0 = 0; r0 < p.M; r0 += 8) {
@@ -120,7 +125,7 @@ __device__ __forceinline__ void quantize_stages(const MxRowsArgs &p, const Pipe 
                     }
                 }
             }
-            // the warp's last stage before this one was four earlier, so the slot's last reader is known to be the one before
+            // (this warp saw the slot of four stages ago free, so no more than one use of this slot is outstanding)
             if (r0 == 0 && !mx_warp_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) {
                 if (lane == 0) pipe_fail(pp);
                 return;
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
                            const MxRowsArgs p)
 {
     using Cfg = MxRowsCfg<BT>;
-    constexpr int STAGES = Cfg::STAGES;
+    const int stages = p.stages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = ptx::smem_addr(smem);
@@ -174,14 +179,13 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
     const int nb = tile % p.tiles_n, tb = tile / p.tiles_n;
     const int kb0 = rank * p.kb_per, kb1 = min(p.num_kb, kb0 + p.kb_per);
 
-    ptx::griddep_launch_dependents();
     const bool aligned = (base & 1023u) == 0;
     if (!aligned && threadIdx.x == 0) atomicOr(p.status, ST_SMEM_ALIGN);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
     Pipe pp;
     pp.full0 = base + Cfg::OFF_BAR;
-    pp.empty0 = pp.full0 + 8 * STAGES;
-    pp.tfull0 = pp.empty0 + 8 * STAGES;
+    pp.empty0 = pp.full0 + 8 * Cfg::MAX_STAGES;
+    pp.tfull0 = pp.empty0 + 8 * Cfg::MAX_STAGES;
     pp.drain = pp.tfull0 + 8;
     pp.tempty0 = 0;
     pp.abort = misc + 1;
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
         if (threadIdx.x == 0) {
             ptx::prefetch_tensormap(&tmW);
             if constexpr (XT == XT_NONE) ptx::prefetch_tensormap(&tmT);
-            for (int s = 0; s < STAGES; ++s) {
+            for (int s = 0; s < stages; ++s) {
                 ptx::mbar_init(pp.full0 + 8 * s, XT == XT_NONE ? 1 : 2);   // + a quantising warp
                 ptx::mbar_init(pp.empty0 + 8 * s, 1);
             }
@@ -204,24 +208,33 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
                 ptx::tma_prefetch_2d(&tmSW, kb * 256, nb);
             }
         }
-        if (warp == 1) {
+    }
+    ptx::cta_sync();
+    ptx::griddep_wait();
+    // Tensor memory is taken when the kernels before this one are done, and the next
+    // one may start when every CTA of this one has it: a CTA that holds tensor memory
+    // never waits for one that still needs it.  (CTAs of this kernel that share an SM
+    // find room for all of them: smem_bytes sees to that.)
+    if (warp >= 1 && warp < 6) {
+        if (warp == 1 && aligned) {
             ptx::tmem_alloc(base + Cfg::OFF_MISC, Cfg::TMEM_COLS);
             ptx::tmem_relinquish();
         }
+        __syncwarp();
+        ptx::tc_fence_before();
+        asm volatile("barrier.sync 2, 160;" ::: "memory");
+        ptx::tc_fence_after();
+        pp.tmem = misc[0];
     }
-    ptx::tc_fence_before();
-    ptx::cta_sync();
-    ptx::tc_fence_after();
-    pp.tmem = misc[0];
-    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
 
-    const uint32_t sW = base + Cfg::OFF_W, sT = base + Cfg::OFF_T, sS = base + Cfg::OFF_S;
+    const uint32_t sW = base + Cfg::OFF_RING, sT = sW + stages * Cfg::W_BYTES, sS = sT + stages * Cfg::T_BYTES;
     if (aligned && warp == 0) {
         if (lane == 0) {
             bool ok = true;
             int issued = 0;
+            uint32_t stage = 0, phase = 0;
             for (int kb = kb0; kb < kb1; ++kb, ++issued) {
-                const uint32_t stage = (uint32_t)issued % STAGES, phase = ((uint32_t)issued / STAGES) & 1u;
                 if (!pipe_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) { ok = false; break; }
                 const uint32_t fb = pp.full0 + 8 * stage;
                 ptx::mbar_arrive_expect_tx(fb, (uint32_t)(XT == XT_NONE ? Cfg::STAGE_BYTES : Cfg::W_BYTES + 1024));
@@ -231,18 +244,19 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
                     ptx::tma_load_2d(sT + stage * Cfg::T_BYTES, &tmT, fb, kb * 64, tb * BT);
                     ptx::tma_load_2d(sS + stage * Cfg::S_BYTES + 1024u, &tmST, fb, kb * 256, tb);
                 }
+                if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
             }
             if (!ok) pipe_fail(pp);
             // every copy has landed before the ring's memory is used again or the CTA exits
-            for (int u = max(0, issued - STAGES); u < issued; ++u)
-                ptx::mbar_wait_bounded(pp.full0 + 8 * (u % STAGES), (u / STAGES) & 1, DRAIN_NS, nullptr);
+            for (int u = max(0, issued - stages); u < issued; ++u)
+                ptx::mbar_wait_bounded(pp.full0 + 8 * (u % stages), (u / stages) & 1, DRAIN_NS, nullptr);
         }
     } else if (aligned && warp == 1) {
         {                                                     // the whole warp: see mma_mxf4
             const uint32_t id0 = ptx::idesc_mxf4(128, BT, 0, 0), id2 = ptx::idesc_mxf4(128, BT, 2, 2);
             bool ok = true;
-            for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-                const uint32_t stage = (uint32_t)i % STAGES, phase = ((uint32_t)i / STAGES) & 1u;
+            uint32_t stage = 0, phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t w0 = sW + stage * Cfg::W_BYTES, t0 = sT + stage * Cfg::T_BYTES;
@@ -259,8 +273,9 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
                     if (k < n)
                         ptx::mma_mxf4(pp.tmem, ptx::smem_desc(w0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B),
                                       ptx::smem_desc(t0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B), k & 1 ? id2 : id0,
-                                      ts + 4 * (k >> 1), ts + 8 + 4 * (k >> 1), (i | k) != 0 ? 1u : 0u);
+                                      ts + 4 * (k >> 1), ts + 8 + 4 * (k >> 1), (kb > kb0 || k > 0) ? 1u : 0u);
                 ptx::commit_elected(pp.empty0 + 8 * stage);
+                if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
             }
             if (ok) ptx::commit_elected(pp.tfull0);
             else if (lane == 0) pipe_fail(pp);
@@ -302,7 +317,7 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
         }
     } else {
         // partial tile [column][lane] over the ring, whose copies and MMAs are done
-        float *part = reinterpret_cast<float *>(smem);
+        float *part = reinterpret_cast<float *>(smem + Cfg::OFF_RING);
         if (epi && good) {
 #pragma unroll 1
             for (int c = 0; c < BT; c += 16) {
@@ -316,7 +331,7 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
         if (epi && good) {
             // this CTA's slice of the columns: 16 at a time, or the 2 to 8 it has
             const int cols = BT / p.split, c0 = rank * cols;
-            const uint32_t at = base + (uint32_t)(c0 * 128 + q * 32 + lane) * 4u;
+            const uint32_t at = base + Cfg::OFF_RING + (uint32_t)(c0 * 128 + q * 32 + lane) * 4u;
             auto slice = [&](auto ch) {
                 constexpr int CH = decltype(ch)::value;
                 for (int c = 0; c < cols && tb * BT + c0 + c < p.M; c += CH) {
@@ -347,7 +362,7 @@ static cudaError_t launch_rows_t(const MxRowsLaunch &L, cudaStream_t stream)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)L.grid);
     cfg.blockDim = dim3(ROWS_THREADS<XT>);
-    cfg.dynamicSmemBytes = MxRowsCfg<BT>::SMEM_BYTES;
+    cfg.dynamicSmemBytes = (size_t)MxRowsCfg<BT>::smem_bytes(L.args);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -385,7 +400,7 @@ template <int OUT, int BT, int XT>
 static cudaError_t setup_rows_t()
 {
     return cudaFuncSetAttribute(gemm_mxfp4_rows_kernel<OUT, BT, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                MxRowsCfg<BT>::SMEM_BYTES);
+                                MxRowsCfg<BT>::OFF_RING + MxRowsCfg<BT>::MAX_STAGES * MxRowsCfg<BT>::STAGE_BYTES);
 }
 
 template <int OUT, int BT>
@@ -408,11 +423,31 @@ static cudaError_t setup_rows_o()
     return e;
 }
 
-cudaError_t setup_mxfp4_rows_kernels()
+// Clusters of `split` CTAs that are resident at once (with a full ring).
+template <int BT>
+static cudaError_t rows_clusters(int split, int *n)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(split * 64));
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = MxRowsCfg<BT>::OFF_RING + MxRowsCfg<BT>::MAX_STAGES * MxRowsCfg<BT>::STAGE_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, gemm_mxfp4_rows_kernel<OUT_BF16, BT, XT_NONE>, &cfg);
+}
+
+cudaError_t setup_mxfp4_rows_kernels(int (&max_clusters)[4])
 {
     cudaError_t e = setup_rows_o<OUT_BF16>();
     if (e == cudaSuccess) e = setup_rows_o<OUT_F16>();
     if (e == cudaSuccess) e = setup_rows_o<OUT_F32>();
+    max_clusters[0] = 1 << 30;
+    for (int i = 1; i < 4 && e == cudaSuccess; ++i) e = rows_clusters<128>(1 << i, &max_clusters[i]);
     return e;
 }
 

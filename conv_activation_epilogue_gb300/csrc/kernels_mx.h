@@ -48,6 +48,7 @@ struct MxRowsArgs {
     int nk64, num_kb;    // as above
     int tiles_n;         // tiles of 128 rows of B
     int split, kb_per;   // CTAs of a tile's cluster, K blocks of each
+    int stages;          // of the ring
     int act;
     float alpha;
     const float *bias;
@@ -65,7 +66,10 @@ struct MxRowsLaunch {
     int grid;
 };
 
-cudaError_t setup_mxfp4_rows_kernels();
+constexpr int MX_ROWS_STAGES(int bt) { return bt <= 32 ? 5 : (bt == 64 ? 8 : 6); }   // at most
+
+// max_clusters[i]: clusters of 2^i CTAs resident at once, one CTA to an SM
+cudaError_t setup_mxfp4_rows_kernels(int (&max_clusters)[4]);
 cudaError_t launch_gemm_mxfp4_rows(const MxRowsLaunch &L, cudaStream_t stream);
 
 // A mixture-of-experts layer for a few tokens.
