@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libmmact.so")
 SOURCES = ["api.cu", "gemm.cu", "gemm_splitk.cu", "gemm_pair.cu", "conv.cu", "conv_vec.cu", "conv_nhwc.cu", "conv_tmem.cu", "elementwise.cu", "noalloc.cu",
            "api_mx.cu", "mxfp4.cu", "gemm_mxfp4.cu",
-           "gemm_mxfp4_rows.cu", "moe.cu"]
+           "gemm_mxfp4_rows.cu", "moe.cu", "moe_mxfp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

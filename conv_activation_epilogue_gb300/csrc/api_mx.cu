@@ -53,7 +53,7 @@ mmact_status mx_context(MxContext *out)
     if (!ready[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(mutex);               // setting up twice is harmless
         if (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels(clusters[dev]) != cudaSuccess ||
-            setup_moe_kernels() != cudaSuccess)
+            setup_moe_kernels() != cudaSuccess || setup_moe_mxfp4_kernels() != cudaSuccess)
             return MMACT_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
@@ -226,9 +226,11 @@ constexpr int64_t MOE_K_PAD = 256;   // K of a stage of tokens
 
 // Where the parts of mmact_moe's workspace begin.
 struct MoeWorkspace {
-    int64_t logits, x_hi, x_lo, h_hi, h_lo, part, bytes;
+    int64_t logits, x, x_scales, h, h_scales, part, bytes;
 };
 
+// The same for both forms of the weights: x padded (2 bytes a value) or its terms
+// (4 bytes a value and a quarter), h in two halves (4 bytes) or its terms.
 MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
 {
     MoeWorkspace w;
@@ -240,10 +242,10 @@ MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t t
         return here;
     };
     w.logits = take(T * E * 4);
-    w.x_hi = take(T * Hp * 2);
-    w.x_lo = take(T * Hp * 2);
-    w.h_hi = take(T * top * Ip * 2);
-    w.h_lo = take(T * top * Ip * 2);
+    w.x = take(T * Hp * 4);
+    w.x_scales = take(T * Hp / 4);
+    w.h = take(T * top * Ip * 4);
+    w.h_scales = take(T * top * Ip / 4);
     w.part = take(T * top * H * 4);
     w.bytes = at;
     return w;
@@ -406,7 +408,6 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
     a.Ip = (int)round_up(I, MOE_K_PAD);
     a.act = (int)act;
     a.alpha = alpha;
-    a.w_type = mx ? 2 : (w_dtype == MMACT_BF16 ? 1 : 0);
     a.x = x;
     a.router = router;
     a.w1 = w1;
@@ -423,23 +424,30 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
     char *ws = static_cast<char *>(workspace);
     a.counters = reinterpret_cast<unsigned int *>(ws);
     a.logits = reinterpret_cast<float *>(ws + w.logits);
-    a.x_hi = reinterpret_cast<uint16_t *>(ws + w.x_hi);
-    a.x_lo = reinterpret_cast<uint16_t *>(ws + w.x_lo);
-    a.h_hi = reinterpret_cast<uint16_t *>(ws + w.h_hi);
-    a.h_lo = reinterpret_cast<uint16_t *>(ws + w.h_lo);
+    if (mx) {
+        a.x_codes = reinterpret_cast<uint8_t *>(ws + w.x);
+        a.x_scales = reinterpret_cast<uint8_t *>(ws + w.x_scales);
+        a.h_codes = reinterpret_cast<uint8_t *>(ws + w.h);
+        a.h_scales = reinterpret_cast<uint8_t *>(ws + w.h_scales);
+    } else {
+        a.x_pad = reinterpret_cast<uint16_t *>(ws + w.x);
+        a.h_hi = reinterpret_cast<uint16_t *>(ws + w.h);
+        a.h_lo = a.h_hi + T * top * a.Ip;
+    }
     a.part = reinterpret_cast<float *>(ws + w.part);
     a.status = c.dev.status;
     a.wait_ns = c.dev.wait_ns;
     L.x_out = out_kind(x_dtype);
-    // Rows of a tile: the most (128, all eight product warps) that still give three
-    // quarters of the SMs an item of the up product, were every choice another
-    // expert; half and a quarter of that for layers with fewer.
+    // Rows of a tile: 128; for 16-bit weights half and a quarter of that when not even three quarters of the
+    // SMs would have an item of the up product, were every choice another expert.
     a.half_rows = 64;
     const int64_t groups = std::min(T * top, E);
-    while (a.half_rows > 16 && groups * ((a.R1 + 2 * a.half_rows - 1) / (2 * a.half_rows)) < c.dev.sm_count * 3 / 4)
+    while (!mx && a.half_rows > 16 &&
+           groups * ((a.R1 + 2 * a.half_rows - 1) / (2 * a.half_rows)) < c.dev.sm_count * 3 / 4)
         a.half_rows /= 2;
     L.grid = c.dev.sm_count;
     if (!moe_encode(&L.tm1, w1, E * a.R1, H, mx, a.half_rows) || !moe_encode(&L.tm2, w2, E * H, I, mx, a.half_rows))
         return MMACT_ERR_CUDA;
-    return enqueued(launch_moe(L, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return enqueued(mx ? launch_moe_mxfp4(L, st) : launch_moe(L, st));
 }

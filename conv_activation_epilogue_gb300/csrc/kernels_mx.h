@@ -79,7 +79,6 @@ struct MoeArgs {
     int half_rows;               // rows of half a tile of weights: 64, 32 or 16
     int Hp, Ip;                  // H and I rounded up to whole ring stages (row pitches of the workspace's arrays)
     int gated, normalize, act;
-    int w_type;                  // 0 fp16, 1 bf16, 2 MXFP4
     float alpha;
     const void *x, *router;      // [T, H], [E, H]
     const void *w1, *w2;         // [E, R1, H], [E, H, I] (MXFP4: codes of [E * R1, H], [E * H, I])
@@ -91,8 +90,10 @@ struct MoeArgs {
     // workspace
     unsigned int *counters;      // two grid barriers
     float *logits;               // [T, E]
-    uint16_t *x_hi, *x_lo;       // x as the products read it [T, Hp] (lo: fp16 x with MXFP4 weights)
-    uint16_t *h_hi, *h_lo;       // h in bf16 halves [T * top, Ip]
+    uint16_t *x_pad;             // 16-bit weights: x [T, Hp], zeros past H
+    uint16_t *h_hi, *h_lo;       // 16-bit weights: h in bf16 halves [T * top, Ip]
+    uint8_t *x_codes, *x_scales; // MXFP4: x and h as sums of eight MXFP4 terms: a KB of codes and 64
+    uint8_t *h_codes, *h_scales; //   scales for each token (slot) and 256 K
     float *part;                 // [T * top, H]
     unsigned int *status;
     unsigned long long wait_ns;
@@ -106,7 +107,9 @@ struct MoeLaunch {
 };
 
 cudaError_t setup_moe_kernels();
-cudaError_t launch_moe(const MoeLaunch &L, cudaStream_t stream);
+cudaError_t launch_moe(const MoeLaunch &L, cudaStream_t stream);          // 16-bit weights
+cudaError_t setup_moe_mxfp4_kernels();
+cudaError_t launch_moe_mxfp4(const MoeLaunch &L, cudaStream_t stream);    // half_rows 64
 
 // out [rows, cols] = act(bias): a product over an empty K.
 cudaError_t launch_mx_bias_act(const float *bias, void *out, int64_t rows, int64_t cols, int out_kind, int act,
