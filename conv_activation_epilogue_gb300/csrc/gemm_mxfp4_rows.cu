@@ -254,26 +254,16 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
     } else if (aligned && warp == 1) {
         {                                                     // the whole warp: see mma_mxf4
             const uint32_t id0 = ptx::idesc_mxf4(128, BT, 0, 0), id2 = ptx::idesc_mxf4(128, BT, 2, 2);
+            const uint64_t w0 = ptx::smem_desc(sW, 16u, 1024u, ptx::SWIZZLE_128B), t0 = ptx::smem_desc(sT, 16u, 1024u, ptx::SWIZZLE_128B);
+            const uint64_t s0 = ptx::smem_desc(sS, 16u, 128u, ptx::SWIZZLE_NONE);
             bool ok = true;
             uint32_t stage = 0, phase = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
                 ptx::tc_fence_after();
-                const uint32_t w0 = sW + stage * Cfg::W_BYTES, t0 = sT + stage * Cfg::T_BYTES;
-                const uint32_t s0 = sS + stage * Cfg::S_BYTES, ts = pp.tmem + Cfg::SCALE_COL + stage * 16u;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    ptx::tmem_cp_scales(ts + 4 * j, ptx::smem_desc(s0 + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
-                    ptx::tmem_cp_scales(ts + 8 + 4 * j,
-                                        ptx::smem_desc(s0 + 1024u + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
-                }
-                const int n = min(4, p.nk64 - 4 * kb);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < n)
-                        ptx::mma_mxf4(pp.tmem, ptx::smem_desc(w0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B),
-                                      ptx::smem_desc(t0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B), k & 1 ? id2 : id0,
-                                      ts + 4 * (k >> 1), ts + 8 + 4 * (k >> 1), (kb > kb0 || k > 0) ? 1u : 0u);
+                ptx::mma_mxf4_stage(pp.tmem, w0 + stage * (Cfg::W_BYTES >> 4), t0 + stage * (Cfg::T_BYTES >> 4),
+                                    s0 + stage * (Cfg::S_BYTES >> 4), pp.tmem + Cfg::SCALE_COL + stage * 16u, id0, id2,
+                                    min(4, p.nk64 - 4 * kb), kb > kb0 ? 1u : 0u);
                 ptx::commit_elected(pp.empty0 + 8 * stage);
                 if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
             }

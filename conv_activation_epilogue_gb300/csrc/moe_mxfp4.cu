@@ -242,6 +242,9 @@ __device__ __forceinline__ bool mxe_scales(const MoeArgs &p, const MoeShared &S,
 __device__ __forceinline__ bool mxe_mma(const MoeShared &S, const MxePipe &m, const MoeProduct &pr, uint32_t &use, uint32_t &item)
 {
     const int nk64 = (pr.K + 63) / 64;
+    const uint64_t w0 = ptx::smem_desc(m.ring, 16u, 1024u, ptx::SWIZZLE_128B);
+    const uint64_t t0 = ptx::smem_desc(m.tokens, 16u, 1024u, ptx::SWIZZLE_128B);
+    const uint64_t s0 = ptx::smem_desc(m.scales, 16u, 128u, ptx::SWIZZLE_NONE);
     return each_item(S, pr, [&](int ai, int) {
         const int cnt = S.first[ai + 1] - S.first[ai], n = cnt < 2 ? 16 : (8 * cnt + 15) & ~15;
         const uint32_t id0 = ptx::idesc_mxf4(128, n, 0, 0), id2 = ptx::idesc_mxf4(128, n, 2, 2);
@@ -252,20 +255,8 @@ __device__ __forceinline__ bool mxe_mma(const MoeShared &S, const MxePipe &m, co
             const uint32_t slot = use % MXE_STAGES;
             if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * slot, (use / MXE_STAGES) & 1u)) return false;
             ptx::tc_fence_after();
-            const uint32_t w0 = m.ring + slot * MXE_W_BYTES, t0 = m.tokens + slot * MXE_T_BYTES;
-            const uint32_t s0 = m.scales + slot * MXE_S_BYTES, ts = m.pp.tmem + MXE_SCALE_COL + slot * 16u;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ptx::tmem_cp_scales(ts + 4 * j, ptx::smem_desc(s0 + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
-                ptx::tmem_cp_scales(ts + 8 + 4 * j, ptx::smem_desc(s0 + 1024u + 512u * j, 16u, 128u, ptx::SWIZZLE_NONE));
-            }
-            const int left = min(4, nk64 - 4 * s);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < left)
-                    ptx::mma_mxf4(d, ptx::smem_desc(w0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B),
-                                  ptx::smem_desc(t0 + 32u * k, 16u, 1024u, ptx::SWIZZLE_128B), k & 1 ? id2 : id0,
-                                  ts + 4 * (k >> 1), ts + 8 + 4 * (k >> 1), (s | k) != 0 ? 1u : 0u);
+            ptx::mma_mxf4_stage(d, w0 + slot * (MXE_W_BYTES >> 4), t0 + slot * (MXE_T_BYTES >> 4), s0 + slot * (MXE_S_BYTES >> 4),
+                                m.pp.tmem + MXE_SCALE_COL + slot * 16u, id0, id2, min(4, nk64 - 4 * s), s != 0 ? 1u : 0u);
             ptx::commit_elected(m.pp.empty0 + 8 * slot);
         }
         ptx::commit_elected(m.pp.tfull0 + 8 * buf);

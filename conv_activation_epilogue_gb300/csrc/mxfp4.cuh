@@ -296,6 +296,46 @@ __device__ __forceinline__ void commit_elected_pair(uint32_t bar, uint16_t mask)
 
 #undef MMACT_ELECTED
 
+// One ring stage of 256 K of a product of 128 rows (A) by a tile (B) of at most 128:
+// four scale tiles of 512 bytes (A's two, then B's) to 16 columns of tensor memory
+// from `ts` on, and a K = 64 MMA for each 32 bytes of the operands' rows; `n` of them,
+// 4 but in the last stage.  `a`, `b`, `s` are the descriptors of the stage's parts.
+// The usual case is one block with one election: descriptors made one by one, with a
+// branch around each MMA, took 640 clocks a stage, as long as a stage's weights come
+// in.
+__device__ __forceinline__ void mma_mxf4_stage(uint32_t d, uint64_t a, uint64_t b, uint64_t s, uint32_t ts, uint32_t id0,
+                                               uint32_t id2, int n, uint32_t accumulate)
+{
+    if (n == 4) {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3, s1, s2, s3;\n\t"
+            ".reg .b32 t1, t2, t3;\n\t"
+            "setp.ne.b32 p, %7, 0;\n\t"
+            "add.s64 s1, %3, 32;\n\tadd.s64 s2, %3, 64;\n\tadd.s64 s3, %3, 96;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+            "add.s32 t1, %4, 4;\n\tadd.s32 t2, %4, 8;\n\tadd.s32 t3, %4, 12;\n\t"
+            "elect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], %3;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [t1], s1;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [t2], s2;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [t3], s3;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %5, [%4], [t2], p;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a1, b1, %6, [%4], [t2], 1;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a2, b2, %5, [t1], [t3], 1;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a3, b3, %6, [t1], [t3], 1;\n\t"
+            "}" ::"r"(d),
+            "l"(a), "l"(b), "l"(s), "r"(ts), "r"(id0), "r"(id2), "r"(accumulate)
+            : "memory");
+        return;
+    }
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) tmem_cp_scales(ts + 4 * j, s + 32 * j);
+#pragma unroll 1
+    for (int k = 0; k < n; ++k)
+        mma_mxf4(d, a + 2 * k, b + 2 * k, k & 1 ? id2 : id0, ts + 4 * (k >> 1), ts + 8 + 4 * (k >> 1), accumulate | (uint32_t)k);
+}
+
 // Instruction descriptor for kind::mxf4: A and B E2M1 (format 1), scales UE8M0,
 // M and N extents; sa and sb (0 or 2) say which two bytes of the 32-bit scale
 // columns hold this instruction's scales.
