@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         ptx::fence_mbar_init();
     }
     ptx::griddep_wait();                                       // the router's logits
-    plan_experts<MOE_GROUP, MOE_THREADS>(p, S, reinterpret_cast<float *>(smem),
+    plan_experts<MOE_GROUP, MOE_THREADS>(p, S, reinterpret_cast<uint32_t *>(smem),
                                          reinterpret_cast<uint32_t *>(smem + MOE_OFF_TOKENS));
 
     const MoeProduct up = up_product(p, MOE_STAGE_K, MOE_TOKEN_K), down = down_product(p, MOE_STAGE_K, MOE_TOKEN_K);

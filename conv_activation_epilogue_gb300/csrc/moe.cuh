@@ -22,6 +22,11 @@ __device__ __forceinline__ uint32_t logit_key(float x)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float key_logit(uint32_t key)
+{
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
 // Whole-warp forms of TMA instructions, issued by one elected lane (see mma_mxf4).
 #define MMACT_ELECTED "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
 
@@ -119,58 +124,59 @@ struct MoeShared {
     uint64_t bar[MOE_MAX_BARS];
 };
 
-// Top k of N tokens t, t + stride, ... by one warp: each round the largest key of
-// those left, then the lowest index that has it; then the softmax weights, one to
-// a lane.  A round is a chain of dependent steps: several tokens go through it
-// side by side.
-template <int N>
-__device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, const float *logits, int t, int stride, int lane,
-                                               bool write)
+// Top k of a token by LANES lanes of a warp (32 / LANES tokens side by side; every
+// lane of the warp calls it): each round the largest key of those left, then the
+// lowest index that has it, whose key becomes 0; then the softmax weights.  `keys`:
+// the token's, in shared memory; lane `sub` of the token reads and clears only those
+// at sub + i * LANES.
+template <int LANES>
+__device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, uint32_t *keys, int t, bool valid, bool write)
 {
-    static_assert(MOE_MAX_E <= 32 * 32, "one bit for each of a lane's logits");
-    uint32_t taken[N] = {};                                    // bit i: this lane's logit i * 32 + lane is chosen
-    int mine[N] = {}, first[N] = {};
+    const int sub = threadIdx.x & (LANES - 1);
+    short *choice = S.choice + t * p.top;
+    float *probs = S.probs + t * p.top;
     for (int j = 0; j < p.top; ++j) {
-        uint32_t key[N] = {}, at[N] = {};
-        for (int e = lane, i = 0; e < p.E; e += 32, ++i)
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const uint32_t k = (taken[n] >> i) & 1u ? 0u : logit_key(logits[(t + n * stride) * p.E + e]);
-                if (k > key[n]) key[n] = k, at[n] = (uint32_t)e;
-            }
+        uint32_t key = 0, at = 0xffffu;
+#pragma unroll 4
+        for (int e = sub; e < p.E; e += LANES) {
+            const uint32_t k = keys[e];
+            if (k > key) key = k, at = (uint32_t)e;
+        }
         __syncwarp();
-        uint32_t best[N];
+        if constexpr (LANES == 32) {
+            const uint32_t best = __reduce_max_sync(0xffffffffu, key);
+            at = __reduce_min_sync(0xffffffffu, key == best ? at : 0xffffu);
+            key = best;
+        } else {
 #pragma unroll
-        for (int n = 0; n < N; ++n) best[n] = __reduce_max_sync(0xffffffffu, key[n]);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int e = (int)__reduce_min_sync(0xffffffffu, key[n] == best[n] ? at[n] : 0xffffu);
-            if ((e & 31) == lane) taken[n] |= 1u << (e >> 5);
-            if (j == 0) first[n] = e;
-            if (j == lane) mine[n] = e;
+            for (int o = LANES / 2; o > 0; o >>= 1) {
+                const uint32_t k2 = __shfl_xor_sync(0xffffffffu, key, o), at2 = __shfl_xor_sync(0xffffffffu, at, o);
+                if (k2 > key || (k2 == key && at2 < at)) key = k2, at = at2;
+            }
+        }
+        if (valid) {
+            if ((int)(at & (LANES - 1)) == sub) keys[at] = 0;
+            if (sub == 0) choice[j] = (short)at, probs[j] = key_logit(key);
         }
     }
+    __syncwarp();
+    const float peak = probs[0];
+    float total = 0.0f;
+    if (!p.normalize) {
+        for (int e = sub; e < p.E; e += LANES)
+            if (keys[e] != 0) total += expf(key_logit(keys[e]) - peak);
+    }
+    for (int j = sub; j < p.top; j += LANES) total += expf(probs[j] - peak);
+    __syncwarp();
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const float *row = logits + (t + n * stride) * p.E;
-        const float peak = row[first[n]];
-        const float w = lane < p.top ? expf(row[mine[n]] - peak) : 0.0f;
-        float total = w;
-        if (!p.normalize) {
-            total = 0.0f;
-            for (int e = lane; e < p.E; e += 32) total += expf(row[e] - peak);
-            __syncwarp();
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (lane < p.top) {
-            const int at = (t + n * stride) * p.top + lane;
-            S.choice[at] = (short)mine[n];
-            S.probs[at] = w / total;
-            if (write) {
-                p.experts[at] = mine[n];
-                p.probs[at] = w / total;
-            }
+    for (int o = LANES / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (!valid) return;
+    for (int j = sub; j < p.top; j += LANES) {
+        const float w = expf(probs[j] - peak) / total;
+        probs[j] = w;
+        if (write) {
+            p.experts[t * p.top + j] = choice[j];
+            p.probs[t * p.top + j] = w;
         }
     }
 }
@@ -192,27 +198,28 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S, uint
         S.count[e] = (short)c;
     }
     ptx::cta_sync();
-    if (tid < 32) {                                            // 32 experts at a time: running sums over the warp
-        int n = 0, at = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + tid, c = e < p.E ? S.count[e] : 0, groups = (c + GROUP - 1) / GROUP;
-            int sum = c, gsum = groups;
+    if (tid < 32) {                                            // consecutive experts to a lane, one running sum over the warp
+        const int per = (p.E + 31) / 32, e0 = tid * per, e1 = min(p.E, e0 + per);
+        int sum = 0, gsum = 0;
+        for (int e = e0; e < e1; ++e) sum += S.count[e], gsum += (S.count[e] + GROUP - 1) / GROUP;
+        __syncwarp();
+        int at = sum, n = gsum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, sum, o), gup = __shfl_up_sync(0xffffffffu, gsum, o);
-                if (tid >= o) sum += up, gsum += gup;
-            }
-            if (e < p.E) S.start[e] = (short)(at + sum - c);
-            for (int g = 0; g < groups; ++g) {
-                S.act[n + gsum - groups + g] = (short)e;
-                S.first[n + gsum - groups + g] = (short)(at + sum - c + g * GROUP);
-            }
-            n += __shfl_sync(0xffffffffu, gsum, 31);
-            at += __shfl_sync(0xffffffffu, sum, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, at, o), gup = __shfl_up_sync(0xffffffffu, n, o);
+            if (tid >= o) at += up, n += gup;
+        }
+        const int all = __shfl_sync(0xffffffffu, at, 31), groups = __shfl_sync(0xffffffffu, n, 31);
+        at -= sum, n -= gsum;
+        for (int e = e0; e < e1; ++e) {
+            const int c = S.count[e];
+            S.start[e] = (short)at;
+            for (int g = 0; g * GROUP < c; ++g, ++n) S.act[n] = (short)e, S.first[n] = (short)(at + g * GROUP);
+            at += c;
         }
         if (tid == 0) {
-            S.first[n] = (short)at;
-            S.nact = n;
+            S.first[groups] = (short)all;
+            S.nact = groups;
         }
     }
     ptx::cta_sync();
@@ -226,22 +233,36 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S, uint
 }
 
 // Choice and lists by every thread of an experts kernel: all logits go where the
-// rings will be (`logits`: T x E floats), the lists' masks to `mask`.
+// rings will be (`keys`: T x E words), the lists' masks to `mask`.  A warp takes a
+// token, or with more tokens than warps four at a time, eight lanes to each: the
+// rounds are chains of dependent steps and of warp reductions, which an SM does one
+// at a time (WHY).
 template <int GROUP, int THREADS>
-__device__ __forceinline__ void plan_experts(const MoeArgs &p, MoeShared &S, float *logits, uint32_t *mask)
+__device__ __forceinline__ void plan_experts(const MoeArgs &p, MoeShared &S, uint32_t *keys, uint32_t *mask)
 {
     constexpr int WARPS = THREADS / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < p.T * p.E; i += THREADS) logits[i] = __ldcg(p.logits + i);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.E, n4 = n / 4;
+    for (int i = threadIdx.x; i < n4; i += 4 * THREADS) {
+        float4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u * THREADS < n4) v[u] = __ldcg(reinterpret_cast<const float4 *>(p.logits) + i + u * THREADS);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u * THREADS < n4)
+                reinterpret_cast<uint4 *>(keys)[i + u * THREADS] =
+                    make_uint4(logit_key(v[u].x), logit_key(v[u].y), logit_key(v[u].z), logit_key(v[u].w));
+    }
+    if ((int)threadIdx.x < n - 4 * n4) keys[4 * n4 + threadIdx.x] = logit_key(__ldcg(p.logits + 4 * n4 + threadIdx.x));
     ptx::cta_sync();
-    for (int t = warp; t < p.T; t += 4 * WARPS) {
-        const int left = (p.T - t + WARPS - 1) / WARPS;        // tokens of this warp from t on
-        const bool write = blockIdx.x == 0;
-        if (left == 1) choose_experts<1>(p, S, logits, t, WARPS, lane, write);
-        else if (left == 2) choose_experts<2>(p, S, logits, t, WARPS, lane, write);
-        else if (left == 3) choose_experts<3>(p, S, logits, t, WARPS, lane, write);
-        else choose_experts<4>(p, S, logits, t, WARPS, lane, write);
+    const bool write = blockIdx.x == 0;
+    if (p.T <= WARPS) {
+        if (warp < p.T) choose_experts<32>(p, S, keys + warp * p.E, warp, true, write);
+    } else {
+        for (int t0 = warp * 4; t0 < p.T; t0 += WARPS * 4) {
+            const int t = min(t0 + (lane >> 3), p.T - 1);
+            choose_experts<8>(p, S, keys + t * p.E, t, t0 + (lane >> 3) < p.T, write);
+        }
     }
     ptx::cta_sync();
     build_lists<GROUP, THREADS>(p, S, mask);

@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(MXE_THREADS, 1)
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    plan_experts<MXE_GROUP, MXE_THREADS>(p, S, reinterpret_cast<float *>(smem),
+    plan_experts<MXE_GROUP, MXE_THREADS>(p, S, reinterpret_cast<uint32_t *>(smem),
                                          reinterpret_cast<uint32_t *>(smem + MOE_MAX_T * MOE_MAX_E * 4));
     ptx::tc_fence_after();
     m.pp.tmem = S.tmem;
