@@ -3,6 +3,7 @@
 // every check happens on the host before anything is enqueued.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -274,6 +275,31 @@ mmact_status moe_sizes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
     return MMACT_OK;
 }
 
+// Half the rows of a tile of 16-bit weights: the one with which the busiest SM has
+// the least to do, counted in rows x K.  A ring stage takes as long as one of 100
+// rows at least (measured on 32 tokens, 6 of 64 experts of 2048 x 1408: tiles of
+// 128 rows 191 us, 96 rows 216, 64 rows 281), so smaller tiles pay only where whole
+// rounds of the SMs are saved: 16 tokens, 2 of 16 experts of 4096 x 1792, 126 us with
+// tiles of 128 rows, 117 with 112; one token, 2 of 8 experts of the same, 51.8 us with
+// 128, 49.8 with 96; 64 tokens, 2 of 8 ungated experts of 1024 x 768, 47.7 and 43.7 (64
+// rows).  The number of chosen experts is not known here: it is taken as what random
+// choices give and a twentieth.
+int moe_half_rows(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, bool gated, int sms)
+{
+    const double expected = (double)E * (1.0 - std::pow(1.0 - (double)top / (double)E, (double)T));
+    const int64_t chosen = T == 1 ? top : std::min({E, T * top, (int64_t)std::ceil(expected * 1.05)});
+    int best = 64;
+    double least = 0;
+    for (int half = 64; half >= 32; half -= 8) {
+        const int64_t step = gated ? half : 2 * half, up = chosen * ((I + step - 1) / step);
+        const int64_t down = chosen * ((H + 2 * half - 1) / (2 * half));
+        const double cost = (double)std::max(2 * half, 100) *
+                            ((double)((up + sms - 1) / sms) * (double)H + (double)((down + sms - 1) / sms) * (double)I);
+        if (half == 64 || cost < 0.97 * least) least = cost, best = half;
+    }
+    return best;
+}
+
 }  // namespace
 }  // namespace mmact
 
@@ -438,13 +464,7 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
     a.status = c.dev.status;
     a.wait_ns = c.dev.wait_ns;
     L.x_out = out_kind(x_dtype);
-    // Rows of a tile: 128; for 16-bit weights half and a quarter of that when not even three quarters of the
-    // SMs would have an item of the up product, were every choice another expert.
-    a.half_rows = 64;
-    const int64_t groups = std::min(T * top, E);
-    while (!mx && a.half_rows > 16 &&
-           groups * ((a.R1 + 2 * a.half_rows - 1) / (2 * a.half_rows)) < c.dev.sm_count * 3 / 4)
-        a.half_rows /= 2;
+    a.half_rows = mx ? 64 : moe_half_rows(T, H, I, E, top, gated != 0, c.dev.sm_count);
     L.grid = c.dev.sm_count;
     if (!moe_encode(&L.tm1, w1, E * a.R1, H, mx, a.half_rows) || !moe_encode(&L.tm2, w2, E * H, I, mx, a.half_rows))
         return MMACT_ERR_CUDA;

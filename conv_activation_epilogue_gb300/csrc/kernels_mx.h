@@ -76,7 +76,7 @@ cudaError_t launch_gemm_mxfp4_rows(const MxRowsLaunch &L, cudaStream_t stream);
 struct MoeArgs {
     int T, H, I, E, top;         // tokens, model width, experts' width, experts, experts per token
     int R1;                      // rows of one expert's w1: 2 I when gated, else I
-    int half_rows;               // rows of half a tile of weights: 64, 32 or 16
+    int half_rows;               // rows of half a tile of weights: a multiple of 8, 64 at most
     int Hp, Ip;                  // H and I rounded up to whole ring stages (row pitches of the workspace's arrays)
     int gated, normalize, act;
     float alpha;
