@@ -319,8 +319,9 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
         }
         ptx::cluster_sync();
         if (epi && good) {
-            // this CTA's slice of the columns: 16 at a time, or the 2 to 8 it has
-            const int cols = BT / p.split, c0 = rank * cols;
+            // this CTA's slice of the columns that exist: 16 at a time, or the 2 to 8 it has
+            const int rows = min(BT, p.M - tb * BT), even = ((rows + p.split - 1) / p.split + 15) & ~15;
+            const int cols = min(BT / p.split, even), c0 = rank * cols;
             const uint32_t at = base + Cfg::OFF_RING + (uint32_t)(c0 * 128 + q * 32 + lane) * 4u;
             auto slice = [&](auto ch) {
                 constexpr int CH = decltype(ch)::value;
