@@ -42,22 +42,38 @@ constexpr int MOE_MMA_WARPS = 8;
 constexpr int MOE_THREADS = 32 * (2 + MOE_MMA_WARPS);
 constexpr int MOE_GROUP = 32;                                  // tokens of one expert that share a read of its weights
 
-// Two rings.  A stage of weights is at most 128 rows x 128 bytes: 8 stages, about
-// twice what has to be in flight on an SM.  A stage of tokens is the group's
-// tokens over 256 K (four stages of weights), hi and lo, a record for each: 512
-// bytes to a copy, because copies of 128 bytes were measured to keep one warp busy
-// for twice the time of the weights' stage.  A record is 64 bytes longer than a
-// multiple of 128, so that two tokens' 64-byte pieces lie on different banks.
-constexpr int MOE_STAGE_BYTES = 16384, MOE_STAGES = 8, MOE_STAGE_K = 64;
-constexpr int MOE_TOKEN_K = 256, MOE_TOKEN = MOE_TOKEN_K * 2, MOE_RECORD = 2 * MOE_TOKEN + 64;
-constexpr int MOE_SPAN = MOE_TOKEN_K / MOE_STAGE_K;
-constexpr int MOE_TOKENS = MOE_GROUP * MOE_RECORD, MOE_TSTAGES = 2;
-constexpr int MOE_OFF_TOKENS = MOE_STAGES * MOE_STAGE_BYTES;
-constexpr int MOE_SMEM = MOE_OFF_TOKENS + MOE_TSTAGES * MOE_TOKENS + (int)sizeof(MoeShared);
-static_assert(MOE_SMEM <= 232448, "shared memory budget");
-static_assert(2 * MOE_STAGES + 2 * MOE_TSTAGES <= MOE_MAX_BARS, "barriers");
-static_assert(MOE_MAX_T * MOE_MAX_E * 4 <= MOE_OFF_TOKENS, "all logits");
-static_assert(MOE_MAX_E * MOE_MAX_T * MOE_MAX_K / 8 <= MOE_TSTAGES * MOE_TOKENS, "a bit for each expert and slot");
+// Two rings.  A stage of weights is 64 K of a tile, at most 128 rows x 128 bytes.  A
+// stage of tokens is the group's tokens over 256 K (four stages of weights), hi and
+// lo, a record for each: 512 bytes to a copy, because copies of 128 bytes were measured
+// to keep one warp busy for twice the time of the weights' stage.  A record is 64
+// bytes longer than a multiple of 128, so that two tokens' 64-byte pieces lie on
+// different banks.  The tokens' ring has room for as many as the call can send to one
+// expert, and four stages of few: h comes from L2 when the grid barrier opens, and
+// with two stages its latency was most of a small down product's time.  The rest is
+// weights' stages, filled while the CTA waits for the barrier.
+constexpr int MOE_STAGE_K = 64, MOE_TOKEN_K = 256, MOE_SPAN = MOE_TOKEN_K / MOE_STAGE_K;
+constexpr int MOE_TOKEN = MOE_TOKEN_K * 2, MOE_RECORD = 2 * MOE_TOKEN + 64, MOE_MAX_STAGES = 12, MOE_MAX_TSTAGES = 4;
+constexpr int MOE_RINGS = (232448 - (int)sizeof(MoeShared)) & ~15;
+static_assert(2 * MOE_MAX_STAGES + 2 * MOE_MAX_TSTAGES <= MOE_MAX_BARS, "barriers");
+
+// Shared memory of a call: the rings, then MoeShared.
+struct MoeLayout {
+    int stages, tstages, stage_bytes, token_bytes, off_tokens, off_shared;
+    __host__ __device__ MoeLayout(int T, int half_rows)
+    {
+        stage_bytes = half_rows * 256;
+        token_bytes = (T < MOE_GROUP ? (T + 7) & ~7 : MOE_GROUP) * MOE_RECORD;
+        tstages = T <= 16 ? MOE_MAX_TSTAGES : 2;
+        const int room = (MOE_RINGS - tstages * token_bytes) / stage_bytes;
+        stages = room < MOE_MAX_STAGES ? room : MOE_MAX_STAGES;
+        off_tokens = stages * stage_bytes;
+        off_shared = off_tokens + tstages * token_bytes;
+    }
+};
+// all logits in the weights' ring, a bit for each expert and slot in the tokens' ring
+static_assert(MOE_MAX_T * MOE_MAX_E * 4 <= 8 * 16384 && 8 * 16384 <= MOE_RINGS - 2 * MOE_GROUP * MOE_RECORD, "logits");
+static_assert(MOE_MAX_E * MOE_MAX_T * MOE_MAX_K / 8 <= 2 * MOE_GROUP * MOE_RECORD &&
+              MOE_MAX_E * MOE_MAX_K <= 2 * 8 * MOE_RECORD, "bits");
 
 // ------------------------------------------------------------------ helpers --
 template <bool BF16>
@@ -158,60 +174,121 @@ struct MoePipe {
     Pipe pp;                         // weights: full0, empty0
     uint32_t tfull0, tempty0;        // tokens
     uint32_t ring, tokens;           // shared addresses
+    uint32_t stages, tstages, stage_bytes, token_bytes;
 };
 
-// Stages used so far by a role.
-struct MoeUse {
-    uint32_t w, t;
+// A role's place in a ring.
+struct MoePlace {
+    uint32_t slot, phase;
+    __device__ __forceinline__ void next(uint32_t stages)
+    {
+        if (++slot == stages) slot = 0, phase ^= 1u;
+    }
 };
 
-// One warp's rows of an item over all of K: the two units of 32 K of each stage,
-// 8 values to a lane.  SPLITW: fp16 weights as two bf16 halves.
-template <bool BF, int NT, bool LO, bool SPLITW>
-__device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
-                                         MoeUse use)
+// What a warp multiplies in one stage: two units of 32 K, 8 values to a lane of its
+// two rows and of its tokens.
+template <int NT, bool LO>
+struct MoeFragments {
+    uint4 a[2], b[2];
+    MoeTokens<NT, LO> x[2];
+};
+
+// A warp's walk over the stages of an item: `w` and `t` are the stage that is
+// fetched next, `wr` and `tr` the one that is given back next.
+struct MoeWalk {
+    MoePlace w, t, wr, tr;
+};
+
+template <int NT, bool LO>
+__device__ __forceinline__ bool fetch(MoeFragments<NT, LO> &f, const MoePipe &m, const MoeItem &it, MoeWalk &walk, int s, int stages)
 {
     const int lane = threadIdx.x & 31;
     const uint32_t sw = (uint32_t)(lane >> 2), t4 = (uint32_t)(lane & 3);   // the 128-byte swizzle: chunk ^ (row & 7)
     const uint32_t c0 = (t4 ^ sw) << 4, c1 = ((4u + t4) ^ sw) << 4;
-    float low[LO ? NT : 1][4] = {};
-#pragma unroll 1
-    for (int s = 0; s < pr.stages; ++s, ++use.w) {
-        const uint32_t slot = use.w % MOE_STAGES, row = m.ring + slot * MOE_STAGE_BYTES + it.row;
-        const uint32_t part = (uint32_t)s % MOE_SPAN, tslot = use.t % MOE_TSTAGES;
-        const uint32_t tok = m.tokens + tslot * MOE_TOKENS + sw * MOE_RECORD + part * (MOE_STAGE_K * 2u) + t4 * 16u;
-        if (part == 0 && !mx_warp_wait(m.pp, m.tfull0 + 8 * tslot, (use.t / MOE_TSTAGES) & 1u)) return false;
-        if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * slot, (use.w / MOE_STAGES) & 1u)) return false;
+    const uint32_t part = (uint32_t)s % MOE_SPAN;
+    const uint32_t row = m.ring + walk.w.slot * m.stage_bytes + it.row;
+    const uint32_t tok = m.tokens + walk.t.slot * m.token_bytes + sw * MOE_RECORD + part * (MOE_STAGE_K * 2u) + t4 * 16u;
+    if (part == 0 && !mx_warp_wait(m.pp, m.tfull0 + 8 * walk.t.slot, walk.t.phase)) return false;
+    if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * walk.w.slot, walk.w.phase)) return false;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint4 fa = ptx::ld_shared_v4(row + (u ? c1 : c0)), fb = ptx::ld_shared_v4(row + it.upper + (u ? c1 : c0));
-            MoeTokens<NT, LO> x;
-            load_tokens<NT, LO>(x, tok + u * 64u);
-            uint32_t a[4] = {fa.x, fa.y, fa.z, fa.w}, b[4] = {fb.x, fb.y, fb.z, fb.w};
-            if constexpr (SPLITW) {
-                // the weights' lo halves meet the tokens' hi halves only
-                uint32_t al[4], bl[4];
+    for (int u = 0; u < 2; ++u) {
+        f.a[u] = ptx::ld_shared_v4(row + (u ? c1 : c0));
+        f.b[u] = ptx::ld_shared_v4(row + it.upper + (u ? c1 : c0));
+        load_tokens<NT, LO>(f.x[u], tok + u * 64u);
+    }
+    walk.w.next(m.stages);
+    if (part == MOE_SPAN - 1 || s == stages - 1) walk.t.next(m.tstages);
+    return true;
+}
+
+// SPLITW: fp16 weights as two bf16 halves, whose lo halves meet the tokens' hi halves only.
+template <bool BF, int NT, bool LO, bool SPLITW>
+__device__ __forceinline__ void multiply(float (&acc)[NT][4], float (&low)[LO ? NT : 1][4], const MoeFragments<NT, LO> &f)
+{
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 va = unpack2<OUT_F16>(a[i]), vb = unpack2<OUT_F16>(b[i]);
-                    split_pair(va.x, va.y, a[i], al[i]);
-                    split_pair(vb.x, vb.y, b[i], bl[i]);
-                }
+    for (int u = 0; u < 2; ++u) {
+        uint32_t a[4] = {f.a[u].x, f.a[u].y, f.a[u].z, f.a[u].w}, b[4] = {f.b[u].x, f.b[u].y, f.b[u].z, f.b[u].w};
+        if constexpr (SPLITW) {
+            uint32_t al[4], bl[4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_16816<true>(low[n], al[0], bl[0], al[1], bl[1], x.h[n].x, x.h[n].y);
-                    mma_16816<true>(low[n], al[2], bl[2], al[3], bl[3], x.h[n].z, x.h[n].w);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float2 va = unpack2<OUT_F16>(a[i]), vb = unpack2<OUT_F16>(b[i]);
+                split_pair(va.x, va.y, a[i], al[i]);
+                split_pair(vb.x, vb.y, b[i], bl[i]);
             }
-            piece_mma<BF || SPLITW, NT, LO>(acc, low, a, b, x);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_16816<true>(low[n], al[0], bl[0], al[1], bl[1], f.x[u].h[n].x, f.x[u].h[n].y);
+                mma_16816<true>(low[n], al[2], bl[2], al[3], bl[3], f.x[u].h[n].z, f.x[u].h[n].w);
+            }
         }
-        const bool last = part == MOE_SPAN - 1 || s == pr.stages - 1;   // of its stage of tokens
-        __syncwarp();
-        if (lane == 0) {
-            ptx::mbar_arrive(m.pp.empty0 + 8 * slot);
-            if (last) ptx::mbar_arrive(m.tempty0 + 8 * tslot);
+        piece_mma<BF || SPLITW, NT, LO>(acc, low, a, b, f.x[u]);
+    }
+}
+
+__device__ __forceinline__ void give_back(const MoePipe &m, MoeWalk &walk, int s, int stages)
+{
+    const bool last = s % MOE_SPAN == MOE_SPAN - 1 || s == stages - 1;      // of its stage of tokens
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        ptx::mbar_arrive(m.pp.empty0 + 8 * walk.wr.slot);
+        if (last) ptx::mbar_arrive(m.tempty0 + 8 * walk.tr.slot);
+    }
+    walk.wr.next(m.stages);
+    if (last) walk.tr.next(m.tstages);
+}
+
+// One warp's rows of an item over all of K.  With up to 8 tokens a stage's fragments
+// are loaded while the one before is multiplied: one token, 2 of 8 experts of 4096 x
+// 1792, 49.8 us without, 47.7 with it.  With 16 tokens the second set of fragments costs
+// more than it hides: 64 tokens, 8 of 64 experts of the same, 472 us without, 489 with.
+template <bool BF, int NT, bool LO, bool SPLITW>
+__device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
+                                         MoeWalk &walk)
+{
+    float low[LO ? NT : 1][4] = {};
+    MoeFragments<NT, LO> f;
+    if constexpr (NT == 1) {
+        MoeFragments<NT, LO> g;
+        if (!fetch<NT, LO>(f, m, it, walk, 0, pr.stages)) return false;
+#pragma unroll 1
+        for (int s = 0; s < pr.stages; s += 2) {
+            if (s + 1 < pr.stages && !fetch<NT, LO>(g, m, it, walk, s + 1, pr.stages)) return false;
+            multiply<BF, NT, LO, SPLITW>(acc, low, f);
+            give_back(m, walk, s, pr.stages);
+            if (s + 1 == pr.stages) break;
+            if (s + 2 < pr.stages && !fetch<NT, LO>(f, m, it, walk, s + 2, pr.stages)) return false;
+            multiply<BF, NT, LO, SPLITW>(acc, low, g);
+            give_back(m, walk, s + 1, pr.stages);
         }
-        use.t += last ? 1u : 0u;
+    } else {
+#pragma unroll 1
+        for (int s = 0; s < pr.stages; ++s) {
+            if (!fetch<NT, LO>(f, m, it, walk, s, pr.stages)) return false;
+            multiply<BF, NT, LO, SPLITW>(acc, low, f);
+            give_back(m, walk, s, pr.stages);
+        }
     }
     if constexpr (LO)
 #pragma unroll
@@ -224,7 +301,7 @@ __device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, 
 // One item of the up (DOWN = false) or down product by one warp, stores included.
 template <int XT, bool DOWN, int NT>
 __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, const MoePipe &m, const MoeProduct &pr,
-                                         const MoeUse &use, int ai, int tile)
+                                         MoeWalk &walk, int ai, int tile)
 {
     const int w = (int)(threadIdx.x >> 5) - 1, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int e = S.act[ai], first = S.first[ai], cnt = S.first[ai + 1] - first;
@@ -234,7 +311,7 @@ __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, c
     it.row = (uint32_t)(8 * w + g) * 128u;
     it.upper = (uint32_t)p.half_rows * 128u;
     float acc[NT][4] = {};
-    if (!item_mma<XT == OUT_BF16, NT, DOWN, DOWN && XT == OUT_F16>(acc, m, pr, it, use)) return false;
+    if (!item_mma<XT == OUT_BF16, NT, DOWN, DOWN && XT == OUT_F16>(acc, m, pr, it, walk)) return false;
 
     // acc[n][0..1]: the lower row, tokens n * 8 + 2 t4 and the next; acc[n][2..3]: the upper row
     const bool gated = pr.pairs;
@@ -275,14 +352,14 @@ __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, c
 
 template <int XT, bool DOWN>
 __device__ __forceinline__ bool mma_phase(const MoeArgs &p, const MoeShared &S, const MoePipe &m, const MoeProduct &pr,
-                                          MoeUse &use)
+                                          MoeWalk &walk)
 {
     const int n = S.nact * pr.tiles;
-    for (int i = blockIdx.x; i < n; i += gridDim.x, use.w += (uint32_t)pr.stages, use.t += (uint32_t)pr.tstages) {
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int ai = i / pr.tiles, tile = i - ai * pr.tiles, cnt = S.first[ai + 1] - S.first[ai];
-        const bool ok = cnt <= 8    ? run_item<XT, DOWN, 1>(p, S, m, pr, use, ai, tile)
-                        : cnt <= 16 ? run_item<XT, DOWN, 2>(p, S, m, pr, use, ai, tile)
-                                    : run_item<XT, DOWN, 4>(p, S, m, pr, use, ai, tile);
+        const bool ok = cnt <= 8    ? run_item<XT, DOWN, 1>(p, S, m, pr, walk, ai, tile)
+                        : cnt <= 16 ? run_item<XT, DOWN, 2>(p, S, m, pr, walk, ai, tile)
+                                    : run_item<XT, DOWN, 4>(p, S, m, pr, walk, ai, tile);
         if (!ok) return false;
     }
     return true;
@@ -290,7 +367,7 @@ __device__ __forceinline__ bool mma_phase(const MoeArgs &p, const MoeShared &S, 
 
 // ------------------------------------------------------------------- kernel --
 __device__ __forceinline__ bool produce(const CUtensorMap *map, const MoeArgs &p, const MoeShared &S, const MoePipe &m,
-                                        const MoeProduct &pr, uint32_t &use, uint64_t pol)
+                                        const MoeProduct &pr, MoePlace &to, uint64_t pol)
 {
     const int n = S.nact * pr.tiles;
     const uint32_t box = (uint32_t)p.half_rows * 128u;
@@ -298,12 +375,12 @@ __device__ __forceinline__ bool produce(const CUtensorMap *map, const MoeArgs &p
         const int ai = i / pr.tiles, tile = i - ai * pr.tiles, row = S.act[ai] * pr.rows + tile * pr.step;
         // the upper half of the last tile may have no rows (its products are not stored either)
         const bool both = pr.pairs || tile * pr.step + p.half_rows < pr.limit;
-        for (int s = 0; s < pr.stages; ++s, ++use) {
-            const uint32_t slot = use % MOE_STAGES, full = m.pp.full0 + 8 * slot, to = m.ring + slot * MOE_STAGE_BYTES;
-            if (!mx_warp_wait(m.pp, m.pp.empty0 + 8 * slot, ((use / MOE_STAGES) & 1u) ^ 1u)) return false;
+        for (int s = 0; s < pr.stages; ++s, to.next(m.stages)) {
+            const uint32_t full = m.pp.full0 + 8 * to.slot, at = m.ring + to.slot * m.stage_bytes;
+            if (!mx_warp_wait(m.pp, m.pp.empty0 + 8 * to.slot, to.phase ^ 1u)) return false;
             elected_expect_tx(full, both ? 2u * box : box);
-            elected_load_2d(to, map, full, s * 64, row, pol);
-            if (both) elected_load_2d(to + box, map, full, s * 64, row + pr.half, pol);
+            elected_load_2d(at, map, full, s * MOE_STAGE_K, row, pol);
+            if (both) elected_load_2d(at + box, map, full, s * MOE_STAGE_K, row + pr.half, pol);
         }
     }
     return true;
@@ -312,7 +389,7 @@ __device__ __forceinline__ bool produce(const CUtensorMap *map, const MoeArgs &p
 // The tokens of every item, in the weights' order: lane c copies token c's pieces.
 template <bool DOWN>
 __device__ __forceinline__ bool produce_tokens(const MoeArgs &p, const MoeShared &S, const MoePipe &m, const MoeProduct &pr,
-                                               uint32_t &use)
+                                               MoePlace &to)
 {
     const int lane = threadIdx.x & 31, n = S.nact * pr.tiles;
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
@@ -320,15 +397,15 @@ __device__ __forceinline__ bool produce_tokens(const MoeArgs &p, const MoeShared
         const int64_t slot_of = lane < cnt ? S.slot[first + lane] : 0;
         const int64_t from = DOWN ? slot_of * p.Ip : slot_of / p.top * p.Hp;
         const uint16_t *hi = (DOWN ? p.h_hi : p.x_pad) + from, *lo = p.h_lo + from;
-        for (int s = 0; s < pr.tstages; ++s, ++use) {
-            const uint32_t slot = use % MOE_TSTAGES, full = m.tfull0 + 8 * slot;
-            const uint32_t to = m.tokens + slot * MOE_TOKENS + (uint32_t)lane * MOE_RECORD;
-            if (!mx_warp_wait(m.pp, m.tempty0 + 8 * slot, ((use / MOE_TSTAGES) & 1u) ^ 1u)) return false;
+        for (int s = 0; s < pr.tstages; ++s, to.next(m.tstages)) {
+            const uint32_t full = m.tfull0 + 8 * to.slot;
+            const uint32_t at = m.tokens + to.slot * m.token_bytes + (uint32_t)lane * MOE_RECORD;
+            if (!mx_warp_wait(m.pp, m.tempty0 + 8 * to.slot, to.phase ^ 1u)) return false;
             elected_expect_tx(full, (uint32_t)cnt * MOE_TOKEN * (DOWN ? 2u : 1u));
             __syncwarp();
             if (lane < cnt) {
-                bulk_load(to, hi + s * MOE_TOKEN_K, MOE_TOKEN, full);
-                if constexpr (DOWN) bulk_load(to + MOE_TOKEN, lo + s * MOE_TOKEN_K, MOE_TOKEN, full);
+                bulk_load(at, hi + s * MOE_TOKEN_K, MOE_TOKEN, full);
+                if constexpr (DOWN) bulk_load(at + MOE_TOKEN, lo + s * MOE_TOKEN_K, MOE_TOKEN, full);
             }
             __syncwarp();
         }
@@ -336,22 +413,36 @@ __device__ __forceinline__ bool produce_tokens(const MoeArgs &p, const MoeShared
     return true;
 }
 
+// Every copy has landed before the CTA exits: the last one of each slot, from the
+// oldest on (before the first round, a slot of an earlier phase has no copy and its
+// barrier's phase before the first counts as complete).
+__device__ __forceinline__ void drain(const Pipe &pp, uint32_t full0, MoePlace to, uint32_t stages)
+{
+    for (uint32_t i = 0; i < stages; ++i, to.next(stages))
+        ptx::mbar_wait_bounded(full0 + 8 * to.slot, to.phase ^ 1u, DRAIN_NS, nullptr);
+}
+
 template <int XT>
 __global__ void __launch_bounds__(MOE_THREADS, 1)
     moe_experts_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, const MoeArgs p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    MoeShared &S = *reinterpret_cast<MoeShared *>(smem + MOE_SMEM - sizeof(MoeShared));
+    const MoeLayout layout(p.T, p.half_rows);
+    MoeShared &S = *reinterpret_cast<MoeShared *>(smem + layout.off_shared);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     ptx::griddep_launch_dependents();
     const int active = p.half_rows / 8;                        // product warps that have rows
     MoePipe m;
     m.ring = ptx::smem_addr(smem);
-    m.tokens = m.ring + MOE_OFF_TOKENS;
+    m.tokens = m.ring + (uint32_t)layout.off_tokens;
+    m.stages = (uint32_t)layout.stages;
+    m.tstages = (uint32_t)layout.tstages;
+    m.stage_bytes = (uint32_t)layout.stage_bytes;
+    m.token_bytes = (uint32_t)layout.token_bytes;
     m.pp.full0 = ptx::smem_addr(S.bar);
-    m.pp.empty0 = m.pp.full0 + 8 * MOE_STAGES;
-    m.tfull0 = m.pp.empty0 + 8 * MOE_STAGES;
-    m.tempty0 = m.tfull0 + 8 * MOE_TSTAGES;
+    m.pp.empty0 = m.pp.full0 + 8 * m.stages;
+    m.tfull0 = m.pp.empty0 + 8 * m.stages;
+    m.tempty0 = m.tfull0 + 8 * m.tstages;
     m.pp.abort = reinterpret_cast<volatile uint32_t *>(&S.abort_flag);
     m.pp.status = p.status;
     m.pp.wait_ns = p.wait_ns;
@@ -360,11 +451,11 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         if (!aligned) atomicOr(p.status, ST_SMEM_ALIGN);
         ptx::prefetch_tensormap(&tm1);
         ptx::prefetch_tensormap(&tm2);
-        for (int s = 0; s < MOE_STAGES; ++s) {
+        for (uint32_t s = 0; s < m.stages; ++s) {
             ptx::mbar_init(m.pp.full0 + 8 * s, 1);
             ptx::mbar_init(m.pp.empty0 + 8 * s, (uint32_t)active);
         }
-        for (int s = 0; s < MOE_TSTAGES; ++s) {
+        for (uint32_t s = 0; s < m.tstages; ++s) {
             ptx::mbar_init(m.tfull0 + 8 * s, 1);
             ptx::mbar_init(m.tempty0 + 8 * s, (uint32_t)active);
         }
@@ -373,38 +464,35 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     }
     ptx::griddep_wait();                                       // the router's logits
     plan_experts<MOE_GROUP, MOE_THREADS>(p, S, reinterpret_cast<uint32_t *>(smem),
-                                         reinterpret_cast<uint32_t *>(smem + MOE_OFF_TOKENS));
+                                         reinterpret_cast<uint32_t *>(smem + layout.off_tokens));
 
     const MoeProduct up = up_product(p, MOE_STAGE_K, MOE_TOKEN_K), down = down_product(p, MOE_STAGE_K, MOE_TOKEN_K);
     bool ok = aligned;
     if (warp == 0) {
-        uint32_t use = 0;
+        MoePlace to = {0, 0};
         const uint64_t pol = ptx::createpolicy_evict_first();  // weights are read once
-        ok = ok && produce(&tm1, p, S, m, up, use, pol) && produce(&tm2, p, S, m, down, use, pol);
+        ok = ok && produce(&tm1, p, S, m, up, to, pol) && produce(&tm2, p, S, m, down, to, pol);
         if (!ok && lane == 0) pipe_fail(m.pp);
-        // every copy has landed before the CTA exits
-        for (uint32_t u = use > (uint32_t)MOE_STAGES ? use - MOE_STAGES : 0; u < use; ++u)
-            ptx::mbar_wait_bounded(m.pp.full0 + 8 * (u % MOE_STAGES), (u / MOE_STAGES) & 1u, DRAIN_NS, nullptr);
+        drain(m.pp, m.pp.full0, to, m.stages);
     } else if (warp == 1 + MOE_MMA_WARPS) {
-        uint32_t use = 0;
-        ok = ok && produce_tokens<false>(p, S, m, up, use);
+        MoePlace to = {0, 0};
+        ok = ok && produce_tokens<false>(p, S, m, up, to);
         // every h is written before any is read
         if (ok) ok = __all_sync(0xffffffffu, lane != 0 || grid_wait(m.pp, p.counters)) != 0;
         fence_proxy_async_all();
-        ok = ok && produce_tokens<true>(p, S, m, down, use);
+        ok = ok && produce_tokens<true>(p, S, m, down, to);
         if (!ok && lane == 0) pipe_fail(m.pp);
-        for (uint32_t u = use > (uint32_t)MOE_TSTAGES ? use - MOE_TSTAGES : 0; u < use; ++u)
-            ptx::mbar_wait_bounded(m.tfull0 + 8 * (u % MOE_TSTAGES), (u / MOE_TSTAGES) & 1u, DRAIN_NS, nullptr);
+        drain(m.pp, m.tfull0, to, m.tstages);
     } else {
-        MoeUse use = {0, 0};
-        if (ok && warp <= active) ok = mma_phase<XT, false>(p, S, m, up, use);
+        MoeWalk walk = {};
+        if (ok && warp <= active) ok = mma_phase<XT, false>(p, S, m, up, walk);
         // this CTA's part of h is written
         fence_proxy_async_all();
         __syncwarp();
         asm volatile("barrier.sync 1, %0;" ::"n"(32 * MOE_MMA_WARPS) : "memory");
         if (ok && threadIdx.x == 32) grid_arrive(p.counters);
         __syncwarp();
-        if (ok && warp <= active) ok = mma_phase<XT, true>(p, S, m, down, use);
+        if (ok && warp <= active) ok = mma_phase<XT, true>(p, S, m, down, walk);
         if (!ok && lane == 0) pipe_fail(m.pp);
     }
     __syncwarp();
@@ -419,14 +507,15 @@ static cudaError_t launch_t(const MoeLaunch &L, cudaStream_t stream)
     const cudaError_t e = launch_k(moe_router_kernel<XT>, dim3((unsigned)(a.E * groups + a.T * ((a.Hp + 1023) / 1024))),
                                    dim3(MOE_ROUTER_THREADS), 0, stream, a, groups);
     if (e != cudaSuccess) return e;
-    return launch_cooperative(moe_experts_kernel<XT>, L.grid, MOE_THREADS, MOE_SMEM, stream, L.tm1, L.tm2, a);
+    return launch_cooperative(moe_experts_kernel<XT>, L.grid, MOE_THREADS,
+                              (size_t)MoeLayout(a.T, a.half_rows).off_shared + sizeof(MoeShared), stream, L.tm1, L.tm2, a);
 }
 
 cudaError_t setup_moe_kernels()
 {
     const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    const cudaError_t e = cudaFuncSetAttribute(moe_experts_kernel<OUT_BF16>, attr, MOE_SMEM);
-    return e == cudaSuccess ? cudaFuncSetAttribute(moe_experts_kernel<OUT_F16>, attr, MOE_SMEM) : e;
+    const cudaError_t e = cudaFuncSetAttribute(moe_experts_kernel<OUT_BF16>, attr, MOE_RINGS + (int)sizeof(MoeShared));
+    return e == cudaSuccess ? cudaFuncSetAttribute(moe_experts_kernel<OUT_F16>, attr, MOE_RINGS + (int)sizeof(MoeShared)) : e;
 }
 
 cudaError_t launch_moe(const MoeLaunch &L, cudaStream_t stream)

