@@ -208,6 +208,76 @@ def test_results_repeat_and_graphs_replay():
     check(L, out, 4, "bf16")
 
 
+@pytest.mark.parametrize("dtype,weights", TYPES)
+@pytest.mark.parametrize("T,H,I,E,top,gated", [(32, 4096, 1792, 16, 4, True), (64, 2048, 2056, 12, 3, False),
+                                               (1, 2048, 1024, 64, 8, True)])
+def test_large_layers_under_load(dtype, weights, T, H, I, E, top, gated):
+    """Rings that turn over hundreds of times, calls back to back; the plain form in fp64 on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    x = torch.randint(-16, 17, (T, H), generator=g, device="cuda").double() / 8
+    router = torch.randint(-4, 5, (E, H), generator=g, device="cuda").double() / 64
+    up = 2 * I if gated else I
+    t = TORCH[dtype]
+    w, dev, scales = {}, {}, {}
+    for name, rows, k in (("w1", up, H), ("w2", H, I)):
+        v = torch.randn((E * rows, k), generator=g, device="cuda") * k ** -0.5
+        if weights == "mxfp4":
+            nc, ns = mmact.mmact_mxfp4_size(E * rows, k)
+            dev[name] = torch.empty((E * rows, nc // (E * rows)), dtype=torch.uint8, device="cuda")
+            scales[name] = torch.empty(ns, dtype=torch.uint8, device="cuda")
+            mmact.mmact_quantize_mxfp4(v, dev[name], scales[name])
+            mmact.mmact_dequantize_mxfp4(dev[name], scales[name], v)
+        else:
+            v = v.to(t)
+            dev[name], scales[name] = v.view(E, rows, k), None
+        w[name] = v.view(E, rows, k)
+    y = torch.empty((T, H), dtype=t, device="cuda")
+    experts = torch.empty((T, top), dtype=torch.int32, device="cuda")
+    probs = torch.empty((T, top), dtype=torch.float32, device="cuda")
+    work = torch.full((mmact.mmact_moe_workspace_bytes(T, H, I, E, top),), 0xFF, dtype=torch.uint8, device="cuda")
+    xd, rd = x.to(t), router.to(t)
+    results = []
+    for _ in range(12):
+        mmact.mmact_moe(xd, rd, dev["w1"], dev["w2"], y, experts, probs, work, "silu", gated=gated,
+                        w1_scales=scales["w1"], w2_scales=scales["w2"])
+        results.append(y.clone())
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+    assert all(torch.equal(r, results[0]) for r in results)
+
+    logits = x @ router.T
+    ids = torch.sort(logits, dim=1, descending=True, stable=True).indices[:, :top]
+    assert torch.equal(experts.long(), ids)
+    ex = torch.exp(logits - logits.max(dim=1, keepdim=True).values)
+    chosen = torch.gather(ex, 1, ids)
+    p = chosen / chosen.sum(dim=1, keepdim=True)
+    dl = ref.sum_error(H + 1) * (x.abs() @ router.abs().T).max(dim=1).values
+    dp = 2 * dl + (E + 8) * 2.0 ** -23
+    assert bool(((probs.double() - p).abs() <= dp[:, None] * p).all())
+    want, bound = torch.zeros_like(x), torch.zeros_like(x)
+    for e in range(E):                                   # the bounds of mx_reference.moe
+        at, j = torch.nonzero(ids == e, as_tuple=True)
+        if at.numel() == 0:
+            continue
+        w1, w2 = w["w1"][e].double(), w["w2"][e].double()
+        z = x[at] @ w1.T
+        dz = ref.sum_error(H + 1) * (x[at].abs() @ w1.abs().T)
+        a = torch.nn.functional.silu(z[:, :I])
+        da = ref.SLOPE * dz[:, :I] + torch.from_numpy(np.asarray(ref.act_error(z[:, :I].cpu().numpy(), "silu"))).cuda()
+        if gated:
+            h, dh = a * z[:, I:], da * z[:, I:].abs() + (a.abs() + da) * dz[:, I:]
+        else:
+            h, dh = a, da
+        dh = dh + (2.0 ** -23 + 2.0 ** -16) * h.abs()
+        o, mag = h @ w2.T, h.abs() @ w2.abs().T
+        do = dh @ w2.abs().T + (ref.sum_error(3 * (I + 1)) + 2.0 ** -16) * mag
+        want[at] += p[at, j, None] * o
+        bound[at] += p[at, j, None] * (do + (dp[at, None] + (top + 2) * 2.0 ** -23) * (o.abs() + do))
+    want, bound = want.cpu().numpy(), bound.cpu().numpy()
+    err = np.abs(host64(y) - want)
+    lim = bound + ref.ulp(np.abs(want) + bound, dtype)
+    assert np.all(err <= lim), float((err / lim).max())
+
+
 def test_no_tokens_and_refusals():
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     work = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
