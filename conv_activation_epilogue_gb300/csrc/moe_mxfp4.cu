@@ -4,7 +4,7 @@
 // Turning 4-bit weights into 16-bit values is more work than an SM can do in the
 // time that it reads them (on mma.sync, with the weights widened in registers, 16
 // tokens through 4 of 128 experts of 4096 x 2048 took 265 us where the bytes take
-// 102; this form takes 146).  So the weights go to the tensor core as they
+// 102; this form takes 121).  So the weights go to the tensor core as they
 // are, and the tokens take their form: a value is written as a sum of eight MXFP4
 // terms, the first the value rounded to the 4-bit grid, each next one the
 // rounding of what is left, every term with a scale of its own for 32 values (the
@@ -71,6 +71,37 @@ __device__ __forceinline__ int64_t term_scale_at(int64_t token, int stages, int 
     return (token * stages + (blk >> 3)) * MXE_ATOM_SCALES + term * 8 + (blk & 7);
 }
 
+// Eight values r of `token` from K = k on, a multiple of 8, as their terms; four
+// neighbouring lanes share a block.  (A lane to each value, with a warp maximum and
+// three exchanges a term, made the epilogue what a layer with many tokens an expert
+// waited for: 64 tokens, 4 of 4 experts of 2048 x 2048, 117 us, 60 so.  Unrolled, the
+// terms cost one token 4 us more when the code is not in the SM's cache.)
+__device__ __forceinline__ void put_terms(float (&r)[8], uint8_t *codes, uint8_t *scales, int64_t token, int stages, int k,
+                                          bool valid)
+{
+#pragma unroll 1
+    for (int j = 0; j < MXE_TERMS; ++j) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(r[i]) & 0x7fffffffu);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const uint32_t b = term_scale_byte(amax);
+        const float inv = mx_inv_scale(b == 255u ? 0u : b), x = mx_scale(b);
+        float v[8], q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r[i] * inv;
+        const uint32_t c = b == 255u ? 0u : mx_encode8(v);
+        mx_decode8(c, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = b == 255u ? 0.0f : r[i] - q[i] * x;   // exact
+        if (valid) {
+            *reinterpret_cast<uint32_t *>(codes + term_codes_at(token, stages, k >> 5, j) + (threadIdx.x & 3) * 4) = c;
+            if ((threadIdx.x & 3) == 0) scales[term_scale_at(token, stages, k >> 5, j)] = (uint8_t)b;
+        }
+    }
+}
+
 // ------------------------------------------------------------------- router --
 // The CTAs past the logits' prepare what the experts kernel reads: its counters,
 // the terms of x up to a whole stage (zeros past H), and zero terms past h's
@@ -98,27 +129,7 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_mxfp4_router_kernel(co
         r[2 * i] = f.x;
         r[2 * i + 1] = f.y;
     }
-#pragma unroll
-    for (int j = 0; j < MXE_TERMS; ++j) {
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(r[i]) & 0x7fffffffu);
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const uint32_t b = term_scale_byte(amax);
-        const float inv = mx_inv_scale(b == 255u ? 0u : b), x = mx_scale(b);
-        float v[8], q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = r[i] * inv;
-        const uint32_t c = b == 255u ? 0u : mx_encode8(v);
-        mx_decode8(c, q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = b == 255u ? 0.0f : r[i] - q[i] * x;   // exact
-        if (k < p.Hp) {
-            *reinterpret_cast<uint32_t *>(p.x_codes + term_codes_at(t, stages, k >> 5, j) + (threadIdx.x & 3) * 4) = c;
-            if ((threadIdx.x & 3) == 0) p.x_scales[term_scale_at(t, stages, k >> 5, j)] = (uint8_t)b;
-        }
-    }
+    put_terms(r, p.x_codes, p.x_scales, t, stages, k, k < p.Hp);
     fence_proxy_async_all();                                   // bulk copies read the terms
     if (at != t * chunks) return;
     const int blocks = (p.I + 31) / 32, hstages = p.Ip / MXE_K, pad = hstages * 8 - blocks;
@@ -323,32 +334,30 @@ __device__ __forceinline__ bool mxe_epilogue(const MoeArgs &p, const MoeShared &
         ++item;
         if constexpr (!DOWN) {
             mxe_epilogue_sync();                               // a gate row's up row is another warp's
-            const int blk = (tile * pr.step + q * 32) >> 5, hstages = p.Ip / MXE_K;
-            if ((!pr.pairs || q < 2) && blk * 32 < p.I) {
-#pragma unroll 1
-                for (int c = 0; c < cnt; ++c) {
-                    float h = act_mx(p.act, ex[c * 128 + row], p.alpha);
-                    if (pr.pairs) h *= ex[c * 128 + row + 64];
-                    if (!in) h = 0.0f;
-                    const int64_t slot = S.slot[first + c];
-                    // the block's eight terms: a lane for each value
+            // four lanes to a block of a token, eight rows each: with 64 gate rows and 16 tokens one for everyone
+            const int blocks = pr.pairs ? 2 : 4, units = cnt * blocks, hstages = p.Ip / MXE_K;
+            for (int u0 = q * 8; u0 < units; u0 += 32) {
+                const int u = min(u0 + (lane >> 2), units - 1), c = u / blocks, at = (u - c * blocks) * 32 + (lane & 3) * 8;
+                const int first_row = tile * pr.step + at;
+                float h[8];
 #pragma unroll
-                    for (int j = 0; j < MXE_TERMS; ++j) {
-                        const uint32_t b = term_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu));
-                        const float v[8] = {h * mx_inv_scale(b == 255u ? 0u : b), 0, 0, 0, 0, 0, 0, 0};
-                        const uint32_t code = b == 255u ? 0u : mx_encode8(v);
-                        float back[8];
-                        mx_decode8(code, back);
-                        h = b == 255u ? 0.0f : h - back[0] * mx_scale(b);
-                        uint32_t w = code << (4 * (lane & 7));
-                        w |= __shfl_xor_sync(0xffffffffu, w, 1);
-                        w |= __shfl_xor_sync(0xffffffffu, w, 2);
-                        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-                        if ((lane & 7) == 0)
-                            *reinterpret_cast<uint32_t *>(p.h_codes + term_codes_at(slot, hstages, blk, j) + (lane >> 3) * 4) = w;
-                        if (lane == 0) p.h_scales[term_scale_at(slot, hstages, blk, j)] = (uint8_t)b;
-                    }
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 g = *reinterpret_cast<const float4 *>(ex + c * 128 + at + i);
+                    h[i] = g.x, h[i + 1] = g.y, h[i + 2] = g.z, h[i + 3] = g.w;
                 }
+                act_mx_all(p.act, h, p.alpha);
+                if (pr.pairs)
+#pragma unroll
+                    for (int i = 0; i < 8; i += 4) {
+                        const float4 g = *reinterpret_cast<const float4 *>(ex + c * 128 + 64 + at + i);
+                        h[i] *= g.x, h[i + 1] *= g.y, h[i + 2] *= g.z, h[i + 3] *= g.w;
+                    }
+                if (first_row >= pr.limit)                     // I is a multiple of 8
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = 0.0f;
+                __syncwarp();
+                put_terms(h, p.h_codes, p.h_scales, S.slot[first + c], hstages, first_row,
+                          u0 + (lane >> 2) < units && (first_row & ~31) < p.I);
             }
             __syncwarp();
         }

@@ -547,8 +547,8 @@ mmact_status mmact_gemm_mxfp4(const void *a_codes, const void *a_scales, const v
 /*
  * C = act(q(x) x W^T + bias): x [M, K] row-major in x_dtype (F16, BF16 or F32)
  * is quantised to MXFP4 on the way in, W [N, K] is held in MXFP4.  The same
- * result as mmact_quantize_mxfp4 into `workspace` and mmact_gemm_mxfp4 (up to
- * 32 rows are quantised inside the product's kernel instead).
+ * result as mmact_quantize_mxfp4 into `workspace` and mmact_gemm_mxfp4 (a few
+ * rows are quantised inside the product's kernel instead).
  *   workspace  at least mmact_linear_mxfp4_workspace_bytes, 16-byte aligned,
  *              contents ignored and undefined afterwards; calls that may
  *              overlap on the GPU need one each.
@@ -588,9 +588,12 @@ mmact_status mmact_set_gemm_mxfp4_kernel(int mode);
  *   experts [T, top] int32 and probs [T, top] fp32 are outputs
  *   workspace  at least mmact_moe_workspace_bytes, 16-byte aligned, contents
  *      ignored; calls that may overlap on the GPU need one each
- * Sums, the softmax and h are held in fp32 (h as two bf16 halves, 16 bits of
- * it, between the products); y is rounded once.  The sum over j is taken in
- * order: results repeat bit for bit.  Limits: H and I multiples of 8 and at
+ * Sums, the softmax and h are held in fp32; y is rounded once.  16-bit weights:
+ * h stands as two bf16 halves, 16 bits of it, between the products.  MXFP4
+ * weights are multiplied as they are: x and h stand as sums of eight MXFP4
+ * terms, what they leave out being below 2^-24 of the largest of 32 values, and
+ * an x with an infinity or a NaN makes its token's y NaN.  The sum over j is
+ * taken in order: results repeat bit for bit.  Limits: H and I multiples of 8 and at
  * least 8, 1 <= top <= min(E, 16), E <= 512, T <= 64, else
  * MMACT_ERR_UNSUPPORTED.  T == 0 enqueues nothing.
  */
