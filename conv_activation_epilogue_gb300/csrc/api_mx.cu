@@ -276,24 +276,22 @@ mmact_status moe_sizes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
 }
 
 // Half the rows of a tile of 16-bit weights: the one with which the busiest SM has
-// the least to do, counted in rows x K.  A ring stage takes as long as one of 100
-// rows at least (measured on 32 tokens, 6 of 64 experts of 2048 x 1408: tiles of
-// 128 rows 191 us, 96 rows 216, 64 rows 281), so smaller tiles pay only where whole
-// rounds of the SMs are saved: 16 tokens, 2 of 16 experts of 4096 x 1792, 126 us with
-// tiles of 128 rows, 117 with 112; one token, 2 of 8 experts of the same, 51.8 us with
-// 128, 49.8 with 96; 64 tokens, 2 of 8 ungated experts of 1024 x 768, 47.7 and 43.7 (64
-// rows).  The number of chosen experts is not known here: it is taken as what random
-// choices give and a twentieth.
+// the least to do, counted in rows x K.  Smaller tiles pay where they save a round of
+// the SMs or bring all of them to work: 16 tokens, 2 of 16 experts of 4096 x 1792, 117.5
+// us with tiles of 128 rows, 110 with 112; one token, 2 of 8 experts of the same, 43.7
+// and 39.6 us with 64 rows.  Where they do not they cost: 32 tokens, 6 of 64 experts of
+// 2048 x 1408, 188 us with 128 rows, 197 with 64, 244 with 48 (a ring stage takes as
+// long as one of 72 rows at least).  The number of chosen experts is not known here: it
+// is taken as what random choices give.
 int moe_half_rows(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, bool gated, int sms)
 {
-    const double expected = (double)E * (1.0 - std::pow(1.0 - (double)top / (double)E, (double)T));
-    const int64_t chosen = T == 1 ? top : std::min({E, T * top, (int64_t)std::ceil(expected * 1.05)});
+    const int64_t chosen = std::llround((double)E * (1.0 - std::pow(1.0 - (double)top / (double)E, (double)T)));
     int best = 64;
     double least = 0;
     for (int half = 64; half >= 32; half -= 8) {
         const int64_t step = gated ? half : 2 * half, up = chosen * ((I + step - 1) / step);
         const int64_t down = chosen * ((H + 2 * half - 1) / (2 * half));
-        const double cost = (double)std::max(2 * half, 100) *
+        const double cost = (double)std::max(2 * half, 72) *
                             ((double)((up + sms - 1) / sms) * (double)H + (double)((down + sms - 1) / sms) * (double)I);
         if (half == 64 || cost < 0.97 * least) least = cost, best = half;
     }

@@ -42,38 +42,46 @@ constexpr int MOE_MMA_WARPS = 8;
 constexpr int MOE_THREADS = 32 * (2 + MOE_MMA_WARPS);
 constexpr int MOE_GROUP = 32;                                  // tokens of one expert that share a read of its weights
 
-// Two rings.  A stage of weights is 64 K of a tile, at most 128 rows x 128 bytes.  A
-// stage of tokens is the group's tokens over 256 K (four stages of weights), hi and
-// lo, a record for each: 512 bytes to a copy, because copies of 128 bytes were measured
-// to keep one warp busy for twice the time of the weights' stage.  A record is 64
-// bytes longer than a multiple of 128, so that two tokens' 64-byte pieces lie on
-// different banks.  The tokens' ring has room for as many as the call can send to one
+// Two rings.  A stage of weights is 128 K of a tile, two boxes of 64 K for each half:
+// with 64 K a stage, what a warp does once a stage (waits, addresses, giving it back)
+// took longer than the multiplication (one token, 2 of 8 experts of 4096 x 1792: 47.7 us,
+// with 128 K 41.6; 64 tokens, 8 of 64 experts: 456 and 445).  A stage of tokens is the
+// group's tokens over 256 K (two stages of weights), hi and lo, a record for each: 512
+// bytes to a copy, because copies of 128 bytes were measured to keep one warp busy for
+// longer than the weights take.  A record is 64 bytes longer than a multiple of 128, so
+// that two tokens' 64-byte pieces lie on different banks.  The tokens' ring has room for as many as the call can send to one
 // expert, and four stages of few: h comes from L2 when the grid barrier opens, and
 // with two stages its latency was most of a small down product's time.  The rest is
 // weights' stages, filled while the CTA waits for the barrier.
-constexpr int MOE_STAGE_K = 64, MOE_TOKEN_K = 256, MOE_SPAN = MOE_TOKEN_K / MOE_STAGE_K;
-constexpr int MOE_TOKEN = MOE_TOKEN_K * 2, MOE_RECORD = 2 * MOE_TOKEN + 64, MOE_MAX_STAGES = 12, MOE_MAX_TSTAGES = 4;
+constexpr int MOE_STAGE_K = 128, MOE_BOXES = MOE_STAGE_K / 64, MOE_TOKEN_K = 256, MOE_SPAN = MOE_TOKEN_K / MOE_STAGE_K;
+constexpr int MOE_TOKEN = MOE_TOKEN_K * 2, MOE_RECORD = 2 * MOE_TOKEN + 64, MOE_MAX_STAGES = 9, MOE_MAX_TSTAGES = 4;
 constexpr int MOE_RINGS = (232448 - (int)sizeof(MoeShared)) & ~15;
 static_assert(2 * MOE_MAX_STAGES + 2 * MOE_MAX_TSTAGES <= MOE_MAX_BARS, "barriers");
 
 // Shared memory of a call: the rings, then MoeShared.
 struct MoeLayout {
     int stages, tstages, stage_bytes, token_bytes, off_tokens, off_shared;
-    __host__ __device__ MoeLayout(int T, int half_rows)
+    __host__ __device__ constexpr MoeLayout(int T, int half_rows)
+        : stages(0), tstages(T <= 16 ? MOE_MAX_TSTAGES : 2), stage_bytes(MOE_BOXES * half_rows * 256),
+          token_bytes((T < MOE_GROUP ? (T + 7) & ~7 : MOE_GROUP) * MOE_RECORD), off_tokens(0), off_shared(0)
     {
-        stage_bytes = half_rows * 256;
-        token_bytes = (T < MOE_GROUP ? (T + 7) & ~7 : MOE_GROUP) * MOE_RECORD;
-        tstages = T <= 16 ? MOE_MAX_TSTAGES : 2;
         const int room = (MOE_RINGS - tstages * token_bytes) / stage_bytes;
         stages = room < MOE_MAX_STAGES ? room : MOE_MAX_STAGES;
         off_tokens = stages * stage_bytes;
         off_shared = off_tokens + tstages * token_bytes;
     }
 };
-// all logits in the weights' ring, a bit for each expert and slot in the tokens' ring
-static_assert(MOE_MAX_T * MOE_MAX_E * 4 <= 8 * 16384 && 8 * 16384 <= MOE_RINGS - 2 * MOE_GROUP * MOE_RECORD, "logits");
-static_assert(MOE_MAX_E * MOE_MAX_T * MOE_MAX_K / 8 <= 2 * MOE_GROUP * MOE_RECORD &&
-              MOE_MAX_E * MOE_MAX_K <= 2 * 8 * MOE_RECORD, "bits");
+
+// Before the rings start, all logits and after them a bit for each expert and slot
+// stand in their place: both fit for every T and tile height.
+constexpr bool plan_fits()
+{
+    for (int half = 32; half <= 64; half += 8)
+        for (int T = 1; T <= MOE_MAX_T; ++T)
+            if (T * MOE_MAX_E * 4 + MOE_MAX_E * ((T * MOE_MAX_K + 31) / 32) * 4 > MoeLayout(T, half).off_shared) return false;
+    return true;
+}
+static_assert(plan_fits(), "logits and bits");
 
 // ------------------------------------------------------------------ helpers --
 template <bool BF16>
@@ -186,22 +194,21 @@ struct MoePlace {
     }
 };
 
-// What a warp multiplies in one stage: two units of 32 K, 8 values to a lane of its
-// two rows and of its tokens.
+// What a warp multiplies in one stage: units of 32 K, 8 values to a lane of its two
+// rows and of its tokens.
 template <int NT, bool LO>
 struct MoeFragments {
-    uint4 a[2], b[2];
-    MoeTokens<NT, LO> x[2];
+    uint4 a[2 * MOE_BOXES], b[2 * MOE_BOXES];
+    MoeTokens<NT, LO> x[2 * MOE_BOXES];
 };
 
-// A warp's walk over the stages of an item: `w` and `t` are the stage that is
-// fetched next, `wr` and `tr` the one that is given back next.
+// A warp's walk over the stages of its items.
 struct MoeWalk {
-    MoePlace w, t, wr, tr;
+    MoePlace w, t;
 };
 
 template <int NT, bool LO>
-__device__ __forceinline__ bool fetch(MoeFragments<NT, LO> &f, const MoePipe &m, const MoeItem &it, MoeWalk &walk, int s, int stages)
+__device__ __forceinline__ bool fetch(MoeFragments<NT, LO> &f, const MoePipe &m, const MoeItem &it, const MoeWalk &walk, int s)
 {
     const int lane = threadIdx.x & 31;
     const uint32_t sw = (uint32_t)(lane >> 2), t4 = (uint32_t)(lane & 3);   // the 128-byte swizzle: chunk ^ (row & 7)
@@ -212,13 +219,12 @@ __device__ __forceinline__ bool fetch(MoeFragments<NT, LO> &f, const MoePipe &m,
     if (part == 0 && !mx_warp_wait(m.pp, m.tfull0 + 8 * walk.t.slot, walk.t.phase)) return false;
     if (!mx_warp_wait(m.pp, m.pp.full0 + 8 * walk.w.slot, walk.w.phase)) return false;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        f.a[u] = ptx::ld_shared_v4(row + (u ? c1 : c0));
-        f.b[u] = ptx::ld_shared_v4(row + it.upper + (u ? c1 : c0));
+    for (int u = 0; u < 2 * MOE_BOXES; ++u) {
+        const uint32_t at = row + (uint32_t)(u >> 1) * (2u * it.upper) + (u & 1 ? c1 : c0);
+        f.a[u] = ptx::ld_shared_v4(at);
+        f.b[u] = ptx::ld_shared_v4(at + it.upper);
         load_tokens<NT, LO>(f.x[u], tok + u * 64u);
     }
-    walk.w.next(m.stages);
-    if (part == MOE_SPAN - 1 || s == stages - 1) walk.t.next(m.tstages);
     return true;
 }
 
@@ -227,7 +233,7 @@ template <bool BF, int NT, bool LO, bool SPLITW>
 __device__ __forceinline__ void multiply(float (&acc)[NT][4], float (&low)[LO ? NT : 1][4], const MoeFragments<NT, LO> &f)
 {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < 2 * MOE_BOXES; ++u) {
         uint32_t a[4] = {f.a[u].x, f.a[u].y, f.a[u].z, f.a[u].w}, b[4] = {f.b[u].x, f.b[u].y, f.b[u].z, f.b[u].w};
         if constexpr (SPLITW) {
             uint32_t al[4], bl[4];
@@ -252,43 +258,25 @@ __device__ __forceinline__ void give_back(const MoePipe &m, MoeWalk &walk, int s
     const bool last = s % MOE_SPAN == MOE_SPAN - 1 || s == stages - 1;      // of its stage of tokens
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
-        ptx::mbar_arrive(m.pp.empty0 + 8 * walk.wr.slot);
-        if (last) ptx::mbar_arrive(m.tempty0 + 8 * walk.tr.slot);
+        ptx::mbar_arrive(m.pp.empty0 + 8 * walk.w.slot);
+        if (last) ptx::mbar_arrive(m.tempty0 + 8 * walk.t.slot);
     }
-    walk.wr.next(m.stages);
-    if (last) walk.tr.next(m.tstages);
+    walk.w.next(m.stages);
+    if (last) walk.t.next(m.tstages);
 }
 
-// One warp's rows of an item over all of K.  With up to 8 tokens a stage's fragments
-// are loaded while the one before is multiplied: one token, 2 of 8 experts of 4096 x
-// 1792, 49.8 us without, 47.7 with it.  With 16 tokens the second set of fragments costs
-// more than it hides: 64 tokens, 8 of 64 experts of the same, 472 us without, 489 with.
+// One warp's rows of an item over all of K.
 template <bool BF, int NT, bool LO, bool SPLITW>
 __device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
                                          MoeWalk &walk)
 {
     float low[LO ? NT : 1][4] = {};
-    MoeFragments<NT, LO> f;
-    if constexpr (NT == 1) {
-        MoeFragments<NT, LO> g;
-        if (!fetch<NT, LO>(f, m, it, walk, 0, pr.stages)) return false;
 #pragma unroll 1
-        for (int s = 0; s < pr.stages; s += 2) {
-            if (s + 1 < pr.stages && !fetch<NT, LO>(g, m, it, walk, s + 1, pr.stages)) return false;
-            multiply<BF, NT, LO, SPLITW>(acc, low, f);
-            give_back(m, walk, s, pr.stages);
-            if (s + 1 == pr.stages) break;
-            if (s + 2 < pr.stages && !fetch<NT, LO>(f, m, it, walk, s + 2, pr.stages)) return false;
-            multiply<BF, NT, LO, SPLITW>(acc, low, g);
-            give_back(m, walk, s + 1, pr.stages);
-        }
-    } else {
-#pragma unroll 1
-        for (int s = 0; s < pr.stages; ++s) {
-            if (!fetch<NT, LO>(f, m, it, walk, s, pr.stages)) return false;
-            multiply<BF, NT, LO, SPLITW>(acc, low, f);
-            give_back(m, walk, s, pr.stages);
-        }
+    for (int s = 0; s < pr.stages; ++s) {
+        MoeFragments<NT, LO> f;
+        if (!fetch<NT, LO>(f, m, it, walk, s)) return false;
+        multiply<BF, NT, LO, SPLITW>(acc, low, f);
+        give_back(m, walk, s, pr.stages);
     }
     if constexpr (LO)
 #pragma unroll
@@ -378,9 +366,12 @@ __device__ __forceinline__ bool produce(const CUtensorMap *map, const MoeArgs &p
         for (int s = 0; s < pr.stages; ++s, to.next(m.stages)) {
             const uint32_t full = m.pp.full0 + 8 * to.slot, at = m.ring + to.slot * m.stage_bytes;
             if (!mx_warp_wait(m.pp, m.pp.empty0 + 8 * to.slot, to.phase ^ 1u)) return false;
-            elected_expect_tx(full, both ? 2u * box : box);
-            elected_load_2d(at, map, full, s * MOE_STAGE_K, row, pol);
-            if (both) elected_load_2d(at + box, map, full, s * MOE_STAGE_K, row + pr.half, pol);
+            elected_expect_tx(full, (both ? 2u * box : box) * MOE_BOXES);
+#pragma unroll
+            for (int b = 0; b < MOE_BOXES; ++b) {              // K past the end arrives as zeros
+                elected_load_2d(at + 2u * b * box, map, full, s * MOE_STAGE_K + 64 * b, row, pol);
+                if (both) elected_load_2d(at + (2u * b + 1u) * box, map, full, s * MOE_STAGE_K + 64 * b, row + pr.half, pol);
+            }
         }
     }
     return true;
@@ -464,7 +455,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     }
     ptx::griddep_wait();                                       // the router's logits
     plan_experts<MOE_GROUP, MOE_THREADS>(p, S, reinterpret_cast<uint32_t *>(smem),
-                                         reinterpret_cast<uint32_t *>(smem + layout.off_tokens));
+                                         reinterpret_cast<uint32_t *>(smem + p.T * p.E * 4));
 
     const MoeProduct up = up_product(p, MOE_STAGE_K, MOE_TOKEN_K), down = down_product(p, MOE_STAGE_K, MOE_TOKEN_K);
     bool ok = aligned;

@@ -209,6 +209,14 @@ def test_results_repeat_and_graphs_replay():
 
 
 @pytest.mark.parametrize("dtype,weights", TYPES)
+@pytest.mark.parametrize("T,H,I,gated", [(64, 64, 16, True), (64, 72, 200, False), (49, 40, 72, True), (16, 64, 16, False)])
+def test_the_most_experts_and_choices(dtype, weights, T, H, I, gated):
+    L = layer(T + I, T, H, I, 512, dtype, weights, gated, True)
+    out = run(L, 16, dtype, weights, gated=gated)
+    check(L, out, 16, dtype, gated=gated)
+
+
+@pytest.mark.parametrize("dtype,weights", TYPES)
 @pytest.mark.parametrize("T,H,I,E,top,gated", [(32, 4096, 1792, 16, 4, True), (64, 2048, 2056, 12, 3, False),
                                                (1, 2048, 1024, 64, 8, True)])
 def test_large_layers_under_load(dtype, weights, T, H, I, E, top, gated):
