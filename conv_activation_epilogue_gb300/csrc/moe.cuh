@@ -64,49 +64,54 @@ __device__ __forceinline__ void fence_proxy_async_all()
 }
 
 // ------------------------------------------------------------------- router --
-constexpr int MOE_ROUTER_THREADS = 128;
+// A CTA is a chain of loads: 16 tokens, 2 of 16 experts of 4096 x 1792 take 56.2 us with 128
+// threads, 54 with 256; 512 help no further and cost layers of many experts (64 tokens,
+// 8 of 64 experts of 2048 x 1024, MXFP4: 78.8 us with 256, 82.2 with 512).
+constexpr int MOE_ROUTER_THREADS = 256, MOE_ROUTER_K = MOE_ROUTER_THREADS * 8;
 
-// Router logits by one CTA, for an expert and eight tokens: four warps share K.
+// Router logits by one CTA, for an expert and eight tokens: its warps share K.
 template <int XT>
 __device__ __forceinline__ void router_logits(const MoeArgs &p, int block, int token_groups)
 {
-    __shared__ float red[4][8];
+    __shared__ float red[MOE_ROUTER_THREADS / 32][8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint16_t *xs = static_cast<const uint16_t *>(p.x);
-        const int e = block / token_groups, t0 = (block - e * token_groups) * 8, n = min(8, p.T - t0);
-        const uint16_t *r = static_cast<const uint16_t *>(p.router) + (int64_t)e * p.H;
-        float s[8] = {};
-        for (int k = threadIdx.x * 8; k < p.H; k += MOE_ROUTER_THREADS * 8) {
-            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(r + k));
-            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-            uint4 a[8];                                        // tokens past the last one: the last one again
+    const int e = block / token_groups, t0 = (block - e * token_groups) * 8, n = min(8, p.T - t0);
+    const uint16_t *r = static_cast<const uint16_t *>(p.router) + (int64_t)e * p.H;
+    float s[8] = {};
+    for (int k = threadIdx.x * 8; k < p.H; k += MOE_ROUTER_K) {
+        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(r + k));
+        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+        uint4 a[8];                                        // tokens past the last one: the last one again
 #pragma unroll
-            for (int t = 0; t < 8; ++t) a[t] = __ldg(reinterpret_cast<const uint4 *>(xs + (int64_t)(t0 + min(t, n - 1)) * p.H + k));
-            float2 g[4];
+        for (int t = 0; t < 8; ++t) a[t] = __ldg(reinterpret_cast<const uint4 *>(xs + (int64_t)(t0 + min(t, n - 1)) * p.H + k));
+        float2 g[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) g[j] = unpack2<XT>(bw[j]);
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const uint32_t aw[4] = {a[t].x, a[t].y, a[t].z, a[t].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = unpack2<XT>(aw[j]);
-                    s[t] = fmaf(f.x, g[j].x, s[t]);
-                    s[t] = fmaf(f.y, g[j].y, s[t]);
-                }
-            }
-        }
+        for (int j = 0; j < 4; ++j) g[j] = unpack2<XT>(bw[j]);
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
+            const uint32_t aw[4] = {a[t].x, a[t].y, a[t].z, a[t].w};
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
-            if (lane == 0) red[warp][t] = s[t];
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack2<XT>(aw[j]);
+                s[t] = fmaf(f.x, g[j].x, s[t]);
+                s[t] = fmaf(f.y, g[j].y, s[t]);
+            }
         }
-        __syncthreads();
-        if (threadIdx.x < n)
-            p.logits[(int64_t)(t0 + threadIdx.x) * p.E + e] =
-                (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]) +
-                (p.router_bias != nullptr ? p.router_bias[e] : 0.0f);
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
+        if (lane == 0) red[warp][t] = s[t];
+    }
+    __syncthreads();
+    if (threadIdx.x < n) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < MOE_ROUTER_THREADS / 32; ++w) sum += red[w][threadIdx.x];
+        p.logits[(int64_t)(t0 + threadIdx.x) * p.E + e] = sum + (p.router_bias != nullptr ? p.router_bias[e] : 0.0f);
+    }
 }
 
 // ------------------------------------------------------------ choice of experts --

@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_mxfp4_router_kernel(co
         router_logits<XT>(p, (int)blockIdx.x, token_groups);
         return;
     }
-    // 1024 K of one token, 8 values to a thread, four threads to a block
-    const int chunks = (p.Hp + 1023) / 1024, at = (int)blockIdx.x - p.E * token_groups, t = at / chunks;
-    const int k = (at - t * chunks) * 1024 + (int)threadIdx.x * 8, stages = p.Hp / MXE_K;
+    // MOE_ROUTER_K of one token, 8 values to a thread, four threads to a block
+    const int chunks = (p.Hp + MOE_ROUTER_K - 1) / MOE_ROUTER_K, at = (int)blockIdx.x - p.E * token_groups, t = at / chunks;
+    const int k = (at - t * chunks) * MOE_ROUTER_K + (int)threadIdx.x * 8, stages = p.Hp / MXE_K;
     if (at == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
     uint4 raw = make_uint4(0, 0, 0, 0);
     if (k < p.H) raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.H + k));
@@ -471,8 +471,9 @@ static cudaError_t launch_t(const MoeLaunch &L, cudaStream_t stream)
 {
     const MoeArgs &a = L.args;
     const int groups = (a.T + 7) / 8;
-    const cudaError_t e = launch_k(moe_mxfp4_router_kernel<XT>, dim3((unsigned)(a.E * groups + a.T * ((a.Hp + 1023) / 1024))),
-                                   dim3(MOE_ROUTER_THREADS), 0, stream, a, groups);
+    const int ctas = a.E * groups + a.T * ((a.Hp + MOE_ROUTER_K - 1) / MOE_ROUTER_K);
+    const cudaError_t e =
+        launch_k(moe_mxfp4_router_kernel<XT>, dim3((unsigned)ctas), dim3(MOE_ROUTER_THREADS), 0, stream, a, groups);
     if (e != cudaSuccess) return e;
     return launch_cooperative(moe_mxfp4_kernel<XT>, L.grid, MXE_THREADS, MXE_SMEM, stream, L.tm1, L.tm2, a);
 }
