@@ -35,7 +35,7 @@
 // which keeps h's fp32 range.
 //
 // Measured (bf16, GB300): 64 tokens, 8 of 64 experts of 4096 x 1792 (2.8 GB of weights)
-// 444 us, 6.3 TB/s.  One token, 8 of 64 experts of 2048 x 1024 (101 MB): 32 us, of which
+// 442 us, 6.4 TB/s.  One token, 8 of 64 experts of 2048 x 1024 (101 MB): 32 us, of which
 // the weights take 15; the router kernel is 4, choice and lists 4, the two grid
 // barriers with what they leave idle 5.
 #include "moe.cuh"

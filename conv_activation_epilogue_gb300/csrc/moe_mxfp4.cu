@@ -4,14 +4,15 @@
 // Turning 4-bit weights into 16-bit values is more work than an SM can do in the
 // time that it reads them (on mma.sync, with the weights widened in registers, 16
 // tokens through 4 of 128 experts of 4096 x 2048 took 265 us where the bytes take
-// 102; this form takes 121).  So the weights go to the tensor core as they
+// 102; this form takes 120).  So the weights go to the tensor core as they
 // are, and the tokens take their form: a value is written as a sum of eight MXFP4
 // terms, the first the value rounded to the 4-bit grid, each next one the
 // rounding of what is left, every term with a scale of its own for 32 values (the
-// smallest power of two that keeps the largest of them within 6).  A term brings
-// three bits: what eight leave out is below 2^-24 of the block's largest value
-// (measured 1.3e-8 of it), so a product of weights with the sum of the terms is
-// one with fp32 tokens.  The terms are eight columns of the MMA; with few tokens
+// smallest power of two X that keeps the largest of them within 6 X).  The first term
+// leaves at most a quarter of the block's largest value; when a term leaves at most X,
+// the next leaves at most X / 8 (its own scale is X / 4, or X / 8 and less where less
+// than 3 X / 4 is left): eight leave at most 2^-23, the precision of fp32 tokens.  The
+// terms are eight columns of the MMA; with few tokens
 // the columns are free.  They are also eight rows of 128 bytes, one 1024-byte atom
 // of the shared-memory layout for 256 K, which is kept swizzled in global memory
 // and moves by one bulk copy a token.
