@@ -119,14 +119,15 @@ __device__ __forceinline__ void quantize_stages(const MxRowsArgs &p, const Pipe 
             for (int u = 0; u < 2; ++u) {
                 const int row = r0 + 4 * u + (lane >> 3);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int j = 0; j < Raw8<XT>::WORDS; ++j) r[u][q].w[j] = 0;
-                    if (row < p.M && n > 8 * q) {
-                        const int64_t at = (int64_t)row * p.K + k0 + 8 * q;
-                        if (vec) load8<XT, true>(p.x, at, n - 8 * q, r[u][q]);
-                        else load8<XT, false>(p.x, at, n - 8 * q, r[u][q]);
-                    }
+                if (row < p.M && n > 0) {
+                    const int64_t at = (int64_t)row * p.K + k0;
+                    if (vec)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) load8<XT, true>(p.x, at + 8 * q, n - 8 * q, r[u][q]);
+                    else load32_any<XT>(p.x, at, n, (int64_t)p.M * p.K, r[u]);
                 }
             }
             // (this warp saw the slot of four stages ago free, so no more than one use of this slot is outstanding)

@@ -40,8 +40,12 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void *__restrict__ 
         for (int j = 0; j < Raw8<T>::WORDS; ++j) r[q].w[j] = 0;
     if (row < rows && blk < kb) {
         const int n = (int)min((int64_t)32, K - k0);
+        if constexpr (VEC) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) load8<T, VEC>(x, row * K + k0 + 8 * q, n - 8 * q, r[q]);
+            for (int q = 0; q < 4; ++q) load8<T, true>(x, row * K + k0 + 8 * q, n - 8 * q, r[q]);
+        } else {
+            load32_any<T>(x, row * K + k0, n, rows * K, r);
+        }
     }
     uint32_t amax = 0;
 #pragma unroll

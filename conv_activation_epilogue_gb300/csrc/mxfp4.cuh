@@ -127,6 +127,49 @@ __device__ __forceinline__ void load8(const void *x, int64_t i, int n, Raw8<T> &
     }
 }
 
+// A block of n <= 32 consecutive values x[at..at+n) (the rest 0) that begins anywhere,
+// of a tensor of `total` values: the aligned 16 bytes that hold them, shifted into
+// place.  (By single values, 32 lanes each 64 bytes from the next, rows that are not a
+// multiple of 16 bytes took three times as long: 5447 x 3659 bf16 35.8 us, 11.6 so.)
+// Where those reach past the end of the tensor, by single values.
+template <int T>
+__device__ __forceinline__ void load32_any(const void *x, int64_t at, int n, int64_t total, Raw8<T> (&r)[4])
+{
+    constexpr int ES = T == IN_F32 ? 4 : 2, WORDS = 8 * ES, PER = WORDS / 4;
+    const int shift = (int)(at * ES) & 15, bytes = shift + n * ES;
+    const int64_t from = at * ES - shift;
+    if (from + ((bytes + 15) & ~15) > total * ES) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load8<T, false>(x, at + 8 * q, n - 8 * q, r[q]);
+        return;
+    }
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(x) + from);
+    uint32_t u[WORDS + 4];
+#pragma unroll
+    for (int c = 0; c <= WORDS / 4; ++c) {
+        const uint4 v = 16 * c < bytes ? __ldg(p + c) : make_uint4(0, 0, 0, 0);
+        u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
+    }
+    if (shift & 8)
+#pragma unroll
+        for (int j = 0; j < WORDS + 2; ++j) u[j] = u[j + 2];
+    if (shift & 4)
+#pragma unroll
+        for (int j = 0; j < WORDS + 1; ++j) u[j] = u[j + 1];
+#pragma unroll
+    for (int j = 0; j < WORDS; ++j) {
+        uint32_t w = u[j];
+        if constexpr (T == IN_F32) {
+            if (j >= n) w = 0;
+        } else {
+            if (shift & 2) w = __funnelshift_r(u[j], u[j + 1], 16);
+            if (2 * j >= n) w = 0;
+            else if (2 * j + 1 >= n) w &= 0xffffu;
+        }
+        r[j / PER].w[j % PER] = w;
+    }
+}
+
 // The largest |value| of raw words so far: of 16-bit types in each half of `m`
 // (their magnitudes order as unsigned integers, infinities and NaN on top).
 template <int T>
