@@ -231,7 +231,7 @@ struct MoeWorkspace {
 };
 
 // The same for both forms of the weights: x padded (2 bytes a value) or its terms
-// (4 bytes a value and a quarter), h in two halves (4 bytes) or its terms.
+// (4 bytes a value and a quarter), h in three parts (6 bytes) or its terms.
 MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
 {
     MoeWorkspace w;
@@ -245,7 +245,7 @@ MoeWorkspace moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t t
     w.logits = take(T * E * 4);
     w.x = take(T * Hp * 4);
     w.x_scales = take(T * Hp / 4);
-    w.h = take(T * top * Ip * 4);
+    w.h = take(T * top * Ip * 6);
     w.h_scales = take(T * top * Ip / 4);
     w.part = take(T * top * H * 4);
     w.bytes = at;
@@ -455,8 +455,7 @@ MMACT_EXPORT mmact_status mmact_moe(const void *x, const void *router, const flo
         a.h_scales = reinterpret_cast<uint8_t *>(ws + w.h_scales);
     } else {
         a.x_pad = reinterpret_cast<uint16_t *>(ws + w.x);
-        a.h_hi = reinterpret_cast<uint16_t *>(ws + w.h);
-        a.h_lo = a.h_hi + T * top * a.Ip;
+        a.h = reinterpret_cast<uint16_t *>(ws + w.h);
     }
     a.part = reinterpret_cast<float *>(ws + w.part);
     a.status = c.dev.status;

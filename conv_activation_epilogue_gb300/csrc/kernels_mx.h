@@ -91,7 +91,7 @@ struct MoeArgs {
     unsigned int *counters;      // two grid barriers
     float *logits;               // [T, E]
     uint16_t *x_pad;             // 16-bit weights: x [T, Hp], zeros past H
-    uint16_t *h_hi, *h_lo;       // 16-bit weights: h in bf16 halves [T * top, Ip]
+    uint16_t *h;                 // 16-bit weights: h as three bf16 parts, [T * top][Ip / 128][3][128]
     uint8_t *x_codes, *x_scales; // MXFP4: x and h as sums of eight MXFP4 terms: a KB of codes and 64
     uint8_t *h_codes, *h_scales; //   scales for each token (slot) and 256 K
     float *part;                 // [T * top, H]

@@ -29,10 +29,12 @@
 //                both operands agree, so fragments are 16-byte loads in memory
 //                order.
 //
-// The intermediate h is held as two bf16 halves hi = bf16(h), lo = bf16(h - hi),
-// 16 bits of it, and multiplied as both, so no rounding to 16 bits stands between
-// the two products.  fp16 down weights are split the same way (hi + lo is exact),
-// which keeps h's fp32 range.
+// The intermediate h is held as three bf16 parts of 8 bits each, h = hi + mid + lo
+// exactly, and multiplied as all of them: nothing is rounded between the two
+// products.  (Two parts, 16 bits of h, take 3 % less of the time of 64 tokens, and put y
+// in bf16 1.0e-4 instead of 0.6e-4, in the 2-norm, from what fp32 gives.)  fp16 down weights are split
+// into two (hi + lo is exact), which keeps h's fp32 range; of their products with
+// the parts, lo x lo, 2^-24 of hi x hi, is left out.
 //
 // Measured (bf16, GB300): 64 tokens, 8 of 64 experts of 4096 x 1792 (2.8 GB of weights)
 // 442 us, 6.4 TB/s.  One token, 8 of 64 experts of 2048 x 1024 (101 MB): 32 us, of which
@@ -50,42 +52,52 @@ constexpr int MOE_GROUP = 32;                                  // tokens of one 
 // with 64 K a stage, what a warp does once a stage (waits, addresses, giving it back)
 // took longer than the multiplication (one token, 2 of 8 experts of 4096 x 1792: 47.7 us,
 // with 128 K 41.6; 64 tokens, 8 of 64 experts: 456 and 445).  A stage of tokens is the
-// group's tokens over 256 K (two stages of weights), hi and lo, a record for each: 512
-// bytes to a copy, because copies of 128 bytes were measured to keep one warp busy for
-// longer than the weights take.  A record is 64 bytes longer than a multiple of 128, so
-// that two tokens' 64-byte pieces lie on different banks.  The tokens' ring has room for as many as the call can send to one
-// expert, and four stages of few: h comes from L2 when the grid barrier opens, and
-// with two stages its latency was most of a small down product's time.  The rest is
-// weights' stages, filled while the CTA waits for the barrier.
-constexpr int MOE_STAGE_K = 128, MOE_BOXES = MOE_STAGE_K / 64, MOE_TOKEN_K = 256, MOE_SPAN = MOE_TOKEN_K / MOE_STAGE_K;
-constexpr int MOE_TOKEN = MOE_TOKEN_K * 2, MOE_RECORD = 2 * MOE_TOKEN + 64, MOE_MAX_STAGES = 9, MOE_MAX_TSTAGES = 4;
+// group's tokens, a record for each and a copy to a record: x over 256 K (two stages of
+// weights, 512 bytes), or h over 128 K (its three parts, 768 bytes), because copies of
+// 128 bytes were measured to keep one warp busy for longer than the weights take.  A
+// record is 64 bytes longer than a multiple of 128, so that two tokens' 64-byte pieces
+// lie on different banks.  The tokens' ring has room for as many as the call can send to
+// one expert, and more stages of few: h comes from L2 when the grid barrier opens, and
+// with 512 K of it in flight its latency was most of a small down product's time.  The
+// rest is weights' stages, filled while the CTA waits for the barrier.
+constexpr int MOE_STAGE_K = 128, MOE_BOXES = MOE_STAGE_K / 64, MOE_PARTS = 3, MOE_PART = MOE_STAGE_K * 2;
+constexpr int MOE_RECORD = MOE_PARTS * MOE_PART + 64, MOE_MAX_STAGES = 9, MOE_MAX_TSTAGES = 8;
+// Stages of weights to a stage of tokens, and what one copy of them is: of x, of h.
+template <bool DOWN>
+constexpr int MOE_SPAN = DOWN ? 1 : 2;
+template <bool DOWN>
+constexpr int MOE_TOKEN_K = MOE_SPAN<DOWN> * MOE_STAGE_K;
+template <bool DOWN>
+constexpr int MOE_TOKEN = MOE_TOKEN_K<DOWN> * 2 * (DOWN ? MOE_PARTS : 1);
+static_assert(MOE_TOKEN<false> <= MOE_RECORD && MOE_TOKEN<true> <= MOE_RECORD, "records");
 constexpr int MOE_RINGS = (232448 - (int)sizeof(MoeShared)) & ~15;
 static_assert(2 * MOE_MAX_STAGES + 2 * MOE_MAX_TSTAGES <= MOE_MAX_BARS, "barriers");
 
-// Shared memory of a call: the rings, then MoeShared.
+// Shared memory of a call: the rings, then MoeShared.  Before the rings start, all
+// logits and after them a bit for each expert and slot stand in their place.
 struct MoeLayout {
     int stages, tstages, stage_bytes, token_bytes, off_tokens, off_shared;
     __host__ __device__ constexpr MoeLayout(int T, int half_rows)
-        : stages(0), tstages(T <= 16 ? MOE_MAX_TSTAGES : 2), stage_bytes(MOE_BOXES * half_rows * 256),
+        : stages(0), tstages(T <= 8 ? MOE_MAX_TSTAGES : (T <= 16 ? 6 : 3)), stage_bytes(MOE_BOXES * half_rows * 256),
           token_bytes((T < MOE_GROUP ? (T + 7) & ~7 : MOE_GROUP) * MOE_RECORD), off_tokens(0), off_shared(0)
     {
         const int room = (MOE_RINGS - tstages * token_bytes) / stage_bytes;
         stages = room < MOE_MAX_STAGES ? room : MOE_MAX_STAGES;
         off_tokens = stages * stage_bytes;
-        off_shared = off_tokens + tstages * token_bytes;
+        const int rings = off_tokens + tstages * token_bytes, plan = T * MOE_MAX_E * 4 + MOE_MAX_E * ((T * MOE_MAX_K + 31) / 32) * 4;
+        off_shared = rings > plan ? rings : plan;
     }
 };
 
-// Before the rings start, all logits and after them a bit for each expert and slot
-// stand in their place: both fit for every T and tile height.
-constexpr bool plan_fits()
+// Every T and tile height has room, and two stages of weights at least.
+constexpr bool layout_fits()
 {
     for (int half = 32; half <= 64; half += 8)
         for (int T = 1; T <= MOE_MAX_T; ++T)
-            if (T * MOE_MAX_E * 4 + MOE_MAX_E * ((T * MOE_MAX_K + 31) / 32) * 4 > MoeLayout(T, half).off_shared) return false;
+            if (MoeLayout(T, half).off_shared > MOE_RINGS || MoeLayout(T, half).stages < 2) return false;
     return true;
 }
-static_assert(plan_fits(), "logits and bits");
+static_assert(layout_fits(), "rings, logits and bits");
 
 // ------------------------------------------------------------------ helpers --
 template <bool BF16>
@@ -102,6 +114,24 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
                      "{%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Where the first part of h of a slot at `row` stands; the others follow MOE_STAGE_K
+// values apart.
+__device__ __forceinline__ int64_t h_at(const MoeArgs &p, int64_t slot, int row)
+{
+    return slot * p.Ip * MOE_PARTS + row / MOE_STAGE_K * (MOE_PARTS * MOE_STAGE_K) + row % MOE_STAGE_K;
+}
+
+// h as three bf16 parts: the first 8 bits, the next, the last.
+__device__ __forceinline__ void put_parts(uint16_t *h, float v)
+{
+#pragma unroll
+    for (int j = 0; j < MOE_PARTS; ++j) {
+        const uint32_t b = __float_as_uint(v) & 0xffff0000u;
+        h[j * MOE_STAGE_K] = (uint16_t)(b >> 16);
+        v -= __uint_as_float(b);
+    }
 }
 
 // Hi and lo bf16 halves of a pair of fp32 values.
@@ -135,9 +165,9 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
     if (at != t * chunks) return;
     const int pad = (p.Ip - p.I) / 8;                          // eights of zeros past h's rows
     for (int i = threadIdx.x; i < pad * p.top; i += MOE_ROUTER_THREADS) {
-        const int64_t to = ((int64_t)t * p.top + i / pad) * p.Ip + p.I + i % pad * 8;
-        *reinterpret_cast<uint4 *>(p.h_hi + to) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(p.h_lo + to) = make_uint4(0, 0, 0, 0);
+        const int64_t to = h_at(p, (int64_t)t * p.top + i / pad, p.I + i % pad * 8);
+#pragma unroll
+        for (int j = 0; j < MOE_PARTS; ++j) *reinterpret_cast<uint4 *>(p.h + to + j * MOE_STAGE_K) = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -149,35 +179,35 @@ struct MoeItem {
 };
 
 // Tokens of one piece of K (16 bytes of each row): this lane's 8 values of one
-// token of each eight, hi and lo.
-template <int NT, bool LO>
+// token of each eight, x or the parts of h.
+template <int NT, bool DOWN>
 struct MoeTokens {
-    uint4 h[NT], l[LO ? NT : 1];
+    static constexpr int PARTS = DOWN ? MOE_PARTS : 1;
+    uint4 v[PARTS][NT];
 };
 
-template <int NT, bool LO>
-__device__ __forceinline__ void load_tokens(MoeTokens<NT, LO> &x, uint32_t at)
+template <int NT, bool DOWN>
+__device__ __forceinline__ void load_tokens(MoeTokens<NT, DOWN> &x, uint32_t at)
 {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        x.h[n] = ptx::ld_shared_v4(at + n * 8 * MOE_RECORD);
-        if constexpr (LO) x.l[n] = ptx::ld_shared_v4(at + n * 8 * MOE_RECORD + MOE_TOKEN);
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < MoeTokens<NT, DOWN>::PARTS; ++j) x.v[j][n] = ptx::ld_shared_v4(at + n * 8 * MOE_RECORD + j * MOE_PART);
 }
 
-// acc += 16 rows x tokens over one piece: a, b the two rows' four pairs of values.
-// The lo halves have sums of their own, so that half as many instructions wait
-// for one another.
-template <bool BF, int NT, bool LO>
-__device__ __forceinline__ void piece_mma(float (&acc)[NT][4], float (&low)[LO ? NT : 1][4], const uint32_t (&a)[4],
-                                          const uint32_t (&b)[4], const MoeTokens<NT, LO> &x)
+// acc[j] += 16 rows x part j of the tokens over one piece: a, b the two rows' four
+// pairs of values.  The parts have sums of their own, so that fewer instructions
+// wait for one another.
+template <bool BF, int NT, bool DOWN, int PARTS>
+__device__ __forceinline__ void piece_mma(float (&acc)[MoeTokens<NT, DOWN>::PARTS][NT][4], int first, const uint32_t (&a)[4],
+                                          const uint32_t (&b)[4], const MoeTokens<NT, DOWN> &x)
 {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        mma_16816<BF>(acc[n], a[0], b[0], a[1], b[1], x.h[n].x, x.h[n].y);
-        if constexpr (LO) mma_16816<BF>(low[n], a[0], b[0], a[1], b[1], x.l[n].x, x.l[n].y);
-        mma_16816<BF>(acc[n], a[2], b[2], a[3], b[3], x.h[n].z, x.h[n].w);
-        if constexpr (LO) mma_16816<BF>(low[n], a[2], b[2], a[3], b[3], x.l[n].z, x.l[n].w);
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j) mma_16816<BF>(acc[first + j][n], a[0], b[0], a[1], b[1], x.v[j][n].x, x.v[j][n].y);
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j) mma_16816<BF>(acc[first + j][n], a[2], b[2], a[3], b[3], x.v[j][n].z, x.v[j][n].w);
     }
 }
 
@@ -200,10 +230,10 @@ struct MoePlace {
 
 // What a warp multiplies in one stage: units of 32 K, 8 values to a lane of its two
 // rows and of its tokens.
-template <int NT, bool LO>
+template <int NT, bool DOWN>
 struct MoeFragments {
     uint4 a[2 * MOE_BOXES], b[2 * MOE_BOXES];
-    MoeTokens<NT, LO> x[2 * MOE_BOXES];
+    MoeTokens<NT, DOWN> x[2 * MOE_BOXES];
 };
 
 // A warp's walk over the stages of its items.
@@ -211,13 +241,13 @@ struct MoeWalk {
     MoePlace w, t;
 };
 
-template <int NT, bool LO>
-__device__ __forceinline__ bool fetch(MoeFragments<NT, LO> &f, const MoePipe &m, const MoeItem &it, const MoeWalk &walk, int s)
+template <int NT, bool DOWN>
+__device__ __forceinline__ bool fetch(MoeFragments<NT, DOWN> &f, const MoePipe &m, const MoeItem &it, const MoeWalk &walk, int s)
 {
     const int lane = threadIdx.x & 31;
     const uint32_t sw = (uint32_t)(lane >> 2), t4 = (uint32_t)(lane & 3);   // the 128-byte swizzle: chunk ^ (row & 7)
     const uint32_t c0 = (t4 ^ sw) << 4, c1 = ((4u + t4) ^ sw) << 4;
-    const uint32_t part = (uint32_t)s % MOE_SPAN;
+    const uint32_t part = (uint32_t)s % MOE_SPAN<DOWN>;
     const uint32_t row = m.ring + walk.w.slot * m.stage_bytes + it.row;
     const uint32_t tok = m.tokens + walk.t.slot * m.token_bytes + sw * MOE_RECORD + part * (MOE_STAGE_K * 2u) + t4 * 16u;
     if (part == 0 && !mx_warp_wait(m.pp, m.tfull0 + 8 * walk.t.slot, walk.t.phase)) return false;
@@ -227,14 +257,15 @@ __device__ __forceinline__ bool fetch(MoeFragments<NT, LO> &f, const MoePipe &m,
         const uint32_t at = row + (uint32_t)(u >> 1) * (2u * it.upper) + (u & 1 ? c1 : c0);
         f.a[u] = ptx::ld_shared_v4(at);
         f.b[u] = ptx::ld_shared_v4(at + it.upper);
-        load_tokens<NT, LO>(f.x[u], tok + u * 64u);
+        load_tokens<NT, DOWN>(f.x[u], tok + u * 64u);
     }
     return true;
 }
 
-// SPLITW: fp16 weights as two bf16 halves, whose lo halves meet the tokens' hi halves only.
-template <bool BF, int NT, bool LO, bool SPLITW>
-__device__ __forceinline__ void multiply(float (&acc)[NT][4], float (&low)[LO ? NT : 1][4], const MoeFragments<NT, LO> &f)
+// SPLITW: fp16 weights as two bf16 halves, whose lo halves meet the tokens' first two
+// parts only.
+template <bool BF, int NT, bool DOWN, bool SPLITW>
+__device__ __forceinline__ void multiply(float (&acc)[MoeTokens<NT, DOWN>::PARTS][NT][4], const MoeFragments<NT, DOWN> &f)
 {
 #pragma unroll
     for (int u = 0; u < 2 * MOE_BOXES; ++u) {
@@ -247,19 +278,16 @@ __device__ __forceinline__ void multiply(float (&acc)[NT][4], float (&low)[LO ? 
                 split_pair(va.x, va.y, a[i], al[i]);
                 split_pair(vb.x, vb.y, b[i], bl[i]);
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma_16816<true>(low[n], al[0], bl[0], al[1], bl[1], f.x[u].h[n].x, f.x[u].h[n].y);
-                mma_16816<true>(low[n], al[2], bl[2], al[3], bl[3], f.x[u].h[n].z, f.x[u].h[n].w);
-            }
+            piece_mma<true, NT, DOWN, 2>(acc, 1, al, bl, f.x[u]);
         }
-        piece_mma<BF || SPLITW, NT, LO>(acc, low, a, b, f.x[u]);
+        piece_mma<BF || SPLITW, NT, DOWN, MoeTokens<NT, DOWN>::PARTS>(acc, 0, a, b, f.x[u]);
     }
 }
 
+template <bool DOWN>
 __device__ __forceinline__ void give_back(const MoePipe &m, MoeWalk &walk, int s, int stages)
 {
-    const bool last = s % MOE_SPAN == MOE_SPAN - 1 || s == stages - 1;      // of its stage of tokens
+    const bool last = s % MOE_SPAN<DOWN> == MOE_SPAN<DOWN> - 1 || s == stages - 1;      // of its stage of tokens
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
         ptx::mbar_arrive(m.pp.empty0 + 8 * walk.w.slot);
@@ -270,23 +298,27 @@ __device__ __forceinline__ void give_back(const MoePipe &m, MoeWalk &walk, int s
 }
 
 // One warp's rows of an item over all of K.
-template <bool BF, int NT, bool LO, bool SPLITW>
-__device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
+template <bool BF, int NT, bool DOWN, bool SPLITW>
+__device__ __forceinline__ bool item_mma(float (&sum)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
                                          MoeWalk &walk)
 {
-    float low[LO ? NT : 1][4] = {};
+    constexpr int PARTS = MoeTokens<NT, DOWN>::PARTS;
+    float acc[PARTS][NT][4] = {};
 #pragma unroll 1
     for (int s = 0; s < pr.stages; ++s) {
-        MoeFragments<NT, LO> f;
-        if (!fetch<NT, LO>(f, m, it, walk, s)) return false;
-        multiply<BF, NT, LO, SPLITW>(acc, low, f);
-        give_back(m, walk, s, pr.stages);
+        MoeFragments<NT, DOWN> f;
+        if (!fetch<NT, DOWN>(f, m, it, walk, s)) return false;
+        multiply<BF, NT, DOWN, SPLITW>(acc, f);
+        give_back<DOWN>(m, walk, s, pr.stages);
     }
-    if constexpr (LO)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[n][j] += low[n][j];
+        for (int i = 0; i < 4; ++i) {                          // the smallest first
+            sum[n][i] = acc[PARTS - 1][n][i];
+#pragma unroll
+            for (int j = PARTS - 2; j >= 0; --j) sum[n][i] += acc[j][n][i];
+        }
     return true;
 }
 
@@ -302,7 +334,7 @@ __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, c
     MoeItem it;
     it.row = (uint32_t)(8 * w + g) * 128u;
     it.upper = (uint32_t)p.half_rows * 128u;
-    float acc[NT][4] = {};
+    float acc[NT][4];
     if (!item_mma<XT == OUT_BF16, NT, DOWN, DOWN && XT == OUT_F16>(acc, m, pr, it, walk)) return false;
 
     // acc[n][0..1]: the lower row, tokens n * 8 + 2 t4 and the next; acc[n][2..3]: the upper row
@@ -324,12 +356,7 @@ __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, c
                 if (in1) p.part[s * p.H + r] = v1;
                 if (in2) p.part[s * p.H + r2] = v2;
             } else {
-                auto put = [&](int row, float v) {
-                    const int64_t at = s * p.Ip + row;
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                    p.h_hi[at] = __bfloat16_as_ushort(hi);
-                    p.h_lo[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v - __bfloat162float(hi)));
-                };
+                auto put = [&](int row, float v) { put_parts(p.h + h_at(p, s, row), v); };
                 v1 = act_mx(p.act, v1, p.alpha);
                 if (gated) {
                     if (in1) put(r, v1 * v2);
@@ -390,18 +417,14 @@ __device__ __forceinline__ bool produce_tokens(const MoeArgs &p, const MoeShared
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int ai = i / pr.tiles, first = S.first[ai], cnt = S.first[ai + 1] - first;
         const int64_t slot_of = lane < cnt ? S.slot[first + lane] : 0;
-        const int64_t from = DOWN ? slot_of * p.Ip : slot_of / p.top * p.Hp;
-        const uint16_t *hi = (DOWN ? p.h_hi : p.x_pad) + from, *lo = p.h_lo + from;
+        const uint16_t *from = DOWN ? p.h + slot_of * p.Ip * MOE_PARTS : p.x_pad + slot_of / p.top * p.Hp;
         for (int s = 0; s < pr.tstages; ++s, to.next(m.tstages)) {
             const uint32_t full = m.tfull0 + 8 * to.slot;
             const uint32_t at = m.tokens + to.slot * m.token_bytes + (uint32_t)lane * MOE_RECORD;
             if (!mx_warp_wait(m.pp, m.tempty0 + 8 * to.slot, to.phase ^ 1u)) return false;
-            elected_expect_tx(full, (uint32_t)cnt * MOE_TOKEN * (DOWN ? 2u : 1u));
+            elected_expect_tx(full, (uint32_t)cnt * MOE_TOKEN<DOWN>);
             __syncwarp();
-            if (lane < cnt) {
-                bulk_load(at, hi + s * MOE_TOKEN_K, MOE_TOKEN, full);
-                if constexpr (DOWN) bulk_load(at + MOE_TOKEN, lo + s * MOE_TOKEN_K, MOE_TOKEN, full);
-            }
+            if (lane < cnt) bulk_load(at, from + s * (MOE_TOKEN<DOWN> / 2), MOE_TOKEN<DOWN>, full);
             __syncwarp();
         }
     }
@@ -461,7 +484,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
     plan_experts<MOE_GROUP, MOE_THREADS>(p, S, reinterpret_cast<uint32_t *>(smem),
                                          reinterpret_cast<uint32_t *>(smem + p.T * p.E * 4));
 
-    const MoeProduct up = up_product(p, MOE_STAGE_K, MOE_TOKEN_K), down = down_product(p, MOE_STAGE_K, MOE_TOKEN_K);
+    const MoeProduct up = up_product(p, MOE_STAGE_K, MOE_TOKEN_K<false>), down = down_product(p, MOE_STAGE_K, MOE_TOKEN_K<true>);
     bool ok = aligned;
     if (warp == 0) {
         MoePlace to = {0, 0};

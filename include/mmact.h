@@ -589,7 +589,7 @@ mmact_status mmact_set_gemm_mxfp4_kernel(int mode);
  *   workspace  at least mmact_moe_workspace_bytes, 16-byte aligned, contents
  *      ignored; calls that may overlap on the GPU need one each
  * Sums, the softmax and h are held in fp32; y is rounded once.  16-bit weights:
- * h stands as two bf16 halves, 16 bits of it, between the products.  MXFP4
+ * h stands as three bf16 parts, which hold it exactly, between the products.  MXFP4
  * weights are multiplied as they are: x and h stand as sums of eight MXFP4
  * terms, which leave out at most 2^-23 of the largest of 32 values, and
  * an x with an infinity or a NaN makes its token's y NaN.  The sum over j is

@@ -1,0 +1,45 @@
+"""What the mixture-of-experts layer keeps of h, its intermediate, on the GPU: the down
+product takes differences of values of h that agree in their first 16 bits, so that y
+shows the bits that follow."""
+import numpy as np
+import pytest
+import torch
+
+import mx_reference as ref
+from conv_activation_epilogue_gb300 import build, mmact
+from test_gpu_moe import run
+from test_gpu_mxfp4 import host64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    mmact.load()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,I", [(1, 272), (12, 272), (24, 48), (64, 640)])
+def test_h_keeps_the_bits_of_fp32(dtype, T, I):
+    """h[i] = (1 + a 2^-12 + b 2^-23) s, whole a and b, the same a for h[2 r] and h[2 r + 1];
+    y[r] = h[2 r] - h[2 r + 1].  Bound: h is a sum of three products and y one of two values,
+    in at most three parts each (sum_error)."""
+    rng = np.random.default_rng(T + I)
+    H, E = I // 2, 3
+    L = {"x": np.zeros((T, H)), "router": np.zeros((E, H)), "rb": np.array([0.0, 2.0, 1.0]), "b1": None, "b2": None,
+         "w1": np.zeros((E, I, H)), "w2": np.zeros((E, H, I))}
+    s = np.exp2(rng.integers(0, 2, T))                         # one in fp16 has 2^-23 as a subnormal
+    L["x"][:, 0], L["x"][:, 1], L["x"][:, 2] = s, s * 2.0 ** -12, s * 2.0 ** -23
+    a, b = rng.integers(-127, 128, (E, H)).repeat(2, axis=1), rng.integers(-127, 128, (E, I))
+    L["w1"][:, :, 0], L["w1"][:, :, 1], L["w1"][:, :, 2] = 1.0, a, b
+    r = np.arange(H)
+    L["w2"][:, r, 2 * r], L["w2"][:, r, 2 * r + 1] = 1.0, -1.0
+    y, experts, _, _, _ = run(L, 1, dtype, dtype, "none", gated=False)
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+    assert torch.all(experts == 1)
+    want = s[:, None] * (b[1, 0::2] - b[1, 1::2]) * 2.0 ** -23
+    mag = 1.0 + 127 * 2.0 ** -12 + 127 * 2.0 ** -23
+    bound = s[:, None] * mag * 2.0 * (ref.sum_error(3) + ref.sum_error(6))
+    err = np.abs(host64(y) - want)
+    assert np.all(err <= bound + ref.ulp(np.abs(want) + bound, dtype)), float((err / bound).max())
