@@ -100,6 +100,10 @@ constexpr bool layout_fits()
 static_assert(layout_fits(), "rings, logits and bits");
 
 // ------------------------------------------------------------------ helpers --
+// c += a 16 x 16 tile of weights by 16 x 8 of tokens.  The tensor core does not round
+// this sum but truncates it: over 256 of these in a row, 4096 K of products of one sign,
+// sums were measured 100 (bf16) to 220 (fp16) units of 2^-23 too small, so that more
+// of y's bf16 values than with sums rounded to nearest came out a step away.
 template <bool BF16>
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1)
@@ -195,20 +199,13 @@ __device__ __forceinline__ void load_tokens(MoeTokens<NT, DOWN> &x, uint32_t at)
         for (int j = 0; j < MoeTokens<NT, DOWN>::PARTS; ++j) x.v[j][n] = ptx::ld_shared_v4(at + n * 8 * MOE_RECORD + j * MOE_PART);
 }
 
-// acc[j] += 16 rows x part j of the tokens over one piece: a, b the two rows' four
-// pairs of values.  The parts have sums of their own, so that fewer instructions
-// wait for one another.
-template <bool BF, int NT, bool DOWN, int PARTS>
-__device__ __forceinline__ void piece_mma(float (&acc)[MoeTokens<NT, DOWN>::PARTS][NT][4], int first, const uint32_t (&a)[4],
-                                          const uint32_t (&b)[4], const MoeTokens<NT, DOWN> &x)
+// c += 16 rows x eight tokens over one piece: a, b the two rows' four pairs of values,
+// v the tokens'.
+template <bool BF>
+__device__ __forceinline__ void piece_mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[4], const uint4 &v)
 {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int j = 0; j < PARTS; ++j) mma_16816<BF>(acc[first + j][n], a[0], b[0], a[1], b[1], x.v[j][n].x, x.v[j][n].y);
-#pragma unroll
-        for (int j = 0; j < PARTS; ++j) mma_16816<BF>(acc[first + j][n], a[2], b[2], a[3], b[3], x.v[j][n].z, x.v[j][n].w);
-    }
+    mma_16816<BF>(c, a[0], b[0], a[1], b[1], v.x, v.y);
+    mma_16816<BF>(c, a[2], b[2], a[3], b[3], v.z, v.w);
 }
 
 // The rings of one CTA.
@@ -262,25 +259,38 @@ __device__ __forceinline__ bool fetch(MoeFragments<NT, DOWN> &f, const MoePipe &
     return true;
 }
 
-// SPLITW: fp16 weights as two bf16 halves, whose lo halves meet the tokens' first two
-// parts only.
+// A stage's products.  Each piece has a sum of its own on the tensor core, a few
+// instructions long, its smallest parts first, which is added to the running sum by an
+// fp32 addition.  SPLITW: fp16 weights as two bf16 halves, whose lo halves meet the
+// tokens' first two parts only.
 template <bool BF, int NT, bool DOWN, bool SPLITW>
-__device__ __forceinline__ void multiply(float (&acc)[MoeTokens<NT, DOWN>::PARTS][NT][4], const MoeFragments<NT, DOWN> &f)
+__device__ __forceinline__ void multiply(float (&acc)[NT][4], const MoeFragments<NT, DOWN> &f)
 {
 #pragma unroll
     for (int u = 0; u < 2 * MOE_BOXES; ++u) {
         uint32_t a[4] = {f.a[u].x, f.a[u].y, f.a[u].z, f.a[u].w}, b[4] = {f.b[u].x, f.b[u].y, f.b[u].z, f.b[u].w};
+        uint32_t al[4], bl[4];
         if constexpr (SPLITW) {
-            uint32_t al[4], bl[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 va = unpack2<OUT_F16>(a[i]), vb = unpack2<OUT_F16>(b[i]);
                 split_pair(va.x, va.y, a[i], al[i]);
                 split_pair(vb.x, vb.y, b[i], bl[i]);
             }
-            piece_mma<true, NT, DOWN, 2>(acc, 1, al, bl, f.x[u]);
         }
-        piece_mma<BF || SPLITW, NT, DOWN, MoeTokens<NT, DOWN>::PARTS>(acc, 0, a, b, f.x[u]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float c[4] = {};
+#pragma unroll
+            for (int j = MoeTokens<NT, DOWN>::PARTS - 1; j >= 0; --j) {
+                if constexpr (SPLITW) {
+                    if (j < MOE_PARTS - 1) piece_mma<true>(c, al, bl, f.x[u].v[j][n]);
+                }
+                piece_mma<BF || SPLITW>(c, a, b, f.x[u].v[j][n]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] += c[i];
+        }
     }
 }
 
@@ -299,11 +309,9 @@ __device__ __forceinline__ void give_back(const MoePipe &m, MoeWalk &walk, int s
 
 // One warp's rows of an item over all of K.
 template <bool BF, int NT, bool DOWN, bool SPLITW>
-__device__ __forceinline__ bool item_mma(float (&sum)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
+__device__ __forceinline__ bool item_mma(float (&acc)[NT][4], const MoePipe &m, const MoeProduct &pr, const MoeItem &it,
                                          MoeWalk &walk)
 {
-    constexpr int PARTS = MoeTokens<NT, DOWN>::PARTS;
-    float acc[PARTS][NT][4] = {};
 #pragma unroll 1
     for (int s = 0; s < pr.stages; ++s) {
         MoeFragments<NT, DOWN> f;
@@ -311,14 +319,6 @@ __device__ __forceinline__ bool item_mma(float (&sum)[NT][4], const MoePipe &m, 
         multiply<BF, NT, DOWN, SPLITW>(acc, f);
         give_back<DOWN>(m, walk, s, pr.stages);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {                          // the smallest first
-            sum[n][i] = acc[PARTS - 1][n][i];
-#pragma unroll
-            for (int j = PARTS - 2; j >= 0; --j) sum[n][i] += acc[j][n][i];
-        }
     return true;
 }
 
@@ -334,7 +334,7 @@ __device__ __forceinline__ bool run_item(const MoeArgs &p, const MoeShared &S, c
     MoeItem it;
     it.row = (uint32_t)(8 * w + g) * 128u;
     it.upper = (uint32_t)p.half_rows * 128u;
-    float acc[NT][4];
+    float acc[NT][4] = {};
     if (!item_mma<XT == OUT_BF16, NT, DOWN, DOWN && XT == OUT_F16>(acc, m, pr, it, walk)) return false;
 
     // acc[n][0..1]: the lower row, tokens n * 8 + 2 t4 and the next; acc[n][2..3]: the upper row

@@ -8,7 +8,7 @@ import torch
 import mx_reference as ref
 from conv_activation_epilogue_gb300 import build, mmact
 from test_gpu_moe import run
-from test_gpu_mxfp4 import host64
+from test_gpu_mxfp4 import host64, tensor
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,44 @@ def test_h_keeps_the_bits_of_fp32(dtype, T, I):
     bound = s[:, None] * mag * 2.0 * (ref.sum_error(3) + ref.sum_error(6))
     err = np.abs(host64(y) - want)
     assert np.all(err <= bound + ref.ulp(np.abs(want) + bound, dtype)), float((err / bound).max())
+
+
+def sum_bound(products: np.ndarray, instructions: int) -> np.ndarray:
+    """Bound on a sum of positive products along the last axis that is taken in pieces of 32: each
+    piece by that many instructions of the tensor core, each off by at most two units of 2^-23 of the
+    piece, each running sum by half a unit."""
+    n = products.shape[-1]
+    assert n % 32 == 0
+    running = products.reshape(*products.shape[:-1], n // 32, 32).sum(axis=-1).cumsum(axis=-1)
+    return 2.0 ** -23 * (2 * instructions * running[..., -1] + 0.5 * running.sum(axis=-1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [1, 12, 24])
+@pytest.mark.parametrize("product", ["up", "down"])
+def test_long_sums_are_not_truncated(dtype, T, product):
+    """4096 products of one sign, and a bias of their sum, negative, rounded to fp32: what is left is
+    the sum's error (a sum that is truncated in every step loses 100 to 200 units of 2^-23)."""
+    K, R = 4096, 64
+    rng = np.random.default_rng(T)
+    a = host64(tensor(rng.uniform(0.5, 2.0, K), dtype))
+    w = host64(tensor(rng.uniform(0.5, 2.0, (R, K)), dtype))
+    exact = w @ a
+    bias = -exact.astype(np.float32).astype(np.float64)
+    if product == "up":
+        H, I = K, R
+        L = {"x": np.tile(a, (T, 1)), "w1": w[None], "b1": bias[None], "w2": np.zeros((1, H, I)), "b2": None}
+        L["w2"][0, np.arange(R), np.arange(R)] = 1.0
+        instructions = 2
+    else:
+        H, I = R, K
+        L = {"x": np.zeros((T, H)), "w1": np.zeros((1, I, H)), "b1": None, "w2": w[None], "b2": bias[None]}
+        L["x"][:, 0], L["w1"][0, :, 0] = 1.0, a
+        instructions = 10                                      # h in three parts, an fp16 weight in two
+    L["router"], L["rb"] = np.zeros((1, H)), None
+    y = run(L, 1, dtype, dtype, "none", gated=False)[0]
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+    want, bound = exact + bias, sum_bound(w * a, instructions)
+    got = host64(y)[:, :R]
+    lim = bound + ref.ulp(np.abs(want) + bound, dtype)
+    assert np.all(np.abs(got - want) <= lim), float((np.abs(got - want) / lim).max())
