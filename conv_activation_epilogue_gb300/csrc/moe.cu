@@ -127,23 +127,32 @@ __device__ __forceinline__ int64_t h_at(const MoeArgs &p, int64_t slot, int row)
     return slot * p.Ip * MOE_PARTS + row / MOE_STAGE_K * (MOE_PARTS * MOE_STAGE_K) + row % MOE_STAGE_K;
 }
 
-// h as three bf16 parts: the first 8 bits, the next, the last.
+// h as three bf16 parts: the first 8 bits, the next, the last.  All of them have h's
+// sign and none is 0 unless h is (a part that leaves nothing for the next ones is
+// taken one step smaller), so that an infinite weight makes the infinity that it makes
+// with h itself, and no NaN.  An infinite h is 1 + 1 + infinity: what meets the last part
+// are the weights' hi halves, which are 0 only where the weights are.
 __device__ __forceinline__ void put_parts(uint16_t *h, float v)
 {
+    const bool inf = (__float_as_uint(v) & 0x7fffffffu) == 0x7f800000u;
 #pragma unroll
-    for (int j = 0; j < MOE_PARTS; ++j) {
-        const uint32_t b = __float_as_uint(v) & 0xffff0000u;
+    for (int j = 0; j < MOE_PARTS - 1; ++j) {
+        uint32_t b = __float_as_uint(v) & 0xffff0000u;
+        if (v == __uint_as_float(b) && v != 0.0f) b -= 0x10000u;
+        if (inf) b = 0x3f800000u | (b & 0x80000000u);
         h[j * MOE_STAGE_K] = (uint16_t)(b >> 16);
         v -= __uint_as_float(b);
     }
+    h[(MOE_PARTS - 1) * MOE_STAGE_K] = (uint16_t)(__float_as_uint(v) >> 16);
 }
 
-// Hi and lo bf16 halves of a pair of fp32 values.
+// Hi and lo bf16 halves of a pair of fp16 values.  Where a value is infinite, lo is the
+// number 256 and not the NaN of inf - inf: no lo is above 128.
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo)
 {
     hi = pack2<OUT_BF16>(a, b);
     const float2 f = unpack2<OUT_BF16>(hi);
-    lo = pack2<OUT_BF16>(a - f.x, b - f.y);
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(pack2<OUT_BF16>(a - f.x, b - f.y)), "r"(0x43804380u));
 }
 
 // ------------------------------------------------------------------- router --

@@ -591,10 +591,10 @@ mmact_status mmact_set_gemm_mxfp4_kernel(int mode);
  * Sums, the softmax and h are held in fp32; y is rounded once.  16-bit weights:
  * h stands as three bf16 parts, which hold it exactly, between the products.  MXFP4
  * weights are multiplied as they are: x and h stand as sums of eight MXFP4
- * terms, which leave out at most 2^-23 of the largest of 32 values, and
- * an x with an infinity or a NaN makes its token's y NaN.  The sum over j is
- * taken in order: results repeat bit for bit.  Limits: H and I multiples of 8 and at
- * least 8, 1 <= top <= min(E, 16), E <= 512, T <= 64, else
+ * terms, which leave out at most 2^-23 of the largest of 32 values; an x with an
+ * infinity or a NaN, or an h that overflows, makes its token's y NaN.  The sum over
+ * j is taken in order: results repeat bit for bit.  Limits: H and I multiples of 8
+ * and at least 8, 1 <= top <= min(E, 16), E <= 512, T <= 64, else
  * MMACT_ERR_UNSUPPORTED.  T == 0 enqueues nothing.
  */
 mmact_status mmact_moe(const void *x, const void *router, const float *router_bias, const void *w1,

@@ -84,3 +84,42 @@ def test_long_sums_are_not_truncated(dtype, T, product):
     got = host64(y)[:, :R]
     lim = bound + ref.ulp(np.abs(want) + bound, dtype)
     assert np.all(np.abs(got - want) <= lim), float((np.abs(got - want) / lim).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [2, 20])
+def test_infinite_h_and_weights_give_what_the_formula_gives(dtype, T):
+    """h from a bias of infinities (an h that overflowed), weights that are infinite: y is the
+    infinity of the formula, or NaN where that has 0 x inf or inf - inf."""
+    H, I, inf = 16, 24, np.inf
+    L = {"x": np.zeros((T, H)), "router": np.zeros((1, H)), "rb": None, "w1": np.zeros((1, I, H)), "b1": np.zeros((1, I)),
+         "w2": np.zeros((1, H, I)), "b2": None}
+    L["x"][:, 0] = 1.0
+    L["w1"][0, :, 0] = np.array([1.0, -2.0, 0.0, 0.5, 1.2578125, -1.0] * 4)       # h, with b1
+    w2 = L["w2"][0]
+    w2[:, 0] = np.arange(H) - 3.0
+    w2[0, 0], w2[1, 0], w2[2, 1], w2[3, 1], w2[4, 4] = inf, -inf, inf, -inf, inf
+    w2[5, 0], w2[5, 1] = inf, inf                              # inf - inf
+    w2[6, 2] = inf                                             # inf x 0
+    w2[7, 1], w2[7, 4] = -inf, inf
+    for case in range(3):
+        if case == 1:                                          # from here on two values of h are infinite
+            L["b1"][0, 8], L["b1"][0, 9] = inf, -inf
+        if case == 2:
+            w2[:, 8], w2[:, 9] = 1.0 / 3.0, -0.125              # f16: with lo halves
+            w2[8, 9], w2[9, 8], w2[10, 8], w2[10, 9] = 0.0, -100.3, inf, -inf
+            w2[11, 8], w2[11, 9] = 3.0e-5, -60001.0
+        for k in ("w1", "w2"):
+            L[k] = host64(tensor(L[k], dtype))
+        w2 = L["w2"][0]
+        y = host64(run(L, 1, dtype, dtype, "none", gated=False)[0])
+        with np.errstate(invalid="ignore"):
+            h = L["w1"][0] @ L["x"][0] + L["b1"][0]
+            want = (w2 * h).sum(axis=1)
+        assert np.isnan(want).any() and np.isinf(want).any() == (case != 1)
+        for t in range(T):
+            assert np.array_equal(np.isnan(y[t]), np.isnan(want)), (case, t, y[t], want)
+            bad = ~np.isfinite(want)
+            assert np.array_equal(y[t][bad & ~np.isnan(want)], want[bad & ~np.isnan(want)])
+            assert np.all(np.abs(y[t][~bad] - want[~bad]) <= ref.ulp(want[~bad], dtype))
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
