@@ -218,10 +218,19 @@ __device__ __forceinline__ float silu_f32(float z)
     return z < -87.0f ? z * 0.0f : __fdividef(z, 1.0f + __expf(-z));
 }
 
+// max(z, 0), NaN for a NaN: a block that the quantiser marked must not come out as zeros.
+__device__ __forceinline__ float relu_f32(float z)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));
+    return r;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_mx(float z, float alpha)
 {
     if constexpr (ACT == ACT_SILU) return silu_f32(z);
+    else if constexpr (ACT == ACT_RELU) return relu_f32(z);
     else return act_f32<ACT>(z, alpha);
 }
 
