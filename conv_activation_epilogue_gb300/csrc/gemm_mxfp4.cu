@@ -48,7 +48,7 @@ struct MxPairCfg {
     static constexpr int OFF_BAR = OFF_S + STAGES * S_BYTES;
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
-    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(SMEM_BYTES <= CTA_SMEM && SMEM_BYTES >= tmem_min_smem((int)TMEM_COLS), "shared memory budget");
     static_assert(SCALE_COL + STAGES * SLOT_COLS <= TMEM_COLS, "tensor memory budget");
 };
 

@@ -33,34 +33,10 @@
 
 #include "common.cuh"
 #include "kernels_mx.h"
+#include "mx_layout.h"
 #include "mxfp4.cuh"
 
 namespace mmact {
-
-// Shared memory: barriers, then the ring: p.stages of weights, of tokens, of scales
-// (as many as the K blocks of a CTA ask for, so that small products leave room for
-// the next kernel's CTAs, whose set-up then overlaps).
-template <int BT>
-struct MxRowsCfg {
-    static constexpr int W_BYTES = 128 * 128, T_BYTES = BT * 128, S_BYTES = 2 * 1024;
-    static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + S_BYTES;
-    // Up to 32 rows: two CTAs fit on an SM, for the same overlap; else as many as fit.
-    static constexpr int MAX_STAGES = MX_ROWS_STAGES(BT);
-    static constexpr uint32_t SCALE_COL = BT;                            // 16 columns for each stage
-    static constexpr uint32_t TMEM_COLS = BT + 16 * MAX_STAGES <= 128 ? 128 : 256;
-    static constexpr int OFF_BAR = 0, OFF_MISC = (2 * MAX_STAGES + 2) * 8, OFF_RING = 1024;
-    static constexpr int PART_BYTES = BT * 512;                          // a partial tile, over the ring
-    // at least so much that no more CTAs share an SM's 227 KB than its 512 columns of tensor memory serve
-    static constexpr int MIN_SMEM = 232448 / (512 / (int)TMEM_COLS + 1) + 1024;
-    static int smem_bytes(const MxRowsArgs &a)
-    {
-        const int ring = OFF_RING + a.stages * STAGE_BYTES, part = a.split > 1 ? OFF_RING + PART_BYTES : 0;
-        const int need = ring > part ? ring : part;
-        return need > MIN_SMEM ? need : MIN_SMEM;
-    }
-    static_assert(OFF_MISC + 16 <= OFF_RING && OFF_RING + MAX_STAGES * STAGE_BYTES <= 232448, "shared memory budget");
-    static_assert(BT + 16 * MAX_STAGES <= TMEM_COLS, "tensor memory budget");
-};
 
 // C[m0 + j][n] = act(z[j] + bias) for this lane's n and the rows that exist:
 // element stores, a warp covering 32 consecutive n.
@@ -218,8 +194,8 @@ __global__ void __launch_bounds__(ROWS_THREADS<XT>, 1)
     ptx::griddep_wait();
     // Tensor memory is taken when the kernels before this one are done, and the next
     // one may start when every CTA of this one has it: a CTA that holds tensor memory
-    // never waits for one that still needs it.  (CTAs of this kernel that share an SM
-    // find room for all of them: smem_bytes sees to that.)
+    // never waits for one of its stream that still needs it.  Nor for one of another
+    // stream: CTAs that share an SM all find their columns (see MxRowsCfg).
     if (warp >= 1 && warp < 6) {
         if (warp == 1 && aligned) {
             ptx::tmem_alloc(base + Cfg::OFF_MISC, Cfg::TMEM_COLS);
@@ -358,7 +334,7 @@ static cudaError_t launch_rows_t(const MxRowsLaunch &L, cudaStream_t stream)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)L.grid);
     cfg.blockDim = dim3(ROWS_THREADS<XT>);
-    cfg.dynamicSmemBytes = (size_t)MxRowsCfg<BT>::smem_bytes(L.args);
+    cfg.dynamicSmemBytes = (size_t)MxRowsCfg<BT>::smem_bytes(L.args.stages, L.args.split);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

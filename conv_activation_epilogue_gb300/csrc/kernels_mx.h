@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "mmact.h"
+#include "mx_layout.h"
 
 namespace mmact {
 
@@ -65,8 +66,6 @@ struct MxRowsLaunch {
     int x_type;          // OUT_* of args.x; < 0: A is tmT, tmST
     int grid;
 };
-
-constexpr int MX_ROWS_STAGES(int bt) { return bt <= 32 ? 5 : (bt == 64 ? 8 : 6); }   // at most
 
 // max_clusters[i]: clusters of 2^i CTAs resident at once, one CTA to an SM
 cudaError_t setup_mxfp4_rows_kernels(int (&max_clusters)[4]);

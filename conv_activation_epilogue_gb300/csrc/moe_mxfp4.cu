@@ -44,7 +44,7 @@ constexpr int MXE_OFF_EX = MXE_OFF_S + MXE_STAGES * MXE_S_BYTES;     // [token][
 constexpr int MXE_OFF_SHARED = MXE_OFF_EX + MXE_GROUP * 128 * 4;
 constexpr int MXE_SMEM = MXE_OFF_SHARED + (int)sizeof(MoeShared);
 constexpr uint32_t MXE_ACC = 128, MXE_SCALE_COL = 256, MXE_TMEM = 512;
-static_assert(MXE_SMEM <= 232448, "shared memory budget");
+static_assert(MXE_SMEM <= CTA_SMEM && MXE_SMEM >= tmem_min_smem((int)MXE_TMEM), "shared memory budget");
 static_assert(MXE_SCALE_COL + 16 * MXE_STAGES <= MXE_TMEM, "tensor memory budget");
 static_assert(2 * MXE_STAGES + 5 <= MOE_MAX_BARS, "barriers");
 static_assert(MOE_MAX_T * MOE_MAX_E * 4 <= MXE_OFF_S, "all logits");
