@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
     if (at == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
     if (k < p.Hp)
         *reinterpret_cast<uint4 *>(p.x_pad + (int64_t)t * p.Hp + k) =
-            k < p.H ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.H + k))
+            k < p.H ? __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.H + k))
                     : make_uint4(0, 0, 0, 0);
     if (at != t * chunks) return;
     const int pad = (p.Ip - p.I) / 8;                          // eights of zeros past h's rows

@@ -80,11 +80,11 @@ __device__ __forceinline__ void router_logits(const MoeArgs &p, int block, int t
     const uint16_t *r = static_cast<const uint16_t *>(p.router) + (int64_t)e * p.H;
     float s[8] = {};
     for (int k = threadIdx.x * 8; k < p.H; k += MOE_ROUTER_K) {
-        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(r + k));
+        const uint4 b = *reinterpret_cast<const uint4 *>(r + k);
         const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
         uint4 a[8];                                        // tokens past the last one: the last one again
 #pragma unroll
-        for (int t = 0; t < 8; ++t) a[t] = __ldg(reinterpret_cast<const uint4 *>(xs + (int64_t)(t0 + min(t, n - 1)) * p.H + k));
+        for (int t = 0; t < 8; ++t) a[t] = *reinterpret_cast<const uint4 *>(xs + (int64_t)(t0 + min(t, n - 1)) * p.H + k);
         float2 g[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[j] = unpack2<XT>(bw[j]);

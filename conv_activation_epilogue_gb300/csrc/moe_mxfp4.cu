@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_mxfp4_router_kernel(co
     const int k = (at - t * chunks) * MOE_ROUTER_K + (int)threadIdx.x * 8, stages = p.Hp / MXE_K;
     if (at == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0;
     uint4 raw = make_uint4(0, 0, 0, 0);
-    if (k < p.H) raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.H + k));
+    if (k < p.H) raw = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.H + k));
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float r[8];
 #pragma unroll
@@ -228,8 +228,8 @@ __device__ __forceinline__ bool mxe_scales(const MoeArgs &p, const MoeShared &S,
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 const int s = s0 + d;
-                a[d][0] = has_row && 2 * s < tiles ? __ldg(reinterpret_cast<const uint32_t *>(wp + (int64_t)s * 1024)) : 0u;
-                a[d][1] = has_row && 2 * s + 1 < tiles ? __ldg(reinterpret_cast<const uint32_t *>(wp + (int64_t)s * 1024 + 512)) : 0u;
+                a[d][0] = has_row && 2 * s < tiles ? *reinterpret_cast<const uint32_t *>(wp + (int64_t)s * 1024) : 0u;
+                a[d][1] = has_row && 2 * s + 1 < tiles ? *reinterpret_cast<const uint32_t *>(wp + (int64_t)s * 1024 + 512) : 0u;
                 b[d] = has_term && s < pr.stages ? __ldcg(reinterpret_cast<const uint2 *>(tp + s * MXE_ATOM_SCALES)) : make_uint2(0, 0);
             }
 #pragma unroll

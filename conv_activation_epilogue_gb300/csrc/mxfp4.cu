@@ -24,8 +24,8 @@ __device__ __forceinline__ void store1(void *p, int64_t i, float v)
 // 2^lanes_log2 consecutive lanes take the blocks of a row; rows past the last
 // one, up to a multiple of 128, only get their zero scales.
 template <int T, bool VEC>
-__global__ void __launch_bounds__(256) quantize_kernel(const void *__restrict__ x, uint8_t *__restrict__ codes,
-                                                       uint8_t *__restrict__ scales, int64_t rows, int64_t K,
+__global__ void __launch_bounds__(256) quantize_kernel(const void *x, uint8_t *codes,
+                                                       uint8_t *scales, int64_t rows, int64_t K,
                                                        int lanes_log2, int segs)
 {
     ptx::griddep_launch_dependents();
@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void *__restrict__ 
 // The eight warps of a CTA take eight consecutive blocks, and the codes go
 // through shared memory so that each row's 128 bytes are written together.
 template <int T, bool VEC>
-__global__ void __launch_bounds__(256) quantize_trans_kernel(const void *__restrict__ x, uint8_t *__restrict__ codes,
-                                                             uint8_t *__restrict__ scales, int64_t rows, int64_t K,
+__global__ void __launch_bounds__(256) quantize_trans_kernel(const void *x, uint8_t *codes,
+                                                             uint8_t *scales, int64_t rows, int64_t K,
                                                              int col_tiles)
 {
     constexpr int WPP = T == IN_F32 ? 2 : 1;                   // words of a pair of columns
@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(256) quantize_trans_kernel(const void *__restr
 // lane; a block of 256 threads covers `tpr` tiles (a power of two, at most 16) of
 // 16 / tpr rows, U times (U sets of loads in flight).
 template <int T, bool VEC, int U>
-__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restrict__ codes,
-                                                         const uint8_t *__restrict__ scales, void *__restrict__ y,
+__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes,
+                                                         const uint8_t *scales, void *y,
                                                          int64_t rows, int64_t K, int tpr_log2, int segs)
 {
     ptx::griddep_launch_dependents();
@@ -308,7 +308,7 @@ static cudaError_t dequantize_t(const uint8_t *codes, const uint8_t *scales, voi
 }
 
 template <int T>
-__global__ void __launch_bounds__(256) mx_bias_act_kernel(const float *__restrict__ bias, void *__restrict__ out,
+__global__ void __launch_bounds__(256) mx_bias_act_kernel(const float *bias, void *out,
                                                           int64_t rows, int64_t cols, int act, float alpha)
 {
     ptx::griddep_launch_dependents();

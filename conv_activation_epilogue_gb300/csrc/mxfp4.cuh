@@ -97,7 +97,9 @@ __device__ __forceinline__ void mx_decode8(uint32_t c, float (&v)[8])
 enum : int { IN_F32 = OUT_F32, IN_F16 = OUT_F16, IN_BF16 = OUT_BF16 };
 
 // Eight consecutive values x[i..i+8) as raw 32-bit words, two 16-bit values or
-// one fp32 to a word (values at or past `n` are 0).
+// one fp32 to a word (values at or past `n` are 0).  (Here and in the kernels no input
+// is read through the read-only path: a kernel is on its SMs before griddep_wait
+// returns, while the one before it may still write what it will read.)
 template <int T>
 struct Raw8 {
     static constexpr int WORDS = T == IN_F32 ? 8 : 4;
@@ -111,7 +113,7 @@ __device__ __forceinline__ void load8(const void *x, int64_t i, int n, Raw8<T> &
 #pragma unroll
         for (int j = 0; j < Raw8<T>::WORDS / 4; ++j) {
             const char *p = static_cast<const char *>(x) + i * (T == IN_F32 ? 4 : 2) + 16 * j;
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
             r.w[4 * j] = u.x, r.w[4 * j + 1] = u.y, r.w[4 * j + 2] = u.z, r.w[4 * j + 3] = u.w;
         }
     } else {
@@ -147,7 +149,7 @@ __device__ __forceinline__ void load32_any(const void *x, int64_t at, int n, int
     uint32_t u[WORDS + 4];
 #pragma unroll
     for (int c = 0; c <= WORDS / 4; ++c) {
-        const uint4 v = 16 * c < bytes ? __ldg(p + c) : make_uint4(0, 0, 0, 0);
+        const uint4 v = 16 * c < bytes ? p[c] : make_uint4(0, 0, 0, 0);
         u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
     }
     if (shift & 8)
