@@ -46,58 +46,6 @@ namespace mmact {
 
 constexpr int MOE_MMA_WARPS = 8;
 constexpr int MOE_THREADS = 32 * (2 + MOE_MMA_WARPS);
-constexpr int MOE_GROUP = 32;                                  // tokens of one expert that share a read of its weights
-
-// Two rings.  A stage of weights is 128 K of a tile, two boxes of 64 K for each half:
-// with 64 K a stage, what a warp does once a stage (waits, addresses, giving it back)
-// took longer than the multiplication (one token, 2 of 8 experts of 4096 x 1792: 47.7 us,
-// with 128 K 41.6; 64 tokens, 8 of 64 experts: 456 and 445).  A stage of tokens is the
-// group's tokens, a record for each and a copy to a record: x over 256 K (two stages of
-// weights, 512 bytes), or h over 128 K (its three parts, 768 bytes), because copies of
-// 128 bytes were measured to keep one warp busy for longer than the weights take.  A
-// record is 64 bytes longer than a multiple of 128, so that two tokens' 64-byte pieces
-// lie on different banks.  The tokens' ring has room for as many as the call can send to
-// one expert, and more stages of few: h comes from L2 when the grid barrier opens, and
-// with 512 K of it in flight its latency was most of a small down product's time.  The
-// rest is weights' stages, filled while the CTA waits for the barrier.
-constexpr int MOE_STAGE_K = 128, MOE_BOXES = MOE_STAGE_K / 64, MOE_PARTS = 3, MOE_PART = MOE_STAGE_K * 2;
-constexpr int MOE_RECORD = MOE_PARTS * MOE_PART + 64, MOE_MAX_STAGES = 9, MOE_MAX_TSTAGES = 8;
-// Stages of weights to a stage of tokens, and what one copy of them is: of x, of h.
-template <bool DOWN>
-constexpr int MOE_SPAN = DOWN ? 1 : 2;
-template <bool DOWN>
-constexpr int MOE_TOKEN_K = MOE_SPAN<DOWN> * MOE_STAGE_K;
-template <bool DOWN>
-constexpr int MOE_TOKEN = MOE_TOKEN_K<DOWN> * 2 * (DOWN ? MOE_PARTS : 1);
-static_assert(MOE_TOKEN<false> <= MOE_RECORD && MOE_TOKEN<true> <= MOE_RECORD, "records");
-constexpr int MOE_RINGS = (232448 - (int)sizeof(MoeShared)) & ~15;
-static_assert(2 * MOE_MAX_STAGES + 2 * MOE_MAX_TSTAGES <= MOE_MAX_BARS, "barriers");
-
-// Shared memory of a call: the rings, then MoeShared.  Before the rings start, all
-// logits and after them a bit for each expert and slot stand in their place.
-struct MoeLayout {
-    int stages, tstages, stage_bytes, token_bytes, off_tokens, off_shared;
-    __host__ __device__ constexpr MoeLayout(int T, int half_rows)
-        : stages(0), tstages(T <= 8 ? MOE_MAX_TSTAGES : (T <= 16 ? 6 : 3)), stage_bytes(MOE_BOXES * half_rows * 256),
-          token_bytes((T < MOE_GROUP ? (T + 7) & ~7 : MOE_GROUP) * MOE_RECORD), off_tokens(0), off_shared(0)
-    {
-        const int room = (MOE_RINGS - tstages * token_bytes) / stage_bytes;
-        stages = room < MOE_MAX_STAGES ? room : MOE_MAX_STAGES;
-        off_tokens = stages * stage_bytes;
-        const int rings = off_tokens + tstages * token_bytes, plan = T * MOE_MAX_E * 4 + MOE_MAX_E * ((T * MOE_MAX_K + 31) / 32) * 4;
-        off_shared = rings > plan ? rings : plan;
-    }
-};
-
-// Every T and tile height has room, and two stages of weights at least.
-constexpr bool layout_fits()
-{
-    for (int half = 32; half <= 64; half += 8)
-        for (int T = 1; T <= MOE_MAX_T; ++T)
-            if (MoeLayout(T, half).off_shared > MOE_RINGS || MoeLayout(T, half).stages < 2) return false;
-    return true;
-}
-static_assert(layout_fits(), "rings, logits and bits");
 
 // ------------------------------------------------------------------ helpers --
 // c += a 16 x 16 tile of weights by 16 x 8 of tokens.  The tensor core does not round
@@ -385,9 +333,10 @@ __device__ __forceinline__ bool mma_phase(const MoeArgs &p, const MoeShared &S, 
     const int n = S.nact * pr.tiles;
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int ai = i / pr.tiles, tile = i - ai * pr.tiles, cnt = S.first[ai + 1] - S.first[ai];
-        const bool ok = cnt <= 8    ? run_item<XT, DOWN, 1>(p, S, m, pr, walk, ai, tile)
-                        : cnt <= 16 ? run_item<XT, DOWN, 2>(p, S, m, pr, walk, ai, tile)
-                                    : run_item<XT, DOWN, 4>(p, S, m, pr, walk, ai, tile);
+        const int eights = moe_eights(cnt);
+        const bool ok = eights == 1   ? run_item<XT, DOWN, 1>(p, S, m, pr, walk, ai, tile)
+                        : eights == 2 ? run_item<XT, DOWN, 2>(p, S, m, pr, walk, ai, tile)
+                                      : run_item<XT, DOWN, 4>(p, S, m, pr, walk, ai, tile);
         if (!ok) return false;
     }
     return true;

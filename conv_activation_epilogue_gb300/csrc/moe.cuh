@@ -9,10 +9,6 @@
 
 namespace mmact {
 
-constexpr int MOE_MAX_T = 64, MOE_MAX_K = 16, MOE_MAX_E = 512;
-constexpr int MOE_MIN_GROUP = 16;                              // tokens of an expert that share a read of its weights, at least
-constexpr int MOE_MAX_BARS = 40;
-
 // A logit as a key whose unsigned order is the float order, NaN above all, and
 // -0 equal to +0; never 0.
 __device__ __forceinline__ uint32_t logit_key(float x)
@@ -115,20 +111,6 @@ __device__ __forceinline__ void router_logits(const MoeArgs &p, int block, int t
 }
 
 // ------------------------------------------------------------ choice of experts --
-// Shared memory of an experts kernel beside its rings.
-struct MoeShared {
-    float probs[MOE_MAX_T * MOE_MAX_K];
-    short choice[MOE_MAX_T * MOE_MAX_K];           // slot t * k + j -> expert
-    short slot[MOE_MAX_T * MOE_MAX_K];             // slots by expert
-    short count[MOE_MAX_E], start[MOE_MAX_E];      // slots of an expert, its first entry of slot[]
-    short act[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP];       // groups of tokens of one expert, by expert:
-    short first[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP + 1];                   // the expert and the first entry of slot[]
-    int nact;
-    int abort_flag, go;
-    uint32_t tmem;
-    uint64_t bar[MOE_MAX_BARS];
-};
-
 // Top k of a token by LANES lanes of a warp (32 / LANES tokens side by side; every
 // lane of the warp calls it): each round the largest key of those left, then the
 // lowest index that has it, whose key becomes 0; then the softmax weights.  `keys`:

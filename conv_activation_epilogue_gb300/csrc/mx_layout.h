@@ -4,6 +4,12 @@
 
 #include <cstdint>
 
+#ifdef __CUDACC__
+#define MX_HOST_DEVICE __host__ __device__
+#else
+#define MX_HOST_DEVICE
+#endif
+
 namespace mmact {
 
 constexpr int CTA_SMEM = 232448;               // shared memory that one CTA can ask for
@@ -45,5 +51,83 @@ struct MxRowsCfg {
     static_assert(OFF_MISC + 16 <= OFF_RING && OFF_RING + MAX_STAGES * STAGE_BYTES <= CTA_SMEM, "shared memory budget");
     static_assert(BT + 16 * MAX_STAGES <= TMEM_COLS, "tensor memory budget");
 };
+
+// ----------------------------------------------------------- mixture of experts --
+constexpr int MOE_MAX_T = 64, MOE_MAX_K = 16, MOE_MAX_E = 512;
+constexpr int MOE_MIN_GROUP = 16;                              // tokens of an expert that share a read of its weights, at least
+constexpr int MOE_MAX_BARS = 40;
+
+// Shared memory of an experts kernel beside its rings.
+struct MoeShared {
+    float probs[MOE_MAX_T * MOE_MAX_K];
+    short choice[MOE_MAX_T * MOE_MAX_K];           // slot t * k + j -> expert
+    short slot[MOE_MAX_T * MOE_MAX_K];             // slots by expert
+    short count[MOE_MAX_E], start[MOE_MAX_E];      // slots of an expert, its first entry of slot[]
+    short act[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP];       // groups of tokens of one expert, by expert:
+    short first[MOE_MAX_E + MOE_MAX_T * MOE_MAX_K / MOE_MIN_GROUP + 1];                   // the expert and the first entry of slot[]
+    int nact;
+    int abort_flag, go;
+    uint32_t tmem;
+    uint64_t bar[MOE_MAX_BARS];
+};
+
+// ------------------------------------------------ mixture of experts, 16-bit weights --
+constexpr int MOE_GROUP = 32;                                  // tokens of one expert that share a read of its weights
+
+// Two rings.  A stage of weights is 128 K of a tile, two boxes of 64 K for each half:
+// with 64 K a stage, what a warp does once a stage (waits, addresses, giving it back)
+// took longer than the multiplication (one token, 2 of 8 experts of 4096 x 1792: 47.7 us,
+// with 128 K 41.6; 64 tokens, 8 of 64 experts: 456 and 445).  A stage of tokens is the
+// group's tokens, a record for each and a copy to a record: x over 256 K (two stages of
+// weights, 512 bytes), or h over 128 K (its three parts, 768 bytes), because copies of
+// 128 bytes were measured to keep one warp busy for longer than the weights take.  A
+// record is 64 bytes longer than a multiple of 128, so that two tokens' 64-byte pieces
+// lie on different banks.  The tokens' ring has room for as many as the call can send to
+// one expert, and more stages of few: h comes from L2 when the grid barrier opens, and
+// with 512 K of it in flight its latency was most of a small down product's time.  The
+// rest is weights' stages, filled while the CTA waits for the barrier.
+constexpr int MOE_STAGE_K = 128, MOE_BOXES = MOE_STAGE_K / 64, MOE_PARTS = 3, MOE_PART = MOE_STAGE_K * 2;
+constexpr int MOE_RECORD = MOE_PARTS * MOE_PART + 64, MOE_MAX_STAGES = 9, MOE_MAX_TSTAGES = 8;
+// Stages of weights to a stage of tokens, and what one copy of them is: of x, of h.
+template <bool DOWN>
+constexpr int MOE_SPAN = DOWN ? 1 : 2;
+template <bool DOWN>
+constexpr int MOE_TOKEN_K = MOE_SPAN<DOWN> * MOE_STAGE_K;
+template <bool DOWN>
+constexpr int MOE_TOKEN = MOE_TOKEN_K<DOWN> * 2 * (DOWN ? MOE_PARTS : 1);
+static_assert(MOE_TOKEN<false> <= MOE_RECORD && MOE_TOKEN<true> <= MOE_RECORD, "records");
+constexpr int MOE_RINGS = (CTA_SMEM - (int)sizeof(MoeShared)) & ~15;
+static_assert(2 * MOE_MAX_STAGES + 2 * MOE_MAX_TSTAGES <= MOE_MAX_BARS, "barriers");
+
+// Groups of eight tokens that a product warp multiplies for `tokens` of them, and so
+// the records that it reads of a stage, whether there are tokens in them or not: what
+// they hold reaches columns that are not stored.
+MX_HOST_DEVICE constexpr int moe_eights(int tokens) { return tokens <= 8 ? 1 : (tokens <= 16 ? 2 : 4); }
+
+// Shared memory of a call: the rings, then MoeShared.  Before the rings start, all
+// logits and after them a bit for each expert and slot stand in their place.
+struct MoeLayout {
+    int stages, tstages, stage_bytes, token_bytes, off_tokens, off_shared;
+    MX_HOST_DEVICE constexpr MoeLayout(int T, int half_rows)
+        : stages(0), tstages(T <= 8 ? MOE_MAX_TSTAGES : (T <= 16 ? 6 : 3)), stage_bytes(MOE_BOXES * half_rows * 256),
+          token_bytes(8 * moe_eights(T < MOE_GROUP ? T : MOE_GROUP) * MOE_RECORD), off_tokens(0), off_shared(0)
+    {
+        const int room = (MOE_RINGS - tstages * token_bytes) / stage_bytes;
+        stages = room < MOE_MAX_STAGES ? room : MOE_MAX_STAGES;
+        off_tokens = stages * stage_bytes;
+        const int rings = off_tokens + tstages * token_bytes, plan = T * MOE_MAX_E * 4 + MOE_MAX_E * ((T * MOE_MAX_K + 31) / 32) * 4;
+        off_shared = rings > plan ? rings : plan;
+    }
+};
+
+// Every T and tile height has room, and two stages of weights at least.
+constexpr bool layout_fits()
+{
+    for (int half = 32; half <= 64; half += 8)
+        for (int T = 1; T <= MOE_MAX_T; ++T)
+            if (MoeLayout(T, half).off_shared > MOE_RINGS || MoeLayout(T, half).stages < 2) return false;
+    return true;
+}
+static_assert(layout_fits(), "rings, logits and bits");
 
 }  // namespace mmact

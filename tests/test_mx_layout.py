@@ -52,3 +52,38 @@ def test_few_rows_leave_room_for_the_next_kernels_ctas(rows_kernels):
     for bt, _, _, smem, _ in rows_kernels:
         if bt <= 32:
             assert 2 * (smem + RESERVED) <= SM_SMEM
+
+
+@pytest.fixture(scope="module")
+def moe_layouts(tmp_path_factory):
+    """(tokens, half a tile's rows, weight stages, bytes of one, token stages, bytes of one, their offset,
+    MoeShared's offset, its size, bytes of a token's record)"""
+    return compiled(tmp_path_factory, """
+int main()
+{
+    for (int T = 1; T <= MOE_MAX_T; ++T)
+        for (int half = 32; half <= 64; half += 8) {
+            const MoeLayout l(T, half);
+            std::printf("%d %d %d %d %d %d %d %d %d %d\\n", T, half, l.stages, l.stage_bytes, l.tstages, l.token_bytes, l.off_tokens,
+                        l.off_shared, (int)sizeof(MoeShared), MOE_RECORD);
+        }
+}
+""")
+
+
+def test_a_token_stage_holds_every_record_that_is_read(moe_layouts):
+    """An expert with n tokens is multiplied 8, 16 or 32 at a time, from as many records."""
+    assert len(moe_layouts) == 64 * 5
+    for T, _, _, _, _, token_bytes, _, _, _, record in moe_layouts:
+        for n in range(1, min(T, 32) + 1):
+            assert (8 if n <= 8 else 16 if n <= 16 else 32) * record <= token_bytes, (T, n)
+
+
+def test_the_mixtures_rings_do_not_overlap(moe_layouts):
+    for T, half, stages, stage_bytes, tstages, token_bytes, off_tokens, off_shared, shared, _ in moe_layouts:
+        assert stages >= 2 and tstages >= 2 and stages * stage_bytes <= off_tokens
+        assert stage_bytes == 2 * half * 256                 # 128 K of 2 * half rows
+        assert off_tokens + tstages * token_bytes <= off_shared and off_shared % 16 == 0
+        assert off_shared + shared <= SM_SMEM - RESERVED
+        # all logits, and a bit for each expert and slot, before the rings start
+        assert T * 512 * 4 + 512 * ((T * 16 + 31) // 32) * 4 <= off_shared
