@@ -106,7 +106,9 @@ __device__ __forceinline__ void quantize_stages(const MxRowsArgs &p, const Pipe 
                     else load32_any<XT>(p.x, at, n, (int64_t)p.M * p.K, r[u]);
                 }
             }
-            // (this warp saw the slot of four stages ago free, so no more than one use of this slot is outstanding)
+            // A slot goes to another warp in its next use.  This warp saw the slot of four stages ago free, so that with
+            // four stages or more all but the last use of this one are over, and the parity names that use.
+            static_assert(Cfg::MAX_STAGES >= 4, "a ring of fewer stages than MAX_STAGES never wraps");
             if (r0 == 0 && !mx_warp_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) {
                 if (lane == 0) pipe_fail(pp);
                 return;
