@@ -123,9 +123,9 @@ struct TmapEntry {
     TmapKey key;
     bool valid;
 };
-// 64 sets of 4 entries, per host thread: one call encodes at most 4 maps, so the
-// maps of a call never evict one another, whatever their hashes.
-constexpr int TMAP_SETS = 64, TMAP_WAYS = 4;
+// 32 sets of 8 entries, per host thread: one call encodes at most 5 maps, so the
+// maps of a repeated call all stay, whatever their hashes.
+constexpr int TMAP_SETS = 32, TMAP_WAYS = 8;
 thread_local TmapEntry t_tmap_cache[TMAP_SETS][TMAP_WAYS];
 thread_local uint8_t t_tmap_next[TMAP_SETS];   // way to replace next in each set (round robin)
 std::atomic<uint64_t> g_tmap_hits{0}, g_tmap_encodes{0};
