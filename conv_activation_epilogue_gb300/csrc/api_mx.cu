@@ -223,7 +223,7 @@ cudaError_t quantize_launch(const void *x, void *codes, void *scales, int64_t ro
                                  transposed != 0, stream);
 }
 
-constexpr int64_t MOE_K_PAD = 256;   // K of a stage of tokens
+constexpr int64_t MOE_K_PAD = 256;   // whole stages of either form of the weights
 
 // Where the parts of mmact_moe's workspace begin.
 struct MoeWorkspace {
@@ -270,8 +270,8 @@ mmact_status moe_sizes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
     if (T > MOE_MAX_TOKENS || E > MOE_MAX_EXPERTS || top < 1 || top > MOE_MAX_TOP || top > E || H < 8 || I < 8 ||
         H % 8 != 0 || I % 8 != 0)
         return MMACT_ERR_UNSUPPORTED;
-    // rows of the experts' matrices and the items of a product are counted in 32 bits
-    if (E * 2 * I > MAX_DIM || E * H > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
+    // rows of the experts' matrices, and H and I up to whole stages, are counted in 32 bits
+    if (E * 2 * I > MAX_DIM - MOE_K_PAD || E * H > MAX_DIM - MOE_K_PAD) return MMACT_ERR_UNSUPPORTED;
     return MMACT_OK;
 }
 

@@ -72,7 +72,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 // values apart.
 __device__ __forceinline__ int64_t h_at(const MoeArgs &p, int64_t slot, int row)
 {
-    return slot * p.Ip * MOE_PARTS + row / MOE_STAGE_K * (MOE_PARTS * MOE_STAGE_K) + row % MOE_STAGE_K;
+    return slot * p.Ip * MOE_PARTS + (int64_t)(row / MOE_STAGE_K) * (MOE_PARTS * MOE_STAGE_K) + row % MOE_STAGE_K;
 }
 
 // h as three bf16 parts: the first 8 bits, the next, the last.  All of them have h's
@@ -382,7 +382,7 @@ __device__ __forceinline__ bool produce_tokens(const MoeArgs &p, const MoeShared
             if (!mx_warp_wait(m.pp, m.tempty0 + 8 * to.slot, to.phase ^ 1u)) return false;
             elected_expect_tx(full, (uint32_t)cnt * MOE_TOKEN<DOWN>);
             __syncwarp();
-            if (lane < cnt) bulk_load(at, from + s * (MOE_TOKEN<DOWN> / 2), MOE_TOKEN<DOWN>, full);
+            if (lane < cnt) bulk_load(at, from + (int64_t)s * (MOE_TOKEN<DOWN> / 2), MOE_TOKEN<DOWN>, full);
             __syncwarp();
         }
     }

@@ -197,7 +197,7 @@ __device__ __forceinline__ bool mxe_tokens(const MoeArgs &p, const MoeShared &S,
             elected_expect_tx(full, (uint32_t)cnt * MXE_ATOM);
             __syncwarp();
             if (lane < cnt)
-                bulk_load(m.tokens + slot * MXE_T_BYTES + (uint32_t)lane * MXE_ATOM, from + s * MXE_ATOM, MXE_ATOM, full);
+                bulk_load(m.tokens + slot * MXE_T_BYTES + (uint32_t)lane * MXE_ATOM, from + (int64_t)s * MXE_ATOM, MXE_ATOM, full);
             __syncwarp();
         }
         return true;
@@ -230,7 +230,7 @@ __device__ __forceinline__ bool mxe_scales(const MoeArgs &p, const MoeShared &S,
                 const int s = s0 + d;
                 a[d][0] = has_row && 2 * s < tiles ? *reinterpret_cast<const uint32_t *>(wp + (int64_t)s * 1024) : 0u;
                 a[d][1] = has_row && 2 * s + 1 < tiles ? *reinterpret_cast<const uint32_t *>(wp + (int64_t)s * 1024 + 512) : 0u;
-                b[d] = has_term && s < pr.stages ? __ldcg(reinterpret_cast<const uint2 *>(tp + s * MXE_ATOM_SCALES)) : make_uint2(0, 0);
+                b[d] = has_term && s < pr.stages ? __ldcg(reinterpret_cast<const uint2 *>(tp + (int64_t)s * MXE_ATOM_SCALES)) : make_uint2(0, 0);
             }
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
