@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
         *reinterpret_cast<uint4 *>(p.x_pad + (int64_t)t * p.Hp + k) =
             k < p.H ? __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + (int64_t)t * p.H + k))
                     : make_uint4(0, 0, 0, 0);
+    fence_proxy_async_all();                                   // bulk copies read x and the zeros
     if (at != t * chunks) return;
     const int pad = (p.Ip - p.I) / 8;                          // eights of zeros past h's rows
     for (int i = threadIdx.x; i < pad * p.top; i += MOE_ROUTER_THREADS) {
@@ -130,6 +131,7 @@ __global__ void __launch_bounds__(MOE_ROUTER_THREADS) moe_router_kernel(const Mo
 #pragma unroll
         for (int j = 0; j < MOE_PARTS; ++j) *reinterpret_cast<uint4 *>(p.h + to + j * MOE_STAGE_K) = make_uint4(0, 0, 0, 0);
     }
+    fence_proxy_async_all();
 }
 
 // ----------------------------------------------------------------- products --
@@ -452,6 +454,7 @@ __global__ void __launch_bounds__(MOE_THREADS, 1)
         drain(m.pp, m.pp.full0, to, m.stages);
     } else if (warp == 1 + MOE_MMA_WARPS) {
         MoePlace to = {0, 0};
+        fence_proxy_async_all();
         ok = ok && produce_tokens<false>(p, S, m, up, to);
         // every h is written before any is read
         if (ok) ok = __all_sync(0xffffffffu, lane != 0 || grid_wait(m.pp, p.counters)) != 0;
