@@ -328,8 +328,11 @@ MMACT_EXPORT mmact_status mmact_dequantize_mxfp4(const void *codes, const void *
     if (rows == 0 || K == 0) return MMACT_OK;
     if (codes == nullptr || scales == nullptr || y == nullptr) return MMACT_ERR_INVALID_ARG;
     if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return MMACT_ERR_UNSUPPORTED;
+    DeviceContext dev;
+    const mmact_status st = device_context(&dev);
+    if (st != MMACT_OK) return st;
     return enqueued(launch_dequantize_mxfp4(static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), y,
-                                            out_kind(y_dtype), rows, K, static_cast<cudaStream_t>(stream)));
+                                            out_kind(y_dtype), rows, K, dev.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 MMACT_EXPORT mmact_status mmact_gemm_mxfp4(const void *a_codes, const void *a_scales, const void *b_codes,

@@ -14,7 +14,7 @@ namespace mmact {
 cudaError_t launch_quantize_mxfp4(const void *x, int type, uint8_t *codes, uint8_t *scales, int64_t rows, int64_t K,
                                   bool trans, cudaStream_t s);
 cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, void *y, int type, int64_t rows,
-                                    int64_t K, cudaStream_t s);
+                                    int64_t K, int sms, cudaStream_t s);
 
 // Product of two MXFP4 matrices with the fused epilogue.
 struct MxGemmArgs {

@@ -250,15 +250,14 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes,
 }
 
 // The grid of dequantize_kernel: a CTA takes as many of a row's tiles as it has, up to
-// 16, and U sets of rows; U = 4 once that still leaves four CTAs for each of the
-// 152 SMs, so that small calls spread over more SMs and large ones keep more
-// loads in flight.
+// 16, and U sets of rows; U = 4 once that still leaves four CTAs for each SM, so that
+// small calls spread over more SMs and large ones keep more loads in flight.
 struct RowGrid {
     int tpr_log2, segs, u;
     int64_t grid;
 };
 
-static RowGrid row_grid(int64_t rows, int64_t K)
+static RowGrid row_grid(int64_t rows, int64_t K, int sms)
 {
     const int64_t tiles = mx_tiles(K);
     RowGrid g;
@@ -266,7 +265,7 @@ static RowGrid row_grid(int64_t rows, int64_t K)
     while (g.tpr_log2 < 4 && (1 << g.tpr_log2) < tiles) ++g.tpr_log2;
     g.segs = (int)((tiles + (1 << g.tpr_log2) - 1) >> g.tpr_log2);
     const int64_t per = 16 >> g.tpr_log2;
-    g.u = (rows + per * 4 - 1) / (per * 4) * g.segs >= 4 * 152 ? 4 : 1;
+    g.u = (rows + per * 4 - 1) / (per * 4) * g.segs >= 4 * sms ? 4 : 1;
     g.grid = (rows + per * g.u - 1) / (per * g.u) * g.segs;
     return g;
 }
@@ -295,11 +294,11 @@ static cudaError_t quantize_t(const void *x, uint8_t *codes, uint8_t *scales, in
 }
 
 template <int T>
-static cudaError_t dequantize_t(const uint8_t *codes, const uint8_t *scales, void *y, int64_t rows, int64_t K,
+static cudaError_t dequantize_t(const uint8_t *codes, const uint8_t *scales, void *y, int64_t rows, int64_t K, int sms,
                                 cudaStream_t s)
 {
     const int e = T == IN_F32 ? 4 : 2;
-    const RowGrid g = row_grid(rows, K);
+    const RowGrid g = row_grid(rows, K, sms);
     if (g.grid > INT32_MAX) return cudaErrorInvalidValue;
     const bool vec = K * e % 16 == 0;
     auto k = g.u == 4 ? (vec ? dequantize_kernel<T, true, 4> : dequantize_kernel<T, false, 4>)
@@ -337,11 +336,11 @@ cudaError_t launch_quantize_mxfp4(const void *x, int type, uint8_t *codes, uint8
 }
 
 cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, void *y, int type, int64_t rows,
-                                    int64_t K, cudaStream_t s)
+                                    int64_t K, int sms, cudaStream_t s)
 {
-    if (type == IN_BF16) return dequantize_t<IN_BF16>(codes, scales, y, rows, K, s);
-    if (type == IN_F16) return dequantize_t<IN_F16>(codes, scales, y, rows, K, s);
-    return dequantize_t<IN_F32>(codes, scales, y, rows, K, s);
+    if (type == IN_BF16) return dequantize_t<IN_BF16>(codes, scales, y, rows, K, sms, s);
+    if (type == IN_F16) return dequantize_t<IN_F16>(codes, scales, y, rows, K, sms, s);
+    return dequantize_t<IN_F32>(codes, scales, y, rows, K, sms, s);
 }
 
 }  // namespace mmact
