@@ -74,21 +74,6 @@ __device__ __forceinline__ void mx_epi_unit(uint32_t taddr, const float *bias, i
 {
     constexpr int HALVES = OUT == OUT_F32 ? 1 : 2;           // 32 columns at a time
     uint32_t r[HALVES][32];
-    float bs[HALVES][32];                                    // ahead of the accumulators: their latencies overlap
-#pragma unroll
-    for (int h = 0; h < HALVES; ++h) {
-        const float *src = bias + 32 * h;
-        if (bias != nullptr && nvalid >= 32 * (h + 1) && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(src + j);
-                bs[h][j] = f.x, bs[h][j + 1] = f.y, bs[h][j + 2] = f.z, bs[h][j + 3] = f.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) bs[h][j] = bias != nullptr && 32 * h + j < nvalid ? src[j] : 0.0f;
-        }
-    }
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) ptx::tmem_ld32(taddr + 32 * h, r[h]);
 #pragma unroll
@@ -96,7 +81,21 @@ __device__ __forceinline__ void mx_epi_unit(uint32_t taddr, const float *bias, i
     loaded();
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
-        const float (&b)[32] = bs[h];
+        float b[32] = {};
+        const float *src = bias + 32 * h;
+        if (bias != nullptr) {
+            if (nvalid >= 32 * (h + 1) && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(src + j);
+                    b[j] = f.x, b[j + 1] = f.y, b[j + 2] = f.z, b[j + 3] = f.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (32 * h + j < nvalid) b[j] = src[j];
+            }
+        }
         const uint32_t row = buf + (uint32_t)lane * 128u, sw = (uint32_t)(lane & 7);
         constexpr int PER = OUT == OUT_F32 ? 4 : 8;           // values per 16 bytes
 #pragma unroll
