@@ -335,10 +335,10 @@ __device__ __forceinline__ bool mma_phase(const MoeArgs &p, const MoeShared &S, 
     const int n = S.nact * pr.tiles;
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int ai = i / pr.tiles, tile = i - ai * pr.tiles, cnt = S.first[ai + 1] - S.first[ai];
-        const int eights = moe_eights(cnt);
-        const bool ok = eights == 1   ? run_item<XT, DOWN, 1>(p, S, m, pr, walk, ai, tile)
-                        : eights == 2 ? run_item<XT, DOWN, 2>(p, S, m, pr, walk, ai, tile)
-                                      : run_item<XT, DOWN, 4>(p, S, m, pr, walk, ai, tile);
+        // moe_eights(cnt), spelled out (by its value 64 tokens, 8 of 64 experts of 4096 x 1792 took 461 us instead of 457)
+        const bool ok = cnt <= 8    ? run_item<XT, DOWN, 1>(p, S, m, pr, walk, ai, tile)
+                        : cnt <= 16 ? run_item<XT, DOWN, 2>(p, S, m, pr, walk, ai, tile)
+                                    : run_item<XT, DOWN, 4>(p, S, m, pr, walk, ai, tile);
         if (!ok) return false;
     }
     return true;
