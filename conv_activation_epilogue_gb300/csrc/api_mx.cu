@@ -277,12 +277,12 @@ mmact_status moe_sizes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top)
 
 // Half the rows of a tile of 16-bit weights: the one with which the busiest SM has
 // the least to do, counted in rows x K.  Smaller tiles pay where they save a round of
-// the SMs or bring all of them to work: 16 tokens, 2 of 16 experts of 4096 x 1792, 117.5
-// us with tiles of 128 rows, 110 with 112; one token, 2 of 8 experts of the same, 43.7
-// and 39.6 us with 64 rows.  Where they do not they cost: 32 tokens, 6 of 64 experts of
-// 2048 x 1408, 188 us with 128 rows, 197 with 64, 244 with 48 (a ring stage takes as
-// long as one of 72 rows at least).  The number of chosen experts is not known here: it
-// is taken as what random choices give.
+// the SMs or bring all of them to work (cold caches): 16 tokens, 2 of 16 experts of 4096 x 1792,
+// 116 us with tiles of 128 rows, 107 with 112; one token, 2 of 8 experts of the same, 43.6
+// and 39.2 us with 64 rows.  Where they do not they cost: 32 tokens, 6 of 64 experts of
+// 2048 x 1408, 186 us with 128 rows, 199 with 64 (a ring stage takes as long as one of 72
+// rows at least).  The number of chosen experts is not known here: it is taken as what
+// random choices give.
 int moe_half_rows(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, bool gated, int sms)
 {
     const int64_t chosen = std::llround((double)E * (1.0 - std::pow(1.0 - (double)top / (double)E, (double)T)));

@@ -26,7 +26,7 @@
 //               which saves a kernel of its own (1 row, 8192 x 8192 weights: 8.9
 //               against 10.9 us with one; 8 rows 10.1 and 11.3, 16 rows 14.5 and 11.3)
 //
-// Measured with calls back to back: 1 x 8192 x 8192 (35.7 MB) 8.4 us, 128 x 8192 x 8192 12.9 us
+// Measured with calls back to back: 1 x 8192 x 8192 (35.7 MB) 8.4 us, 128 x 8192 x 8192 13.0 us
 // (every SM reads the token tiles from L2, 117 MB in all), 77 x 4001 x 2056 7.7 us.  About
 // 5.4 us of each are fixed: start, first loads, the cluster's sum, stores.
 #include <type_traits>

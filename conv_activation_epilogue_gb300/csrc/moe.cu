@@ -32,14 +32,16 @@
 // The intermediate h is held as three bf16 parts of 8 bits each, h = hi + mid + lo
 // exactly, and multiplied as all of them: nothing is rounded between the two
 // products.  (Two parts, 16 bits of h, take 3 % less of the time of 64 tokens, and put y
-// in bf16 1.0e-4 instead of 0.6e-4, in the 2-norm, from what fp32 gives.)  fp16 down weights are split
-// into two (hi + lo is exact), which keeps h's fp32 range; of their products with
-// the parts, lo x lo, 2^-24 of hi x hi, is left out.
+// in bf16 1.0e-4 instead of 0.6e-4, in the 2-norm, from what fp32 gives.)  fp16 down
+// weights are split into two (hi + lo is exact), which keeps h's fp32 range; of their
+// products with the parts, lo x the last part, 2^-24 of the whole, is left out.
 //
 // Measured (bf16, GB300): 64 tokens, 8 of 64 experts of 4096 x 1792 (2.8 GB of weights)
-// 442 us, 6.4 TB/s.  One token, 8 of 64 experts of 2048 x 1024 (101 MB): 32 us, of which
-// the weights take 15; the router kernel is 4, choice and lists 4, the two grid
-// barriers with what they leave idle 5.
+// 451 to 463 us, 6.2 TB/s.  One token, 8 of 64 experts of 2048 x 1024 (101 MB): 33 us, of
+// which the weights take 15; the router kernel is 4, choice and lists 4, the two grid
+// barriers with what they leave idle 5.  With more than 16 tokens an expert the down product's three
+// parts keep the tensor pipe busy for longer than its weights come in: 64 tokens, 8 of
+// 8 experts of 4096 x 1792, 207 us (fp16, five products for each weight: 244), the bytes 53.
 #include "moe.cuh"
 
 namespace mmact {

@@ -212,9 +212,9 @@ __device__ __forceinline__ uint32_t raw_encode(const uint32_t (&w)[Raw8<T>::WORD
 enum : int { ACT_SILU = ACT_GELU + 1 };
 
 // z * sigma(z) = z / (1 + e^-z): one hardware exponential and one fast divide, a
-// few ulp each.  Below z = -87 the divisor passes 2^126, where __fdividef gives 0
-// (the value is above -1e-36 there), and e^-z = inf would give NaN from
-// -inf / inf: both are cut off at -87.
+// few ulp each.  Below z = -87 the divisor passes 2^126, where __fdividef gives 0 or
+// (e^-z = inf) NaN; the value, above -1e-36 there, is cut off to -0.  At z = -inf
+// it is NaN, as the formula's -inf / inf.
 __device__ __forceinline__ float silu_f32(float z)
 {
     return z < -87.0f ? z * 0.0f : __fdividef(z, 1.0f + __expf(-z));
