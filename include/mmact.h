@@ -461,7 +461,7 @@ mmact_status mmact_set_gemm_l2_policy(int mode);
 
 /*
  * Tensor-map cache counters (diagnostic; no counterpart in the pages).  Every
- * call encodes up to four TMA tensor maps on the host; an encoded map depends
+ * call encodes up to five TMA tensor maps on the host; an encoded map depends
  * only on its address, shape, strides, box and dtype, so the library keeps up
  * to 256 per host thread (32 sets of 8), keyed by all of them, and a call that repeats an
  * earlier call's tensors and shapes copies them instead of encoding again.
