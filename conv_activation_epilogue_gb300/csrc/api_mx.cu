@@ -11,6 +11,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "api_checks.h"
 #include "api_internal.h"
 #include "common.cuh"
 #include "kernels_mx.h"
@@ -21,17 +22,6 @@
 
 namespace mmact {
 namespace {
-
-constexpr int MAX_DEVICES = 64;
-constexpr int64_t MAX_DIM = (int64_t(1) << 31) - 1;
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-int out_kind(mmact_dtype d) { return d == MMACT_BF16 ? OUT_BF16 : (d == MMACT_F16 ? OUT_F16 : OUT_F32); }
-int elem_bytes(mmact_dtype d) { return d == MMACT_F32 ? 4 : 2; }
-bool valid_16(mmact_dtype d) { return d == MMACT_F16 || d == MMACT_BF16; }
-bool valid_float(mmact_dtype d) { return valid_16(d) || d == MMACT_F32; }
-bool valid_act(mmact_act a) { return a >= MMACT_ACT_NONE && a <= MMACT_ACT_SILU; }
 
 std::atomic<int> g_mx_kernel{0};   // 0: chosen per shape; 1: rows kernel; 2: pair kernel
 
@@ -65,8 +55,6 @@ mmact_status mx_context(MxContext *out)
 
 int64_t mx_codes_bytes(int64_t rows, int64_t K) { return rows * (mx_blocks(K) * 16); }
 int64_t mx_scales_bytes(int64_t rows, int64_t K) { return (rows + 127) / 128 * mx_tiles(K) * 512; }
-int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-bool mx_dims(int64_t rows, int64_t K) { return rows >= 0 && K >= 0 && rows <= MAX_DIM && K <= MAX_DIM; }
 
 mmact_status mx_gemm_check(const void *ac, const void *as, const void *bc, const void *bs, const float *bias,
                            const void *C, int64_t M, int64_t N, int64_t K, mmact_dtype cd, mmact_act act)
@@ -213,8 +201,6 @@ cudaError_t mx_gemm_launch(const MxPlan &plan, cudaStream_t stream)
 {
     return plan.pair ? launch_gemm_mxfp4_pair(plan.P, stream) : launch_gemm_mxfp4_rows(plan.R, stream);
 }
-
-mmact_status enqueued(cudaError_t e) { return e == cudaSuccess ? MMACT_OK : MMACT_ERR_CUDA; }
 
 cudaError_t quantize_launch(const void *x, void *codes, void *scales, int64_t rows, int64_t K, mmact_dtype xd,
                             int transposed, cudaStream_t stream)

@@ -4,21 +4,12 @@
 // us (6.4 TB/s), transposed 30.5, the way back 27.8; fp32 61.8 (a lane's 128 bytes in
 // eight loads; 4.9 TB/s), 47.4 and 60.1.  Transposed with an odd number of rows, by
 // single 16-bit values: 8191 x 8192 bf16 56.
-#include <type_traits>
-
 #include "common.cuh"
 #include "kernels_mx.h"
 #include "mxfp4.cuh"
+#include "row_stores.cuh"
 
 namespace mmact {
-
-template <int T>
-__device__ __forceinline__ void store1(void *p, int64_t i, float v)
-{
-    if constexpr (T == IN_F32) static_cast<float *>(p)[i] = v;
-    else if constexpr (T == IN_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half *>(p)[i] = __float2half_rn(v);
-}
 
 // x [rows, K] row-major.  A lane takes one block of 32 values: its loads (64 or
 // 128 consecutive bytes) are all in flight before the first is used, the largest
@@ -204,32 +195,8 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes,
         for (int j = 0; j < 8; ++j) v[j] *= s;
         const int64_t i = row * K + k0;
         if constexpr (!VEC) {
-            // Rows that begin anywhere: through shared memory, so that 16 lanes write consecutive words (eight values
-            // a lane, one by one: 5447 x 3659 bf16 57 us, so 13.8).
-            using E = std::conditional_t<T == IN_F32, uint32_t, uint16_t>;
-            __shared__ __align__(16) E stage[16][128];
-            E *line = stage[unit];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) store1<T>(line, l * 8 + j, v[j]);
-            __syncwarp();
             const int n = row < rows ? (int)min((int64_t)128, K - tile * 128) : 0;
-            const int64_t i0 = i - l * 8;
-            E *out = static_cast<E *>(y) + i0;
-            if constexpr (T == IN_F32) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (q * 16 + l < n) __stcs(out + q * 16 + l, line[q * 16 + l]);
-            } else {
-                const int odd = (int)(i0 & 1);                 // pairs of values at even offsets
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int e = odd + 2 * (q * 16 + l);
-                    if (e + 1 < n) __stcs(reinterpret_cast<uint32_t *>(out + e), line[e] | ((uint32_t)line[e + 1] << 16));
-                }
-                if (l == 0 && odd != 0 && n > 0) out[0] = line[0];
-                if (l == 1 && n > odd && ((n - odd) & 1) != 0) out[n - 1] = line[n - 1];
-            }
-            __syncwarp();
+            store_line_any<T>(y, i - l * 8, n, v, unit, l);
         } else if (k0 + 8 <= K) {
             if constexpr (T == IN_F32) {
                 float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(y) + i);
@@ -249,27 +216,6 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *codes,
                 if (k0 + j < K) store1<T>(y, i + j, v[j]);
         }
     }
-}
-
-// The grid of dequantize_kernel: a CTA takes as many of a row's tiles as it has, up to
-// 16, and U sets of rows; U = 4 once that still leaves four CTAs for each SM, so that
-// small calls spread over more SMs and large ones keep more loads in flight.
-struct RowGrid {
-    int tpr_log2, segs, u;
-    int64_t grid;
-};
-
-static RowGrid row_grid(int64_t rows, int64_t K, int sms)
-{
-    const int64_t tiles = mx_tiles(K);
-    RowGrid g;
-    g.tpr_log2 = 0;
-    while (g.tpr_log2 < 4 && (1 << g.tpr_log2) < tiles) ++g.tpr_log2;
-    g.segs = (int)((tiles + (1 << g.tpr_log2) - 1) >> g.tpr_log2);
-    const int64_t per = 16 >> g.tpr_log2;
-    g.u = (rows + per * 4 - 1) / (per * 4) * g.segs >= 4 * sms ? 4 : 1;
-    g.grid = (rows + per * g.u - 1) / (per * g.u) * g.segs;
-    return g;
 }
 
 template <int T>
