@@ -1,0 +1,308 @@
+// api_fp8.cu -- the C ABI of the 8-bit floating-point operators (include/mmact.h):
+// argument validation and launch planning.  As in api.cu, every check happens on the
+// host before anything is enqueued.
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "api_checks.h"
+#include "api_internal.h"
+#include "fp8.cuh"
+#include "kernels_fp8.h"
+#include "kernels_mx.h"
+#include "mmact.h"
+
+#define MMACT_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace mmact {
+namespace {
+
+bool valid_f8(mmact_dtype d) { return d == MMACT_E4M3 || d == MMACT_E5M2; }
+int f8_kind(mmact_dtype d) { return d == MMACT_E5M2 ? F8_E5M2 : F8_E4M3; }
+
+// The current device, with this file's kernels set up on it (once per device).
+struct F8Context {
+    DeviceContext dev;
+    int max_pairs;                   // CTA pairs of the pair kernel resident at once
+};
+
+mmact_status f8_context(F8Context *out)
+{
+    static std::mutex mutex;
+    static std::atomic<bool> ready[MAX_DEVICES];
+    static int pairs[MAX_DEVICES];
+    const mmact_status s = device_context(&out->dev);
+    if (s != MMACT_OK) return s;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(mutex);               // setting up twice is harmless
+        if (setup_fp8_pair_kernels(&pairs[dev]) != cudaSuccess) return MMACT_ERR_CUDA;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    out->max_pairs = pairs[dev];
+    return MMACT_OK;
+}
+
+int64_t f8_codes_bytes(int64_t rows, int64_t K) { return rows * f8_pitch(K); }
+int64_t f8_scales_bytes(int64_t rows, int64_t K) { return (rows + 127) / 128 * f8_tiles(K) * 512; }
+
+// A matrix in 8 bits.
+struct F8Matrix {
+    const void *codes, *scales;
+    mmact_dtype type;
+};
+
+mmact_status f8_gemm_check(const F8Matrix &A, const F8Matrix &B, const float *bias, const void *C, int64_t M, int64_t N,
+                           int64_t K, mmact_dtype cd, mmact_act act)
+{
+    if (!mx_dims(M, K) || !mx_dims(N, K)) return MMACT_ERR_INVALID_ARG;
+    if (((A.codes == nullptr || A.scales == nullptr) && M * K != 0) ||
+        ((B.codes == nullptr || B.scales == nullptr) && N * K != 0) || (C == nullptr && M * N != 0))
+        return MMACT_ERR_INVALID_ARG;
+    if (!valid_f8(A.type) || !valid_f8(B.type) || !valid_float(cd) || !valid_act(act)) return MMACT_ERR_INVALID_ARG;
+    if (bias != nullptr && !aligned4(bias)) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(A.codes) || !aligned16(A.scales) || !aligned16(B.codes) || !aligned16(B.scales) || !aligned16(C))
+        return MMACT_ERR_UNSUPPORTED;
+    if (((M + 127) / 128) * ((N + 127) / 128) > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
+    return MMACT_OK;
+}
+
+// Tensor maps of an 8-bit matrix: its codes as 16-bit words (box 64 words = 128 codes x
+// `box_rows` rows, 128-byte swizzle) and its scale tiles as 32-bit words (box 128 words = a
+// tile, of `box_tiles` rows of tiles).  Rows, codes and tiles past the end arrive as zeros.
+bool f8_encode(CUtensorMap *mc, CUtensorMap *ms, const F8Matrix &m, int64_t rows, int64_t K, uint32_t box_rows,
+               uint32_t box_tiles)
+{
+    const uint64_t dc[2] = {(uint64_t)f8_pitch(K) / 2, (uint64_t)rows}, sc[1] = {(uint64_t)f8_pitch(K)};
+    const uint32_t bc[2] = {64, box_rows};
+    const uint64_t ds[2] = {(uint64_t)f8_tiles(K) * 128, (uint64_t)(rows + 127) / 128};
+    const uint64_t ss[1] = {(uint64_t)f8_tiles(K) * 512};
+    const uint32_t bs[2] = {128, box_tiles};
+    return encode_tensor_map(mc, MMACT_BF16, 2, m.codes, dc, sc, bc, true) &&
+           encode_tensor_map(ms, MMACT_F32, 2, m.scales, ds, ss, bs, false);
+}
+
+mmact_status f8_gemm_plan(F8GemmLaunch &L, const F8Matrix &A, const F8Matrix &B, const float *bias, void *C, int64_t M,
+                          int64_t N, int64_t K, mmact_dtype cd, mmact_act act, float alpha)
+{
+    F8Context c;
+    const mmact_status st = f8_context(&c);
+    if (st != MMACT_OK) return st;
+    if (c.max_pairs < 1) return MMACT_ERR_CUDA;
+    std::memset(&L, 0, sizeof(L));
+    F8GemmArgs &a = L.args;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.nk32 = (int)((K + 31) / 32);
+    a.num_kb = (int)f8_blocks(K);
+    a.tiles_m = (int)((M + 255) / 256);
+    a.tiles_n = (int)((N + 255) / 256);
+    a.num_tiles = a.tiles_m * a.tiles_n;
+    a.group_m = 8;
+    a.act = (int)act;
+    a.alpha = alpha;
+    a.bias = bias;
+    a.C = C;
+    a.idesc = ptx::idesc_f8(f8_kind(A.type), f8_kind(B.type), 256, 256);
+    a.status = c.dev.status;
+    a.wait_ns = c.dev.wait_ns;
+    const int ce = elem_bytes(cd);
+    a.c_tma = N * ce % 16 == 0 ? 1 : 0;
+    L.out = out_kind(cd);
+    L.grid = 2 * (int)std::min<int64_t>(a.num_tiles, c.max_pairs);
+    if (!f8_encode(&L.tmA, &L.tmSA, A, M, K, 128, 1) || !f8_encode(&L.tmB, &L.tmSB, B, N, K, 128, 2)) return MMACT_ERR_CUDA;
+    if (a.c_tma) {
+        const uint64_t dC[2] = {(uint64_t)N, (uint64_t)M}, sC[1] = {(uint64_t)N * ce};
+        const uint32_t bC[2] = {(uint32_t)(128 / ce), 32};
+        if (!encode_tensor_map(&L.tmC, cd, 2, C, dC, sC, bC, true)) return MMACT_ERR_CUDA;
+    }
+    return MMACT_OK;
+}
+
+cudaError_t quantize_launch(const void *x, const F8Matrix &m, int64_t rows, int64_t K, mmact_dtype xd, bool square,
+                            bool transposed, cudaStream_t stream)
+{
+    return launch_quantize_fp8(x, out_kind(xd), static_cast<uint8_t *>(const_cast<void *>(m.codes)),
+                               static_cast<uint8_t *>(const_cast<void *>(m.scales)), rows, K, f8_kind(m.type), square,
+                               transposed, stream);
+}
+
+// Takes consecutive parts of a workspace, each from a multiple of 512 bytes.
+struct Parts {
+    char *base;
+    int64_t at = 0;
+    void *take(int64_t bytes)
+    {
+        char *here = base + at;
+        at += round_up(bytes, 512);
+        return here;
+    }
+    F8Matrix matrix(int64_t rows, int64_t K, mmact_dtype type)
+    {
+        void *codes = take(f8_codes_bytes(rows, K));
+        return F8Matrix{codes, take(f8_scales_bytes(rows, K)), type};
+    }
+};
+
+int64_t linear_bytes(int64_t M, int64_t K)
+{
+    return round_up(f8_codes_bytes(M, K), 512) + f8_scales_bytes(M, K);
+}
+
+// More tiles of 128 x 128 than are counted in 32 bits.
+bool backward_too_large(int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tm = (M + 127) / 128, tn = (N + 127) / 128, tk = (K + 127) / 128;
+    return tm * tk > MAX_DIM || tn * tk > MAX_DIM || tm * tn > MAX_DIM;
+}
+
+// dy by rows, dy and x by columns, partial column sums
+int64_t backward_bytes(int64_t M, int64_t N, int64_t K)
+{
+    return linear_bytes(M, N) + linear_bytes(N, M) + linear_bytes(K, M) + round_up((M + 127) / 128 * N * 4, 512);
+}
+
+}  // namespace
+}  // namespace mmact
+
+using namespace mmact;
+
+MMACT_EXPORT mmact_status mmact_fp8_size(int64_t rows, int64_t K, int64_t *codes_bytes, int64_t *scales_bytes)
+{
+    if (!mx_dims(rows, K) || codes_bytes == nullptr || scales_bytes == nullptr) return MMACT_ERR_INVALID_ARG;
+    *codes_bytes = f8_codes_bytes(rows, K);
+    *scales_bytes = f8_scales_bytes(rows, K);
+    return MMACT_OK;
+}
+
+MMACT_EXPORT mmact_status mmact_quantize_fp8(const void *x, void *codes, void *scales, int64_t rows, int64_t K,
+                                             mmact_dtype x_dtype, mmact_dtype code_dtype, int64_t block_rows, int transposed,
+                                             void *stream)
+{
+    if (!mx_dims(rows, K) || !valid_float(x_dtype) || !valid_f8(code_dtype)) return MMACT_ERR_INVALID_ARG;
+    if (block_rows != 1 && block_rows != 128) return MMACT_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return MMACT_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MMACT_ERR_UNSUPPORTED;
+    return enqueued(quantize_launch(x, F8Matrix{codes, scales, code_dtype}, rows, K, x_dtype, block_rows == 128,
+                                    transposed != 0, static_cast<cudaStream_t>(stream)));
+}
+
+MMACT_EXPORT mmact_status mmact_dequantize_fp8(const void *codes, const void *scales, void *y, int64_t rows, int64_t K,
+                                               mmact_dtype code_dtype, mmact_dtype y_dtype, void *stream)
+{
+    if (!mx_dims(rows, K) || !valid_float(y_dtype) || !valid_f8(code_dtype)) return MMACT_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return MMACT_OK;
+    if (codes == nullptr || scales == nullptr || y == nullptr) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return MMACT_ERR_UNSUPPORTED;
+    DeviceContext dev;
+    const mmact_status st = device_context(&dev);
+    if (st != MMACT_OK) return st;
+    return enqueued(launch_dequantize_fp8(static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), y,
+                                          out_kind(y_dtype), rows, K, f8_kind(code_dtype), dev.sm_count,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+MMACT_EXPORT mmact_status mmact_gemm_fp8(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales,
+                                         const float *bias, void *C, int64_t M, int64_t N, int64_t K, mmact_dtype a_dtype,
+                                         mmact_dtype b_dtype, mmact_dtype c_dtype, mmact_act act, float alpha, void *stream)
+{
+    const F8Matrix A{a_codes, a_scales, a_dtype}, B{b_codes, b_scales, b_dtype};
+    mmact_status s = f8_gemm_check(A, B, bias, C, M, N, K, c_dtype, act);
+    if (s != MMACT_OK) return s;
+    if (M == 0 || N == 0) return MMACT_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
+    F8GemmLaunch L;
+    s = f8_gemm_plan(L, A, B, bias, C, M, N, K, c_dtype, act, alpha);
+    return s == MMACT_OK ? enqueued(launch_gemm_fp8_pair(L, st)) : s;
+}
+
+MMACT_EXPORT mmact_status mmact_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t *bytes)
+{
+    if (!mx_dims(M, K) || bytes == nullptr) return MMACT_ERR_INVALID_ARG;
+    *bytes = linear_bytes(M, K);
+    return MMACT_OK;
+}
+
+MMACT_EXPORT mmact_status mmact_linear_fp8(const void *x, const void *w_codes, const void *w_scales, const float *bias,
+                                           void *C, int64_t M, int64_t N, int64_t K, mmact_dtype x_dtype, mmact_dtype w_dtype,
+                                           mmact_dtype c_dtype, mmact_act act, float alpha, void *workspace, void *stream)
+{
+    if (!mx_dims(M, K) || !valid_float(x_dtype)) return MMACT_ERR_INVALID_ARG;
+    if ((x == nullptr || workspace == nullptr) && M * K != 0) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(workspace)) return MMACT_ERR_UNSUPPORTED;
+    Parts ws{static_cast<char *>(workspace)};
+    const F8Matrix A = M * K != 0 ? ws.matrix(M, K, MMACT_E4M3) : F8Matrix{workspace, workspace, MMACT_E4M3};
+    const F8Matrix W{w_codes, w_scales, w_dtype};
+    mmact_status s = f8_gemm_check(A, W, bias, C, M, N, K, c_dtype, act);
+    if (s != MMACT_OK) return s;
+    if (M == 0 || N == 0) return MMACT_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
+    F8GemmLaunch L;
+    if ((s = f8_gemm_plan(L, A, W, bias, C, M, N, K, c_dtype, act, alpha)) != MMACT_OK) return s;
+    if ((s = enqueued(quantize_launch(x, A, M, K, x_dtype, false, false, st))) != MMACT_OK) return s;
+    return enqueued(launch_gemm_fp8_pair(L, st));
+}
+
+MMACT_EXPORT mmact_status mmact_linear_fp8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t *bytes)
+{
+    if (!mx_dims(M, K) || !mx_dims(N, K) || bytes == nullptr) return MMACT_ERR_INVALID_ARG;
+    if (backward_too_large(M, N, K)) return MMACT_ERR_UNSUPPORTED;
+    *bytes = backward_bytes(M, N, K);
+    return MMACT_OK;
+}
+
+MMACT_EXPORT mmact_status mmact_linear_fp8_backward(const void *dy, const void *x, const void *wt_codes, const void *wt_scales,
+                                                    void *dx, void *dw, float *db, int64_t M, int64_t N, int64_t K,
+                                                    mmact_dtype x_dtype, mmact_dtype wt_dtype, mmact_dtype grad_dtype,
+                                                    mmact_dtype dw_dtype, void *workspace, void *stream)
+{
+    if (!mx_dims(M, K) || !mx_dims(N, K)) return MMACT_ERR_INVALID_ARG;
+    if (!valid_float(x_dtype) || !valid_f8(wt_dtype) || !valid_f8(grad_dtype) || !valid_float(dw_dtype))
+        return MMACT_ERR_INVALID_ARG;
+    const bool any = dx != nullptr || dw != nullptr || db != nullptr;
+    if (any && (dy == nullptr || workspace == nullptr) && M * N != 0) return MMACT_ERR_INVALID_ARG;
+    if (dx != nullptr && (wt_codes == nullptr || wt_scales == nullptr) && M * N * K != 0) return MMACT_ERR_INVALID_ARG;
+    if (dw != nullptr && (x == nullptr || workspace == nullptr) && M * K != 0 && N != 0) return MMACT_ERR_INVALID_ARG;
+    if (db != nullptr && !aligned4(db)) return MMACT_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(wt_codes) || !aligned16(wt_scales) || !aligned16(dx) ||
+        !aligned16(dw) || !aligned16(workspace))
+        return MMACT_ERR_UNSUPPORTED;
+    if (backward_too_large(M, N, K)) return MMACT_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    mmact_status s = MMACT_OK;
+    const bool want_dx = dx != nullptr && M * K != 0, want_dw = dw != nullptr && N * K != 0, want_db = db != nullptr && N != 0;
+    // sums over nothing are zeros
+    if (want_dx && N == 0) return enqueued(launch_mx_bias_act(nullptr, dx, M, K, out_kind(x_dtype), 0, 0.0f, st));
+    if (M == 0) {
+        if (want_dw) s = enqueued(launch_mx_bias_act(nullptr, dw, N, K, out_kind(dw_dtype), 0, 0.0f, st));
+        if (s == MMACT_OK && want_db) s = enqueued(launch_mx_bias_act(nullptr, db, 1, N, OUT_F32, 0, 0.0f, st));
+        return s;
+    }
+    Parts ws{static_cast<char *>(workspace)};
+    const F8Matrix gy = ws.matrix(M, N, grad_dtype), gyt = ws.matrix(N, M, grad_dtype), xt = ws.matrix(K, M, MMACT_E4M3);
+    float *part = static_cast<float *>(ws.take(0));
+    F8GemmLaunch X, W;
+    if (want_dx && (s = f8_gemm_plan(X, gy, F8Matrix{wt_codes, wt_scales, wt_dtype}, nullptr, dx, M, K, N, x_dtype,
+                                     MMACT_ACT_NONE, 0.0f)) != MMACT_OK)
+        return s;
+    if (want_dw && (s = f8_gemm_plan(W, gyt, xt, nullptr, dw, N, K, M, dw_dtype, MMACT_ACT_NONE, 0.0f)) != MMACT_OK) return s;
+    if (want_dx) {
+        if ((s = enqueued(quantize_launch(dy, gy, M, N, x_dtype, false, false, st))) != MMACT_OK) return s;
+        if ((s = enqueued(launch_gemm_fp8_pair(X, st))) != MMACT_OK) return s;
+    }
+    if (want_dw) {
+        if ((s = enqueued(quantize_launch(dy, gyt, N, M, x_dtype, false, true, st))) != MMACT_OK) return s;
+        if ((s = enqueued(quantize_launch(x, xt, K, M, x_dtype, false, true, st))) != MMACT_OK) return s;
+        if ((s = enqueued(launch_gemm_fp8_pair(W, st))) != MMACT_OK) return s;
+    }
+    return want_db ? enqueued(launch_column_sums(dy, out_kind(x_dtype), part, db, M, N, st)) : MMACT_OK;
+}

@@ -19,8 +19,9 @@ LIBRARY = os.path.join(_HERE, "libmmact.so")
 
 MMACT_OK, MMACT_ERR_INVALID_ARG, MMACT_ERR_UNSUPPORTED, MMACT_ERR_CUDA, MMACT_ERR_TIMEOUT = range(5)
 ACT = {"none": 0, "relu": 1, "leaky_relu": 2, "tanh": 3, "sigmoid": 4, "gelu": 5,
-       "silu": 6}   # silu: MXFP4 products and mmact_moe only
+       "silu": 6}   # silu: MXFP4 and 8-bit products and mmact_moe only
 DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+FP8_DTYPE = {torch.float8_e4m3fn: 5, torch.float8_e5m2: 6}   # codes of 8-bit matrices
 MMACT_MXFP4 = 4  # mmact_moe's weights in the 4-bit microscaled format
 MMACT_TF32 = 3   # fp32 inputs computed as tf32 (one pass); float32 tensors default to split precision
 
@@ -40,6 +41,9 @@ SYMBOLS = [
     "mmact_mxfp4_size", "mmact_quantize_mxfp4", "mmact_dequantize_mxfp4", "mmact_gemm_mxfp4",
     "mmact_linear_mxfp4", "mmact_linear_mxfp4_workspace_bytes", "mmact_moe", "mmact_moe_workspace_bytes",
     "mmact_set_gemm_mxfp4_kernel",
+    "mmact_fp8_size", "mmact_quantize_fp8", "mmact_dequantize_fp8", "mmact_gemm_fp8", "mmact_linear_fp8",
+    "mmact_linear_fp8_workspace_bytes", "mmact_linear_fp8_backward", "mmact_linear_fp8_backward_workspace_bytes",
+    "mmact_moe_route", "mmact_moe_route_workspace_bytes", "mmact_moe_route_backward",
 ]
 
 
@@ -117,6 +121,22 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     L.mmact_moe.argtypes = [vp] * 12 + [i64] * 5 + [ci, ci, ci, f32, ci, ci, vp, vp]
     L.mmact_moe_workspace_bytes.argtypes = [i64] * 5 + [p_i64]
     L.mmact_set_gemm_mxfp4_kernel.argtypes = [ci]
+    L.mmact_fp8_size.argtypes = [i64, i64, p_i64, p_i64]
+    L.mmact_quantize_fp8.argtypes = [vp, vp, vp, i64, i64, ci, ci, i64, ci, vp]
+    L.mmact_dequantize_fp8.argtypes = [vp, vp, vp, i64, i64, ci, ci, vp]
+    L.mmact_gemm_fp8.argtypes = [vp] * 6 + [i64, i64, i64, ci, ci, ci, ci, f32, vp]
+    L.mmact_linear_fp8.argtypes = [vp] * 5 + [i64, i64, i64, ci, ci, ci, ci, f32, vp, vp]
+    L.mmact_linear_fp8_workspace_bytes.argtypes = [i64, i64, p_i64]
+    L.mmact_linear_fp8_backward.argtypes = [vp] * 7 + [i64, i64, i64, ci, ci, ci, ci, vp, vp]
+    L.mmact_linear_fp8_backward_workspace_bytes.argtypes = [i64, i64, i64, p_i64]
+    L.mmact_moe_route.argtypes = [vp] * 6 + [i64, i64, i64, ci, ci, f32, vp, vp]
+    L.mmact_moe_route_workspace_bytes.argtypes = [i64, i64, p_i64]
+    L.mmact_moe_route_backward.argtypes = [vp] * 7 + [i64, i64, i64, ci, ci, f32, vp]
+    for name in ("mmact_moe_route", "mmact_moe_route_workspace_bytes", "mmact_moe_route_backward",
+                 "mmact_fp8_size", "mmact_quantize_fp8", "mmact_dequantize_fp8", "mmact_gemm_fp8", "mmact_linear_fp8",
+                 "mmact_linear_fp8_workspace_bytes", "mmact_linear_fp8_backward",
+                 "mmact_linear_fp8_backward_workspace_bytes"):
+        getattr(L, name).restype = ci
     for name in ("mmact_mxfp4_size", "mmact_quantize_mxfp4", "mmact_dequantize_mxfp4", "mmact_gemm_mxfp4",
                  "mmact_linear_mxfp4", "mmact_linear_mxfp4_workspace_bytes", "mmact_moe",
                  "mmact_moe_workspace_bytes", "mmact_set_gemm_mxfp4_kernel"):
@@ -534,6 +554,154 @@ def mmact_set_gemm_mxfp4_kernel(mode: int) -> None:
     _check(load().mmact_set_gemm_mxfp4_kernel(int(mode)), "mmact_set_gemm_mxfp4_kernel")
 
 
+def mmact_fp8_size(rows: int, K: int) -> tuple[int, int]:
+    """(bytes of codes, bytes of scales) of an 8-bit matrix [rows, K] (see include/mmact.h)."""
+    c, s = ctypes.c_int64(0), ctypes.c_int64(0)
+    _check(load().mmact_fp8_size(int(rows), int(K), ctypes.byref(c), ctypes.byref(s)), "mmact_fp8_size")
+    return c.value, s.value
+
+
+_F8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+
+
+def _fp8_ptrs(codes, scales, rows: int, K: int, name: str):
+    # the sizes of mmact_fp8_size; the codes' dtype is the format; _dev says what else is wrong
+    code = FP8_DTYPE.get(codes.dtype) if isinstance(codes, torch.Tensor) else None
+    if code is None or not codes.is_cuda or not codes.is_contiguous():
+        _dev(codes, name + " codes", _F8)
+    _dev(scales, name + " scales", _BYTES)
+    if codes.numel() != rows * ((K + 15) // 16 * 16):
+        raise ValueError(f"{name} codes must hold {rows} x {(K + 15) // 16 * 16} bytes")
+    if scales.numel() != (rows + 127) // 128 * ((K + 511) // 512) * 512:
+        raise ValueError(f"{name} scales must hold {(rows + 127) // 128} x {(K + 511) // 512} tiles of 512 bytes")
+    return codes.data_ptr(), scales.data_ptr(), code
+
+
+def _here(first, *rest) -> None:
+    """The tensors of a call lie on one device, the current one: its stream gets the kernels."""
+    dev = first.device
+    if dev.index != (_CUR_DEVICE() if _CUR_DEVICE is not None else torch.cuda.current_device()):
+        raise ValueError(f"tensors on {dev}, which is not the current device")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and on {t.device}")
+
+
+def mmact_quantize_fp8(x, codes, scales, block_rows: int = 1, transposed: bool = False, stream=None) -> None:
+    """Quantise x [rows, K] (or, transposed, [K, rows]) to 8 bits with a scale for 128 values along K,
+    or (block_rows 128) for 128 x 128; codes is a float8_e4m3fn or float8_e5m2 tensor and scales a uint8
+    tensor of mmact_fp8_size(rows, K) bytes."""
+    px, dt, rows, K = _matrix(x, "x")
+    if transposed:
+        rows, K = K, rows
+    pc, ps, kind = _fp8_ptrs(codes, scales, rows, K, "x")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    _here(x, codes, scales)
+    s = (_lib or load()).mmact_quantize_fp8(px, pc, ps, rows, K, dt, kind, block_rows, 1 if transposed else 0,
+                                            _stream_handle(stream))
+    if s:
+        _check(s, "mmact_quantize_fp8")
+
+
+def mmact_dequantize_fp8(codes, scales, y, stream=None) -> None:
+    """y [rows, K] = the values of an 8-bit matrix."""
+    py, dt, rows, K = _matrix(y, "y")
+    pc, ps, kind = _fp8_ptrs(codes, scales, rows, K, "y")
+    _here(y, codes, scales)
+    s = (_lib or load()).mmact_dequantize_fp8(pc, ps, py, rows, K, kind, dt, _stream_handle(stream))
+    if s:
+        _check(s, "mmact_dequantize_fp8")
+
+
+def mmact_gemm_fp8(a_codes, a_scales, b_codes, b_scales, bias, C, K: int, act: str = "none", alpha: float = 0.0,
+                   stream=None) -> None:
+    """C = act(A @ B.T + bias) of 8-bit matrices A [M, K] and B [N, K]; C [M, N]."""
+    pc, dt, M, N = _matrix(C, "C")
+    pa, psa, ka = _fp8_ptrs(a_codes, a_scales, M, K, "A")
+    pb, psb, kb = _fp8_ptrs(b_codes, b_scales, N, K, "B")
+    pbias = _bias_ptr(bias, N)
+    _here(C, a_codes, a_scales, b_codes, b_scales, bias)
+    s = (_lib or load()).mmact_gemm_fp8(pa, psa, pb, psb, pbias, pc, M, N, K, ka, kb, dt, ACT[act], alpha,
+                                        _stream_handle(stream))
+    if s:
+        _check(s, "mmact_gemm_fp8")
+
+
+def mmact_linear_fp8_workspace_bytes(M: int, K: int) -> int:
+    """Bytes of the workspace that mmact_linear_fp8 needs for x [M, K]."""
+    out = ctypes.c_int64(0)
+    _check(load().mmact_linear_fp8_workspace_bytes(int(M), int(K), ctypes.byref(out)), "mmact_linear_fp8_workspace_bytes")
+    return out.value
+
+
+def mmact_linear_fp8(x, w_codes, w_scales, bias, C, workspace, act: str = "none", alpha: float = 0.0,
+                     stream=None) -> None:
+    """C = act(q(x) @ W.T + bias): x [M, K] is quantised to E4M3 on the way in, W [N, K] is held in 8 bits."""
+    px, xd, M, K = _matrix(x, "x")
+    pc, cd, rows, N = _matrix(C, "C")
+    if rows != M:
+        raise ValueError("x must be [M, K] and C [M, N]")
+    pw, ps, kw = _fp8_ptrs(w_codes, w_scales, N, K, "W")
+    pbias = _bias_ptr(bias, N)
+    pws = _dev(workspace, "workspace", _BYTES)
+    if workspace.numel() < -(-M * ((K + 15) // 16 * 16) // 512) * 512 + (M + 127) // 128 * ((K + 511) // 512) * 512:
+        raise ValueError("workspace must hold mmact_linear_fp8_workspace_bytes(M, K) bytes")
+    _here(x, C, w_codes, w_scales, bias, workspace)
+    s = (_lib or load()).mmact_linear_fp8(px, pw, ps, pbias, pc, M, N, K, xd, kw, cd, ACT[act], alpha, pws,
+                                          _stream_handle(stream))
+    if s:
+        _check(s, "mmact_linear_fp8")
+
+
+def mmact_linear_fp8_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of the workspace that mmact_linear_fp8_backward needs for x [M, K] and dy [M, N]."""
+    out = ctypes.c_int64(0)
+    _check(load().mmact_linear_fp8_backward_workspace_bytes(int(M), int(N), int(K), ctypes.byref(out)),
+           "mmact_linear_fp8_backward_workspace_bytes")
+    return out.value
+
+
+_F8_BACKWARD_WORKSPACE: dict = {}
+
+
+def mmact_linear_fp8_backward(dy, x, wt_codes, wt_scales, dx, dw, db, workspace, grad_type=torch.float8_e5m2,
+                              stream=None) -> None:
+    """Gradients of x @ W.T + bias in 8 bits (see include/mmact.h): dy [M, N] and x [M, K] of one dtype, Wt
+    [K, N] = W turned round in 8 bits; dx [M, K] of x's dtype, dw [N, K], db [N] float32, each may be None.
+    dy is quantised to grad_type, x to E4M3."""
+    pdy, xd, M, N = _matrix(dy, "dy")
+    px, xd2, rows, K = _matrix(x, "x")
+    if rows != M or xd2 != xd:
+        raise ValueError("dy must be [M, N] and x [M, K] of the same dtype")
+    if grad_type not in FP8_DTYPE:
+        raise TypeError(f"grad_type {grad_type} not in {_F8}")
+    pdx = pdw = pw = ps = None
+    kw, wd = FP8_DTYPE[torch.float8_e4m3fn], DTYPE[torch.float32]
+    if dx is not None:
+        pdx = _dev(dx, "dx", (x.dtype,))
+        if tuple(dx.shape) != (M, K):
+            raise ValueError("dx must be [M, K]")
+        pw, ps, kw = _fp8_ptrs(wt_codes, wt_scales, K, N, "Wt")
+    if dw is not None:
+        pdw, wd, r, c = _matrix(dw, "dw")
+        if (r, c) != (N, K):
+            raise ValueError("dw must be [N, K]")
+    pdb = _f32_ptr(db, (N,), "db")
+    pws = _dev(workspace, "workspace", _BYTES)
+    need = _F8_BACKWARD_WORKSPACE.get((M, N, K))
+    if need is None:
+        if len(_F8_BACKWARD_WORKSPACE) > 1024:
+            _F8_BACKWARD_WORKSPACE.clear()
+        need = _F8_BACKWARD_WORKSPACE[M, N, K] = mmact_linear_fp8_backward_workspace_bytes(M, N, K)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    _here(dy, x, dx, dw, db, workspace, *(() if dx is None else (wt_codes, wt_scales)))
+    _check((_lib or load()).mmact_linear_fp8_backward(pdy, px, pw, ps, pdx, pdw, pdb, M, N, K, xd, kw,
+                                                      FP8_DTYPE[grad_type], wd, pws, _stream_handle(stream)),
+           "mmact_linear_fp8_backward")
+
+
 def mmact_moe_workspace_bytes(T: int, H: int, I: int, E: int, top: int) -> int:
     """Bytes of the workspace that mmact_moe needs."""
     out = ctypes.c_int64(0)
@@ -607,6 +775,78 @@ def mmact_moe(x, router, w1, w2, y, experts, probs, workspace, act: str = "silu"
                        _f32_ptr(b1, (E, halves * I), "b1"), p2, ps2, _f32_ptr(b2, (E, H), "b2"), py, pe, pp, T, H, I, E,
                        top, DTYPE[x.dtype], wd, ACT[act], float(alpha), 1 if gated else 0, 1 if normalize else 0, pws,
                        _stream_handle(stream)), "mmact_moe")
+
+
+def mmact_moe_route_workspace_bytes(T: int, E: int) -> int:
+    """Bytes of the workspace that mmact_moe_route needs."""
+    out = ctypes.c_int64(0)
+    _check(load().mmact_moe_route_workspace_bytes(int(T), int(E), ctypes.byref(out)), "mmact_moe_route_workspace_bytes")
+    return out.value
+
+
+_ROUTE_WORKSPACE: dict = {}
+
+
+def _route_args(logits, mask, experts, counts):
+    pz, dt, T, E = _matrix(logits, "logits")
+    pe, pc = _dev(experts, "experts", (torch.int32,)), _dev(counts, "counts", (torch.int32,))
+    if experts.dim() != 2 or experts.shape[0] != T:
+        raise ValueError("experts must be [T, top]")
+    if counts.numel() != E + 1:
+        raise ValueError("counts must be [E + 1]")
+    pm = None
+    if mask is not None:
+        pm = _dev(mask, "mask", (torch.uint8, torch.bool))
+        if tuple(mask.shape) != (T,):
+            raise ValueError("mask must be [T]")
+    return pz, pm, pe, pc, T, E, experts.shape[1], dt
+
+
+def _one_f32(t, name: str):
+    p = _dev(t, name, (torch.float32,))
+    if t.numel() != 1:
+        raise ValueError(f"{name} must have one element")
+    return p
+
+
+def mmact_moe_route(logits, experts, probs, counts, loss, workspace, coef: float = 1.0, normalize: bool = True, mask=None,
+                    stream=None) -> None:
+    """A router in training (see include/mmact.h): from logits [T, E] the outputs experts [T, top] int32, probs
+    [T, top] float32, counts [E + 1] int32 and loss [1] float32; mask [T] uint8 or bool leaves out tokens."""
+    pz, pm, pe, pc, T, E, top, dt = _route_args(logits, mask, experts, counts)
+    pp, pl = _dev(probs, "probs", (torch.float32,)), _one_f32(loss, "loss")
+    if probs.shape != experts.shape:
+        raise ValueError("experts and probs must be [T, top]")
+    pws = _dev(workspace, "workspace", _BYTES)
+    need = _ROUTE_WORKSPACE.get((T, E))
+    if need is None:
+        if len(_ROUTE_WORKSPACE) > 1024:
+            _ROUTE_WORKSPACE.clear()
+        need = _ROUTE_WORKSPACE[T, E] = mmact_moe_route_workspace_bytes(T, E)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    _here(logits, mask, experts, probs, counts, loss, workspace)
+    s = (_lib or load()).mmact_moe_route(pz, pm, pe, pp, pc, pl, T, E, top, dt, 1 if normalize else 0, coef, pws,
+                                         _stream_handle(stream))
+    if s:
+        _check(s, "mmact_moe_route")
+
+
+def mmact_moe_route_backward(logits, experts, counts, dprobs, dloss, dlogits, coef: float = 1.0, normalize: bool = True,
+                             mask=None, stream=None) -> None:
+    """The gradient dlogits [T, E] of mmact_moe_route's logits from dprobs [T, top] and dloss [1] (float32, either
+    may be None); logits, experts, counts, coef, normalize and mask are the forward pass's."""
+    pz, pm, pe, pc, T, E, top, dt = _route_args(logits, mask, experts, counts)
+    pd = _dev(dlogits, "dlogits", (logits.dtype,))
+    if dlogits.shape != logits.shape:
+        raise ValueError("dlogits must be [T, E]")
+    pg = _f32_ptr(dprobs, tuple(experts.shape), "dprobs")
+    pl = None if dloss is None else _one_f32(dloss, "dloss")
+    _here(logits, mask, experts, counts, dprobs, dloss, dlogits)
+    s = (_lib or load()).mmact_moe_route_backward(pz, pm, pe, pc, pg, pl, pd, T, E, top, dt, 1 if normalize else 0, coef,
+                                                  _stream_handle(stream))
+    if s:
+        _check(s, "mmact_moe_route_backward")
 
 
 def mmact_get_last_error(stream=None) -> int:

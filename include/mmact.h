@@ -26,10 +26,18 @@
  *   C = act(A x B^T + bias), A and B in MXFP4             mmact_gemm_mxfp4, mmact_linear_mxfp4
  *     Products of 4-bit operands with the same epilogue (OCP Microscaling
  *     Formats specification 1.0: E2M1 elements, a power-of-two scale for 32).
+ *   codes, scales = fp8(x); x = values(codes, scales)     mmact_quantize_fp8, mmact_dequantize_fp8
+ *   C = act(A x B^T + bias), A and B in 8 bits            mmact_gemm_fp8, mmact_linear_fp8
+ *   dx, dw, db of the linear layer                        mmact_linear_fp8_backward
+ *     Products of 8-bit floating-point operands with the same epilogue, a
+ *     power-of-two scale for 128 values, and their gradients.
  *   y = mixture of experts(x)                             mmact_moe
  *     Router, choice of experts, both products, activation and weighted sum
  *     for a few tokens; experts' weights in 16 bits or in MXFP4.
- *     (The pages have no counterpart of either: these are the operators that
+ *   experts, probs, counts, loss = router(logits)         mmact_moe_route, mmact_moe_route_backward
+ *     The router of a mixture in training: choice, probabilities, slots of each
+ *     expert and the loss that balances them, and the logits' gradient.
+ *     (The pages have no counterpart of these: they are the operators that
  *     a model's feed-forward path needs beside the products above.)
  *
  * Activations (all evaluated in fp32 on the fp32 accumulator plus the fp32
@@ -43,8 +51,8 @@
  *   MMACT_ACT_GELU        z/2 * (1 + erf(z / sqrt(2)))   (the fused_matmul_relu
  *                         article's matmul + GELU / Sigmoid / Tanh family; exact
  *                         erf form, the pages print no formula)
- *   MMACT_ACT_SILU        z / (1 + e^-z)       (mmact_gemm_mxfp4, mmact_linear_mxfp4
- *                         and mmact_moe only)
+ *   MMACT_ACT_SILU        z / (1 + e^-z)       (mmact_gemm_mxfp4, mmact_linear_mxfp4,
+ *                         mmact_gemm_fp8, mmact_linear_fp8 and mmact_moe only)
  *
  * Conventions for every entry point
  *   - Tensor pointers are DEVICE pointers (cudaMalloc / torch CUDA memory) on
@@ -88,7 +96,7 @@ typedef enum {
     MMACT_ACT_TANH = 3,
     MMACT_ACT_SIGMOID = 4,
     MMACT_ACT_GELU = 5,
-    MMACT_ACT_SILU = 6   /* MXFP4 products and mmact_moe only */
+    MMACT_ACT_SILU = 6   /* MXFP4 and 8-bit products and mmact_moe only */
 } mmact_act;
 
 typedef enum {
@@ -96,7 +104,9 @@ typedef enum {
     MMACT_BF16 = 1,
     MMACT_F32 = 2,   /* as an input: fp32 values used to fp32 accuracy (split precision, below) */
     MMACT_TF32 = 3,  /* input only: fp32 values rounded to tf32 (10 fraction bits) by the tensor core */
-    MMACT_MXFP4 = 4  /* mmact_moe's weights only: 4-bit microscaled (below) */
+    MMACT_MXFP4 = 4, /* mmact_moe's weights only: 4-bit microscaled (below) */
+    MMACT_E4M3 = 5,  /* 8-bit floating point with block scales (below): 4 exponent bits, 3 fraction bits */
+    MMACT_E5M2 = 6   /* the same with 5 and 2 */
 } mmact_dtype;
 
 /*
@@ -571,6 +581,100 @@ mmact_status mmact_linear_mxfp4_workspace_bytes(int64_t M, int64_t K, int64_t *b
 mmact_status mmact_set_gemm_mxfp4_kernel(int mode);
 
 /*
+ * 8-bit floating point with a scale for each block of 128.  128 consecutive values
+ * along K share a scale X = 2^(b - 127), b one byte (255: NaN); a value is X times an
+ * E4M3 number (4 exponent bits, 3 fraction bits, largest 448, no infinities) or an
+ * E5M2 number (largest 57344).  A matrix [rows, K] is two arrays:
+ *   codes   [rows][KP] bytes, KP = K rounded up to a multiple of 16; codes past K
+ *           have to be 0 (mmact_quantize_fp8 writes them so)
+ *   scales  tiles of 512 bytes, [ceil(rows / 128)][ceil(KB / 4)], KB = ceil(K / 128); the
+ *           scale of row r and block b is byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of
+ *           its tile, the order in which the tensor core reads them; bytes of
+ *           rows and blocks that do not exist are 0
+ * Both arrays are 16-byte aligned.  Scales are powers of two because the tensor core
+ * multiplies by those itself; a matrix quantised elsewhere with other scales is
+ * brought into this form by mmact_quantize_fp8 from its values.  mmact_fp8_size gives
+ * the arrays' sizes in bytes (host only; MMACT_ERR_INVALID_ARG for a null pointer or
+ * a negative extent).
+ */
+mmact_status mmact_fp8_size(int64_t rows, int64_t K, int64_t *codes_bytes, int64_t *scales_bytes);
+
+/*
+ * Quantise x with blocks along K.
+ *   x  transposed == 0: [rows, K] row-major; transposed != 0: [K, rows]
+ *      row-major (mmact_gemm's B, or a weight turned round for
+ *      mmact_linear_fp8_backward); x_dtype F16, BF16 or F32
+ *   code_dtype  E4M3 or E5M2
+ *   block_rows  1: 128 values of one row share a scale; 128: so do 128 rows (row
+ *      128 i and the 127 after it: the blocks of a weight, whose transposed form has
+ *      the same codes).  The arrays are laid out alike.
+ *   X is the smallest power of two, 2^-127 at least, for which no |x| / X passes
+ *   the type's largest number; values x / X are rounded to nearest even.  A block
+ *   with an infinity or a NaN gets b = 255 and codes 0: it reads back as NaN.
+ * Every byte of codes and scales is written.  Results do not depend on the
+ * order of anything: they are exact.
+ */
+mmact_status mmact_quantize_fp8(const void *x, void *codes, void *scales, int64_t rows, int64_t K,
+                                mmact_dtype x_dtype, mmact_dtype code_dtype, int64_t block_rows, int transposed,
+                                void *stream);
+
+/* y [rows, K] row-major (F16, BF16 or F32) = the values of an 8-bit matrix, rounded to y_dtype (the largest
+ * value of a block may have been rounded up to a power of two that y_dtype does not reach: infinity). */
+mmact_status mmact_dequantize_fp8(const void *codes, const void *scales, void *y, int64_t rows, int64_t K,
+                                  mmact_dtype code_dtype, mmact_dtype y_dtype, void *stream);
+
+/*
+ * C = act(A x B^T + bias) of 8-bit matrices A [M, K] and B [N, K] (each E4M3 or
+ * E5M2, both with their blocks along K), bias [N] fp32 or NULL, C [M, N] row-major
+ * in c_dtype, accumulated in fp32 on the tensor cores and rounded once.  Any M, N
+ * and K: an N whose rows of C are not a multiple of 16 bytes is stored element by
+ * element (slower).  M == 0 or N == 0 enqueues nothing; K == 0 gives
+ * C = act(bias).  A NaN scale makes the rows or columns of C it reaches NaN.
+ */
+mmact_status mmact_gemm_fp8(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales,
+                            const float *bias, void *C, int64_t M, int64_t N, int64_t K, mmact_dtype a_dtype,
+                            mmact_dtype b_dtype, mmact_dtype c_dtype, mmact_act act, float alpha, void *stream);
+
+/*
+ * C = act(q(x) x W^T + bias): x [M, K] row-major in x_dtype (F16, BF16 or F32)
+ * is quantised to E4M3 (block_rows 1) on the way in, W [N, K] is held in 8 bits
+ * (w_dtype).  The same result as mmact_quantize_fp8 into `workspace` and
+ * mmact_gemm_fp8.
+ *   workspace  at least mmact_linear_fp8_workspace_bytes, 16-byte aligned,
+ *              contents ignored and undefined afterwards; calls that may
+ *              overlap on the GPU need one each.
+ */
+mmact_status mmact_linear_fp8(const void *x, const void *w_codes, const void *w_scales, const float *bias, void *C,
+                              int64_t M, int64_t N, int64_t K, mmact_dtype x_dtype, mmact_dtype w_dtype,
+                              mmact_dtype c_dtype, mmact_act act, float alpha, void *workspace, void *stream);
+
+/* Bytes of mmact_linear_fp8's workspace (host only). */
+mmact_status mmact_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t *bytes);
+
+/*
+ * Gradients of z = q(x) x W^T + bias from dy = the gradient of z (before the
+ * activation), x [M, K] and dy [M, N] row-major in x_dtype (F16, BF16 or F32):
+ *   dx [M, K] (x_dtype)   = q(dy) x Wt^T, q along N; Wt [K, N] is W turned round, in 8
+ *                           bits (wt_dtype) with its blocks along N: mmact_quantize_fp8 of
+ *                           W [N, K] with rows = K, K = N, transposed = 1 and block_rows
+ *                           128 gives W's own codes when W was quantised with 128
+ *   dw [N, K] (dw_dtype)  = q(dy^T) x q(x^T)^T, q along M
+ *   db [N] fp32           = sum over M of dy, unquantised, in fp32, in an order that
+ *                           depends on M alone
+ * dy is quantised to grad_dtype (E4M3 or E5M2), x to E4M3.  Each of dx, dw and db may
+ * be NULL and is then not computed; each other one is overwritten.  Products over
+ * an empty dimension are zeros.  The outputs must not overlap the inputs.
+ *   workspace  at least mmact_linear_fp8_backward_workspace_bytes, as above.
+ */
+mmact_status mmact_linear_fp8_backward(const void *dy, const void *x, const void *wt_codes, const void *wt_scales,
+                                       void *dx, void *dw, float *db, int64_t M, int64_t N, int64_t K,
+                                       mmact_dtype x_dtype, mmact_dtype wt_dtype, mmact_dtype grad_dtype,
+                                       mmact_dtype dw_dtype, void *workspace, void *stream);
+
+/* Bytes of mmact_linear_fp8_backward's workspace (host only). */
+mmact_status mmact_linear_fp8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t *bytes);
+
+/*
  * A whole mixture-of-experts layer for a few tokens (T <= 64), in two kernels:
  *   logits[t][e] = x[t] . router[e] + router_bias[e]
  *   experts[t]   = the `top` experts of the largest logits, largest first (equal
@@ -605,6 +709,50 @@ mmact_status mmact_moe(const void *x, const void *router, const float *router_bi
 
 /* Bytes of mmact_moe's workspace (host only). */
 mmact_status mmact_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top, int64_t *bytes);
+
+/*
+ * The router of a mixture-of-experts layer in training, from its logits (any number
+ * of tokens; mmact_moe's own choice and probabilities for the same logits):
+ *   logits [T, E] row-major in logits_dtype (F16, BF16 or F32), 16-byte aligned
+ *   mask   [T] bytes or NULL: a token whose byte is 0 is left out
+ *   experts[t][j] the `top` experts of the largest logits, largest first (equal
+ *          logits: the lower index first; NaN counts as the largest).  An expert whose
+ *          logit is -inf is never chosen: such slots, and those of tokens left out, are -1
+ *   probs[t][j]   softmax of the chosen logits (normalize != 0), or of all logits at
+ *          the chosen experts (normalize == 0); 0 in a slot of -1
+ *   counts[e]     slots that chose expert e; counts[E] the number n of tokens with a slot
+ *   loss[0] = coef * E * sum_e counts[e] / (n top) * (1 / n) sum_t softmax(logits[t])[e], over
+ *          the tokens with a slot; 0 when there is none.  It is coef when both shares are even.
+ *   experts [T, top] int32, probs [T, top] fp32, counts [E + 1] int32, loss [1] fp32: outputs
+ *   workspace  at least mmact_moe_route_workspace_bytes, 16-byte aligned, contents
+ *          ignored; calls that may overlap on the GPU need one each
+ * Softmax and sums are held in fp32 and added up in a fixed order: results repeat
+ * bit for bit on one kind of device.  A token with a NaN or +inf among its logits has
+ * NaN probabilities and makes the loss NaN.  Limits: 1 <= E <= 512, 1 <= top <= min(E, 16),
+ * T top < 2^31, else MMACT_ERR_UNSUPPORTED.  T == 0 gives counts and loss of 0.
+ */
+mmact_status mmact_moe_route(const void *logits, const uint8_t *mask, int32_t *experts, float *probs,
+                             int32_t *counts, float *loss, int64_t T, int64_t E, int64_t top,
+                             mmact_dtype logits_dtype, int normalize, float coef, void *workspace, void *stream);
+
+/* Bytes of mmact_moe_route's workspace (host only). */
+mmact_status mmact_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t *bytes);
+
+/*
+ * The gradient of mmact_moe_route's logits from those of its probabilities (dprobs [T,
+ * top] fp32, or NULL for zeros) and of its loss (dloss, one fp32 on the device, or
+ * NULL for 0); logits, mask, experts and counts are the forward pass's, normalize and
+ * coef too.  The choice and the counts are constants:
+ *   dlogits[t] = softmax's derivative, at logits[t], of
+ *                dprobs . probs + dloss * coef * E / (n^2 top) * counts . softmax
+ *   dlogits [T, E] in logits_dtype, overwritten; rows of tokens left out, or with
+ *          nothing but -inf, are 0.  Slots outside 0..E-1 count as -1; an expert twice
+ *          among a token's slots adds up.
+ */
+mmact_status mmact_moe_route_backward(const void *logits, const uint8_t *mask, const int32_t *experts,
+                                      const int32_t *counts, const float *dprobs, const float *dloss, void *dlogits,
+                                      int64_t T, int64_t E, int64_t top, mmact_dtype logits_dtype, int normalize,
+                                      float coef, void *stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *mmact_status_string(mmact_status status);
