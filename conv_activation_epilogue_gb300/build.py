@@ -20,7 +20,8 @@ LIBRARY = os.path.join(HERE, "libmmact.so")
 SOURCES = ["api.cu", "gemm.cu", "gemm_splitk.cu", "gemm_pair.cu", "conv.cu", "conv_vec.cu", "conv_nhwc.cu", "conv_tmem.cu", "elementwise.cu", "noalloc.cu",
            "api_mx.cu", "mxfp4.cu", "gemm_mxfp4.cu",
            "gemm_mxfp4_rows.cu", "moe.cu", "moe_mxfp4.cu",
-           "api_fp8.cu", "fp8.cu", "gemm_fp8.cu", "api_route.cu", "moe_route.cu"]
+           "api_fp8.cu", "fp8.cu", "gemm_fp8.cu", "gemm_fp8_rows.cu",
+           "api_route.cu", "moe_route.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

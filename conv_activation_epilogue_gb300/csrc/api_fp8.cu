@@ -25,27 +25,32 @@ namespace {
 bool valid_f8(mmact_dtype d) { return d == MMACT_E4M3 || d == MMACT_E5M2; }
 int f8_kind(mmact_dtype d) { return d == MMACT_E5M2 ? F8_E5M2 : F8_E4M3; }
 
+std::atomic<int> g_f8_kernel{0};   // 0: chosen per shape; 1: rows kernel; 2: pair kernel
+
 // The current device, with this file's kernels set up on it (once per device).
 struct F8Context {
     DeviceContext dev;
     int max_pairs;                   // CTA pairs of the pair kernel resident at once
+    const int *max_clusters;         // [i]: clusters of 2^i CTAs of the rows kernel
 };
 
 mmact_status f8_context(F8Context *out)
 {
     static std::mutex mutex;
     static std::atomic<bool> ready[MAX_DEVICES];
-    static int pairs[MAX_DEVICES];
+    static int pairs[MAX_DEVICES], clusters[MAX_DEVICES][4];
     const mmact_status s = device_context(&out->dev);
     if (s != MMACT_OK) return s;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
     if (!ready[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(mutex);               // setting up twice is harmless
-        if (setup_fp8_pair_kernels(&pairs[dev]) != cudaSuccess) return MMACT_ERR_CUDA;
+        if (setup_fp8_pair_kernels(&pairs[dev]) != cudaSuccess || setup_fp8_rows_kernels(clusters[dev]) != cudaSuccess)
+            return MMACT_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
     out->max_pairs = pairs[dev];
+    out->max_clusters = clusters[dev];
     return MMACT_OK;
 }
 
@@ -88,41 +93,116 @@ bool f8_encode(CUtensorMap *mc, CUtensorMap *ms, const F8Matrix &m, int64_t rows
            encode_tensor_map(ms, MMACT_F32, 2, m.scales, ds, ss, bs, false);
 }
 
-mmact_status f8_gemm_plan(F8GemmLaunch &L, const F8Matrix &A, const F8Matrix &B, const float *bias, void *C, int64_t M,
-                          int64_t N, int64_t K, mmact_dtype cd, mmact_act act, float alpha)
+// Plan of one product: either kernel's launch.
+struct F8Plan {
+    bool pair, quantize;             // quantize: x first, by a kernel of its own
+    F8GemmLaunch P;
+    F8RowsLaunch R;
+};
+
+// Whether a product runs on the pair kernel: when the rows kernel would have more
+// tiles (128 x 128) than there are SMs.
+bool f8_choose_pair(const F8Context &c, int64_t M, int64_t N)
+{
+    const int mode = g_f8_kernel.load();
+    if (c.max_pairs < 1 || mode == 1) return false;
+    if (mode == 2) return true;
+    return M > 128 && ((M + 127) / 128) * ((N + 127) / 128) > c.dev.sm_count;
+}
+
+// Rows of x up to which the rows kernel quantises them itself.
+constexpr int64_t F8_FUSED_ROWS = 8;
+
+// `x` (or null): A [M, K] in x_type, to be quantised into A, as by f8_gemm_launch, or
+// by the rows kernel on the way.
+mmact_status f8_gemm_plan(F8Plan &plan, const F8Matrix &A, const F8Matrix &B, const float *bias, void *C, int64_t M,
+                          int64_t N, int64_t K, mmact_dtype cd, mmact_act act, float alpha, const void *x = nullptr,
+                          mmact_dtype x_type = MMACT_F32)
 {
     F8Context c;
     const mmact_status st = f8_context(&c);
     if (st != MMACT_OK) return st;
-    if (c.max_pairs < 1) return MMACT_ERR_CUDA;
+    const int nk32 = (int)((K + 31) / 32), num_kb = (int)f8_blocks(K);
+    plan.pair = f8_choose_pair(c, M, N);
+    plan.quantize = x != nullptr && plan.pair;
+    if (plan.pair) {
+        F8GemmLaunch &L = plan.P;
+        std::memset(&L, 0, sizeof(L));
+        F8GemmArgs &a = L.args;
+        a.M = (int)M;
+        a.N = (int)N;
+        a.nk32 = nk32;
+        a.num_kb = num_kb;
+        a.tiles_m = (int)((M + 255) / 256);
+        a.tiles_n = (int)((N + 255) / 256);
+        a.num_tiles = a.tiles_m * a.tiles_n;
+        a.group_m = 8;
+        a.act = (int)act;
+        a.alpha = alpha;
+        a.bias = bias;
+        a.C = C;
+        a.idesc = ptx::idesc_f8(f8_kind(A.type), f8_kind(B.type), 256, 256);
+        a.status = c.dev.status;
+        a.wait_ns = c.dev.wait_ns;
+        const int ce = elem_bytes(cd);
+        a.c_tma = N * ce % 16 == 0 ? 1 : 0;
+        L.out = out_kind(cd);
+        L.grid = 2 * (int)std::min<int64_t>(a.num_tiles, c.max_pairs);
+        if (!f8_encode(&L.tmA, &L.tmSA, A, M, K, 128, 1) || !f8_encode(&L.tmB, &L.tmSB, B, N, K, 128, 2)) return MMACT_ERR_CUDA;
+        if (a.c_tma) {
+            const uint64_t dC[2] = {(uint64_t)N, (uint64_t)M}, sC[1] = {(uint64_t)N * ce};
+            const uint32_t bC[2] = {(uint32_t)(128 / ce), 32};
+            if (!encode_tensor_map(&L.tmC, cd, 2, C, dC, sC, bC, true)) return MMACT_ERR_CUDA;
+        }
+        return MMACT_OK;
+    }
+    F8RowsLaunch &L = plan.R;
     std::memset(&L, 0, sizeof(L));
-    F8GemmArgs &a = L.args;
+    F8RowsArgs &a = L.args;
     a.M = (int)M;
     a.N = (int)N;
-    a.nk32 = (int)((K + 31) / 32);
-    a.num_kb = (int)f8_blocks(K);
-    a.tiles_m = (int)((M + 255) / 256);
-    a.tiles_n = (int)((N + 255) / 256);
-    a.num_tiles = a.tiles_m * a.tiles_n;
-    a.group_m = 8;
+    a.K = (int)K;
+    a.nk32 = nk32;
+    a.num_kb = num_kb;
+    a.tiles_n = (int)((N + 127) / 128);
+    const int sms = c.dev.sm_count;
+    // the narrowest tile that takes every row (a narrower one than 128 has to be the only one)
+    int bt = 16;
+    while (bt < 128 && bt < M) bt *= 2;
+    const int64_t tiles = a.tiles_n * ((M + bt - 1) / bt);
+    if (tiles * 8 > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
+    // CTAs to a tile: as long as that leaves no cluster waiting for SMs and each CTA two K blocks
+    int split = 1, log2 = 0;
+    while (split < 8 && tiles * split * 2 <= sms && tiles <= c.max_clusters[log2 + 1] && num_kb >= split * 2) split *= 2, ++log2;
+    a.kb_per = (num_kb + split - 1) / split;
+    while (split > 1 && (split - 1) * a.kb_per >= num_kb) split /= 2, a.kb_per = (num_kb + split - 1) / split;
+    a.stages = std::min(F8_ROWS_STAGES(bt), a.kb_per);
+    a.split = split;
     a.act = (int)act;
     a.alpha = alpha;
     a.bias = bias;
     a.C = C;
-    a.idesc = ptx::idesc_f8(f8_kind(A.type), f8_kind(B.type), 256, 256);
+    // the operands change sides: B's rows are the instruction's A
+    a.idesc = ptx::idesc_f8(f8_kind(B.type), f8_kind(A.type), 128, bt);
     a.status = c.dev.status;
     a.wait_ns = c.dev.wait_ns;
-    const int ce = elem_bytes(cd);
-    a.c_tma = N * ce % 16 == 0 ? 1 : 0;
     L.out = out_kind(cd);
-    L.grid = 2 * (int)std::min<int64_t>(a.num_tiles, c.max_pairs);
-    if (!f8_encode(&L.tmA, &L.tmSA, A, M, K, 128, 1) || !f8_encode(&L.tmB, &L.tmSB, B, N, K, 128, 2)) return MMACT_ERR_CUDA;
-    if (a.c_tma) {
-        const uint64_t dC[2] = {(uint64_t)N, (uint64_t)M}, sC[1] = {(uint64_t)N * ce};
-        const uint32_t bC[2] = {(uint32_t)(128 / ce), 32};
-        if (!encode_tensor_map(&L.tmC, cd, 2, C, dC, sC, bC, true)) return MMACT_ERR_CUDA;
+    L.bt = bt;
+    L.grid = (int)(tiles * split);
+    L.x_type = -1;
+    plan.quantize = x != nullptr && M > F8_FUSED_ROWS;
+    if (!f8_encode(&L.tmW, &L.tmSW, B, N, K, 128, 1)) return MMACT_ERR_CUDA;
+    if (x != nullptr && !plan.quantize) {
+        a.x = x;
+        L.x_type = out_kind(x_type);
+        return MMACT_OK;
     }
-    return MMACT_OK;
+    return f8_encode(&L.tmT, &L.tmST, A, M, K, (uint32_t)bt, 1) ? MMACT_OK : MMACT_ERR_CUDA;
+}
+
+cudaError_t f8_gemm_launch(const F8Plan &plan, cudaStream_t stream)
+{
+    return plan.pair ? launch_gemm_fp8_pair(plan.P, stream) : launch_gemm_fp8_rows(plan.R, stream);
 }
 
 cudaError_t quantize_launch(const void *x, const F8Matrix &m, int64_t rows, int64_t K, mmact_dtype xd, bool square,
@@ -219,9 +299,16 @@ MMACT_EXPORT mmact_status mmact_gemm_fp8(const void *a_codes, const void *a_scal
     if (M == 0 || N == 0) return MMACT_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
-    F8GemmLaunch L;
+    F8Plan L;
     s = f8_gemm_plan(L, A, B, bias, C, M, N, K, c_dtype, act, alpha);
-    return s == MMACT_OK ? enqueued(launch_gemm_fp8_pair(L, st)) : s;
+    return s == MMACT_OK ? enqueued(f8_gemm_launch(L, st)) : s;
+}
+
+MMACT_EXPORT mmact_status mmact_set_gemm_fp8_kernel(int mode)
+{
+    if (mode < 0 || mode > 2) return MMACT_ERR_INVALID_ARG;
+    g_f8_kernel.store(mode);
+    return MMACT_OK;
 }
 
 MMACT_EXPORT mmact_status mmact_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t *bytes)
@@ -246,10 +333,10 @@ MMACT_EXPORT mmact_status mmact_linear_fp8(const void *x, const void *w_codes, c
     if (M == 0 || N == 0) return MMACT_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
-    F8GemmLaunch L;
-    if ((s = f8_gemm_plan(L, A, W, bias, C, M, N, K, c_dtype, act, alpha)) != MMACT_OK) return s;
-    if ((s = enqueued(quantize_launch(x, A, M, K, x_dtype, false, false, st))) != MMACT_OK) return s;
-    return enqueued(launch_gemm_fp8_pair(L, st));
+    F8Plan L;
+    if ((s = f8_gemm_plan(L, A, W, bias, C, M, N, K, c_dtype, act, alpha, x, x_dtype)) != MMACT_OK) return s;
+    if (L.quantize && (s = enqueued(quantize_launch(x, A, M, K, x_dtype, false, false, st))) != MMACT_OK) return s;
+    return enqueued(f8_gemm_launch(L, st));
 }
 
 MMACT_EXPORT mmact_status mmact_linear_fp8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t *bytes)
@@ -290,19 +377,19 @@ MMACT_EXPORT mmact_status mmact_linear_fp8_backward(const void *dy, const void *
     Parts ws{static_cast<char *>(workspace)};
     const F8Matrix gy = ws.matrix(M, N, grad_dtype), gyt = ws.matrix(N, M, grad_dtype), xt = ws.matrix(K, M, MMACT_E4M3);
     float *part = static_cast<float *>(ws.take(0));
-    F8GemmLaunch X, W;
+    F8Plan X, W;
     if (want_dx && (s = f8_gemm_plan(X, gy, F8Matrix{wt_codes, wt_scales, wt_dtype}, nullptr, dx, M, K, N, x_dtype,
                                      MMACT_ACT_NONE, 0.0f)) != MMACT_OK)
         return s;
     if (want_dw && (s = f8_gemm_plan(W, gyt, xt, nullptr, dw, N, K, M, dw_dtype, MMACT_ACT_NONE, 0.0f)) != MMACT_OK) return s;
     if (want_dx) {
         if ((s = enqueued(quantize_launch(dy, gy, M, N, x_dtype, false, false, st))) != MMACT_OK) return s;
-        if ((s = enqueued(launch_gemm_fp8_pair(X, st))) != MMACT_OK) return s;
+        if ((s = enqueued(f8_gemm_launch(X, st))) != MMACT_OK) return s;
     }
     if (want_dw) {
         if ((s = enqueued(quantize_launch(dy, gyt, N, M, x_dtype, false, true, st))) != MMACT_OK) return s;
         if ((s = enqueued(quantize_launch(x, xt, K, M, x_dtype, false, true, st))) != MMACT_OK) return s;
-        if ((s = enqueued(launch_gemm_fp8_pair(W, st))) != MMACT_OK) return s;
+        if ((s = enqueued(f8_gemm_launch(W, st))) != MMACT_OK) return s;
     }
     return want_db ? enqueued(launch_column_sums(dy, out_kind(x_dtype), part, db, M, N, st)) : MMACT_OK;
 }

@@ -44,4 +44,35 @@ struct F8GemmLaunch {
 cudaError_t setup_fp8_pair_kernels(int *max_pairs);   // max_pairs: CTA pairs resident at once
 cudaError_t launch_gemm_fp8_pair(const F8GemmLaunch &L, cudaStream_t stream);
 
+// The same product with few rows or tiles: W = B's rows on the MMA's 128 lanes,
+// T = A's rows on its columns, the K blocks of a tile shared by a cluster.
+struct F8RowsArgs {
+    int M, N, K;
+    const void *x;       // A not yet quantised [M, K], or null
+    int nk32, num_kb;    // as above
+    int tiles_n;         // tiles of 128 rows of B
+    int split, kb_per;   // CTAs of a tile's cluster, K blocks of each
+    int stages;          // of the ring
+    int act;
+    float alpha;
+    const float *bias;
+    void *C;
+    uint32_t idesc;      // operand formats, 128 x bt
+    unsigned int *status;
+    unsigned long long wait_ns;
+};
+
+struct F8RowsLaunch {
+    CUtensorMap tmW, tmT, tmSW, tmST;
+    F8RowsArgs args;
+    int out;
+    int bt;              // rows of A in a tile: 16, 32, 64 or 128
+    int x_type;          // OUT_* of args.x; < 0: A is tmT, tmST
+    int grid;
+};
+
+// max_clusters[i]: clusters of 2^i CTAs resident at once, one CTA to an SM
+cudaError_t setup_fp8_rows_kernels(int (&max_clusters)[4]);
+cudaError_t launch_gemm_fp8_rows(const F8RowsLaunch &L, cudaStream_t stream);
+
 }  // namespace mmact

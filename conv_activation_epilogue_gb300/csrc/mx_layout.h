@@ -52,6 +52,31 @@ struct MxRowsCfg {
     static_assert(BT + 16 * MAX_STAGES <= TMEM_COLS, "tensor memory budget");
 };
 
+// -------------------------------- products of few rows or tiles, 8-bit operands --
+constexpr int F8_ROWS_STAGES(int bt) { return bt <= 32 ? 5 : (bt == 64 ? 8 : 6); }   // at most
+
+// The same with ring stages of 128 K: the weights' and the tokens' scale tile are 512
+// bytes each, 8 columns of tensor memory.
+template <int BT>
+struct F8RowsCfg {
+    static constexpr int W_BYTES = 128 * 128, T_BYTES = BT * 128, S_BYTES = 1024;
+    static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + S_BYTES;
+    static constexpr int MAX_STAGES = F8_ROWS_STAGES(BT);
+    static constexpr uint32_t SCALE_COL = BT;
+    static constexpr uint32_t TMEM_COLS = BT + 8 * MAX_STAGES <= 128 ? 128 : 256;
+    static constexpr int OFF_BAR = 0, OFF_MISC = (2 * MAX_STAGES + 2) * 8, OFF_RING = 1024;
+    static constexpr int PART_BYTES = BT * 512;                          // a partial tile, over the ring
+    static constexpr int MIN_SMEM = tmem_min_smem((int)TMEM_COLS);
+    static constexpr int smem_bytes(int stages, int split)
+    {
+        const int ring = OFF_RING + stages * STAGE_BYTES, part = split > 1 ? OFF_RING + PART_BYTES : 0;
+        const int need = ring > part ? ring : part;
+        return need > MIN_SMEM ? need : MIN_SMEM;
+    }
+    static_assert(OFF_MISC + 16 <= OFF_RING && OFF_RING + MAX_STAGES * STAGE_BYTES <= CTA_SMEM, "shared memory budget");
+    static_assert(BT + 8 * MAX_STAGES <= TMEM_COLS, "tensor memory budget");
+};
+
 // ----------------------------------------------------------- mixture of experts --
 constexpr int MOE_MAX_T = 64, MOE_MAX_K = 16, MOE_MAX_E = 512;
 constexpr int MOE_MIN_GROUP = 16;                              // tokens of an expert that share a read of its weights, at least

@@ -43,6 +43,7 @@ SYMBOLS = [
     "mmact_set_gemm_mxfp4_kernel",
     "mmact_fp8_size", "mmact_quantize_fp8", "mmact_dequantize_fp8", "mmact_gemm_fp8", "mmact_linear_fp8",
     "mmact_linear_fp8_workspace_bytes", "mmact_linear_fp8_backward", "mmact_linear_fp8_backward_workspace_bytes",
+    "mmact_set_gemm_fp8_kernel",
     "mmact_moe_route", "mmact_moe_route_workspace_bytes", "mmact_moe_route_backward",
 ]
 
@@ -132,7 +133,8 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     L.mmact_moe_route.argtypes = [vp] * 6 + [i64, i64, i64, ci, ci, f32, vp, vp]
     L.mmact_moe_route_workspace_bytes.argtypes = [i64, i64, p_i64]
     L.mmact_moe_route_backward.argtypes = [vp] * 7 + [i64, i64, i64, ci, ci, f32, vp]
-    for name in ("mmact_moe_route", "mmact_moe_route_workspace_bytes", "mmact_moe_route_backward",
+    L.mmact_set_gemm_fp8_kernel.argtypes = [ci]
+    for name in ("mmact_set_gemm_fp8_kernel", "mmact_moe_route", "mmact_moe_route_workspace_bytes", "mmact_moe_route_backward",
                  "mmact_fp8_size", "mmact_quantize_fp8", "mmact_dequantize_fp8", "mmact_gemm_fp8", "mmact_linear_fp8",
                  "mmact_linear_fp8_workspace_bytes", "mmact_linear_fp8_backward",
                  "mmact_linear_fp8_backward_workspace_bytes"):
@@ -579,12 +581,12 @@ def _fp8_ptrs(codes, scales, rows: int, K: int, name: str):
 
 def _here(first, *rest) -> None:
     """The tensors of a call lie on one device, the current one: its stream gets the kernels."""
-    dev = first.device
-    if dev.index != (_CUR_DEVICE() if _CUR_DEVICE is not None else torch.cuda.current_device()):
-        raise ValueError(f"tensors on {dev}, which is not the current device")
+    dev = first.get_device()
+    if dev != (_CUR_DEVICE() if _CUR_DEVICE is not None else torch.cuda.current_device()):
+        raise ValueError(f"tensors on device {dev}, which is not the current one")
     for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and on {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on devices {dev} and {t.get_device()}")
 
 
 def mmact_quantize_fp8(x, codes, scales, block_rows: int = 1, transposed: bool = False, stream=None) -> None:
@@ -626,6 +628,11 @@ def mmact_gemm_fp8(a_codes, a_scales, b_codes, b_scales, bias, C, K: int, act: s
                                         _stream_handle(stream))
     if s:
         _check(s, "mmact_gemm_fp8")
+
+
+def mmact_set_gemm_fp8_kernel(mode: int) -> None:
+    """8-bit products: 0 kernel chosen per shape; 1 few rows or tiles; 2 CTA pairs."""
+    _check(load().mmact_set_gemm_fp8_kernel(int(mode)), "mmact_set_gemm_fp8_kernel")
 
 
 def mmact_linear_fp8_workspace_bytes(M: int, K: int) -> int:

@@ -636,10 +636,19 @@ mmact_status mmact_gemm_fp8(const void *a_codes, const void *a_scales, const voi
                             mmact_dtype b_dtype, mmact_dtype c_dtype, mmact_act act, float alpha, void *stream);
 
 /*
+ * Tuning and testing aid: the kernel of mmact_gemm_fp8, mmact_linear_fp8 and
+ * mmact_linear_fp8_backward.  mode: 0 = chosen per shape (the default), 1 = the kernel
+ * for few rows or tiles (128 rows of B by 16 to 128 rows of A, K shared by clusters), 2 =
+ * the kernel for large outputs (256 x 256 tiles on CTA pairs).  Applies to later calls
+ * in the process.  Returns MMACT_ERR_INVALID_ARG for other values.
+ */
+mmact_status mmact_set_gemm_fp8_kernel(int mode);
+
+/*
  * C = act(q(x) x W^T + bias): x [M, K] row-major in x_dtype (F16, BF16 or F32)
  * is quantised to E4M3 (block_rows 1) on the way in, W [N, K] is held in 8 bits
  * (w_dtype).  The same result as mmact_quantize_fp8 into `workspace` and
- * mmact_gemm_fp8.
+ * mmact_gemm_fp8 (a few rows are quantised inside the product's kernel instead).
  *   workspace  at least mmact_linear_fp8_workspace_bytes, 16-byte aligned,
  *              contents ignored and undefined afterwards; calls that may
  *              overlap on the GPU need one each.

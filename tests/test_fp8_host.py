@@ -108,6 +108,13 @@ def test_backward_host_validation(lib):
     assert backward(lib, M=0, N=0, K=0) == OK
 
 
+def test_kernel_mode_validation(lib):
+    for bad in (-1, 3):
+        assert lib.mmact_set_gemm_fp8_kernel(bad) == E
+    for good in (1, 2, 0):
+        assert lib.mmact_set_gemm_fp8_kernel(good) == OK
+
+
 def test_cpu_tensors_are_refused(lib):
     x = torch.zeros((4, 64))
     codes = torch.zeros((4, 64), dtype=torch.uint8).view(torch.float8_e4m3fn)

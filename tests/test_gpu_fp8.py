@@ -136,6 +136,14 @@ def ref_half_step(v, dtype):
     return mx.ulp(v, dtype) / 2
 
 
+@pytest.fixture(params=[0, 1, 2], ids=["chosen", "rows", "pair"])
+def kernel(request):
+    """Each kernel for every shape: the shape's own choice is only about speed."""
+    mmact.mmact_set_gemm_fp8_kernel(request.param)
+    yield request.param
+    mmact.mmact_set_gemm_fp8_kernel(0)
+
+
 GEMMS = [(1, 1, 1), (1, 128, 32), (1, 136, 64), (2, 8, 96), (7, 129, 100), (16, 256, 256), (17, 100, 288), (33, 260, 511),
          (64, 640, 512), (65, 72, 1000), (128, 128, 128), (129, 127, 130), (200, 512, 2048), (256, 264, 768), (300, 1000, 320),
          (513, 520, 544), (640, 384, 4096)]
@@ -143,7 +151,7 @@ GEMMS = [(1, 1, 1), (1, 128, 32), (1, 136, 64), (2, 8, 96), (7, 129, 100), (16, 
 
 @pytest.mark.parametrize("M,N,K", GEMMS)
 @pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
-def test_gemm(M, N, K, out):
+def test_gemm(M, N, K, out, kernel):
     rng = np.random.default_rng(M * 7919 + N * 31 + K)
     (ac, as_, av), (bc, bs, bv) = random_f8(rng, M, K), random_f8(rng, N, K, K ** -0.5, "e4m3", True)
     bias = rng.normal(0, 1, N).astype(np.float32)
@@ -157,7 +165,7 @@ def test_gemm(M, N, K, out):
 @pytest.mark.parametrize("a", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("b", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("M,N,K", [(3, 200, 160), (130, 192, 300), (400, 300, 1100)])
-def test_gemm_formats(a, b, M, N, K):
+def test_gemm_formats(a, b, M, N, K, kernel):
     rng = np.random.default_rng(M + N + K)
     (ac, as_, av), (bc, bs, bv) = random_f8(rng, M, K, kind=a), random_f8(rng, N, K, K ** -0.5, b)
     C = torch.full((M, N), float("nan"), dtype=torch.float32, device="cuda")
@@ -168,7 +176,7 @@ def test_gemm_formats(a, b, M, N, K):
 
 @pytest.mark.parametrize("name", ["none", "relu", "leaky_relu", "tanh", "sigmoid", "gelu", "silu"])
 @pytest.mark.parametrize("M,N,K", [(3, 200, 160), (130, 192, 300), (260, 300, 256)])
-def test_gemm_activations(name, M, N, K):
+def test_gemm_activations(name, M, N, K, kernel):
     rng = np.random.default_rng(M + N + K)
     (ac, as_, av), (bc, bs, bv) = random_f8(rng, M, K), random_f8(rng, N, K, K ** -0.5)
     for out, bias in (("f32", None), ("bf16", rng.normal(0, 1, N).astype(np.float32))):
@@ -179,7 +187,7 @@ def test_gemm_activations(name, M, N, K):
 
 
 @pytest.mark.parametrize("M", [700, 40])
-def test_gemm_against_its_own_scales(M):
+def test_gemm_against_its_own_scales(M, kernel):
     """A one-hot A picks single values of B through every block and row: each scale byte and code
     has to be the one of its own row, block and place (exact)."""
     rng = np.random.default_rng(5)
@@ -194,7 +202,7 @@ def test_gemm_against_its_own_scales(M):
 
 
 @pytest.mark.parametrize("M", [2, 140, 300])
-def test_gemm_nan_scales_reach_their_row_or_column_only(M):
+def test_gemm_nan_scales_reach_their_row_or_column_only(M, kernel):
     rng = np.random.default_rng(6)
     N, K = 200, 640
     (ac, as_, av), (bc, bs, bv) = random_f8(rng, M, K), random_f8(rng, N, K)
@@ -228,7 +236,7 @@ LINEARS = [(1, 512, 1024), (1, 333, 100), (5, 72, 640), (8, 1000, 4096), (9, 264
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("M,N,K", LINEARS)
-def test_linear_is_quantise_and_gemm(dtype, M, N, K):
+def test_linear_is_quantise_and_gemm(dtype, M, N, K, kernel):
     rng = np.random.default_rng(M + K)
     x = tensor(rng.normal(0, 1, (M, K)) * np.exp2(rng.integers(-4, 5, (M, 1))), dtype)
     wc, ws, wv = random_f8(rng, N, K, K ** -0.5, "e5m2" if N % 2 else "e4m3", True)
@@ -292,7 +300,7 @@ def values64(codes, scales, rows, K):
 
 @pytest.mark.parametrize("M,N,K", [(1, 520, 8192), (16, 136, 4100), (100, 400, 2500), (1536, 1280, 640), (2816, 2560, 96),
                                    (130, 8200, 1030), (5000, 40, 2048)])
-def test_gemm_many_k_blocks_and_many_tiles(M, N, K):
+def test_gemm_many_k_blocks_and_many_tiles(M, N, K, kernel):
     """Rings that go round, several tiles for each CTA pair."""
     g = torch.Generator(device="cuda").manual_seed(M + K)
     a, b = (torch.empty((r, K), device="cuda").normal_(0, 1, generator=g) for r in (M, N))
