@@ -265,3 +265,14 @@ def test_refusals():
         mmact.mmact_moe_route(z, nine, nine.float(), counts, loss, work)
     assert ei.value.status == mmact.MMACT_ERR_UNSUPPORTED
     assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+
+
+@pytest.mark.parametrize("T,E,top", [(70, 64, 8), (33, 256, 8), (20, 512, 16), (50, 30, 3)])
+def test_equal_logits_everywhere(T, E, top):
+    """A router whose weights are zeros: the first experts are chosen, by every token."""
+    z = torch.zeros((T, E), device="cuda").bfloat16()
+    z[1::2] = -0.0
+    z[5] = 1.0
+    z[7, E // 2:] = 1.0                                        # half of them
+    check_forward(z, host64(z), top, 1.0, True)
+    check_forward(z, host64(z), top, 1.0, False)
