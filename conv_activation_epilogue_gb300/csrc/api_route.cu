@@ -1,6 +1,7 @@
 // api_route.cu -- the C ABI of the router in training (include/mmact.h): argument
 // validation and launches.  As in api.cu, every check happens on the host before
 // anything is enqueued.
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 
@@ -39,7 +40,8 @@ MMACT_EXPORT mmact_status mmact_moe_route_workspace_bytes(int64_t T, int64_t E, 
     if (bytes == nullptr) return MMACT_ERR_INVALID_ARG;
     const mmact_status s = route_sizes(T, E, 1);
     if (s != MMACT_OK) return s;
-    const int64_t grid = route_grid(T, E, ROUTE_MAX_SMS);
+    // more lanes to a token are more CTAs
+    const int64_t grid = std::max(route_grid(T, E, 1, ROUTE_MAX_SMS), route_grid(T, E, ROUTE_MAX_TOP, ROUTE_MAX_SMS));
     *bytes = route_part_bytes(grid, E) + grid * (E + 1) * 4;
     return MMACT_OK;
 }
@@ -58,7 +60,7 @@ MMACT_EXPORT mmact_status mmact_moe_route(const void *logits, const uint8_t *mas
     if (!aligned16(logits) || !aligned16(workspace)) return MMACT_ERR_UNSUPPORTED;
     DeviceContext dev;
     if ((s = device_context(&dev)) != MMACT_OK) return s;
-    const int grid = route_grid(T, E, dev.sm_count < ROUTE_MAX_SMS ? dev.sm_count : ROUTE_MAX_SMS);
+    const int grid = route_grid(T, E, top, dev.sm_count < ROUTE_MAX_SMS ? dev.sm_count : ROUTE_MAX_SMS);
     RouteArgs a;
     a.T = T;
     a.E = (int)E;

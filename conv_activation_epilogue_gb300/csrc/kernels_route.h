@@ -35,7 +35,7 @@ struct RouteBackwardArgs {
     void *dlogits;               // [T, E]
 };
 
-int route_grid(int64_t T, int64_t E, int sms);        // CTAs of either pass
+int route_grid(int64_t T, int64_t E, int64_t top, int sms);        // CTAs of the forward pass
 cudaError_t launch_moe_route(const RouteArgs &a, int type, int grid, cudaStream_t s);
 cudaError_t launch_moe_route_backward(const RouteBackwardArgs &a, int type, int sms, cudaStream_t s);
 

@@ -2,15 +2,15 @@
 // probabilities, slots of each expert and balance loss from the logits, and the
 // gradient of the logits.
 //
-// G lanes take a token (8 to 32; 32 / G tokens to a warp), each NV consecutive logits, in
-// registers.  A logit becomes an unsigned key of the same order.  The choice: the top-th
-// largest of the lanes' largest keys bounds the choice from below, so that few keys
-// besides the chosen ones reach it; those go to a list in shared memory, and each one's
-// rank in it (by key, then index) is its slot.  Where the list would be long (many equal
-// keys), the warp picks the largest key `top` times.  (Picking alone, a
-// warp to a token, 131072 x 256 fp32 logits with 8 to choose took 183 us.)  The softmax
-// is taken in the same registers, and each lane adds up its own columns over all its
-// tokens; groups, warps and CTAs are added up in their order, so results repeat bit for bit.
+// G lanes take a token (8 to 32; 32 / G tokens to a warp), NV logits each, in registers.
+// The choice: the top-th largest of the lanes' largest logits bounds it from below, so
+// that few logits besides the chosen ones reach it; those go to a list in shared
+// memory, and each one's rank in it (by value, then index) is its slot.  Where the list
+// would be long (many equal logits) or there are NaN, the warp picks the largest of
+// them `top` times.  (Picking alone, a warp to a token, 131072 x 256 fp32 logits with 8
+// to choose took 183 us.)  The softmax is taken in the same registers, and each lane
+// adds up its own columns over all its tokens; groups, warps and CTAs are added up in
+// their order, so results repeat bit for bit.
 #include "common.cuh"
 #include "kernels_route.h"
 #include "mxfp4.cuh"
@@ -20,28 +20,39 @@ namespace mmact {
 
 constexpr int ROUTE_WARPS = 8;
 
-// NV logits of a row from column c on; columns past E are -inf.  VEC: rows begin on
-// 16-byte boundaries (or NV values are fewer bytes, and rows begin on those).
-template <int T, int NV, bool VEC>
-__device__ __forceinline__ void route_load(const void *p, int64_t row, int E, int c, float (&z)[NV])
+// Column of a lane's j-th logit.  VEC (rows begin on 16-byte boundaries, or on those of NV
+// values where these are fewer bytes): NV consecutive ones; else every G-th, so that
+// single values are loaded and stored side by side.
+template <int G, int NV, bool VEC>
+__device__ __forceinline__ int route_col(int l, int j)
 {
-    constexpr int ES = T == IN_F32 ? 4 : 2, BYTES = NV * ES < 16 ? NV * ES : 16, PER = BYTES / ES;
-    const char *at = static_cast<const char *>(p) + (row * E + c) * ES;
+    return VEC ? l * NV + j : j * G + l;
+}
+
+template <int T, int NV>
+constexpr int ROUTE_BYTES = NV * (T == IN_F32 ? 4 : 2) < 16 ? NV * (T == IN_F32 ? 4 : 2) : 16;   // of a vector access
+
+// A lane's logits of a row; columns past E are -inf.
+template <int T, int G, int NV, bool VEC>
+__device__ __forceinline__ void route_load(const void *p, int64_t row, int E, int l, float (&z)[NV])
+{
+    constexpr int ES = T == IN_F32 ? 4 : 2, BYTES = ROUTE_BYTES<T, NV>, PER = BYTES / ES;
+    const char *at = static_cast<const char *>(p) + row * E * ES;
+    if constexpr (VEC) {
+        static_assert(BYTES >= 8, "two words at least");
 #pragma unroll
-    for (int g = 0; g < NV / PER; ++g) {
-        if constexpr (VEC && BYTES >= 4) {
+        for (int g = 0; g < NV / PER; ++g) {
+            const int c = l * NV + g * PER;
             uint32_t w[BYTES / 4];
 #pragma unroll
             for (int j = 0; j < BYTES / 4; ++j) w[j] = T == IN_F32 ? 0xff800000u : (T == IN_BF16 ? 0xff80ff80u : 0xfc00fc00u);
-            if (c + g * PER < E) {
+            if (c < E) {
                 if constexpr (BYTES == 16) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(at + g * 16);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(at + c * ES);
                     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-                } else if constexpr (BYTES == 8) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(at);
-                    w[0] = u.x, w[1] = u.y;
                 } else {
-                    w[0] = *reinterpret_cast<const uint32_t *>(at);
+                    const uint2 u = *reinterpret_cast<const uint2 *>(at + c * ES);
+                    w[0] = u.x, w[1] = u.y;
                 }
             }
 #pragma unroll
@@ -53,16 +64,16 @@ __device__ __forceinline__ void route_load(const void *p, int64_t row, int E, in
                     z[g * PER + 2 * j] = f.x, z[g * PER + 2 * j + 1] = f.y;
                 }
             }
-        } else {
+        }
+    } else {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const int i = g * PER + j;
-                z[i] = -INFINITY;
-                if (c + i < E) {
-                    if constexpr (T == IN_F32) z[i] = reinterpret_cast<const float *>(at)[i];
-                    else if constexpr (T == IN_BF16) z[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(at)[i]);
-                    else z[i] = __half2float(reinterpret_cast<const __half *>(at)[i]);
-                }
+        for (int j = 0; j < NV; ++j) {
+            const int c = route_col<G, NV, VEC>(l, j);
+            z[j] = -INFINITY;
+            if (c < E) {
+                if constexpr (T == IN_F32) z[j] = reinterpret_cast<const float *>(at)[c];
+                else if constexpr (T == IN_BF16) z[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(at)[c]);
+                else z[j] = __half2float(reinterpret_cast<const __half *>(at)[c]);
             }
         }
     }
@@ -110,16 +121,65 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v)
     }
 }
 
-constexpr int ROUTE_LIST = 64;             // keys of a token that are ranked, at most
+// max that a NaN wins
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
-// A token's choice in shared memory.
+template <int G>
+__device__ __forceinline__ float group_max_nan(float v)
+{
+    if constexpr (G == 32) {
+        float r;
+        asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+        return r;
+    } else {
+#pragma unroll
+        for (int d = G / 2; d > 0; d >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
+        return v;
+    }
+}
+
+constexpr int ROUTE_LIST = 64;             // logits of a token that are ranked, at most
+constexpr float ROUTE_LOWEST = -3.402823466e38f;               // the lowest logit but -inf
+
+// A token's choice in shared memory: logits (their bits) and indices.
 struct RouteSlots {
-    uint2 list[ROUTE_LIST];                // key, index
+    uint2 list[ROUTE_LIST];
     uint2 slot[ROUTE_MAX_TOP];
 };
 
+// The choice by picking, for every token of a warp: G lanes, `top` times the largest
+// logit, of equal ones that of the lowest column.
+template <int G, int NV, bool VEC>
+__device__ __noinline__ void route_pick(const float *z, RouteSlots &my, int l, int top)
+{
+    uint32_t key[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) key[j] = route_key(z[j]);
+    for (int k = 0; k < top; ++k) {
+        uint32_t best = 0, col = 0xffffffffu;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (key[j] > best) best = key[j], col = (uint32_t)route_col<G, NV, VEC>(l, j);   // columns rise with j
+        const uint32_t m = group_max<G>(best);
+        if (m == 0u || best != m) col = 0xffffffffu;
+        const uint32_t at = ~group_max<G>(~col);
+        if (at != 0xffffffffu && at == col) {
+            my.slot[k] = make_uint2(__float_as_uint(route_value(m)), at);
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (route_col<G, NV, VEC>(l, j) == (int)at) key[j] = 0;
+        }
+    }
+    __syncwarp();
+}
+
 template <int T, int G, int NV, bool VEC>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS, 3) route_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 3) route_kernel(const RouteArgs a)
 {
     ptx::griddep_launch_dependents();
     constexpr int PER = 32 / G, GROUPS = ROUTE_WARPS * PER;
@@ -128,8 +188,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, 3) route_kernel(const RouteA
         float sums[GROUPS][G * NV];
     } sh;
     __shared__ int slots[ROUTE_MAX_EXPERTS + 1];
-    const int lane = threadIdx.x & 31, l = lane % G, c = l * NV, E = a.E, top = a.top, group = threadIdx.x / G;
-    const uint32_t mates = G == 32 ? 0xffffffffu : ((1u << (G % 32)) - 1u) << (lane - l);
+    const int lane = threadIdx.x & 31, l = lane % G, E = a.E, top = a.top, group = threadIdx.x / G;
     RouteSlots &my = sh.s[group];
     for (int i = threadIdx.x; i <= E; i += blockDim.x) slots[i] = 0;
     __syncthreads();
@@ -138,42 +197,33 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, 3) route_kernel(const RouteA
 #pragma unroll
     for (int j = 0; j < NV; ++j) acc[j] = 0.0f;
     int tokens = 0;
-    const int64_t step = (int64_t)gridDim.x * GROUPS, last = a.T - 1;
-    // the same number of rounds for every group of a warp; the last token again where there is none left
-    const int64_t first = (int64_t)blockIdx.x * GROUPS + group, warp0 = first - lane / G;
-    route_load<T, NV, VEC>(a.logits, min(first, last), E, c, next);
-    for (int64_t t0 = 0; warp0 + t0 < a.T; t0 += step) {
-        const int64_t t = first + t0;
-        float z[NV];
+    // rounds in which the warp has a token; the last one again where a group has none
+    const int64_t step = (int64_t)gridDim.x * GROUPS, last = a.T - 1, first = (int64_t)blockIdx.x * GROUPS + group;
+    const int64_t warp0 = first - lane / G;
+    const int rounds = warp0 < a.T ? (int)((a.T - warp0 + step - 1) / step) : 0;
+    if (rounds > 0) route_load<T, G, NV, VEC>(a.logits, min(first, last), E, l, next);
+    int64_t t = first;
+    for (int round = 0; round < rounds; ++round, t += step) {
+        float z[NV], best = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NV; ++j) z[j] = next[j];
-        if (warp0 + t0 + step < a.T) route_load<T, NV, VEC>(a.logits, min(t + step, last), E, c, next);
-        const bool on = t < a.T && (a.mask == nullptr || a.mask[t] != 0);
-        uint32_t key[NV], best = 0;
+        if (round + 1 < rounds) route_load<T, G, NV, VEC>(a.logits, min(t + step, last), E, l, next);
+        if (t >= a.T || (a.mask != nullptr && a.mask[t] == 0))
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            key[j] = on ? route_key(z[j]) : 0u;
-            best = max(best, key[j]);
+            for (int j = 0; j < NV; ++j) z[j] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) best = max_nan(best, z[j]);
+        const float peak = group_max_nan<G>(best);
+        // Lower bound of the choice: `top` times the largest of the lanes' largest logits, equal ones at once.
+        float bound = peak, rest = best;
+        for (int k = 1; k < top; ++k) {
+            if (rest == bound) rest = -INFINITY;
+            bound = group_max_nan<G>(rest);
         }
-        const uint32_t peak_key = group_max<G>(best);
-        // Lower bound of the choice: lanes' largest keys, equal ones at once, until there are `top`.
-        uint32_t bound = peak_key, rest = best;
-        {
-            int n = 0;
-            for (int k = 0; k < top; ++k) {
-                const uint32_t same = __ballot_sync(0xffffffffu, rest == bound) & mates;
-                if (n < top) n += __popc(same);
-                const bool more = n < top && bound != 0u;
-                if (!__any_sync(0xffffffffu, more)) break;
-                if (rest == bound) rest = 0u;
-                const uint32_t m = group_max<G>(rest);
-                if (more) bound = m;
-            }
-        }
-        bound = max(bound, 1u);                                // fewer lanes than slots: every key but -inf's
+        bound = max_nan(bound, ROUTE_LOWEST);                  // with fewer lanes than slots: all but -inf
         int mine = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) mine += key[j] >= bound ? 1 : 0;
+        for (int j = 0; j < NV; ++j) mine += z[j] >= bound ? 1 : 0;
         int at = mine;
 #pragma unroll
         for (int d = 1; d < G; d <<= 1) {
@@ -182,46 +232,36 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, 3) route_kernel(const RouteA
         }
         const int n = __shfl_sync(0xffffffffu, at, G - 1, G);
         for (int k = l; k < top; k += G) my.slot[k] = make_uint2(0u, 0xffffffffu);
-        if (__any_sync(0xffffffffu, n > ROUTE_LIST)) {
-            for (int k = 0; k < top; ++k) {
-                const uint32_t m = group_max<G>(best);
-                const uint32_t same = __ballot_sync(0xffffffffu, best == m) & mates;
-                __syncwarp();
-                if (m != 0u && lane == __ffs(same) - 1) {
-                    best = 0;
-                    bool taken = false;
-#pragma unroll
-                    for (int j = 0; j < NV; ++j) {
-                        if (!taken && key[j] == m) taken = true, my.slot[k] = make_uint2(m, (uint32_t)(c + j)), key[j] = 0;
-                        best = max(best, key[j]);
-                    }
-                }
-                __syncwarp();
-            }
+        if (__any_sync(0xffffffffu, n > ROUTE_LIST || peak != peak)) {
+            __syncwarp();
+            route_pick<G, NV, VEC>(z, my, l, top);
         } else {
             at -= mine;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                if (key[j] >= bound) my.list[at++] = make_uint2(key[j], (uint32_t)(c + j));
+                if (z[j] >= bound) my.list[at++] = make_uint2(__float_as_uint(z[j]), (uint32_t)route_col<G, NV, VEC>(l, j));
             __syncwarp();
             for (int i = l; i < n; i += G) {
                 const uint2 me = my.list[i];
+                const float v = __uint_as_float(me.x);
                 int rank = 0;
-                for (int j = 0; j < n; ++j) {                  // the list is in the order of the columns
-                    const uint32_t other = my.list[j].x;
-                    rank += other > me.x || (other == me.x && j < i) ? 1 : 0;
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) {
+                    const uint2 other = my.list[j];
+                    const float w = __uint_as_float(other.x);
+                    rank += w > v || (w == v && other.y < me.y) ? 1 : 0;
                 }
                 if (rank < top) my.slot[rank] = me;
             }
             __syncwarp();
         }
-        const float peak = route_value(peak_key);
-        float ex[NV], sum = 0.0f;
+        const bool some = peak != -INFINITY;
+        float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) ex[j] = peak_key != 0u ? route_exp(z[j] - peak) : 0.0f, sum += ex[j];
-        const float total = group_sum<G>(sum), inv = peak_key != 0u ? 1.0f / total : 0.0f;
+        for (int j = 0; j < NV; ++j) z[j] = some ? route_exp(z[j] - peak) : 0.0f, sum += z[j];
+        const float total = group_sum<G>(sum), inv = some ? __fdividef(1.0f, total) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) acc[j] += ex[j] * inv;
+        for (int j = 0; j < NV; ++j) acc[j] += z[j] * inv;
         constexpr int SL = (ROUTE_MAX_TOP + G - 1) / G;        // slots of a lane
         int expert[SL];
         float p[SL], chosen = 0.0f;
@@ -232,18 +272,18 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, 3) route_kernel(const RouteA
             if (k < top) {
                 const uint2 s = my.slot[k];
                 expert[i] = (int)s.y;
-                if (expert[i] >= 0) p[i] = route_exp(route_value(s.x) - peak);
+                if (expert[i] >= 0) p[i] = route_exp(__uint_as_float(s.x) - peak);
             }
             chosen += p[i];
         }
-        const float over = a.normalize ? group_sum<G>(chosen) : total;
-        if (l == 0 && peak_key != 0u) ++tokens;
+        const float over = a.normalize ? __fdividef(1.0f, group_sum<G>(chosen)) : inv;
+        if (l == 0 && some) ++tokens;
 #pragma unroll
         for (int i = 0; i < SL; ++i) {
             const int k = l + i * G;
             if (k < top && t < a.T) {
                 a.experts[t * top + k] = expert[i];
-                a.probs[t * top + k] = expert[i] >= 0 ? p[i] / over : 0.0f;
+                a.probs[t * top + k] = expert[i] >= 0 ? p[i] * over : 0.0f;
                 if (expert[i] >= 0) atomicAdd(&slots[expert[i]], 1);
             }
         }
@@ -252,7 +292,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, 3) route_kernel(const RouteA
     if (tokens != 0) atomicAdd(&slots[E], tokens);
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NV; ++j) sh.sums[group][c + j] = acc[j];
+    for (int j = 0; j < NV; ++j) sh.sums[group][route_col<G, NV, VEC>(l, j)] = acc[j];
     __syncthreads();
     for (int i = threadIdx.x; i <= E; i += blockDim.x) {
         if (i < E) {
@@ -324,54 +364,60 @@ __global__ void __launch_bounds__(ROUTE_FINISH_THREADS) route_finish_kernel(cons
     if (ctas > 1) ptx::cluster_sync();                         // no CTA leaves while its sums are read
 }
 
-// NV values from column c on to a row of dlogits, rounded to its type.
-template <int T, int NV, bool VEC>
-__device__ __forceinline__ void route_store(void *p, int64_t row, int E, int c, const float (&v)[NV])
+// A lane's values to a row of dlogits, rounded to its type.
+template <int T, int G, int NV, bool VEC>
+__device__ __forceinline__ void route_store(void *p, int64_t row, int E, int l, const float (&v)[NV])
 {
-    constexpr int ES = T == IN_F32 ? 4 : 2, BYTES = NV * ES < 16 ? NV * ES : 16, PER = BYTES / ES;
-    const int64_t i0 = row * E + c;
-    char *at = static_cast<char *>(p) + i0 * ES;
+    constexpr int ES = T == IN_F32 ? 4 : 2, BYTES = ROUTE_BYTES<T, NV>, PER = BYTES / ES;
+    char *at = static_cast<char *>(p) + row * E * ES;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int g = 0; g < NV / PER; ++g) {
-        if constexpr (VEC && BYTES >= 4) {
-            if (c + g * PER >= E) continue;
+        for (int g = 0; g < NV / PER; ++g) {
+            const int c = l * NV + g * PER;
+            if (c >= E) continue;
             uint32_t w[BYTES / 4];
 #pragma unroll
             for (int j = 0; j < BYTES / 4; ++j) {
                 if constexpr (T == IN_F32) w[j] = __float_as_uint(v[g * PER + j]);
                 else w[j] = pack2<T>(v[g * PER + 2 * j], v[g * PER + 2 * j + 1]);
             }
-            if constexpr (BYTES == 16) *reinterpret_cast<uint4 *>(at + g * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            else if constexpr (BYTES == 8) *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t *>(at) = w[0];
-        } else {
+            if constexpr (BYTES == 16) *reinterpret_cast<uint4 *>(at + c * ES) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2 *>(at + c * ES) = make_uint2(w[0], w[1]);
+        }
+    } else {
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (c + g * PER + j < E) store1<T>(p, i0 + g * PER + j, v[g * PER + j]);
+        for (int j = 0; j < NV; ++j) {
+            const int c = route_col<G, NV, VEC>(l, j);
+            if (c < E) store1<T>(at, c, v[j]);
         }
     }
 }
 
 // dz = p (u - p.u) + the chosen probabilities' part, u = coef E / (n^2 top) dloss counts.
 template <int T, int G, int NV, bool VEC>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_backward_kernel(const RouteBackwardArgs a)
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 4) route_backward_kernel(const RouteBackwardArgs a)
 {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     constexpr int PER = 32 / G, GROUPS = ROUTE_WARPS * PER, SL = (ROUTE_MAX_TOP + G - 1) / G;
     // e^z of a token; what its slots add (zeros but while a token is worked on)
     __shared__ __align__(16) float row[GROUPS][G * NV], extra[GROUPS][G * NV];
-    const int lane = threadIdx.x & 31, l = lane % G, c = l * NV, E = a.E, top = a.top, group = threadIdx.x / G;
+    const int lane = threadIdx.x & 31, l = lane % G, E = a.E, top = a.top, group = threadIdx.x / G;
     float u[NV], next[NV], g_next[SL];
     int e_next[SL];
     {
         const float n = (float)a.counts[E];
         const float up = n > 0.0f ? a.coef * (float)E / n / (n * (float)top) * (a.dloss != nullptr ? a.dloss[0] : 0.0f) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) u[j] = c + j < E ? up * (float)a.counts[c + j] : 0.0f, extra[group][c + j] = 0.0f;
+        for (int j = 0; j < NV; ++j) {
+            const int c = route_col<G, NV, VEC>(l, j);
+            u[j] = c < E ? up * (float)a.counts[c] : 0.0f;
+            extra[group][c] = 0.0f;
+        }
     }
-    const int64_t step = (int64_t)gridDim.x * GROUPS, last = a.T - 1;
-    const int64_t first = (int64_t)blockIdx.x * GROUPS + group, warp0 = first - lane / G;
+    const int64_t step = (int64_t)gridDim.x * GROUPS, last = a.T - 1, first = (int64_t)blockIdx.x * GROUPS + group;
+    const int64_t warp0 = first - lane / G;
+    const int rounds = warp0 < a.T ? (int)((a.T - warp0 + step - 1) / step) : 0;
     auto slots = [&](int64_t t) {
 #pragma unroll
         for (int i = 0; i < SL; ++i) {
@@ -383,25 +429,26 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_backward_kernel(const 
             if (e >= 0 && e < E) e_next[i] = e;
         }
     };
-    route_load<T, NV, VEC>(a.logits, min(first, last), E, c, next);
-    slots(min(first, last));
-    for (int64_t t0 = 0; warp0 + t0 < a.T; t0 += step) {
-        const int64_t t = first + t0;
+    if (rounds > 0) {
+        route_load<T, G, NV, VEC>(a.logits, min(first, last), E, l, next);
+        slots(min(first, last));
+    }
+    int64_t t = first;
+    for (int round = 0; round < rounds; ++round, t += step) {
         float v[NV], g[SL], peak = -INFINITY, sum = 0.0f, dot = 0.0f;
         int e[SL];
 #pragma unroll
         for (int j = 0; j < NV; ++j) v[j] = next[j];
 #pragma unroll
         for (int i = 0; i < SL; ++i) e[i] = e_next[i], g[i] = g_next[i];
-        if (warp0 + t0 + step < a.T) {
-            route_load<T, NV, VEC>(a.logits, min(t + step, last), E, c, next);
+        if (round + 1 < rounds) {
+            route_load<T, G, NV, VEC>(a.logits, min(t + step, last), E, l, next);
             slots(min(t + step, last));
         }
         const bool masked = a.mask != nullptr && a.mask[min(t, last)] == 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(peak) : "f"(v[j]));
-#pragma unroll
-        for (int d = G / 2; d > 0; d >>= 1) asm("max.NaN.f32 %0, %0, %1;" : "+f"(peak) : "f"(__shfl_xor_sync(0xffffffffu, peak, d)));
+        for (int j = 0; j < NV; ++j) peak = max_nan(peak, v[j]);
+        peak = group_max_nan<G>(peak);
         const bool on = peak != -INFINITY && !masked;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -409,15 +456,16 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_backward_kernel(const 
             sum += v[j];
             dot += v[j] * u[j];
         }
-        if constexpr (NV % 4 == 0) {
+        if constexpr (VEC) {
 #pragma unroll
-            for (int j = 0; j < NV; j += 4) *reinterpret_cast<float4 *>(&row[group][c + j]) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            for (int j = 0; j < NV; j += 4)
+                *reinterpret_cast<float4 *>(&row[group][l * NV + j]) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         } else {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) row[group][c + j] = v[j];
+            for (int j = 0; j < NV; ++j) row[group][j * G + l] = v[j];
         }
         __syncwarp();
-        const float total = group_sum<G>(sum), inv = on ? 1.0f / total : 0.0f;
+        const float total = group_sum<G>(sum), inv = on ? __fdividef(1.0f, total) : 0.0f;
         dot = group_sum<G>(dot) * inv;
         float mine[SL], chosen = 0.0f, mg = 0.0f;
 #pragma unroll
@@ -427,7 +475,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_backward_kernel(const 
             mg += mine[i] * g[i];
         }
         const float over = a.normalize ? group_sum<G>(chosen) : total;
-        const float inv_over = over != 0.0f ? 1.0f / over : 0.0f;           // 0: a token without slots, or left out
+        const float inv_over = over != 0.0f ? __fdividef(1.0f, over) : 0.0f;           // 0: a token without slots, or left out
         mg = group_sum<G>(mg) * inv_over;
         const float off = a.normalize ? dot : dot + mg;
 #pragma unroll
@@ -447,41 +495,58 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_backward_kernel(const 
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) v[j] *= inv * (u[j] - off);
-        if constexpr (NV % 4 == 0) {
+        if constexpr (VEC) {
 #pragma unroll
             for (int j = 0; j < NV; j += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(&extra[group][c + j]);
+                const float4 x = *reinterpret_cast<const float4 *>(&extra[group][l * NV + j]);
                 v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) v[j] += extra[group][c + j];
+            for (int j = 0; j < NV; ++j) v[j] += extra[group][j * G + l];
         }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < SL; ++i)
             if (e[i] >= 0) extra[group][e[i]] = 0.0f;
-        if (t < a.T) route_store<T, NV, VEC>(a.dlogits, t, E, c, v);
+        if (t < a.T) route_store<T, G, NV, VEC>(a.dlogits, t, E, l, v);
         __syncwarp();
     }
 }
 
-// Lanes to a token and logits to a lane, by the number of experts: as few lanes as leave
-// registers for the logits (a warp takes 32 / G tokens at once, so that its reductions
-// and its ranking serve all of them).
-int route_lanes(int E) { return E <= 64 ? 8 : (E <= 128 ? 16 : 32); }
+// Lanes to a token and logits to a lane: as few lanes as leave registers for the logits (a
+// warp takes 32 / G tokens at once, so that its reductions and its ranking serve all of
+// them), but, for the choice, about twice as many lanes with logits as there are slots,
+// or the lanes' largest logits bound it badly.
+struct RouteShape {
+    int lanes, each;
+};
 
-int route_grid(int64_t T, int64_t E, int sms)
+static RouteShape route_shape(int E, int top)
 {
-    const int64_t groups = ROUTE_WARPS * 32 / route_lanes((int)E), ctas = (T + groups - 1) / groups;
-    return (int)(ctas < 3 * sms ? ctas : 3 * sms);
+    if (E <= 32) return {8, 4};
+    if (E <= 64) return top <= 4 ? RouteShape{8, 8} : RouteShape{16, 4};
+    if (E <= 128) return top <= 4 ? RouteShape{8, 16} : RouteShape{16, 8};
+    if (E <= 256) return top <= 8 ? RouteShape{16, 16} : RouteShape{32, 8};
+    return {32, 16};
+}
+
+static int route_ctas(int64_t T, RouteShape shape, int ctas_per_sm, int sms)
+{
+    const int64_t groups = ROUTE_WARPS * 32 / shape.lanes, ctas = (T + groups - 1) / groups;
+    return (int)(ctas < ctas_per_sm * sms ? ctas : ctas_per_sm * sms);
+}
+
+int route_grid(int64_t T, int64_t E, int64_t top, int sms)
+{
+    const RouteShape s = route_shape((int)E, (int)top);
+    return route_ctas(T, s, s.each > 8 ? 2 : 3, sms);
 }
 
 template <int T, int NV>
 static bool route_vec(int E)
 {
-    constexpr int BYTES = NV * (T == IN_F32 ? 4 : 2) < 16 ? NV * (T == IN_F32 ? 4 : 2) : 16;
-    return E * (T == IN_F32 ? 4 : 2) % BYTES == 0;
+    return E * (T == IN_F32 ? 4 : 2) % ROUTE_BYTES<T, NV> == 0;
 }
 
 template <int T, int G, int NV>
@@ -519,21 +584,28 @@ static cudaError_t route_backward_t(const RouteBackwardArgs &a, int grid, cudaSt
 template <int T>
 static cudaError_t route_e(const RouteArgs &a, int grid, cudaStream_t s)
 {
-    if (a.E <= 32) return route_t<T, 8, 4>(a, grid, s);
-    if (a.E <= 64) return route_t<T, 8, 8>(a, grid, s);
-    if (a.E <= 128) return route_t<T, 16, 8>(a, grid, s);
-    if (a.E <= 256) return route_t<T, 32, 8>(a, grid, s);
-    return route_t<T, 32, 16>(a, grid, s);
+    const RouteShape h = route_shape(a.E, a.top);
+    if (h.lanes == 8) {
+        if (h.each == 4) return route_t<T, 8, 4>(a, grid, s);
+        if (h.each == 8) return route_t<T, 8, 8>(a, grid, s);
+        return route_t<T, 8, 16>(a, grid, s);
+    }
+    if (h.lanes == 16) {
+        if (h.each == 4) return route_t<T, 16, 4>(a, grid, s);
+        if (h.each == 8) return route_t<T, 16, 8>(a, grid, s);
+        return route_t<T, 16, 16>(a, grid, s);
+    }
+    return h.each == 8 ? route_t<T, 32, 8>(a, grid, s) : route_t<T, 32, 16>(a, grid, s);
 }
 
 template <int T>
-static cudaError_t route_backward_e(const RouteBackwardArgs &a, int grid, cudaStream_t s)
+static cudaError_t route_backward_e(const RouteBackwardArgs &a, int sms, cudaStream_t s)
 {
-    if (a.E <= 32) return route_backward_t<T, 8, 4>(a, grid, s);
-    if (a.E <= 64) return route_backward_t<T, 8, 8>(a, grid, s);
-    if (a.E <= 128) return route_backward_t<T, 16, 8>(a, grid, s);
-    if (a.E <= 256) return route_backward_t<T, 32, 8>(a, grid, s);
-    return route_backward_t<T, 32, 16>(a, grid, s);
+    if (a.E <= 32) return route_backward_t<T, 8, 4>(a, route_ctas(a.T, {8, 4}, 4, sms), s);
+    if (a.E <= 64) return route_backward_t<T, 8, 8>(a, route_ctas(a.T, {8, 8}, 4, sms), s);
+    if (a.E <= 128) return route_backward_t<T, 16, 8>(a, route_ctas(a.T, {16, 8}, 4, sms), s);
+    if (a.E <= 256) return route_backward_t<T, 32, 8>(a, route_ctas(a.T, {32, 8}, 4, sms), s);
+    return route_backward_t<T, 32, 16>(a, route_ctas(a.T, {32, 16}, 2, sms), s);
 }
 
 cudaError_t launch_moe_route(const RouteArgs &a, int type, int grid, cudaStream_t s)
@@ -545,10 +617,9 @@ cudaError_t launch_moe_route(const RouteArgs &a, int type, int grid, cudaStream_
 
 cudaError_t launch_moe_route_backward(const RouteBackwardArgs &a, int type, int sms, cudaStream_t s)
 {
-    const int grid = route_grid(a.T, a.E, sms);
-    if (type == IN_BF16) return route_backward_e<IN_BF16>(a, grid, s);
-    if (type == IN_F16) return route_backward_e<IN_F16>(a, grid, s);
-    return route_backward_e<IN_F32>(a, grid, s);
+    if (type == IN_BF16) return route_backward_e<IN_BF16>(a, sms, s);
+    if (type == IN_F16) return route_backward_e<IN_F16>(a, sms, s);
+    return route_backward_e<IN_F32>(a, sms, s);
 }
 
 }  // namespace mmact
