@@ -25,9 +25,11 @@ mmact_status route_sizes(int64_t T, int64_t E, int64_t top)
     return MMACT_OK;
 }
 
-// Partial results of as many CTAs as a device of 512 SMs would get (a workspace's size
-// depends on T and E alone).
+// Partial results of as many CTAs as there can be: 8 tokens to a CTA at least (8 warps, a
+// whole one to a token at most), one for each SM of a device of 512 at most.  A
+// workspace's size depends on T and E alone.
 constexpr int ROUTE_MAX_SMS = 512;
+int64_t route_max_grid(int64_t T) { return std::min<int64_t>((T + 7) / 8, ROUTE_MAX_SMS); }
 int64_t route_part_bytes(int64_t grid, int64_t E) { return round_up(grid * E * 4, 256); }
 
 }  // namespace
@@ -40,8 +42,7 @@ MMACT_EXPORT mmact_status mmact_moe_route_workspace_bytes(int64_t T, int64_t E, 
     if (bytes == nullptr) return MMACT_ERR_INVALID_ARG;
     const mmact_status s = route_sizes(T, E, 1);
     if (s != MMACT_OK) return s;
-    // more lanes to a token are more CTAs
-    const int64_t grid = std::max(route_grid(T, E, 1, ROUTE_MAX_SMS), route_grid(T, E, ROUTE_MAX_TOP, ROUTE_MAX_SMS));
+    const int64_t grid = route_max_grid(T);
     *bytes = route_part_bytes(grid, E) + grid * (E + 1) * 4;
     return MMACT_OK;
 }
@@ -60,7 +61,7 @@ MMACT_EXPORT mmact_status mmact_moe_route(const void *logits, const uint8_t *mas
     if (!aligned16(logits) || !aligned16(workspace)) return MMACT_ERR_UNSUPPORTED;
     DeviceContext dev;
     if ((s = device_context(&dev)) != MMACT_OK) return s;
-    const int grid = route_grid(T, E, top, dev.sm_count < ROUTE_MAX_SMS ? dev.sm_count : ROUTE_MAX_SMS);
+    const int sms = std::min(dev.sm_count, ROUTE_MAX_SMS), grid = route_grid(T, E, top, sms);
     RouteArgs a;
     a.T = T;
     a.E = (int)E;
@@ -75,7 +76,7 @@ MMACT_EXPORT mmact_status mmact_moe_route(const void *logits, const uint8_t *mas
     a.loss = loss;
     a.part = static_cast<float *>(workspace);
     a.part_counts = reinterpret_cast<int *>(static_cast<char *>(workspace) + route_part_bytes(grid, E));
-    return enqueued(launch_moe_route(a, out_kind(logits_dtype), grid, static_cast<cudaStream_t>(stream)));
+    return enqueued(launch_moe_route(a, out_kind(logits_dtype), grid, sms, static_cast<cudaStream_t>(stream)));
 }
 
 MMACT_EXPORT mmact_status mmact_moe_route_backward(const void *logits, const uint8_t *mask, const int32_t *experts,

@@ -36,7 +36,7 @@ struct RouteBackwardArgs {
 };
 
 int route_grid(int64_t T, int64_t E, int64_t top, int sms);        // CTAs of the forward pass
-cudaError_t launch_moe_route(const RouteArgs &a, int type, int grid, cudaStream_t s);
+cudaError_t launch_moe_route(const RouteArgs &a, int type, int grid, int sms, cudaStream_t s);   // grid of route_grid
 cudaError_t launch_moe_route_backward(const RouteBackwardArgs &a, int type, int sms, cudaStream_t s);
 
 }  // namespace mmact

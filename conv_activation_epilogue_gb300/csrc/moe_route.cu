@@ -18,31 +18,39 @@
 
 namespace mmact {
 
-constexpr int ROUTE_WARPS = 8;
+constexpr int ROUTE_WARPS = 8;             // of a CTA of the backward pass
+// Of a CTA of the forward pass, one CTA to an SM: as many as have registers for NV logits,
+// the next token's and the sums, or 8 when that is one token for each group of lanes.  (Several smaller CTAs to an SM are as many partial sums
+// more for the last kernel: 131072 x 256 66.6 us with two of 8 warps, 62.9 with one of 16.)
+template <int NV>
+constexpr int ROUTE_FORWARD_WARPS = NV > 8 ? 16 : 24;
 
-// Column of a lane's j-th logit.  VEC (rows begin on 16-byte boundaries, or on those of NV
-// values where these are fewer bytes): NV consecutive ones; else every G-th, so that
-// single values are loaded and stored side by side.
-template <int G, int NV, bool VEC>
+
+// Values of an access: with VEC (rows begin on 16-byte boundaries, or on those of NV
+// values where these are fewer bytes) 16 bytes of them, else one.
+template <int T, int NV>
+constexpr int ROUTE_BYTES = NV * (T == IN_F32 ? 4 : 2) < 16 ? NV * (T == IN_F32 ? 4 : 2) : 16;
+template <int T, int NV, bool VEC>
+constexpr int ROUTE_PER = VEC ? ROUTE_BYTES<T, NV> / (T == IN_F32 ? 4 : 2) : 1;
+
+// Column of a lane's j-th logit, rising with j: the lanes' accesses lie side by side.
+template <int G, int PER>
 __device__ __forceinline__ int route_col(int l, int j)
 {
-    return VEC ? l * NV + j : j * G + l;
+    return (j / PER * G + l) * PER + j % PER;
 }
-
-template <int T, int NV>
-constexpr int ROUTE_BYTES = NV * (T == IN_F32 ? 4 : 2) < 16 ? NV * (T == IN_F32 ? 4 : 2) : 16;   // of a vector access
 
 // A lane's logits of a row; columns past E are -inf.
 template <int T, int G, int NV, bool VEC>
 __device__ __forceinline__ void route_load(const void *p, int64_t row, int E, int l, float (&z)[NV])
 {
-    constexpr int ES = T == IN_F32 ? 4 : 2, BYTES = ROUTE_BYTES<T, NV>, PER = BYTES / ES;
+    constexpr int ES = T == IN_F32 ? 4 : 2, BYTES = ROUTE_BYTES<T, NV>, PER = ROUTE_PER<T, NV, VEC>;
     const char *at = static_cast<const char *>(p) + row * E * ES;
     if constexpr (VEC) {
         static_assert(BYTES >= 8, "two words at least");
 #pragma unroll
         for (int g = 0; g < NV / PER; ++g) {
-            const int c = l * NV + g * PER;
+            const int c = route_col<G, PER>(l, g * PER);
             uint32_t w[BYTES / 4];
 #pragma unroll
             for (int j = 0; j < BYTES / 4; ++j) w[j] = T == IN_F32 ? 0xff800000u : (T == IN_BF16 ? 0xff80ff80u : 0xfc00fc00u);
@@ -68,7 +76,7 @@ __device__ __forceinline__ void route_load(const void *p, int64_t row, int E, in
     } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = route_col<G, NV, VEC>(l, j);
+            const int c = route_col<G, PER>(l, j);
             z[j] = -INFINITY;
             if (c < E) {
                 if constexpr (T == IN_F32) z[j] = reinterpret_cast<const float *>(at)[c];
@@ -143,19 +151,46 @@ __device__ __forceinline__ float group_max_nan(float v)
     }
 }
 
-constexpr int ROUTE_LIST = 64;             // logits of a token that are ranked, at most
+// Lower bound of the choice of `top`: the top-th largest of the lanes' largest logits
+// (`best`; equal ones may count once), -inf with fewer lanes than slots.  A warp's
+// reductions are one instruction each; in less than a warp all lanes compare themselves with all
+// others, by shuffles that do not wait for one another.
+template <int G>
+__device__ __forceinline__ float route_bound(float best, float peak, int top)
+{
+    if constexpr (G == 32) {
+        float bound = peak;
+        for (int k = 1; k < top; ++k) {
+            if (best == bound) best = -INFINITY;
+            bound = group_max_nan<G>(best);
+        }
+        return bound;
+    } else {
+        int above = 0;
+#pragma unroll
+        for (int d = 1; d < G; ++d) above += __shfl_xor_sync(0xffffffffu, best, d) > best ? 1 : 0;
+        float bound = above < top ? best : peak;
+#pragma unroll
+        for (int d = G / 2; d > 0; d >>= 1) bound = fminf(bound, __shfl_xor_sync(0xffffffffu, bound, d));
+        return top <= G ? bound : -INFINITY;
+    }
+}
+
+template <int G>
+constexpr int ROUTE_LIST = G == 32 ? 64 : 32;                  // logits of a token that are ranked, at most
 constexpr float ROUTE_LOWEST = -3.402823466e38f;               // the lowest logit but -inf
 
 // A token's choice in shared memory: logits (their bits) and indices.
+template <int G>
 struct RouteSlots {
-    uint2 list[ROUTE_LIST];
+    uint2 list[ROUTE_LIST<G>];
     uint2 slot[ROUTE_MAX_TOP];
 };
 
 // The choice by picking, for every token of a warp: G lanes, `top` times the largest
 // logit, of equal ones that of the lowest column.
-template <int G, int NV, bool VEC>
-__device__ __noinline__ void route_pick(const float *z, RouteSlots &my, int l, int top)
+template <int G, int NV, int PER>
+__device__ __noinline__ void route_pick(const float *z, RouteSlots<G> &my, int l, int top)
 {
     uint32_t key[NV];
 #pragma unroll
@@ -164,7 +199,7 @@ __device__ __noinline__ void route_pick(const float *z, RouteSlots &my, int l, i
         uint32_t best = 0, col = 0xffffffffu;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (key[j] > best) best = key[j], col = (uint32_t)route_col<G, NV, VEC>(l, j);   // columns rise with j
+            if (key[j] > best) best = key[j], col = (uint32_t)route_col<G, PER>(l, j);   // columns rise with j
         const uint32_t m = group_max<G>(best);
         if (m == 0u || best != m) col = 0xffffffffu;
         const uint32_t at = ~group_max<G>(~col);
@@ -172,24 +207,26 @@ __device__ __noinline__ void route_pick(const float *z, RouteSlots &my, int l, i
             my.slot[k] = make_uint2(__float_as_uint(route_value(m)), at);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                if (route_col<G, NV, VEC>(l, j) == (int)at) key[j] = 0;
+                if (route_col<G, PER>(l, j) == (int)at) key[j] = 0;
         }
     }
     __syncwarp();
 }
 
 template <int T, int G, int NV, bool VEC>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 3) route_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(32 * ROUTE_FORWARD_WARPS<NV>, 1) route_kernel(const RouteArgs a)
 {
     ptx::griddep_launch_dependents();
-    constexpr int PER = 32 / G, GROUPS = ROUTE_WARPS * PER;
+    constexpr int GROUPS = ROUTE_FORWARD_WARPS<NV> * 32 / G, PER = ROUTE_PER<T, NV, VEC>;
+    const int groups = blockDim.x / G;                         // GROUPS at most
     __shared__ union {
-        RouteSlots s[GROUPS];
+        RouteSlots<G> s[GROUPS];
         float sums[GROUPS][G * NV];
     } sh;
     __shared__ int slots[ROUTE_MAX_EXPERTS + 1];
     const int lane = threadIdx.x & 31, l = lane % G, E = a.E, top = a.top, group = threadIdx.x / G;
-    RouteSlots &my = sh.s[group];
+    const uint32_t mates = (G == 32 ? 0xffffffffu : (1u << (G % 32)) - 1u) << (lane - l), below = mates & ((1u << lane) - 1u);
+    RouteSlots<G> &my = sh.s[group];
     for (int i = threadIdx.x; i <= E; i += blockDim.x) slots[i] = 0;
     __syncthreads();
     ptx::griddep_wait();
@@ -198,7 +235,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 3) route_kernel
     for (int j = 0; j < NV; ++j) acc[j] = 0.0f;
     int tokens = 0;
     // rounds in which the warp has a token; the last one again where a group has none
-    const int64_t step = (int64_t)gridDim.x * GROUPS, last = a.T - 1, first = (int64_t)blockIdx.x * GROUPS + group;
+    const int64_t step = (int64_t)gridDim.x * groups, last = a.T - 1, first = (int64_t)blockIdx.x * groups + group;
     const int64_t warp0 = first - lane / G;
     const int rounds = warp0 < a.T ? (int)((a.T - warp0 + step - 1) / step) : 0;
     if (rounds > 0) route_load<T, G, NV, VEC>(a.logits, min(first, last), E, l, next);
@@ -214,32 +251,26 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 3) route_kernel
 #pragma unroll
         for (int j = 0; j < NV; ++j) best = max_nan(best, z[j]);
         const float peak = group_max_nan<G>(best);
-        // Lower bound of the choice: `top` times the largest of the lanes' largest logits, equal ones at once.
-        float bound = peak, rest = best;
-        for (int k = 1; k < top; ++k) {
-            if (rest == bound) rest = -INFINITY;
-            bound = group_max_nan<G>(rest);
-        }
-        bound = max_nan(bound, ROUTE_LOWEST);                  // with fewer lanes than slots: all but -inf
+        const float bound = max_nan(route_bound<G>(best, peak, top), ROUTE_LOWEST);
         int mine = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) mine += z[j] >= bound ? 1 : 0;
-        int at = mine;
+        // first place in the list of a lane's logits, from the counts' three low bits
+        int at = 0, n = 0;
 #pragma unroll
-        for (int d = 1; d < G; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, at, d, G);
-            if (l >= d) at += v;
+        for (int b = 0; b < 3; ++b) {
+            const uint32_t set = __ballot_sync(0xffffffffu, (mine >> b & 1) != 0) & mates;
+            at += __popc(set & below) << b;
+            n += __popc(set) << b;
         }
-        const int n = __shfl_sync(0xffffffffu, at, G - 1, G);
         for (int k = l; k < top; k += G) my.slot[k] = make_uint2(0u, 0xffffffffu);
-        if (__any_sync(0xffffffffu, n > ROUTE_LIST || peak != peak)) {
+        if (__any_sync(0xffffffffu, n > ROUTE_LIST<G> || mine > 7 || peak != peak)) {
             __syncwarp();
-            route_pick<G, NV, VEC>(z, my, l, top);
+            route_pick<G, NV, PER>(z, my, l, top);
         } else {
-            at -= mine;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                if (z[j] >= bound) my.list[at++] = make_uint2(__float_as_uint(z[j]), (uint32_t)route_col<G, NV, VEC>(l, j));
+                if (z[j] >= bound) my.list[at++] = make_uint2(__float_as_uint(z[j]), (uint32_t)route_col<G, PER>(l, j));
             __syncwarp();
             for (int i = l; i < n; i += G) {
                 const uint2 me = my.list[i];
@@ -256,9 +287,10 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 3) route_kernel
             __syncwarp();
         }
         const bool some = peak != -INFINITY;
+        const float zero = some ? peak : 0.0f;                 // with nothing but -inf: e^-inf
         float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) z[j] = some ? route_exp(z[j] - peak) : 0.0f, sum += z[j];
+        for (int j = 0; j < NV; ++j) z[j] = route_exp(z[j] - zero), sum += z[j];
         const float total = group_sum<G>(sum), inv = some ? __fdividef(1.0f, total) : 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) acc[j] += z[j] * inv;
@@ -292,13 +324,13 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 3) route_kernel
     if (tokens != 0) atomicAdd(&slots[E], tokens);
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NV; ++j) sh.sums[group][route_col<G, NV, VEC>(l, j)] = acc[j];
+    for (int j = 0; j < NV; ++j) sh.sums[group][route_col<G, PER>(l, j)] = acc[j];
     __syncthreads();
     for (int i = threadIdx.x; i <= E; i += blockDim.x) {
         if (i < E) {
             float s = 0.0f;
-#pragma unroll
-            for (int w = 0; w < GROUPS; ++w) s += sh.sums[w][i];
+#pragma unroll 8
+            for (int w = 0; w < groups; ++w) s += sh.sums[w][i];
             a.part[(int64_t)blockIdx.x * E + i] = s;
         }
         a.part_counts[(int64_t)blockIdx.x * (E + 1) + i] = slots[i];
@@ -313,22 +345,26 @@ constexpr int ROUTE_FINISH_THREADS = 1024;
 __global__ void __launch_bounds__(ROUTE_FINISH_THREADS) route_finish_kernel(const RouteArgs a, int grid, int ctas)
 {
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    __shared__ float share[ROUTE_FINISH_THREADS], terms[ROUTE_FINISH_THREADS / 32], loss;
-    __shared__ int count[ROUTE_FINISH_THREADS];
-    const int E = a.E, rank = ctas > 1 ? (int)ptx::cluster_ctarank() : 0;
-    // columns 0..E of counts; column E has no share
+    __shared__ float share[ROUTE_FINISH_THREADS], terms[ROUTE_FINISH_THREADS / 32];
+    __shared__ int count[ROUTE_FINISH_THREADS], tokens;
+    const int E = a.E, rank = ctas > 1 ? (int)ptx::cluster_ctarank() : 0, lane = threadIdx.x & 31;
     int cols = 32;
-    while (cols < E + 1) cols *= 2;                            // at most 1024
+    while (cols < E) cols *= 2;                                // at most 512
     const int per = ROUTE_FINISH_THREADS / cols, col = threadIdx.x & (cols - 1), sub = threadIdx.x / cols;
     float s = 0.0f;
-    int n = 0;
-    if (col <= E) {
+    int n = 0, t = 0;
+    ptx::griddep_wait();
+    if (col < E) {
 #pragma unroll 8
         for (int g = rank + sub * ctas; g < grid; g += ctas * per) {
-            if (col < E) s += a.part[(int64_t)g * E + col];
+            s += a.part[(int64_t)g * E + col];
             n += a.part_counts[(int64_t)g * (E + 1) + col];
         }
+    }
+    if (rank == 0 && threadIdx.x < 32) {
+        for (int g = lane; g < grid; g += 32) t += a.part_counts[(int64_t)g * (E + 1) + E];
+        t = __reduce_add_sync(0xffffffffu, t);
+        if (lane == 0) tokens = t, a.counts[E] = t;
     }
     share[threadIdx.x] = s;
     count[threadIdx.x] = n;
@@ -347,18 +383,16 @@ __global__ void __launch_bounds__(ROUTE_FINISH_THREADS) route_finish_kernel(cons
                 s += ptx::ld_cluster_f32(ptx::mapa(ptx::smem_addr(&share[col]), (uint32_t)r));
                 n += (int)ptx::ld_cluster_u32(ptx::mapa(ptx::smem_addr(&count[col]), (uint32_t)r));
             }
-            if (col <= E) a.counts[col] = n;
-            if (col < E) term = (float)n * s;
-            if (col == E) loss = (float)n;
+            if (col < E) a.counts[col] = n, term = (float)n * s;
         }
         term = group_sum<32>(term);
-        if ((threadIdx.x & 31) == 0) terms[threadIdx.x >> 5] = term;
+        if (lane == 0) terms[threadIdx.x >> 5] = term;
         __syncthreads();
         if (threadIdx.x == 0) {
             float sum = 0.0f;
             for (int w = 0; w < cols / 32; ++w) sum += terms[w];
-            const float tokens = loss;
-            a.loss[0] = tokens == 0.0f ? 0.0f : a.coef * (float)E * (sum / tokens) / (tokens * (float)a.top);
+            const float f = (float)tokens;
+            a.loss[0] = tokens == 0 ? 0.0f : a.coef * (float)E * (sum / f) / (f * (float)a.top);
         }
     }
     if (ctas > 1) ptx::cluster_sync();                         // no CTA leaves while its sums are read
@@ -368,12 +402,12 @@ __global__ void __launch_bounds__(ROUTE_FINISH_THREADS) route_finish_kernel(cons
 template <int T, int G, int NV, bool VEC>
 __device__ __forceinline__ void route_store(void *p, int64_t row, int E, int l, const float (&v)[NV])
 {
-    constexpr int ES = T == IN_F32 ? 4 : 2, BYTES = ROUTE_BYTES<T, NV>, PER = BYTES / ES;
+    constexpr int ES = T == IN_F32 ? 4 : 2, BYTES = ROUTE_BYTES<T, NV>, PER = ROUTE_PER<T, NV, VEC>;
     char *at = static_cast<char *>(p) + row * E * ES;
     if constexpr (VEC) {
 #pragma unroll
         for (int g = 0; g < NV / PER; ++g) {
-            const int c = l * NV + g * PER;
+            const int c = route_col<G, PER>(l, g * PER);
             if (c >= E) continue;
             uint32_t w[BYTES / 4];
 #pragma unroll
@@ -387,7 +421,7 @@ __device__ __forceinline__ void route_store(void *p, int64_t row, int E, int l, 
     } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = route_col<G, NV, VEC>(l, j);
+            const int c = route_col<G, PER>(l, j);
             if (c < E) store1<T>(at, c, v[j]);
         }
     }
@@ -399,7 +433,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 4) route_backwa
 {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    constexpr int PER = 32 / G, GROUPS = ROUTE_WARPS * PER, SL = (ROUTE_MAX_TOP + G - 1) / G;
+    constexpr int GROUPS = ROUTE_WARPS * 32 / G, PER = ROUTE_PER<T, NV, VEC>, SL = (ROUTE_MAX_TOP + G - 1) / G;
     // e^z of a token; what its slots add (zeros but while a token is worked on)
     __shared__ __align__(16) float row[GROUPS][G * NV], extra[GROUPS][G * NV];
     const int lane = threadIdx.x & 31, l = lane % G, E = a.E, top = a.top, group = threadIdx.x / G;
@@ -410,7 +444,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 4) route_backwa
         const float up = n > 0.0f ? a.coef * (float)E / n / (n * (float)top) * (a.dloss != nullptr ? a.dloss[0] : 0.0f) : 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = route_col<G, NV, VEC>(l, j);
+            const int c = route_col<G, PER>(l, j);
             u[j] = c < E ? up * (float)a.counts[c] : 0.0f;
             extra[group][c] = 0.0f;
         }
@@ -456,13 +490,13 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 4) route_backwa
             sum += v[j];
             dot += v[j] * u[j];
         }
-        if constexpr (VEC) {
+        if constexpr (PER % 4 == 0) {
 #pragma unroll
             for (int j = 0; j < NV; j += 4)
-                *reinterpret_cast<float4 *>(&row[group][l * NV + j]) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                *reinterpret_cast<float4 *>(&row[group][route_col<G, PER>(l, j)]) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
         } else {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) row[group][j * G + l] = v[j];
+            for (int j = 0; j < NV; ++j) row[group][route_col<G, PER>(l, j)] = v[j];
         }
         __syncwarp();
         const float total = group_sum<G>(sum), inv = on ? __fdividef(1.0f, total) : 0.0f;
@@ -495,15 +529,15 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, NV > 8 ? 2 : 4) route_backwa
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) v[j] *= inv * (u[j] - off);
-        if constexpr (VEC) {
+        if constexpr (PER % 4 == 0) {
 #pragma unroll
             for (int j = 0; j < NV; j += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(&extra[group][l * NV + j]);
+                const float4 x = *reinterpret_cast<const float4 *>(&extra[group][route_col<G, PER>(l, j)]);
                 v[j] += x.x, v[j + 1] += x.y, v[j + 2] += x.z, v[j + 3] += x.w;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) v[j] += extra[group][j * G + l];
+            for (int j = 0; j < NV; ++j) v[j] += extra[group][route_col<G, PER>(l, j)];
         }
         __syncwarp();
 #pragma unroll
@@ -531,16 +565,23 @@ static RouteShape route_shape(int E, int top)
     return {32, 16};
 }
 
-static int route_ctas(int64_t T, RouteShape shape, int ctas_per_sm, int sms)
+static int route_ctas(int64_t T, int lanes, int warps, int most)
 {
-    const int64_t groups = ROUTE_WARPS * 32 / shape.lanes, ctas = (T + groups - 1) / groups;
-    return (int)(ctas < ctas_per_sm * sms ? ctas : ctas_per_sm * sms);
+    const int64_t groups = warps * 32 / lanes, ctas = (T + groups - 1) / groups;
+    return (int)(ctas < most ? ctas : most);
+}
+
+// Warps of a CTA of the forward pass.
+static int route_warps(int64_t T, RouteShape s, int sms)
+{
+    if (T * s.lanes <= (int64_t)sms * 8 * 32) return 8;
+    return s.each > 8 ? ROUTE_FORWARD_WARPS<16> : ROUTE_FORWARD_WARPS<8>;
 }
 
 int route_grid(int64_t T, int64_t E, int64_t top, int sms)
 {
     const RouteShape s = route_shape((int)E, (int)top);
-    return route_ctas(T, s, s.each > 8 ? 2 : 3, sms);
+    return route_ctas(T, s.lanes, route_warps(T, s, sms), sms);
 }
 
 template <int T, int NV>
@@ -550,11 +591,11 @@ static bool route_vec(int E)
 }
 
 template <int T, int G, int NV>
-static cudaError_t route_t(const RouteArgs &a, int grid, cudaStream_t s)
+static cudaError_t route_t(const RouteArgs &a, int grid, int warps, cudaStream_t s)
 {
     auto k = route_vec<T, NV>(a.E) ? route_kernel<T, G, NV, true> : route_kernel<T, G, NV, false>;
     if (grid > 0) {                                            // without tokens: zeros
-        const cudaError_t e = launch_k(k, dim3((unsigned)grid), dim3(32 * ROUTE_WARPS), 0, s, a);
+        const cudaError_t e = launch_k(k, dim3((unsigned)grid), dim3((unsigned)(32 * warps)), 0, s, a);
         if (e != cudaSuccess) return e;
     }
     const int ctas = grid > 32 ? 8 : 1;
@@ -582,37 +623,38 @@ static cudaError_t route_backward_t(const RouteBackwardArgs &a, int grid, cudaSt
 }
 
 template <int T>
-static cudaError_t route_e(const RouteArgs &a, int grid, cudaStream_t s)
+static cudaError_t route_e(const RouteArgs &a, int grid, int sms, cudaStream_t s)
 {
     const RouteShape h = route_shape(a.E, a.top);
+    const int w = route_warps(a.T, h, sms);
     if (h.lanes == 8) {
-        if (h.each == 4) return route_t<T, 8, 4>(a, grid, s);
-        if (h.each == 8) return route_t<T, 8, 8>(a, grid, s);
-        return route_t<T, 8, 16>(a, grid, s);
+        if (h.each == 4) return route_t<T, 8, 4>(a, grid, w, s);
+        if (h.each == 8) return route_t<T, 8, 8>(a, grid, w, s);
+        return route_t<T, 8, 16>(a, grid, w, s);
     }
     if (h.lanes == 16) {
-        if (h.each == 4) return route_t<T, 16, 4>(a, grid, s);
-        if (h.each == 8) return route_t<T, 16, 8>(a, grid, s);
-        return route_t<T, 16, 16>(a, grid, s);
+        if (h.each == 4) return route_t<T, 16, 4>(a, grid, w, s);
+        if (h.each == 8) return route_t<T, 16, 8>(a, grid, w, s);
+        return route_t<T, 16, 16>(a, grid, w, s);
     }
-    return h.each == 8 ? route_t<T, 32, 8>(a, grid, s) : route_t<T, 32, 16>(a, grid, s);
+    return h.each == 8 ? route_t<T, 32, 8>(a, grid, w, s) : route_t<T, 32, 16>(a, grid, w, s);
 }
 
 template <int T>
 static cudaError_t route_backward_e(const RouteBackwardArgs &a, int sms, cudaStream_t s)
 {
-    if (a.E <= 32) return route_backward_t<T, 8, 4>(a, route_ctas(a.T, {8, 4}, 4, sms), s);
-    if (a.E <= 64) return route_backward_t<T, 8, 8>(a, route_ctas(a.T, {8, 8}, 4, sms), s);
-    if (a.E <= 128) return route_backward_t<T, 16, 8>(a, route_ctas(a.T, {16, 8}, 4, sms), s);
-    if (a.E <= 256) return route_backward_t<T, 32, 8>(a, route_ctas(a.T, {32, 8}, 4, sms), s);
-    return route_backward_t<T, 32, 16>(a, route_ctas(a.T, {32, 16}, 2, sms), s);
+    if (a.E <= 32) return route_backward_t<T, 8, 4>(a, route_ctas(a.T, 8, ROUTE_WARPS, 4 * sms), s);
+    if (a.E <= 64) return route_backward_t<T, 8, 8>(a, route_ctas(a.T, 8, ROUTE_WARPS, 4 * sms), s);
+    if (a.E <= 128) return route_backward_t<T, 16, 8>(a, route_ctas(a.T, 16, ROUTE_WARPS, 4 * sms), s);
+    if (a.E <= 256) return route_backward_t<T, 32, 8>(a, route_ctas(a.T, 32, ROUTE_WARPS, 4 * sms), s);
+    return route_backward_t<T, 32, 16>(a, route_ctas(a.T, 32, ROUTE_WARPS, 2 * sms), s);
 }
 
-cudaError_t launch_moe_route(const RouteArgs &a, int type, int grid, cudaStream_t s)
+cudaError_t launch_moe_route(const RouteArgs &a, int type, int grid, int sms, cudaStream_t s)
 {
-    if (type == IN_BF16) return route_e<IN_BF16>(a, grid, s);
-    if (type == IN_F16) return route_e<IN_F16>(a, grid, s);
-    return route_e<IN_F32>(a, grid, s);
+    if (type == IN_BF16) return route_e<IN_BF16>(a, grid, sms, s);
+    if (type == IN_F16) return route_e<IN_F16>(a, grid, sms, s);
+    return route_e<IN_F32>(a, grid, sms, s);
 }
 
 cudaError_t launch_moe_route_backward(const RouteBackwardArgs &a, int type, int sms, cudaStream_t s)
