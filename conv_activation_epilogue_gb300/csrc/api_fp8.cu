@@ -96,7 +96,7 @@ bool f8_encode(CUtensorMap *mc, CUtensorMap *ms, const F8Matrix &m, int64_t rows
 // Plan of one product: either kernel's launch.
 struct F8Plan {
     bool pair, quantize;             // quantize: x first, by a kernel of its own
-    F8GemmLaunch P;
+    F8Problem P;
     F8RowsLaunch R;
 };
 
@@ -126,30 +126,26 @@ mmact_status f8_gemm_plan(F8Plan &plan, const F8Matrix &A, const F8Matrix &B, co
     plan.pair = f8_choose_pair(c, M, N);
     plan.quantize = x != nullptr && plan.pair;
     if (plan.pair) {
-        F8GemmLaunch &L = plan.P;
+        F8Problem &L = plan.P;
         std::memset(&L, 0, sizeof(L));
-        F8GemmArgs &a = L.args;
-        a.M = (int)M;
-        a.N = (int)N;
-        a.nk32 = nk32;
-        a.num_kb = num_kb;
-        a.tiles_m = (int)((M + 255) / 256);
-        a.tiles_n = (int)((N + 255) / 256);
-        a.num_tiles = a.tiles_m * a.tiles_n;
-        a.group_m = 8;
-        a.act = (int)act;
-        a.alpha = alpha;
-        a.bias = bias;
-        a.C = C;
-        a.idesc = ptx::idesc_f8(f8_kind(A.type), f8_kind(B.type), 256, 256);
-        a.status = c.dev.status;
-        a.wait_ns = c.dev.wait_ns;
+        L.M = (int)M;
+        L.N = (int)N;
+        L.nk32 = nk32;
+        L.num_kb = num_kb;
+        L.tiles_m = (int)((M + 255) / 256);
+        L.tiles_n = (int)((N + 255) / 256);
+        L.num_tiles = L.tiles_m * L.tiles_n;
+        L.group_m = 8;
+        L.act = (int)act;
+        L.alpha = alpha;
+        L.bias = bias;
+        L.C = C;
+        L.idesc = ptx::idesc_f8(f8_kind(A.type), f8_kind(B.type), 256, 256);
         const int ce = elem_bytes(cd);
-        a.c_tma = N * ce % 16 == 0 ? 1 : 0;
+        L.c_tma = N * ce % 16 == 0 ? 1 : 0;
         L.out = out_kind(cd);
-        L.grid = 2 * (int)std::min<int64_t>(a.num_tiles, c.max_pairs);
         if (!f8_encode(&L.tmA, &L.tmSA, A, M, K, 128, 1) || !f8_encode(&L.tmB, &L.tmSB, B, N, K, 128, 2)) return MMACT_ERR_CUDA;
-        if (a.c_tma) {
+        if (L.c_tma) {
             const uint64_t dC[2] = {(uint64_t)N, (uint64_t)M}, sC[1] = {(uint64_t)N * ce};
             const uint32_t bC[2] = {(uint32_t)(128 / ce), 32};
             if (!encode_tensor_map(&L.tmC, cd, 2, C, dC, sC, bC, true)) return MMACT_ERR_CUDA;
@@ -200,9 +196,33 @@ mmact_status f8_gemm_plan(F8Plan &plan, const F8Matrix &A, const F8Matrix &B, co
     return f8_encode(&L.tmT, &L.tmST, A, M, K, (uint32_t)bt, 1) ? MMACT_OK : MMACT_ERR_CUDA;
 }
 
-cudaError_t f8_gemm_launch(const F8Plan &plan, cudaStream_t stream)
+// Launches a product, or two that do not depend on each other (`other`, or null).
+mmact_status f8_gemm_launch(const F8Plan &plan, const F8Plan *other, cudaStream_t stream)
 {
-    return plan.pair ? launch_gemm_fp8_pair(plan.P, stream) : launch_gemm_fp8_rows(plan.R, stream);
+    if (!plan.pair || (other != nullptr && !other->pair)) {
+        mmact_status s = MMACT_OK;
+        if (other != nullptr) s = f8_gemm_launch(*other, nullptr, stream);
+        if (s != MMACT_OK) return s;
+        if (!plan.pair) return enqueued(launch_gemm_fp8_rows(plan.R, stream));
+        other = nullptr;
+    }
+    F8Context c;
+    const mmact_status s = f8_context(&c);
+    if (s != MMACT_OK) return s;
+    F8GemmArgs a;
+    std::memset(&a, 0, sizeof(a));
+    // the one with the longer tiles first: the others fill the last round
+    const bool swap = other != nullptr && other->P.num_kb > plan.P.num_kb;
+    a.prob[0] = swap ? other->P : plan.P;
+    a.tiles[0] = a.prob[0].num_tiles;
+    if (other != nullptr) {
+        a.prob[1] = swap ? plan.P : other->P;
+        a.tiles[1] = a.prob[1].num_tiles;
+        a.lead = std::max(1, (a.prob[0].num_kb + a.prob[1].num_kb / 2) / a.prob[1].num_kb);
+    }
+    a.status = c.dev.status;
+    a.wait_ns = c.dev.wait_ns;
+    return enqueued(launch_gemm_fp8_pair(a, (int)std::min<int64_t>((int64_t)a.tiles[0] + a.tiles[1], c.max_pairs), stream));
 }
 
 cudaError_t quantize_launch(const void *x, const F8Matrix &m, int64_t rows, int64_t K, mmact_dtype xd, bool square,
@@ -301,7 +321,7 @@ MMACT_EXPORT mmact_status mmact_gemm_fp8(const void *a_codes, const void *a_scal
     if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
     F8Plan L;
     s = f8_gemm_plan(L, A, B, bias, C, M, N, K, c_dtype, act, alpha);
-    return s == MMACT_OK ? enqueued(f8_gemm_launch(L, st)) : s;
+    return s == MMACT_OK ? f8_gemm_launch(L, nullptr, st) : s;
 }
 
 MMACT_EXPORT mmact_status mmact_set_gemm_fp8_kernel(int mode)
@@ -336,7 +356,7 @@ MMACT_EXPORT mmact_status mmact_linear_fp8(const void *x, const void *w_codes, c
     F8Plan L;
     if ((s = f8_gemm_plan(L, A, W, bias, C, M, N, K, c_dtype, act, alpha, x, x_dtype)) != MMACT_OK) return s;
     if (L.quantize && (s = enqueued(quantize_launch(x, A, M, K, x_dtype, false, false, st))) != MMACT_OK) return s;
-    return enqueued(f8_gemm_launch(L, st));
+    return f8_gemm_launch(L, nullptr, st);
 }
 
 MMACT_EXPORT mmact_status mmact_linear_fp8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t *bytes)
@@ -382,14 +402,22 @@ MMACT_EXPORT mmact_status mmact_linear_fp8_backward(const void *dy, const void *
                                      MMACT_ACT_NONE, 0.0f)) != MMACT_OK)
         return s;
     if (want_dw && (s = f8_gemm_plan(W, gyt, xt, nullptr, dw, N, K, M, dw_dtype, MMACT_ACT_NONE, 0.0f)) != MMACT_OK) return s;
-    if (want_dx) {
-        if ((s = enqueued(quantize_launch(dy, gy, M, N, x_dtype, false, false, st))) != MMACT_OK) return s;
-        if ((s = enqueued(f8_gemm_launch(X, st))) != MMACT_OK) return s;
-    }
+    F8Grads g;
+    std::memset(&g, 0, sizeof(g));
+    g.dy = dy;
+    g.x = x;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    auto bytes = [](const void *p) { return static_cast<uint8_t *>(const_cast<void *>(p)); };
+    if (want_dx) g.row_codes = bytes(gy.codes), g.row_scales = bytes(gy.scales);
     if (want_dw) {
-        if ((s = enqueued(quantize_launch(dy, gyt, N, M, x_dtype, false, true, st))) != MMACT_OK) return s;
-        if ((s = enqueued(quantize_launch(x, xt, K, M, x_dtype, false, true, st))) != MMACT_OK) return s;
-        if ((s = enqueued(f8_gemm_launch(W, st))) != MMACT_OK) return s;
+        g.col_codes = bytes(gyt.codes), g.col_scales = bytes(gyt.scales);
+        g.xt_codes = bytes(xt.codes), g.xt_scales = bytes(xt.scales);
     }
-    return want_db ? enqueued(launch_column_sums(dy, out_kind(x_dtype), part, db, M, N, st)) : MMACT_OK;
+    if (want_db) g.part = part;
+    if ((s = enqueued(launch_quantize_fp8_grads(g, out_kind(x_dtype), f8_kind(grad_dtype), st))) != MMACT_OK) return s;
+    if (want_db && (s = enqueued(launch_column_sums(part, db, M, N, st))) != MMACT_OK) return s;
+    if (!want_dx && !want_dw) return MMACT_OK;
+    return f8_gemm_launch(want_dw ? W : X, want_dw && want_dx ? &X : nullptr, st);
 }

@@ -118,29 +118,25 @@ __global__ void __launch_bounds__(512) quantize_f8_square_kernel(const void *x, 
     if ((threadIdx.x & 3) == 0) scales[mx_scale_at(row, kb, tiles)] = (uint8_t)(row < rows ? b : 0u);
 }
 
-// x [K, rows] row-major, blocks along K (the right operand of a row-major product, or
-// a matrix whose gradient is summed over its rows).  A CTA takes 128 K of 128 columns, a warp
-// 32 K of 64 columns, two to a lane: 32 coalesced loads in flight.  Each column's (SQUARE:
-// the tile's) largest |x| and the codes go through shared memory, and each row's 128
-// bytes of codes are written together.
-template <int T, int F8, bool VEC, bool SQUARE>
-__global__ void __launch_bounds__(256) quantize_f8_trans_kernel(const void *x, uint8_t *codes, uint8_t *scales, int64_t rows,
-                                                                int64_t K, int col_tiles)
+// ------------------------------------------------------ tiles of 128 K x 128 columns --
+// x [K, cols] row-major.  A CTA of 8 warps takes 128 K of 128 columns, a warp 32 K of 64
+// columns, two to a lane: 32 coalesced loads in flight, values in registers as raw words.
+template <int T>
+constexpr int PAIR_WORDS = T == IN_F32 ? 2 : 1;                // words of a pair of columns
+
+struct TileSmem {
+    uint32_t codes[128][33];                                   // [column][32 words] (+1: the lanes' columns on other banks)
+    uint32_t amax[4][128];
+};
+
+// `vec`: pairs of columns are aligned.
+template <int T>
+__device__ __forceinline__ void load_pairs(const void *x, int64_t K, int64_t cols, int64_t k0, int64_t c0, int64_t col, bool vec,
+                                           uint32_t (&a)[32 * PAIR_WORDS<T>])
 {
-    constexpr int WPP = T == IN_F32 ? 2 : 1;                   // words of a pair of columns
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    __shared__ uint32_t sc[128][33];                           // [row][32 words] (+1: the lanes' rows on other banks)
-    __shared__ __align__(8) uint32_t sm[4][128];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kq = warp & 3, c = (warp >> 2) * 64 + 2 * lane;
-    const int64_t kt = blockIdx.x / col_tiles;
-    const int64_t c0 = (int64_t)(blockIdx.x - kt * col_tiles) * 128;
-    const int64_t k0 = kt * 128 + kq * 32, col = c0 + c;
-    const int64_t tiles = f8_tiles(K), pitch = f8_pitch(K);
-    uint32_t a[32 * WPP];
-    if (VEC && c0 + 128 <= rows && k0 + 32 <= K) {             // a whole tile: the same for the warp
-        const char *p = static_cast<const char *>(x) + (k0 * rows + col) * (T == IN_F32 ? 4 : 2);
-        const int64_t line = rows * (T == IN_F32 ? 4 : 2);
+    if (vec && c0 + 128 <= cols && k0 + 32 <= K) {             // a whole tile: the same for the warp
+        const char *p = static_cast<const char *>(x) + (k0 * cols + col) * (T == IN_F32 ? 4 : 2);
+        const int64_t line = cols * (T == IN_F32 ? 4 : 2);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             if constexpr (T == IN_F32) {
@@ -153,8 +149,8 @@ __global__ void __launch_bounds__(256) quantize_f8_trans_kernel(const void *x, u
     } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            const int64_t i = (k0 + j) * rows + col;
-            const bool in0 = k0 + j < K && col < rows, in1 = k0 + j < K && col + 1 < rows;
+            const int64_t i = (k0 + j) * cols + col;
+            const bool in0 = k0 + j < K && col < cols, in1 = k0 + j < K && col + 1 < cols;
             if constexpr (T == IN_F32) {
                 a[2 * j] = in0 ? static_cast<const uint32_t *>(x)[i] : 0u;
                 a[2 * j + 1] = in1 ? static_cast<const uint32_t *>(x)[i + 1] : 0u;
@@ -164,6 +160,26 @@ __global__ void __launch_bounds__(256) quantize_f8_trans_kernel(const void *x, u
             }
         }
     }
+}
+
+// The pair of values of row j of the tile.
+template <int T>
+__device__ __forceinline__ float2 pair_of(const uint32_t (&a)[32 * PAIR_WORDS<T>], int j)
+{
+    if constexpr (T == IN_F32) return make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]));
+    else return unpack2<T>(a[j]);
+}
+
+// The tile turned round, blocks along K: row `col` of codes [cols, K].  Each column's
+// (SQUARE: the tile's) largest |x| and the codes go through shared memory, and each
+// row's 128 bytes of codes are written together.
+template <int T, int F8, bool SQUARE>
+__device__ __forceinline__ void store_columns(const uint32_t (&a)[32 * PAIR_WORDS<T>], TileSmem &sh, uint8_t *codes,
+                                              uint8_t *scales, int64_t rows, int64_t K, int64_t kt, int64_t c0)
+{
+    constexpr int WPP = PAIR_WORDS<T>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kq = warp & 3, c = (warp >> 2) * 64 + 2 * lane;
+    const int64_t tiles = f8_tiles(K), pitch = f8_pitch(K), col = c0 + c;
     uint32_t m[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -176,17 +192,17 @@ __global__ void __launch_bounds__(256) quantize_f8_trans_kernel(const void *x, u
     }
     if constexpr (SQUARE) {
         m[0] = __reduce_max_sync(0xffffffffu, max(m[0], m[1]));
-        if (lane == 0) sm[0][warp] = m[0];
+        if (lane == 0) sh.amax[0][warp] = m[0];
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[0] = max(m[0], sm[0][j]);
+        for (int j = 0; j < 8; ++j) m[0] = max(m[0], sh.amax[0][j]);
         m[1] = m[0];
     } else {
-        *reinterpret_cast<uint2 *>(&sm[kq][c]) = make_uint2(m[0], m[1]);
+        *reinterpret_cast<uint2 *>(&sh.amax[kq][c]) = make_uint2(m[0], m[1]);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint2 u = *reinterpret_cast<const uint2 *>(&sm[j][c]);
+            const uint2 u = *reinterpret_cast<const uint2 *>(&sh.amax[j][c]);
             m[0] = max(m[0], u.x);
             m[1] = max(m[1], u.y);
         }
@@ -195,27 +211,18 @@ __global__ void __launch_bounds__(256) quantize_f8_trans_kernel(const void *x, u
     const float inv0 = mx_inv_scale(b0 == 255u ? 0u : b0), inv1 = mx_inv_scale(b1 == 255u ? 0u : b1);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-        float v[4], w[4];
+        float2 f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (T == IN_F32) {
-                v[j] = __uint_as_float(a[2 * (4 * q + j)]) * inv0;
-                w[j] = __uint_as_float(a[2 * (4 * q + j) + 1]) * inv1;
-            } else {
-                const float2 f = unpack2<T>(a[4 * q + j]);
-                v[j] = f.x * inv0;
-                w[j] = f.y * inv1;
-            }
-        }
-        sc[c][kq * 8 + q] = b0 == 255u ? 0u : f8_encode4<F8>(v[0], v[1], v[2], v[3]);
-        sc[c + 1][kq * 8 + q] = b1 == 255u ? 0u : f8_encode4<F8>(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 4; ++j) f[j] = pair_of<T>(a, 4 * q + j);
+        sh.codes[c][kq * 8 + q] = b0 == 255u ? 0u : f8_encode4<F8>(f[0].x * inv0, f[1].x * inv0, f[2].x * inv0, f[3].x * inv0);
+        sh.codes[c + 1][kq * 8 + q] = b1 == 255u ? 0u : f8_encode4<F8>(f[0].y * inv1, f[1].y * inv1, f[2].y * inv1, f[3].y * inv1);
     }
     __syncthreads();
     // codes: 4 bytes to a thread, a warp writes 128 bytes of one row at a time
 #pragma unroll 4
     for (int r = warp; r < 128; r += 8)
         if (c0 + r < rows && kt * 128 + lane * 4 < pitch)
-            *reinterpret_cast<uint32_t *>(codes + (c0 + r) * pitch + kt * 128 + lane * 4) = sc[r][lane];
+            *reinterpret_cast<uint32_t *>(codes + (c0 + r) * pitch + kt * 128 + lane * 4) = sh.codes[r][lane];
     // scales: a byte a row, and zeros for rows and blocks that do not exist
     if (kq == 0) {
         const int64_t last = kt == f8_blocks(K) - 1 ? tiles * 4 : kt + 1;
@@ -224,6 +231,104 @@ __global__ void __launch_bounds__(256) quantize_f8_trans_kernel(const void *x, u
             scales[mx_scale_at(col + 1, b, tiles)] = (uint8_t)(b == kt && col + 1 < rows ? b1 : 0u);
         }
     }
+}
+
+template <int T, int F8, bool SQUARE>
+__global__ void __launch_bounds__(256) quantize_f8_trans_kernel(const void *x, uint8_t *codes, uint8_t *scales, int64_t rows,
+                                                                int64_t K, int col_tiles, bool vec)
+{
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    __shared__ TileSmem sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t kt = blockIdx.x / col_tiles, c0 = (int64_t)(blockIdx.x - kt * col_tiles) * 128;
+    uint32_t a[32 * PAIR_WORDS<T>];
+    load_pairs<T>(x, K, rows, kt * 128 + (warp & 3) * 32, c0, c0 + (warp >> 2) * 64 + 2 * lane, vec, a);
+    store_columns<T, F8, SQUARE>(a, sh, codes, scales, rows, K, kt, c0);
+}
+
+// The tile as it is, blocks along its 128 columns: rows of codes [K, cols].  A row's
+// largest |x| is the warp's (one reduction instruction a row), then that of the two
+// warps that share the row; `amax` [2][128] and `inv` [8][32] are shared memory.
+template <int T, int F8>
+__device__ __forceinline__ void store_rows(const uint32_t (&a)[32 * PAIR_WORDS<T>], uint32_t (*amax)[128], float (*inv)[32],
+                                           uint8_t *codes, uint8_t *scales, int64_t rows, int64_t cols, int64_t rt, int64_t ct)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kq = warp & 3, half = warp >> 2;
+    const int64_t tiles = f8_tiles(cols), pitch = f8_pitch(cols), row = rt * 128 + kq * 32 + lane;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        uint32_t v;
+        if constexpr (T == IN_F32) {
+            v = max(a[2 * j] & 0x7fffffffu, a[2 * j + 1] & 0x7fffffffu);
+        } else {
+            const uint32_t w = a[j] & 0x7fff7fffu;
+            v = max(w & 0xffffu, w >> 16);
+        }
+        v = __reduce_max_sync(0xffffffffu, v);
+        if (lane == j) m = v;
+    }
+    amax[half][kq * 32 + lane] = m;
+    __syncthreads();
+    m = max(m, amax[half ^ 1][kq * 32 + lane]);
+    if constexpr (T != IN_F32) m = bits_of<T>(m);
+    const uint32_t b = f8_scale_byte<F8>(m);
+    inv[warp][lane] = b == 255u ? -1.0f : mx_inv_scale(b);     // -1: codes 0
+    __syncwarp();
+    const int64_t c = ct * 128 + half * 64 + 2 * lane;
+    uint8_t *to = codes + (rt * 128 + kq * 32) * pitch + c;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float s = inv[warp][j];
+        const float2 f = pair_of<T>(a, j);
+        const uint32_t v = f8_encode4<F8>(f.x * s, f.y * s, 0.0f, 0.0f);
+        if (rt * 128 + kq * 32 + j < rows && c < pitch) *reinterpret_cast<uint16_t *>(to + j * pitch) = (uint16_t)(s < 0.0f ? 0u : v);
+    }
+    if (half == 0) {
+        const int64_t last = ct == f8_blocks(cols) - 1 ? tiles * 4 : ct + 1;
+        for (int64_t k = ct; k < last; ++k) scales[mx_scale_at(row, k, tiles)] = (uint8_t)(k == ct && row < rows ? b : 0u);
+    }
+}
+
+// What the backward pass of a linear layer makes of dy [M, N] and x [M, K], in one
+// launch: dy by rows (for dx), dy turned round and its column sums (dw, db), x turned round
+// (dw): dy is read once.  The first CTAs take tiles of dy, the others of x.
+template <int T, int F8>
+__global__ void __launch_bounds__(256) quantize_f8_grads_kernel(const F8Grads g)
+{
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    __shared__ TileSmem sh;
+    __shared__ uint32_t amax[2][128];
+    __shared__ float inv[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kq = warp & 3, c = (warp >> 2) * 64 + 2 * lane;
+    uint32_t a[32 * PAIR_WORDS<T>];
+    if ((int64_t)blockIdx.x >= g.dy_tiles) {
+        const int64_t i = blockIdx.x - g.dy_tiles, tk = (g.K + 127) / 128, rt = i / tk, c0 = (i - rt * tk) * 128;
+        load_pairs<T>(g.x, g.M, g.K, rt * 128 + kq * 32, c0, c0 + c, g.K % 2 == 0, a);
+        store_columns<T, F8_E4M3, false>(a, sh, g.xt_codes, g.xt_scales, g.K, g.M, rt, c0);
+        return;
+    }
+    const int64_t tn = (g.N + 127) / 128, rt = blockIdx.x / tn, ct = blockIdx.x - rt * tn, c0 = ct * 128;
+    load_pairs<T>(g.dy, g.M, g.N, rt * 128 + kq * 32, c0, c0 + c, g.N % 2 == 0, a);
+    if (g.row_codes != nullptr) store_rows<T, F8>(a, amax, inv, g.row_codes, g.row_scales, g.M, g.N, rt, ct);
+    if (g.part != nullptr) {                                   // rows in order, then quarters of the tile
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float2 f = pair_of<T>(a, j);
+            sum.x += f.x, sum.y += f.y;
+        }
+        float(*sums)[128] = reinterpret_cast<float(*)[128]>(&sh.codes[0][0]);
+        sums[kq][c] = sum.x, sums[kq][c + 1] = sum.y;
+        __syncthreads();
+        const int64_t col = c0 + threadIdx.x;
+        if (threadIdx.x < 128 && col < g.N)
+            g.part[rt * g.N + col] = sums[0][threadIdx.x] + sums[1][threadIdx.x] + sums[2][threadIdx.x] + sums[3][threadIdx.x];
+        __syncthreads();
+    }
+    if (g.col_codes != nullptr) store_columns<T, F8, false>(a, sh, g.col_codes, g.col_scales, g.N, g.M, rt, c0);
 }
 
 // codes and scales -> y [rows, K].  Sixteen lanes take one row's block of 128 values, 8
@@ -286,36 +391,24 @@ __global__ void __launch_bounds__(256) dequantize_f8_kernel(const uint8_t *codes
     }
 }
 
-// Sums of 128 rows of 256 columns, a column to a thread, into part [ceil(rows / 128)][cols];
-// then those over all row blocks, in order.
-template <int T>
-__global__ void __launch_bounds__(256) column_part_kernel(const void *x, float *part, int64_t rows, int64_t cols, int col_tiles)
-{
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int64_t rb = blockIdx.x / col_tiles, c = (blockIdx.x - rb * col_tiles) * 256 + threadIdx.x;
-    if (c >= cols) return;
-    const int64_t last = min(rows, (rb + 1) * 128);
-    float sum = 0.0f;
-#pragma unroll 8
-    for (int64_t r = rb * 128; r < last; ++r) {
-        const int64_t i = r * cols + c;
-        if constexpr (T == IN_F32) sum += static_cast<const float *>(x)[i];
-        else if constexpr (T == IN_BF16) sum += __bfloat162float(static_cast<const __nv_bfloat16 *>(x)[i]);
-        else sum += __half2float(static_cast<const __half *>(x)[i]);
-    }
-    part[rb * cols + c] = sum;
-}
-
+// db from the tiles' column sums: 32 columns to a CTA, every 8th row block to a warp, then
+// the warps in order.
 __global__ void __launch_bounds__(256) column_sum_kernel(const float *part, float *out, int64_t blocks, int64_t cols)
 {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= cols) return;
+    __shared__ float sums[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float sum = 0.0f;
+    if (c < cols)
 #pragma unroll 8
-    for (int64_t b = 0; b < blocks; ++b) sum += part[b * cols + c];
+        for (int64_t b = warp; b < blocks; b += 8) sum += part[b * cols + c];
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp != 0 || c >= cols) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) sum += sums[w][lane];
     out[c] = sum;
 }
 
@@ -328,9 +421,8 @@ static cudaError_t quantize_t(const void *x, uint8_t *codes, uint8_t *scales, in
     if (trans) {
         const int64_t col_tiles = padded / 128, grid = f8_blocks(K) * col_tiles;
         if (grid > INT32_MAX) return cudaErrorInvalidValue;
-        auto k = rows % 2 == 0 ? (square ? quantize_f8_trans_kernel<T, F8, true, true> : quantize_f8_trans_kernel<T, F8, true, false>)
-                               : (square ? quantize_f8_trans_kernel<T, F8, false, true> : quantize_f8_trans_kernel<T, F8, false, false>);
-        return launch_k(k, dim3((unsigned)grid), dim3(256), 0, s, x, codes, scales, rows, K, (int)col_tiles);
+        auto k = square ? quantize_f8_trans_kernel<T, F8, true> : quantize_f8_trans_kernel<T, F8, false>;
+        return launch_k(k, dim3((unsigned)grid), dim3(256), 0, s, x, codes, scales, rows, K, (int)col_tiles, rows % 2 == 0);
     }
     const bool vec = K * e % 16 == 0;
     if (square) {
@@ -394,14 +486,26 @@ cudaError_t launch_dequantize_fp8(const uint8_t *codes, const uint8_t *scales, v
                          : dequantize_f8<F8_E5M2>(codes, scales, y, type, rows, K, sms, s);
 }
 
-cudaError_t launch_column_sums(const void *x, int type, float *part, float *out, int64_t rows, int64_t cols, cudaStream_t s)
+cudaError_t launch_quantize_fp8_grads(F8Grads g, int type, int f8, cudaStream_t s)
 {
-    const int64_t col_tiles = (cols + 255) / 256, blocks = (rows + 127) / 128, grid = blocks * col_tiles;
+    const int64_t tm = (g.M + 127) / 128, tn = (g.N + 127) / 128, tk = (g.K + 127) / 128;
+    g.dy_tiles = g.row_codes != nullptr || g.col_codes != nullptr || g.part != nullptr ? tm * tn : 0;
+    const int64_t grid = g.dy_tiles + (g.xt_codes != nullptr ? tm * tk : 0);
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    auto k = type == IN_BF16 ? column_part_kernel<IN_BF16>
-                             : (type == IN_F16 ? column_part_kernel<IN_F16> : column_part_kernel<IN_F32>);
-    const cudaError_t e = launch_k(k, dim3((unsigned)grid), dim3(256), 0, s, x, part, rows, cols, (int)col_tiles);
-    return e != cudaSuccess ? e : launch_k(column_sum_kernel, dim3((unsigned)col_tiles), dim3(256), 0, s, part, out, blocks, cols);
+    if (grid == 0) return cudaSuccess;
+    void (*k)(const F8Grads);
+    if (f8 == F8_E4M3)
+        k = type == IN_BF16 ? quantize_f8_grads_kernel<IN_BF16, F8_E4M3>
+                            : (type == IN_F16 ? quantize_f8_grads_kernel<IN_F16, F8_E4M3> : quantize_f8_grads_kernel<IN_F32, F8_E4M3>);
+    else
+        k = type == IN_BF16 ? quantize_f8_grads_kernel<IN_BF16, F8_E5M2>
+                            : (type == IN_F16 ? quantize_f8_grads_kernel<IN_F16, F8_E5M2> : quantize_f8_grads_kernel<IN_F32, F8_E5M2>);
+    return launch_k(k, dim3((unsigned)grid), dim3(256), 0, s, g);
+}
+
+cudaError_t launch_column_sums(const float *part, float *out, int64_t rows, int64_t cols, cudaStream_t s)
+{
+    return launch_k(column_sum_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, s, part, out, (rows + 127) / 128, cols);
 }
 
 }  // namespace mmact

@@ -12,6 +12,10 @@
 // stage is.  The epilogue of a tile takes the shared columns first and lets the next
 // tile's MMAs start as soon as they are in registers, before it works on them.
 //
+// Two products that do not depend on each other (a linear layer's two gradients) can share
+// one launch: the pairs go on from the tiles of the one to the tiles of the other, instead
+// of waiting twice for the slowest.
+//
 //   warp 0      (both CTAs) TMA producer; copies complete on the even CTA's barriers
 //   warp 1      TMEM allocation; in the even CTA the scale copies and the MMAs
 //   warps 2..9  (both CTAs) epilogue of the CTA's 128 rows, two warps for each 32
@@ -45,8 +49,8 @@ struct F8PairCfg {
     static_assert(SCALE_COL + STAGES * SLOT_COLS <= TMEM_COLS, "tensor memory budget");
 };
 
-// Pair tile t -> (M block, N block) of 256 x 256, grouped M-first.
-__device__ __forceinline__ void f8_tile(int t, const F8GemmArgs &p, int &mb, int &nb)
+// Tile t of a product -> (M block, N block) of 256 x 256, grouped M-first.
+__device__ __forceinline__ void f8_tile(int t, const F8Problem &p, int &mb, int &nb)
 {
     const int per_group = p.group_m * p.tiles_n;
     const int g = t / per_group;
@@ -57,15 +61,69 @@ __device__ __forceinline__ void f8_tile(int t, const F8GemmArgs &p, int &mb, int
     nb = r / gm;
 }
 
+// A pair's i-th tile: of the first product in rounds of all pairs, then of the second.
+// In the first's last round some pairs have no tile; they begin with the second, `lead`
+// rounds of their own.  False when there is none.
+__device__ __forceinline__ bool f8_schedule(int i, int pair, int npairs, const F8GemmArgs &p, int &which, int &t)
+{
+    const int rest = p.tiles[0] % npairs, own = p.tiles[0] / npairs + (pair < rest ? 1 : 0);
+    which = 0;
+    t = pair + i * npairs;
+    if (i < own) return true;
+    which = 1;
+    i -= own;
+    const int early = rest != 0 ? npairs - rest : 0, ahead = early * p.lead;
+    if (early != 0 && pair >= rest && i < p.lead) t = i * early + pair - rest;
+    else t = ahead + (i - (early != 0 && pair >= rest ? p.lead : 0)) * npairs + pair;
+    return t < p.tiles[1];
+}
+
+// The epilogue of one tile: this warp's 32 rows, every other unit of columns.
 template <int OUT>
-__global__ void __launch_bounds__(F8PairCfg::THREADS, 1)
-    gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                           const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                           const __grid_constant__ CUtensorMap tmC, const F8GemmArgs p)
+__device__ __forceinline__ void f8_epilogue(const F8Problem &p, int mb, int nb, uint32_t rank, bool upper, int part, uint32_t tbase,
+                                            uint32_t buf, int lane, int row0, uint32_t tempty, uint32_t tempty_leader)
+{
+    constexpr int COLS = OUT == OUT_F32 ? 32 : 64;
+    constexpr int NU = 256 / COLS, SHARED = 64 / COLS;        // units of a tile; of the columns that it shares
+    const uint64_t pol_c = ptx::createpolicy_evict_first();   // C is not read back here
+    // the shared columns are the last of the lower accumulator and the first of the upper one
+    const int first = upper ? 0 : NU - SHARED;
+#pragma unroll 1
+    for (int i = part; i < NU; i += 2) {
+        const int u = (first + i) & (NU - 1);
+        const int col0 = nb * 256 + u * COLS;
+        if (lane == 0) ptx::bulk_wait_read<0>();
+        __syncwarp();
+        mx_epi_unit<OUT>(p.act, tbase + u * COLS, p.bias != nullptr ? p.bias + col0 : nullptr, p.N - col0, p.alpha, buf, lane, [&] {
+            // The warp's first unit: the shared columns are among the first units of the warps that have them,
+            // and every warp is past the tile before.
+            if (i != part) return;
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) ptx::mbar_arrive(tempty);
+                else ptx::mbar_arrive_cluster(tempty_leader);
+            }
+        });
+        if (p.c_tma) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < p.M && col0 < p.N) {
+                ptx::tma_store_2d_hint(&p.tmC, buf, col0, row0, pol_c);
+                ptx::bulk_commit();
+            }
+        } else {
+            __syncwarp();
+            mx_store_elements<OUT>(p.C, buf, row0, col0, p.M, p.N, lane);
+            __syncwarp();
+        }
+    }
+}
+
+__global__ void __launch_bounds__(F8PairCfg::THREADS, 1) gemm_fp8_pair_kernel(const __grid_constant__ F8GemmArgs p)
 {
     using Cfg = F8PairCfg;
     constexpr int STAGES = Cfg::STAGES;
-    constexpr int COLS = OUT == OUT_F32 ? 32 : 64;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = ptx::smem_addr(smem);
@@ -89,8 +147,8 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1)
     pp.wait_ns = p.wait_ns;
     if (aligned) {
         if (threadIdx.x == 0) {
-            ptx::prefetch_tensormap(&tmA);
-            ptx::prefetch_tensormap(&tmB);
+            ptx::prefetch_tensormap(&p.prob[0].tmA);
+            ptx::prefetch_tensormap(&p.prob[0].tmB);
             for (int s = 0; s < STAGES; ++s) {
                 ptx::mbar_init(pp.full0 + 8 * s, 1);
                 ptx::mbar_init(pp.empty0 + 8 * s, 1);
@@ -123,18 +181,19 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1)
         if (lane == 0) {
             uint32_t stage = 0, phase = 0;
             bool ok = true;
-            for (int t = pair; t < p.num_tiles && ok; t += npairs) {
+            for (int i = 0, w, t; ok && f8_schedule(i, pair, npairs, p, w, t); ++i) {
+                const F8Problem &q = p.prob[w];
                 int mb, nb;
-                f8_tile(t, p, mb, nb);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                f8_tile(t, q, mb, nb);
+                for (int kb = 0; kb < q.num_kb; ++kb) {
                     if (!pipe_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) { ok = false; break; }
                     const uint32_t fb = pp.full0 + 8 * stage;
                     if (leader) ptx::mbar_arrive_expect_tx(fb, 2u * Cfg::STAGE_BYTES);
                     const uint32_t to = ptx::mapa(fb, 0);
-                    ptx::tma_load_2d_pair(sA + stage * Cfg::A_BYTES, &tmA, to, kb * 64, mb * 256 + (int)rank * 128);
-                    ptx::tma_load_2d_pair(sB + stage * Cfg::B_BYTES, &tmB, to, kb * 64, nb * 256 + (int)rank * 128);
-                    ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES, &tmSA, to, (kb >> 2) * 128, mb * 2 + (int)rank);
-                    ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES + 512u, &tmSB, to, (kb >> 2) * 128, nb * 2);
+                    ptx::tma_load_2d_pair(sA + stage * Cfg::A_BYTES, &q.tmA, to, kb * 64, mb * 256 + (int)rank * 128);
+                    ptx::tma_load_2d_pair(sB + stage * Cfg::B_BYTES, &q.tmB, to, kb * 64, nb * 256 + (int)rank * 128);
+                    ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES, &q.tmSA, to, (kb >> 2) * 128, mb * 2 + (int)rank);
+                    ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES + 512u, &q.tmSB, to, (kb >> 2) * 128, nb * 2);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -146,17 +205,20 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1)
             const uint64_t s0 = ptx::smem_desc(sS, 16u, 128u, ptx::SWIZZLE_NONE);
             uint32_t stage = 0, phase = 0, tile = 0;
             bool ok = true;
-            for (int t = pair; t < p.num_tiles && ok; t += npairs, ++tile) {
+            for (int w, t; ok && f8_schedule((int)tile, pair, npairs, p, w, t); ++tile) {
+                const F8Problem &q = p.prob[w];
+                const uint32_t idesc = q.idesc;
+                const int num_kb = q.num_kb, nk32 = q.nk32;
                 // the shared columns of the previous tile's accumulator are read, and all of the one before it
                 if (tile != 0 && !mx_warp_wait(pp, pp.tempty0, (tile - 1) & 1u)) { ok = false; break; }
                 ptx::tc_fence_after();
                 const uint32_t d = pp.tmem + (tile & 1u) * Cfg::ACC_STRIDE;
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                for (int kb = 0; kb < num_kb; ++kb) {
                     if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
                     ptx::tc_fence_after();
                     ptx::mma_f8_stage_pair(d, a0 + stage * (Cfg::A_BYTES >> 4), b0 + stage * (Cfg::B_BYTES >> 4),
                                            s0 + stage * (Cfg::S_BYTES >> 4), pp.tmem + Cfg::SCALE_COL + stage * Cfg::SLOT_COLS,
-                                           p.idesc | ptx::f8_scale_id(kb), min(4, p.nk32 - 4 * kb), kb != 0 ? 1u : 0u);
+                                           idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), kb != 0 ? 1u : 0u);
                     ptx::commit_elected_pair(pp.empty0 + 8 * stage, 3);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -171,49 +233,19 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1)
         const int q = warp & 3, part = (warp - 2) >> 2;
         const uint32_t buf = base + Cfg::OFF_EPI + (uint32_t)(warp - 2) * 4096u;
         const uint32_t tempty_leader = ptx::mapa(pp.tempty0, 0);
-        const uint64_t pol_c = ptx::createpolicy_evict_first();   // C is not read back here
-        constexpr int NU = 256 / COLS, SHARED = 64 / COLS;       // units of a tile; of the columns that it shares
         uint32_t tile = 0;
-        for (int t = pair; t < p.num_tiles; t += npairs, ++tile) {
+        for (int w, t; f8_schedule((int)tile, pair, npairs, p, w, t); ++tile) {
+            const F8Problem &o = p.prob[w];
             int mb, nb;
-            f8_tile(t, p, mb, nb);
+            f8_tile(t, o, mb, nb);
             if (!warp_epi_wait(pp, pp.tfull0 + 8 * (tile & 1u), (tile >> 1) & 1u)) { pipe_fail(pp); break; }
             ptx::tc_fence_after();
-            const uint32_t tbase = pp.tmem + ((uint32_t)(q * 32) << 16) + (tile & 1u) * Cfg::ACC_STRIDE;
+            const bool upper = (tile & 1u) != 0;
+            const uint32_t tbase = pp.tmem + ((uint32_t)(q * 32) << 16) + (upper ? Cfg::ACC_STRIDE : 0u);
             const int row0 = mb * 256 + (int)rank * 128 + q * 32;
-            // the shared columns are the last of the lower accumulator and the first of the upper one
-            const int first = (tile & 1u) == 0 ? NU - SHARED : 0;
-#pragma unroll 1
-            for (int i = part; i < NU; i += 2) {
-                const int u = (first + i) & (NU - 1);
-                const int col0 = nb * 256 + u * COLS;
-                if (lane == 0) ptx::bulk_wait_read<0>();
-                __syncwarp();
-                mx_epi_unit<OUT>(p.act, tbase + u * COLS, p.bias != nullptr ? p.bias + col0 : nullptr, p.N - col0,
-                                 p.alpha, buf, lane, [&] {
-                                     // The warp's first unit: the shared columns are among the first units
-                                     // of the warps that have them, and every warp is past the tile before.
-                                     if (i != part) return;
-                                     ptx::tc_fence_before();
-                                     __syncwarp();
-                                     if (lane == 0) {
-                                         if (leader) ptx::mbar_arrive(pp.tempty0);
-                                         else ptx::mbar_arrive_cluster(tempty_leader);
-                                     }
-                                 });
-                if (p.c_tma) {
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && row0 < p.M && col0 < p.N) {
-                        ptx::tma_store_2d_hint(&tmC, buf, col0, row0, pol_c);
-                        ptx::bulk_commit();
-                    }
-                } else {
-                    __syncwarp();
-                    mx_store_elements<OUT>(p.C, buf, row0, col0, p.M, p.N, lane);
-                    __syncwarp();
-                }
-            }
+            if (o.out == OUT_F32) f8_epilogue<OUT_F32>(o, mb, nb, rank, upper, part, tbase, buf, lane, row0, pp.tempty0, tempty_leader);
+            else if (o.out == OUT_BF16) f8_epilogue<OUT_BF16>(o, mb, nb, rank, upper, part, tbase, buf, lane, row0, pp.tempty0, tempty_leader);
+            else f8_epilogue<OUT_F16>(o, mb, nb, rank, upper, part, tbase, buf, lane, row0, pp.tempty0, tempty_leader);
         }
         if (lane == 0) ptx::bulk_wait<0>();
         __syncwarp();
@@ -246,34 +278,23 @@ static void pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2],
     cfg.numAttrs = 2;
 }
 
-template <int OUT>
-static cudaError_t launch_f8_pair_t(const F8GemmLaunch &L, cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    pair_config(cfg, attr, L.grid, stream);
-    return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<OUT>, L.tmA, L.tmB, L.tmSA, L.tmSB, L.tmC, L.args);
-}
-
 cudaError_t setup_fp8_pair_kernels(int *max_pairs)
 {
-    const auto attr_of = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_pair_kernel<OUT_BF16>, attr_of, F8PairCfg::SMEM_BYTES);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_fp8_pair_kernel<OUT_F16>, attr_of, F8PairCfg::SMEM_BYTES);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_fp8_pair_kernel<OUT_F32>, attr_of, F8PairCfg::SMEM_BYTES);
+    const cudaError_t e = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F8PairCfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     pair_config(cfg, attr, 2 * 128, nullptr);
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(max_pairs, gemm_fp8_pair_kernel<OUT_BF16>, &cfg);
+    return cudaOccupancyMaxActiveClusters(max_pairs, gemm_fp8_pair_kernel, &cfg);
 }
 
-cudaError_t launch_gemm_fp8_pair(const F8GemmLaunch &L, cudaStream_t stream)
+cudaError_t launch_gemm_fp8_pair(const F8GemmArgs &a, int pairs, cudaStream_t stream)
 {
-    if (L.out == OUT_BF16) return launch_f8_pair_t<OUT_BF16>(L, stream);
-    if (L.out == OUT_F16) return launch_f8_pair_t<OUT_F16>(L, stream);
-    return launch_f8_pair_t<OUT_F32>(L, stream);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    pair_config(cfg, attr, 2 * pairs, stream);
+    return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel, a);
 }
 
 }  // namespace mmact

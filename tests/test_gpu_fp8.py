@@ -333,7 +333,7 @@ def backward(dy, x, wt, grad_type, dw_dtype=torch.float32, want=("dx", "dw", "db
 
 @pytest.mark.parametrize("M,N,K", BACKWARDS)
 @pytest.mark.parametrize("dtype,kind,dwt", [("bf16", "e5m2", "f32"), ("f16", "e4m3", "bf16"), ("f32", "e5m2", "f32")])
-def test_backward(M, N, K, dtype, kind, dwt):
+def test_backward(M, N, K, dtype, kind, dwt, kernel):
     rng = np.random.default_rng(M + 3 * N + K)
     dy = tensor(rng.normal(0, 1, (M, N)) * np.exp2(rng.integers(-4, 5, (M, 1))), dtype)
     x = tensor(rng.normal(0, 1, (M, K)), dtype)
@@ -347,6 +347,25 @@ def test_backward(M, N, K, dtype, kind, dwt):
     want, bound = mx.gemm(ref.quantize(gy.T, kind)[2], ref.quantize(gx.T, "e4m3")[2], None, "none", 0.0)
     check(dw, want, bound, dwt)
     check(db[None], gy.sum(axis=0)[None], mx.sum_error(M) * np.abs(gy).sum(axis=0)[None], "f32")
+
+
+@pytest.mark.parametrize("M,N,K", [(2900, 1500, 2600), (700, 5000, 2300), (6000, 2400, 1030), (20000, 600, 300)])
+@pytest.mark.parametrize("dwt", [torch.float32, torch.float16])
+def test_backward_large(M, N, K, dwt):
+    """Both products in one launch, several tiles for each CTA pair, either one the longer."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    dy, x, w = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((M, N), (M, K), (N, K)))
+    wt = quantized(w, "e4m3", True, transposed=True)
+    dx, dw, db = backward(dy, x, wt, F8["e4m3"], dwt)
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+    a, b = values64(*quantized(dy), M, N), values64(*wt, K, N)
+    at, xt = values64(*quantized(dy, transposed=True), N, M), values64(*quantized(x, transposed=True), K, M)
+    for got, l, r, half in ((dx, a, b, 2.0 ** -8), (dw, at, xt, 0.0 if dwt is torch.float32 else 2.0 ** -11)):
+        want = l @ r.t()
+        bound = mx.sum_error(l.shape[1]) * (l.abs() @ r.abs().t())
+        assert bool(((got.double() - want).abs() <= bound + half * (want.abs() + bound)).all())
+    want = dy.double().sum(dim=0)
+    assert bool(((db - want).abs() <= mx.sum_error(M) * dy.double().abs().sum(dim=0)).all())
 
 
 def test_backward_of_the_wanted_gradients_only():
