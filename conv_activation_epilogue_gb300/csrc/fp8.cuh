@@ -122,14 +122,14 @@ __host__ __device__ constexpr uint32_t idesc_f8(int a, int b, int M, int N)
 __device__ __forceinline__ uint32_t f8_scale_id(int kb) { return ((uint32_t)(kb & 3) << 4) | ((uint32_t)(kb & 3) << 29); }
 
 // One ring stage of 128 K over a CTA pair (issued in the even CTA by the whole warp,
-// one elected lane): the scale tiles of the CTA's A rows (512 bytes at `s`) and of all B
-// rows (two tiles behind it) to 12 columns of tensor memory from `ts` on, B's first;
-// then a K = 32 MMA for each 32 bytes of the operands' rows, `n` of them.
+// one elected lane): with `copy`, the scale tiles of the CTA's A rows (512 bytes at `s`)
+// and of all B rows (two tiles behind it) to 12 columns of tensor memory from `ts` on,
+// B's first; then a K = 32 MMA for each 32 bytes of the operands' rows, `n` of them.
 __device__ __forceinline__ void mma_f8_stage_pair(uint32_t d, uint64_t a, uint64_t b, uint64_t s, uint32_t ts, uint32_t id,
-                                                  int n, uint32_t accumulate)
+                                                  int n, uint32_t accumulate, uint32_t copy)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q, n1, n2, n3;\n\t.reg .b64 a1, a2, a3, b1, b2, b3, s1, s2;\n\t"
+        "{\n\t.reg .pred p, q, c, n1, n2, n3;\n\t.reg .b64 a1, a2, a3, b1, b2, b3, s1, s2;\n\t"
         ".reg .b32 t1, t2;\n\t"
         "setp.ne.b32 p, %7, 0;\n\t"
         "add.s64 s1, %3, 32;\n\tadd.s64 s2, %3, 64;\n\t"
@@ -137,16 +137,17 @@ __device__ __forceinline__ void mma_f8_stage_pair(uint32_t d, uint64_t a, uint64
         "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
         "add.s32 t1, %4, 4;\n\tadd.s32 t2, %4, 8;\n\t"
         "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.and.b32 c, %8, 0, q;\n\t"
         "setp.gt.and.s32 n1, %6, 1, q;\n\tsetp.gt.and.s32 n2, %6, 2, q;\n\tsetp.gt.and.s32 n3, %6, 3, q;\n\t"
-        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%4], s1;\n\t"
-        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [t1], s2;\n\t"
-        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [t2], %3;\n\t"
+        "@c tcgen05.cp.cta_group::2.32x128b.warpx4 [%4], s1;\n\t"
+        "@c tcgen05.cp.cta_group::2.32x128b.warpx4 [t1], s2;\n\t"
+        "@c tcgen05.cp.cta_group::2.32x128b.warpx4 [t2], %3;\n\t"
         "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %5, [t2], [%4], p;\n\t"
         "@n1 tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a1, b1, %5, [t2], [%4], 1;\n\t"
         "@n2 tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a2, b2, %5, [t2], [%4], 1;\n\t"
         "@n3 tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a3, b3, %5, [t2], [%4], 1;\n\t"
         "}" ::"r"(d),
-        "l"(a), "l"(b), "l"(s), "r"(ts), "r"(id), "r"(n), "r"(accumulate)
+        "l"(a), "l"(b), "l"(s), "r"(ts), "r"(id), "r"(n), "r"(accumulate), "r"(copy)
         : "memory");
 }
 

@@ -3,14 +3,16 @@
 // 256 x 256 tiles on CTA pairs, tcgen05.mma.cta_group::2.kind::mxf8f6f4.
 //
 // A ring stage is 128 K of the CTA's 128 rows of A and 128 rows of B (16 KB each, by TMA
-// with the 128-byte swizzle) and their scale tiles, which hold the scales of 512 K: the
-// stage's instructions pick its byte of them.  The issuer copies the tiles into tensor
-// memory (tcgen05.cp) ahead of the stage's MMAs.
+// with the 128-byte swizzle).  A scale tile holds the scales of 512 K: every fourth
+// stage brings the tiles of its own A rows and of all B rows, the MMA issuer copies them
+// into tensor memory (tcgen05.cp) ahead of the stage's MMAs, and the instructions of the
+// four stages pick their byte.
 //
-// Tensor memory: two 256-column accumulators that overlap by 64 columns (0..255 and
-// 192..447), then 12 columns of scales for each ring stage, which are free when the
-// stage is.  The epilogue of a tile takes the shared columns first and lets the next
-// tile's MMAs start as soon as they are in registers, before it works on them.
+// Tensor memory: two 256-column accumulators that overlap by 32 columns (0..255 and
+// 224..479), then two slots of 12 columns of scales.  Copies and MMAs of one issuer run
+// in order, so a slot is free again when its next copy comes.  The epilogue of a tile
+// takes the shared columns first and lets the next tile's MMAs start as soon as they are
+// in registers, before it works on them.
 //
 // Two products that do not depend on each other (a linear layer's two gradients) can share
 // one launch: the pairs go on from the tiles of the one to the tiles of the other, instead
@@ -37,7 +39,7 @@ struct F8PairCfg {
     static constexpr int EPI_WARPS = 8, EPI_BYTES = EPI_WARPS * 4096;
     static constexpr int STAGES = 5;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-    static constexpr uint32_t ACC_STRIDE = 192, SCALE_COL = 448, SLOT_COLS = 12, TMEM_COLS = 512;
+    static constexpr uint32_t ACC_STRIDE = 224, SCALE_COL = 480, SLOT_COLS = 12, TMEM_COLS = 512;
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
     static constexpr int OFF_EPI = OFF_B + STAGES * B_BYTES;
@@ -46,7 +48,7 @@ struct F8PairCfg {
     static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 4) * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16;
     static_assert(SMEM_BYTES <= CTA_SMEM && SMEM_BYTES >= tmem_min_smem((int)TMEM_COLS), "shared memory budget");
-    static_assert(SCALE_COL + STAGES * SLOT_COLS <= TMEM_COLS, "tensor memory budget");
+    static_assert(SCALE_COL + 2 * SLOT_COLS <= TMEM_COLS && SCALE_COL >= ACC_STRIDE + 256, "tensor memory budget");
 };
 
 // Tile t of a product -> (M block, N block) of 256 x 256, grouped M-first.
@@ -84,10 +86,10 @@ __device__ __forceinline__ void f8_epilogue(const F8Problem &p, int mb, int nb, 
                                             uint32_t buf, int lane, int row0, uint32_t tempty, uint32_t tempty_leader)
 {
     constexpr int COLS = OUT == OUT_F32 ? 32 : 64;
-    constexpr int NU = 256 / COLS, SHARED = 64 / COLS;        // units of a tile; of the columns that it shares
+    constexpr int NU = 256 / COLS;                            // units of a tile
     const uint64_t pol_c = ptx::createpolicy_evict_first();   // C is not read back here
     // the shared columns are the last of the lower accumulator and the first of the upper one
-    const int first = upper ? 0 : NU - SHARED;
+    const int first = upper ? 0 : NU - 1;
 #pragma unroll 1
     for (int i = part; i < NU; i += 2) {
         const int u = (first + i) & (NU - 1);
@@ -95,8 +97,8 @@ __device__ __forceinline__ void f8_epilogue(const F8Problem &p, int mb, int nb, 
         if (lane == 0) ptx::bulk_wait_read<0>();
         __syncwarp();
         mx_epi_unit<OUT>(p.act, tbase + u * COLS, p.bias != nullptr ? p.bias + col0 : nullptr, p.N - col0, p.alpha, buf, lane, [&] {
-            // The warp's first unit: the shared columns are among the first units of the warps that have them,
-            // and every warp is past the tile before.
+            // The warp's first unit: the shared columns are the first unit of the warps that have them, and every
+            // warp is past the tile before.
             if (i != part) return;
             ptx::tc_fence_before();
             __syncwarp();
@@ -188,12 +190,15 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1) gemm_fp8_pair_kernel(co
                 for (int kb = 0; kb < q.num_kb; ++kb) {
                     if (!pipe_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) { ok = false; break; }
                     const uint32_t fb = pp.full0 + 8 * stage;
-                    if (leader) ptx::mbar_arrive_expect_tx(fb, 2u * Cfg::STAGE_BYTES);
+                    const bool scales = (kb & 3) == 0;
+                    if (leader) ptx::mbar_arrive_expect_tx(fb, 2u * (scales ? Cfg::STAGE_BYTES : Cfg::A_BYTES + Cfg::B_BYTES));
                     const uint32_t to = ptx::mapa(fb, 0);
                     ptx::tma_load_2d_pair(sA + stage * Cfg::A_BYTES, &q.tmA, to, kb * 64, mb * 256 + (int)rank * 128);
                     ptx::tma_load_2d_pair(sB + stage * Cfg::B_BYTES, &q.tmB, to, kb * 64, nb * 256 + (int)rank * 128);
-                    ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES, &q.tmSA, to, (kb >> 2) * 128, mb * 2 + (int)rank);
-                    ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES + 512u, &q.tmSB, to, (kb >> 2) * 128, nb * 2);
+                    if (scales) {
+                        ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES, &q.tmSA, to, (kb >> 2) * 128, mb * 2 + (int)rank);
+                        ptx::tma_load_2d_pair(sS + stage * Cfg::S_BYTES + 512u, &q.tmSB, to, (kb >> 2) * 128, nb * 2);
+                    }
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1) gemm_fp8_pair_kernel(co
         if (leader) {                                         // the whole warp: see mma_mxf4
             const uint64_t a0 = ptx::smem_desc(sA, 16u, 1024u, ptx::SWIZZLE_128B), b0 = ptx::smem_desc(sB, 16u, 1024u, ptx::SWIZZLE_128B);
             const uint64_t s0 = ptx::smem_desc(sS, 16u, 128u, ptx::SWIZZLE_NONE);
-            uint32_t stage = 0, phase = 0, tile = 0;
+            uint32_t stage = 0, phase = 0, tile = 0, slot = 0;
             bool ok = true;
             for (int w, t; ok && f8_schedule((int)tile, pair, npairs, p, w, t); ++tile) {
                 const F8Problem &q = p.prob[w];
@@ -216,9 +221,11 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1) gemm_fp8_pair_kernel(co
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
                     ptx::tc_fence_after();
+                    const bool scales = (kb & 3) == 0;
+                    if (scales) slot ^= 1u;
                     ptx::mma_f8_stage_pair(d, a0 + stage * (Cfg::A_BYTES >> 4), b0 + stage * (Cfg::B_BYTES >> 4),
-                                           s0 + stage * (Cfg::S_BYTES >> 4), pp.tmem + Cfg::SCALE_COL + stage * Cfg::SLOT_COLS,
-                                           idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), kb != 0 ? 1u : 0u);
+                                           s0 + stage * (Cfg::S_BYTES >> 4), pp.tmem + Cfg::SCALE_COL + slot * Cfg::SLOT_COLS,
+                                           idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), kb != 0 ? 1u : 0u, scales ? 1u : 0u);
                     ptx::commit_elected_pair(pp.empty0 + 8 * stage, 3);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
