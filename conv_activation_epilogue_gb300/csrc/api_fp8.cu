@@ -97,7 +97,9 @@ bool f8_encode(CUtensorMap *mc, CUtensorMap *ms, const F8Matrix &m, int64_t rows
 struct F8Plan {
     bool pair, quantize;             // quantize: x first, by a kernel of its own
     F8Problem P;
-    F8RowsLaunch R;
+    F8RowsProblem R;                 // but its bt-wide tiles, which the launch lays out
+    F8Matrix A, B;
+    int x_type;                      // OUT_* of R.x; < 0: A is quantised
 };
 
 // Whether a product runs on the pair kernel: when the rows kernel would have more
@@ -124,6 +126,9 @@ mmact_status f8_gemm_plan(F8Plan &plan, const F8Matrix &A, const F8Matrix &B, co
     if (st != MMACT_OK) return st;
     const int nk32 = (int)((K + 31) / 32), num_kb = (int)f8_blocks(K);
     plan.pair = f8_choose_pair(c, M, N);
+    plan.A = A;
+    plan.B = B;
+    plan.x_type = -1;
     plan.quantize = x != nullptr && plan.pair;
     if (plan.pair) {
         F8Problem &L = plan.P;
@@ -152,63 +157,106 @@ mmact_status f8_gemm_plan(F8Plan &plan, const F8Matrix &A, const F8Matrix &B, co
         }
         return MMACT_OK;
     }
-    F8RowsLaunch &L = plan.R;
-    std::memset(&L, 0, sizeof(L));
-    F8RowsArgs &a = L.args;
+    F8RowsProblem &a = plan.R;
+    std::memset(&a, 0, sizeof(a));
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
     a.nk32 = nk32;
     a.num_kb = num_kb;
     a.tiles_n = (int)((N + 127) / 128);
-    const int sms = c.dev.sm_count;
-    // the narrowest tile that takes every row (a narrower one than 128 has to be the only one)
-    int bt = 16;
-    while (bt < 128 && bt < M) bt *= 2;
-    const int64_t tiles = a.tiles_n * ((M + bt - 1) / bt);
-    if (tiles * 8 > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
-    // CTAs to a tile: as long as that leaves no cluster waiting for SMs and each CTA two K blocks
-    int split = 1, log2 = 0;
-    while (split < 8 && tiles * split * 2 <= sms && tiles <= c.max_clusters[log2 + 1] && num_kb >= split * 2) split *= 2, ++log2;
-    a.kb_per = (num_kb + split - 1) / split;
-    while (split > 1 && (split - 1) * a.kb_per >= num_kb) split /= 2, a.kb_per = (num_kb + split - 1) / split;
-    a.stages = std::min(F8_ROWS_STAGES(bt), a.kb_per);
-    a.split = split;
     a.act = (int)act;
+    a.out = out_kind(cd);
     a.alpha = alpha;
     a.bias = bias;
     a.C = C;
-    // the operands change sides: B's rows are the instruction's A
-    a.idesc = ptx::idesc_f8(f8_kind(B.type), f8_kind(A.type), 128, bt);
-    a.status = c.dev.status;
-    a.wait_ns = c.dev.wait_ns;
-    L.out = out_kind(cd);
-    L.bt = bt;
-    L.grid = (int)(tiles * split);
-    L.x_type = -1;
+    if ((int64_t)a.tiles_n * ((M + 15) / 16) * 8 > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
     plan.quantize = x != nullptr && M > F8_FUSED_ROWS;
-    if (!f8_encode(&L.tmW, &L.tmSW, B, N, K, 128, 1)) return MMACT_ERR_CUDA;
     if (x != nullptr && !plan.quantize) {
         a.x = x;
-        L.x_type = out_kind(x_type);
-        return MMACT_OK;
+        plan.x_type = out_kind(x_type);
     }
-    return f8_encode(&L.tmT, &L.tmST, A, M, K, (uint32_t)bt, 1) ? MMACT_OK : MMACT_ERR_CUDA;
+    return MMACT_OK;
+}
+
+// K blocks of a CTA from which on the rings are deep, so that an SM holds one CTA.  Measured
+// for 1 and 16 rows: 64 of 128 weight rows' tiles of K = 8192 (32 K blocks a CTA) 15.8 and 17.6
+// us with rings of ten stages, 16.1 and 19.2 with five and two CTAs to an SM; 16 tiles of the same
+// K 9.0 and 8.0, 64 tiles of K = 2048 7.4 and 6.9.
+constexpr int F8_DEEP_KB = 24;
+
+// Lays out the tiles of one or two products on the rows kernel.
+mmact_status f8_rows_layout(F8RowsLaunch &L, const F8Context &c, const F8Plan &one, const F8Plan *two)
+{
+    std::memset(&L, 0, sizeof(L));
+    F8RowsArgs &a = L.args;
+    a.prob[0] = one.R;
+    if (two != nullptr) a.prob[1] = two->R;
+    const int n = two != nullptr ? 2 : 1, sms = c.dev.sm_count;
+    // the narrowest tile that takes every row (a narrower one than 128 has to be the only one)
+    int bt = 16, num_kb = a.prob[0].num_kb;
+    int64_t tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        while (bt < 128 && bt < a.prob[i].M) bt *= 2;
+        num_kb = std::min(num_kb, a.prob[i].num_kb);
+    }
+    for (int i = 0; i < n; ++i) {
+        a.prob[i].num_tiles = a.prob[i].tiles_n * ((a.prob[i].M + bt - 1) / bt);
+        tiles += a.prob[i].num_tiles;
+    }
+    if (tiles * 8 > MAX_DIM) return MMACT_ERR_UNSUPPORTED;
+    // CTAs to a tile: as long as that leaves no cluster waiting for SMs and each CTA two K blocks;
+    // of few rows and short K blocks, two CTAs to an SM.
+    int split = 1, log2 = 0;
+    while (split < 8 && tiles * split * 2 <= sms && tiles <= c.max_clusters[log2 + 1] && num_kb >= split * 4) split *= 2, ++log2;
+    if (bt == 16)
+        while (split < 8 && tiles * split * 2 <= 2 * sms && num_kb >= split * 4 && num_kb < split * F8_DEEP_KB) split *= 2;
+    // no CTA without a K block
+    auto idle = [&](int s) {
+        for (int i = 0; i < n; ++i) {
+            const int kb = a.prob[i].num_kb, per = (kb + s - 1) / s;
+            if ((s - 1) * per >= kb) return true;
+        }
+        return false;
+    };
+    while (split > 1 && idle(split)) split /= 2;
+    int most = 0;
+    for (int i = 0; i < n; ++i) {
+        F8RowsProblem &p = a.prob[i];
+        F8RowsMaps &m = a.maps[i];
+        const F8Plan &plan = i == 0 ? one : *two;
+        p.kb_per = (p.num_kb + split - 1) / split;
+        most = std::max(most, p.kb_per);
+        // the operands change sides: B's rows are the instruction's A
+        p.idesc = ptx::idesc_f8(f8_kind(plan.B.type), f8_kind(plan.A.type), 128, bt);
+        if (!f8_encode(&m.tmW, &m.tmSW, plan.B, p.N, p.K, 128, 1)) return MMACT_ERR_CUDA;
+        if (plan.x_type < 0 && !f8_encode(&m.tmT, &m.tmST, plan.A, p.M, p.K, (uint32_t)bt, 1)) return MMACT_ERR_CUDA;
+    }
+    a.stages = std::min(bt <= 32 && most < F8_DEEP_KB ? 5 : F8_ROWS_STAGES(bt), most);
+    a.split = split;
+    a.status = c.dev.status;
+    a.wait_ns = c.dev.wait_ns;
+    L.bt = bt;
+    L.x_type = one.x_type;
+    L.grid = (int)(tiles * split);
+    return MMACT_OK;
 }
 
 // Launches a product, or two that do not depend on each other (`other`, or null).
 mmact_status f8_gemm_launch(const F8Plan &plan, const F8Plan *other, cudaStream_t stream)
 {
-    if (!plan.pair || (other != nullptr && !other->pair)) {
-        mmact_status s = MMACT_OK;
-        if (other != nullptr) s = f8_gemm_launch(*other, nullptr, stream);
-        if (s != MMACT_OK) return s;
-        if (!plan.pair) return enqueued(launch_gemm_fp8_rows(plan.R, stream));
-        other = nullptr;
-    }
     F8Context c;
-    const mmact_status s = f8_context(&c);
+    mmact_status s = f8_context(&c);
     if (s != MMACT_OK) return s;
+    if (other != nullptr && plan.pair != other->pair) {
+        s = f8_gemm_launch(plan, nullptr, stream);
+        return s == MMACT_OK ? f8_gemm_launch(*other, nullptr, stream) : s;
+    }
+    if (!plan.pair) {
+        F8RowsLaunch L;
+        s = f8_rows_layout(L, c, plan, other);
+        return s == MMACT_OK ? enqueued(launch_gemm_fp8_rows(L, stream)) : s;
+    }
     F8GemmArgs a;
     std::memset(&a, 0, sizeof(a));
     // the one with the longer tiles first: the others fill the last round

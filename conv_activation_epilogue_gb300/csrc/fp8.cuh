@@ -151,29 +151,28 @@ __device__ __forceinline__ void mma_f8_stage_pair(uint32_t d, uint64_t a, uint64
         : "memory");
 }
 
-// The same on one CTA: 128 rows (A) by a tile (B) of at most 128, A's scale tile, then
-// B's, to 8 columns from `ts` on.
-__device__ __forceinline__ void mma_f8_stage(uint32_t d, uint64_t a, uint64_t b, uint64_t s, uint32_t ts, uint32_t id, int n,
-                                             uint32_t accumulate)
+// The same on one CTA: 128 rows (A) by a tile (B) of at most 128, A's scale tile (at `sa`),
+// then B's (`sb`), to 8 columns from `ts` on.
+__device__ __forceinline__ void mma_f8_stage(uint32_t d, uint64_t a, uint64_t b, uint64_t sa, uint64_t sb, uint32_t ts,
+                                             uint32_t id, int n, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q, n1, n2, n3;\n\t.reg .b64 a1, a2, a3, b1, b2, b3, s1;\n\t"
+        "{\n\t.reg .pred p, q, n1, n2, n3;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
         ".reg .b32 t1;\n\t"
         "setp.ne.b32 p, %7, 0;\n\t"
-        "add.s64 s1, %3, 32;\n\t"
         "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
         "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
         "add.s32 t1, %4, 4;\n\t"
         "elect.sync _|q, 0xffffffff;\n\t"
         "setp.gt.and.s32 n1, %6, 1, q;\n\tsetp.gt.and.s32 n2, %6, 2, q;\n\tsetp.gt.and.s32 n3, %6, 3, q;\n\t"
         "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], %3;\n\t"
-        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [t1], s1;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [t1], %8;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %5, [%4], [t1], p;\n\t"
         "@n1 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a1, b1, %5, [%4], [t1], 1;\n\t"
         "@n2 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a2, b2, %5, [%4], [t1], 1;\n\t"
         "@n3 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a3, b3, %5, [%4], [t1], 1;\n\t"
         "}" ::"r"(d),
-        "l"(a), "l"(b), "l"(s), "r"(ts), "r"(id), "r"(n), "r"(accumulate)
+        "l"(a), "l"(b), "l"(sa), "r"(ts), "r"(id), "r"(n), "r"(accumulate), "l"(sb)
         : "memory");
 }
 

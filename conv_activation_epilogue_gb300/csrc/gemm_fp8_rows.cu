@@ -14,10 +14,13 @@
 // tile narrower than 128 rows is always the only one, because the MMA takes no
 // scale address that is not a multiple of four columns.
 //
+// Two products that do not depend on each other (a linear layer's two gradients) can share
+// one launch.
+//
 //   warp 0      TMA producer: a ring of stages of 128 K (codes with the 128-byte
-//               swizzle, scale tiles).  While the kernel before this one in the
-//               stream still runs (it may be writing A's codes) the CTA already
-//               asks for its first 16 weight boxes in L2.
+//               swizzle, scale tiles).  (Asking for the first weight boxes in L2 while
+//               the kernel before this one still runs gained nothing: 32 x 4096 x 4096
+//               8.2 us with it, 7.3 without.)
 //   warp 1      TMEM allocation, scale copies into columns of the ring stage, MMAs
 //   warps 2..5  partial tile, reduction, epilogue
 //   warps 6..9  when A arrives as x in 16 or 32 bits, up to 8 rows: they quantise
@@ -38,13 +41,13 @@ namespace mmact {
 // A stage to a warp, so that four stages' loads are in flight; 32 values to a lane, four
 // lanes a row.
 template <int XT, int BT>
-__device__ __forceinline__ void quantize_f8_stages(const F8RowsArgs &p, const Pipe &pp, uint32_t sT, uint32_t sS, int kb0, int kb1)
+__device__ __forceinline__ void quantize_f8_stages(const F8RowsProblem &p, const Pipe &pp, int stages, uint32_t sT, uint32_t sS, int kb0, int kb1)
 {
     using Cfg = F8RowsCfg<BT>;
     const int w = (int)(threadIdx.x >> 5) - 6, lane = threadIdx.x & 31, row = lane >> 2, q0 = lane & 3;
     const bool vec = (int64_t)p.K * (XT == IN_F32 ? 4 : 2) % 16 == 0;
     for (int kb = kb0 + w, i = w; kb < kb1; kb += 4, i += 4) {
-        const uint32_t stage = (uint32_t)(i % p.stages), phase = (uint32_t)(i / p.stages) & 1u;
+        const uint32_t stage = (uint32_t)(i % stages), phase = (uint32_t)(i / stages) & 1u;
         const int k0 = kb * 128 + q0 * 32, n = min(32, p.K - k0);
         Raw8<XT> r[4];
 #pragma unroll
@@ -101,24 +104,27 @@ constexpr int X_CODES = -1;          // A comes as codes and scales
 template <int XT>
 constexpr int F8_ROWS_THREADS = XT == X_CODES ? 192 : 320;
 
-template <int OUT, int BT, int XT>
-__global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
-    gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
-                           const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmST,
-                           const F8RowsArgs p)
+template <int BT, int XT>
+__global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(const __grid_constant__ F8RowsArgs args)
 {
     using Cfg = F8RowsCfg<BT>;
-    const int stages = p.stages;
+    const int stages = args.stages, split = args.split;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = ptx::smem_addr(smem);
-    const int rank = p.split > 1 ? (int)ptx::cluster_ctarank() : 0;
-    const int tile = blockIdx.x / p.split;
+    const int rank = split > 1 ? (int)ptx::cluster_ctarank() : 0;
+    int tile = blockIdx.x / split;
+    const bool second = XT == X_CODES && tile >= args.prob[0].num_tiles;
+    if (second) tile -= args.prob[0].num_tiles;
+    const F8RowsProblem &p = args.prob[second ? 1 : 0];
+    const F8RowsMaps &maps = args.maps[second ? 1 : 0];
+    const uint32_t idesc = p.idesc;
+    const int nk32 = p.nk32;
     const int nb = tile % p.tiles_n, tb = tile / p.tiles_n;
     const int kb0 = rank * p.kb_per, kb1 = min(p.num_kb, kb0 + p.kb_per);
 
     const bool aligned = (base & 1023u) == 0;
-    if (!aligned && threadIdx.x == 0) atomicOr(p.status, ST_SMEM_ALIGN);
+    if (!aligned && threadIdx.x == 0) atomicOr(args.status, ST_SMEM_ALIGN);
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + Cfg::OFF_MISC);
     Pipe pp;
     pp.full0 = base + Cfg::OFF_BAR;
@@ -127,12 +133,12 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
     pp.drain = pp.tfull0 + 8;
     pp.tempty0 = 0;
     pp.abort = misc + 1;
-    pp.status = p.status;
-    pp.wait_ns = p.wait_ns;
+    pp.status = args.status;
+    pp.wait_ns = args.wait_ns;
     if (aligned) {
         if (threadIdx.x == 0) {
-            ptx::prefetch_tensormap(&tmW);
-            if constexpr (XT == X_CODES) ptx::prefetch_tensormap(&tmT);
+            ptx::prefetch_tensormap(&maps.tmW);
+            if constexpr (XT == X_CODES) ptx::prefetch_tensormap(&maps.tmT);
             for (int s = 0; s < stages; ++s) {
                 ptx::mbar_init(pp.full0 + 8 * s, XT == X_CODES ? 1 : 2);   // + a quantising warp
                 ptx::mbar_init(pp.empty0 + 8 * s, 1);
@@ -141,10 +147,6 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
             ptx::mbar_init(pp.drain, 1);
             misc[1] = 0;
             ptx::fence_mbar_init();
-            for (int kb = kb0; kb < min(kb1, kb0 + 16); ++kb) {
-                ptx::tma_prefetch_2d(&tmW, kb * 64, nb * 128);
-                if (kb == kb0 || (kb & 3) == 0) ptx::tma_prefetch_2d(&tmSW, (kb >> 2) * 128, nb);
-            }
         }
     }
     ptx::cta_sync();
@@ -176,11 +178,11 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
                 if (!pipe_wait(pp, pp.empty0 + 8 * stage, phase ^ 1u)) { ok = false; break; }
                 const uint32_t fb = pp.full0 + 8 * stage;
                 ptx::mbar_arrive_expect_tx(fb, (uint32_t)(XT == X_CODES ? Cfg::STAGE_BYTES : Cfg::W_BYTES + 512));
-                ptx::tma_load_2d(sW + stage * Cfg::W_BYTES, &tmW, fb, kb * 64, nb * 128);
-                ptx::tma_load_2d(sS + stage * Cfg::S_BYTES, &tmSW, fb, (kb >> 2) * 128, nb);
+                ptx::tma_load_2d(sW + stage * Cfg::W_BYTES, &maps.tmW, fb, kb * 64, nb * 128);
+                ptx::tma_load_2d(sS + stage * Cfg::S_BYTES, &maps.tmSW, fb, (kb >> 2) * 128, nb);
                 if constexpr (XT == X_CODES) {
-                    ptx::tma_load_2d(sT + stage * Cfg::T_BYTES, &tmT, fb, kb * 64, tb * BT);
-                    ptx::tma_load_2d(sS + stage * Cfg::S_BYTES + 512u, &tmST, fb, (kb >> 2) * 128, tb);
+                    ptx::tma_load_2d(sT + stage * Cfg::T_BYTES, &maps.tmT, fb, kb * 64, tb * BT);
+                    ptx::tma_load_2d(sS + stage * Cfg::S_BYTES + 512u, &maps.tmST, fb, (kb >> 2) * 128, tb);
                 }
                 if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
             }
@@ -199,8 +201,8 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
                 if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
                 ptx::tc_fence_after();
                 ptx::mma_f8_stage(pp.tmem, w0 + stage * (Cfg::W_BYTES >> 4), t0 + stage * (Cfg::T_BYTES >> 4),
-                                  s0 + stage * (Cfg::S_BYTES >> 4), pp.tmem + Cfg::SCALE_COL + stage * 8u,
-                                  p.idesc | ptx::f8_scale_id(kb), min(4, p.nk32 - 4 * kb), kb > kb0 ? 1u : 0u);
+                                  s0 + stage * (Cfg::S_BYTES >> 4), s0 + stage * (Cfg::S_BYTES >> 4) + 32u, pp.tmem + Cfg::SCALE_COL + stage * 8u,
+                                  idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), kb > kb0 ? 1u : 0u);
                 ptx::commit_elected(pp.empty0 + 8 * stage);
                 if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
             }
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
         }
     }
     if constexpr (XT != X_CODES) {
-        if (aligned && warp >= 6) quantize_f8_stages<XT, BT>(p, pp, sT, sS, kb0, kb1);
+        if (aligned && warp >= 6) quantize_f8_stages<XT, BT>(p, pp, stages, sT, sS, kb0, kb1);
     }
     __syncwarp();
     // The epilogue warps take part in cluster barriers with the others below, so
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
         ptx::tc_fence_after();
     }
     const uint32_t taddr = pp.tmem + ((uint32_t)(q * 32) << 16);
-    if (p.split == 1) {
+    if (split == 1) {
         if (epi && good) {
 #pragma unroll 1
             for (int c = 0; c < BT; c += 16) {
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
                 ptx::tmem_ld16(taddr + c, r);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(r[j]);
-                rows_store<OUT>(p, tb * BT + c, n, z, bias);
+                rows_store(p, p.out, tb * BT + c, n, z, bias);
                 __syncwarp();
             }
         }
@@ -257,15 +259,15 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
         ptx::cluster_sync();
         if (epi && good) {
             // this CTA's slice of the columns that exist: 16 at a time, or the 2 to 8 it has
-            const int rows = min(BT, p.M - tb * BT), even = ((rows + p.split - 1) / p.split + 15) & ~15;
-            const int cols = min(BT / p.split, even), c0 = rank * cols;
+            const int rows = min(BT, p.M - tb * BT), even = ((rows + split - 1) / split + 15) & ~15;
+            const int cols = min(BT / split, even), c0 = rank * cols;
             const uint32_t at = base + Cfg::OFF_RING + (uint32_t)(c0 * 128 + q * 32 + lane) * 4u;
             auto slice = [&](auto ch) {
                 constexpr int CH = decltype(ch)::value;
                 for (int c = 0; c < cols && tb * BT + c0 + c < p.M; c += CH) {
                     float z[CH];
-                    cluster_columns<CH>(at + c * 512u, p.split, z);
-                    rows_store<OUT>(p, tb * BT + c0 + c, n, z, bias);
+                    cluster_columns<CH>(at + c * 512u, split, z);
+                    rows_store(p, p.out, tb * BT + c0 + c, n, z, bias);
                 }
             };
             if (cols >= 16) slice(std::integral_constant<int, 16>());
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1)
     }
 }
 
-template <int OUT, int BT, int XT>
+template <int BT, int XT>
 static cudaError_t launch_rows_t(const F8RowsLaunch &L, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
@@ -301,64 +303,38 @@ static cudaError_t launch_rows_t(const F8RowsLaunch &L, cudaStream_t stream)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.args.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemm_fp8_rows_kernel<OUT, BT, XT>, L.tmW, L.tmT, L.tmSW, L.tmST, L.args);
+    return cudaLaunchKernelEx(&cfg, gemm_fp8_rows_kernel<BT, XT>, L.args);
 }
 
-template <int OUT, int BT>
-static cudaError_t launch_rows_x(const F8RowsLaunch &L, cudaStream_t stream)
+cudaError_t launch_gemm_fp8_rows(const F8RowsLaunch &L, cudaStream_t stream)
 {
-    if (L.x_type == IN_BF16) return launch_rows_t<OUT, BT, IN_BF16>(L, stream);
-    if (L.x_type == IN_F16) return launch_rows_t<OUT, BT, IN_F16>(L, stream);
-    if (L.x_type == IN_F32) return launch_rows_t<OUT, BT, IN_F32>(L, stream);
-    return launch_rows_t<OUT, BT, X_CODES>(L, stream);
-}
-
-template <int OUT>
-static cudaError_t launch_rows_o(const F8RowsLaunch &L, cudaStream_t stream)
-{
+    if (L.x_type == IN_BF16) return launch_rows_t<16, IN_BF16>(L, stream);
+    if (L.x_type == IN_F16) return launch_rows_t<16, IN_F16>(L, stream);
+    if (L.x_type == IN_F32) return launch_rows_t<16, IN_F32>(L, stream);
     switch (L.bt) {
-    case 16: return launch_rows_x<OUT, 16>(L, stream);
-    case 32: return launch_rows_t<OUT, 32, X_CODES>(L, stream);
-    case 64: return launch_rows_t<OUT, 64, X_CODES>(L, stream);
-    default: return launch_rows_t<OUT, 128, X_CODES>(L, stream);
+    case 16: return launch_rows_t<16, X_CODES>(L, stream);
+    case 32: return launch_rows_t<32, X_CODES>(L, stream);
+    case 64: return launch_rows_t<64, X_CODES>(L, stream);
+    default: return launch_rows_t<128, X_CODES>(L, stream);
     }
 }
 
-template <int OUT, int BT, int XT>
+template <int BT, int XT>
 static cudaError_t setup_rows_t()
 {
-    return cudaFuncSetAttribute(gemm_fp8_rows_kernel<OUT, BT, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                F8RowsCfg<BT>::OFF_RING + F8RowsCfg<BT>::MAX_STAGES * F8RowsCfg<BT>::STAGE_BYTES);
+    using Cfg = F8RowsCfg<BT>;
+    return cudaFuncSetAttribute(gemm_fp8_rows_kernel<BT, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Cfg::OFF_RING + Cfg::MAX_STAGES * Cfg::STAGE_BYTES);
 }
 
-template <int OUT, int BT>
-static cudaError_t setup_rows_x()
-{
-    cudaError_t e = setup_rows_t<OUT, BT, X_CODES>();
-    if (e == cudaSuccess) e = setup_rows_t<OUT, BT, IN_BF16>();
-    if (e == cudaSuccess) e = setup_rows_t<OUT, BT, IN_F16>();
-    if (e == cudaSuccess) e = setup_rows_t<OUT, BT, IN_F32>();
-    return e;
-}
-
-template <int OUT>
-static cudaError_t setup_rows_o()
-{
-    cudaError_t e = setup_rows_x<OUT, 16>();
-    if (e == cudaSuccess) e = setup_rows_t<OUT, 32, X_CODES>();
-    if (e == cudaSuccess) e = setup_rows_t<OUT, 64, X_CODES>();
-    if (e == cudaSuccess) e = setup_rows_t<OUT, 128, X_CODES>();
-    return e;
-}
-
-// Clusters of `split` CTAs that are resident at once (with a full ring).
-template <int BT>
+// Clusters of `split` CTAs that are resident at once (with full rings).
 static cudaError_t rows_clusters(int split, int *n)
 {
+    using Cfg = F8RowsCfg<128>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(split * 64));
-    cfg.blockDim = dim3(192);
-    cfg.dynamicSmemBytes = F8RowsCfg<BT>::OFF_RING + F8RowsCfg<BT>::MAX_STAGES * F8RowsCfg<BT>::STAGE_BYTES;
+    cfg.blockDim = dim3(F8_ROWS_THREADS<X_CODES>);
+    cfg.dynamicSmemBytes = Cfg::OFF_RING + Cfg::MAX_STAGES * Cfg::STAGE_BYTES;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)split;
@@ -366,24 +342,21 @@ static cudaError_t rows_clusters(int split, int *n)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(n, gemm_fp8_rows_kernel<OUT_BF16, BT, X_CODES>, &cfg);
+    return cudaOccupancyMaxActiveClusters(n, gemm_fp8_rows_kernel<128, X_CODES>, &cfg);
 }
 
 cudaError_t setup_fp8_rows_kernels(int (&max_clusters)[4])
 {
-    cudaError_t e = setup_rows_o<OUT_BF16>();
-    if (e == cudaSuccess) e = setup_rows_o<OUT_F16>();
-    if (e == cudaSuccess) e = setup_rows_o<OUT_F32>();
+    cudaError_t e = setup_rows_t<16, X_CODES>();
+    if (e == cudaSuccess) e = setup_rows_t<32, X_CODES>();
+    if (e == cudaSuccess) e = setup_rows_t<64, X_CODES>();
+    if (e == cudaSuccess) e = setup_rows_t<128, X_CODES>();
+    if (e == cudaSuccess) e = setup_rows_t<16, IN_BF16>();
+    if (e == cudaSuccess) e = setup_rows_t<16, IN_F16>();
+    if (e == cudaSuccess) e = setup_rows_t<16, IN_F32>();
     max_clusters[0] = 1 << 30;
-    for (int i = 1; i < 4 && e == cudaSuccess; ++i) e = rows_clusters<128>(1 << i, &max_clusters[i]);
+    for (int i = 1; i < 4 && e == cudaSuccess; ++i) e = rows_clusters(1 << i, &max_clusters[i]);
     return e;
-}
-
-cudaError_t launch_gemm_fp8_rows(const F8RowsLaunch &L, cudaStream_t stream)
-{
-    if (L.out == OUT_BF16) return launch_rows_o<OUT_BF16>(L, stream);
-    if (L.out == OUT_F16) return launch_rows_o<OUT_F16>(L, stream);
-    return launch_rows_o<OUT_F32>(L, stream);
 }
 
 }  // namespace mmact

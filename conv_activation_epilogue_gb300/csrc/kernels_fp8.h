@@ -60,28 +60,39 @@ cudaError_t launch_gemm_fp8_pair(const F8GemmArgs &a, int pairs, cudaStream_t st
 
 // The same product with few rows or tiles: W = B's rows on the MMA's 128 lanes,
 // T = A's rows on its columns, the K blocks of a tile shared by a cluster.
-struct F8RowsArgs {
+struct F8RowsProblem {
     int M, N, K;
-    const void *x;       // A not yet quantised [M, K], or null
     int nk32, num_kb;    // as above
     int tiles_n;         // tiles of 128 rows of B
-    int split, kb_per;   // CTAs of a tile's cluster, K blocks of each
-    int stages;          // of the ring
-    int act;
+    int num_tiles;
+    int kb_per;          // K blocks of a CTA of the tile's cluster
+    int act, out;
     float alpha;
-    const float *bias;
-    void *C;
     uint32_t idesc;      // operand formats, 128 x bt
+    const float *bias;
+    const void *x;       // A not yet quantised [M, K], or null
+    void *C;
+};
+
+struct F8RowsMaps {
+    CUtensorMap tmW, tmT, tmSW, tmST;
+};
+
+// One product, or two that do not depend on each other.  What every thread reads is
+// together at the front: the first reads of a kernel's arguments miss.
+struct F8RowsArgs {
+    int split;           // CTAs of a tile's cluster
+    int stages;          // of the ring
     unsigned int *status;
     unsigned long long wait_ns;
+    F8RowsProblem prob[2];
+    F8RowsMaps maps[2];
 };
 
 struct F8RowsLaunch {
-    CUtensorMap tmW, tmT, tmSW, tmST;
     F8RowsArgs args;
-    int out;
     int bt;              // rows of A in a tile: 16, 32, 64 or 128
-    int x_type;          // OUT_* of args.x; < 0: A is tmT, tmST
+    int x_type;          // OUT_* of the first product's x; < 0: its A is tmT, tmST
     int grid;
 };
 

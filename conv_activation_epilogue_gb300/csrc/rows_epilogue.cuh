@@ -9,14 +9,11 @@
 
 namespace mmact {
 
-// C[m0 + j][n] = act(z[j] + bias) for this lane's n and the rows that exist:
-// element stores, a warp covering 32 consecutive n.
+// C[m0 + j][n] = z[j] for this lane's n and the rows that exist: element stores, a warp
+// covering 32 consecutive n.
 template <int OUT, int CH, typename Args>
-__device__ __forceinline__ void rows_store(const Args &p, int m0, int n, float (&z)[CH], float bias)
+__device__ __forceinline__ void rows_write(const Args &p, int m0, int n, const float (&z)[CH])
 {
-#pragma unroll
-    for (int j = 0; j < CH; ++j) z[j] += bias;
-    act_mx_all(p.act, z, p.alpha);
     if (n >= p.N) return;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
@@ -26,6 +23,32 @@ __device__ __forceinline__ void rows_store(const Args &p, int m0, int n, float (
         else if constexpr (OUT == OUT_BF16) static_cast<__nv_bfloat16 *>(p.C)[at] = __float2bfloat16_rn(z[j]);
         else static_cast<__half *>(p.C)[at] = __float2half_rn(z[j]);
     }
+}
+
+// act(z[j] + bias)
+template <int CH, typename Args>
+__device__ __forceinline__ void rows_activate(const Args &p, float (&z)[CH], float bias)
+{
+#pragma unroll
+    for (int j = 0; j < CH; ++j) z[j] += bias;
+    act_mx_all(p.act, z, p.alpha);
+}
+
+template <int OUT, int CH, typename Args>
+__device__ __forceinline__ void rows_store(const Args &p, int m0, int n, float (&z)[CH], float bias)
+{
+    rows_activate(p, z, bias);
+    rows_write<OUT>(p, m0, n, z);
+}
+
+// The same with the output's type at run time.
+template <int CH, typename Args>
+__device__ __forceinline__ void rows_store(const Args &p, int out, int m0, int n, float (&z)[CH], float bias)
+{
+    rows_activate(p, z, bias);
+    if (out == OUT_F32) rows_write<OUT_F32>(p, m0, n, z);
+    else if (out == OUT_BF16) rows_write<OUT_BF16>(p, m0, n, z);
+    else rows_write<OUT_F16>(p, m0, n, z);
 }
 
 // Sum of CH columns of the cluster's partial tiles at this thread's lane, in rank
