@@ -93,6 +93,9 @@ bool f8_encode(CUtensorMap *mc, CUtensorMap *ms, const F8Matrix &m, int64_t rows
            encode_tensor_map(ms, MMACT_F32, 2, m.scales, ds, ss, bs, false);
 }
 
+// K blocks whose products an accumulator takes when the output is fp32 (gemm_fp8.cu).
+constexpr int F8_CHUNK_KB = 32;
+
 // Plan of one product: either kernel's launch.
 struct F8Plan {
     bool pair, quantize;             // quantize: x first, by a kernel of its own
@@ -137,6 +140,7 @@ mmact_status f8_gemm_plan(F8Plan &plan, const F8Matrix &A, const F8Matrix &B, co
         L.N = (int)N;
         L.nk32 = nk32;
         L.num_kb = num_kb;
+        L.chunk_kb = cd == MMACT_F32 ? F8_CHUNK_KB : (num_kb + 3) & ~3;
         L.tiles_m = (int)((M + 255) / 256);
         L.tiles_n = (int)((N + 255) / 256);
         L.num_tiles = L.tiles_m * L.tiles_n;
@@ -211,6 +215,9 @@ mmact_status f8_rows_layout(F8RowsLaunch &L, const F8Context &c, const F8Plan &o
     while (split < 8 && tiles * split * 2 <= sms && tiles <= c.max_clusters[log2 + 1] && num_kb >= split * 4) split *= 2, ++log2;
     if (bt == 16)
         while (split < 8 && tiles * split * 2 <= 2 * sms && num_kb >= split * 4 && num_kb < split * F8_DEEP_KB) split *= 2;
+    // fp32 outputs: K in as many accumulators as the cluster allows
+    for (int i = 0; i < n; ++i)
+        while (a.prob[i].out == OUT_F32 && split < 8 && a.prob[i].num_kb > split * F8_CHUNK_KB) split *= 2;
     // no CTA without a K block
     auto idle = [&](int s) {
         for (int i = 0; i < n; ++i) {

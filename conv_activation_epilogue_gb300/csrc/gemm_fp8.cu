@@ -14,6 +14,12 @@
 // takes the shared columns first and lets the next tile's MMAs start as soon as they are
 // in registers, before it works on them.
 //
+// The tensor core cuts off what an addition to the accumulator has below its last bit
+// (2^-24 of the sum and up, always towards zero: sums of 8192 positive products came out
+// 3.9e-6 too small).  Far below a 16-bit output's rounding; for fp32 outputs a tile's K is
+// summed in chunks of 4096, each in a fresh accumulator, and the epilogue's warps add the chunks up in
+// registers, rounded.
+//
 // Two products that do not depend on each other (a linear layer's two gradients) can share
 // one launch: the pairs go on from the tiles of the one to the tiles of the other, instead
 // of waiting twice for the slowest.
@@ -122,6 +128,74 @@ __device__ __forceinline__ void f8_epilogue(const F8Problem &p, int mb, int nb, 
     }
 }
 
+// The epilogue of one tile in several chunks of K, fp32 output: the warp's 32 rows and
+// every other 32 columns (units u = 2 k + part).  `chunk` counts the accumulators used
+// so far.  False when a wait ran out.
+__device__ __forceinline__ bool f8_epilogue_chunks(const F8Problem &p, const Pipe &pp, uint32_t &chunk, int chunks, int nb, uint32_t rank,
+                                                   int part, uint32_t tmem, uint32_t buf, int lane, int row0,
+                                                   uint32_t tempty_leader)
+{
+    const uint64_t pol_c = ptx::createpolicy_evict_first();
+    float sum[4][32];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[k][j] = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c, ++chunk) {
+        if (!warp_epi_wait(pp, pp.tfull0 + 8 * (chunk & 1u), (chunk >> 1) & 1u)) return false;
+        ptx::tc_fence_after();
+        const uint32_t base = tmem + (chunk & 1u) * F8PairCfg::ACC_STRIDE + part * 32;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // the shared columns are the first or the last unit
+            const int k = i < 2 ? 0 : (i < 4 ? 3 : i / 2 - 1), h = (i & 1) * 16;
+            uint32_t r[16];
+            ptx::tmem_ld16(base + 64 * k + h, r);
+            if (i == 3) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) ptx::mbar_arrive(pp.tempty0);
+                    else ptx::mbar_arrive_cluster(tempty_leader);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[k][h + j] += __uint_as_float(r[j]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int col0 = nb * 256 + 64 * k + 32 * part;
+        if (lane == 0) ptx::bulk_wait_read<0>();
+        __syncwarp();
+        if (p.bias != nullptr)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[k][j] += col0 + j < p.N ? p.bias[col0 + j] : 0.0f;
+        act_mx_all(p.act, sum[k], p.alpha);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            ptx::st_shared_v4(buf + (uint32_t)lane * 128u + (((uint32_t)c ^ (uint32_t)(lane & 7)) << 4), __float_as_uint(sum[k][4 * c]),
+                              __float_as_uint(sum[k][4 * c + 1]), __float_as_uint(sum[k][4 * c + 2]), __float_as_uint(sum[k][4 * c + 3]));
+        if (p.c_tma) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < p.M && col0 < p.N) {
+                ptx::tma_store_2d_hint(&p.tmC, buf, col0, row0, pol_c);
+                ptx::bulk_commit();
+            }
+        } else {
+            __syncwarp();
+            mx_store_elements<OUT_F32>(p.C, buf, row0, col0, p.M, p.N, lane);
+            __syncwarp();
+        }
+    }
+    return true;
+}
+
+// CHUNKS: some product sums its K in several accumulators (its sums take the epilogue's
+// registers, 9728 x 8192 x 512 in bf16 55 us with it, 51 without).
+template <bool CHUNKS>
 __global__ void __launch_bounds__(F8PairCfg::THREADS, 1) gemm_fp8_pair_kernel(const __grid_constant__ F8GemmArgs p)
 {
     using Cfg = F8PairCfg;
@@ -210,27 +284,31 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1) gemm_fp8_pair_kernel(co
             const uint64_t s0 = ptx::smem_desc(sS, 16u, 128u, ptx::SWIZZLE_NONE);
             uint32_t stage = 0, phase = 0, tile = 0, slot = 0;
             bool ok = true;
+            uint32_t chunk = 0;                                // accumulators used so far
             for (int w, t; ok && f8_schedule((int)tile, pair, npairs, p, w, t); ++tile) {
                 const F8Problem &q = p.prob[w];
                 const uint32_t idesc = q.idesc;
-                const int num_kb = q.num_kb, nk32 = q.nk32;
-                // the shared columns of the previous tile's accumulator are read, and all of the one before it
-                if (tile != 0 && !mx_warp_wait(pp, pp.tempty0, (tile - 1) & 1u)) { ok = false; break; }
-                ptx::tc_fence_after();
-                const uint32_t d = pp.tmem + (tile & 1u) * Cfg::ACC_STRIDE;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                const int num_kb = q.num_kb, nk32 = q.nk32, chunk_kb = q.chunk_kb;
+                for (int kb = 0, left = 0; kb < num_kb; ++kb, --left) {
+                    const uint32_t d = pp.tmem + (chunk & 1u) * Cfg::ACC_STRIDE;
+                    const bool begin = left == 0;
+                    if (begin) {
+                        left = min(chunk_kb, num_kb - kb);
+                        // the shared columns of the previous accumulator are read, and all of the one before it
+                        if (chunk != 0 && !mx_warp_wait(pp, pp.tempty0, (chunk - 1) & 1u)) { ok = false; break; }
+                        ptx::tc_fence_after();
+                    }
                     if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
                     ptx::tc_fence_after();
                     const bool scales = (kb & 3) == 0;
                     if (scales) slot ^= 1u;
                     ptx::mma_f8_stage_pair(d, a0 + stage * (Cfg::A_BYTES >> 4), b0 + stage * (Cfg::B_BYTES >> 4),
                                            s0 + stage * (Cfg::S_BYTES >> 4), pp.tmem + Cfg::SCALE_COL + slot * Cfg::SLOT_COLS,
-                                           idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), kb != 0 ? 1u : 0u, scales ? 1u : 0u);
+                                           idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), begin ? 0u : 1u, scales ? 1u : 0u);
                     ptx::commit_elected_pair(pp.empty0 + 8 * stage, 3);
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (left == 1) ptx::commit_elected_pair(pp.tfull0 + 8 * (chunk++ & 1u), 3);
                 }
-                if (!ok) break;
-                ptx::commit_elected_pair(pp.tfull0 + 8 * (tile & 1u), 3);
             }
             if (!ok && lane == 0) pipe_fail(pp);
             ptx::commit_elected_pair(pp.drain, 1);
@@ -240,16 +318,28 @@ __global__ void __launch_bounds__(F8PairCfg::THREADS, 1) gemm_fp8_pair_kernel(co
         const int q = warp & 3, part = (warp - 2) >> 2;
         const uint32_t buf = base + Cfg::OFF_EPI + (uint32_t)(warp - 2) * 4096u;
         const uint32_t tempty_leader = ptx::mapa(pp.tempty0, 0);
-        uint32_t tile = 0;
+        uint32_t tile = 0, chunk = 0;
         for (int w, t; f8_schedule((int)tile, pair, npairs, p, w, t); ++tile) {
             const F8Problem &o = p.prob[w];
             int mb, nb;
             f8_tile(t, o, mb, nb);
-            if (!warp_epi_wait(pp, pp.tfull0 + 8 * (tile & 1u), (tile >> 1) & 1u)) { pipe_fail(pp); break; }
-            ptx::tc_fence_after();
-            const bool upper = (tile & 1u) != 0;
-            const uint32_t tbase = pp.tmem + ((uint32_t)(q * 32) << 16) + (upper ? Cfg::ACC_STRIDE : 0u);
+            const uint32_t lanes = pp.tmem + ((uint32_t)(q * 32) << 16);
             const int row0 = mb * 256 + (int)rank * 128 + q * 32;
+            if constexpr (CHUNKS) {
+                if (o.num_kb > o.chunk_kb) {
+                    const int chunks = (o.num_kb + o.chunk_kb - 1) / o.chunk_kb;
+                    if (!f8_epilogue_chunks(o, pp, chunk, chunks, nb, rank, part, lanes, buf, lane, row0, tempty_leader)) {
+                        pipe_fail(pp);
+                        break;
+                    }
+                    continue;
+                }
+            }
+            if (!warp_epi_wait(pp, pp.tfull0 + 8 * (chunk & 1u), (chunk >> 1) & 1u)) { pipe_fail(pp); break; }
+            ptx::tc_fence_after();
+            const bool upper = (chunk & 1u) != 0;
+            const uint32_t tbase = lanes + (upper ? Cfg::ACC_STRIDE : 0u);
+            ++chunk;
             if (o.out == OUT_F32) f8_epilogue<OUT_F32>(o, mb, nb, rank, upper, part, tbase, buf, lane, row0, pp.tempty0, tempty_leader);
             else if (o.out == OUT_BF16) f8_epilogue<OUT_BF16>(o, mb, nb, rank, upper, part, tbase, buf, lane, row0, pp.tempty0, tempty_leader);
             else f8_epilogue<OUT_F16>(o, mb, nb, rank, upper, part, tbase, buf, lane, row0, pp.tempty0, tempty_leader);
@@ -287,13 +377,15 @@ static void pair_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2],
 
 cudaError_t setup_fp8_pair_kernels(int *max_pairs)
 {
-    const cudaError_t e = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F8PairCfg::SMEM_BYTES);
+    const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_pair_kernel<false>, smem, F8PairCfg::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_fp8_pair_kernel<true>, smem, F8PairCfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     pair_config(cfg, attr, 2 * 128, nullptr);
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(max_pairs, gemm_fp8_pair_kernel, &cfg);
+    return cudaOccupancyMaxActiveClusters(max_pairs, gemm_fp8_pair_kernel<true>, &cfg);
 }
 
 cudaError_t launch_gemm_fp8_pair(const F8GemmArgs &a, int pairs, cudaStream_t stream)
@@ -301,7 +393,8 @@ cudaError_t launch_gemm_fp8_pair(const F8GemmArgs &a, int pairs, cudaStream_t st
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     pair_config(cfg, attr, 2 * pairs, stream);
-    return cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel, a);
+    const bool chunks = a.prob[0].num_kb > a.prob[0].chunk_kb || (a.tiles[1] != 0 && a.prob[1].num_kb > a.prob[1].chunk_kb);
+    return cudaLaunchKernelEx(&cfg, chunks ? gemm_fp8_pair_kernel<true> : gemm_fp8_pair_kernel<false>, a);
 }
 
 }  // namespace mmact

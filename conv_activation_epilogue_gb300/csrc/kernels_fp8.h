@@ -37,6 +37,7 @@ struct F8Problem {
     int M, N;
     int nk32;            // K steps of 32 (one instruction each) that hold values
     int tiles_m, tiles_n, num_tiles, num_kb;   // num_kb: K blocks of 128 (one ring stage each)
+    int chunk_kb;        // of these summed in one accumulator: a multiple of 4
     int group_m;
     int act, out;        // out: OUT_* of C
     float alpha;

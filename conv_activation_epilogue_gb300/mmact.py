@@ -566,40 +566,63 @@ def mmact_fp8_size(rows: int, K: int) -> tuple[int, int]:
 _F8 = (torch.float8_e4m3fn, torch.float8_e5m2)
 
 
-def _fp8_ptrs(codes, scales, rows: int, K: int, name: str):
+def _device(first, name: str) -> int:
+    """The current device, asked for when a call's first tensor lies on any."""
+    if not isinstance(first, torch.Tensor) or first.get_device() < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return _CUR_DEVICE() if _CUR_DEVICE is not None else torch.cuda.current_device()
+
+
+def _on(t, name: str, dtype, dev: int) -> int:
+    """Pointer of a contiguous tensor of that dtype on device `dev`, the current one (its stream gets the
+    kernels): one line for what is right, as small calls take no longer than their checks."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, (dtype,))
+    raise ValueError(f"{name} is on device {t.get_device()}, the current one is {dev}")
+
+
+def _matrix_on(t, name: str, dev: int):
+    """(pointer, dtype code, rows, columns) of a contiguous 2-D tensor of floats on device `dev`."""
+    p, code, rows, cols = _matrix(t, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the current one is {dev}")
+    return p, code, rows, cols
+
+
+def _bias_on(bias, n: int, dev: int):
+    if bias is None:
+        return None
+    p = _on(bias, "bias", torch.float32, dev)
+    if bias.numel() != n:
+        raise ValueError(f"bias must have {n} elements")
+    return p
+
+
+def _fp8_ptrs(codes, scales, rows: int, K: int, name: str, dev: int):
     # the sizes of mmact_fp8_size; the codes' dtype is the format; _dev says what else is wrong
     code = FP8_DTYPE.get(codes.dtype) if isinstance(codes, torch.Tensor) else None
-    if code is None or not codes.is_cuda or not codes.is_contiguous():
+    if code is None:
         _dev(codes, name + " codes", _F8)
-    _dev(scales, name + " scales", _BYTES)
+    pc, ps = _on(codes, name + " codes", codes.dtype, dev), _on(scales, name + " scales", torch.uint8, dev)
     if codes.numel() != rows * ((K + 15) // 16 * 16):
         raise ValueError(f"{name} codes must hold {rows} x {(K + 15) // 16 * 16} bytes")
     if scales.numel() != (rows + 127) // 128 * ((K + 511) // 512) * 512:
         raise ValueError(f"{name} scales must hold {(rows + 127) // 128} x {(K + 511) // 512} tiles of 512 bytes")
-    return codes.data_ptr(), scales.data_ptr(), code
-
-
-def _here(first, *rest) -> None:
-    """The tensors of a call lie on one device, the current one: its stream gets the kernels."""
-    dev = first.get_device()
-    if dev != (_CUR_DEVICE() if _CUR_DEVICE is not None else torch.cuda.current_device()):
-        raise ValueError(f"tensors on device {dev}, which is not the current one")
-    for t in rest:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on devices {dev} and {t.get_device()}")
+    return pc, ps, code
 
 
 def mmact_quantize_fp8(x, codes, scales, block_rows: int = 1, transposed: bool = False, stream=None) -> None:
     """Quantise x [rows, K] (or, transposed, [K, rows]) to 8 bits with a scale for 128 values along K,
     or (block_rows 128) for 128 x 128; codes is a float8_e4m3fn or float8_e5m2 tensor and scales a uint8
     tensor of mmact_fp8_size(rows, K) bytes."""
-    px, dt, rows, K = _matrix(x, "x")
+    dev = _device(x, "x")
+    px, dt, rows, K = _matrix_on(x, "x", dev)
     if transposed:
         rows, K = K, rows
-    pc, ps, kind = _fp8_ptrs(codes, scales, rows, K, "x")
+    pc, ps, kind = _fp8_ptrs(codes, scales, rows, K, "x", dev)
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    _here(x, codes, scales)
     s = (_lib or load()).mmact_quantize_fp8(px, pc, ps, rows, K, dt, kind, block_rows, 1 if transposed else 0,
                                             _stream_handle(stream))
     if s:
@@ -608,9 +631,9 @@ def mmact_quantize_fp8(x, codes, scales, block_rows: int = 1, transposed: bool =
 
 def mmact_dequantize_fp8(codes, scales, y, stream=None) -> None:
     """y [rows, K] = the values of an 8-bit matrix."""
-    py, dt, rows, K = _matrix(y, "y")
-    pc, ps, kind = _fp8_ptrs(codes, scales, rows, K, "y")
-    _here(y, codes, scales)
+    dev = _device(codes, "codes")
+    py, dt, rows, K = _matrix_on(y, "y", dev)
+    pc, ps, kind = _fp8_ptrs(codes, scales, rows, K, "y", dev)
     s = (_lib or load()).mmact_dequantize_fp8(pc, ps, py, rows, K, kind, dt, _stream_handle(stream))
     if s:
         _check(s, "mmact_dequantize_fp8")
@@ -619,12 +642,11 @@ def mmact_dequantize_fp8(codes, scales, y, stream=None) -> None:
 def mmact_gemm_fp8(a_codes, a_scales, b_codes, b_scales, bias, C, K: int, act: str = "none", alpha: float = 0.0,
                    stream=None) -> None:
     """C = act(A @ B.T + bias) of 8-bit matrices A [M, K] and B [N, K]; C [M, N]."""
-    pc, dt, M, N = _matrix(C, "C")
-    pa, psa, ka = _fp8_ptrs(a_codes, a_scales, M, K, "A")
-    pb, psb, kb = _fp8_ptrs(b_codes, b_scales, N, K, "B")
-    pbias = _bias_ptr(bias, N)
-    _here(C, a_codes, a_scales, b_codes, b_scales, bias)
-    s = (_lib or load()).mmact_gemm_fp8(pa, psa, pb, psb, pbias, pc, M, N, K, ka, kb, dt, ACT[act], alpha,
+    dev = _device(a_codes, "a_codes")
+    pc, dt, M, N = _matrix_on(C, "C", dev)
+    pa, psa, ka = _fp8_ptrs(a_codes, a_scales, M, K, "A", dev)
+    pb, psb, kb = _fp8_ptrs(b_codes, b_scales, N, K, "B", dev)
+    s = (_lib or load()).mmact_gemm_fp8(pa, psa, pb, psb, _bias_on(bias, N, dev), pc, M, N, K, ka, kb, dt, ACT[act], alpha,
                                         _stream_handle(stream))
     if s:
         _check(s, "mmact_gemm_fp8")
@@ -645,17 +667,16 @@ def mmact_linear_fp8_workspace_bytes(M: int, K: int) -> int:
 def mmact_linear_fp8(x, w_codes, w_scales, bias, C, workspace, act: str = "none", alpha: float = 0.0,
                      stream=None) -> None:
     """C = act(q(x) @ W.T + bias): x [M, K] is quantised to E4M3 on the way in, W [N, K] is held in 8 bits."""
-    px, xd, M, K = _matrix(x, "x")
-    pc, cd, rows, N = _matrix(C, "C")
+    dev = _device(x, "x")
+    px, xd, M, K = _matrix_on(x, "x", dev)
+    pc, cd, rows, N = _matrix_on(C, "C", dev)
     if rows != M:
         raise ValueError("x must be [M, K] and C [M, N]")
-    pw, ps, kw = _fp8_ptrs(w_codes, w_scales, N, K, "W")
-    pbias = _bias_ptr(bias, N)
-    pws = _dev(workspace, "workspace", _BYTES)
+    pw, ps, kw = _fp8_ptrs(w_codes, w_scales, N, K, "W", dev)
+    pws = _on(workspace, "workspace", torch.uint8, dev)
     if workspace.numel() < -(-M * ((K + 15) // 16 * 16) // 512) * 512 + (M + 127) // 128 * ((K + 511) // 512) * 512:
         raise ValueError("workspace must hold mmact_linear_fp8_workspace_bytes(M, K) bytes")
-    _here(x, C, w_codes, w_scales, bias, workspace)
-    s = (_lib or load()).mmact_linear_fp8(px, pw, ps, pbias, pc, M, N, K, xd, kw, cd, ACT[act], alpha, pws,
+    s = (_lib or load()).mmact_linear_fp8(px, pw, ps, _bias_on(bias, N, dev), pc, M, N, K, xd, kw, cd, ACT[act], alpha, pws,
                                           _stream_handle(stream))
     if s:
         _check(s, "mmact_linear_fp8")
@@ -677,25 +698,29 @@ def mmact_linear_fp8_backward(dy, x, wt_codes, wt_scales, dx, dw, db, workspace,
     """Gradients of x @ W.T + bias in 8 bits (see include/mmact.h): dy [M, N] and x [M, K] of one dtype, Wt
     [K, N] = W turned round in 8 bits; dx [M, K] of x's dtype, dw [N, K], db [N] float32, each may be None.
     dy is quantised to grad_type, x to E4M3."""
-    pdy, xd, M, N = _matrix(dy, "dy")
-    px, xd2, rows, K = _matrix(x, "x")
+    dev = _device(dy, "dy")
+    pdy, xd, M, N = _matrix_on(dy, "dy", dev)
+    px, xd2, rows, K = _matrix_on(x, "x", dev)
     if rows != M or xd2 != xd:
         raise ValueError("dy must be [M, N] and x [M, K] of the same dtype")
     if grad_type not in FP8_DTYPE:
         raise TypeError(f"grad_type {grad_type} not in {_F8}")
-    pdx = pdw = pw = ps = None
+    pdx = pdw = pdb = pw = ps = None
     kw, wd = FP8_DTYPE[torch.float8_e4m3fn], DTYPE[torch.float32]
     if dx is not None:
-        pdx = _dev(dx, "dx", (x.dtype,))
-        if tuple(dx.shape) != (M, K):
+        pdx = _on(dx, "dx", x.dtype, dev)
+        if dx.shape != x.shape:
             raise ValueError("dx must be [M, K]")
-        pw, ps, kw = _fp8_ptrs(wt_codes, wt_scales, K, N, "Wt")
+        pw, ps, kw = _fp8_ptrs(wt_codes, wt_scales, K, N, "Wt", dev)
     if dw is not None:
-        pdw, wd, r, c = _matrix(dw, "dw")
-        if (r, c) != (N, K):
+        pdw, wd, r, c = _matrix_on(dw, "dw", dev)
+        if r != N or c != K:
             raise ValueError("dw must be [N, K]")
-    pdb = _f32_ptr(db, (N,), "db")
-    pws = _dev(workspace, "workspace", _BYTES)
+    if db is not None:
+        pdb = _on(db, "db", torch.float32, dev)
+        if db.dim() != 1 or db.shape[0] != N:
+            raise ValueError("db must be [N]")
+    pws = _on(workspace, "workspace", torch.uint8, dev)
     need = _F8_BACKWARD_WORKSPACE.get((M, N, K))
     if need is None:
         if len(_F8_BACKWARD_WORKSPACE) > 1024:
@@ -703,10 +728,10 @@ def mmact_linear_fp8_backward(dy, x, wt_codes, wt_scales, dx, dw, db, workspace,
         need = _F8_BACKWARD_WORKSPACE[M, N, K] = mmact_linear_fp8_backward_workspace_bytes(M, N, K)
     if workspace.numel() < need:
         raise ValueError(f"workspace must hold {need} bytes")
-    _here(dy, x, dx, dw, db, workspace, *(() if dx is None else (wt_codes, wt_scales)))
-    _check((_lib or load()).mmact_linear_fp8_backward(pdy, px, pw, ps, pdx, pdw, pdb, M, N, K, xd, kw,
-                                                      FP8_DTYPE[grad_type], wd, pws, _stream_handle(stream)),
-           "mmact_linear_fp8_backward")
+    s = (_lib or load()).mmact_linear_fp8_backward(pdy, px, pw, ps, pdx, pdw, pdb, M, N, K, xd, kw, FP8_DTYPE[grad_type], wd,
+                                                   pws, _stream_handle(stream))
+    if s:
+        _check(s, "mmact_linear_fp8_backward")
 
 
 def mmact_moe_workspace_bytes(T: int, H: int, I: int, E: int, top: int) -> int:
@@ -794,23 +819,23 @@ def mmact_moe_route_workspace_bytes(T: int, E: int) -> int:
 _ROUTE_WORKSPACE: dict = {}
 
 
-def _route_args(logits, mask, experts, counts):
-    pz, dt, T, E = _matrix(logits, "logits")
-    pe, pc = _dev(experts, "experts", (torch.int32,)), _dev(counts, "counts", (torch.int32,))
+def _route_args(logits, mask, experts, counts, dev: int):
+    pz, dt, T, E = _matrix_on(logits, "logits", dev)
+    pe, pc = _on(experts, "experts", torch.int32, dev), _on(counts, "counts", torch.int32, dev)
     if experts.dim() != 2 or experts.shape[0] != T:
         raise ValueError("experts must be [T, top]")
     if counts.numel() != E + 1:
         raise ValueError("counts must be [E + 1]")
     pm = None
     if mask is not None:
-        pm = _dev(mask, "mask", (torch.uint8, torch.bool))
-        if tuple(mask.shape) != (T,):
+        pm = _on(mask, "mask", torch.bool if mask.dtype is torch.bool else torch.uint8, dev)
+        if mask.dim() != 1 or mask.shape[0] != T:
             raise ValueError("mask must be [T]")
     return pz, pm, pe, pc, T, E, experts.shape[1], dt
 
 
-def _one_f32(t, name: str):
-    p = _dev(t, name, (torch.float32,))
+def _one_on(t, name: str, dev: int) -> int:
+    p = _on(t, name, torch.float32, dev)
     if t.numel() != 1:
         raise ValueError(f"{name} must have one element")
     return p
@@ -820,11 +845,12 @@ def mmact_moe_route(logits, experts, probs, counts, loss, workspace, coef: float
                     stream=None) -> None:
     """A router in training (see include/mmact.h): from logits [T, E] the outputs experts [T, top] int32, probs
     [T, top] float32, counts [E + 1] int32 and loss [1] float32; mask [T] uint8 or bool leaves out tokens."""
-    pz, pm, pe, pc, T, E, top, dt = _route_args(logits, mask, experts, counts)
-    pp, pl = _dev(probs, "probs", (torch.float32,)), _one_f32(loss, "loss")
+    dev = _device(logits, "logits")
+    pz, pm, pe, pc, T, E, top, dt = _route_args(logits, mask, experts, counts, dev)
+    pp, pl = _on(probs, "probs", torch.float32, dev), _one_on(loss, "loss", dev)
     if probs.shape != experts.shape:
         raise ValueError("experts and probs must be [T, top]")
-    pws = _dev(workspace, "workspace", _BYTES)
+    pws = _on(workspace, "workspace", torch.uint8, dev)
     need = _ROUTE_WORKSPACE.get((T, E))
     if need is None:
         if len(_ROUTE_WORKSPACE) > 1024:
@@ -832,7 +858,6 @@ def mmact_moe_route(logits, experts, probs, counts, loss, workspace, coef: float
         need = _ROUTE_WORKSPACE[T, E] = mmact_moe_route_workspace_bytes(T, E)
     if workspace.numel() < need:
         raise ValueError(f"workspace must hold {need} bytes")
-    _here(logits, mask, experts, probs, counts, loss, workspace)
     s = (_lib or load()).mmact_moe_route(pz, pm, pe, pp, pc, pl, T, E, top, dt, 1 if normalize else 0, coef, pws,
                                          _stream_handle(stream))
     if s:
@@ -843,13 +868,18 @@ def mmact_moe_route_backward(logits, experts, counts, dprobs, dloss, dlogits, co
                              mask=None, stream=None) -> None:
     """The gradient dlogits [T, E] of mmact_moe_route's logits from dprobs [T, top] and dloss [1] (float32, either
     may be None); logits, experts, counts, coef, normalize and mask are the forward pass's."""
-    pz, pm, pe, pc, T, E, top, dt = _route_args(logits, mask, experts, counts)
-    pd = _dev(dlogits, "dlogits", (logits.dtype,))
+    dev = _device(logits, "logits")
+    pz, pm, pe, pc, T, E, top, dt = _route_args(logits, mask, experts, counts, dev)
+    pd = _on(dlogits, "dlogits", logits.dtype, dev)
     if dlogits.shape != logits.shape:
         raise ValueError("dlogits must be [T, E]")
-    pg = _f32_ptr(dprobs, tuple(experts.shape), "dprobs")
-    pl = None if dloss is None else _one_f32(dloss, "dloss")
-    _here(logits, mask, experts, counts, dprobs, dloss, dlogits)
+    pg = pl = None
+    if dprobs is not None:
+        pg = _on(dprobs, "dprobs", torch.float32, dev)
+        if dprobs.shape != experts.shape:
+            raise ValueError("dprobs must be [T, top]")
+    if dloss is not None:
+        pl = _one_on(dloss, "dloss", dev)
     s = (_lib or load()).mmact_moe_route_backward(pz, pm, pe, pc, pg, pl, pd, T, E, top, dt, 1 if normalize else 0, coef,
                                                   _stream_handle(stream))
     if s:

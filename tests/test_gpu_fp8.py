@@ -434,6 +434,23 @@ def test_backward_in_a_graph_on_its_own_workspace():
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 520, 8192), (300, 520, 12345), (2000, 2600, 8192), (200, 8000, 20000)])
+def test_fp32_sums_over_long_k(M, N, K, kernel):
+    """Positive products, so that errors of one sign add up.  Per chunk of 32 K blocks 128 additions of 32 products each may cut
+    off up to 2^-23 of the sum so far, which grows evenly: half of that on average, 64 * 2^-23; then the chunks'
+    additions, rounded.  (Chunks of 4096 K in the pair kernel; clusters of at most 8 on the other.)"""
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    a, b = (torch.rand((r, K), device="cuda", generator=g) for r in (M, N))
+    (ac, as_), (bc, bs) = quantized(a), quantized(b)
+    C = torch.full((M, N), float("nan"), device="cuda")
+    bias = torch.rand(N, device="cuda", generator=g)
+    mmact.mmact_gemm_fp8(ac, as_, bc, bs, bias, C, K, "leaky_relu", 0.5)
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+    want = values64(ac, as_, M, K) @ values64(bc, bs, N, K).t() + bias.double()
+    chunks = -(-K // 4096)
+    assert float(((C.double() - want).abs() / want).max()) <= (64 + chunks + 2) * 2.0 ** -23
+
+
 def test_long_rows_pass_32_bit_offsets():
     """More than 2^31 values: a matrix whose last rows lie past 32-bit byte and element offsets."""
     rows, K = 70000, 32768
