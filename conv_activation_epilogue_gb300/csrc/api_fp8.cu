@@ -93,8 +93,10 @@ bool f8_encode(CUtensorMap *mc, CUtensorMap *ms, const F8Matrix &m, int64_t rows
            encode_tensor_map(ms, MMACT_F32, 2, m.scales, ds, ss, bs, false);
 }
 
-// K blocks whose products an accumulator takes when the output is fp32 (gemm_fp8.cu).
-constexpr int F8_CHUNK_KB = 32;
+// K blocks whose products an accumulator takes when the output is fp32 (gemm_fp8.cu): on
+// the pair kernel, where a new accumulator costs a microsecond, and on the rows kernel,
+// where it costs CTAs.
+constexpr int F8_CHUNK_KB = 16, F8_ROWS_CHUNK_KB = 32;
 
 // Plan of one product: either kernel's launch.
 struct F8Plan {
@@ -217,7 +219,7 @@ mmact_status f8_rows_layout(F8RowsLaunch &L, const F8Context &c, const F8Plan &o
         while (split < 8 && tiles * split * 2 <= 2 * sms && num_kb >= split * 4 && num_kb < split * F8_DEEP_KB) split *= 2;
     // fp32 outputs: K in as many accumulators as the cluster allows
     for (int i = 0; i < n; ++i)
-        while (a.prob[i].out == OUT_F32 && split < 8 && a.prob[i].num_kb > split * F8_CHUNK_KB) split *= 2;
+        while (a.prob[i].out == OUT_F32 && split < 8 && a.prob[i].num_kb > split * F8_ROWS_CHUNK_KB) split *= 2;
     // no CTA without a K block
     auto idle = [&](int s) {
         for (int i = 0; i < n; ++i) {

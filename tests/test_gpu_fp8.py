@@ -299,9 +299,9 @@ def values64(codes, scales, rows, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 520, 8192), (16, 136, 4100), (100, 400, 2500), (1536, 1280, 640), (2816, 2560, 96),
-                                   (130, 8200, 1030), (5000, 40, 2048)])
+                                   (130, 8200, 1030), (5000, 40, 2048), (9, 8192, 8192), (3, 8192, 8192), (16, 2048, 8192)])
 def test_gemm_many_k_blocks_and_many_tiles(M, N, K, kernel):
-    """Rings that go round, several tiles for each CTA pair."""
+    """Rings that go round, deep ones, two CTAs to an SM, several tiles for each CTA pair."""
     g = torch.Generator(device="cuda").manual_seed(M + K)
     a, b = (torch.empty((r, K), device="cuda").normal_(0, 1, generator=g) for r in (M, N))
     (ac, as_), (bc, bs) = quantized(a), quantized(b, "e4m3", True)
@@ -436,9 +436,9 @@ def test_backward_in_a_graph_on_its_own_workspace():
 
 @pytest.mark.parametrize("M,N,K", [(300, 520, 8192), (300, 520, 12345), (2000, 2600, 8192), (200, 8000, 20000)])
 def test_fp32_sums_over_long_k(M, N, K, kernel):
-    """Positive products, so that errors of one sign add up.  Per chunk of 32 K blocks 128 additions of 32 products each may cut
-    off up to 2^-23 of the sum so far, which grows evenly: half of that on average, 64 * 2^-23; then the chunks'
-    additions, rounded.  (Chunks of 4096 K in the pair kernel; clusters of at most 8 on the other.)"""
+    """Positive products, so that errors of one sign add up.  An accumulator takes at most 32 K blocks: 128 additions of
+    32 products, each of which may cut off up to 2^-23 of the sum so far, which grows evenly: half of that on average,
+    64 * 2^-23; then the partial sums' additions and the bias, rounded."""
     g = torch.Generator(device="cuda").manual_seed(M + K)
     a, b = (torch.rand((r, K), device="cuda", generator=g) for r in (M, N))
     (ac, as_), (bc, bs) = quantized(a), quantized(b)
@@ -447,7 +447,7 @@ def test_fp32_sums_over_long_k(M, N, K, kernel):
     mmact.mmact_gemm_fp8(ac, as_, bc, bs, bias, C, K, "leaky_relu", 0.5)
     assert mmact.mmact_get_last_error() == mmact.MMACT_OK
     want = values64(ac, as_, M, K) @ values64(bc, bs, N, K).t() + bias.double()
-    chunks = -(-K // 4096)
+    chunks = -(-K // 2048)
     assert float(((C.double() - want).abs() / want).max()) <= (64 + chunks + 2) * 2.0 ** -23
 
 
