@@ -190,7 +190,7 @@ struct RouteSlots {
 // The choice by picking, for every token of a warp: G lanes, `top` times the largest
 // logit, of equal ones that of the lowest column.
 template <int G, int NV, int PER>
-__device__ __noinline__ void route_pick(const float *z, RouteSlots<G> &my, int l, int top)
+__device__ __forceinline__ void route_pick(const float (&z)[NV], RouteSlots<G> &my, int l, int top)
 {
     uint32_t key[NV];
 #pragma unroll
