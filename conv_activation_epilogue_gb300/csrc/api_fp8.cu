@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -251,35 +252,47 @@ mmact_status f8_rows_layout(F8RowsLaunch &L, const F8Context &c, const F8Plan &o
     return MMACT_OK;
 }
 
-// Launches a product, or two that do not depend on each other (`other`, or null).
-mmact_status f8_gemm_launch(const F8Plan &plan, const F8Plan *other, cudaStream_t stream)
+// What one or two products enqueue: at most one launch of each kernel.
+struct F8Launch {
+    bool rows;
+    int pairs;                       // 0: none of the pair kernel
+    F8GemmArgs P;
+    F8RowsLaunch R;
+};
+
+// Lays out a product, or two that do not depend on each other (`other`, or null).
+mmact_status f8_gemm_layout(F8Launch &L, const F8Plan &plan, const F8Plan *other)
 {
     F8Context c;
-    mmact_status s = f8_context(&c);
+    const mmact_status s = f8_context(&c);
     if (s != MMACT_OK) return s;
-    if (other != nullptr && plan.pair != other->pair) {
-        s = f8_gemm_launch(plan, nullptr, stream);
-        return s == MMACT_OK ? f8_gemm_launch(*other, nullptr, stream) : s;
+    const F8Plan *on[2] = {nullptr, nullptr}, *few[2] = {nullptr, nullptr};    // of the pair kernel; of the rows kernel
+    int non = 0, nfew = 0;
+    for (const F8Plan *q : {&plan, other})
+        if (q != nullptr) (q->pair ? on[non++] : few[nfew++]) = q;
+    L.rows = nfew != 0;
+    L.pairs = 0;
+    if (non != 0) {
+        F8GemmArgs &a = L.P;
+        std::memset(&a, 0, sizeof(a));
+        // the one with the longer tiles first: the others fill the last round
+        if (non == 2 && on[1]->P.num_kb > on[0]->P.num_kb) std::swap(on[0], on[1]);
+        for (int i = 0; i < non; ++i) {
+            a.prob[i] = on[i]->P;
+            a.tiles[i] = a.prob[i].num_tiles;
+        }
+        if (non == 2) a.lead = std::max(1, (a.prob[0].num_kb + a.prob[1].num_kb / 2) / a.prob[1].num_kb);
+        a.status = c.dev.status;
+        a.wait_ns = c.dev.wait_ns;
+        L.pairs = (int)std::min<int64_t>((int64_t)a.tiles[0] + a.tiles[1], c.max_pairs);
     }
-    if (!plan.pair) {
-        F8RowsLaunch L;
-        s = f8_rows_layout(L, c, plan, other);
-        return s == MMACT_OK ? enqueued(launch_gemm_fp8_rows(L, stream)) : s;
-    }
-    F8GemmArgs a;
-    std::memset(&a, 0, sizeof(a));
-    // the one with the longer tiles first: the others fill the last round
-    const bool swap = other != nullptr && other->P.num_kb > plan.P.num_kb;
-    a.prob[0] = swap ? other->P : plan.P;
-    a.tiles[0] = a.prob[0].num_tiles;
-    if (other != nullptr) {
-        a.prob[1] = swap ? plan.P : other->P;
-        a.tiles[1] = a.prob[1].num_tiles;
-        a.lead = std::max(1, (a.prob[0].num_kb + a.prob[1].num_kb / 2) / a.prob[1].num_kb);
-    }
-    a.status = c.dev.status;
-    a.wait_ns = c.dev.wait_ns;
-    return enqueued(launch_gemm_fp8_pair(a, (int)std::min<int64_t>((int64_t)a.tiles[0] + a.tiles[1], c.max_pairs), stream));
+    return nfew != 0 ? f8_rows_layout(L.R, c, *few[0], few[1]) : MMACT_OK;
+}
+
+cudaError_t f8_gemm_launch(const F8Launch &L, cudaStream_t stream)
+{
+    const cudaError_t e = L.pairs != 0 ? launch_gemm_fp8_pair(L.P, L.pairs, stream) : cudaSuccess;
+    return e == cudaSuccess && L.rows ? launch_gemm_fp8_rows(L.R, stream) : e;
 }
 
 cudaError_t quantize_launch(const void *x, const F8Matrix &m, int64_t rows, int64_t K, mmact_dtype xd, bool square,
@@ -376,9 +389,11 @@ MMACT_EXPORT mmact_status mmact_gemm_fp8(const void *a_codes, const void *a_scal
     if (M == 0 || N == 0) return MMACT_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
-    F8Plan L;
-    s = f8_gemm_plan(L, A, B, bias, C, M, N, K, c_dtype, act, alpha);
-    return s == MMACT_OK ? f8_gemm_launch(L, nullptr, st) : s;
+    F8Plan plan;
+    F8Launch L;
+    if ((s = f8_gemm_plan(plan, A, B, bias, C, M, N, K, c_dtype, act, alpha)) != MMACT_OK) return s;
+    if ((s = f8_gemm_layout(L, plan, nullptr)) != MMACT_OK) return s;
+    return enqueued(f8_gemm_launch(L, st));
 }
 
 MMACT_EXPORT mmact_status mmact_set_gemm_fp8_kernel(int mode)
@@ -410,10 +425,12 @@ MMACT_EXPORT mmact_status mmact_linear_fp8(const void *x, const void *w_codes, c
     if (M == 0 || N == 0) return MMACT_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return enqueued(launch_mx_bias_act(bias, C, M, N, out_kind(c_dtype), (int)act, alpha, st));
-    F8Plan L;
-    if ((s = f8_gemm_plan(L, A, W, bias, C, M, N, K, c_dtype, act, alpha, x, x_dtype)) != MMACT_OK) return s;
-    if (L.quantize && (s = enqueued(quantize_launch(x, A, M, K, x_dtype, false, false, st))) != MMACT_OK) return s;
-    return f8_gemm_launch(L, nullptr, st);
+    F8Plan plan;
+    F8Launch L;
+    if ((s = f8_gemm_plan(plan, A, W, bias, C, M, N, K, c_dtype, act, alpha, x, x_dtype)) != MMACT_OK) return s;
+    if ((s = f8_gemm_layout(L, plan, nullptr)) != MMACT_OK) return s;
+    if (plan.quantize && (s = enqueued(quantize_launch(x, A, M, K, x_dtype, false, false, st))) != MMACT_OK) return s;
+    return enqueued(f8_gemm_launch(L, st));
 }
 
 MMACT_EXPORT mmact_status mmact_linear_fp8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t *bytes)
@@ -459,6 +476,9 @@ MMACT_EXPORT mmact_status mmact_linear_fp8_backward(const void *dy, const void *
                                      MMACT_ACT_NONE, 0.0f)) != MMACT_OK)
         return s;
     if (want_dw && (s = f8_gemm_plan(W, gyt, xt, nullptr, dw, N, K, M, dw_dtype, MMACT_ACT_NONE, 0.0f)) != MMACT_OK) return s;
+    F8Launch L;
+    const bool products = want_dx || want_dw;
+    if (products && (s = f8_gemm_layout(L, want_dw ? W : X, want_dw && want_dx ? &X : nullptr)) != MMACT_OK) return s;
     F8Grads g;
     std::memset(&g, 0, sizeof(g));
     g.dy = dy;
@@ -475,6 +495,5 @@ MMACT_EXPORT mmact_status mmact_linear_fp8_backward(const void *dy, const void *
     if (want_db) g.part = part;
     if ((s = enqueued(launch_quantize_fp8_grads(g, out_kind(x_dtype), f8_kind(grad_dtype), st))) != MMACT_OK) return s;
     if (want_db && (s = enqueued(launch_column_sums(part, db, M, N, st))) != MMACT_OK) return s;
-    if (!want_dx && !want_dw) return MMACT_OK;
-    return f8_gemm_launch(want_dw ? W : X, want_dw && want_dx ? &X : nullptr, st);
+    return products ? enqueued(f8_gemm_launch(L, st)) : MMACT_OK;
 }

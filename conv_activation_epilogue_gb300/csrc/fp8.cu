@@ -1,6 +1,8 @@
 // fp8.cu -- quantisation to 8-bit floating point with a scale for each block of 128,
 // and back: streaming kernels, bound by HBM (2 or 4 bytes read and 1.01 written per
-// value, and the other way round).
+// value, and the other way round).  Measured on 8192 x 8192 bf16, inputs in turn: rows to
+// E4M3 29 us (7.0 TB/s, a part of the codes stays in L2), turned round in blocks of 128 x 128
+// and back to values 62.6 (6.45 TB/s).
 #include "common.cuh"
 #include "fp8.cuh"
 #include "kernels_fp8.h"
@@ -325,7 +327,10 @@ __device__ __forceinline__ void store_rows(const uint32_t (&a)[32 * PAIR_WORDS<T
 
 // What the backward pass of a linear layer makes of dy [M, N] and x [M, K], in one
 // launch: dy by rows (for dx), dy turned round and its column sums (dw, db), x turned round
-// (dw): dy is read once.  The first CTAs take tiles of dy, the others of x.
+// (dw): dy is read once.  The first CTAs take tiles of dy, the others of x.  8192 x 4096
+// bf16 of each: 55 us (134 MB read, 101 written: 4.3 TB/s; 35 us at the copy rate): a tile is
+// reduced twice, by rows and by columns, and three CTAs of an SM overlap little of that
+// (two: 67 us).
 template <int T, int F8>
 __global__ void __launch_bounds__(256, T == IN_F32 ? 2 : 3) quantize_f8_grads_kernel(const F8Grads g)
 {

@@ -30,6 +30,11 @@
 //   warp 1      TMEM allocation; in the even CTA the scale copies and the MMAs
 //   warps 2..9  (both CTAs) epilogue of the CTA's 128 rows, two warps for each 32
 //
+// Bound by the tensor pipe and, called for longer, the power cap.  Measured with calls back
+// to back, LeakyReLU, bf16 out: 8192 x 8192 x 8192 306 to 313 us (3.5 to 3.6 PFLOP/s; a stage takes 336
+// ns, and about a microsecond passes between tiles; after seconds of it 356 to 364),
+// 4096 x 4096 x 4096 45.3 us, 9728 x 8192 x 512 51 us.
+//
 // Every wait is bounded, and both CTAs pass a final cluster barrier before TMEM
 // is released.
 #include "common.cuh"

@@ -26,6 +26,11 @@
 //   warps 6..9  when A arrives as x in 16 or 32 bits, up to 8 rows: they quantise
 //               its stages into the ring, where the codes would have been copied,
 //               which saves a kernel of its own
+//
+// Bound by the weights' bytes and about 5 us of fixed parts (start, first loads, the
+// cluster's sum, stores).  Measured with weights from HBM: 1 x 8192 x 8192 with x quantised inside
+// 15.5 us, 16 rows 14.4 (67 MB: 4.7 TB/s), 128 rows 18; 32, 64, 128 x 4096 x 4096 7.3,
+// 8.5, 9.9 us.
 #include <type_traits>
 
 #include "common.cuh"

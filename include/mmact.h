@@ -672,7 +672,8 @@ mmact_status mmact_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t *byt
  *                           depends on M alone
  * dy is quantised to grad_dtype (E4M3 or E5M2), x to E4M3.  Each of dx, dw and db may
  * be NULL and is then not computed; each other one is overwritten.  Products over
- * an empty dimension are zeros.  The outputs must not overlap the inputs.
+ * an empty dimension are zeros.  dy, x, Wt's arrays, dx, dw and workspace are 16-byte
+ * aligned; the outputs must not overlap the inputs or each other.
  *   workspace  at least mmact_linear_fp8_backward_workspace_bytes, as above.
  */
 mmact_status mmact_linear_fp8_backward(const void *dy, const void *x, const void *wt_codes, const void *wt_scales,
@@ -754,9 +755,10 @@ mmact_status mmact_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t *byte
  * coef too.  The choice and the counts are constants:
  *   dlogits[t] = softmax's derivative, at logits[t], of
  *                dprobs . probs + dloss * coef * E / (n^2 top) * counts . softmax
- *   dlogits [T, E] in logits_dtype, overwritten; rows of tokens left out, or with
- *          nothing but -inf, are 0.  Slots outside 0..E-1 count as -1; an expert twice
- *          among a token's slots adds up.
+ *   dlogits [T, E] in logits_dtype, 16-byte aligned, overwritten; rows of tokens left
+ *          out, or with nothing but -inf, are 0 (whatever stands in them and their dprobs).
+ *          Slots outside 0..E-1 count as -1, and their dprobs are not looked at; an expert
+ *          twice among a token's slots adds up.  dlogits may be logits.
  */
 mmact_status mmact_moe_route_backward(const void *logits, const uint8_t *mask, const int32_t *experts,
                                       const int32_t *counts, const float *dprobs, const float *dloss, void *dlogits,

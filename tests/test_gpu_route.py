@@ -205,6 +205,16 @@ def test_many_tokens(T, E, top, dtype):
                  + (2.0 ** -25 if dtype == "f16" else 0.0)).all())
 
 
+@pytest.mark.parametrize("T,E,top,dtype", [(5000, 64, 8, "bf16"), (3001, 257, 3, "f32"), (4000, 30, 2, "f16")])
+def test_backward_in_place(T, E, top, dtype):
+    t, _ = logits(np.random.default_rng(T), T, E, dtype)
+    experts, probs, counts, loss = forward(t, top)
+    dp, dz = torch.randn((T, top), device="cuda"), torch.empty_like(t)
+    mmact.mmact_moe_route_backward(t, experts, counts, dp, loss, dz)
+    mmact.mmact_moe_route_backward(t, experts, counts, dp, loss, t)
+    assert torch.equal(t, dz)
+
+
 def test_no_tokens():
     experts, probs, counts, loss = forward(torch.empty((0, 30), device="cuda"), 3)
     assert not counts.any() and float(loss) == 0.0
@@ -276,3 +286,33 @@ def test_equal_logits_everywhere(T, E, top):
     z[7, E // 2:] = 1.0                                        # half of them
     check_forward(z, host64(z), top, 1.0, True)
     check_forward(z, host64(z), top, 1.0, False)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+def test_what_stands_in_left_out_tokens_and_empty_slots_is_not_looked_at(normalize):
+    """Padded tokens hold anything, upstream gradients of slots that chose nobody too."""
+    rng = np.random.default_rng(6)
+    T, E, top = 60, 24, 4
+    t, z = logits(rng, T, E, "f32")
+    z[5, 2:] = -np.inf                                         # two slots of four
+    z[9] = -np.inf
+    t.copy_(torch.from_numpy(z))
+    mask = np.ones(T, dtype=np.uint8)
+    mask[[3, 20, 59]] = 0
+    dev_mask = torch.tensor(mask, device="cuda")
+    clean = forward(t, top, 0.3, normalize, dev_mask)
+    dp = torch.randn((T, top), device="cuda")
+    dl, dz, again = torch.ones(1, device="cuda"), torch.empty_like(t), torch.empty_like(t)
+    mmact.mmact_moe_route_backward(t, clean[0], clean[2], dp, dl, dz, coef=0.3, normalize=normalize, mask=dev_mask)
+    t[3], t[20, 7], t[59, 0] = float("nan"), float("inf"), -float("inf")
+    dp[[3, 9, 20, 59]] = float("nan")
+    dp[5, 2:] = float("inf")
+    for a, b in zip(forward(t, top, 0.3, normalize, dev_mask), clean):
+        assert torch.equal(a, b)
+    listed = clean[0].clone()
+    listed[3] = torch.arange(top)                              # a left-out token's list of its own
+    mmact.mmact_moe_route_backward(t, listed, clean[2], dp, dl, again, coef=0.3, normalize=normalize, mask=dev_mask)
+    assert torch.equal(dz, again) and not again[[3, 9, 20, 59]].any()
+    want, bound = ref.backward(z, clean[0].cpu().numpy(), clean[2].cpu().numpy(), np.nan_to_num(host64(dp), posinf=0.0), 1.0, top,
+                               0.3, normalize, mask)
+    assert np.all(np.abs(host64(dz) - want) <= bound + mx.ulp(np.abs(want) + bound, "f32") / 2)
