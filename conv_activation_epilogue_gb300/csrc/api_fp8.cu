@@ -108,30 +108,46 @@ struct F8Plan {
     int x_type;                      // OUT_* of R.x; < 0: A is quantised
 };
 
-// Whether a product runs on the pair kernel: when the rows kernel would have more
-// tiles (128 x 128) than there are SMs.
-bool f8_choose_pair(const F8Context &c, int64_t M, int64_t N)
+int64_t f8_row_tiles(int64_t M, int64_t N) { return ((M + 127) / 128) * ((N + 127) / 128); }
+
+// Whether a product runs on the pair kernel: when the rows kernel would have more tiles
+// (128 x 128) than there are SMs, or K is short for the tiles there are.  Measured (us, rows
+// and pair): 256 tiles of K = 4096 28.7 and 15.7, 160 28.0 and 15.2; 128 tiles of K = 4096 14.7 and
+// 14.9, 2048 10.2 and 10.0, 1024 7.8 and 7.2; 64 of 8192 16.4 and 22.7, 4096 12.0 and 14.7, 2048 9.7 and
+// 9.3, 1024 8.1 and 7.1, 512 7.1 and 6.0; 16 of 2048 7.7 and 9.1, 1024 6.9 and 6.9, 512 6.9 and 5.9.
+bool f8_choose_pair(const F8Context &c, int64_t M, int64_t N, int64_t K)
 {
     const int mode = g_f8_kernel.load();
     if (c.max_pairs < 1 || mode == 1) return false;
     if (mode == 2) return true;
-    return M > 128 && ((M + 127) / 128) * ((N + 127) / 128) > c.dev.sm_count;
+    const int64_t tiles = f8_row_tiles(M, N);
+    return M > 128 && (tiles > c.dev.sm_count || K <= 16 * std::max<int64_t>(tiles, 48));
 }
 
-// Rows of x up to which the rows kernel quantises them itself.
+// The kernel that two products share when they would choose different ones: the rows
+// kernel where both have no more tiles than SMs.
+bool f8_share_pair(const F8Context &c, int64_t tiles0, int64_t tiles1)
+{
+    return c.max_pairs >= 1 && std::max(tiles0, tiles1) > c.dev.sm_count;
+}
+
+// Rows of x up to which the rows kernel quantises them itself.  Measured (us, inside and by
+// a kernel before): 1 x 8192 x 8192 14.3 and 16.2, 8 rows 15.3 and 16.6, 8 x 4096 x 4096 6.7 and 8.5.
 constexpr int64_t F8_FUSED_ROWS = 8;
+
+enum : int { F8_ANY, F8_ROWS, F8_PAIR };   // kernel of a plan
 
 // `x` (or null): A [M, K] in x_type, to be quantised into A, as by f8_gemm_launch, or
 // by the rows kernel on the way.
 mmact_status f8_gemm_plan(F8Plan &plan, const F8Matrix &A, const F8Matrix &B, const float *bias, void *C, int64_t M,
                           int64_t N, int64_t K, mmact_dtype cd, mmact_act act, float alpha, const void *x = nullptr,
-                          mmact_dtype x_type = MMACT_F32)
+                          mmact_dtype x_type = MMACT_F32, int kernel = F8_ANY)
 {
     F8Context c;
     const mmact_status st = f8_context(&c);
     if (st != MMACT_OK) return st;
     const int nk32 = (int)((K + 31) / 32), num_kb = (int)f8_blocks(K);
-    plan.pair = f8_choose_pair(c, M, N);
+    plan.pair = kernel == F8_ANY ? f8_choose_pair(c, M, N, K) : kernel == F8_PAIR;
     plan.A = A;
     plan.B = B;
     plan.x_type = -1;
@@ -472,10 +488,19 @@ MMACT_EXPORT mmact_status mmact_linear_fp8_backward(const void *dy, const void *
     const F8Matrix gy = ws.matrix(M, N, grad_dtype), gyt = ws.matrix(N, M, grad_dtype), xt = ws.matrix(K, M, MMACT_E4M3);
     float *part = static_cast<float *>(ws.take(0));
     F8Plan X, W;
+    int kernel = F8_ANY;
+    if (want_dx && want_dw) {
+        F8Context c;
+        if ((s = f8_context(&c)) != MMACT_OK) return s;
+        if (f8_choose_pair(c, M, K, N) != f8_choose_pair(c, N, K, M))
+            kernel = f8_share_pair(c, f8_row_tiles(M, K), f8_row_tiles(N, K)) ? F8_PAIR : F8_ROWS;
+    }
     if (want_dx && (s = f8_gemm_plan(X, gy, F8Matrix{wt_codes, wt_scales, wt_dtype}, nullptr, dx, M, K, N, x_dtype,
-                                     MMACT_ACT_NONE, 0.0f)) != MMACT_OK)
+                                     MMACT_ACT_NONE, 0.0f, nullptr, MMACT_F32, kernel)) != MMACT_OK)
         return s;
-    if (want_dw && (s = f8_gemm_plan(W, gyt, xt, nullptr, dw, N, K, M, dw_dtype, MMACT_ACT_NONE, 0.0f)) != MMACT_OK) return s;
+    if (want_dw && (s = f8_gemm_plan(W, gyt, xt, nullptr, dw, N, K, M, dw_dtype, MMACT_ACT_NONE, 0.0f, nullptr,
+                                     MMACT_F32, kernel)) != MMACT_OK)
+        return s;
     F8Launch L;
     const bool products = want_dx || want_dw;
     if (products && (s = f8_gemm_layout(L, want_dw ? W : X, want_dw && want_dx ? &X : nullptr)) != MMACT_OK) return s;
