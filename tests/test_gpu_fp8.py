@@ -474,6 +474,48 @@ def test_long_rows_pass_32_bit_offsets():
         assert torch.equal(C[i], x[:, k].float() * f)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 8192, 8192), (8, 8192, 8192), (5, 4100, 8195), (3, 520, 16000)])
+@pytest.mark.parametrize("out", [torch.float32, torch.float16])
+def test_linear_of_few_rows_over_long_k(M, N, K, out):
+    """Rows quantised inside the product: deep rings that go round, rows that begin anywhere."""
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    x, w = torch.randn((M, K), generator=g, device="cuda").bfloat16(), torch.randn((N, K), generator=g, device="cuda").bfloat16()
+    q = quantized(w, "e4m3", True)
+    C = torch.full((M, N), float("nan"), dtype=out, device="cuda")
+    work = torch.full((mmact.mmact_linear_fp8_workspace_bytes(M, K),), 0xFF, dtype=torch.uint8, device="cuda")
+    mmact.mmact_linear_fp8(x, *q, None, C, work)
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+    a, b = values64(*quantized(x), M, K), values64(*q, N, K)
+    want, bound = a @ b.t(), mx.sum_error(K) * (a.abs() @ b.abs().t())
+    assert bool(((C.double() - want).abs() <= bound + (2.0 ** -24 if out is torch.float32 else 2.0 ** -11) * (want.abs() + bound)
+                 + 2.0 ** -25).all())
+
+
+def test_backward_passes_32_bit_offsets():
+    """More than 2^31 values of dy: the last tokens' gradients and what they add to the weights' and the bias's."""
+    M, N, K = 70000, 32768, 40
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    dy[-200:] = torch.randn((200, N), generator=g, device="cuda").bfloat16()
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    wt = quantized(torch.randn((N, K), generator=g, device="cuda").bfloat16(), "e4m3", True, transposed=True)
+    dx, dw, db = backward(dy, x, wt, F8["e4m3"])
+    assert mmact.mmact_get_last_error() == mmact.MMACT_OK
+    assert not dx[:-200].any()
+    tail, a = dy[-200:], values64(*quantized(dy[-200:].contiguous()), 200, N)
+    b = values64(*wt, K, N)
+    want, bound = a @ b.t(), mx.sum_error(N) * (a.abs() @ b.abs().t())
+    assert bool(((dx[-200:].double() - want).abs() <= bound + 2.0 ** -8 * (want.abs() + bound)).all())
+    # the last 112 rows are a block of their own, the 88 before them lie in the block that ends at 69888
+    first = M - 112 - 128
+    a = values64(*quantized(dy[first:].t().contiguous()), N, 240)
+    b = values64(*quantized(x[first:].t().contiguous()), K, 240)
+    want, bound = a @ b.t(), mx.sum_error(M) * (a.abs() @ b.abs().t())
+    assert bool(((dw.double() - want).abs() <= bound + 2.0 ** -24 * (want.abs() + bound)).all())
+    want = tail.double().sum(dim=0)
+    assert bool(((db - want).abs() <= mx.sum_error(M) * tail.double().abs().sum(dim=0)).all())
+
+
 def test_refusals():
     x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
     codes = torch.zeros((4, 64), dtype=torch.uint8, device="cuda").view(F8["e4m3"])

@@ -215,6 +215,26 @@ def test_backward_in_place(T, E, top, dtype):
     assert torch.equal(t, dz)
 
 
+def test_tokens_past_32_bit_offsets():
+    """More than 2^31 logits: copies of a few tokens, so that every copy's choice and gradient are known."""
+    E, top, base = 512, 4, 1000
+    z = torch.randn((base, E), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").bfloat16()
+    experts, probs, counts, loss = forward(z, top)
+    copies = 4300
+    many = z.repeat(copies, 1)
+    e, p, c, l = forward(many, top)
+    assert torch.equal(c.long(), counts.long() * copies) and torch.equal(e.view(copies, base, top), experts.expand(copies, base, top))
+    assert torch.equal(p.view(copies, base, top), probs.expand(copies, base, top))
+    # the same shares: the same loss, from sums over tokens in another order
+    assert abs(float(l) - float(loss)) <= 2 * (ref.prob_error(None) + 8192 * 2.0 ** -23) * float(loss)
+    dp = torch.randn((base, top), device="cuda")
+    dz, dmany = torch.empty_like(z), torch.full_like(many, float("nan"))
+    mmact.mmact_moe_route_backward(z, experts, counts, dp, None, dz)
+    mmact.mmact_moe_route_backward(many, e, c, dp.repeat(copies, 1), None, dmany)
+    assert torch.equal(dmany.view(copies, base, E)[[0, 1, 2100, 4200, 4299]], dz.expand(5, base, E))
+    assert bool((dmany.view(copies, base, E) == dz).all())
+
+
 def test_no_tokens():
     experts, probs, counts, loss = forward(torch.empty((0, 30), device="cuda"), 3)
     assert not counts.any() and float(loss) == 0.0
