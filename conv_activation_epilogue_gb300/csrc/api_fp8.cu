@@ -94,9 +94,9 @@ bool f8_encode(CUtensorMap *mc, CUtensorMap *ms, const F8Matrix &m, int64_t rows
            encode_tensor_map(ms, MMACT_F32, 2, m.scales, ds, ss, bs, false);
 }
 
-// K blocks whose products an accumulator takes when the output is fp32 (gemm_fp8.cu): on
-// the pair kernel, where a new accumulator costs a microsecond, and on the rows kernel,
-// where it costs CTAs.
+// K blocks whose products an accumulator takes, at most, when the output is fp32 (gemm_fp8.cu):
+// on the pair kernel, where a new accumulator costs a microsecond, and on the rows kernel,
+// where it costs CTAs and, once a tile's cluster has eight, a pause.
 constexpr int F8_CHUNK_KB = 16, F8_ROWS_CHUNK_KB = 32;
 
 // Plan of one product: either kernel's launch.
@@ -252,6 +252,8 @@ mmact_status f8_rows_layout(F8RowsLaunch &L, const F8Context &c, const F8Plan &o
         F8RowsMaps &m = a.maps[i];
         const F8Plan &plan = i == 0 ? one : *two;
         p.kb_per = (p.num_kb + split - 1) / split;
+        p.chunk_kb = p.out == OUT_F32 ? F8_ROWS_CHUNK_KB : p.num_kb;
+        L.chunks = L.chunks || p.kb_per > p.chunk_kb;
         most = std::max(most, p.kb_per);
         // the operands change sides: B's rows are the instruction's A
         p.idesc = ptx::idesc_f8(f8_kind(plan.B.type), f8_kind(plan.A.type), 128, bt);

@@ -17,6 +17,13 @@
 // Two products that do not depend on each other (a linear layer's two gradients) can share
 // one launch.
 //
+// The tensor core cuts off additions to its accumulator (see gemm_fp8.cu): for fp32 outputs an
+// accumulator takes 32 K blocks at most.  A CTA with more of them (K above 32768, or a
+// cluster that another product in the launch keeps small) goes on in the same columns once
+// the epilogue's warps have read them, and those add up the chunks in registers, rounded.
+// A tile has the tensor memory of one accumulator, so the MMAs pause for that, about a
+// microsecond to 4096 K.
+//
 //   warp 0      TMA producer: a ring of stages of 128 K (codes with the 128-byte
 //               swizzle, scale tiles).  (Asking for the first weight boxes in L2 while
 //               the kernel before this one still runs gained nothing: 32 x 4096 x 4096
@@ -104,12 +111,48 @@ __device__ __forceinline__ void quantize_f8_stages(const F8RowsProblem &p, const
     }
 }
 
+// The chunks of a CTA's K blocks, all read out of the one accumulator and added up, rounded; the sum takes the
+// accumulator's place.  False when a wait ran out.
+template <int BT>
+__device__ __forceinline__ bool rows_chunks(const Pipe &pp, uint32_t taddr, int chunks, int lane)
+{
+    if (chunks == 1) return true;
+    float sum[BT];
+#pragma unroll
+    for (int j = 0; j < BT; ++j) sum[j] = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+        if (!warp_epi_wait(pp, pp.tfull0, (uint32_t)c & 1u)) return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < BT; i += 16) {
+            uint32_t r[16];
+            ptx::tmem_ld16(taddr + i, r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[i + j] += __uint_as_float(r[j]);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(pp.tempty0);
+    }
+#pragma unroll
+    for (int i = 0; i < BT; i += 16) {
+        uint32_t r[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(sum[i + j]);
+        ptx::tmem_st16(taddr + i, r);
+    }
+    ptx::tmem_st_wait();
+    return true;
+}
+
 constexpr int X_CODES = -1;          // A comes as codes and scales
 
 template <int XT>
 constexpr int F8_ROWS_THREADS = XT == X_CODES ? 192 : 320;
 
-template <int BT, int XT>
+// CHUNKS: some CTA sums its K blocks in several accumulators.
+template <int BT, int XT, bool CHUNKS>
 __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(const __grid_constant__ F8RowsArgs args)
 {
     using Cfg = F8RowsCfg<BT>;
@@ -126,7 +169,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
     const uint32_t idesc = p.idesc;
     const int nk32 = p.nk32;
     const int nb = tile % p.tiles_n, tb = tile / p.tiles_n;
-    const int kb0 = rank * p.kb_per, kb1 = min(p.num_kb, kb0 + p.kb_per);
+    const int kb0 = rank * p.kb_per, kb1 = min(p.num_kb, kb0 + p.kb_per), chunk_kb = p.chunk_kb;
 
     const bool aligned = (base & 1023u) == 0;
     if (!aligned && threadIdx.x == 0) atomicOr(args.status, ST_SMEM_ALIGN);
@@ -136,7 +179,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
     pp.empty0 = pp.full0 + 8 * Cfg::MAX_STAGES;
     pp.tfull0 = pp.empty0 + 8 * Cfg::MAX_STAGES;
     pp.drain = pp.tfull0 + 8;
-    pp.tempty0 = 0;
+    pp.tempty0 = pp.drain + 8;                // the accumulator is read, its next chunk may begin
     pp.abort = misc + 1;
     pp.status = args.status;
     pp.wait_ns = args.wait_ns;
@@ -150,6 +193,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
             }
             ptx::mbar_init(pp.tfull0, 1);
             ptx::mbar_init(pp.drain, 1);
+            ptx::mbar_init(pp.tempty0, 4);
             misc[1] = 0;
             ptx::fence_mbar_init();
         }
@@ -201,13 +245,22 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
             const uint64_t w0 = ptx::smem_desc(sW, 16u, 1024u, ptx::SWIZZLE_128B), t0 = ptx::smem_desc(sT, 16u, 1024u, ptx::SWIZZLE_128B);
             const uint64_t s0 = ptx::smem_desc(sS, 16u, 128u, ptx::SWIZZLE_NONE);
             bool ok = true;
-            uint32_t stage = 0, phase = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
+            uint32_t stage = 0, phase = 0, chunk = 0;
+            for (int kb = kb0, left = chunk_kb; kb < kb1; ++kb, --left) {
+                bool begin = kb == kb0;
+                if constexpr (CHUNKS) {
+                    if (left == 0) {
+                        ptx::commit_elected(pp.tfull0);
+                        if (!mx_warp_wait(pp, pp.tempty0, chunk++ & 1u)) { ok = false; break; }
+                        left = chunk_kb;
+                        begin = true;
+                    }
+                }
                 if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
                 ptx::tc_fence_after();
                 ptx::mma_f8_stage(pp.tmem, w0 + stage * (Cfg::W_BYTES >> 4), t0 + stage * (Cfg::T_BYTES >> 4),
                                   s0 + stage * (Cfg::S_BYTES >> 4), s0 + stage * (Cfg::S_BYTES >> 4) + 32u, pp.tmem + Cfg::SCALE_COL + stage * 8u,
-                                  idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), kb > kb0 ? 1u : 0u);
+                                  idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), begin ? 0u : 1u);
                 ptx::commit_elected(pp.empty0 + 8 * stage);
                 if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
             }
@@ -227,14 +280,18 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
     const bool epi = warp >= 2 && warp < 6;
     const float bias = epi && p.bias != nullptr && n < p.N ? p.bias[n] : 0.0f;
     bool good = aligned;
+    const uint32_t taddr = pp.tmem + ((uint32_t)(q * 32) << 16);
     if (epi && aligned) {
-        if (!warp_epi_wait(pp, pp.tfull0, 0)) {
-            pipe_fail(pp);
-            good = false;
+        uint32_t last = 0;                                    // parity of the last chunk
+        if constexpr (CHUNKS) {
+            const int chunks = (kb1 - kb0 + chunk_kb - 1) / chunk_kb;
+            good = rows_chunks<BT>(pp, taddr, chunks, lane);
+            last = (uint32_t)(chunks - 1) & 1u;
         }
+        if (good && !warp_epi_wait(pp, pp.tfull0, last)) good = false;
+        if (!good) pipe_fail(pp);
         ptx::tc_fence_after();
     }
-    const uint32_t taddr = pp.tmem + ((uint32_t)(q * 32) << 16);
     if (split == 1) {
         if (epi && good) {
 #pragma unroll 1
@@ -291,7 +348,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
     }
 }
 
-template <int BT, int XT>
+template <int BT, int XT, bool CHUNKS>
 static cudaError_t launch_rows_t(const F8RowsLaunch &L, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
@@ -308,7 +365,13 @@ static cudaError_t launch_rows_t(const F8RowsLaunch &L, cudaStream_t stream)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = L.args.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, gemm_fp8_rows_kernel<BT, XT>, L.args);
+    return cudaLaunchKernelEx(&cfg, gemm_fp8_rows_kernel<BT, XT, CHUNKS>, L.args);
+}
+
+template <int BT, int XT>
+static cudaError_t launch_rows_t(const F8RowsLaunch &L, cudaStream_t stream)
+{
+    return L.chunks ? launch_rows_t<BT, XT, true>(L, stream) : launch_rows_t<BT, XT, false>(L, stream);
 }
 
 cudaError_t launch_gemm_fp8_rows(const F8RowsLaunch &L, cudaStream_t stream)
@@ -328,8 +391,10 @@ template <int BT, int XT>
 static cudaError_t setup_rows_t()
 {
     using Cfg = F8RowsCfg<BT>;
-    return cudaFuncSetAttribute(gemm_fp8_rows_kernel<BT, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Cfg::OFF_RING + Cfg::MAX_STAGES * Cfg::STAGE_BYTES);
+    const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    constexpr int bytes = Cfg::OFF_RING + Cfg::MAX_STAGES * Cfg::STAGE_BYTES;
+    const cudaError_t e = cudaFuncSetAttribute(gemm_fp8_rows_kernel<BT, XT, false>, smem, bytes);
+    return e == cudaSuccess ? cudaFuncSetAttribute(gemm_fp8_rows_kernel<BT, XT, true>, smem, bytes) : e;
 }
 
 // Clusters of `split` CTAs that are resident at once (with full rings).
@@ -347,7 +412,7 @@ static cudaError_t rows_clusters(int split, int *n)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(n, gemm_fp8_rows_kernel<128, X_CODES>, &cfg);
+    return cudaOccupancyMaxActiveClusters(n, gemm_fp8_rows_kernel<128, X_CODES, false>, &cfg);
 }
 
 cudaError_t setup_fp8_rows_kernels(int (&max_clusters)[4])

@@ -67,6 +67,7 @@ struct F8RowsProblem {
     int tiles_n;         // tiles of 128 rows of B
     int num_tiles;
     int kb_per;          // K blocks of a CTA of the tile's cluster
+    int chunk_kb;        // of these summed in one accumulator
     int act, out;
     float alpha;
     uint32_t idesc;      // operand formats, 128 x bt
@@ -94,6 +95,7 @@ struct F8RowsLaunch {
     F8RowsArgs args;
     int bt;              // rows of A in a tile: 16, 32, 64 or 128
     int x_type;          // OUT_* of the first product's x; < 0: its A is tmT, tmST
+    bool chunks;         // some CTA has more K blocks than an accumulator takes
     int grid;
 };
 

@@ -66,7 +66,7 @@ struct F8RowsCfg {
     static constexpr int MAX_STAGES = F8_ROWS_STAGES(BT);
     static constexpr uint32_t SCALE_COL = BT;
     static constexpr uint32_t TMEM_COLS = BT + 8 * MAX_STAGES <= 128 ? 128 : 256;
-    static constexpr int OFF_BAR = 0, OFF_MISC = (2 * MAX_STAGES + 2) * 8, OFF_RING = 1024;
+    static constexpr int OFF_BAR = 0, OFF_MISC = (2 * MAX_STAGES + 3) * 8, OFF_RING = 1024;
     static constexpr int PART_BYTES = BT * 512;                          // a partial tile, over the ring
     static constexpr int MIN_SMEM = tmem_min_smem((int)TMEM_COLS);
     static constexpr int smem_bytes(int stages, int split)

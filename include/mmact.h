@@ -626,7 +626,11 @@ mmact_status mmact_dequantize_fp8(const void *codes, const void *scales, void *y
 /*
  * C = act(A x B^T + bias) of 8-bit matrices A [M, K] and B [N, K] (each E4M3 or
  * E5M2, both with their blocks along K), bias [N] fp32 or NULL, C [M, N] row-major
- * in c_dtype, accumulated in fp32 on the tensor cores and rounded once.  Any M, N
+ * in c_dtype, accumulated in fp32 on the tensor cores and rounded once.  The tensor
+ * cores cut off each addition towards zero: into F32, one accumulator takes 4096 of
+ * K at most and the accumulators are added up rounded, so that errors of one
+ * sign do not grow with K; into 16 bits they stay below the output's rounding up to
+ * K of some 10^5.  How K is divided depends on the sizes, not on the values.  Any M, N
  * and K: an N whose rows of C are not a multiple of 16 bytes is stored element by
  * element (slower).  M == 0 or N == 0 enqueues nothing; K == 0 gives
  * C = act(bias).  A NaN scale makes the rows or columns of C it reaches NaN.
@@ -671,7 +675,9 @@ mmact_status mmact_linear_fp8_workspace_bytes(int64_t M, int64_t K, int64_t *byt
  *   db [N] fp32           = sum over M of dy, unquantised, in fp32, in an order that
  *                           depends on M alone
  * dy is quantised to grad_dtype (E4M3 or E5M2), x to E4M3.  Each of dx, dw and db may
- * be NULL and is then not computed; each other one is overwritten.  Products over
+ * be NULL and is then not computed; each other one is overwritten.  How the sums of
+ * dx and dw are divided (see mmact_gemm_fp8) depends on the sizes and on which of the two are wanted: dw
+ * alone and dw beside dx may differ in last bits.  Products over
  * an empty dimension are zeros.  dy, x, Wt's arrays, dx, dw and workspace are 16-byte
  * aligned; the outputs must not overlap the inputs or each other.
  *   workspace  at least mmact_linear_fp8_backward_workspace_bytes, as above.
