@@ -124,18 +124,31 @@ bool f8_choose_pair(const F8Context &c, int64_t M, int64_t N, int64_t K)
     return M > 128 && (tiles > c.dev.sm_count || K <= 16 * std::max<int64_t>(tiles, 48));
 }
 
-// The kernel that two products share when they would choose different ones: the rows
-// kernel where both have no more tiles than SMs.
-bool f8_share_pair(const F8Context &c, int64_t tiles0, int64_t tiles1)
-{
-    return c.max_pairs >= 1 && std::max(tiles0, tiles1) > c.dev.sm_count;
-}
-
 // Rows of x up to which the rows kernel quantises them itself.  Measured (us, inside and by
 // a kernel before): 1 x 8192 x 8192 14.3 and 16.2, 8 rows 15.3 and 16.6, 8 x 4096 x 4096 6.7 and 8.5.
 constexpr int64_t F8_FUSED_ROWS = 8;
 
-enum : int { F8_ANY, F8_ROWS, F8_PAIR };   // kernel of a plan
+enum : int { F8_ANY, F8_ROWS, F8_PAIR };   // kernel of a plan; F8_ANY: the product's own choice
+
+// The kernel of both gradients, so that they share a launch, or F8_ANY: each its own.  When the two
+// would choose different ones, that of the rows kernel (m x n, over k) has few tiles and many K blocks, the other
+// (`other_tiles`, `other_kb`) the reverse.  A shared launch ends no earlier than the few tiles: from some 40 K blocks on that is
+// later than two launches do.  Measured (us, the whole backward pass, M x N x K: own kernels, both rows, both pair):
+//   few tiles, long K    8192 x 512 x 512 (16 tiles of 64 K blocks) 31, 41, 41; 131072 x 512 x 512 260, 987, 512;
+//                        18000 x 64 x 100 29, 53, 64; 8192 x 512 x 1024 (32 tiles) 36, 72, 43; 256 x 8192 x 1024 32, 48, 38
+//   shorter              4096 x 512 x 512 (32 K blocks) 27, 25, 28; 1024 x 4096 x 512 30, 32, 26
+//   more tiles           8192 x 1024 x 1024 (64 tiles) 48, 90, 49; 8192 x 768 x 2048 (96) 70, 146, 53
+// With 128 tokens or fewer the rows kernel shares little work between its CTAs, and the other product's many tiles
+// fill the pairs: 100 x 6500 x 2000 (16 tiles of 51) 33, 59, 38, but 128 x 6144 x 4096 (32 of 48) 44, 83, 41.
+// A shared launch is of pairs when a product has more tiles than SMs or there is much to do (K blocks of both
+// products' tiles together): 2048 x 1024 x 1024 (2048) 30, 25, 21; 1024 x 4096 x 512 (2048) above; 4096 x 512 x 512
+// (1024) above; 2048 x 512 x 512 (512) 24, 16, 18.
+int f8_shared_kernel(const F8Context &c, int64_t m, int64_t n, int64_t k, int64_t other_tiles, int64_t other_kb)
+{
+    const int64_t tiles = f8_row_tiles(m, n), kb = f8_blocks(k);
+    if (tiles <= c.max_pairs / (m <= 128 ? 4 : 2) && kb >= 40 + tiles / 2) return F8_ANY;
+    return std::max(tiles, other_tiles) > c.dev.sm_count || tiles * kb + other_tiles * other_kb >= 10 * c.dev.sm_count ? F8_PAIR : F8_ROWS;
+}
 
 // `x` (or null): A [M, K] in x_type, to be quantised into A, as by f8_gemm_launch, or
 // by the rows kernel on the way.
@@ -494,8 +507,9 @@ MMACT_EXPORT mmact_status mmact_linear_fp8_backward(const void *dy, const void *
     if (want_dx && want_dw) {
         F8Context c;
         if ((s = f8_context(&c)) != MMACT_OK) return s;
-        if (f8_choose_pair(c, M, K, N) != f8_choose_pair(c, N, K, M))
-            kernel = f8_share_pair(c, f8_row_tiles(M, K), f8_row_tiles(N, K)) ? F8_PAIR : F8_ROWS;
+        const bool dx_pair = f8_choose_pair(c, M, K, N), dw_pair = f8_choose_pair(c, N, K, M);
+        if (dw_pair && !dx_pair) kernel = f8_shared_kernel(c, M, K, N, f8_row_tiles(N, K), f8_blocks(M));
+        if (dx_pair && !dw_pair) kernel = f8_shared_kernel(c, N, K, M, f8_row_tiles(M, K), f8_blocks(N));
     }
     if (want_dx && (s = f8_gemm_plan(X, gy, F8Matrix{wt_codes, wt_scales, wt_dtype}, nullptr, dx, M, K, N, x_dtype,
                                      MMACT_ACT_NONE, 0.0f, nullptr, MMACT_F32, kernel)) != MMACT_OK)
