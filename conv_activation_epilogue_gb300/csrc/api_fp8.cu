@@ -482,7 +482,7 @@ MMACT_EXPORT mmact_status mmact_linear_fp8_backward(const void *dy, const void *
         return MMACT_ERR_INVALID_ARG;
     const bool any = dx != nullptr || dw != nullptr || db != nullptr;
     if (any && (dy == nullptr || workspace == nullptr) && M * N != 0) return MMACT_ERR_INVALID_ARG;
-    if (dx != nullptr && (wt_codes == nullptr || wt_scales == nullptr) && M * N * K != 0) return MMACT_ERR_INVALID_ARG;
+    if (dx != nullptr && (wt_codes == nullptr || wt_scales == nullptr) && M != 0 && N * K != 0) return MMACT_ERR_INVALID_ARG;
     if (dw != nullptr && (x == nullptr || workspace == nullptr) && M * K != 0 && N != 0) return MMACT_ERR_INVALID_ARG;
     if (db != nullptr && !aligned4(db)) return MMACT_ERR_INVALID_ARG;
     if (!aligned16(dy) || !aligned16(x) || !aligned16(wt_codes) || !aligned16(wt_scales) || !aligned16(dx) ||
