@@ -164,11 +164,18 @@ bool encode(CUtensorMap *m, mmact_dtype dt, int rank, const void *ptr, const uin
             return true;
         }
     }
-    CUresult r = g_encode(m, (CUtensorMapDataType)k.dt, (cuuint32_t)rank, const_cast<void *>(ptr), k.gd, k.gs,
-                          k.bx, k.es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return false;
+    auto make = [&] {
+        return g_encode(m, (CUtensorMapDataType)k.dt, (cuuint32_t)rank, const_cast<void *>(ptr), k.gd, k.gs,
+                        k.bx, k.es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    // The encoder is the driver's and refuses a thread without a context.  A thread whose first CUDA
+    // call this is has none yet: a call of the runtime gives it the device's own.
+    if (!make()) {
+        void *address = nullptr;
+        if (cudaGetSymbolAddress(&address, g_status) != cudaSuccess || !make()) return false;
+    }
     g_tmap_encodes.fetch_add(1, std::memory_order_relaxed);
     TmapEntry &e = t_tmap_cache[set][t_tmap_next[set]];
     t_tmap_next[set] = (uint8_t)((t_tmap_next[set] + 1) % TMAP_WAYS);
