@@ -45,8 +45,10 @@ mmact_status f8_context(F8Context *out)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> lock(mutex);               // setting up twice is harmless
-        if (setup_fp8_pair_kernels(&pairs[dev]) != cudaSuccess || setup_fp8_rows_kernels(clusters[dev]) != cudaSuccess)
+        std::lock_guard<std::mutex> lock(mutex);
+        // once: other threads read pairs and clusters as soon as `ready` says so
+        if (!ready[dev].load(std::memory_order_relaxed) &&
+            (setup_fp8_pair_kernels(&pairs[dev]) != cudaSuccess || setup_fp8_rows_kernels(clusters[dev]) != cudaSuccess))
             return MMACT_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }

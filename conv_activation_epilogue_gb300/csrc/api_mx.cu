@@ -42,9 +42,11 @@ mmact_status mx_context(MxContext *out)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return MMACT_ERR_CUDA;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> lock(mutex);               // setting up twice is harmless
-        if (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels(clusters[dev]) != cudaSuccess ||
-            setup_moe_kernels() != cudaSuccess || setup_moe_mxfp4_kernels() != cudaSuccess)
+        std::lock_guard<std::mutex> lock(mutex);
+        // once: other threads read pairs and clusters as soon as `ready` says so
+        if (!ready[dev].load(std::memory_order_relaxed) &&
+            (setup_mxfp4_pair_kernels(&pairs[dev]) != cudaSuccess || setup_mxfp4_rows_kernels(clusters[dev]) != cudaSuccess ||
+             setup_moe_kernels() != cudaSuccess || setup_moe_mxfp4_kernels() != cudaSuccess))
             return MMACT_ERR_CUDA;
         ready[dev].store(true, std::memory_order_release);
     }
