@@ -13,7 +13,7 @@
 // their order, so results repeat bit for bit.
 //
 // Measured, logits from HBM: 131072 x 256 fp32 with 8 to choose 58 us forward (142 MB; bound
-// by instructions, some 300 a token), 57 us backward (277 MB, 4.9 TB/s; bound by the
+// by instructions, 335 a token), 57 us backward (277 MB, 4.9 TB/s; bound by the
 // latency of a warp's reductions); 64 x 64 4.8 us, two launches.
 #include "common.cuh"
 #include "kernels_route.h"
