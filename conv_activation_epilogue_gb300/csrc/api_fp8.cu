@@ -96,10 +96,8 @@ bool f8_encode(CUtensorMap *mc, CUtensorMap *ms, const F8Matrix &m, int64_t rows
            encode_tensor_map(ms, MMACT_F32, 2, m.scales, ds, ss, bs, false);
 }
 
-// K blocks whose products an accumulator takes, at most, when the output is fp32 (gemm_fp8.cu):
-// on the pair kernel, where a new accumulator costs a microsecond, and on the rows kernel,
-// where it costs CTAs and, once a tile's cluster has eight, a pause.
-constexpr int F8_CHUNK_KB = 16, F8_ROWS_CHUNK_KB = 32;
+// K blocks whose products an accumulator takes, at most, when the output is fp32 (gemm_fp8.cu).
+constexpr int F8_CHUNK_KB = 16;
 
 // Plan of one product: either kernel's launch.
 struct F8Plan {
@@ -249,9 +247,10 @@ mmact_status f8_rows_layout(F8RowsLaunch &L, const F8Context &c, const F8Plan &o
     while (split < 8 && tiles * split * 2 <= sms && tiles <= c.max_clusters[log2 + 1] && num_kb >= split * 4) split *= 2, ++log2;
     if (bt == 16)
         while (split < 8 && tiles * split * 2 <= 2 * sms && num_kb >= split * 4 && num_kb < split * F8_DEEP_KB) split *= 2;
-    // fp32 outputs: K in as many accumulators as the cluster allows
-    for (int i = 0; i < n; ++i)
-        while (a.prob[i].out == OUT_F32 && split < 8 && a.prob[i].num_kb > split * F8_ROWS_CHUNK_KB) split *= 2;
+    // of two products, no CTA of the longer one with more than 32 K blocks (gradients of 8192 x 2048 x 128, 64 tiles of 16 K blocks
+    // and 16 of 64: 39.7 us, 45.5 without; one product alone is the slower for it: 128 x 8192 x 16384 36.4, 29.6 without)
+    for (int i = 0; i < n && n == 2; ++i)
+        while (split < 8 && a.prob[i].num_kb > split * 32) split *= 2;
     // no CTA without a K block
     auto idle = [&](int s) {
         for (int i = 0; i < n; ++i) {
@@ -267,7 +266,7 @@ mmact_status f8_rows_layout(F8RowsLaunch &L, const F8Context &c, const F8Plan &o
         F8RowsMaps &m = a.maps[i];
         const F8Plan &plan = i == 0 ? one : *two;
         p.kb_per = (p.num_kb + split - 1) / split;
-        p.chunk_kb = p.out == OUT_F32 ? F8_ROWS_CHUNK_KB : p.num_kb;
+        p.chunk_kb = p.out == OUT_F32 ? F8_CHUNK_KB : p.num_kb;
         L.chunks = L.chunks || p.kb_per > p.chunk_kb;
         most = std::max(most, p.kb_per);
         // the operands change sides: B's rows are the instruction's A

@@ -627,7 +627,7 @@ mmact_status mmact_dequantize_fp8(const void *codes, const void *scales, void *y
  * C = act(A x B^T + bias) of 8-bit matrices A [M, K] and B [N, K] (each E4M3 or
  * E5M2, both with their blocks along K), bias [N] fp32 or NULL, C [M, N] row-major
  * in c_dtype, accumulated in fp32 on the tensor cores and rounded once.  The tensor
- * cores cut off each addition towards zero: into F32, one accumulator takes 4096 of
+ * cores cut off each addition towards zero: into F32, one accumulator takes 2048 of
  * K at most and the accumulators are added up rounded, so that errors of one
  * sign do not grow with K; into 16 bits they stay below the output's rounding up to
  * K of some 10^5.  How K is divided depends on the sizes, not on the values.  Any M, N
