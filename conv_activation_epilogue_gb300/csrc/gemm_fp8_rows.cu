@@ -18,10 +18,10 @@
 // one launch.
 //
 // The tensor core cuts off additions to its accumulator (see gemm_fp8.cu): for fp32 outputs an
-// accumulator takes 16 K blocks at most.  A CTA with more of them goes on in the same columns once the
-// epilogue's warps have read them, and those add up the chunks in registers, rounded.  A tile has the tensor
-// memory of one accumulator, so the MMAs pause for that, some 0.1 us each time: 128 x 8192 x 8192 (two chunks to a
-// CTA) 18.5 us in one accumulator, 18.8; 256 x 512 x 131072 (eight) 42.7 with chunks twice as long, 43.0.
+// accumulator takes 16 K blocks at most, and a CTA with more of them has three accumulators in turn, which
+// the epilogue's warps add up, rounded, while the MMAs go on.  (128 x 8192 x 8192 from x in bf16, two chunks to a CTA,
+// 23.4 us; 23.3 with all of K in one accumulator; 23.9 with one that the MMAs had to wait for and sums in 128
+// registers a thread.  256 x 512 x 131072, eight chunks, 42.4 and 42.1, 42.5.)
 //
 //   warp 0      TMA producer: a ring of stages of 128 K (codes with the 128-byte
 //               swizzle, scale tiles).  (Asking for the first weight boxes in L2 while
@@ -110,38 +110,34 @@ __device__ __forceinline__ void quantize_f8_stages(const F8RowsProblem &p, const
     }
 }
 
-// The chunks of a CTA's K blocks, all read out of the one accumulator and added up, rounded; the sum takes the
-// accumulator's place.  False when a wait ran out.
+// What the epilogue does with the chunks of a CTA's K blocks as they come: each takes over the sum of
+// those before it, rounded, but the last, which is only waited for.  Chunk c is in accumulator c % 3.  The MMAs
+// wait for chunk c to be taken over (`tempty0`) before they say that c + 1 is complete and begin c + 2: so neither
+// side is ever two phases of a barrier ahead of the other, and chunk c's accumulator is read (with c + 1) before c + 3
+// takes it.  False when a wait ran out.
 template <int BT>
 __device__ __forceinline__ bool rows_chunks(const Pipe &pp, uint32_t taddr, int chunks, int lane)
 {
-    if (chunks == 1) return true;
-    float sum[BT];
-#pragma unroll
-    for (int j = 0; j < BT; ++j) sum[j] = 0.0f;
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-        if (!warp_epi_wait(pp, pp.tfull0, (uint32_t)c & 1u)) return false;
+        if (!warp_epi_wait(pp, pp.tfull0 + 8 * (c & 1), (uint32_t)(c >> 1) & 1u)) return false;
         ptx::tc_fence_after();
+        if (c == chunks - 1) break;
+        const uint32_t sum = taddr + (uint32_t)((c + 2) % 3 * BT), here = taddr + (uint32_t)(c % 3 * BT);
+#pragma unroll 1
+        for (int i = 0; i < BT && c != 0; i += 16) {
+            uint32_t a[16], b[16];
+            ptx::tmem_ld16(sum + i, a);
+            ptx::tmem_ld16(here + i, b);
 #pragma unroll
-        for (int i = 0; i < BT; i += 16) {
-            uint32_t r[16];
-            ptx::tmem_ld16(taddr + i, r);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum[i + j] += __uint_as_float(r[j]);
+            for (int j = 0; j < 16; ++j) b[j] = __float_as_uint(__uint_as_float(a[j]) + __uint_as_float(b[j]));
+            ptx::tmem_st16(here + i, b);
         }
+        ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(pp.tempty0);
     }
-#pragma unroll
-    for (int i = 0; i < BT; i += 16) {
-        uint32_t r[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(sum[i + j]);
-        ptx::tmem_st16(taddr + i, r);
-    }
-    ptx::tmem_st_wait();
     return true;
 }
 
@@ -154,7 +150,7 @@ constexpr int F8_ROWS_THREADS = XT == X_CODES ? 192 : 320;
 template <int BT, int XT, bool CHUNKS>
 __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(const __grid_constant__ F8RowsArgs args)
 {
-    using Cfg = F8RowsCfg<BT>;
+    using Cfg = F8RowsCfg<BT, CHUNKS>;
     const int stages = args.stages, split = args.split;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -177,8 +173,8 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
     pp.full0 = base + Cfg::OFF_BAR;
     pp.empty0 = pp.full0 + 8 * Cfg::MAX_STAGES;
     pp.tfull0 = pp.empty0 + 8 * Cfg::MAX_STAGES;
-    pp.drain = pp.tfull0 + 8;
-    pp.tempty0 = pp.drain + 8;                // the accumulator is read, its next chunk may begin
+    pp.drain = pp.tfull0 + 16;                // tfull0: two, of even and odd chunks
+    pp.tempty0 = pp.drain + 8;                // a chunk has taken over the sum so far
     pp.abort = misc + 1;
     pp.status = args.status;
     pp.wait_ns = args.wait_ns;
@@ -191,6 +187,7 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
                 ptx::mbar_init(pp.empty0 + 8 * s, 1);
             }
             ptx::mbar_init(pp.tfull0, 1);
+            ptx::mbar_init(pp.tfull0 + 8, 1);
             ptx::mbar_init(pp.drain, 1);
             ptx::mbar_init(pp.tempty0, 4);
             misc[1] = 0;
@@ -244,26 +241,28 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
             const uint64_t w0 = ptx::smem_desc(sW, 16u, 1024u, ptx::SWIZZLE_128B), t0 = ptx::smem_desc(sT, 16u, 1024u, ptx::SWIZZLE_128B);
             const uint64_t s0 = ptx::smem_desc(sS, 16u, 128u, ptx::SWIZZLE_NONE);
             bool ok = true;
-            uint32_t stage = 0, phase = 0, chunk = 0;
+            uint32_t stage = 0, phase = 0, chunk = 0, d = pp.tmem;
             for (int kb = kb0, left = chunk_kb; kb < kb1; ++kb, --left) {
                 bool begin = kb == kb0;
                 if constexpr (CHUNKS) {
                     if (left == 0) {
-                        ptx::commit_elected(pp.tfull0);
-                        if (!mx_warp_wait(pp, pp.tempty0, chunk++ & 1u)) { ok = false; break; }
+                        // the chunk before this one is taken over: see rows_chunks
+                        if (chunk != 0 && !mx_warp_wait(pp, pp.tempty0, (chunk - 1) & 1u)) { ok = false; break; }
+                        ptx::commit_elected(pp.tfull0 + 8 * (chunk & 1u));
+                        d = pp.tmem + ++chunk % 3 * BT;
                         left = chunk_kb;
                         begin = true;
                     }
                 }
                 if (!mx_warp_wait(pp, pp.full0 + 8 * stage, phase)) { ok = false; break; }
                 ptx::tc_fence_after();
-                ptx::mma_f8_stage(pp.tmem, w0 + stage * (Cfg::W_BYTES >> 4), t0 + stage * (Cfg::T_BYTES >> 4),
+                ptx::mma_f8_stage(d, w0 + stage * (Cfg::W_BYTES >> 4), t0 + stage * (Cfg::T_BYTES >> 4),
                                   s0 + stage * (Cfg::S_BYTES >> 4), s0 + stage * (Cfg::S_BYTES >> 4) + 32u, pp.tmem + Cfg::SCALE_COL + stage * 8u,
                                   idesc | ptx::f8_scale_id(kb), min(4, nk32 - 4 * kb), begin ? 0u : 1u);
                 ptx::commit_elected(pp.empty0 + 8 * stage);
                 if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
             }
-            if (ok) ptx::commit_elected(pp.tfull0);
+            if (ok) ptx::commit_elected(pp.tfull0 + 8 * (chunk & 1u));
             else if (lane == 0) pipe_fail(pp);
             ptx::commit_elected(pp.drain);
             ptx::mbar_wait_bounded(pp.drain, 0, DRAIN_NS, nullptr);
@@ -279,28 +278,40 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
     const bool epi = warp >= 2 && warp < 6;
     const float bias = epi && p.bias != nullptr && n < p.N ? p.bias[n] : 0.0f;
     bool good = aligned;
-    const uint32_t taddr = pp.tmem + ((uint32_t)(q * 32) << 16);
+    uint32_t taddr = pp.tmem + ((uint32_t)(q * 32) << 16), before = taddr;
+    bool more = false;                                        // the sum of the chunks before the last is at `before`
     if (epi && aligned) {
-        uint32_t last = 0;                                    // parity of the last chunk
         if constexpr (CHUNKS) {
             const int chunks = (kb1 - kb0 + chunk_kb - 1) / chunk_kb;
             good = rows_chunks<BT>(pp, taddr, chunks, lane);
-            last = (uint32_t)(chunks - 1) & 1u;
+            more = chunks > 1;
+            if (more) before = taddr + (uint32_t)((chunks - 2) % 3 * BT), taddr += (uint32_t)((chunks - 1) % 3 * BT);
+        } else {
+            good = warp_epi_wait(pp, pp.tfull0, 0);
         }
-        if (good && !warp_epi_wait(pp, pp.tfull0, last)) good = false;
         if (!good) pipe_fail(pp);
         ptx::tc_fence_after();
     }
+    // 16 columns of this warp's lanes
+    auto sums = [&](int c, float (&z)[16]) {
+        uint32_t r[16];
+        ptx::tmem_ld16(taddr + c, r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(r[j]);
+        if constexpr (CHUNKS) {
+            if (!more) return;
+            ptx::tmem_ld16(before + c, r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) z[j] += __uint_as_float(r[j]);
+        }
+    };
     if (split == 1) {
         if (epi && good) {
 #pragma unroll 1
             for (int c = 0; c < BT; c += 16) {
                 if (tb * BT + c >= p.M) break;
-                uint32_t r[16];
                 float z[16];
-                ptx::tmem_ld16(taddr + c, r);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) z[j] = __uint_as_float(r[j]);
+                sums(c, z);
                 rows_store(p, p.out, tb * BT + c, n, z, bias);
                 __syncwarp();
             }
@@ -311,10 +322,10 @@ __global__ void __launch_bounds__(F8_ROWS_THREADS<XT>, 1) gemm_fp8_rows_kernel(c
         if (epi && good) {
 #pragma unroll 1
             for (int c = 0; c < BT; c += 16) {
-                uint32_t r[16];
-                ptx::tmem_ld16(taddr + c, r);
+                float z[16];
+                sums(c, z);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) part[(c + j) * 128 + q * 32 + lane] = __uint_as_float(r[j]);
+                for (int j = 0; j < 16; ++j) part[(c + j) * 128 + q * 32 + lane] = z[j];
             }
         }
         ptx::cluster_sync();
@@ -353,7 +364,7 @@ static cudaError_t launch_rows_t(const F8RowsLaunch &L, cudaStream_t stream)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)L.grid);
     cfg.blockDim = dim3(F8_ROWS_THREADS<XT>);
-    cfg.dynamicSmemBytes = (size_t)F8RowsCfg<BT>::smem_bytes(L.args.stages, L.args.split);
+    cfg.dynamicSmemBytes = (size_t)F8RowsCfg<BT, CHUNKS>::smem_bytes(L.args.stages, L.args.split);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

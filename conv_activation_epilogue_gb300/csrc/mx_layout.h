@@ -58,15 +58,16 @@ struct MxRowsCfg {
 constexpr int F8_ROWS_STAGES(int bt) { return bt <= 32 ? 10 : (bt == 64 ? 8 : 6); }   // at most
 
 // The same with ring stages of 128 K: the weights' and the tokens' scale tile are 512
-// bytes each, 8 columns of tensor memory.
-template <int BT>
+// bytes each, 8 columns of tensor memory.  CHUNKS: three accumulators.
+template <int BT, bool CHUNKS = false>
 struct F8RowsCfg {
     static constexpr int W_BYTES = 128 * 128, T_BYTES = BT * 128, S_BYTES = 1024;
     static constexpr int STAGE_BYTES = W_BYTES + T_BYTES + S_BYTES;
     static constexpr int MAX_STAGES = F8_ROWS_STAGES(BT);
-    static constexpr uint32_t SCALE_COL = BT;
-    static constexpr uint32_t TMEM_COLS = BT + 8 * MAX_STAGES <= 128 ? 128 : 256;
-    static constexpr int OFF_BAR = 0, OFF_MISC = (2 * MAX_STAGES + 3) * 8, OFF_RING = 1024;
+    static constexpr int ACCS = CHUNKS ? 3 : 1;
+    static constexpr uint32_t SCALE_COL = ACCS * BT, COLS = SCALE_COL + 8 * MAX_STAGES;
+    static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : (COLS <= 256 ? 256 : 512);
+    static constexpr int OFF_BAR = 0, OFF_MISC = (2 * MAX_STAGES + 4) * 8, OFF_RING = 1024;
     static constexpr int PART_BYTES = BT * 512;                          // a partial tile, over the ring
     static constexpr int MIN_SMEM = tmem_min_smem((int)TMEM_COLS);
     static constexpr int smem_bytes(int stages, int split)
@@ -76,7 +77,7 @@ struct F8RowsCfg {
         return need > MIN_SMEM ? need : MIN_SMEM;
     }
     static_assert(OFF_MISC + 16 <= OFF_RING && OFF_RING + MAX_STAGES * STAGE_BYTES <= CTA_SMEM, "shared memory budget");
-    static_assert(BT + 8 * MAX_STAGES <= TMEM_COLS, "tensor memory budget");
+    static_assert(COLS <= TMEM_COLS && MIN_SMEM <= OFF_RING + MAX_STAGES * STAGE_BYTES, "tensor memory budget");
 };
 
 // ----------------------------------------------------------- mixture of experts --

@@ -23,6 +23,7 @@ template <typename Cfg> void all(int kind, int bt)
 int main()
 {
     all<F8RowsCfg<16>>(8, 16); all<F8RowsCfg<32>>(8, 32); all<F8RowsCfg<64>>(8, 64); all<F8RowsCfg<128>>(8, 128);
+    all<F8RowsCfg<16, true>>(24, 16); all<F8RowsCfg<32, true>>(24, 32); all<F8RowsCfg<64, true>>(24, 64); all<F8RowsCfg<128, true>>(24, 128);
     all<MxRowsCfg<16>>(4, 16); all<MxRowsCfg<32>>(4, 32); all<MxRowsCfg<64>>(4, 64); all<MxRowsCfg<128>>(4, 128);
 }
 """
@@ -30,7 +31,7 @@ int main()
 
 @pytest.fixture(scope="module")
 def plans(tmp_path_factory):
-    """(operands' bits, rows of a tile, ring stages, CTAs of a cluster, shared memory, columns, two offsets, most stages)"""
+    """(operands' bits, times the accumulators, rows of a tile, ring stages, CTAs of a cluster, shared memory, columns, two offsets, most stages)"""
     d = tmp_path_factory.mktemp("layout")
     (d / "m.cpp").write_text(PROGRAM)
     subprocess.run(["g++", "-std=c++17", "-I", CSRC, str(d / "m.cpp"), "-o", str(d / "m")], check=True)
@@ -51,18 +52,18 @@ def test_ctas_that_share_an_sm_all_have_their_columns(plans):
 
 
 def test_parts_do_not_overlap(plans):
-    """Barriers (full and empty of each stage, accumulator full, drained and read), two words, the ring or a partial tile."""
+    """Barriers (full and empty of each stage, even and odd chunk full, drained, sum taken over), two words, the ring or a partial tile."""
     for bits, bt, stages, split, smem, cols, misc, ring, most in plans:
-        if bits != 8:
+        if bits == 4:
             continue
-        assert (2 * most + 3) * 8 <= misc and misc % 8 == 0 and misc + 16 <= ring and ring % 1024 == 0
+        assert (2 * most + 4) * 8 <= misc and misc % 8 == 0 and misc + 16 <= ring and ring % 1024 == 0
         assert ring + stages * (128 * 128 + bt * 128 + 1024) <= smem
         assert split == 1 or ring + bt * 512 <= smem
-        assert bt + 8 * most <= cols
+        assert bits // 8 * bt + 8 * most <= cols
 
 
 def test_few_rows_leave_room_for_another_cta(plans):
     """Two CTAs of up to 32 rows share an SM with rings of five stages."""
     for bits, bt, stages, _, smem, _, _, _, _ in plans:
-        if bits == 8 and bt <= 32 and stages <= 5:
+        if bits != 4 and bt <= 32 and stages <= 5:
             assert 2 * (smem + RESERVED) <= SM_SMEM
