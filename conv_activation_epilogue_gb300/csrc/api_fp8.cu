@@ -134,7 +134,7 @@ enum : int { F8_ANY, F8_ROWS, F8_PAIR };   // kernel of a plan; F8_ANY: the prod
 // would choose different ones, that of the rows kernel (m x n, over k) has few tiles and many K blocks, the other
 // (`other_tiles`, `other_kb`) the reverse.  A shared launch ends no earlier than the few tiles: from some 40 K blocks on that is
 // later than two launches do.  Measured (us, the whole backward pass, M x N x K: own kernels, both rows, both pair):
-//   few tiles, long K    8192 x 512 x 512 (16 tiles of 64 K blocks) 31, 41, 41; 131072 x 512 x 512 260, 987, 512;
+//   few tiles, long K    8192 x 512 x 512 (16 tiles of 64 K blocks) 31, 41, 41; 131072 x 512 x 512 251, 987, 512;
 //                        18000 x 64 x 100 29, 53, 64; 8192 x 512 x 1024 (32 tiles) 36, 72, 43; 256 x 8192 x 1024 32, 48, 38
 //   shorter              4096 x 512 x 512 (32 K blocks) 27, 25, 28; 1024 x 4096 x 512 30, 32, 26
 //   more tiles           8192 x 1024 x 1024 (64 tiles) 48, 90, 49; 8192 x 768 x 2048 (96) 70, 146, 53
