@@ -138,8 +138,10 @@ enum : int { F8_ANY, F8_ROWS, F8_PAIR };   // kernel of a plan; F8_ANY: the prod
 //                        18000 x 64 x 100 29, 53, 64; 8192 x 512 x 1024 (32 tiles) 36, 72, 43; 256 x 8192 x 1024 32, 48, 38
 //   shorter              4096 x 512 x 512 (32 K blocks) 27, 25, 28; 1024 x 4096 x 512 30, 32, 26
 //   more tiles           8192 x 1024 x 1024 (64 tiles) 48, 90, 49; 8192 x 768 x 2048 (96) 70, 146, 53
-// With 128 tokens or fewer the rows kernel shares little work between its CTAs, and the other product's many tiles
-// fill the pairs: 100 x 6500 x 2000 (16 tiles of 51) 33, 59, 38, but 128 x 6144 x 4096 (32 of 48) 44, 83, 41.
+// With m (the tokens, or dw's rows) 128 or less the other product is all stores and keeps the pairs busy for longer:
+// 100 x 6500 x 2000 (16 tiles of 51 K blocks) 33, 59, 38, but 128 x 6144 x 4096 (32 of 48) 44, 83, 41; from about
+// 112 K blocks on its tiles are no longer long enough: 128 x 12288 x 4096 (32 of 96) 68, 154, 65; 16384 x 64 x 4096 (32 of
+// 128) 98, 209, 110; 64 x 16384 x 8192 (64 of 128) 137, 357, 168.
 // A shared launch is of pairs when a product has more tiles than SMs or there is much to do (K blocks of both
 // products' tiles together): 2048 x 1024 x 1024 (2048) 30, 25, 21; 1024 x 4096 x 512 (2048) above; 4096 x 512 x 512
 // (1024) above; 2048 x 512 x 512 (512) 24, 16, 18.
@@ -147,6 +149,7 @@ int f8_shared_kernel(const F8Context &c, int64_t m, int64_t n, int64_t k, int64_
 {
     const int64_t tiles = f8_row_tiles(m, n), kb = f8_blocks(k);
     if (tiles <= c.max_pairs / (m <= 128 ? 4 : 2) && kb >= 40 + tiles / 2) return F8_ANY;
+    if (m <= 128 && tiles <= c.max_pairs && kb >= 112) return F8_ANY;
     return std::max(tiles, other_tiles) > c.dev.sm_count || tiles * kb + other_tiles * other_kb >= 10 * c.dev.sm_count ? F8_PAIR : F8_ROWS;
 }
 

@@ -74,7 +74,8 @@ class Layer:
 # both sides of each rule by which the two products share a launch or do not
 SIZES = [(8192, 512, 512), (6144, 512, 512), (4096, 512, 512), (8192, 768, 768), (8192, 1024, 1024), (8192, 768, 2048), (18000, 64, 100),
          (5001, 99, 257), (4000, 99, 257), (256, 8192, 1024), (200, 8000, 300), (100, 6500, 2000), (64, 8192, 512), (128, 6144, 4096),
-         (64, 16384, 128), (2048, 1024, 1024), (2048, 512, 512), (1024, 4096, 512), (1, 9000, 130), (20000, 1, 1000)]
+         (64, 16384, 128), (2048, 1024, 1024), (2048, 512, 512), (1024, 4096, 512), (1, 9000, 130), (20000, 1, 1000),
+         (16384, 64, 4096), (12288, 128, 4096), (64, 16384, 4096)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
